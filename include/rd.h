@@ -64,6 +64,8 @@ typedef enum { RD_BF16 = 0, RD_F16 = 1, RD_F32 = 2, RD_I32 = 3 } rd_dtype;
 /* Limits of this implementation (RD_ERR_UNSUPPORTED beyond them). */
 #define RD_MAX_BEAMS      32    /* W                                   */
 #define RD_MAX_PACKED    256    /* P_cap / P_max                       */
+#define RD_MAX_ROWS    16384    /* rows of a block table, pairs of a fork (page operators) */
+#define RD_MAX_PAGES  262144    /* pages of a pool (page operators)     */
 
 const char* rd_status_string(rd_status s);
 
@@ -229,6 +231,101 @@ rd_status rd_commit_accepted(int B, int W, int L, int P_max, int Hkv, int D,
                              const int32_t* block_table, int max_pages,
                              const int32_t* ctx_lens, int32_t* new_ctx_lens,
                              int32_t* dev_status, rd_stream_t stream);
+
+/*
+ * Page operators: who owns which page of the paged cache that
+ * rd_tree_attention_paged reads and rd_commit_accepted writes (paged KV caching:
+ * NVIDIA blog "ReDrafter in TensorRT-LLM", introduction).  Their state is
+ *
+ *   block_table int32 [R, max_pages]  row r's pages, in order of position
+ *   row_pages   int32 [R]             how many of them row r holds
+ *   page_refs   int32 [num_pages]     rows (and other owners) that hold a page;
+ *                                     0: the page is free.  An owner outside the
+ *                                     tables (a kept prompt) holds its pages by
+ *                                     adding 1.
+ *   k_pool, v_pool [layers, num_pages, page_bytes] the pages themselves, any
+ *                                     element type; page_bytes (of one page of K,
+ *                                     or V, in one layer) a multiple of 16
+ *                                     (RD_ERR_UNSUPPORTED), bases 16-byte aligned
+ *
+ * Free pages are handed out in ascending order of their ids, so every outcome
+ * depends on the tables alone.  R and n <= RD_MAX_ROWS, num_pages <=
+ * RD_MAX_PAGES, R * max_pages < 2^31 (RD_ERR_UNSUPPORTED).  Calls that change the
+ * same tables must not overlap in time.
+ */
+
+/*
+ * rd_resize_pages -- reserve, trim and free: row r comes to hold
+ * ceil(new_lens[r] / page_size) pages (0: all are given back; a negative
+ * new_lens[r] leaves the row alone).
+ *
+ * Rows that shrink go first: their entries behind the new end become -1 and the
+ * pages lose one reference.  Then the rows that grow take the lowest free pages,
+ * in row order.  The first row that the free pages no longer cover, and every
+ * growing row behind it, stay as they are and set RD_DEV_OVERFLOW.  A row that holds or
+ * wants more than max_pages sets RD_DEV_BAD_LENGTH and is left alone; an entry
+ * out of range, or naming a page that nobody holds, sets RD_DEV_BAD_INDEX and
+ * gives nothing back.
+ */
+rd_status rd_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* row_pages,
+                          int32_t* page_refs, int num_pages, const int32_t* new_lens,
+                          int page_size, int32_t* dev_status, rd_stream_t stream);
+
+/*
+ * rd_fork_pages -- branch requests: for i < n, row child[i] becomes a copy of row
+ * parent[i] of length ctx_lens[parent[i]].
+ *
+ * The pages that the length fills are shared (one reference more each); a last,
+ * partly filled page is copied to a new page of the child's own (its used
+ * positions, K and V, all layers), so that both rows can go on writing behind
+ * their length.  Pages that the parent holds beyond its length are not shared.  Sets
+ * the child's table row, row_pages and ctx_lens.  All parents are read as they were before
+ * the call.  parent[i] < 0: no pair.
+ *
+ * A child must hold no pages.  A row out of range, a child that holds pages, is
+ * its own parent, or is named by an earlier pair sets RD_DEV_BAD_INDEX; a parent whose
+ * length is negative or not covered by its pages sets RD_DEV_BAD_LENGTH; a pair
+ * for whose last page no free page is left sets RD_DEV_OVERFLOW: that pair is
+ * skipped.  Workspace: rd_fork_pages_workspace_size(n) bytes, no initial contents.
+ */
+size_t rd_fork_pages_workspace_size(int n);
+rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
+                        int page_size, int32_t* block_table, int R, int max_pages,
+                        int32_t* row_pages, int32_t* page_refs, int32_t* ctx_lens,
+                        const int32_t* parent, const int32_t* child, int n, void* workspace,
+                        size_t ws_bytes, int32_t* dev_status, rd_stream_t stream);
+
+/*
+ * rd_copy_pages -- page dst[i] = page src[i] for i < n, K and V, all layers.
+ *
+ * src[i] < 0: no pair; src[i] == dst[i]: nothing to do.  The pairs are copied
+ * side by side, so none may depend on another: a pair with an id out of range,
+ * with the destination of an earlier pair, or whose source is the destination of
+ * another pair sets RD_DEV_BAD_INDEX and is skipped.  Touches no table.
+ * Workspace: rd_copy_pages_workspace_size(n) bytes, no initial contents.
+ */
+size_t rd_copy_pages_workspace_size(int n);
+rd_status rd_copy_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
+                        const int32_t* src, const int32_t* dst, int n, void* workspace,
+                        size_t ws_bytes, int32_t* dev_status, rd_stream_t stream);
+
+/*
+ * rd_compact_pages -- move the pages that are held to the lowest ids.
+ *
+ * With n_live pages held, the k-th lowest free page below n_live receives the
+ * k-th lowest held page at or above it (K and V, all layers, and its reference count),
+ * and every table entry j < row_pages[r] follows.  Afterwards exactly the pages [0, n_live)
+ * are held.  remap int32 [num_pages] receives each page's new id (-1 for a page
+ * that was free), for owners outside the tables; n_live int32 [1].  An entry
+ * that is out of range or names a free page sets RD_DEV_BAD_INDEX and stays.
+ * Workspace: rd_compact_pages_workspace_size(num_pages) bytes, no initial contents.
+ */
+size_t rd_compact_pages_workspace_size(int num_pages);
+rd_status rd_compact_pages(void* k_pool, void* v_pool, int layers, int num_pages,
+                           size_t page_bytes, int32_t* block_table, int R, int max_pages,
+                           const int32_t* row_pages, int32_t* page_refs, int32_t* remap,
+                           int32_t* n_live, void* workspace, size_t ws_bytes,
+                           int32_t* dev_status, rd_stream_t stream);
 
 /*
  * rd_causal_attention -- causal prefill of the context-phase requests of an

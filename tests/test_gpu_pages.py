@@ -1,0 +1,270 @@
+"""The paged cache's page operators on the GPU against the plain Python oracle:
+tables, reference counts, status bits and the pools' bits, all exactly."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import pages as op
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def _rd():
+    import tree_attention_verify_gb300 as rd
+    return rd
+
+
+def _d(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def _pool(rng, layers, N, ps, Hkv, D):
+    return rng.integers(-2 ** 15, 2 ** 15, (layers, N, ps, Hkv, D)).astype(np.int16)
+
+
+def _bf16(x):
+    return _d(x).view(torch.bfloat16)
+
+
+def _tables(rng, R, N, width, share=0.2):
+    """A cache in use: random rows over distinct pages, some pages held twice."""
+    table, held, refs = np.full((R, width), -1, np.int32), np.zeros(R, np.int32), np.zeros(N, np.int32)
+    ids = list(rng.permutation(N))
+    for r in range(R):
+        k = int(rng.integers(0, width + 1)) if rng.random() < 0.7 else 0
+        k = min(k, len(ids))
+        for j in range(k):
+            used = np.flatnonzero(refs)
+            p = int(rng.choice(used)) if len(used) and rng.random() < share and j == 0 else int(ids.pop())
+            table[r, j] = p
+            refs[p] += 1
+        held[r] = k
+    return table, held, refs
+
+
+@pytest.mark.parametrize("R,N,width,ps", [(1, 1, 1, 64), (1, 40, 9, 64), (13, 100, 7, 128), (200, 2049, 17, 64),
+                                          (1500, 40000, 33, 1), (3, 262144, 5, 16), (16384, 3000, 3, 64)])
+def test_resize(R, N, width, ps):
+    rd = _rd()
+    rng = np.random.default_rng(R + N)
+    table, held, refs = _tables(rng, R, N, width)
+    lens = np.where(rng.random(R) < 0.2, -1, np.where(rng.random(R) < 0.3, 0, rng.integers(0, width * ps + 1, R)))
+    lens = lens.astype(np.int32)
+    t, h, f, st = _d(table), _d(held), _d(refs), _status()
+    for step in range(2):                     # the second call works on what the first left
+        want = op.oracle_resize_pages(table, held, refs, lens, ps)
+        st.zero_()
+        got = rd.rd_resize_pages(t, h, f, _d(lens), ps, dev_status=st)
+        assert got is h and st.item() == want[3]
+        for a, b in zip((t, h, f), want):
+            np.testing.assert_array_equal(a.cpu().numpy(), b)
+        table, held, refs = want[:3]
+        lens = rng.integers(-1, width * ps + 1, R).astype(np.int32)
+
+
+def test_resize_flags_what_does_not_fit_and_what_is_wrong():
+    rd = _rd()
+    table = np.array([[0, 9, -5, -1], [1, 2, -1, -1], [3, -1, -1, -1], [-1, -1, -1, -1], [4, 4, -1, -1]], np.int32)
+    held, refs = np.array([3, 2, 9, 0, 2], np.int32), np.array([1, 1, 0, 1, 1, 0, 0, 1], np.int32)
+    for lens in ([0, 0, 0, 0, 0], [64, 300, 5, 64, 0], [-1, 128, -1, 257, 256], [192, 128, 0, 256, 256],
+                 [192, 192, 3, 64 * 4, 129]):
+        lens = np.array(lens, np.int32)
+        want = op.oracle_resize_pages(table, held, refs, lens, 64)
+        t, h, f, st = _d(table), _d(held), _d(refs), _status()
+        rd.rd_resize_pages(t, h, f, _d(lens), 64, dev_status=st)
+        assert st.item() == want[3] and want[3] != 0
+        for a, b in zip((t, h, f), want):
+            np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("R,N,width,ps,Hkv,D,layers,n", [
+    (2, 3, 2, 64, 1, 64, 1, 1), (9, 50, 5, 64, 3, 128, 2, 4), (40, 300, 6, 128, 2, 64, 3, 25),
+    (400, 2500, 6, 64, 1, 64, 1, 180), (30, 60, 4, 16, 1, 8, 5, 20)])
+def test_fork(R, N, width, ps, Hkv, D, layers, n):
+    rd = _rd()
+    rng = np.random.default_rng(R * N)
+    table, held, refs = _tables(rng, R, N, width)
+    ctx = np.maximum(0, held * ps - rng.integers(0, 2 * ps, R)).astype(np.int32)
+    ctx = np.where(rng.random(R) < 0.3, held * ps, ctx).astype(np.int32)
+    k, v = _pool(rng, layers, N, ps, Hkv, D), _pool(rng, layers, N, ps, Hkv, D)
+    empty, full = np.flatnonzero(held == 0), np.flatnonzero(held > 0)
+    kid = rng.choice(empty, n).astype(np.int32)              # some rows twice
+    par = np.where(rng.random(n) < 0.15, -1, rng.choice(full if len(full) else empty, n)).astype(np.int32)
+    want = op.oracle_fork_pages(k, v, table, held, refs, ctx, par, kid)
+    kp, vp, t, h, f, c, st = _bf16(k), _bf16(v), _d(table), _d(held), _d(refs), _d(ctx), _status()
+    rd.rd_fork_pages(kp, vp, t, h, f, c, _d(par), _d(kid), dev_status=st)
+    assert st.item() == want[6]
+    for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, h, f, c), want):
+        np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+def test_fork_flags_and_skips_what_is_wrong():
+    rd = _rd()
+    rng = np.random.default_rng(3)
+    N, ps = 12, 64
+    k, v = _pool(rng, 1, N, ps, 1, 64), _pool(rng, 1, N, ps, 1, 64)
+    table, held, refs = np.full((8, 3), -1, np.int32), np.zeros(8, np.int32), np.zeros(N, np.int32)
+    table[0, :2], table[1, :3], table[2, :1] = [4, 7], [1, 99, 2], [5]
+    held[:3] = [2, 3, 1]
+    refs[[4, 7, 1, 2, 5]] = 1
+    ctx = np.array([100, 150, 65, -2, 0, 0, 0, 0], np.int32)
+    cases = [([0, 0], [3, 3]), ([0, 8, 0], [4, 5, -1]), ([0, 0], [0, 1]), ([2, 3, 0], [5, 6, 7]), ([1, 4], [3, 6]),
+             ([0, 3], [3, 5]), ([0] * 5, [3, 4, 5, 6, 7])]
+    for par, kid in cases:
+        for spare in (N, 2):                 # two spare pages only: the last pairs find none
+            full = refs.copy()
+            full[np.flatnonzero(refs == 0)[spare:]] = 1
+            par_, kid_ = np.array(par, np.int32), np.array(kid, np.int32)
+            want = op.oracle_fork_pages(k, v, table, held, full, ctx, par_, kid_)
+            kp, vp, t, h, f, c, st = _bf16(k), _bf16(v), _d(table), _d(held), _d(full), _d(ctx), _status()
+            rd.rd_fork_pages(kp, vp, t, h, f, c, _d(par_), _d(kid_), dev_status=st)
+            assert st.item() == want[6]
+            for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, h, f, c), want):
+                np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("N,ps,Hkv,D,layers,n", [(2, 64, 1, 64, 1, 1), (40, 64, 8, 128, 1, 13), (30, 64, 3, 64, 4, 15),
+                                                 (700, 1, 1, 8, 2, 300), (64, 256, 2, 128, 2, 31)])
+def test_copy(N, ps, Hkv, D, layers, n):
+    rd = _rd()
+    rng = np.random.default_rng(N + n)
+    k, v = _pool(rng, layers, N, ps, Hkv, D), _pool(rng, layers, N, ps, Hkv, D)
+    ids = rng.permutation(N)
+    src, dst = ids[:n].astype(np.int32), ids[n:2 * n].astype(np.int32)
+    src[rng.random(n) < 0.1] = -1
+    if n > 3:
+        src[1] = src[0] if src[0] >= 0 else ids[0]          # one source twice
+    want = op.oracle_copy_pages(k, v, src, dst)
+    kp, vp, st = _bf16(k), _bf16(v), _status()
+    rd.rd_copy_pages(kp, vp, _d(src), _d(dst), dev_status=st)
+    assert st.item() == 0 == want[2]
+    np.testing.assert_array_equal(kp.view(torch.int16).cpu().numpy(), want[0])
+    np.testing.assert_array_equal(vp.view(torch.int16).cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_copy_skips_pairs_that_depend_on_one_another(seed):
+    rd = _rd()
+    rng = np.random.default_rng(seed)
+    N, n = 600, 520                           # more pairs than one block compares at a time
+    k, v = _pool(rng, 1, N, 1, 1, 8), _pool(rng, 1, N, 1, 1, 8)
+    src, dst = rng.integers(-2, N + 3, n).astype(np.int32), rng.integers(-1, N + 1, n).astype(np.int32)
+    want = op.oracle_copy_pages(k, v, src, dst)
+    kp, vp, st = _bf16(k), _bf16(v), _status()
+    rd.rd_copy_pages(kp, vp, _d(src), _d(dst), dev_status=st)
+    assert st.item() == want[2] == rd.DEV_BAD_INDEX
+    np.testing.assert_array_equal(kp.view(torch.int16).cpu().numpy(), want[0])
+    np.testing.assert_array_equal(vp.view(torch.int16).cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("R,N,width,ps,Hkv,D,layers", [(1, 1, 1, 64, 1, 64, 1), (5, 33, 4, 64, 2, 128, 2),
+                                                       (60, 400, 5, 64, 1, 64, 3), (300, 9000, 12, 1, 1, 8, 1)])
+def test_compact(R, N, width, ps, Hkv, D, layers):
+    rd = _rd()
+    rng = np.random.default_rng(R + 7 * N)
+    table, held, refs = _tables(rng, R, N, width)
+    refs[rng.integers(0, N)] += 1             # a page that somebody holds outside the tables
+    k, v = _pool(rng, layers, N, ps, Hkv, D), _pool(rng, layers, N, ps, Hkv, D)
+    want = op.oracle_compact_pages(k, v, table, held, refs)
+    kp, vp, t, h, f, st = _bf16(k), _bf16(v), _d(table), _d(held), _d(refs), _status()
+    remap, n_live = rd.rd_compact_pages(kp, vp, t, h, f, dev_status=st)
+    assert st.item() == want[6] == 0 and n_live.item() == want[5]
+    for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, f, remap), want):
+        np.testing.assert_array_equal(a.cpu().numpy(), b)
+    again = rd.rd_compact_pages(kp, vp, t, h, f, dev_status=st)[0]     # nothing left to move
+    np.testing.assert_array_equal(again.cpu().numpy()[:want[5]], np.arange(want[5]))
+    np.testing.assert_array_equal(kp.view(torch.int16).cpu().numpy(), want[0])
+
+
+@pytest.mark.parametrize("refs", [[0, 0, 0, 0], [1, 2, 3, 1], [0, 0, 0, 1], [1, 0, 0, 0]])
+def test_compact_empty_full_and_one_page(refs):
+    rd = _rd()
+    rng = np.random.default_rng(0)
+    k = _pool(rng, 1, 4, 16, 1, 8)
+    refs = np.array(refs, np.int32)
+    table, held = np.array([[3, 77]], np.int32), np.array([2], np.int32)
+    want = op.oracle_compact_pages(k, k, table, held, refs)
+    kp, vp, t, h, f, st = _bf16(k), _bf16(k), _d(table), _d(held), _d(refs), _status()
+    remap, n_live = rd.rd_compact_pages(kp, vp, t, h, f, dev_status=st)
+    assert st.item() == want[6] == rd.DEV_BAD_INDEX and n_live.item() == want[5]
+    for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, f, remap), want):
+        np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+def test_fp8_pools_of_four_dimensions():
+    rd = _rd()
+    rng = np.random.default_rng(8)
+    k = rng.integers(0, 256, (10, 64, 2, 128)).astype(np.uint8)
+    kp, vp = _d(k), _d(k[::-1].copy())
+    rd.rd_copy_pages(kp, vp, _d(np.array([3, 9], np.int32)), _d(np.array([0, 5], np.int32)))
+    k[0], k[5] = k[3], k[9]
+    np.testing.assert_array_equal(kp.cpu().numpy(), k)
+    kf = kp.view(torch.float8_e4m3fn)
+    rd.rd_copy_pages(kf, vp.view(torch.float8_e4m3fn), _d(np.array([1], np.int32)), _d(np.array([2], np.int32)))
+    np.testing.assert_array_equal(kp[2].cpu().numpy(), k[1])
+
+
+def test_captured_step_replays_on_other_tables():
+    # reserve, fork and compact in one graph: each replay works on what the
+    # tables then hold
+    rd = _rd()
+    rng = np.random.default_rng(1)
+    R, N, width, ps = 20, 200, 6, 64
+    k0 = _pool(rng, 1, N, ps, 1, 64)
+    kp, vp, st = _bf16(k0), _bf16(k0), _status()
+    t, h, f = _d(np.full((R, width), -1, np.int32)), _d(np.zeros(R, np.int32)), _d(np.zeros(N, np.int32))
+    c, lens = _d(np.zeros(R, np.int32)), _d(np.zeros(R, np.int32))
+    par, kid = _d(np.array([0, 1], np.int32)), _d(np.array([18, 19], np.int32))
+
+    def step():
+        rd.rd_resize_pages(t, h, f, lens, ps, dev_status=st)
+        rd.rd_fork_pages(kp, vp, t, h, f, c, par, kid, dev_status=st)
+        rd.rd_compact_pages(kp, vp, t, h, f, dev_status=st)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    table, held, refs = (x.cpu().numpy() for x in (t, h, f))
+    ctx, k, v = c.cpu().numpy(), k0, k0
+    k, v = (x.view(torch.int16).cpu().numpy() for x in (kp, vp))
+    for i in range(4):
+        n = np.where(np.arange(R) < 18, rng.integers(0, width * ps, R), 0).astype(np.int32)
+        lens.copy_(_d(n))
+        ctx = np.where(np.arange(R) < 18, n, 0).astype(np.int32)
+        c.copy_(_d(ctx))
+        graph.replay()
+        table, held, refs, st1 = op.oracle_resize_pages(table, held, refs, n, ps)
+        k, v, table, held, refs, ctx, st2 = op.oracle_fork_pages(k, v, table, held, refs, ctx, par.cpu().numpy(),
+                                                                 kid.cpu().numpy())
+        k, v, table, refs, _, _, st3 = op.oracle_compact_pages(k, v, table, held, refs)
+        assert st.item() == st1 | st2 | st3 == 0
+        for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, h, f, c), (k, v, table, held, refs, ctx)):
+            np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+def test_given_stream_and_workspace():
+    rd = _rd()
+    rng = np.random.default_rng(2)
+    k = _pool(rng, 1, 8, 64, 1, 64)
+    kp, vp = _bf16(k), _bf16(k)
+    src, dst = _d(np.array([1], np.int32)), _d(np.array([6], np.int32))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    rd.rd_copy_pages(kp, vp, src, dst, stream=s)
+    rd.rd_copy_pages(kp, vp, dst, src, stream=s, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+    s.synchronize()
+    k[0, 6] = k[0, 1]
+    np.testing.assert_array_equal(kp.view(torch.int16).cpu().numpy(), k)
+    with pytest.raises(ValueError):
+        rd.rd_copy_pages(kp, vp, src, dst, workspace=torch.empty(7, dtype=torch.uint8, device=DEV))
+    with pytest.raises(rd.RdError):           # pages of 12 bytes: not whole 16-byte units
+        rd.rd_copy_pages(torch.zeros(4, 1, 2, 3, dtype=torch.bfloat16, device=DEV),
+                         torch.zeros(4, 1, 2, 3, dtype=torch.bfloat16, device=DEV), src, dst)

@@ -1,0 +1,86 @@
+"""Host-side checks of the page operators, without a GPU: the C entries refuse
+bad arguments before they touch the device, the binding refuses tensors whose
+shapes, types or places disagree."""
+import ctypes
+
+import pytest
+import torch
+
+import tree_attention_verify_gb300 as rd
+
+N = None
+ONE = ctypes.c_void_p(256)
+
+
+def test_resize_validation():
+    f = rd._lib.rd_resize_pages
+    assert f(N, 0, 8, N, N, 16, N, 64, N, N) == rd.RD_OK                      # no rows
+    for args in ((ONE, -1, 8, ONE, ONE, 16, ONE, 64), (ONE, 4, -8, ONE, ONE, 16, ONE, 64),
+                 (ONE, 4, 8, ONE, ONE, -1, ONE, 64), (ONE, 4, 8, ONE, ONE, 16, ONE, 0),
+                 (N, 4, 8, ONE, ONE, 16, ONE, 64), (ONE, 4, 8, N, ONE, 16, ONE, 64),
+                 (ONE, 4, 8, ONE, N, 16, ONE, 64), (ONE, 4, 8, ONE, ONE, 16, N, 64)):
+        assert f(*args, N, N) == rd.RD_ERR_INVALID_ARG, args
+    for args in ((ONE, 16385, 8, ONE, ONE, 16, ONE, 64), (ONE, 4, 8, ONE, ONE, 262145, ONE, 64),
+                 (ONE, 16384, 1 << 17, ONE, ONE, 16, ONE, 64)):
+        assert f(*args, N, N) == rd.RD_ERR_UNSUPPORTED, args
+
+
+def test_fork_validation():
+    f = rd._lib.rd_fork_pages
+    good = dict(k=ONE, v=ONE, layers=2, pages=16, bytes=4096, ps=64, table=ONE, R=4, width=8, rows=ONE,
+                refs=ONE, ctx=ONE, par=ONE, kid=ONE, n=3, ws=ONE, wsb=36)
+
+    def call(**kw):
+        return f(*{**good, **kw}.values(), N, N)
+    assert call(n=0) == rd.RD_OK and call(R=0) == rd.RD_OK
+    for kw in (dict(k=N), dict(v=N), dict(layers=0), dict(pages=-1), dict(bytes=0), dict(ps=0), dict(ps=48),
+               dict(table=N), dict(R=-1), dict(width=-1), dict(rows=N), dict(refs=N), dict(ctx=N), dict(par=N),
+               dict(kid=N), dict(n=-1), dict(ws=N), dict(wsb=35), dict(k=ctypes.c_void_p(264))):
+        assert call(**kw) == rd.RD_ERR_INVALID_ARG, kw
+    for kw in (dict(bytes=4104), dict(n=16385, wsb=1 << 20), dict(R=16385), dict(pages=262145)):
+        assert call(**kw) == rd.RD_ERR_UNSUPPORTED, kw
+    assert rd._lib.rd_fork_pages_workspace_size(3) == 36 and rd._lib.rd_fork_pages_workspace_size(0) == 0
+
+
+def test_copy_and_compact_validation():
+    f = rd._lib.rd_copy_pages
+    assert f(N, N, 1, 16, 4096, N, N, 0, N, 0, N, N) == rd.RD_OK
+    good = dict(k=ONE, v=ONE, layers=2, pages=16, bytes=4096, src=ONE, dst=ONE, n=3, ws=ONE, wsb=24)
+    for kw in (dict(k=N), dict(v=N), dict(src=N), dict(dst=N), dict(n=-1), dict(ws=N), dict(wsb=23),
+               dict(layers=0), dict(v=ctypes.c_void_p(257))):
+        assert f(*{**good, **kw}.values(), N, N) == rd.RD_ERR_INVALID_ARG, kw
+    for kw in (dict(bytes=4100), dict(n=262145, wsb=1 << 22)):
+        assert f(*{**good, **kw}.values(), N, N) == rd.RD_ERR_UNSUPPORTED, kw
+    g = rd._lib.rd_compact_pages
+    good = dict(k=ONE, v=ONE, layers=2, pages=16, bytes=4096, table=ONE, R=4, width=8, rows=ONE, refs=ONE,
+                remap=ONE, live=ONE, ws=ONE, wsb=80)
+    assert rd._lib.rd_compact_pages_workspace_size(16) == 80
+    for kw in (dict(k=N), dict(table=N), dict(rows=N), dict(refs=N), dict(remap=N), dict(live=N), dict(ws=N),
+               dict(wsb=79), dict(pages=-1)):
+        assert g(*{**good, **kw}.values(), N, N) == rd.RD_ERR_INVALID_ARG, kw
+    assert g(*{**good, "bytes": 100}.values(), N, N) == rd.RD_ERR_UNSUPPORTED
+
+
+def _i(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_binding_refuses_before_a_launch():
+    pool, table = torch.zeros(8, 64, 1, 64, dtype=torch.bfloat16), _i(4, 3)
+    # CPU tensors (and with them every call here) are refused by name
+    with pytest.raises(ValueError, match="block_table must be a CUDA tensor"):
+        rd.rd_resize_pages(table, _i(4), _i(8), _i(4), 64)
+    with pytest.raises(ValueError, match="k_pool must be a CUDA tensor"):
+        rd.rd_fork_pages(pool, pool, table, _i(4), _i(8), _i(4), _i(2), _i(2))
+    with pytest.raises(ValueError, match="k_pool must be a CUDA tensor"):
+        rd.rd_copy_pages(pool, pool, _i(2), _i(2))
+    with pytest.raises(ValueError, match="k_pool must be a CUDA tensor"):
+        rd.rd_compact_pages(pool, pool, table, _i(4), _i(8))
+    with pytest.raises(TypeError):
+        rd.rd_resize_pages(table.long(), _i(4), _i(8), _i(4), 64)
+    with pytest.raises(TypeError):
+        rd.rd_copy_pages([1], pool, _i(2), _i(2))
+    with pytest.raises(ValueError, match="at least"):
+        rd._scratch(torch.zeros(3, dtype=torch.uint8), 16, pool, None)
+    with pytest.raises(TypeError):
+        rd._need_status(torch.zeros(1), pool)

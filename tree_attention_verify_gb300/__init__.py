@@ -24,7 +24,8 @@ __all__ = [
     "rd_causal_attention", "rd_unpack", "rd_greedy_accept",
     "rd_greedy_accept_workspace_size", "rd_greedy_accept_noalloc",
     "rd_tree_attention_paged", "rd_commit_accepted", "rd_beam_search_step",
-    "rd_tree_attention_fp8", "rd_sample_accept", "rd_debug_stall_attention", "RdError",
+    "rd_tree_attention_fp8", "rd_sample_accept", "rd_resize_pages", "rd_fork_pages",
+    "rd_copy_pages", "rd_compact_pages", "rd_debug_stall_attention", "RdError",
     "DEV_BAD_INDEX", "DEV_BAD_TOKEN", "DEV_OVERFLOW", "DEV_BAD_LENGTH", "DEV_TIMEOUT",
     "lib_path",
 ]
@@ -66,6 +67,13 @@ def _load() -> ctypes.CDLL:
         "rd_tree_attention_fp8": [I, I, I, I, I, F, P, P, P, P, P, F, F, P, I64, I, P, P, I, P, P,
                                   S, P, P],
         "rd_sample_accept": [P, P, I, I, I, F, P, P, P, P, I, I, P, P, P, P, P, P, P, P],
+        "rd_resize_pages": [P, I, I, P, P, I, P, I, P, P],
+        "rd_fork_pages_workspace_size": [I],
+        "rd_fork_pages": [P, P, I, I, S, I, P, I, I, P, P, P, P, P, I, P, S, P, P],
+        "rd_copy_pages_workspace_size": [I],
+        "rd_copy_pages": [P, P, I, I, S, P, P, I, P, S, P, P],
+        "rd_compact_pages_workspace_size": [I],
+        "rd_compact_pages": [P, P, I, I, S, P, I, I, P, P, P, P, P, S, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -120,6 +128,9 @@ def _check(fn: str, status: int):
 def _run(name: str, like: torch.Tensor, *args, stream=None):
     """Call librd's `name` with `like`'s device current and that device's
     stream (or `stream`) as the last argument; raise RdError on a bad status."""
+    if like.device.index == torch.cuda.current_device():
+        _check(name, getattr(_lib, name)(*args, _stream(stream, like.device)))
+        return
     with torch.cuda.device(like.device):
         _check(name, getattr(_lib, name)(*args, _stream(stream, like.device)))
 
@@ -498,6 +509,139 @@ def rd_beam_search_step(logits, scores_in, beams_in, *, out=None, dev_status=Non
         _ptr(out["beams"]), _ptr(out["scores"]), _ptr(out["parent"]), _ptr(dev_status),
         stream=stream)
     return out
+
+
+# ----------------------------------------------------------------------------
+# page operators of the paged cache
+# ----------------------------------------------------------------------------
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A fresh tensor whose memory belongs to the stream that the call runs on, so
+    that it is not handed out again while the call still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _scratch(workspace, size: int, like: torch.Tensor, stream) -> torch.Tensor:
+    if workspace is None:
+        return _new(max(16, size), torch.uint8, like, stream)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    if workspace.numel() * workspace.element_size() < size:
+        raise ValueError(f"workspace must have at least {size} bytes")
+    return workspace
+
+
+def _need_status(dev_status, like: torch.Tensor):
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, like.device)
+        if dev_status.numel() < 1:
+            raise ValueError("dev_status must have one element")
+
+
+def _pools(k_pool, v_pool):
+    """(layers, num_pages, page_size, bytes of a page) of pools
+    [num_pages, page_size, Hkv, D] or [layers, num_pages, page_size, Hkv, D]."""
+    if not isinstance(k_pool, torch.Tensor) or not isinstance(v_pool, torch.Tensor):
+        raise TypeError("k_pool and v_pool must be torch tensors")
+    _need(k_pool, "k_pool", k_pool.dtype)
+    _need(v_pool, "v_pool", k_pool.dtype, k_pool.device)
+    shape = k_pool.shape
+    if len(shape) not in (4, 5) or v_pool.shape != shape:
+        raise ValueError("k_pool/v_pool must be [num_pages, page_size, Hkv, D] or "
+                         "[layers, num_pages, page_size, Hkv, D], of one shape")
+    page = shape[-3] * shape[-2] * shape[-1] * k_pool.element_size()
+    return (shape[0] if len(shape) == 5 else 1), shape[-4], shape[-3], page
+
+
+def _tables(block_table, row_pages, page_refs, num_pages, device):
+    """(rows, entries of a row) of the page tables, checked against each other."""
+    _need(block_table, "block_table", torch.int32, device, ndim=2)
+    _need(row_pages, "row_pages", torch.int32, block_table.device, ndim=1)
+    _need(page_refs, "page_refs", torch.int32, block_table.device, ndim=1)
+    R, max_pages = block_table.shape
+    if row_pages.shape[0] != R:
+        raise ValueError(f"row_pages must be [{R}], got {tuple(row_pages.shape)}")
+    if num_pages is not None and page_refs.shape[0] != num_pages:
+        raise ValueError(f"page_refs must be [{num_pages}], got {tuple(page_refs.shape)}")
+    return R, max_pages
+
+
+def rd_resize_pages(block_table, row_pages, page_refs, new_lens, page_size: int, *,
+                    dev_status=None, stream=None) -> torch.Tensor:
+    """Reserve, trim and free pages: row r comes to hold ceil(new_lens[r] / page_size)
+    of them (new_lens int32 [R]; 0 frees the row, negative leaves it alone).
+    block_table int32 [R, max_pages], row_pages int32 [R] and page_refs int32
+    [num_pages] change in place; returns row_pages (see rd_resize_pages in rd.h)."""
+    R, max_pages = _tables(block_table, row_pages, page_refs, None, None)
+    _need(new_lens, "new_lens", torch.int32, block_table.device, ndim=1)
+    if new_lens.shape[0] != R:
+        raise ValueError(f"new_lens must be [{R}], got {tuple(new_lens.shape)}")
+    _need_status(dev_status, block_table)
+    _run("rd_resize_pages", block_table,
+         _ptr(block_table), R, max_pages, _ptr(row_pages), _ptr(page_refs), page_refs.shape[0],
+         _ptr(new_lens), int(page_size), _ptr(dev_status), stream=stream)
+    return row_pages
+
+
+def rd_fork_pages(k_pool, v_pool, block_table, row_pages, page_refs, ctx_lens, parent, child, *,
+                  workspace=None, dev_status=None, stream=None) -> None:
+    """Branch requests: row child[i] becomes a copy of row parent[i] (int32 [n];
+    parent -1: no pair), sharing its full pages and copying its last, partly
+    filled one.  The tables, ctx_lens int32 [R] and the pools change in place (see
+    rd_fork_pages in rd.h)."""
+    layers, num_pages, page_size, page = _pools(k_pool, v_pool)
+    R, max_pages = _tables(block_table, row_pages, page_refs, num_pages, k_pool.device)
+    for name, t in (("ctx_lens", ctx_lens), ("parent", parent), ("child", child)):
+        _need(t, name, torch.int32, k_pool.device, ndim=1)
+    n = parent.shape[0]
+    if ctx_lens.shape[0] != R or child.shape[0] != n:
+        raise ValueError("ctx_lens must be [R], and child as long as parent")
+    _need_status(dev_status, k_pool)
+    workspace = _scratch(workspace, 12 * n, k_pool, stream)
+    _run("rd_fork_pages", k_pool,
+         _ptr(k_pool), _ptr(v_pool), layers, num_pages, page, page_size, _ptr(block_table), R,
+         max_pages, _ptr(row_pages), _ptr(page_refs), _ptr(ctx_lens), _ptr(parent), _ptr(child), n,
+         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
+
+
+def rd_copy_pages(k_pool, v_pool, src, dst, *, workspace=None, dev_status=None, stream=None) -> None:
+    """Page dst[i] = page src[i] (int32 [n]; src -1: no pair), K and V, all layers
+    (see rd_copy_pages in rd.h)."""
+    layers, num_pages, _, page = _pools(k_pool, v_pool)
+    _need(src, "src", torch.int32, k_pool.device, ndim=1)
+    _need(dst, "dst", torch.int32, k_pool.device, ndim=1)
+    n = src.shape[0]
+    if dst.shape[0] != n:
+        raise ValueError("src and dst must have the same length")
+    _need_status(dev_status, k_pool)
+    workspace = _scratch(workspace, 8 * n, k_pool, stream)
+    _run("rd_copy_pages", k_pool,
+         _ptr(k_pool), _ptr(v_pool), layers, num_pages, page, _ptr(src), _ptr(dst), n,
+         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
+
+
+def rd_compact_pages(k_pool, v_pool, block_table, row_pages, page_refs, *, remap=None, n_live=None,
+                     workspace=None, dev_status=None, stream=None):
+    """Move the held pages to the lowest ids; the pools, block_table and page_refs
+    change in place.  Returns (remap int32 [num_pages], n_live int32 [1]) (see
+    rd_compact_pages in rd.h)."""
+    layers, num_pages, _, page = _pools(k_pool, v_pool)
+    R, max_pages = _tables(block_table, row_pages, page_refs, num_pages, k_pool.device)
+    remap = _new((num_pages,), torch.int32, k_pool, stream) if remap is None else \
+        _out(remap, "remap", (num_pages,), torch.int32, k_pool)
+    n_live = _new((1,), torch.int32, k_pool, stream) if n_live is None else \
+        _out(n_live, "n_live", (1,), torch.int32, k_pool)
+    _need_status(dev_status, k_pool)
+    workspace = _scratch(workspace, 16 + 8 * (num_pages // 2), k_pool, stream)
+    _run("rd_compact_pages", k_pool,
+         _ptr(k_pool), _ptr(v_pool), layers, num_pages, page, _ptr(block_table), R, max_pages,
+         _ptr(row_pages), _ptr(page_refs), _ptr(remap), _ptr(n_live), _ptr(workspace),
+         workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
+    return remap, n_live
 
 
 def rd_debug_stall_attention(budget_cycles: int) -> None:

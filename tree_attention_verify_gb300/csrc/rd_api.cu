@@ -324,4 +324,104 @@ rd_status rd_beam_search_step(const void* logits, const float* scores_in,
                                          scores_out, parent, dev_status, (cudaStream_t)stream));
 }
 
+static rd_status check_pools(const void* k_pool, const void* v_pool, int layers, int num_pages, size_t page_bytes)
+{
+    if (layers < 1 || num_pages < 0 || page_bytes == 0) return RD_ERR_INVALID_ARG;
+    if (page_bytes % 16 != 0) return RD_ERR_UNSUPPORTED;       /* bulk copies move 16-byte units */
+    if (layers > 65535 || page_bytes > 0x7fffffffu) return RD_ERR_UNSUPPORTED;
+    if (!aligned16(k_pool) || !aligned16(v_pool)) return RD_ERR_INVALID_ARG;
+    return RD_OK;
+}
+
+/* the tables' sizes: one cluster holds the rows' counts in shared memory, and entry
+   counts stay within 32 bits */
+static rd_status check_tables(int R, int max_pages, int num_pages)
+{
+    if (R < 0 || max_pages < 0 || num_pages < 0) return RD_ERR_INVALID_ARG;
+    if (R > RD_MAX_ROWS || num_pages > RD_MAX_PAGES || (long long)R * max_pages > 0x7fffffffLL)
+        return RD_ERR_UNSUPPORTED;
+    return RD_OK;
+}
+
+rd_status rd_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* row_pages,
+                          int32_t* page_refs, int num_pages, const int32_t* new_lens, int page_size,
+                          int32_t* dev_status, rd_stream_t stream)
+{
+    if (page_size < 1) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_tables(R, max_pages, num_pages);
+    if (st != RD_OK) return st;
+    if (R == 0) return RD_OK;
+    if ((max_pages > 0 && !block_table) || !row_pages || (num_pages > 0 && !page_refs) || !new_lens)
+        return RD_ERR_INVALID_ARG;
+    return from_cuda(rd_launch_resize_pages(block_table, R, max_pages, row_pages, page_refs, num_pages,
+                                            new_lens, page_size, dev_status, (cudaStream_t)stream));
+}
+
+size_t rd_fork_pages_workspace_size(int n) { return n > 0 ? (size_t)n * 3 * sizeof(int32_t) : 0; }
+
+rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
+                        int page_size, int32_t* block_table, int R, int max_pages, int32_t* row_pages,
+                        int32_t* page_refs, int32_t* ctx_lens, const int32_t* parent,
+                        const int32_t* child, int n, void* workspace, size_t ws_bytes,
+                        int32_t* dev_status, rd_stream_t stream)
+{
+    if (n < 0 || page_size < 1) return RD_ERR_INVALID_ARG;
+    rd_status st = check_pools(k_pool, v_pool, layers, num_pages, page_bytes);
+    if (st == RD_OK) st = check_tables(R, max_pages, num_pages);
+    if (st != RD_OK) return st;
+    if (page_bytes % page_size != 0) return RD_ERR_INVALID_ARG;
+    if (n > RD_MAX_ROWS) return RD_ERR_UNSUPPORTED;
+    if (n == 0 || R == 0) return RD_OK;
+    if ((num_pages > 0 && (!k_pool || !v_pool || !page_refs)) || (max_pages > 0 && !block_table) ||
+        !row_pages || !ctx_lens || !parent || !child || !workspace)
+        return RD_ERR_INVALID_ARG;
+    if (ws_bytes < rd_fork_pages_workspace_size(n) || reinterpret_cast<uintptr_t>(workspace) % 4 != 0)
+        return RD_ERR_INVALID_ARG;
+    const rd_page_pools pools = {k_pool, v_pool, layers, num_pages, page_bytes};
+    return from_cuda(rd_launch_fork_pages(pools, page_size, block_table, R, max_pages, row_pages, page_refs,
+                                          ctx_lens, parent, child, n, workspace, dev_status,
+                                          (cudaStream_t)stream));
+}
+
+size_t rd_copy_pages_workspace_size(int n) { return n > 0 ? (size_t)n * 2 * sizeof(int32_t) : 0; }
+
+rd_status rd_copy_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
+                        const int32_t* src, const int32_t* dst, int n, void* workspace, size_t ws_bytes,
+                        int32_t* dev_status, rd_stream_t stream)
+{
+    if (n < 0) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_pools(k_pool, v_pool, layers, num_pages, page_bytes);
+    if (st != RD_OK) return st;
+    if (n > RD_MAX_PAGES) return RD_ERR_UNSUPPORTED;
+    if (n == 0) return RD_OK;
+    if ((num_pages > 0 && (!k_pool || !v_pool)) || !src || !dst || !workspace) return RD_ERR_INVALID_ARG;
+    if (ws_bytes < rd_copy_pages_workspace_size(n) || reinterpret_cast<uintptr_t>(workspace) % 4 != 0)
+        return RD_ERR_INVALID_ARG;
+    const rd_page_pools pools = {k_pool, v_pool, layers, num_pages, page_bytes};
+    return from_cuda(rd_launch_copy_pages(pools, src, dst, n, workspace, dev_status, (cudaStream_t)stream));
+}
+
+size_t rd_compact_pages_workspace_size(int num_pages)
+{
+    return num_pages < 0 ? 0 : (4 + 2 * (size_t)(num_pages / 2)) * sizeof(int32_t);
+}
+
+rd_status rd_compact_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
+                           int32_t* block_table, int R, int max_pages, const int32_t* row_pages,
+                           int32_t* page_refs, int32_t* remap, int32_t* n_live, void* workspace,
+                           size_t ws_bytes, int32_t* dev_status, rd_stream_t stream)
+{
+    rd_status st = check_pools(k_pool, v_pool, layers, num_pages, page_bytes);
+    if (st == RD_OK) st = check_tables(R, max_pages, num_pages);
+    if (st != RD_OK) return st;
+    if ((num_pages > 0 && (!k_pool || !v_pool || !page_refs || !remap)) || !n_live || !workspace ||
+        (R > 0 && (!row_pages || (max_pages > 0 && !block_table))))
+        return RD_ERR_INVALID_ARG;
+    if (ws_bytes < rd_compact_pages_workspace_size(num_pages) || reinterpret_cast<uintptr_t>(workspace) % 4 != 0)
+        return RD_ERR_INVALID_ARG;
+    const rd_page_pools pools = {k_pool, v_pool, layers, num_pages, page_bytes};
+    return from_cuda(rd_launch_compact_pages(pools, block_table, R, max_pages, row_pages, page_refs, remap,
+                                             n_live, workspace, dev_status, (cudaStream_t)stream));
+}
+
 }  // extern "C"

@@ -102,3 +102,23 @@ cudaError_t rd_launch_beam_step(const void* logits, const float* scores_in,
                                 const int32_t* beams_in, int B, int W, int V, int t,
                                 int32_t* beams_out, float* scores_out, int32_t* parent,
                                 int32_t* dev_status, cudaStream_t stream);
+
+// Page operators of the paged cache (pages.cu).
+struct rd_page_pools {
+    void* k_pool;             // [layers, num_pages, page_bytes]
+    void* v_pool;
+    int layers, num_pages;
+    size_t page_bytes;
+};
+cudaError_t rd_launch_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* row_pages,
+                                   int32_t* page_refs, int num_pages, const int32_t* new_lens, int page_size,
+                                   int32_t* dev_status, cudaStream_t stream);
+cudaError_t rd_launch_fork_pages(const rd_page_pools& pools, int page_size, int32_t* block_table, int R,
+                                 int max_pages, int32_t* row_pages, int32_t* page_refs, int32_t* ctx_lens,
+                                 const int32_t* parent, const int32_t* child, int n, void* workspace,
+                                 int32_t* dev_status, cudaStream_t stream);
+cudaError_t rd_launch_copy_pages(const rd_page_pools& pools, const int32_t* src, const int32_t* dst, int n,
+                                 void* workspace, int32_t* dev_status, cudaStream_t stream);
+cudaError_t rd_launch_compact_pages(const rd_page_pools& pools, int32_t* block_table, int R, int max_pages,
+                                    const int32_t* row_pages, int32_t* page_refs, int32_t* remap,
+                                    int32_t* n_live, void* workspace, int32_t* dev_status, cudaStream_t stream);
