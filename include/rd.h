@@ -203,6 +203,45 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
                                   int32_t* dev_status, rd_stream_t stream);
 
 /*
+ * rd_tree_attention_shared -- rd_tree_attention_paged for a batch whose groups of
+ * requests share a long prefix (a common prompt; the branches that rd_fork_pages
+ * makes), which is read and multiplied once per group instead of once per request.
+ * Single-token decoding is the case P_max = 1.
+ *
+ * Group g is the requests group_offsets[g] .. group_offsets[g+1] - 1, and the first
+ * prefix_pages[g] entries of their block-table rows name the same pages.  The function
+ * computed is that of rd_tree_attention_paged on the same arguments (ctx_lens
+ * counts the prefix); requests in no group, and groups of one request or
+ * without prefix pages, are allowed.
+ *
+ * group_offsets int32 [n_groups + 1], ascending within [0, B]; prefix_pages int32
+ *              [n_groups].  Offsets that do not ascend set RD_DEV_BAD_INDEX, and
+ *              prefix pages outside [0, max_pages] or longer than max_ctx
+ *              RD_DEV_BAD_LENGTH: nobody shares then (that group does not), and the outputs
+ *              are the same.  A request shorter than its group's prefix sets
+ *              RD_DEV_BAD_LENGTH and is skipped (zero rows).  Rows of a group
+ *              that name different prefix pages set RD_DEV_BAD_INDEX; its first
+ *              request's pages are read for all.
+ * workspace    rd_tree_attention_shared_workspace_size() bytes, 16-byte aligned, no
+ *              initial contents; query it with the device current that the call runs on
+ * Everything else as rd_tree_attention_paged, its limits among them.  K and V of
+ * the packed drafts must be finite (an infinity or NaN in a live draft's V can
+ * reach rows that do not see that draft); what lies behind a context's end in its
+ * last page, and behind packed_len, may hold anything.
+ */
+size_t rd_tree_attention_shared_workspace_size(int B, int P_max, int Hq, int Hkv, int D,
+                                               int max_ctx, int n_groups);
+rd_status rd_tree_attention_shared(int B, int P_max, int Hq, int Hkv, int D, float scale,
+                                   const void* q, const void* k_new, const void* v_new,
+                                   const void* k_pool, const void* v_pool, int num_pages,
+                                   int page_size, const int32_t* block_table, int max_pages,
+                                   const int32_t* ctx_lens, int max_ctx, int n_groups,
+                                   const int32_t* group_offsets, const int32_t* prefix_pages,
+                                   const int32_t* packed_len, const uint32_t* mask,
+                                   int mask_words, void* o, void* workspace, size_t ws_bytes,
+                                   int32_t* dev_status, rd_stream_t stream);
+
+/*
  * rd_commit_accepted -- append the K/V of each request's accepted path to its
  * paged cache, after rd_greedy_accept.
  *
@@ -433,8 +472,8 @@ rd_status rd_greedy_accept(const void* logits, int B, int P_max, int V,
  * counterpart: it exists to test the kernels' bounded waits without a GPU fault.
  *
  * budget_cycles > 0 arms it for every later rd_tree_attention,
- * rd_tree_attention_paged, rd_tree_attention_fp8 and rd_causal_attention
- * launch of this process: before its first MMA, each CTA's MMA-issuing thread
+ * rd_tree_attention_paged, rd_tree_attention_shared, rd_tree_attention_fp8 and
+ * rd_causal_attention launch of this process: before its first MMA, each CTA's MMA-issuing thread
  * waits on a barrier that nothing completes, for at most budget_cycles SM
  * clock cycles.  That wait runs out, the CTA records RD_DEV_TIMEOUT, its other
  * roles stop at their next wait, it waits (with the normal budget) for the

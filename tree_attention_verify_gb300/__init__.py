@@ -23,7 +23,8 @@ __all__ = [
     "rd_pack_beams", "rd_tree_attention", "rd_tree_attention_workspace_size",
     "rd_causal_attention", "rd_unpack", "rd_greedy_accept",
     "rd_greedy_accept_workspace_size", "rd_greedy_accept_noalloc",
-    "rd_tree_attention_paged", "rd_commit_accepted", "rd_beam_search_step",
+    "rd_tree_attention_paged", "rd_tree_attention_shared",
+    "rd_tree_attention_shared_workspace_size", "rd_commit_accepted", "rd_beam_search_step",
     "rd_tree_attention_fp8", "rd_sample_accept", "rd_resize_pages", "rd_fork_pages",
     "rd_copy_pages", "rd_compact_pages", "rd_debug_stall_attention", "RdError",
     "DEV_BAD_INDEX", "DEV_BAD_TOKEN", "DEV_OVERFLOW", "DEV_BAD_LENGTH", "DEV_TIMEOUT",
@@ -62,6 +63,9 @@ def _load() -> ctypes.CDLL:
         "rd_greedy_accept_noalloc": [P, I, I, I, P, P, P, I, I, P, P, P, P, P, P, P],
         "rd_tree_attention_paged": [I, I, I, I, I, F, P, P, P, P, P, I, I, P, I, P, I, P, P, I,
                                     P, P, S, P, P],
+        "rd_tree_attention_shared_workspace_size": [I, I, I, I, I, I, I],
+        "rd_tree_attention_shared": [I, I, I, I, I, F, P, P, P, P, P, I, I, P, I, P, I, I, P, P, P, P,
+                                     I, P, P, S, P, P],
         "rd_commit_accepted": [I, I, I, I, I, I, P, P, P, P, P, P, P, I, I, P, I, P, P, P, P],
         "rd_beam_search_step": [P, P, P, I, I, I, I, P, P, P, P, P],
         "rd_tree_attention_fp8": [I, I, I, I, I, F, P, P, P, P, P, F, F, P, I64, I, P, P, I, P, P,
@@ -344,6 +348,63 @@ def rd_tree_attention_paged(q, k_new, v_new, k_pool, v_pool, block_table, ctx_le
         _ptr(out), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _ptr(dev_status), stream=stream)
+    return out
+
+
+def rd_tree_attention_shared_workspace_size(B: int, P_max: int, Hq: int, Hkv: int, D: int, max_ctx: int,
+                                            n_groups: int, device=None) -> int:
+    """Bytes of workspace of rd_tree_attention_shared on `device` (else the current one)."""
+    f = _lib.rd_tree_attention_shared_workspace_size
+    if device is not None and torch.device(device).type == "cuda":
+        with torch.cuda.device(device):
+            return int(f(B, P_max, Hq, Hkv, D, max_ctx, n_groups))
+    return int(f(B, P_max, Hq, Hkv, D, max_ctx, n_groups))
+
+
+def rd_tree_attention_shared(q, k_new, v_new, k_pool, v_pool, block_table, ctx_lens, group_offsets,
+                             prefix_pages, packed_len, mask, *, max_ctx: int, scale: float = 0.0, out=None,
+                             workspace=None, dev_status=None, stream=None) -> torch.Tensor:
+    """rd_tree_attention_paged for groups of requests that share their leading
+    pages: group g is the requests group_offsets[g] .. group_offsets[g+1] - 1
+    (int32 [n_groups+1]) and shares prefix_pages[g] pages (int32 [n_groups]);
+    each prefix is read once for its group (see rd_tree_attention_shared in rd.h)."""
+    _need(q, "q", torch.bfloat16, ndim=4)
+    dev = q.device
+    for n, t in (("k_new", k_new), ("v_new", v_new), ("k_pool", k_pool), ("v_pool", v_pool)):
+        _need(t, n, torch.bfloat16, dev, ndim=4)
+    _need(block_table, "block_table", torch.int32, dev, ndim=2)
+    for n, t in (("ctx_lens", ctx_lens), ("group_offsets", group_offsets),
+                 ("prefix_pages", prefix_pages), ("packed_len", packed_len)):
+        _need(t, n, torch.int32, dev, ndim=1)
+    if (not isinstance(mask, torch.Tensor) or mask.dim() != 3 or not mask.is_contiguous()
+            or mask.element_size() != 4 or mask.device != dev):
+        raise ValueError("mask must be a contiguous 32-bit [B, P_max, NW] tensor on q's device")
+    B, P, Hq, D = q.shape
+    Hkv = k_new.shape[2]
+    n_groups = prefix_pages.shape[0]
+    if k_new.shape != (B, P, Hkv, D) or v_new.shape != k_new.shape:
+        raise ValueError("k_new/v_new must be [B, P_max, Hkv, D]")
+    if k_pool.shape[2:] != (Hkv, D) or v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool/v_pool must be [num_pages, page_size, Hkv, D]")
+    if (block_table.shape[0] != B or ctx_lens.shape[0] != B or packed_len.shape[0] != B
+            or mask.shape[0] != B or mask.shape[1] != P):
+        raise ValueError("block_table/ctx_lens/packed_len/mask do not match the batch")
+    if group_offsets.shape[0] != n_groups + 1:
+        raise ValueError(f"group_offsets must be [{n_groups + 1}], got {tuple(group_offsets.shape)}")
+    _need_status(dev_status, q)
+    out = _new(q.shape, torch.bfloat16, q, stream) if out is None else \
+        _out(out, "out", q.shape, torch.bfloat16, q)
+    if workspace is None:
+        workspace = _scratch(None, rd_tree_attention_shared_workspace_size(
+            B, P, Hq, Hkv, D, max_ctx, n_groups, dev), q, stream)
+    else:
+        workspace = _scratch(workspace, 0, q, stream)   # its size is checked by the call
+    _run("rd_tree_attention_shared", q,
+         B, P, Hq, Hkv, D, float(scale), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool),
+         _ptr(v_pool), k_pool.shape[0], k_pool.shape[1], _ptr(block_table), block_table.shape[1],
+         _ptr(ctx_lens), int(max_ctx), n_groups, _ptr(group_offsets), _ptr(prefix_pages),
+         _ptr(packed_len), _ptr(mask), mask.shape[2], _ptr(out), _ptr(workspace),
+         workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
     return out
 
 

@@ -81,13 +81,20 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when a max g
 constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
 constexpr int kSkMaxB = 480;               // chunk-range division up to this many requests
 constexpr uint32_t kSkMinChunks = 8;       // chunks per CTA at least (chunk-range division)
+// ... with a shared prefix: every unit's partials are merged with the prefix's
+// anyway, so a finer division costs no further launch
+constexpr uint32_t kSkMinChunksShared = rd_attn_plan::kSharedMinChunks;
 
-template <int D, bool F8 = false, bool PIPE = false> struct Cfg {
+template <int D, bool F8 = false, bool PIPE = false, bool SH = false> struct Cfg {
     // PIPE (the 16-bit path) pipelines S: two S tiles in tensor memory, so that S
     // of the next chunk is computed while the softmax warps work on this one,
     // with the queries in shared memory.  FP8 (whose shared memory holds the
     // 8-bit ring): one S tile and the queries in tensor memory.
     static_assert(F8 != PIPE, "every instantiation is the 16-bit pipelined path or the FP8 path");
+    // SH (shared prefix, shared_prefix.cu): a request's context starts behind the
+    // pages that its group shares; units and pieces leave fp32 partials of their
+    // valid rows for the merge with the prefix's.
+    static_assert(!SH || PIPE, "the shared-prefix variant is the 16-bit path");
     static constexpr bool kPipe = PIPE;
     static constexpr bool kMaySk = PIPE || F8;          // tree attention (chunk ranges possible)
     static constexpr int kNc = kN;                      // KV positions per chunk
@@ -158,6 +165,12 @@ struct TcArgs {
     // failure-detection test hook: > 0 makes the MMA issuer first wait, with
     // this clock budget, on a barrier that nothing completes
     long long stall_budget;
+    // shared prefix: positions of request b that its group's prefix covers, the
+    // partial rows of whole units, and where the chunk-range table goes
+    const int32_t* skip;
+    float* o_rows;
+    float2* ml_rows;
+    uint32_t* sk_table;
     // 16-bit path: the query tiles come by TMA (G a power of two <= 16) through
     // map_q128 (boxes of 128 / G rows x G heads x 64 columns) and map_q16 (16 / G
     // rows), else by plain loads of warp 6
@@ -193,6 +206,7 @@ struct UnitGeo {
     bool zero_tile;       // tree tile without valid rows: write zeros
     int n_rows;           // valid rows of (b, h)
     int64_t kv_base;      // first row of this request / sequence in the K/V map
+                          // (shared prefix: its first position behind the prefix)
     int C;                // context length
     int Pb;               // packed length
     int c_first, n_ctx;   // first context chunk and number of context chunks
@@ -204,15 +218,17 @@ struct UnitGeo {
 };
 
 // Lengths of request b; false (and zero lengths) if they are invalid.
+template <bool SH>
 __device__ __forceinline__ bool req_geo(const TcArgs& a, int b, UnitGeo& g)
 {
     bool bad;
     g.Pb = a.lens[b];
     if (a.block_table != nullptr) {
         const int c = a.ctx_lens[b];
-        g.kv_base = 0;
-        g.C = c;
-        bad = c < 0 || c > a.max_kv || (long long)c > (long long)a.max_pages * a.page_size ||
+        const int first = SH ? a.skip[b] : 0;
+        g.kv_base = first;
+        g.C = c - first;
+        bad = c < first || c > a.max_kv || (long long)c > (long long)a.max_pages * a.page_size ||
               g.Pb < 0 || g.Pb > a.P_max;
     } else {
         const int64_t c0 = a.ctx_offsets[b], c1 = a.ctx_offsets[b + 1];
@@ -230,7 +246,7 @@ __device__ __forceinline__ bool req_geo(const TcArgs& a, int b, UnitGeo& g)
 // kv head: the CTAs take units round-robin, and this order puts the tiles past
 // the valid rows of a tree batch (mostly padding) last instead of interleaving
 // them with the live units.
-template <int NC>
+template <int NC, bool SH>
 __device__ __forceinline__ UnitGeo unit_geo(const TcArgs& a, int u)
 {
     UnitGeo g;
@@ -243,7 +259,7 @@ __device__ __forceinline__ UnitGeo unit_geo(const TcArgs& a, int u)
     g.c_first = g.n_ctx = g.d_first = g.n_draft = 0;
     g.cut = false;
     g.split = 0;
-    const bool ok = req_geo(a, g.b, g);
+    const bool ok = req_geo<SH>(a, g.b, g);
     const int row0 = g.tile * kM;
     if (row0 >= g.n_rows) {
         g.zero_tile = row0 < a.P_max * a.G;
@@ -259,20 +275,22 @@ __device__ __forceinline__ UnitGeo unit_geo(const TcArgs& a, int u)
 // Chunk-range division over n = min(grid, W / kSkMinChunks) CTAs (at least one;
 // no range is empty, and none is so short that its pieces' partials and merge
 // cost more than the chunks): CTA c < n starts at chunk floor(c W / n).
+template <bool SH>
 __device__ __forceinline__ uint32_t sk_ctas(uint32_t W)
 {
-    return max(1u, min((uint32_t)gridDim.x, W / kSkMinChunks));
+    return max(1u, min((uint32_t)gridDim.x, W / (SH ? kSkMinChunksShared : kSkMinChunks)));
 }
+template <bool SH>
 __device__ __forceinline__ uint32_t sk_start(uint32_t W, int c)
 {
-    return (uint32_t)(((uint64_t)c * W) / sk_ctas(W));
+    return (uint32_t)(((uint64_t)c * W) / sk_ctas<SH>(W));
 }
 
 // The table: pre[b] = live chunks of requests before b (pre[B] = W), nb[b] =
 // chunks of one unit of request b (its context and draft chunks; zero without
 // valid rows), tiles of request b = (pre[b + 1] - pre[b]) / (Hkv nb[b]).  Built by
 // one warp before the roles start.
-template <int NC>
+template <int NC, bool SH>
 __device__ void sk_build(const TcArgs& a, uint32_t* pre, uint32_t* nb, int lane)
 {
     uint32_t carry = 0;
@@ -281,7 +299,7 @@ __device__ void sk_build(const TcArgs& a, uint32_t* pre, uint32_t* nb, int lane)
         uint32_t w = 0;
         if (b < a.B) {
             UnitGeo g;
-            if (!req_geo(a, b, g)) rd_flag(a.status, RD_DEV_BAD_LENGTH);
+            if (!req_geo<SH>(a, b, g)) rd_flag(a.status, RD_DEV_BAD_LENGTH);
             const int tiles = (g.n_rows + kM - 1) / kM;
             const uint32_t n = tiles > 0 ? (uint32_t)((g.C + NC - 1) / NC + (g.Pb + NC - 1) / NC) : 0u;
             nb[b] = n;
@@ -298,6 +316,16 @@ __device__ void sk_build(const TcArgs& a, uint32_t* pre, uint32_t* nb, int lane)
     }
     if (lane == 0) pre[0] = 0;
     __syncwarp();
+    if constexpr (SH) {
+        // the merge with the prefix finds a unit's pieces from the table itself
+        if (blockIdx.x == 0)
+            for (int b = lane; b < a.B; b += 32) {
+                a.sk_table[b] = pre[b];
+                a.sk_table[a.B + 1 + b] = nb[b];
+            }
+        if (blockIdx.x == 0 && lane == 0) a.sk_table[a.B] = carry;
+        return;
+    }
     // This CTA's merge descriptor: when its range starts inside a unit that began
     // in the previous CTA's range, that unit is cut and this CTA names it for the
     // merge kernel (unit id in tile-major order, its first CTA c0, its number of
@@ -305,10 +333,10 @@ __device__ void sk_build(const TcArgs& a, uint32_t* pre, uint32_t* nb, int lane)
     if (lane == 0) {
         int4 d = make_int4(-1, 0, 0, 0);
         const uint32_t W = carry;
-        const uint32_t n = W > 0 ? sk_ctas(W) : 0u;
+        const uint32_t n = W > 0 ? sk_ctas<SH>(W) : 0u;
         const int c = blockIdx.x;
         if (c >= 1 && (uint32_t)c < n) {
-            const uint32_t x = sk_start(W, c);
+            const uint32_t x = sk_start<SH>(W, c);
             int lo = 0, hi = a.B - 1;                       // last b with pre[b] <= x
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -317,7 +345,7 @@ __device__ void sk_build(const TcArgs& a, uint32_t* pre, uint32_t* nb, int lane)
             const uint32_t n_b = nb[lo];
             const uint32_t k = (x - pre[lo]) / n_b;
             const uint32_t U0 = pre[lo] + k * n_b;
-            const uint32_t prev = sk_start(W, c - 1);
+            const uint32_t prev = sk_start<SH>(W, c - 1);
             if (U0 < x && U0 >= prev) {
                 const int tile = (int)(k / a.Hkv), h = (int)(k % a.Hkv);
                 const uint32_t last = U0 + n_b - 1;
@@ -337,7 +365,7 @@ struct Work {
     int u;
     uint32_t x;
 };
-template <bool MAYSK>
+template <bool MAYSK, bool SH>
 __device__ __forceinline__ Work work_begin(const TcArgs& a, const uint32_t* pre)
 {
     Work w;
@@ -345,26 +373,26 @@ __device__ __forceinline__ Work work_begin(const TcArgs& a, const uint32_t* pre)
     w.x = 0u;
     if (MAYSK && a.sk) {
         const uint32_t W = pre[a.B];
-        w.x = blockIdx.x < sk_ctas(W) ? sk_start(W, blockIdx.x) : W;   // W: no work
+        w.x = blockIdx.x < sk_ctas<SH>(W) ? sk_start<SH>(W, blockIdx.x) : W;   // W: no work
     }
     return w;
 }
 
 // The CTA's next work item into g (round-robin: every unit, live or not; chunk
 // ranges: pieces of live units only); false when the CTA's work is done.
-template <int NC, bool MAYSK>
+template <int NC, bool MAYSK, bool SH>
 __device__ __forceinline__ bool work_next(const TcArgs& a, const uint32_t* pre, const uint32_t* nb,
                                           Work& w, UnitGeo& g)
 {
     if (!(MAYSK && a.sk)) {
         if (w.u >= a.n_units) return false;
-        g = unit_geo<NC>(a, w.u);
+        g = unit_geo<NC, SH>(a, w.u);
         w.u += gridDim.x;
         return true;
     }
     const uint32_t W = pre[a.B];
-    if (blockIdx.x >= sk_ctas(W)) return false;
-    const uint32_t end = sk_start(W, blockIdx.x + 1);
+    if (blockIdx.x >= sk_ctas<SH>(W)) return false;
+    const uint32_t end = sk_start<SH>(W, blockIdx.x + 1);
     if (w.x >= end) return false;
     int lo = 0, hi = a.B - 1;                               // last b with pre[b] <= x
     while (lo < hi) {
@@ -380,7 +408,7 @@ __device__ __forceinline__ bool work_next(const TcArgs& a, const uint32_t* pre, 
     g.b = b;
     g.tile = (int)(k / a.Hkv);
     g.h = (int)(k % a.Hkv);
-    req_geo(a, b, g);
+    req_geo<SH>(a, b, g);
     g.live = true;
     g.zero_tile = false;
     const int n_cc = (g.C + NC - 1) / NC;
@@ -391,7 +419,7 @@ __device__ __forceinline__ bool work_next(const TcArgs& a, const uint32_t* pre, 
     g.cut = !(cb == 0 && ce == (int)n_b);
     // the unit starts inside this CTA's range (not at its start) and is cut: the
     // range's last piece, slot 2 c + 1; otherwise slot 2 c
-    g.split = 2 * (int)blockIdx.x + ((g.cut && cb == 0 && U0 > sk_start(W, blockIdx.x)) ? 1 : 0);
+    g.split = 2 * (int)blockIdx.x + ((g.cut && cb == 0 && U0 > sk_start<SH>(W, blockIdx.x)) ? 1 : 0);
     w.x = U0 + ce;
     return true;
 }
@@ -446,7 +474,7 @@ __device__ __forceinline__ bool warp_wait_lean(uint64_t* bar, uint32_t parity, v
     return __all_sync(0xffffffffu, ok);
 }
 
-template <int D, bool F8, bool PIPE>
+template <int D, bool F8, bool PIPE, bool SH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map_kc,
                          const __grid_constant__ CUtensorMap map_vc,
@@ -455,7 +483,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                          const __grid_constant__ CUtensorMap map_q128,
                          const __grid_constant__ CUtensorMap map_q16)
 {
-    using C = Cfg<D, F8, PIPE>;
+    using C = Cfg<D, F8, PIPE, SH>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -468,7 +496,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
     // the merge launch that follows a chunk-range launch may start now: its CTAs
     // wait (griddepcontrol.wait) until this grid has completed and its writes are
     // visible, so only their launch overlaps this kernel's tail
-    if (C::kMaySk && a.sk) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (C::kMaySk && (SH || a.sk)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -505,7 +533,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
     uint32_t* sk_pre = reinterpret_cast<uint32_t*>(smem + C::kSkOff);
     uint32_t* sk_nb = sk_pre + kSkMaxB + 1;
     if constexpr (C::kMaySk) {
-        if (a.sk && warp == 0) sk_build<C::kNc>(a, sk_pre, sk_nb, lane);
+        if (a.sk && warp == 0) sk_build<C::kNc, SH>(a, sk_pre, sk_nb, lane);
     }
     if (warp == kProducerWarp && lane == 0) {
         tma_prefetch_desc(&map_kc);
@@ -535,9 +563,9 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
         // ------------------------------------------------- producer (8-bit context)
         if (lane == 0) {
             uint32_t g8 = 0;                              // context chunks only
-            Work wk = work_begin<C::kMaySk>(a, sk_pre);
+            Work wk = work_begin<C::kMaySk, SH>(a, sk_pre);
             UnitGeo geo;
-            while (!*abort && work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, wk, geo)) {
+            while (!*abort && work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, wk, geo)) {
                 if (!geo.live) continue;
                 bool ok = true;
                 for (int j = 0; j < geo.n_ctx; ++j, ++g8) {
@@ -598,9 +626,9 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 *reinterpret_cast<uint4*>(dst + (c >> 3) * (C::kNc * 128) + sw128(row, c & 7)) = y;
             }
         };
-        Work wk = work_begin<C::kMaySk>(a, sk_pre);
+        Work wk = work_begin<C::kMaySk, SH>(a, sk_pre);
         UnitGeo geo;
-        while (!*abort && work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, wk, geo)) {
+        while (!*abort && work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, wk, geo)) {
             if (!geo.live) continue;
             const int n = geo.n_ctx + geo.n_draft;
             bool ok = true;
@@ -651,7 +679,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             };
             auto seek = [&](Cursor& c) {                  // the next live item from c.w on
                 UnitGeo geo;
-                while ((c.more = work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, c.w, geo))) {
+                while ((c.more = work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, c.w, geo))) {
                     if (!geo.live) continue;
                     c.j = 0;
                     c.n = geo.n_ctx + geo.n_draft;
@@ -673,7 +701,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             auto locate = [&](const Cursor& c, bool is_v, const CUtensorMap*& map) -> int {
                 if (c.j < c.n_ctx) {
                     map = is_v ? &map_vc : &map_kc;
-                    const int pos0 = (c.c_first + c.j) * kN;
+                    const int pos0 = (c.c_first + c.j) * kN + (SH ? (int)c.kv_base : 0);
                     if (!paged) return (int)(c.kv_base + pos0);
                     int pg = __ldg(a.block_table + (size_t)c.b * a.max_pages + pos0 / a.page_size);
                     if (pg < 0 || pg >= a.num_pages) {
@@ -702,7 +730,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 return true;
             };
             Cursor ck;
-            ck.w = work_begin<C::kMaySk>(a, sk_pre);
+            ck.w = work_begin<C::kMaySk, SH>(a, sk_pre);
             seek(ck);
             Cursor cv = ck;
             uint32_t gk = 0, gv = 0;                      // K and V chunks issued
@@ -766,9 +794,9 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             return reinterpret_cast<const uint4*>(a.q + (qrow * a.Hq + ug.h * a.G + qr % a.G) * D);
         };
         uint32_t it = 0;
-        Work wk = work_begin<C::kMaySk>(a, sk_pre);
+        Work wk = work_begin<C::kMaySk, SH>(a, sk_pre);
         UnitGeo geo;
-        while (!*abort && work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, wk, geo)) {
+        while (!*abort && work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, wk, geo)) {
             if (!geo.live) continue;
             if (it > 0 && !warp_wait(&bar.q_free, (it - 1) & 1, abort, kWaitBudget)) { fail(); break; }
             if (a.q_tma) {
@@ -779,7 +807,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                     });
                     Work w2 = wk;
                     UnitGeo nx;
-                    if (work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, w2, nx) && nx.live)
+                    if (work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, w2, nx) && nx.live)
                         for_boxes(nx, [&](const CUtensorMap* map, int, int x, int y, int z) {
                             tma_prefetch_3d(map, x, y, z);
                         });
@@ -811,9 +839,9 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
         // ------------------------------------------------ producer (one K + V ring)
         if (lane == 0) {
             uint32_t g = 0;                               // global chunk counter
-            Work wk = work_begin<C::kMaySk>(a, sk_pre);
+            Work wk = work_begin<C::kMaySk, SH>(a, sk_pre);
             UnitGeo geo;
-            while (!*abort && work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, wk, geo)) {
+            while (!*abort && work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, wk, geo)) {
                 if (!geo.live) continue;
                 const int n = geo.n_ctx + geo.n_draft;
                 // first cache row of context chunk j (paged: looked up one chunk ahead,
@@ -885,9 +913,9 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                                               C::kNc * 128, 1024, kSwizzle128B);
             const uint64_t q_desc = smem_desc(smem_addr(smem + C::kQOff), 16, 1024, kSwizzle128B);
             if (a.stall_budget > 0 && !mbar_wait(&bar.never, 0, abort, a.stall_budget)) fail();
-            Work wk = work_begin<C::kMaySk>(a, sk_pre);
+            Work wk = work_begin<C::kMaySk, SH>(a, sk_pre);
             UnitGeo geo;
-            while (!*abort && work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, wk, geo)) {
+            while (!*abort && work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, wk, geo)) {
                 if (!geo.live) continue;
                 const int n = geo.n_ctx + geo.n_draft;
                 if (!mbar_wait(&bar.q_full, unit_iter & 1, abort, kWaitBudget)) { fail(); break; }
@@ -1045,7 +1073,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
         };
         uint32_t g = 0, unit_iter = 0;
         bool q_ready = false;                              // (not PIPE) the next item's queries are written
-        Work wk = work_begin<C::kMaySk>(a, sk_pre);
+        Work wk = work_begin<C::kMaySk, SH>(a, sk_pre);
         UnitGeo geo;
         bool have_next = false;                            // (not PIPE) the next item, looked up ahead
         Work next_w;
@@ -1055,7 +1083,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 geo = next_geo;
                 wk = next_w;
                 have_next = false;
-            } else if (!work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, wk, geo)) {
+            } else if (!work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, wk, geo)) {
                 break;
             }
             // the words the next unit's geometry needs, into L1 now (its loads then
@@ -1063,7 +1091,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             if (!(C::kMaySk && a.sk) && wk.u < a.n_units) prefetch_geo(a, wk.u);
             const int hq0 = geo.h * a.G;
             if (geo.zero_tile) {                           // padded rows of a tree tile
-                zero_tile(geo.b, geo.h, geo.tile);
+                if constexpr (!SH) zero_tile(geo.b, geo.h, geo.tile);   // (SH: the merge writes them)
                 continue;
             }
             if (!geo.live) continue;
@@ -1212,6 +1240,30 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 } else {
                     if (!chunk(std::integral_constant<int, 64>{}, j, gg, sc)) { ok = false; break; }
                 }
+                if constexpr (SH) {
+                    // Rows of V past the context's or the drafts' end hold whatever the
+                    // page or the next request does; a zero weight times an infinity or
+                    // NaN there would spoil the row's sum.  Zero them (16 rows a warp)
+                    // before this chunk's PV, which waits for P below.
+                    const bool ctx = j < geo.n_ctx;
+                    const int live = ctx ? geo.C - (geo.c_first + j) * C::kNc
+                                         : geo.Pb - (geo.d_first + j - geo.n_ctx) * C::kNc;
+                    if (live < C::kNc) {
+                        const int st = (int)(gg % C::kStages);
+                        if (!warp_wait(&bar.v_full[st], (gg / C::kStages) & 1, abort, kWaitBudget)) {
+                            ok = false;
+                            break;
+                        }
+                        unsigned char* v = smem + C::kVOff + st * C::kKBytes;
+                        for (int i = lane; i < 16 * 8 * C::kDB; i += 32) {
+                            const int vr = warp * 16 + (i / 8) % 16, db = i / 128;
+                            if (vr >= live)
+                                *reinterpret_cast<uint4*>(v + db * (C::kNc * 128) + vr * 128 + (i & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -1223,7 +1275,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             if constexpr (!C::kQTma) {
                 if (ok && !warp_wait(&bar.q_free, unit_iter & 1, abort, kWaitBudget)) ok = false;
                 next_w = wk;
-                if (ok && work_next<C::kNc, C::kMaySk>(a, sk_pre, sk_nb, next_w, next_geo)) {
+                if (ok && work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, next_w, next_geo)) {
                     have_next = true;
                     if (next_geo.live) {
                         tc_fence_after();
@@ -1257,7 +1309,26 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             }
             auto mine = [&](int cb) { return !paired || (cb >= D / 64) == (hf == 1); };
             const bool split_mode = geo.cut;
-            if (!split_mode) {
+            if constexpr (SH) {
+                // fp32 partial rows (D floats each, with (m, l) apart): row (b, p, hq) of a
+                // whole unit, row r of its slot for a piece
+                if (valid) {
+                    const size_t at = split_mode ? (size_t)geo.split * kM + r
+                                                 : ((size_t)geo.b * a.P_max + qpos) * a.Hq + hq0 + row % a.G;
+                    float4* op = reinterpret_cast<float4*>((split_mode ? a.o_part : a.o_rows) + at * D);
+#pragma unroll
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        if (mine(cb)) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                op[cb * 8 + q] =
+                                    make_float4(__uint_as_float(ob[cb][4 * q]), __uint_as_float(ob[cb][4 * q + 1]),
+                                                __uint_as_float(ob[cb][4 * q + 2]), __uint_as_float(ob[cb][4 * q + 3]));
+                        }
+                    }
+                    if (hf == 0) (split_mode ? a.ml_part : a.ml_rows)[at] = make_float2(m, l_row);
+                }
+            } else if (!split_mode) {
                 const float inv = (valid && l_row > 0.f) ? a.out_scale / l_row : 0.f;
                 const bool write = qpos < a.P_max;         // valid rows, and padded rows as zeros
                 uint16_t* dst = nullptr;
@@ -1319,7 +1390,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
         }
         // chunk-range division: the tiles past each request's valid rows (the
         // chunk ranges hold live units only), round-robin
-        if (C::kMaySk && a.sk && !*abort) {
+        if (C::kMaySk && !SH && a.sk && !*abort) {
             const int bh = a.B * a.Hkv;
             for (int idx = blockIdx.x; idx < a.n_units; idx += gridDim.x) {
                 const int tile = idx / bh, b = (idx % bh) / a.Hkv, h = idx % a.Hkv;
@@ -1442,18 +1513,18 @@ bool make_fp8_map(CUtensorMap* map, const void* base, int64_t rows, int heads, i
 
 // One launch of an instantiation (dynamic shared memory set per call: cheap, and
 // the attribute must be set on every device the library runs on).
-template <int D, bool F8, bool PIPE>
+template <int D, bool F8, bool PIPE, bool SH = false>
 cudaError_t launch(int grid, cudaStream_t stream, const TcArgs& a, const CUtensorMap& m0,
                    const CUtensorMap& m1, const CUtensorMap& m2, const CUtensorMap& m3,
                    const CUtensorMap& m4, const CUtensorMap& m5)
 {
-    using Cf = Cfg<D, F8, PIPE>;
-    cudaError_t e = cudaFuncSetAttribute(tree_attention_tc_kernel<D, F8, PIPE>,
+    using Cf = Cfg<D, F8, PIPE, SH>;
+    cudaError_t e = cudaFuncSetAttribute(tree_attention_tc_kernel<D, F8, PIPE, SH>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::kSmemBytes);
     if (e != cudaSuccess) return e;
-    tree_attention_tc_kernel<D, F8, PIPE><<<grid, kThreads, Cf::kSmemBytes, stream>>>(a, m0, m1, m2, m3, m4, m5);
+    tree_attention_tc_kernel<D, F8, PIPE, SH><<<grid, kThreads, Cf::kSmemBytes, stream>>>(a, m0, m1, m2, m3, m4, m5);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !a.sk) return e;
+    if (SH || e != cudaSuccess || !a.sk) return e;      // SH: the caller merges
     // chunk-range division: merge the units that CTA boundaries cut, launched as a
     // programmatic dependent (its launch overlaps the attention kernel's tail)
     cudaLaunchConfig_t cfg = {};
@@ -1506,7 +1577,7 @@ cudaError_t rd_launch_attention(const rd_attn_plan& plan, int B, int P_max,
                                 const int32_t* lens, const uint32_t* mask, int mask_words,
                                 void* o, void* workspace, int32_t* dev_status,
                                 cudaStream_t stream, const rd_paged_kv* paged,
-                                const rd_fp8_kv* fp8)
+                                const rd_fp8_kv* fp8, const rd_shared_suffix* shared)
 {
     TcArgs a;
     a.block_table = paged ? paged->block_table : nullptr;
@@ -1544,7 +1615,18 @@ cudaError_t rd_launch_attention(const rd_attn_plan& plan, int B, int P_max,
         a.out_scale = fp8->v_scale;
         a.scale_log2 *= fp8->k_scale;
     }
-    if (plan.stream_k) {
+    a.skip = nullptr;
+    a.o_rows = nullptr;
+    a.ml_rows = nullptr;
+    a.sk_table = nullptr;
+    if (shared != nullptr) {
+        a.skip = shared->skip;
+        a.o_rows = shared->o_rows;
+        a.ml_rows = shared->ml_rows;
+        a.o_part = shared->o_part;
+        a.ml_part = shared->ml_part;
+        a.sk_table = shared->sk_table;
+    } else if (plan.stream_k) {
         const size_t slot_rows = (size_t)2 * plan.grid * kM;
         a.o_part = static_cast<float*>(workspace);
         a.ml_part = reinterpret_cast<float2*>(a.o_part + slot_rows * D);
@@ -1581,6 +1663,9 @@ cudaError_t rd_launch_attention(const rd_attn_plan& plan, int B, int P_max,
               make_q_map(&mq128, q, q_rows, Hq, D, a.G, kM / a.G) &&
               make_q_map(&mq16, q, q_rows, Hq, D, a.G, 16 / a.G);
     if (!a.q_tma) { mq128 = mkc; mq16 = mkc; }
+    if (shared != nullptr)
+        return D == 128 ? launch<128, false, true, true>(grid, stream, a, mkc, mvc, mkd, mvd, mq128, mq16)
+                        : launch<64, false, true, true>(grid, stream, a, mkc, mvc, mkd, mvd, mq128, mq16);
     return D == 128 ? launch<128, false, true>(grid, stream, a, mkc, mvc, mkd, mvd, mq128, mq16)
                     : launch<64, false, true>(grid, stream, a, mkc, mvc, mkd, mvd, mq128, mq16);
 }

@@ -18,6 +18,7 @@
 
 #include <algorithm>
 
+#include "block_scan.cuh"
 #include "rd_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -27,8 +28,8 @@ namespace {
 
 // ------------------------------------------------------------- table kernels
 constexpr int kTableCtas = 8;              // one cluster
-constexpr int kTableThreads = 1024;
-constexpr int kTableWarps = kTableThreads / RD_WARP;
+constexpr int kTableThreads = kScanThreads;
+constexpr int kTableWarps = kScanWarps;
 static_assert(RD_MAX_PAGES == kTableCtas * kTableWarps * 32 * 32, "one 32-page word per lane");
 
 struct ScanSmem {
@@ -36,30 +37,6 @@ struct ScanSmem {
     int cta_total[kTableCtas];             // written by every CTA of the cluster
     int boundary;                          // rd_compact_pages: live pages below n_live
 };
-
-// Exclusive scan of one int per thread over the CTA; `total` is the CTA's sum.
-__device__ __forceinline__ int cta_scan(int x, int* warp_sum, int& total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += y;
-    }
-    __syncthreads();                       // the previous scan's readers are done
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int w = warp_sum[lane];                // kTableWarps == 32
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, d);
-        if (lane >= d) w += y;
-    }
-    total = __shfl_sync(0xffffffffu, w, 31);
-    const int before = __shfl_sync(0xffffffffu, w, warp - 1);
-    return (warp > 0 ? before : 0) + incl - x;
-}
 
 // Exclusive scan of f(i), i < n, into out[0 .. n] (out[n] = the sum): thread t
 // takes a contiguous share.

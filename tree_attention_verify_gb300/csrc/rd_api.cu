@@ -197,6 +197,62 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
                                          dev_status, (cudaStream_t)stream, &pg));
 }
 
+size_t rd_tree_attention_shared_workspace_size(int B, int P_max, int Hq, int Hkv, int D, int max_ctx,
+                                               int n_groups)
+{
+    if (n_groups <= 0) return rd_tree_attention_workspace_size(B, P_max, Hq, Hkv, D, max_ctx);
+    if (B <= 0 || P_max < 1 || !attn_shape_ok(Hq, Hkv, D) || max_ctx < 0 || D < 1) return 0;
+    return rd_shared_workspace_bytes(B, P_max, Hq, Hkv, D, max_ctx, n_groups);
+}
+
+rd_status rd_tree_attention_shared(int B, int P_max, int Hq, int Hkv, int D, float scale,
+                                   const void* q, const void* k_new, const void* v_new,
+                                   const void* k_pool, const void* v_pool, int num_pages,
+                                   int page_size, const int32_t* block_table, int max_pages,
+                                   const int32_t* ctx_lens, int max_ctx, int n_groups,
+                                   const int32_t* group_offsets, const int32_t* prefix_pages,
+                                   const int32_t* packed_len, const uint32_t* mask,
+                                   int mask_words, void* o, void* workspace, size_t ws_bytes,
+                                   int32_t* dev_status, rd_stream_t stream)
+{
+    if (n_groups < 0) return RD_ERR_INVALID_ARG;
+    if (n_groups == 0 || num_pages == 0 || B <= 0)          /* nothing is shared */
+        return rd_tree_attention_paged(B, P_max, Hq, Hkv, D, scale, q, k_new, v_new, k_pool, v_pool,
+                                       num_pages, page_size, block_table, max_pages, ctx_lens, max_ctx,
+                                       packed_len, mask, mask_words, o, workspace, ws_bytes, dev_status,
+                                       stream);
+    if (P_max < 1 || !attn_shape_ok(Hq, Hkv, D) || num_pages < 0 || max_pages < 0 || max_ctx < 0 ||
+        page_size < 1)
+        return RD_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return RD_ERR_UNSUPPORTED;
+    if (page_size % 64 != 0) return RD_ERR_UNSUPPORTED;
+    if (P_max > RD_MAX_PACKED || B > 65535 || Hkv > 65535 || n_groups > 65535) return RD_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size > 0x7fffffffLL) return RD_ERR_UNSUPPORTED;
+    /* the prefix's chunks of 128 positions x 256 rows, counted in 32 bits */
+    if (((long long)B * P_max * (Hq / Hkv) / 256 + n_groups) * Hkv * (max_ctx / 128 + 1LL) > 0x7fffffffLL)
+        return RD_ERR_UNSUPPORTED;
+    if (mask_words != (P_max + 31) / 32) return RD_ERR_INVALID_ARG;
+    if (!q || !k_new || !v_new || !k_pool || !v_pool || !block_table || !ctx_lens || !group_offsets ||
+        !prefix_pages || !packed_len || !mask || !o || !workspace)
+        return RD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) ||
+        !aligned16(v_pool) || !aligned16(o) || !aligned16(workspace))
+        return RD_ERR_INVALID_ARG;
+    if (ws_bytes < rd_shared_workspace_bytes(B, P_max, Hq, Hkv, D, max_ctx, n_groups))
+        return RD_ERR_INVALID_ARG;
+    if (scale <= 0.f) scale = 1.0f / sqrtf((float)D);
+    rd_paged_kv pg;
+    pg.block_table = block_table;
+    pg.ctx_lens = ctx_lens;
+    pg.max_pages = max_pages;
+    pg.page_size = page_size;
+    pg.num_pages = num_pages;
+    return from_cuda(rd_launch_shared_attention(B, P_max, Hq, Hkv, D, scale, q, k_new, v_new, k_pool, v_pool,
+                                                pg, max_ctx, n_groups, group_offsets, prefix_pages,
+                                                packed_len, mask, mask_words, o, workspace, dev_status,
+                                                (cudaStream_t)stream));
+}
+
 rd_status rd_commit_accepted(int B, int W, int L, int P_max, int Hkv, int D,
                              const void* k_new, const void* v_new, const int32_t* unpacker,
                              const int32_t* best_beam, const int32_t* n_accepted,

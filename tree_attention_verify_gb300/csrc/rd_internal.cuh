@@ -63,6 +63,7 @@ struct rd_attn_plan {
     bool stream_k;     // chunk-range division (tree attention), else whole units round-robin
     int grid;          // CTAs of the launch
     size_t ws_bytes;   // workspace bytes needed (chunk ranges: partials of cut units)
+    static constexpr unsigned kSharedMinChunks = 2;   // chunks per CTA at least, with a shared prefix
 };
 struct rd_paged_kv {
     const int32_t* block_table;   // [B, max_pages]
@@ -74,6 +75,16 @@ struct rd_fp8_kv {
     const void* v_cache;
     float k_scale, v_scale;
 };
+// The part of a shared-prefix call behind the prefix (shared_prefix.cu): partial
+// rows instead of outputs.
+struct rd_shared_suffix {
+    const int32_t* skip;     // [B] positions that the group's prefix covers
+    float* o_rows;           // [B, P_max, Hq, D] rows of whole units, with (m, l)
+    float2* ml_rows;
+    float* o_part;           // [2 grid, 128, D] rows of pieces (chunk ranges)
+    float2* ml_part;
+    uint32_t* sk_table;      // [B + 1] chunks before a request, [B] chunks of a unit
+};
 rd_attn_plan rd_attn_make_plan(int B, int P_max, int Hq, int Hkv, int D, int max_kv);
 cudaError_t rd_launch_attention(const rd_attn_plan& plan, int B, int P_max,
                                 int Hq, int Hkv, int D, float scale, const void* q,
@@ -83,7 +94,8 @@ cudaError_t rd_launch_attention(const rd_attn_plan& plan, int B, int P_max,
                                 const int32_t* lens, const uint32_t* mask, int mask_words,
                                 void* o, void* workspace, int32_t* dev_status,
                                 cudaStream_t stream, const rd_paged_kv* paged = nullptr,
-                                const rd_fp8_kv* fp8 = nullptr);
+                                const rd_fp8_kv* fp8 = nullptr,
+                                const rd_shared_suffix* shared = nullptr);
 
 // Causal prefill with paired 128-row query tiles, one CTA per SM (causal_pair.cu).
 cudaError_t rd_launch_causal_pair(int B, int Hq, int Hkv, int D, float scale, const void* q,
@@ -102,6 +114,16 @@ cudaError_t rd_launch_beam_step(const void* logits, const float* scores_in,
                                 const int32_t* beams_in, int B, int W, int V, int t,
                                 int32_t* beams_out, float* scores_out, int32_t* parent,
                                 int32_t* dev_status, cudaStream_t stream);
+
+// Tree attention of groups that share a prefix (shared_prefix.cu).
+size_t rd_shared_workspace_bytes(int B, int P_max, int Hq, int Hkv, int D, int max_ctx, int n_groups);
+cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D, float scale, const void* q,
+                                       const void* k_new, const void* v_new, const void* k_pool,
+                                       const void* v_pool, const rd_paged_kv& paged, int max_ctx,
+                                       int n_groups, const int32_t* group_offsets,
+                                       const int32_t* prefix_pages, const int32_t* packed_len,
+                                       const uint32_t* mask, int mask_words, void* o, void* workspace,
+                                       int32_t* dev_status, cudaStream_t stream);
 
 // Page operators of the paged cache (pages.cu).
 struct rd_page_pools {

@@ -1,0 +1,1019 @@
+// rd_tree_attention_shared: tree attention over a paged cache for a batch whose
+// groups of requests share a long prefix, the prefix read once per group.
+//
+// Softmax attention splits over its keys: with partials
+//   m_i = max_k s_k, l_i = sum_k 2^(s_k - m_i), O_i = sum_k 2^(s_k - m_i) v_k
+// over disjoint key sets i, the output is sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
+// with M = max_i m_i.  So the prefix of a group is one dense product of all its
+// requests' rows with the shared keys, and the rest of each request is the
+// paged tree attention from behind the prefix.  Four launches on one stream:
+//   plan    one CTA: valid requests, the compact list of a group's live rows,
+//           and the table that divides the prefix work over the CTAs;
+//   prefix  (below) fp32 partials of every live row over its group's prefix;
+//   suffix  attention_tc.cu, shared-prefix variant: partials of every row over
+//           its own context and drafts;
+//   merge   the formula above, rounded once to bf16; zeros in padded rows.
+//
+// The prefix kernel: unit = (group, kv head, 256 rows), the rows being the G
+// query heads of each live node of the group, in request order.  One CTA per SM
+// with two 128-row tiles, K and V in chunks of 128 positions.  Every position is
+// visible to every row (whole pages), so there is no mask at all.  The units'
+// chunks form one sequence that the CTAs take in equal ranges, so that one group
+// with few rows still fills the GPU; a unit cut by a range boundary leaves its
+// pieces to the merge.
+// Warp roles (384 threads):
+//   warps 0-3, 4-7  softmax of tile A, of tile B: row r is TMEM lane r.  S from
+//              TMEM, online softmax in exp2 form (O rescaled only when a row
+//              maximum grows by more than 2^8), bf16 P written over S.
+//   warp 8     producer: K_0, V_0, K_1, V_1, ... by TMA into one ring
+//   warp 9     MMA issuer: per chunk j and tile t, O_t += P_t V_j, then S_t of
+//              chunk j + 1, so that the tensor core works on one tile while the
+//              other's softmax runs
+//   warps 10-11  the unit's query rows into shared memory (cp.async, row list),
+//              then the check that a group's tables name the same pages
+// Every wait is bounded by a clock budget; on expiry the CTA records
+// RD_DEV_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "block_scan.cuh"
+#include "rd_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace {
+using namespace rdtc;
+using namespace rdattn;
+
+constexpr int kM = 128;                    // rows per tile = TMEM lanes
+constexpr int kUnitRows = 2 * kM;
+constexpr int kN = 128;                    // KV positions per chunk (two TMA boxes)
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kQWarp0 = 10;                // two query warps
+// Register split: 384 threads launch with 168 registers each (64,512); the two
+// softmax warpgroups take 200 (a row's 128 scores stay in registers), the third
+// keeps 104: 128 x (200 + 200 + 104) = 64,512, per sub-partition 32 x 504.
+constexpr int kRegsLaunch = 168;
+constexpr int kRegsSoftmax = 200;
+constexpr int kRegsOther = 104;
+static_assert(128 * (2 * kRegsSoftmax + kRegsOther) <= kThreads * kRegsLaunch, "register split");
+static_assert(32 * (2 * kRegsSoftmax + kRegsOther) <= 16384, "register split per sub-partition");
+constexpr uint32_t kMinChunks = 2;         // chunks per CTA at least
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
+
+// What the plan kernel leaves in the workspace.
+struct Group {
+    int node0, nodes;      // its live nodes in the compact list
+    int positions;         // prefix length
+    int leader;            // its first request, whose table names the pages
+};
+struct Plan {
+    int32_t* eff_len;      // [B] packed length, 0: the request is skipped
+    int32_t* skip;         // [B] prefix positions of the request
+    int32_t* gid;          // [B] its group, -1: no prefix
+    int32_t* node_base;    // [B + 1] its first node in the compact list
+    int32_t* node_row;     // [B P_max] compact node -> b P_max + p
+    Group* group;          // [n_groups]
+    uint32_t* first;       // [n_groups + 1] chunks of the groups before
+    // partials: rows of whole units, and of pieces (two slots per CTA)
+    float* pre_rows;       // [compact node, Hq, D]
+    float2* pre_ml;
+    float* pre_part;       // [2 grid, 256, D]
+    float2* pre_part_ml;
+    float* suf_rows;       // [B, P_max, Hq, D]
+    float2* suf_ml;
+    float* suf_part;       // [2 suffix grid, 128, D]
+    float2* suf_part_ml;
+    uint32_t* sk_table;    // the suffix's chunk-range table
+};
+
+// ------------------------------------------------------------------------ plan
+struct PlanArgs {
+    int B, P_max, Hkv, G, page_size, max_pages, max_ctx, n_groups;
+    const int32_t* lens;
+    const int32_t* ctx_lens;
+    const int32_t* group_offsets;
+    const int32_t* prefix_pages;
+    Plan p;
+    int32_t* status;
+};
+
+__global__ void __launch_bounds__(kScanThreads, 1)
+plan_kernel(const PlanArgs a)
+{
+    __shared__ int warp_sum[kScanWarps];
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // offsets that do not ascend within [0, B] would give a request two groups:
+    // then nobody shares (the results stay the same)
+    bool bad_offsets = false;
+    for (int g = tid; g < a.n_groups; g += kScanThreads) {
+        const int o0 = a.group_offsets[g], o1 = a.group_offsets[g + 1];
+        bad_offsets = bad_offsets || o0 < 0 || o1 < o0 || o1 > a.B;
+    }
+    bad_offsets = __syncthreads_or(bad_offsets);
+    if (bad_offsets && tid == 0) rd_flag(a.status, RD_DEV_BAD_INDEX);
+    auto pages_of = [&](int g) {
+        const int n = a.prefix_pages[g];
+        return n < 0 || n > a.max_pages || (long long)n * a.page_size > a.max_ctx ? -1 : n;
+    };
+    int carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
+        const int b = b0 + tid;
+        int n = 0, len = 0;
+        if (b < a.B) {
+            int g = -1, skip = 0;
+            if (!bad_offsets) {
+                int lo = 0, hi = a.n_groups;               // groups that start at or before b
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (a.group_offsets[mid] <= b) lo = mid + 1; else hi = mid;
+                }
+                if (lo > 0 && b < a.group_offsets[lo]) {
+                    const int pg = pages_of(lo - 1);
+                    if (pg > 0) {
+                        g = lo - 1;
+                        skip = pg * a.page_size;
+                    }
+                }
+            }
+            const int c = a.ctx_lens[b];
+            len = a.lens[b];
+            if (c < skip || c > a.max_ctx || (long long)c > (long long)a.max_pages * a.page_size || len < 0 ||
+                len > a.P_max) {
+                rd_flag(a.status, RD_DEV_BAD_LENGTH);
+                len = 0;
+            }
+            a.p.eff_len[b] = len;
+            a.p.skip[b] = skip;
+            a.p.gid[b] = g;
+            n = g >= 0 ? len : 0;
+        }
+        int total;
+        const int at = carry + cta_scan(n, warp_sum, total);
+        if (b < a.B) {
+            a.p.node_base[b] = at;
+            for (int p = 0; p < n; ++p) a.p.node_row[at + p] = b * a.P_max + p;
+        }
+        carry += total;
+    }
+    if (tid == 0) a.p.node_base[a.B] = carry;
+    __syncthreads();
+    uint32_t chunks = 0;
+    for (int g0 = 0; g0 < a.n_groups; g0 += kScanThreads) {
+        const int g = g0 + tid;
+        int w = 0;
+        if (g < a.n_groups) {
+            Group grp = {0, 0, 0, 0};
+            if (!bad_offsets) {
+                const int pg = pages_of(g);
+                if (pg < 0) rd_flag(a.status, RD_DEV_BAD_LENGTH);
+                grp.leader = a.group_offsets[g];
+                grp.node0 = a.p.node_base[grp.leader];
+                grp.nodes = a.p.node_base[a.group_offsets[g + 1]] - grp.node0;
+                grp.positions = max(0, pg) * a.page_size;
+                const int units = a.Hkv * ((grp.nodes * a.G + kUnitRows - 1) / kUnitRows);
+                w = units * ((grp.positions + kN - 1) / kN);
+            }
+            a.p.group[g] = grp;
+        }
+        int total;
+        const int at = cta_scan(w, warp_sum, total);
+        if (g < a.n_groups) a.p.first[g] = chunks + at;
+        chunks += total;
+    }
+    if (tid == 0) a.p.first[a.n_groups] = chunks;
+}
+
+// ---------------------------------------------------------------------- prefix
+template <int D> struct Cfg {
+    static constexpr int kDB = D / 64;                  // 128-byte column blocks
+    static constexpr int kStageBytes = kN * D * 2;      // one chunk of K or of V
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kQBytes = kM * D * 2;          // one tile's queries
+    static constexpr int kQOff = kStages * kStageBytes;
+    static constexpr int kBarOff = kQOff + 2 * kQBytes;
+    static constexpr int kSmemBytes = kBarOff + 512 + 1024;   // + barriers + alignment slack
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    // TMEM (512 columns): S of tile t (P over its first half), O of tile t
+    static constexpr uint32_t kTmemCols = 512;
+    __host__ __device__ static constexpr uint32_t s_col(int t) { return 128u * t; }
+    __host__ __device__ static constexpr uint32_t o_col(int t) { return 256u + 128u * t; }
+};
+
+struct PrefixArgs {
+    int B, Hq, Hkv, G, page_size, max_pages, num_pages, n_groups;
+    float scale_log2;
+    const uint16_t* q;                     // [B P_max, Hq, D]
+    const int32_t* block_table;
+    Plan p;
+    int32_t* status;
+    long long stall_budget;                // failure-detection test hook
+};
+
+struct Bar {
+    uint64_t kv_full[8];
+    uint64_t kv_empty[8];
+    uint64_t q_full;          // the unit's query tiles are in shared memory
+    uint64_t q_free;          // every S MMA of the unit has completed
+    uint64_t s_full[2];       // S of the tile's chunk is in TMEM (and PV of the one before is done)
+    uint64_t p_full[2];       // P of the tile's chunk is written (four softmax warps)
+    uint64_t o_final[2];      // the tile's last PV of the unit has completed
+    uint64_t o_free[2];       // the tile's epilogue has read O
+    uint64_t drain;
+    uint64_t never;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Bar) <= 512, "barrier block");
+
+// CTAs that take part, and CTA c's first chunk, of a sequence of W chunks
+__host__ __device__ __forceinline__ uint32_t range_ctas(uint32_t W, uint32_t grid, uint32_t least)
+{
+    const uint32_t n = W / least;
+    return n < 1u ? 1u : (n < grid ? n : grid);
+}
+__device__ __forceinline__ uint32_t range_start(uint32_t W, uint32_t n, uint32_t c)
+{
+    return (uint32_t)(((uint64_t)c * W) / n);
+}
+// the CTA whose range holds chunk x
+__device__ __forceinline__ uint32_t range_of(uint32_t W, uint32_t n, uint32_t x)
+{
+    return (uint32_t)((((uint64_t)x + 1) * n - 1) / W);
+}
+
+// One piece of a unit (all of it, unless cut).
+struct Piece {
+    int h, row0;              // kv head; first row of the unit within its group
+    int rows;                 // rows of the unit (1 .. 256)
+    int c0, n;                // chunks [c0, c0 + n)
+    int slot;                 // piece slot, -1: a whole unit
+    Group g;
+};
+
+// This CTA's range of the chunk sequence, in pieces.
+struct Walk {
+    uint32_t x, end, start;
+    __device__ __forceinline__ void begin(const PrefixArgs& a)
+    {
+        const uint32_t W = a.p.first[a.n_groups];
+        x = end = start = 0u;
+        if (W == 0u) return;
+        const uint32_t n = range_ctas(W, gridDim.x, kMinChunks);
+        if (blockIdx.x >= n) return;
+        x = start = range_start(W, n, blockIdx.x);
+        end = range_start(W, n, blockIdx.x + 1);
+    }
+    __device__ __forceinline__ bool next(const PrefixArgs& a, Piece& u)
+    {
+        if (x >= end) return false;
+        int lo = 0, hi = a.n_groups - 1;                    // last group with first <= x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.p.first[mid] <= x) lo = mid; else hi = mid - 1;
+        }
+        u.g = a.p.group[lo];
+        const uint32_t base = a.p.first[lo];
+        const uint32_t n = (uint32_t)(u.g.positions + kN - 1) / kN;
+        const int all = u.g.nodes * a.G;
+        const uint32_t pairs = (uint32_t)(all + kUnitRows - 1) / kUnitRows;
+        const uint32_t unit = (x - base) / n;
+        const uint32_t u0 = base + unit * n;
+        u.h = (int)(unit / pairs);
+        u.row0 = (int)(unit % pairs) * kUnitRows;
+        u.rows = min(kUnitRows, all - u.row0);
+        u.c0 = (int)(x - u0);
+        const uint32_t stop = min(u0 + n, end);
+        u.n = (int)(stop - x);
+        u.slot = (uint32_t)u.n == n ? -1 : 2 * (int)blockIdx.x + (u.c0 == 0 && u0 > start ? 1 : 0);
+        x = stop;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v)
+{
+    using C = Cfg<D>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bar& bar = *reinterpret_cast<Bar*>(smem + C::kBarOff);
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &bar.abort;
+    volatile int no_abort = 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&bar.kv_full[i], 1);
+            mbar_init(&bar.kv_empty[i], 1);
+        }
+        mbar_init(&bar.q_full, 2);
+        mbar_init(&bar.q_free, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bar.s_full[t], 1);
+            mbar_init(&bar.p_full[t], 4);
+            mbar_init(&bar.o_final[t], 1);
+            mbar_init(&bar.o_free[t], 4);
+        }
+        mbar_init(&bar.drain, 1);
+        mbar_init(&bar.never, 1);
+        bar.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&bar.tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem_base;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the plan is written
+    auto fail = [&]() {
+        *abort = 1;
+        rd_flag(a.status, RD_DEV_TIMEOUT);
+    };
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            uint32_t g = 0;                               // ring entries issued
+            Walk w;
+            w.begin(a);
+            Piece u;
+            while (!*abort && w.next(a, u)) {
+                const int32_t* table = a.block_table + (size_t)u.g.leader * a.max_pages;
+                auto row_of = [&](int pos) -> int {       // pool row of a position of the prefix
+                    int pg = __ldg(table + pos / a.page_size);
+                    if (pg < 0 || pg >= a.num_pages) {
+                        rd_flag(a.status, RD_DEV_BAD_INDEX);
+                        pg = 0;
+                    }
+                    return pg * a.page_size + pos % a.page_size;
+                };
+                // the rows of a chunk's two halves, looked up one chunk ahead
+                auto rows_of = [&](int c, int (&z)[2]) {
+                    const int pos = c * kN;
+                    z[0] = row_of(pos);
+                    z[1] = pos + 64 < u.g.positions ? row_of(pos + 64) : -1;
+                };
+                int z[2], nz[2];
+                rows_of(u.c0, nz);
+                bool ok = true;
+                for (int j = 0; ok && j < u.n; ++j) {
+                    z[0] = nz[0];
+                    z[1] = nz[1];
+                    if (j + 1 < u.n) rows_of(u.c0 + j + 1, nz);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++g) {
+                        const int st = (int)(g % C::kStages);
+                        if (g >= (uint32_t)C::kStages &&
+                            !mbar_wait(&bar.kv_empty[st], ((g / C::kStages) - 1) & 1, abort, kWaitBudget)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bar.kv_full[st], z[1] >= 0 ? C::kStageBytes : C::kStageBytes / 2);
+                        unsigned char* dst = smem + st * C::kStageBytes;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (z[half] < 0) continue;
+#pragma unroll
+                            for (int db = 0; db < C::kDB; ++db)
+                                tma_load_3d(dst + db * (kN * 128) + half * (64 * 128), kv ? &map_v : &map_k,
+                                            &bar.kv_full[st], db * 64, u.h, z[half]);
+                        }
+                    }
+                }
+                if (!ok) { fail(); break; }
+            }
+            // drain: every issued copy must land before the CTA may exit
+            for (uint32_t k = g > (uint32_t)C::kStages ? g - C::kStages : 0u; k < g; ++k)
+                mbar_wait(&bar.kv_full[k % C::kStages], (k / C::kStages) & 1, &no_abort, kWaitBudget);
+        }
+    } else if (warp >= kQWarp0) {
+        // ------------------------------------------------------- query loader
+        // Row m of the unit is head row % G of compact node row / G.  16-byte
+        // pieces, all in flight at once; rows past the unit's are zero.
+        const int t0 = tid - kQWarp0 * 32;                // 0 .. 63
+        uint32_t it = 0;
+        Walk w;
+        w.begin(a);
+        Piece u;
+        while (!*abort && w.next(a, u)) {
+            if (it > 0 && !warp_wait(&bar.q_free, (it - 1) & 1, abort, kWaitBudget)) { fail(); break; }
+            constexpr int kVecs = D / 8;                  // 16-byte pieces of a row
+            const int m_end = u.rows > kM ? kUnitRows : kM;
+#pragma unroll 4
+            for (int i = t0; i < m_end * kVecs; i += 64) {
+                const int m = i / kVecs, c = i % kVecs;
+                unsigned char* dst = smem + C::kQOff + (m / kM) * C::kQBytes + (c >> 3) * (kM * 128) +
+                                     sw128(m % kM, c & 7);
+                if (m < u.rows) {
+                    const int row = u.row0 + m;
+                    const size_t node = a.p.node_row[u.g.node0 + row / a.G];
+                    cp_async16(dst, a.q + (node * a.Hq + u.h * a.G + row % a.G) * D + c * 8);
+                } else {
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.q_full);
+            ++it;
+        }
+        // the tables of a group's requests have to name its first one's pages
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            const int g = a.p.gid[b];
+            if (g < 0) continue;
+            const Group grp = a.p.group[g];
+            const int32_t* mine = a.block_table + (size_t)b * a.max_pages;
+            const int32_t* first = a.block_table + (size_t)grp.leader * a.max_pages;
+            bool differ = false;
+            for (int j = t0; j < grp.positions / a.page_size; j += 64) differ = differ || mine[j] != first[j];
+            if (differ) rd_flag(a.status, RD_DEV_BAD_INDEX);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        // The MMAs of one thread run in issue order, so S_t(j + 1) may overwrite
+        // P_t(j) right behind PV_t(j), and the commit that completes it also
+        // covers PV_t(j): softmax t finds O_t stable when it rescales.
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_bf16(kM, kN, false, false);
+            constexpr uint32_t idSh = idesc_bf16(kM, kN / 2, false, false);
+            constexpr uint32_t idPV = idesc_bf16(kM, D, false, true);
+            const uint64_t k_desc = smem_desc(smem_addr(smem), 16, 1024, kSwizzle128B);
+            const uint64_t v_desc = smem_desc(smem_addr(smem), kN * 128, 1024, kSwizzle128B);
+            const uint64_t q_desc = smem_desc(smem_addr(smem + C::kQOff), 16, 1024, kSwizzle128B);
+            if (a.stall_budget > 0 && !mbar_wait(&bar.never, 0, abort, a.stall_budget)) fail();
+            uint32_t g = 0, it = 0;                       // ring entries, units
+            uint32_t ct[2] = {0u, 0u};                    // chunks of tile t so far
+            uint32_t ut[2] = {0u, 0u};                    // units with tile t so far
+            Walk w;
+            w.begin(a);
+            Piece u;
+            while (!*abort && w.next(a, u)) {
+                const int nb = u.rows > kM ? 2 : 1;       // active tiles
+                // positions of the piece's chunk j: 64 in a prefix's odd last half
+                auto half = [&](int j) { return (u.c0 + j) * kN + 64 >= u.g.positions; };
+                auto stage = [&](uint32_t k) { return (int)(k % C::kStages); };
+                auto full = [&](uint32_t k) {
+                    return mbar_wait(&bar.kv_full[stage(k)], (k / C::kStages) & 1, abort, kWaitBudget);
+                };
+                auto issue_s = [&](int t, int j) {
+                    const uint64_t kd = k_desc + (uint64_t)((stage(g + 2 * j) * C::kStageBytes) >> 4);
+                    const uint64_t qd = q_desc + (uint64_t)((t * C::kQBytes) >> 4);
+                    const uint32_t id = half(j) ? idSh : idS;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * (kM * 128) + (ks & 3) * 32) >> 4;
+                        mma_smem_a(tmem + C::s_col(t), qd + off, kd + off, id, ks > 0);
+                    }
+                    mma_commit(&bar.s_full[t]);
+                };
+                bool ok = mbar_wait(&bar.q_full, it & 1, abort, kWaitBudget) && full(g);
+                if (!ok) { fail(); break; }
+                tc_fence_after();
+                for (int t = 0; t < nb; ++t) issue_s(t, 0);
+                mma_commit(&bar.kv_empty[stage(g)]);
+                if (u.n == 1) mma_commit(&bar.q_free);
+                for (int j = 0; ok && j < u.n; ++j) {
+                    const uint32_t kv = g + 2 * j + 1;    // ring entry of V_j; K_{j+1} is the next
+                    for (int t = 0; t < nb; ++t) {
+                        if (t == 0 && !full(kv)) { ok = false; break; }
+                        if (j == 0 && ut[t] > 0 && !mbar_wait(&bar.o_free[t], (ut[t] - 1) & 1, abort, kWaitBudget)) {
+                            ok = false;
+                            break;
+                        }
+                        if (!mbar_wait(&bar.p_full[t], (ct[t] + j) & 1, abort, kWaitBudget)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint64_t vd = v_desc + (uint64_t)((stage(kv) * C::kStageBytes) >> 4);
+                        const int steps = half(j) ? kN / 32 : kN / 16;
+#pragma unroll
+                        for (int kk = 0; kk < kN / 16; ++kk)
+                            if (kk < steps)
+                                mma_tmem_a(tmem + C::o_col(t), tmem + C::s_col(t) + kk * 8,
+                                           vd + (uint64_t)((kk * 2048) >> 4), idPV, j > 0 || kk > 0);
+                        if (t == nb - 1) mma_commit(&bar.kv_empty[stage(kv)]);
+                        if (j + 1 < u.n) {
+                            if (t == 0 && !full(kv + 1)) { ok = false; break; }
+                            tc_fence_after();
+                            issue_s(t, j + 1);
+                            if (t == nb - 1) {
+                                mma_commit(&bar.kv_empty[stage(kv + 1)]);
+                                if (j + 1 == u.n - 1) mma_commit(&bar.q_free);
+                            }
+                        } else {
+                            mma_commit(&bar.o_final[t]);
+                        }
+                    }
+                }
+                if (!ok) { fail(); break; }
+                for (int t = 0; t < nb; ++t) {
+                    ct[t] += u.n;
+                    ++ut[t];
+                }
+                g += 2 * u.n;
+                ++it;
+            }
+            // drain: every issued MMA must finish before TMEM is freed
+            mma_commit(&bar.drain);
+            mbar_wait(&bar.drain, 0, &no_abort, kWaitBudget);
+        }
+    }
+    } else {
+        // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int t = warp >> 2;                          // tile
+        const int r = tid & (kM - 1);                     // row of the tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t sc = tmem + lane_base + C::s_col(t);
+        const uint32_t oc = tmem + lane_base + C::o_col(t);
+        uint32_t ct = 0, ut = 0;
+        Walk w;
+        w.begin(a);
+        Piece u;
+        while (!*abort && w.next(a, u)) {
+            const int row = t * kM + r;                   // row of the unit
+            if (t == 1 && u.rows <= kM) continue;
+            const bool valid = row < u.rows;
+            // a warp without a valid row leaves S where P belongs: its rows of O are
+            // never read
+            const bool dead = __all_sync(0xffffffffu, !valid);
+            float m = -INFINITY, l = 0.f;
+            // one chunk: NC = 128 positions, or the 64 of an odd last half
+            auto chunk = [&](auto nc, bool first) {
+                constexpr int NC = decltype(nc)::value;
+                uint32_t s[NC];
+#pragma unroll
+                for (int c = 0; c < NC / 32; ++c)
+                    tmem_ld32(sc + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+                tmem_ld_wait();
+                float mx8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx8[e] = __uint_as_float(s[e]);
+#pragma unroll
+                for (int c = 8; c < NC; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], __uint_as_float(s[c]));
+                const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                const float ms = mx * a.scale_log2;
+                const bool need = ms > m + kRescaleThreshold;
+                if (__any_sync(0xffffffffu, need) && !first) {
+                    const float alpha = need ? fast_exp2(m - ms) : 1.f;
+#pragma unroll
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        uint32_t o[32];
+                        tmem_ld32(oc + cb * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                        tmem_st32(oc + cb * 32, o);
+                    }
+                }
+                if (need) {
+                    l *= fast_exp2(m - ms);               // 0 while m is -inf
+                    m = ms;
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < NC / 64; ++h) {
+                    uint32_t pv[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float p0 = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * e]), a.scale_log2, -base));
+                        const float p1 = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * e + 1]), a.scale_log2, -base));
+                        sum[(2 * e) & 7] += p0;
+                        sum[(2 * e + 1) & 7] += p1;
+                        pv[e] = pack_bf16(p0, p1);
+                    }
+                    tmem_st32(sc + 32 * h, pv);
+                }
+                l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+            };
+            bool ok = true;
+            for (int j = 0; j < u.n; ++j) {
+                if (!warp_wait(&bar.s_full[t], (ct + j) & 1, abort, kWaitBudget)) { ok = false; break; }
+                tc_fence_after();
+                if (!dead) {
+                    if ((u.c0 + j) * kN + 64 < u.g.positions)
+                        chunk(std::integral_constant<int, 128>{}, j == 0);
+                    else
+                        chunk(std::integral_constant<int, 64>{}, j == 0);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[t]);
+            }
+            if (!ok || !warp_wait(&bar.o_final[t], ut & 1, abort, kWaitBudget)) { fail(); break; }
+            tc_fence_after();
+            uint32_t o[D / 32][32];
+#pragma unroll
+            for (int cb = 0; cb < D / 32; ++cb) tmem_ld32(oc + cb * 32, o[cb]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.o_free[t]);
+            if (valid) {
+                // fp32 partial row: unnormalised O, and (m, l)
+                size_t at;
+                if (u.slot < 0) {
+                    const int gr = u.row0 + row;
+                    at = (size_t)(u.g.node0 + gr / a.G) * a.Hq + u.h * a.G + gr % a.G;
+                } else {
+                    at = (size_t)u.slot * kUnitRows + row;
+                }
+                float4* dst = reinterpret_cast<float4*>((u.slot < 0 ? a.p.pre_rows : a.p.pre_part) + at * D);
+#pragma unroll
+                for (int cb = 0; cb < D / 32; ++cb)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[cb * 8 + i] = make_float4(__uint_as_float(o[cb][4 * i]), __uint_as_float(o[cb][4 * i + 1]),
+                                                      __uint_as_float(o[cb][4 * i + 2]),
+                                                      __uint_as_float(o[cb][4 * i + 3]));
+                (u.slot < 0 ? a.p.pre_ml : a.p.pre_part_ml)[at] = make_float2(m, l);
+            }
+            ct += u.n;
+            ++ut;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// ----------------------------------------------------------------------- merge
+// CTA = (node (b, p), a run of heads).  A row's partials are its unit's pieces of
+// the prefix, then those of the suffix; lane i of a warp holds (m, l) of piece i
+// and each lane D / 32 columns.  WPR warps share a row's pieces when there are
+// few rows (a short batch is cut into many pieces).
+struct MergeArgs {
+    int B, P_max, Hq, Hkv, G, n_groups, heads;   // heads per CTA
+    uint32_t pre_grid, suf_grid;
+    bool suf_sk;
+    Plan p;
+    uint16_t* o;
+};
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
+
+// the pieces of one row: the first `n` of the slots s0, then 2 (c0 + 1), 2 (c0 + 2), ...
+struct Pieces {
+    const float* o;           // row 0 of the whole-unit rows, or of the slots
+    const float2* ml;
+    size_t row0, step;        // first piece's row; rows from slot to slot
+    size_t row1;              // second piece's row
+    int n;
+    __device__ __forceinline__ size_t row(int i) const { return i == 0 ? row0 : row1 + (size_t)(i - 1) * step; }
+};
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(kMergeThreads)
+merge_kernel(const MergeArgs a)
+{
+    constexpr int V = D / 32;                     // columns per lane
+    __shared__ float part_o[WPR > 1 ? kMergeWarps * D : 1];
+    __shared__ float2 part_ml[WPR > 1 ? kMergeWarps : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blocks = (a.Hq + a.heads - 1) / a.heads;
+    const int node = blockIdx.x / blocks;         // b P_max + p
+    const int h0 = (blockIdx.x % blocks) * a.heads, h1 = min(a.Hq, h0 + a.heads);
+    const int b = node / a.P_max, p = node % a.P_max;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool live = p < a.p.eff_len[b];
+    const int gid = a.p.gid[b];
+    Group grp = {0, 0, 0, 0};
+    uint32_t gfirst = 0, W = 0;
+    if (gid >= 0) {
+        grp = a.p.group[gid];
+        gfirst = a.p.first[gid];
+        W = a.p.first[a.n_groups];
+    }
+    const int cnode = a.p.node_base[b] + p;       // compact node
+    for (int hq = h0 + warp / WPR; hq < h1; hq += kMergeWarps / WPR) {
+        uint16_t* dst = a.o + ((size_t)node * a.Hq + hq) * D + lane * V;
+        if (!live) {
+            if (warp % WPR == 0) {
+                if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(0, 0);
+                else *reinterpret_cast<uint32_t*>(dst) = 0u;
+            }
+            continue;
+        }
+        const int h = hq / a.G, gq = hq % a.G;
+        Pieces pre = {}, suf = {};
+        if (gid >= 0) {
+            const uint32_t n = (uint32_t)(grp.positions + kN - 1) / kN;
+            const int row = (cnode - grp.node0) * a.G + gq;
+            const uint32_t pairs = (uint32_t)(grp.nodes * a.G + kUnitRows - 1) / kUnitRows;
+            const uint32_t u0 = gfirst + ((uint32_t)h * pairs + row / kUnitRows) * n;
+            const uint32_t nc = range_ctas(W, a.pre_grid, kMinChunks);
+            const uint32_t c0 = range_of(W, nc, u0), c1 = range_of(W, nc, u0 + n - 1);
+            pre.n = (int)(c1 - c0) + 1;
+            if (pre.n == 1) {
+                pre.o = a.p.pre_rows;
+                pre.ml = a.p.pre_ml;
+                pre.row0 = (size_t)cnode * a.Hq + hq;
+            } else {
+                pre.o = a.p.pre_part;
+                pre.ml = a.p.pre_part_ml;
+                const size_t r = row % kUnitRows;
+                pre.row0 = (size_t)(2 * c0 + (u0 > range_start(W, nc, c0) ? 1 : 0)) * kUnitRows + r;
+                pre.row1 = (size_t)(2 * (c0 + 1)) * kUnitRows + r;
+                pre.step = 2 * kUnitRows;
+            }
+        }
+        {
+            const int row = p * a.G + gq;
+            suf.n = 1;
+            suf.o = a.p.suf_rows;
+            suf.ml = a.p.suf_ml;
+            suf.row0 = (size_t)node * a.Hq + hq;
+            if (a.suf_sk) {
+                const uint32_t Ws = a.p.sk_table[a.B];
+                const uint32_t n = a.p.sk_table[a.B + 1 + b];
+                const uint32_t u0 = a.p.sk_table[b] + (uint32_t)((row / kM) * a.Hkv + h) * n;
+                const uint32_t nc = range_ctas(Ws, a.suf_grid, rd_attn_plan::kSharedMinChunks);
+                const uint32_t c0 = range_of(Ws, nc, u0), c1 = range_of(Ws, nc, u0 + n - 1);
+                if (c1 > c0) {
+                    suf.n = (int)(c1 - c0) + 1;
+                    suf.o = a.p.suf_part;
+                    suf.ml = a.p.suf_part_ml;
+                    const size_t r = row % kM;
+                    suf.row0 = (size_t)(2 * c0 + (u0 > range_start(Ws, nc, c0) ? 1 : 0)) * kM + r;
+                    suf.row1 = (size_t)(2 * (c0 + 1)) * kM + r;
+                    suf.step = 2 * kM;
+                }
+            }
+        }
+        const int n = pre.n + suf.n;
+        float M = -INFINITY, L = 0.f;
+        float acc[V];
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = 0.f;
+        // this warp's pieces: (warp % WPR), + WPR, ... in batches of 32
+        for (int i0 = warp % WPR; i0 < n; i0 += 32 * WPR) {
+            const int i = i0 + lane * WPR;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            const float* src = nullptr;
+            if (i < n) {
+                const Pieces& s = i < pre.n ? pre : suf;
+                const size_t at = s.row(i < pre.n ? i : i - pre.n);
+                ml = __ldcg(s.ml + at);
+                src = s.o + at * D;
+            }
+            float mx = ml.x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float Mn = fmaxf(M, mx);
+            if (Mn == -INFINITY) {                // no visible key (l = 0), or every score a NaN
+                float l0 = ml.y;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+                L += l0;
+                continue;
+            }
+            const float keep = exp2f(M - Mn);     // 0 while M is -inf
+            M = Mn;
+            const float wgt = exp2f(ml.x - M);
+            float lsum = ml.y * wgt;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, d);
+            L = L * keep + lsum;
+#pragma unroll
+            for (int c = 0; c < V; ++c) acc[c] *= keep;
+            const int cnt = min(32, (n - i0 + WPR - 1) / WPR);
+#pragma unroll 4
+            for (int k = 0; k < cnt; ++k) {
+                const float* from = reinterpret_cast<const float*>(
+                    __shfl_sync(0xffffffffu, (unsigned long long)src, k));
+                const float x = __shfl_sync(0xffffffffu, wgt, k);
+                if constexpr (V == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(from) + lane);
+                    acc[0] += v.x * x; acc[1] += v.y * x; acc[2] += v.z * x; acc[3] += v.w * x;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(from) + lane);
+                    acc[0] += v.x * x; acc[1] += v.y * x;
+                }
+            }
+        }
+        if constexpr (WPR > 1) {
+            __syncthreads();                      // one row per CTA and turn: uniform
+#pragma unroll
+            for (int c = 0; c < V; ++c) part_o[warp * D + lane * V + c] = acc[c];
+            if (lane == 0) part_ml[warp] = make_float2(M, L);
+            __syncthreads();
+            if (warp != 0) continue;
+            float Ma = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kMergeWarps; ++k) Ma = fmaxf(Ma, part_ml[k].x);
+            L = 0.f;
+#pragma unroll
+            for (int c = 0; c < V; ++c) acc[c] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMergeWarps; ++k) {
+                const float x = part_ml[k].x == -INFINITY ? 0.f : exp2f(part_ml[k].x - Ma);
+                L += part_ml[k].y * x;
+#pragma unroll
+                for (int c = 0; c < V; ++c) acc[c] += part_o[k * D + lane * V + c] * x;
+            }
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        if constexpr (V == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
+                                                        pack_bf16(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+// Workspace layout; `base` null: the size only.
+size_t layout(Plan& p, unsigned char* base, int B, int P_max, int Hq, int D, int n_groups, int pre_grid,
+              const rd_attn_plan& suffix)
+{
+    size_t at = 0;
+    auto take = [&](auto*& ptr, size_t n) {
+        using T = std::remove_reference_t<decltype(*ptr)>;
+        ptr = base == nullptr ? nullptr : reinterpret_cast<T*>(base + at);
+        at += (n * sizeof(T) + 255) & ~size_t(255);
+    };
+    const size_t rows = (size_t)B * P_max * Hq;
+    const size_t pre = (size_t)2 * pre_grid * kUnitRows;
+    const size_t suf = suffix.stream_k ? (size_t)2 * suffix.grid * kM : 0;
+    take(p.eff_len, B);
+    take(p.skip, B);
+    take(p.gid, B);
+    take(p.node_base, (size_t)B + 1);
+    take(p.node_row, (size_t)B * P_max);
+    take(p.group, n_groups);
+    take(p.first, (size_t)n_groups + 1);
+    take(p.sk_table, 2 * (size_t)B + 1);
+    take(p.pre_rows, rows * D);
+    take(p.pre_ml, rows);
+    take(p.pre_part, pre * D);
+    take(p.pre_part_ml, pre);
+    take(p.suf_rows, rows * D);
+    take(p.suf_ml, rows);
+    take(p.suf_part, suf * D);
+    take(p.suf_part_ml, suf);
+    return at;
+}
+
+cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <int D>
+cudaError_t launch_prefix(int grid, cudaStream_t stream, PrefixArgs& a, CUtensorMap& mk, CUtensorMap& mv)
+{
+    cudaError_t e = cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Cfg<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&a, &mk, &mv};
+    return launch_dependent(reinterpret_cast<const void*>(prefix_kernel<D>), dim3(grid), dim3(kThreads),
+                            Cfg<D>::kSmemBytes, stream, args);
+}
+
+template <int D>
+cudaError_t launch_merge(cudaStream_t stream, MergeArgs& a)
+{
+    const long long sms = rd_device_sm_count();
+    const long long nodes = (long long)a.B * a.P_max;
+    // few rows: a CTA per row, its warps sharing the row's pieces (which a short
+    // batch has many of); else eight rows at a time per CTA, and as many heads as
+    // leave a few CTAs per SM
+    const bool few = nodes * a.Hq <= 8 * sms;
+    a.heads = few ? 1 : a.Hq;
+    while (!few && a.heads > kMergeWarps && nodes * ((a.Hq + a.heads - 1) / a.heads) < 8 * sms)
+        a.heads = std::max(kMergeWarps, a.heads / 2);
+    const long long grid = nodes * ((a.Hq + a.heads - 1) / a.heads);
+    void* args[] = {&a};
+    return launch_dependent(few ? reinterpret_cast<const void*>(merge_kernel<D, kMergeWarps>)
+                                : reinterpret_cast<const void*>(merge_kernel<D, 1>),
+                            dim3((unsigned)grid), dim3(kMergeThreads), 0, stream, args);
+}
+
+}  // namespace
+
+size_t rd_shared_workspace_bytes(int B, int P_max, int Hq, int Hkv, int D, int max_ctx, int n_groups)
+{
+    Plan p;
+    return layout(p, nullptr, B, P_max, Hq, D, n_groups, rd_device_sm_count(),
+                  rd_attn_make_plan(B, P_max, Hq, Hkv, D, max_ctx));
+}
+
+cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D, float scale, const void* q,
+                                       const void* k_new, const void* v_new, const void* k_pool,
+                                       const void* v_pool, const rd_paged_kv& paged, int max_ctx,
+                                       int n_groups, const int32_t* group_offsets,
+                                       const int32_t* prefix_pages, const int32_t* packed_len,
+                                       const uint32_t* mask, int mask_words, void* o, void* workspace,
+                                       int32_t* dev_status, cudaStream_t stream)
+{
+    const rd_attn_plan suffix = rd_attn_make_plan(B, P_max, Hq, Hkv, D, max_ctx);
+    const int pre_grid = rd_device_sm_count();
+    PlanArgs pa = {};
+    pa.B = B;
+    pa.P_max = P_max;
+    pa.Hkv = Hkv;
+    pa.G = Hq / Hkv;
+    pa.page_size = paged.page_size;
+    pa.max_pages = paged.max_pages;
+    pa.max_ctx = max_ctx;
+    pa.n_groups = n_groups;
+    pa.lens = packed_len;
+    pa.ctx_lens = paged.ctx_lens;
+    pa.group_offsets = group_offsets;
+    pa.prefix_pages = prefix_pages;
+    pa.status = dev_status;
+    layout(pa.p, static_cast<unsigned char*>(workspace), B, P_max, Hq, D, n_groups, pre_grid, suffix);
+    plan_kernel<<<1, kScanThreads, 0, stream>>>(pa);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+
+    PrefixArgs fa = {};
+    fa.B = B;
+    fa.Hq = Hq;
+    fa.Hkv = Hkv;
+    fa.G = pa.G;
+    fa.page_size = paged.page_size;
+    fa.max_pages = paged.max_pages;
+    fa.num_pages = paged.num_pages;
+    fa.n_groups = n_groups;
+    fa.scale_log2 = scale * kLog2e;
+    fa.q = static_cast<const uint16_t*>(q);
+    fa.block_table = paged.block_table;
+    fa.p = pa.p;
+    fa.status = dev_status;
+    fa.stall_budget = rd_attention_stall_budget();
+    CUtensorMap mk, mv;
+    const int64_t pool_rows = (int64_t)paged.num_pages * paged.page_size;
+    if (!make_kv_map(&mk, k_pool, pool_rows, Hkv, D) || !make_kv_map(&mv, v_pool, pool_rows, Hkv, D))
+        return cudaErrorInvalidValue;
+    e = D == 128 ? launch_prefix<128>(pre_grid, stream, fa, mk, mv) : launch_prefix<64>(pre_grid, stream, fa, mk, mv);
+    if (e != cudaSuccess) return e;
+
+    rd_shared_suffix sh;
+    sh.skip = pa.p.skip;
+    sh.o_rows = pa.p.suf_rows;
+    sh.ml_rows = pa.p.suf_ml;
+    sh.o_part = pa.p.suf_part;
+    sh.ml_part = pa.p.suf_part_ml;
+    sh.sk_table = pa.p.sk_table;
+    e = rd_launch_attention(suffix, B, P_max, Hq, Hkv, D, scale, q, k_new, v_new, k_pool, v_pool, nullptr, 0, max_ctx,
+                            pa.p.eff_len, mask, mask_words, o, nullptr, dev_status, stream, &paged, nullptr, &sh);
+    if (e != cudaSuccess) return e;
+
+    MergeArgs ma = {};
+    ma.B = B;
+    ma.P_max = P_max;
+    ma.Hq = Hq;
+    ma.Hkv = Hkv;
+    ma.G = pa.G;
+    ma.n_groups = n_groups;
+    ma.pre_grid = pre_grid;
+    ma.suf_grid = suffix.grid;
+    ma.suf_sk = suffix.stream_k;
+    ma.p = pa.p;
+    ma.o = static_cast<uint16_t*>(o);
+    return D == 128 ? launch_merge<128>(stream, ma) : launch_merge<64>(stream, ma);
+}
