@@ -116,6 +116,18 @@ CASES = {
     "whole units": dict(B=40, W=2, L=3, Hq=40, Hkv=40, D=64, page=128, offsets=[0, 20, 40], pages=[4, 7], suffix=130),
     "more requests than the table": dict(B=500, W=1, L=2, Hq=4, Hkv=2, D=128, page=64, offsets=[0, 1, 499, 500],
                                          pages=[2, 5, 1], suffix=90),
+    # 64 rows per kv head and one more; 16, 32, 33 and 48 of them
+    "64 rows": dict(B=6, W=4, L=4, Hq=8, Hkv=2, D=128, page=64, offsets=[0, 6], pages=[5], suffix=500),
+    "66 rows": dict(B=6, W=11, L=1, Hq=12, Hkv=2, D=128, page=64, offsets=[0, 6], pages=[5], suffix=500),
+    "64 rows d64": dict(B=3, W=8, L=8, Hq=4, Hkv=4, D=64, page=64, offsets=[0, 3], pages=[3], suffix=700),
+    "16 rows": dict(B=5, W=4, L=2, Hq=8, Hkv=4, D=128, page=128, offsets=[1, 5], pages=[2], suffix=300),
+    "32 rows d64": dict(B=5, W=4, L=4, Hq=8, Hkv=4, D=64, page=128, offsets=[0, 5], pages=[2], suffix=300),
+    "33 rows": dict(B=7, W=11, L=1, Hq=6, Hkv=2, D=64, page=64, offsets=[0, 7], pages=[1], suffix=129),
+    "48 rows": dict(B=4, W=8, L=6, Hq=3, Hkv=3, D=128, page=256, offsets=[0, 4], pages=[1], suffix=1000),
+    # two requests whose own contexts are long: cut into many pieces
+    "long own contexts": dict(B=2, W=2, L=4, Hq=8, Hkv=2, D=128, page=64, offsets=[0, 2], pages=[4], suffix=6000),
+    "long own contexts, one token": dict(B=2, W=1, L=1, Hq=8, Hkv=1, D=64, page=64, offsets=[0, 2], pages=[1],
+                                         suffix=9000),
     "long": dict(B=3, W=5, L=4, Hq=4, Hkv=2, D=128, page=64, offsets=[0, 3], pages=[129], suffix=200),
 }
 

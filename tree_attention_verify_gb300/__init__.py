@@ -101,15 +101,13 @@ def lib_path() -> str:
 # marshalling helpers
 # ----------------------------------------------------------------------------
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
-
-
-def _stream(stream, device=None) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return None if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, name: str, dtype, device=None, ndim=None):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (device is None or t.device == device) and (ndim is None or t.dim() == ndim)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -124,6 +122,13 @@ def _need(t: torch.Tensor, name: str, dtype, device=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
 
 
+# A call of a few microseconds on the GPU waits for its host side, so the binding
+# asks torch for plain integers: the current stream's handle (of a device's index),
+# the current device's index.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _check(fn: str, status: int):
     if status != RD_OK:
         raise RdError(fn, status)
@@ -132,11 +137,13 @@ def _check(fn: str, status: int):
 def _run(name: str, like: torch.Tensor, *args, stream=None):
     """Call librd's `name` with `like`'s device current and that device's
     stream (or `stream`) as the last argument; raise RdError on a bad status."""
-    if like.device.index == torch.cuda.current_device():
-        _check(name, getattr(_lib, name)(*args, _stream(stream, like.device)))
+    index = like.get_device()
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
+        _check(name, getattr(_lib, name)(*args, s))
         return
     with torch.cuda.device(like.device):
-        _check(name, getattr(_lib, name)(*args, _stream(stream, like.device)))
+        _check(name, getattr(_lib, name)(*args, s))
 
 
 def _empty(shape, dtype, like: torch.Tensor):
@@ -579,14 +586,14 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """A fresh tensor whose memory belongs to the stream that the call runs on, so
     that it is not handed out again while the call still uses it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _scratch(workspace, size: int, like: torch.Tensor, stream) -> torch.Tensor:
     if workspace is None:
-        return _new(max(16, size), torch.uint8, like, stream)
+        return _new((max(16, size),), torch.uint8, like, stream)
     if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
     if workspace.device != like.device or not workspace.is_contiguous():
@@ -614,8 +621,8 @@ def _pools(k_pool, v_pool):
     if len(shape) not in (4, 5) or v_pool.shape != shape:
         raise ValueError("k_pool/v_pool must be [num_pages, page_size, Hkv, D] or "
                          "[layers, num_pages, page_size, Hkv, D], of one shape")
-    page = shape[-3] * shape[-2] * shape[-1] * k_pool.element_size()
-    return (shape[0] if len(shape) == 5 else 1), shape[-4], shape[-3], page
+    layers, num_pages, page_size, heads, dim = shape if len(shape) == 5 else (1, *shape)
+    return layers, num_pages, page_size, page_size * heads * dim * k_pool.element_size()
 
 
 def _tables(block_table, row_pages, page_refs, num_pages, device):

@@ -81,9 +81,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when a max g
 constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
 constexpr int kSkMaxB = 480;               // chunk-range division up to this many requests
 constexpr uint32_t kSkMinChunks = 8;       // chunks per CTA at least (chunk-range division)
-// ... with a shared prefix: every unit's partials are merged with the prefix's
-// anyway, so a finer division costs no further launch
-constexpr uint32_t kSkMinChunksShared = rd_attn_plan::kSharedMinChunks;
+constexpr uint32_t kSkMinChunksShared = 2; // ... behind a shared prefix, where contexts are short
 
 template <int D, bool F8 = false, bool PIPE = false, bool SH = false> struct Cfg {
     // PIPE (the 16-bit path) pipelines S: two S tiles in tensor memory, so that S
@@ -92,8 +90,8 @@ template <int D, bool F8 = false, bool PIPE = false, bool SH = false> struct Cfg
     // 8-bit ring): one S tile and the queries in tensor memory.
     static_assert(F8 != PIPE, "every instantiation is the 16-bit pipelined path or the FP8 path");
     // SH (shared prefix, shared_prefix.cu): a request's context starts behind the
-    // pages that its group shares; units and pieces leave fp32 partials of their
-    // valid rows for the merge with the prefix's.
+    // pages that its group shares; whole units and pieces leave fp32 partials of
+    // their valid rows, which the caller merges with the prefix's.
     static_assert(!SH || PIPE, "the shared-prefix variant is the 16-bit path");
     static constexpr bool kPipe = PIPE;
     static constexpr bool kMaySk = PIPE || F8;          // tree attention (chunk ranges possible)
@@ -165,12 +163,7 @@ struct TcArgs {
     // failure-detection test hook: > 0 makes the MMA issuer first wait, with
     // this clock budget, on a barrier that nothing completes
     long long stall_budget;
-    // shared prefix: positions of request b that its group's prefix covers, the
-    // partial rows of whole units, and where the chunk-range table goes
-    const int32_t* skip;
-    float* o_rows;
-    float2* ml_rows;
-    uint32_t* sk_table;
+    rd_shared_suffix sh;     // shared prefix: its lengths, and where the partials go
     // 16-bit path: the query tiles come by TMA (G a power of two <= 16) through
     // map_q128 (boxes of 128 / G rows x G heads x 64 columns) and map_q16 (16 / G
     // rows), else by plain loads of warp 6
@@ -215,6 +208,7 @@ struct UnitGeo {
     // + 1 when the unit starts inside this CTA's range and runs past its end)
     bool cut;
     int split;
+    bool first_piece;     // holds the unit's first chunk
 };
 
 // Lengths of request b; false (and zero lengths) if they are invalid.
@@ -222,10 +216,10 @@ template <bool SH>
 __device__ __forceinline__ bool req_geo(const TcArgs& a, int b, UnitGeo& g)
 {
     bool bad;
-    g.Pb = a.lens[b];
+    g.Pb = SH ? __ldcg(a.lens + b) : a.lens[b];      // (SH: written by the plan kernel)
     if (a.block_table != nullptr) {
         const int c = a.ctx_lens[b];
-        const int first = SH ? a.skip[b] : 0;
+        const int first = SH ? __ldcg(a.sh.skip + b) : 0;
         g.kv_base = first;
         g.C = c - first;
         bad = c < first || c > a.max_kv || (long long)c > (long long)a.max_pages * a.page_size ||
@@ -316,16 +310,7 @@ __device__ void sk_build(const TcArgs& a, uint32_t* pre, uint32_t* nb, int lane)
     }
     if (lane == 0) pre[0] = 0;
     __syncwarp();
-    if constexpr (SH) {
-        // the merge with the prefix finds a unit's pieces from the table itself
-        if (blockIdx.x == 0)
-            for (int b = lane; b < a.B; b += 32) {
-                a.sk_table[b] = pre[b];
-                a.sk_table[a.B + 1 + b] = nb[b];
-            }
-        if (blockIdx.x == 0 && lane == 0) a.sk_table[a.B] = carry;
-        return;
-    }
+    if constexpr (SH) return;
     // This CTA's merge descriptor: when its range starts inside a unit that began
     // in the previous CTA's range, that unit is cut and this CTA names it for the
     // merge kernel (unit id in tile-major order, its first CTA c0, its number of
@@ -417,6 +402,7 @@ __device__ __forceinline__ bool work_next(const TcArgs& a, const uint32_t* pre, 
     g.d_first = max(cb, n_cc) - n_cc;
     g.n_draft = max(0, ce - max(cb, n_cc));
     g.cut = !(cb == 0 && ce == (int)n_b);
+    g.first_piece = cb == 0;
     // the unit starts inside this CTA's range (not at its start) and is cut: the
     // range's last piece, slot 2 c + 1; otherwise slot 2 c
     g.split = 2 * (int)blockIdx.x + ((g.cut && cb == 0 && U0 > sk_start<SH>(W, blockIdx.x)) ? 1 : 0);
@@ -676,6 +662,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 bool more;                                // positioned on a live item
                 int j, n, n_ctx, c_first, d_first, b, h;
                 int64_t kv_base;
+                int slot, page;                           // (SH) table entry looked up last
             };
             auto seek = [&](Cursor& c) {                  // the next live item from c.w on
                 UnitGeo geo;
@@ -689,6 +676,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                     c.b = geo.b;
                     c.h = geo.h;
                     c.kv_base = geo.kv_base;
+                    c.slot = -1;
                     return;
                 }
             };
@@ -698,12 +686,20 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             const bool paged = a.block_table != nullptr;
             // tensor map and first row of chunk c.j: context (contiguous, or the page
             // holding it), or the packed drafts
-            auto locate = [&](const Cursor& c, bool is_v, const CUtensorMap*& map) -> int {
+            auto locate = [&](Cursor& c, bool is_v, const CUtensorMap*& map) -> int {
                 if (c.j < c.n_ctx) {
                     map = is_v ? &map_vc : &map_kc;
                     const int pos0 = (c.c_first + c.j) * kN + (SH ? (int)c.kv_base : 0);
                     if (!paged) return (int)(c.kv_base + pos0);
-                    int pg = __ldg(a.block_table + (size_t)c.b * a.max_pages + pos0 / a.page_size);
+                    const int slot = pos0 / a.page_size;
+                    int pg;
+                    if constexpr (SH) {                   // one lookup a page
+                        if (slot != c.slot) c.page = __ldg(a.block_table + (size_t)c.b * a.max_pages + slot);
+                        c.slot = slot;
+                        pg = c.page;
+                    } else {
+                        pg = __ldg(a.block_table + (size_t)c.b * a.max_pages + slot);
+                    }
                     if (pg < 0 || pg >= a.num_pages) {
                         rd_flag(a.status, RD_DEV_BAD_INDEX);
                         pg = 0;
@@ -713,7 +709,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 map = is_v ? &map_vd : &map_kd;
                 return c.b * a.P_max + (c.d_first + c.j - c.n_ctx) * kN;
             };
-            auto issue = [&](const Cursor& c, uint32_t g, bool is_v) -> bool {
+            auto issue = [&](Cursor& c, uint32_t g, bool is_v) -> bool {
                 const int st = g % C::kStages;
                 uint64_t* full = is_v ? &bar.v_full[st] : &bar.kv_full[st];
                 uint64_t* empty = is_v ? &bar.v_empty[st] : &bar.kv_empty[st];
@@ -1075,7 +1071,8 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
         bool q_ready = false;                              // (not PIPE) the next item's queries are written
         Work wk = work_begin<C::kMaySk, SH>(a, sk_pre);
         UnitGeo geo;
-        bool have_next = false;                            // (not PIPE) the next item, looked up ahead
+        bool have_next = false;                            // (not PIPE, SH) the next item, looked up ahead
+        bool no_more = false;                              // (SH) there is none
         Work next_w;
         UnitGeo next_geo;
         while (!*abort) {
@@ -1083,6 +1080,8 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 geo = next_geo;
                 wk = next_w;
                 have_next = false;
+            } else if (SH && no_more) {
+                break;
             } else if (!work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, wk, geo)) {
                 break;
             }
@@ -1091,7 +1090,7 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             if (!(C::kMaySk && a.sk) && wk.u < a.n_units) prefetch_geo(a, wk.u);
             const int hq0 = geo.h * a.G;
             if (geo.zero_tile) {                           // padded rows of a tree tile
-                if constexpr (!SH) zero_tile(geo.b, geo.h, geo.tile);   // (SH: the merge writes them)
+                if constexpr (!SH) zero_tile(geo.b, geo.h, geo.tile);   // (SH: the merge's)
                 continue;
             }
             if (!geo.live) continue;
@@ -1269,6 +1268,11 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[sb]);
             }
+            if constexpr (SH) {                            // the next item's geometry, before the epilogue
+                next_w = wk;
+                have_next = ok && work_next<C::kNc, C::kMaySk, SH>(a, sk_pre, sk_nb, next_w, next_geo);
+                no_more = !have_next;
+            }
             // every S MMA of this unit has completed once q_free does; then the next
             // unit's queries (if it is live) go into the Q columns, so that its first
             // S MMA overlaps this unit's PV drain and epilogue
@@ -1299,7 +1303,20 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_free);
-            if (paired) {
+            if constexpr (SH) {
+                // a paired lane gives its partner the half of the columns that the
+                // partner writes, and takes its own
+                if (paired) {
+#pragma unroll
+                    for (int cb = 0; cb < D / 64; ++cb)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const uint32_t give = hf ? ob[cb][c] : ob[cb + D / 64][c];
+                            const float take = __uint_as_float(__shfl_xor_sync(0xffffffffu, give, 16));
+                            ob[cb][c] = __float_as_uint(__uint_as_float(hf ? ob[cb + D / 64][c] : ob[cb][c]) + take);
+                        }
+                }
+            } else if (paired) {
 #pragma unroll
                 for (int cb = 0; cb < D / 32; ++cb)
 #pragma unroll
@@ -1310,23 +1327,36 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             auto mine = [&](int cb) { return !paired || (cb >= D / 64) == (hf == 1); };
             const bool split_mode = geo.cut;
             if constexpr (SH) {
-                // fp32 partial rows (D floats each, with (m, l) apart): row (b, p, hq) of a
-                // whole unit, row r of its slot for a piece
+                // fp32 partials as below, of a whole unit among the rows: float4 [kv head]
+                // [D / 4][rows], so that a warp's stores cover consecutive rows.  A paired
+                // lane holds columns [hf D/2, (hf + 1) D/2) in ob[0 .. D/64).
                 if (valid) {
-                    const size_t at = split_mode ? (size_t)geo.split * kM + r
-                                                 : ((size_t)geo.b * a.P_max + qpos) * a.Hq + hq0 + row % a.G;
-                    float4* op = reinterpret_cast<float4*>((split_mode ? a.o_part : a.o_rows) + at * D);
+                    const size_t stride = split_mode ? (size_t)kM : a.sh.rows_cap;
+                    const size_t at = split_mode ? (size_t)r : (size_t)geo.b * a.P_max * a.G + row;
+                    const size_t block = split_mode ? geo.split : geo.h;
+                    float4* op = (split_mode ? reinterpret_cast<float4*>(a.o_part) : a.sh.rows) +
+                                 (block * (D / 4) + hf * (D / 8)) * stride + at;
 #pragma unroll
                     for (int cb = 0; cb < D / 32; ++cb) {
-                        if (mine(cb)) {
+                        if (paired && cb >= D / 64) break;
 #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                op[cb * 8 + q] =
-                                    make_float4(__uint_as_float(ob[cb][4 * q]), __uint_as_float(ob[cb][4 * q + 1]),
-                                                __uint_as_float(ob[cb][4 * q + 2]), __uint_as_float(ob[cb][4 * q + 3]));
-                        }
+                        for (int q = 0; q < 8; ++q)
+                            op[(size_t)(cb * 8 + q) * stride] =
+                                make_float4(__uint_as_float(ob[cb][4 * q]), __uint_as_float(ob[cb][4 * q + 1]),
+                                            __uint_as_float(ob[cb][4 * q + 2]), __uint_as_float(ob[cb][4 * q + 3]));
                     }
-                    if (hf == 0) (split_mode ? a.ml_part : a.ml_rows)[at] = make_float2(m, l_row);
+                    if (hf == 0) (split_mode ? a.ml_part : a.sh.rows_ml)[block * stride + at] = make_float2(m, l_row);
+                }
+                // the CTA that has a unit's first chunk names its pieces
+                if (a.sk && tid == 0 && geo.first_piece) {
+                    int n_pieces = 1;
+                    if (split_mode) {
+                        const uint32_t W = sk_pre[a.B];
+                        const uint32_t n_b = sk_nb[geo.b];
+                        const uint32_t last = sk_pre[geo.b] + (uint32_t)(geo.tile * a.Hkv + geo.h + 1) * n_b - 1;
+                        n_pieces = (int)((((uint64_t)last + 1) * sk_ctas<SH>(W) - 1) / W) - (int)blockIdx.x + 1;
+                    }
+                    a.sh.unit[(geo.tile * a.B + geo.b) * a.Hkv + geo.h] = make_int2(n_pieces, geo.split);
                 }
             } else if (!split_mode) {
                 const float inv = (valid && l_row > 0.f) ? a.out_scale / l_row : 0.f;
@@ -1388,6 +1418,8 @@ tree_attention_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map
             g += n;
             ++unit_iter;
         }
+        // this grid's end has to mean the prefix's too (the merge waits for this grid)
+        if (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
         // chunk-range division: the tiles past each request's valid rows (the
         // chunk ranges hold live units only), round-robin
         if (C::kMaySk && !SH && a.sk && !*abort) {
@@ -1522,8 +1554,24 @@ cudaError_t launch(int grid, cudaStream_t stream, const TcArgs& a, const CUtenso
     cudaError_t e = cudaFuncSetAttribute(tree_attention_tc_kernel<D, F8, PIPE, SH>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::kSmemBytes);
     if (e != cudaSuccess) return e;
-    tree_attention_tc_kernel<D, F8, PIPE, SH><<<grid, kThreads, Cf::kSmemBytes, stream>>>(a, m0, m1, m2, m3, m4, m5);
-    e = cudaGetLastError();
+    if constexpr (SH) {
+        // a programmatic dependent of the prefix kernel, which lets it start once the
+        // plan is written; it waits for the partials themselves
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Cf::kSmemBytes;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, tree_attention_tc_kernel<D, F8, PIPE, SH>, a, m0, m1, m2, m3, m4, m5);
+    } else {
+        tree_attention_tc_kernel<D, F8, PIPE, SH><<<grid, kThreads, Cf::kSmemBytes, stream>>>(a, m0, m1, m2, m3, m4, m5);
+        e = cudaGetLastError();
+    }
     if (SH || e != cudaSuccess || !a.sk) return e;      // SH: the caller merges
     // chunk-range division: merge the units that CTA boundaries cut, launched as a
     // programmatic dependent (its launch overlaps the attention kernel's tail)
@@ -1615,18 +1663,8 @@ cudaError_t rd_launch_attention(const rd_attn_plan& plan, int B, int P_max,
         a.out_scale = fp8->v_scale;
         a.scale_log2 *= fp8->k_scale;
     }
-    a.skip = nullptr;
-    a.o_rows = nullptr;
-    a.ml_rows = nullptr;
-    a.sk_table = nullptr;
-    if (shared != nullptr) {
-        a.skip = shared->skip;
-        a.o_rows = shared->o_rows;
-        a.ml_rows = shared->ml_rows;
-        a.o_part = shared->o_part;
-        a.ml_part = shared->ml_part;
-        a.sk_table = shared->sk_table;
-    } else if (plan.stream_k) {
+    a.sh = shared != nullptr ? *shared : rd_shared_suffix{};
+    if (plan.stream_k) {
         const size_t slot_rows = (size_t)2 * plan.grid * kM;
         a.o_part = static_cast<float*>(workspace);
         a.ml_part = reinterpret_cast<float2*>(a.o_part + slot_rows * D);

@@ -63,7 +63,6 @@ struct rd_attn_plan {
     bool stream_k;     // chunk-range division (tree attention), else whole units round-robin
     int grid;          // CTAs of the launch
     size_t ws_bytes;   // workspace bytes needed (chunk ranges: partials of cut units)
-    static constexpr unsigned kSharedMinChunks = 2;   // chunks per CTA at least, with a shared prefix
 };
 struct rd_paged_kv {
     const int32_t* block_table;   // [B, max_pages]
@@ -75,15 +74,15 @@ struct rd_fp8_kv {
     const void* v_cache;
     float k_scale, v_scale;
 };
-// The part of a shared-prefix call behind the prefix (shared_prefix.cu): partial
-// rows instead of outputs.
+// The part of a shared-prefix call behind the prefix (shared_prefix.cu): fp32
+// partials (running maximum m in log2 units, sum l, unnormalised O) instead of
+// outputs, those of pieces in the workspace's slots.
 struct rd_shared_suffix {
     const int32_t* skip;     // [B] positions that the group's prefix covers
-    float* o_rows;           // [B, P_max, Hq, D] rows of whole units, with (m, l)
-    float2* ml_rows;
-    float* o_part;           // [2 grid, 128, D] rows of pieces (chunk ranges)
-    float2* ml_part;
-    uint32_t* sk_table;      // [B + 1] chunks before a request, [B] chunks of a unit
+    float4* rows;            // whole units: [Hkv][D / 4][rows_cap], row (b P_max + p) G + g
+    float2* rows_ml;         // [Hkv][rows_cap]
+    size_t rows_cap;         // B P_max G
+    int2* unit;              // chunk ranges: [tile][b][kv head] pieces, first one's slot
 };
 rd_attn_plan rd_attn_make_plan(int B, int P_max, int Hq, int Hkv, int D, int max_kv);
 cudaError_t rd_launch_attention(const rd_attn_plan& plan, int B, int P_max,

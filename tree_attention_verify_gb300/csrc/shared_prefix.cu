@@ -6,12 +6,14 @@
 // over disjoint key sets i, the output is sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
 // with M = max_i m_i.  So the prefix of a group is one dense product of all its
 // requests' rows with the shared keys, and the rest of each request is the
-// paged tree attention from behind the prefix.  Four launches on one stream:
+// paged tree attention from behind the prefix.  On one stream, each launch a
+// programmatic dependent of the one before:
 //   plan    one CTA: valid requests, the compact list of a group's live rows,
 //           and the table that divides the prefix work over the CTAs;
 //   prefix  (below) fp32 partials of every live row over its group's prefix;
-//   suffix  attention_tc.cu, shared-prefix variant: partials of every row over
-//           its own context and drafts;
+//   suffix  partials of every row over its request's own context and drafts
+//           (shared_suffix.cu for up to 64 rows per kv head, else the shared-prefix
+//           variant of attention_tc.cu);
 //   merge   the formula above, rounded once to bf16; zeros in padded rows.
 //
 // The prefix kernel: unit = (group, kv head, 256 rows), the rows being the G
@@ -41,14 +43,16 @@
 #include "attn_common.cuh"
 #include "block_scan.cuh"
 #include "rd_internal.cuh"
+#include "shared_prefix.cuh"
 #include "tc_ptx.cuh"
 
 namespace {
 using namespace rdtc;
 using namespace rdattn;
+using namespace rdshared;
 
 constexpr int kM = 128;                    // rows per tile = TMEM lanes
-constexpr int kUnitRows = 2 * kM;
+static_assert(kUnitRows == 2 * kM, "two tiles");
 constexpr int kN = 128;                    // KV positions per chunk (two TMA boxes)
 constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8;
@@ -63,39 +67,13 @@ constexpr int kRegsOther = 104;
 static_assert(128 * (2 * kRegsSoftmax + kRegsOther) <= kThreads * kRegsLaunch, "register split");
 static_assert(32 * (2 * kRegsSoftmax + kRegsOther) <= 16384, "register split per sub-partition");
 constexpr uint32_t kMinChunks = 2;         // chunks per CTA at least
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
-
-// What the plan kernel leaves in the workspace.
-struct Group {
-    int node0, nodes;      // its live nodes in the compact list
-    int positions;         // prefix length
-    int leader;            // its first request, whose table names the pages
-};
-struct Plan {
-    int32_t* eff_len;      // [B] packed length, 0: the request is skipped
-    int32_t* skip;         // [B] prefix positions of the request
-    int32_t* gid;          // [B] its group, -1: no prefix
-    int32_t* node_base;    // [B + 1] its first node in the compact list
-    int32_t* node_row;     // [B P_max] compact node -> b P_max + p
-    Group* group;          // [n_groups]
-    uint32_t* first;       // [n_groups + 1] chunks of the groups before
-    // partials: rows of whole units, and of pieces (two slots per CTA)
-    float* pre_rows;       // [compact node, Hq, D]
-    float2* pre_ml;
-    float* pre_part;       // [2 grid, 256, D]
-    float2* pre_part_ml;
-    float* suf_rows;       // [B, P_max, Hq, D]
-    float2* suf_ml;
-    float* suf_part;       // [2 suffix grid, 128, D]
-    float2* suf_part_ml;
-    uint32_t* sk_table;    // the suffix's chunk-range table
-};
 
 // ------------------------------------------------------------------------ plan
 struct PlanArgs {
     int B, P_max, Hkv, G, page_size, max_pages, max_ctx, n_groups;
+    int suffix_chunk;          // positions of a suffix chunk (0: the tcgen05 kernel divides by itself)
     const int32_t* lens;
     const int32_t* ctx_lens;
     const int32_t* group_offsets;
@@ -104,38 +82,64 @@ struct PlanArgs {
     int32_t* status;
 };
 
+// A short chain of dependent reads is all this kernel is, so a batch of up to 1024
+// requests and groups (kSmall) keeps its tables in shared memory between the steps;
+// a larger one reads them back from the workspace.
+template <bool kSmall>
 __global__ void __launch_bounds__(kScanThreads, 1)
 plan_kernel(const PlanArgs a)
 {
+    constexpr int kCap = kSmall ? kScanThreads : 1;
     __shared__ int warp_sum[kScanWarps];
+    __shared__ int s_offsets[kCap + 1], s_pages[kCap], s_base[kCap + 1];
+    __shared__ Group s_group[kCap];
     const int tid = threadIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int32_t* offsets = a.group_offsets;
+    const int32_t* pages = a.prefix_pages;
+    int32_t* base = a.p.node_base;
+    Group* group = a.p.group;
+    int ctx = 0, len = 0;                                  // kSmall: of request tid
+    if constexpr (kSmall) {
+        if (tid < a.B) {
+            ctx = __ldg(a.ctx_lens + tid);
+            len = __ldg(a.lens + tid);
+        }
+        for (int g = tid; g <= a.n_groups; g += kScanThreads) s_offsets[g] = __ldg(offsets + g);
+        if (tid < a.n_groups) s_pages[tid] = __ldg(pages + tid);
+        offsets = s_offsets;
+        pages = s_pages;
+        base = s_base;
+        group = s_group;
+        __syncthreads();
+    }
     // offsets that do not ascend within [0, B] would give a request two groups:
     // then nobody shares (the results stay the same)
     bool bad_offsets = false;
     for (int g = tid; g < a.n_groups; g += kScanThreads) {
-        const int o0 = a.group_offsets[g], o1 = a.group_offsets[g + 1];
+        const int o0 = offsets[g], o1 = offsets[g + 1];
         bad_offsets = bad_offsets || o0 < 0 || o1 < o0 || o1 > a.B;
     }
     bad_offsets = __syncthreads_or(bad_offsets);
     if (bad_offsets && tid == 0) rd_flag(a.status, RD_DEV_BAD_INDEX);
     auto pages_of = [&](int g) {
-        const int n = a.prefix_pages[g];
+        const int n = pages[g];
         return n < 0 || n > a.max_pages || (long long)n * a.page_size > a.max_ctx ? -1 : n;
     };
-    int carry = 0;
+    int carry = 0, my_gid = -1;
+    uint32_t suf_carry = 0;
     for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
         const int b = b0 + tid;
-        int n = 0, len = 0;
+        int n = 0, suf = 0;
         if (b < a.B) {
             int g = -1, skip = 0;
             if (!bad_offsets) {
                 int lo = 0, hi = a.n_groups;               // groups that start at or before b
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
-                    if (a.group_offsets[mid] <= b) lo = mid + 1; else hi = mid;
+                    if (offsets[mid] <= b) lo = mid + 1; else hi = mid;
                 }
-                if (lo > 0 && b < a.group_offsets[lo]) {
+                if (lo > 0 && b < offsets[lo]) {
                     const int pg = pages_of(lo - 1);
                     if (pg > 0) {
                         g = lo - 1;
@@ -143,52 +147,80 @@ plan_kernel(const PlanArgs a)
                     }
                 }
             }
-            const int c = a.ctx_lens[b];
-            len = a.lens[b];
-            if (c < skip || c > a.max_ctx || (long long)c > (long long)a.max_pages * a.page_size || len < 0 ||
+            if constexpr (!kSmall) {
+                ctx = a.ctx_lens[b];
+                len = a.lens[b];
+            }
+            if (ctx < skip || ctx > a.max_ctx || (long long)ctx > (long long)a.max_pages * a.page_size || len < 0 ||
                 len > a.P_max) {
                 rd_flag(a.status, RD_DEV_BAD_LENGTH);
                 len = 0;
             }
             a.p.eff_len[b] = len;
             a.p.skip[b] = skip;
-            a.p.gid[b] = g;
+            a.p.gid[b] = my_gid = g;
             n = g >= 0 ? len : 0;
+            if (a.suffix_chunk > 0 && len > 0)
+                suf = a.Hkv * ((ctx - skip + a.suffix_chunk - 1) / a.suffix_chunk + (len + a.suffix_chunk - 1) / a.suffix_chunk);
         }
         int total;
         const int at = carry + cta_scan(n, warp_sum, total);
         if (b < a.B) {
-            a.p.node_base[b] = at;
+            base[b] = at;
             for (int p = 0; p < n; ++p) a.p.node_row[at + p] = b * a.P_max + p;
         }
         carry += total;
+        if (a.suffix_chunk > 0) {
+            const int before = cta_scan(suf, warp_sum, total);
+            if (b < a.B) a.p.suf_first[b] = suf_carry + before;
+            suf_carry += total;
+        }
     }
-    if (tid == 0) a.p.node_base[a.B] = carry;
+    if (tid == 0) {
+        base[a.B] = carry;
+        if (a.suffix_chunk > 0) a.p.suf_first[a.B] = suf_carry;
+    }
     __syncthreads();
     uint32_t chunks = 0;
+    int all_units = 0;
     for (int g0 = 0; g0 < a.n_groups; g0 += kScanThreads) {
         const int g = g0 + tid;
-        int w = 0;
-        if (g < a.n_groups) {
-            Group grp = {0, 0, 0, 0};
-            if (!bad_offsets) {
-                const int pg = pages_of(g);
-                if (pg < 0) rd_flag(a.status, RD_DEV_BAD_LENGTH);
-                grp.leader = a.group_offsets[g];
-                grp.node0 = a.p.node_base[grp.leader];
-                grp.nodes = a.p.node_base[a.group_offsets[g + 1]] - grp.node0;
-                grp.positions = max(0, pg) * a.page_size;
-                const int units = a.Hkv * ((grp.nodes * a.G + kUnitRows - 1) / kUnitRows);
-                w = units * ((grp.positions + kN - 1) / kN);
-            }
-            a.p.group[g] = grp;
+        int w = 0, units = 0;
+        Group grp = {0, 0, 0, 0, 0, 0};
+        if (g < a.n_groups && !bad_offsets) {
+            const int pg = pages_of(g);
+            if (pg < 0) rd_flag(a.status, RD_DEV_BAD_LENGTH);
+            grp.leader = offsets[g];
+            grp.node0 = base[grp.leader];
+            grp.nodes = base[offsets[g + 1]] - grp.node0;
+            grp.positions = max(0, pg) * a.page_size;
+            grp.pairs = (grp.nodes * a.G + kUnitRows - 1) / kUnitRows;
+            units = a.Hkv * grp.pairs;
+            w = units * ((grp.positions + kN - 1) / kN);
         }
-        int total;
+        int total, total_units;
         const int at = cta_scan(w, warp_sum, total);
-        if (g < a.n_groups) a.p.first[g] = chunks + at;
+        grp.unit0 = all_units + cta_scan(units, warp_sum, total_units);
+        if (g < a.n_groups) {
+            a.p.group[g] = grp;
+            if constexpr (kSmall) s_group[g] = grp;
+            a.p.first[g] = chunks + at;
+        }
         chunks += total;
+        all_units += total_units;
     }
     if (tid == 0) a.p.first[a.n_groups] = chunks;
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kScanThreads) {
+        const int g = kSmall ? my_gid : a.p.gid[b];
+        int4 req = make_int4(-1, 0, 0, 0);
+        if (g >= 0) {
+            const Group grp = group[g];
+            const int node = base[b];
+            req = make_int4(grp.unit0, grp.pairs, (node - grp.node0) * a.G, node * a.G);
+        }
+        a.p.req[b] = req;
+    }
 }
 
 // ---------------------------------------------------------------------- prefix
@@ -233,28 +265,14 @@ struct Bar {
 };
 static_assert(sizeof(Bar) <= 512, "barrier block");
 
-// CTAs that take part, and CTA c's first chunk, of a sequence of W chunks
-__host__ __device__ __forceinline__ uint32_t range_ctas(uint32_t W, uint32_t grid, uint32_t least)
-{
-    const uint32_t n = W / least;
-    return n < 1u ? 1u : (n < grid ? n : grid);
-}
-__device__ __forceinline__ uint32_t range_start(uint32_t W, uint32_t n, uint32_t c)
-{
-    return (uint32_t)(((uint64_t)c * W) / n);
-}
-// the CTA whose range holds chunk x
-__device__ __forceinline__ uint32_t range_of(uint32_t W, uint32_t n, uint32_t x)
-{
-    return (uint32_t)((((uint64_t)x + 1) * n - 1) / W);
-}
-
 // One piece of a unit (all of it, unless cut).
 struct Piece {
     int h, row0;              // kv head; first row of the unit within its group
     int rows;                 // rows of the unit (1 .. 256)
     int c0, n;                // chunks [c0, c0 + n)
     int slot;                 // piece slot, -1: a whole unit
+    int unit;
+    uint32_t last;            // the unit's last chunk in the sequence
     Group g;
 };
 
@@ -283,7 +301,7 @@ struct Walk {
         const uint32_t base = a.p.first[lo];
         const uint32_t n = (uint32_t)(u.g.positions + kN - 1) / kN;
         const int all = u.g.nodes * a.G;
-        const uint32_t pairs = (uint32_t)(all + kUnitRows - 1) / kUnitRows;
+        const uint32_t pairs = (uint32_t)u.g.pairs;
         const uint32_t unit = (x - base) / n;
         const uint32_t u0 = base + unit * n;
         u.h = (int)(unit / pairs);
@@ -293,6 +311,8 @@ struct Walk {
         const uint32_t stop = min(u0 + n, end);
         u.n = (int)(stop - x);
         u.slot = (uint32_t)u.n == n ? -1 : 2 * (int)blockIdx.x + (u.c0 == 0 && u0 > start ? 1 : 0);
+        u.unit = u.g.unit0 + (int)unit;
+        u.last = u0 + n - 1;
         x = stop;
         return true;
     }
@@ -350,6 +370,9 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
     tc_fence_after();
     const uint32_t tmem = bar.tmem_base;
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the plan is written
+    // the suffix kernel may start (it reads the plan, and waits for this grid before
+    // it reads the partials)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     auto fail = [&]() {
         *abort = 1;
         rd_flag(a.status, RD_DEV_TIMEOUT);
@@ -364,7 +387,13 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
             Walk w;
             w.begin(a);
             Piece u;
+            const uint32_t W = a.p.first[a.n_groups];
             while (!*abort && w.next(a, u)) {
+                if (u.c0 == 0) {                          // the unit starts here: name its pieces
+                    const uint32_t nc = range_ctas(W, gridDim.x, kMinChunks);
+                    const int n = u.slot < 0 ? 1 : (int)(range_of(W, nc, u.last) - blockIdx.x) + 1;
+                    a.p.unit[u.unit] = make_int2(n, u.slot);
+                }
                 const int32_t* table = a.block_table + (size_t)u.g.leader * a.max_pages;
                 auto row_of = [&](int pos) -> int {       // pool row of a position of the prefix
                     int pg = __ldg(table + pos / a.page_size);
@@ -639,23 +668,20 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_free[t]);
             if (valid) {
-                // fp32 partial row: unnormalised O, and (m, l)
-                size_t at;
-                if (u.slot < 0) {
-                    const int gr = u.row0 + row;
-                    at = (size_t)(u.g.node0 + gr / a.G) * a.Hq + u.h * a.G + gr % a.G;
-                } else {
-                    at = (size_t)u.slot * kUnitRows + row;
-                }
-                float4* dst = reinterpret_cast<float4*>((u.slot < 0 ? a.p.pre_rows : a.p.pre_part) + at * D);
+                // fp32 partials, four columns of consecutive rows side by side
+                const bool whole = u.slot < 0;
+                const size_t stride = whole ? a.p.rows_cap : kUnitRows;
+                const size_t at = whole ? (size_t)u.g.node0 * a.G + u.row0 + row : (size_t)row;
+                const size_t block = whole ? u.h : u.slot;
+                float4* dst = (whole ? a.p.rows : a.p.part) + block * (D / 4) * stride + at;
 #pragma unroll
                 for (int cb = 0; cb < D / 32; ++cb)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        dst[cb * 8 + i] = make_float4(__uint_as_float(o[cb][4 * i]), __uint_as_float(o[cb][4 * i + 1]),
-                                                      __uint_as_float(o[cb][4 * i + 2]),
-                                                      __uint_as_float(o[cb][4 * i + 3]));
-                (u.slot < 0 ? a.p.pre_ml : a.p.pre_part_ml)[at] = make_float2(m, l);
+                        dst[(size_t)(cb * 8 + i) * stride] =
+                            make_float4(__uint_as_float(o[cb][4 * i]), __uint_as_float(o[cb][4 * i + 1]),
+                                        __uint_as_float(o[cb][4 * i + 2]), __uint_as_float(o[cb][4 * i + 3]));
+                (whole ? a.p.rows_ml : a.p.part_ml)[block * stride + at] = make_float2(m, l);
             }
             ct += u.n;
             ++ut;
@@ -671,193 +697,161 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
 }
 
 // ----------------------------------------------------------------------- merge
-// CTA = (node (b, p), a run of heads).  A row's partials are its unit's pieces of
-// the prefix, then those of the suffix; lane i of a warp holds (m, l) of piece i
-// and each lane D / 32 columns.  WPR warps share a row's pieces when there are
-// few rows (a short batch is cut into many pieces).
+// CTA = (request, kv head, R rows p G + g).  What bounds it is the chain of reads
+// that leads to the partials (request, unit, then (m, l) and O), so each CTA walks
+// that chain once for its rows and then has all their pieces on the way at the same
+// time: copies into shared memory (cp.async) hold no registers.  A row's pieces are
+// those of its prefix unit and of its suffix unit, kMergePieces of them a round.
 struct MergeArgs {
-    int B, P_max, Hq, Hkv, G, n_groups, heads;   // heads per CTA
-    uint32_t pre_grid, suf_grid;
-    bool suf_sk;
+    int P_max, Hq, Hkv, G, B;
+    int blocks;               // CTAs per (request, kv head)
+    bool table;               // suffix units have an entry in the table of pieces
     Plan p;
     uint16_t* o;
 };
 constexpr int kMergeThreads = 256;
-constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kMergePieces = 2;
+constexpr int kMergeRows = 64;
+template <int D> constexpr int kMergeSmem = kMergePieces * kMergeRows * D * 4;
 
-// the pieces of one row: the first `n` of the slots s0, then 2 (c0 + 1), 2 (c0 + 2), ...
-struct Pieces {
-    const float* o;           // row 0 of the whole-unit rows, or of the slots
-    const float2* ml;
-    size_t row0, step;        // first piece's row; rows from slot to slot
-    size_t row1;              // second piece's row
-    int n;
-    __device__ __forceinline__ size_t row(int i) const { return i == 0 ? row0 : row1 + (size_t)(i - 1) * step; }
-};
-
-template <int D, int WPR>
+template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 merge_kernel(const MergeArgs a)
 {
-    constexpr int V = D / 32;                     // columns per lane
-    __shared__ float part_o[WPR > 1 ? kMergeWarps * D : 1];
-    __shared__ float2 part_ml[WPR > 1 ? kMergeWarps : 1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int blocks = (a.Hq + a.heads - 1) / a.heads;
-    const int node = blockIdx.x / blocks;         // b P_max + p
-    const int h0 = (blockIdx.x % blocks) * a.heads, h1 = min(a.Hq, h0 + a.heads);
-    const int b = node / a.P_max, p = node % a.P_max;
+    extern __shared__ float4 stage[];                     // [piece][D / 4][kMergeRows]
+    __shared__ Pieces s_pc[2][kMergeRows];
+    constexpr int kParts = kMergeThreads / kMergeRows;    // threads of a row
+    constexpr int kQ = D / 4 / kParts;                    // float4 columns of a thread
+    const int bh = blockIdx.x / a.blocks;
+    const int b = bh / a.Hkv, h = bh % a.Hkv;
+    const int row0 = (blockIdx.x % a.blocks) * kMergeRows;
+    const int tid = threadIdx.x;
+    const int r = tid % kMergeRows, part = tid / kMergeRows, row = row0 + r;      // row = p G + g
+    const int all = a.P_max * a.G;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const bool live = p < a.p.eff_len[b];
-    const int gid = a.p.gid[b];
-    Group grp = {0, 0, 0, 0};
-    uint32_t gfirst = 0, W = 0;
-    if (gid >= 0) {
-        grp = a.p.group[gid];
-        gfirst = a.p.first[gid];
-        W = a.p.first[a.n_groups];
+    const int len = __ldcg(a.p.eff_len + b);
+    int n = 0;                                            // the row's pieces
+    if (part == 0 && row < len * a.G) {
+        const int4 req = __ldcg(a.p.req + b);
+        int2 su = make_int2(1, 0);
+        if (a.table) su = __ldcg(a.p.suffix.unit + ((size_t)(row / a.p.slot_rows) * a.B + b) * a.Hkv + h);
+        Pieces pre = {};
+        if (req.x >= 0) {
+            const int gr = req.z + row;
+            pre = pieces_of<D>(__ldcg(a.p.unit + req.x + h * req.y + gr / kUnitRows), a.p, h, req.w + row,
+                               gr % kUnitRows);
+        }
+        s_pc[0][r] = pre;
+        s_pc[1][r] = pieces_at<D>(su, a.p.suffix.rows, a.p.suffix.rows_ml, a.p.suffix.rows_cap, h, (size_t)b * all + row,
+                                  a.p.suf_part, a.p.suf_part_ml, a.p.slot_rows, row % a.p.slot_rows);
+        n = pre.n + su.x;
     }
-    const int cnode = a.p.node_base[b] + p;       // compact node
-    for (int hq = h0 + warp / WPR; hq < h1; hq += kMergeWarps / WPR) {
-        uint16_t* dst = a.o + ((size_t)node * a.Hq + hq) * D + lane * V;
-        if (!live) {
-            if (warp % WPR == 0) {
-                if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(0, 0);
-                else *reinterpret_cast<uint32_t*>(dst) = 0u;
-            }
-            continue;
-        }
-        const int h = hq / a.G, gq = hq % a.G;
-        Pieces pre = {}, suf = {};
-        if (gid >= 0) {
-            const uint32_t n = (uint32_t)(grp.positions + kN - 1) / kN;
-            const int row = (cnode - grp.node0) * a.G + gq;
-            const uint32_t pairs = (uint32_t)(grp.nodes * a.G + kUnitRows - 1) / kUnitRows;
-            const uint32_t u0 = gfirst + ((uint32_t)h * pairs + row / kUnitRows) * n;
-            const uint32_t nc = range_ctas(W, a.pre_grid, kMinChunks);
-            const uint32_t c0 = range_of(W, nc, u0), c1 = range_of(W, nc, u0 + n - 1);
-            pre.n = (int)(c1 - c0) + 1;
-            if (pre.n == 1) {
-                pre.o = a.p.pre_rows;
-                pre.ml = a.p.pre_ml;
-                pre.row0 = (size_t)cnode * a.Hq + hq;
-            } else {
-                pre.o = a.p.pre_part;
-                pre.ml = a.p.pre_part_ml;
-                const size_t r = row % kUnitRows;
-                pre.row0 = (size_t)(2 * c0 + (u0 > range_start(W, nc, c0) ? 1 : 0)) * kUnitRows + r;
-                pre.row1 = (size_t)(2 * (c0 + 1)) * kUnitRows + r;
-                pre.step = 2 * kUnitRows;
-            }
-        }
-        {
-            const int row = p * a.G + gq;
-            suf.n = 1;
-            suf.o = a.p.suf_rows;
-            suf.ml = a.p.suf_ml;
-            suf.row0 = (size_t)node * a.Hq + hq;
-            if (a.suf_sk) {
-                const uint32_t Ws = a.p.sk_table[a.B];
-                const uint32_t n = a.p.sk_table[a.B + 1 + b];
-                const uint32_t u0 = a.p.sk_table[b] + (uint32_t)((row / kM) * a.Hkv + h) * n;
-                const uint32_t nc = range_ctas(Ws, a.suf_grid, rd_attn_plan::kSharedMinChunks);
-                const uint32_t c0 = range_of(Ws, nc, u0), c1 = range_of(Ws, nc, u0 + n - 1);
-                if (c1 > c0) {
-                    suf.n = (int)(c1 - c0) + 1;
-                    suf.o = a.p.suf_part;
-                    suf.ml = a.p.suf_part_ml;
-                    const size_t r = row % kM;
-                    suf.row0 = (size_t)(2 * c0 + (u0 > range_start(Ws, nc, c0) ? 1 : 0)) * kM + r;
-                    suf.row1 = (size_t)(2 * (c0 + 1)) * kM + r;
-                    suf.step = 2 * kM;
-                }
+    const int live = min(kMergeRows, len * a.G - row0);   // may be <= 0
+    int most = n;                                         // of the CTA's rows
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+    __shared__ int s_most[kMergeThreads / 32];
+    if ((tid & 31) == 0) s_most[tid >> 5] = most;
+    __syncthreads();
+    most = 0;
+#pragma unroll
+    for (int i = 0; i < kMergeThreads / 32; ++i) most = max(most, s_most[i]);
+    n = r < live ? s_pc[0][r].n + s_pc[1][r].n : 0;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[kQ];
+#pragma unroll
+    for (int e = 0; e < kQ; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < most; k0 += kMergePieces) {
+        // the round's pieces: thread part of row r fetches its own columns
+        float2 ml[kMergePieces];
+#pragma unroll
+        for (int i = 0; i < kMergePieces; ++i) {
+            const int k = k0 + i;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (k < n) {
+                const int pn = s_pc[0][r].n;
+                const Pieces& q = s_pc[k < pn ? 0 : 1][r];
+                const int kk = k < pn ? k : k - pn;
+                const float4* src = q.o(kk) + (size_t)(part * kQ) * q.stride;
+                const size_t stride = q.stride;
+#pragma unroll
+                for (int e = 0; e < kQ; ++e)
+                    cp_async16(stage + (i * (D / 4) + part * kQ + e) * kMergeRows + r, src + (size_t)e * stride);
+                ml[i] = __ldcg(q.ml(kk));
             }
         }
-        const int n = pre.n + suf.n;
-        float M = -INFINITY, L = 0.f;
-        float acc[V];
+        cp_async_wait_all();                              // each thread reads only what it fetched
+        float Mn = M;
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = 0.f;
-        // this warp's pieces: (warp % WPR), + WPR, ... in batches of 32
-        for (int i0 = warp % WPR; i0 < n; i0 += 32 * WPR) {
-            const int i = i0 + lane * WPR;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            const float* src = nullptr;
-            if (i < n) {
-                const Pieces& s = i < pre.n ? pre : suf;
-                const size_t at = s.row(i < pre.n ? i : i - pre.n);
-                ml = __ldcg(s.ml + at);
-                src = s.o + at * D;
-            }
-            float mx = ml.x;
+        for (int i = 0; i < kMergePieces; ++i) Mn = fmaxf(Mn, ml[i].x);
+        const float base = Mn == -INFINITY ? 0.f : Mn;    // no visible key yet (or only NaN scores)
+        const float keep = exp2f(M - base);               // 0 while M is -inf
+        M = Mn;
+        L *= keep;
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float Mn = fmaxf(M, mx);
-            if (Mn == -INFINITY) {                // no visible key (l = 0), or every score a NaN
-                float l0 = ml.y;
+        for (int e = 0; e < kQ; ++e) {
+            acc[e].x *= keep; acc[e].y *= keep; acc[e].z *= keep; acc[e].w *= keep;
+        }
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-                L += l0;
-                continue;
-            }
-            const float keep = exp2f(M - Mn);     // 0 while M is -inf
-            M = Mn;
-            const float wgt = exp2f(ml.x - M);
-            float lsum = ml.y * wgt;
+        for (int i = 0; i < kMergePieces; ++i) {
+            if (k0 + i >= n) continue;
+            const float w = exp2f(ml[i].x - base);
+            L += ml[i].y * w;                             // (NaN scores: l = NaN, m = -inf, 0 x NaN)
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, d);
-            L = L * keep + lsum;
-#pragma unroll
-            for (int c = 0; c < V; ++c) acc[c] *= keep;
-            const int cnt = min(32, (n - i0 + WPR - 1) / WPR);
-#pragma unroll 4
-            for (int k = 0; k < cnt; ++k) {
-                const float* from = reinterpret_cast<const float*>(
-                    __shfl_sync(0xffffffffu, (unsigned long long)src, k));
-                const float x = __shfl_sync(0xffffffffu, wgt, k);
-                if constexpr (V == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(from) + lane);
-                    acc[0] += v.x * x; acc[1] += v.y * x; acc[2] += v.z * x; acc[3] += v.w * x;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(from) + lane);
-                    acc[0] += v.x * x; acc[1] += v.y * x;
-                }
+            for (int e = 0; e < kQ; ++e) {
+                const float4 x = stage[(i * (D / 4) + part * kQ + e) * kMergeRows + r];
+                acc[e].x += x.x * w; acc[e].y += x.y * w; acc[e].z += x.z * w; acc[e].w += x.w * w;
             }
         }
-        if constexpr (WPR > 1) {
-            __syncthreads();                      // one row per CTA and turn: uniform
-#pragma unroll
-            for (int c = 0; c < V; ++c) part_o[warp * D + lane * V + c] = acc[c];
-            if (lane == 0) part_ml[warp] = make_float2(M, L);
-            __syncthreads();
-            if (warp != 0) continue;
-            float Ma = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kMergeWarps; ++k) Ma = fmaxf(Ma, part_ml[k].x);
-            L = 0.f;
-#pragma unroll
-            for (int c = 0; c < V; ++c) acc[c] = 0.f;
-#pragma unroll
-            for (int k = 0; k < kMergeWarps; ++k) {
-                const float x = part_ml[k].x == -INFINITY ? 0.f : exp2f(part_ml[k].x - Ma);
-                L += part_ml[k].y * x;
-#pragma unroll
-                for (int c = 0; c < V; ++c) acc[c] += part_o[k * D + lane * V + c] * x;
-            }
-        }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        if constexpr (V == 4)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
-                                                        pack_bf16(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
     }
+    if (row >= all) return;
+    const float inv = r < live ? (L == 0.f ? 0.f : 1.f / L) : 0.f;    // padded rows: zeros
+    uint4* dst = reinterpret_cast<uint4*>(
+        a.o + (((size_t)b * a.P_max + row / a.G) * a.Hq + h * a.G + row % a.G) * D + part * (D / kParts));
+#pragma unroll
+    for (int e = 0; e < kQ; e += 2)
+        dst[e / 2] = make_uint4(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv),
+                                pack_bf16(acc[e + 1].x * inv, acc[e + 1].y * inv),
+                                pack_bf16(acc[e + 1].z * inv, acc[e + 1].w * inv));
 }
 
 // ------------------------------------------------------------------ host side
-// Workspace layout; `base` null: the size only.
-size_t layout(Plan& p, unsigned char* base, int B, int P_max, int Hq, int D, int n_groups, int pre_grid,
-              const rd_attn_plan& suffix)
+template <int D>
+cudaError_t launch_merge(dim3 grid, cudaStream_t stream, MergeArgs& a)
+{
+    cudaError_t e = cudaFuncSetAttribute(merge_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem<D>);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&a};
+    return launch_dependent(reinterpret_cast<const void*>(merge_kernel<D>), grid, dim3(kMergeThreads), kMergeSmem<D>,
+                            stream, args);
+}
+
+// Which kernel takes the part behind the prefix.  Up to 64 rows per kv head the one
+// of shared_suffix.cu, which reads each key once for all of them; with more rows
+// the tcgen05 kernel, whose tiles hold 128.
+struct SuffixChoice {
+    bool few_rows;
+    bool table;               // units have an entry in the table of pieces
+    int grid, slot_rows, tiles;
+    rd_attn_plan plan;        // tcgen05
+};
+SuffixChoice choose_suffix(int B, int P_max, int Hq, int Hkv, int D, int max_ctx)
+{
+    SuffixChoice s;
+    const int rows = P_max * (Hq / Hkv);
+    s.few_rows = rows <= kSuffixMaxRows;
+    s.plan = rd_attn_make_plan(B, P_max, Hq, Hkv, D, max_ctx);
+    s.table = s.few_rows || s.plan.stream_k;
+    s.grid = s.few_rows ? rd_suffix_grid(rows) : s.plan.grid;
+    s.slot_rows = s.few_rows ? kSuffixMaxRows : kM;
+    s.tiles = s.few_rows ? 1 : s.plan.tiles;
+    return s;
+}
+
+// Workspace layout; `base` null: the size only.  The suffix's own workspace (its
+// slots, as rd_attn_make_plan sizes them) comes last.
+size_t layout(Plan& p, void*& suffix_ws, unsigned char* base, int B, int P_max, int Hq, int Hkv, int D,
+              int n_groups, int pre_grid, const SuffixChoice& suffix)
 {
     size_t at = 0;
     auto take = [&](auto*& ptr, size_t n) {
@@ -865,9 +859,8 @@ size_t layout(Plan& p, unsigned char* base, int B, int P_max, int Hq, int D, int
         ptr = base == nullptr ? nullptr : reinterpret_cast<T*>(base + at);
         at += (n * sizeof(T) + 255) & ~size_t(255);
     };
-    const size_t rows = (size_t)B * P_max * Hq;
-    const size_t pre = (size_t)2 * pre_grid * kUnitRows;
-    const size_t suf = suffix.stream_k ? (size_t)2 * suffix.grid * kM : 0;
+    p.rows_cap = (size_t)B * P_max * (Hq / Hkv);
+    const size_t slots = (size_t)2 * pre_grid;
     take(p.eff_len, B);
     take(p.skip, B);
     take(p.gid, B);
@@ -875,31 +868,24 @@ size_t layout(Plan& p, unsigned char* base, int B, int P_max, int Hq, int D, int
     take(p.node_row, (size_t)B * P_max);
     take(p.group, n_groups);
     take(p.first, (size_t)n_groups + 1);
-    take(p.sk_table, 2 * (size_t)B + 1);
-    take(p.pre_rows, rows * D);
-    take(p.pre_ml, rows);
-    take(p.pre_part, pre * D);
-    take(p.pre_part_ml, pre);
-    take(p.suf_rows, rows * D);
-    take(p.suf_ml, rows);
-    take(p.suf_part, suf * D);
-    take(p.suf_part_ml, suf);
-    return at;
-}
-
-cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, kernel, args);
+    take(p.req, B);
+    take(p.unit, (p.rows_cap / kUnitRows + n_groups) * Hkv);
+    take(p.rows, p.rows_cap * Hkv * (D / 4));
+    take(p.rows_ml, p.rows_cap * Hkv);
+    take(p.part, slots * kUnitRows * (D / 4));
+    take(p.part_ml, slots * kUnitRows);
+    take(p.suffix.rows, p.rows_cap * Hkv * (D / 4));
+    take(p.suffix.rows_ml, p.rows_cap * Hkv);
+    take(p.suffix.unit, suffix.table ? (size_t)suffix.tiles * B * Hkv : 0);
+    take(p.suf_first, suffix.few_rows ? (size_t)B + 1 : 0);
+    p.suffix.rows_cap = p.rows_cap;
+    p.suffix.skip = p.skip;
+    p.slot_rows = suffix.slot_rows;
+    suffix_ws = base == nullptr ? nullptr : base + at;
+    const size_t suf_rows = (size_t)2 * suffix.grid * suffix.slot_rows;
+    p.suf_part = static_cast<float4*>(suffix_ws);
+    p.suf_part_ml = reinterpret_cast<float2*>(p.suf_part + suf_rows * (D / 4));
+    return at + (suffix.few_rows ? suf_rows * (D * sizeof(float) + sizeof(float2)) : suffix.plan.ws_bytes);
 }
 
 template <int D>
@@ -913,32 +899,14 @@ cudaError_t launch_prefix(int grid, cudaStream_t stream, PrefixArgs& a, CUtensor
                             Cfg<D>::kSmemBytes, stream, args);
 }
 
-template <int D>
-cudaError_t launch_merge(cudaStream_t stream, MergeArgs& a)
-{
-    const long long sms = rd_device_sm_count();
-    const long long nodes = (long long)a.B * a.P_max;
-    // few rows: a CTA per row, its warps sharing the row's pieces (which a short
-    // batch has many of); else eight rows at a time per CTA, and as many heads as
-    // leave a few CTAs per SM
-    const bool few = nodes * a.Hq <= 8 * sms;
-    a.heads = few ? 1 : a.Hq;
-    while (!few && a.heads > kMergeWarps && nodes * ((a.Hq + a.heads - 1) / a.heads) < 8 * sms)
-        a.heads = std::max(kMergeWarps, a.heads / 2);
-    const long long grid = nodes * ((a.Hq + a.heads - 1) / a.heads);
-    void* args[] = {&a};
-    return launch_dependent(few ? reinterpret_cast<const void*>(merge_kernel<D, kMergeWarps>)
-                                : reinterpret_cast<const void*>(merge_kernel<D, 1>),
-                            dim3((unsigned)grid), dim3(kMergeThreads), 0, stream, args);
-}
-
 }  // namespace
 
 size_t rd_shared_workspace_bytes(int B, int P_max, int Hq, int Hkv, int D, int max_ctx, int n_groups)
 {
     Plan p;
-    return layout(p, nullptr, B, P_max, Hq, D, n_groups, rd_device_sm_count(),
-                  rd_attn_make_plan(B, P_max, Hq, Hkv, D, max_ctx));
+    void* suffix_ws;
+    return layout(p, suffix_ws, nullptr, B, P_max, Hq, Hkv, D, n_groups, rd_device_sm_count(),
+                  choose_suffix(B, P_max, Hq, Hkv, D, max_ctx));
 }
 
 cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D, float scale, const void* q,
@@ -949,7 +917,7 @@ cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D,
                                        const uint32_t* mask, int mask_words, void* o, void* workspace,
                                        int32_t* dev_status, cudaStream_t stream)
 {
-    const rd_attn_plan suffix = rd_attn_make_plan(B, P_max, Hq, Hkv, D, max_ctx);
+    const SuffixChoice suffix = choose_suffix(B, P_max, Hq, Hkv, D, max_ctx);
     const int pre_grid = rd_device_sm_count();
     PlanArgs pa = {};
     pa.B = B;
@@ -960,13 +928,16 @@ cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D,
     pa.max_pages = paged.max_pages;
     pa.max_ctx = max_ctx;
     pa.n_groups = n_groups;
+    pa.suffix_chunk = suffix.few_rows ? rd_suffix_chunk(rd_suffix_row_warps(P_max * pa.G)) : 0;
     pa.lens = packed_len;
     pa.ctx_lens = paged.ctx_lens;
     pa.group_offsets = group_offsets;
     pa.prefix_pages = prefix_pages;
     pa.status = dev_status;
-    layout(pa.p, static_cast<unsigned char*>(workspace), B, P_max, Hq, D, n_groups, pre_grid, suffix);
-    plan_kernel<<<1, kScanThreads, 0, stream>>>(pa);
+    void* suffix_ws;
+    layout(pa.p, suffix_ws, static_cast<unsigned char*>(workspace), B, P_max, Hq, Hkv, D, n_groups, pre_grid, suffix);
+    if (B <= kScanThreads && n_groups <= kScanThreads) plan_kernel<true><<<1, kScanThreads, 0, stream>>>(pa);
+    else plan_kernel<false><<<1, kScanThreads, 0, stream>>>(pa);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
@@ -992,28 +963,25 @@ cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D,
     e = D == 128 ? launch_prefix<128>(pre_grid, stream, fa, mk, mv) : launch_prefix<64>(pre_grid, stream, fa, mk, mv);
     if (e != cudaSuccess) return e;
 
-    rd_shared_suffix sh;
-    sh.skip = pa.p.skip;
-    sh.o_rows = pa.p.suf_rows;
-    sh.ml_rows = pa.p.suf_ml;
-    sh.o_part = pa.p.suf_part;
-    sh.ml_part = pa.p.suf_part_ml;
-    sh.sk_table = pa.p.sk_table;
-    e = rd_launch_attention(suffix, B, P_max, Hq, Hkv, D, scale, q, k_new, v_new, k_pool, v_pool, nullptr, 0, max_ctx,
-                            pa.p.eff_len, mask, mask_words, o, nullptr, dev_status, stream, &paged, nullptr, &sh);
+    if (suffix.few_rows)
+        e = rd_launch_shared_suffix(pa.p, B, P_max, Hq, Hkv, D, fa.scale_log2, q, k_new, v_new, k_pool, v_pool, paged,
+                                    mask, mask_words, dev_status, stream);
+    else
+        e = rd_launch_attention(suffix.plan, B, P_max, Hq, Hkv, D, scale, q, k_new, v_new, k_pool, v_pool, nullptr, 0, max_ctx,
+                                pa.p.eff_len, mask, mask_words, o, suffix_ws, dev_status, stream, &paged, nullptr,
+                                &pa.p.suffix);
     if (e != cudaSuccess) return e;
 
     MergeArgs ma = {};
-    ma.B = B;
     ma.P_max = P_max;
     ma.Hq = Hq;
     ma.Hkv = Hkv;
     ma.G = pa.G;
-    ma.n_groups = n_groups;
-    ma.pre_grid = pre_grid;
-    ma.suf_grid = suffix.grid;
-    ma.suf_sk = suffix.stream_k;
+    ma.B = B;
+    ma.blocks = (P_max * pa.G + kMergeRows - 1) / kMergeRows;
+    ma.table = suffix.table;
     ma.p = pa.p;
     ma.o = static_cast<uint16_t*>(o);
-    return D == 128 ? launch_merge<128>(stream, ma) : launch_merge<64>(stream, ma);
+    const dim3 merge_grid((unsigned)((size_t)B * Hkv * ma.blocks));
+    return D == 128 ? launch_merge<128>(merge_grid, stream, ma) : launch_merge<64>(merge_grid, stream, ma);
 }
