@@ -276,20 +276,25 @@ def test_refuses_before_a_launch():
         call(s, out=torch.empty(1, 1, 2, 64, dtype=torch.bfloat16, device=DEV))
 
 
-def test_a_wait_that_runs_out_is_reported():
+@pytest.mark.parametrize("name", ["one token each", "many rows", "48 rows"])
+def test_a_wait_that_runs_out_is_reported(name):
     rd = _rd()
-    s = make(**CASES["one token each"], seed=2)
+    s = make(**CASES[name], seed=2)
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
-    rd.rd_debug_stall_attention(20_000_000)
-    try:
-        call(s, st)
-        torch.cuda.synchronize()
-    finally:
-        rd.rd_debug_stall_attention(0)
-    assert st.item() & rd.DEV_TIMEOUT
-    st.zero_()
-    check(call(s, st), s)
-    assert st.item() == 0
+    B, P, Hq, D = s["q"].shape
+    size = rd.rd_tree_attention_shared_workspace_size(B, P, Hq, s["k_new"].shape[2], D, s["max_ctx"], len(s["pages"]), DEV)
+    for fill in (0, 255, 7):                           # tables that the kernels then leave as they are
+        ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV)
+        rd.rd_debug_stall_attention(2_000_000)
+        try:
+            call(s, st, workspace=ws)
+            torch.cuda.synchronize()
+        finally:
+            rd.rd_debug_stall_attention(0)
+        assert st.item() & rd.DEV_TIMEOUT
+        st.zero_()
+        check(call(s, st, workspace=ws), s)
+        assert st.item() == 0
 
 
 def test_a_run_of_steps_over_one_cache():

@@ -255,7 +255,8 @@ struct Bar {
     uint64_t q_full;          // the unit's query tiles are in shared memory
     uint64_t q_free;          // every S MMA of the unit has completed
     uint64_t s_full[2];       // S of the tile's chunk is in TMEM (and PV of the one before is done)
-    uint64_t p_full[2];       // P of the tile's chunk is written (four softmax warps)
+    uint64_t p_half[2];       // P of the chunk's first 64 positions is written (four softmax warps)
+    uint64_t p_full[2];       // ... of all of them
     uint64_t o_final[2];      // the tile's last PV of the unit has completed
     uint64_t o_free[2];       // the tile's epilogue has read O
     uint64_t drain;
@@ -322,7 +323,40 @@ __device__ __forceinline__ void cp_async16(void* smem, const void* gmem)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(gmem) : "memory");
 }
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// two floats in one 64-bit register pair (first: low half)
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -348,6 +382,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
         mbar_init(&bar.q_free, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar.s_full[t], 1);
+            mbar_init(&bar.p_half[t], 4);
             mbar_init(&bar.p_full[t], 4);
             mbar_init(&bar.o_final[t], 1);
             mbar_init(&bar.o_free[t], 4);
@@ -444,32 +479,45 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
         }
     } else if (warp >= kQWarp0) {
         // ------------------------------------------------------- query loader
-        // Row m of the unit is head row % G of compact node row / G.  16-byte
-        // pieces, all in flight at once; rows past the unit's are zero.
+        // Warp t loads tile t.  Row m of the unit is head row % G of compact node
+        // row / G; a lane looks four rows up while the tile before is still in use,
+        // then half a warp copies a row in 16-byte pieces (cp.async), all 128 rows'
+        // in flight at once.  Rows past the unit's are zero.
+        constexpr int kVecs = D / 8;                      // 16-byte pieces of a row
+        constexpr int kRowsAtOnce = 32 / kVecs;
         const int t0 = tid - kQWarp0 * 32;                // 0 .. 63
+        const int t = warp - kQWarp0;
         uint32_t it = 0;
         Walk w;
         w.begin(a);
         Piece u;
         while (!*abort && w.next(a, u)) {
-            if (it > 0 && !warp_wait(&bar.q_free, (it - 1) & 1, abort, kWaitBudget)) { fail(); break; }
-            constexpr int kVecs = D / 8;                  // 16-byte pieces of a row
-            const int m_end = u.rows > kM ? kUnitRows : kM;
-#pragma unroll 4
-            for (int i = t0; i < m_end * kVecs; i += 64) {
-                const int m = i / kVecs, c = i % kVecs;
-                unsigned char* dst = smem + C::kQOff + (m / kM) * C::kQBytes + (c >> 3) * (kM * 128) +
-                                     sw128(m % kM, c & 7);
-                if (m < u.rows) {
-                    const int row = u.row0 + m;
-                    const size_t node = a.p.node_row[u.g.node0 + row / a.G];
-                    cp_async16(dst, a.q + (node * a.Hq + u.h * a.G + row % a.G) * D + c * 8);
-                } else {
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-                }
+            const bool active = t == 0 || u.rows > kM;
+            uint32_t at[4];                               // row of q, of tile rows lane + 32 k
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int m = t * kM + lane + 32 * k, row = u.row0 + m;
+                at[k] = 0xffffffffu;
+                if (m < u.rows)
+                    at[k] = (uint32_t)__ldcg(a.p.node_row + u.g.node0 + row / a.G) * a.Hq + u.h * a.G + row % a.G;
             }
-            cp_async_wait_all();
-            fence_proxy_async_smem();
+            if (it > 0 && !warp_wait(&bar.q_free, (it - 1) & 1, abort, kWaitBudget)) { fail(); break; }
+            if (active) {
+                const int c = lane % kVecs;
+                unsigned char* base = smem + C::kQOff + t * C::kQBytes + (c >> 3) * (kM * 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll 4
+                    for (int i = 0; i < 32; i += kRowsAtOnce) {
+                        const int m = i + lane / kVecs;
+                        const uint32_t row = __shfl_sync(0xffffffffu, at[k], m);
+                        unsigned char* dst = base + sw128(32 * k + m, c & 7);
+                        if (row != 0xffffffffu) cp_async16(dst, a.q + (size_t)row * D + c * 8);
+                        else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+                    }
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.q_full);
             ++it;
@@ -490,88 +538,128 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
         // The MMAs of one thread run in issue order, so S_t(j + 1) may overwrite
         // P_t(j) right behind PV_t(j), and the commit that completes it also
         // covers PV_t(j): softmax t finds O_t stable when it rescales.
-        if (lane == 0) {
-            constexpr uint32_t idS = idesc_bf16(kM, kN, false, false);
-            constexpr uint32_t idSh = idesc_bf16(kM, kN / 2, false, false);
-            constexpr uint32_t idPV = idesc_bf16(kM, D, false, true);
-            const uint64_t k_desc = smem_desc(smem_addr(smem), 16, 1024, kSwizzle128B);
-            const uint64_t v_desc = smem_desc(smem_addr(smem), kN * 128, 1024, kSwizzle128B);
-            const uint64_t q_desc = smem_desc(smem_addr(smem + C::kQOff), 16, 1024, kSwizzle128B);
-            if (a.stall_budget > 0 && !mbar_wait(&bar.never, 0, abort, a.stall_budget)) fail();
-            uint32_t g = 0, it = 0;                       // ring entries, units
-            uint32_t ct[2] = {0u, 0u};                    // chunks of tile t so far
-            uint32_t ut[2] = {0u, 0u};                    // units with tile t so far
-            Walk w;
-            w.begin(a);
-            Piece u;
-            while (!*abort && w.next(a, u)) {
-                const int nb = u.rows > kM ? 2 : 1;       // active tiles
-                // positions of the piece's chunk j: 64 in a prefix's odd last half
-                auto half = [&](int j) { return (u.c0 + j) * kN + 64 >= u.g.positions; };
-                auto stage = [&](uint32_t k) { return (int)(k % C::kStages); };
-                auto full = [&](uint32_t k) {
-                    return mbar_wait(&bar.kv_full[stage(k)], (k / C::kStages) & 1, abort, kWaitBudget);
-                };
-                auto issue_s = [&](int t, int j) {
-                    const uint64_t kd = k_desc + (uint64_t)((stage(g + 2 * j) * C::kStageBytes) >> 4);
-                    const uint64_t qd = q_desc + (uint64_t)((t * C::kQBytes) >> 4);
-                    const uint32_t id = half(j) ? idSh : idS;
+        // The whole warp walks the loop and one elected lane issues: the operands
+        // are then the same in all lanes and stay in uniform registers.  With only
+        // lane 0 in the loop each of the 32 MMAs of a chunk took the issuer 109
+        // cycles, against the 64 that the tensor core needs.  Every elected block ends
+        // in __syncwarp: a lane that ran ahead into the next wait could hold up the
+        // one that has yet to issue what that wait is for.
+        constexpr uint32_t idS = idesc_bf16(kM, kN, false, false);
+        constexpr uint32_t idSh = idesc_bf16(kM, kN / 2, false, false);
+        constexpr uint32_t idPV = idesc_bf16(kM, D, false, true);
+        constexpr uint32_t kStage16 = C::kStageBytes >> 4;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // descriptors: only the low word (the start address) changes
+        const uint64_t k_desc = smem_desc(smem_addr(smem), 16, 1024, kSwizzle128B);
+        const uint64_t v_desc = smem_desc(smem_addr(smem), kN * 128, 1024, kSwizzle128B);
+        const uint64_t q_desc = smem_desc(smem_addr(smem + C::kQOff), 16, 1024, kSwizzle128B);
+        const uint32_t k_lo = __shfl_sync(0xffffffffu, (uint32_t)k_desc, 0), k_hi = (uint32_t)(k_desc >> 32);
+        const uint32_t v_lo = __shfl_sync(0xffffffffu, (uint32_t)v_desc, 0), v_hi = (uint32_t)(v_desc >> 32);
+        const uint32_t q_lo = __shfl_sync(0xffffffffu, (uint32_t)q_desc, 0), q_hi = (uint32_t)(q_desc >> 32);
+        const bool leader = elect_one();
+        if (a.stall_budget > 0 && !warp_wait(&bar.never, 0, abort, a.stall_budget)) fail();
+        uint32_t st = 0, ph = 0;                          // the ring's next entry, its phase
+        uint32_t it = 0;                                  // units
+        uint32_t pp[2] = {0u, 0u};                        // phase of p_half and p_full
+        uint32_t ut[2] = {0u, 0u};                        // units with tile t so far
+        auto step = [&](uint32_t& s_, uint32_t& p_) {     // take the ring's next entry
+            s_ = st;
+            p_ = ph;
+            if (++st == (uint32_t)C::kStages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        };
+        auto commit = [&](uint64_t* b) {
+            if (leader) mma_commit(b);
+            __syncwarp();
+        };
+        auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, abort, kWaitBudget); };
+        Walk w;
+        w.begin(a);
+        Piece u;
+        while (!*abort && w.next(a, u)) {
+            const int n = __shfl_sync(0xffffffffu, u.n, 0);
+            const int nb = __shfl_sync(0xffffffffu, u.rows, 0) > kM ? 2 : 1;      // active tiles
+            // an odd last half: 64 positions
+            const int odd = __shfl_sync(0xffffffffu, (u.c0 + u.n - 1) * kN + 64 >= u.g.positions ? u.n - 1 : -1, 0);
+            auto issue_s = [&](int t, uint32_t ks, int j) {
+                const uint32_t id = j == odd ? idSh : idS;
+                const uint32_t kd = k_lo + ks * kStage16, qd = q_lo + t * (C::kQBytes >> 4);
+                if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * (kM * 128) + (ks & 3) * 32) >> 4;
-                        mma_smem_a(tmem + C::s_col(t), qd + off, kd + off, id, ks > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4;
+                        mma_smem_a(tm + C::s_col(t), desc64(qd + off, q_hi), desc64(kd + off, k_hi), id, k > 0);
                     }
                     mma_commit(&bar.s_full[t]);
-                };
-                bool ok = mbar_wait(&bar.q_full, it & 1, abort, kWaitBudget) && full(g);
-                if (!ok) { fail(); break; }
-                tc_fence_after();
-                for (int t = 0; t < nb; ++t) issue_s(t, 0);
-                mma_commit(&bar.kv_empty[stage(g)]);
-                if (u.n == 1) mma_commit(&bar.q_free);
-                for (int j = 0; ok && j < u.n; ++j) {
-                    const uint32_t kv = g + 2 * j + 1;    // ring entry of V_j; K_{j+1} is the next
-                    for (int t = 0; t < nb; ++t) {
-                        if (t == 0 && !full(kv)) { ok = false; break; }
-                        if (j == 0 && ut[t] > 0 && !mbar_wait(&bar.o_free[t], (ut[t] - 1) & 1, abort, kWaitBudget)) {
-                            ok = false;
-                            break;
-                        }
-                        if (!mbar_wait(&bar.p_full[t], (ct[t] + j) & 1, abort, kWaitBudget)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint64_t vd = v_desc + (uint64_t)((stage(kv) * C::kStageBytes) >> 4);
-                        const int steps = half(j) ? kN / 32 : kN / 16;
+                }
+                __syncwarp();
+            };
+            uint32_t ks, kp, vs, vp;
+            step(ks, kp);
+            bool ok = wait(&bar.q_full, it & 1) && wait(&bar.kv_full[ks], kp);
+            if (!ok) { fail(); break; }
+            tc_fence_after();
+            issue_s(0, ks, 0);
+            if (nb == 2) issue_s(1, ks, 0);
+            commit(&bar.kv_empty[ks]);
+            if (n == 1) commit(&bar.q_free);
+            for (int j = 0; ok && j < n; ++j) {
+                const bool more = j + 1 < n;
+                step(vs, vp);
+                if (more) step(ks, kp);
 #pragma unroll
-                        for (int kk = 0; kk < kN / 16; ++kk)
-                            if (kk < steps)
-                                mma_tmem_a(tmem + C::o_col(t), tmem + C::s_col(t) + kk * 8,
-                                           vd + (uint64_t)((kk * 2048) >> 4), idPV, j > 0 || kk > 0);
-                        if (t == nb - 1) mma_commit(&bar.kv_empty[stage(kv)]);
-                        if (j + 1 < u.n) {
-                            if (t == 0 && !full(kv + 1)) { ok = false; break; }
-                            tc_fence_after();
-                            issue_s(t, j + 1);
-                            if (t == nb - 1) {
-                                mma_commit(&bar.kv_empty[stage(kv + 1)]);
-                                if (j + 1 == u.n - 1) mma_commit(&bar.q_free);
-                            }
-                        } else {
-                            mma_commit(&bar.o_final[t]);
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= nb) break;
+                    if (t == 0) ok = wait(&bar.kv_full[vs], vp);
+                    if (j == 0 && ut[t] > 0) ok = ok && wait(&bar.o_free[t], (ut[t] - 1) & 1);
+                    // the first 64 positions' product starts while the softmax warps
+                    // work on the other half
+                    ok = ok && wait(&bar.p_half[t], pp[t]);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t vd = v_lo + vs * kStage16;
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < kN / 32; ++k)
+                            mma_tmem_a(tm + C::o_col(t), tm + C::s_col(t) + k * 8, desc64(vd + k * 128, v_hi), idPV,
+                                       j > 0 || k > 0);
+                    }
+                    __syncwarp();
+                    ok = wait(&bar.p_full[t], pp[t]);
+                    if (!ok) break;
+                    pp[t] ^= 1u;
+                    tc_fence_after();
+                    if (j != odd && leader) {
+#pragma unroll
+                        for (int k = kN / 32; k < kN / 16; ++k)
+                            mma_tmem_a(tm + C::o_col(t), tm + C::s_col(t) + k * 8, desc64(vd + k * 128, v_hi), idPV, true);
+                    }
+                    __syncwarp();
+                    if (t == nb - 1) commit(&bar.kv_empty[vs]);
+                    if (more) {
+                        if (t == 0) ok = wait(&bar.kv_full[ks], kp);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(t, ks, j + 1);
+                        if (t == nb - 1) {
+                            commit(&bar.kv_empty[ks]);
+                            if (j + 2 == n) commit(&bar.q_free);
                         }
+                    } else {
+                        commit(&bar.o_final[t]);
                     }
                 }
-                if (!ok) { fail(); break; }
-                for (int t = 0; t < nb; ++t) {
-                    ct[t] += u.n;
-                    ++ut[t];
-                }
-                g += 2 * u.n;
-                ++it;
             }
-            // drain: every issued MMA must finish before TMEM is freed
-            mma_commit(&bar.drain);
-            mbar_wait(&bar.drain, 0, &no_abort, kWaitBudget);
+            if (!ok) { fail(); break; }
+            ++ut[0];
+            if (nb == 2) ++ut[1];
+            ++it;
         }
+        // drain: every issued MMA must finish before TMEM is freed
+        commit(&bar.drain);
+        mbar_wait(&bar.drain, 0, &no_abort, kWaitBudget);
     }
     } else {
         // ------------------------------------------------------------ softmax
@@ -593,7 +681,10 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
             // never read
             const bool dead = __all_sync(0xffffffffu, !valid);
             float m = -INFINITY, l = 0.f;
-            // one chunk: NC = 128 positions, or the 64 of an odd last half
+            // one chunk: NC = 128 positions, or the 64 of an odd last half.  Two
+            // columns an instruction where the machine has one (fma, add), and P in
+            // two halves, each handed to the issuer as soon as it is written
+            const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
             auto chunk = [&](auto nc, bool first) {
                 constexpr int NC = decltype(nc)::value;
                 uint32_t s[NC];
@@ -605,7 +696,11 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
                 for (int e = 0; e < 8; ++e) mx8[e] = __uint_as_float(s[e]);
 #pragma unroll
-                for (int c = 8; c < NC; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], __uint_as_float(s[c]));
+                for (int c = 8; c < NC; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        mx8[e] = c + 8 + e < NC ? fmaxf(fmaxf(mx8[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 8 + e]))
+                                                : fmaxf(mx8[e], __uint_as_float(s[c + e]));
                 const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                        fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
                 const float ms = mx * a.scale_log2;
@@ -627,36 +722,49 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
                     m = ms;
                 }
                 const float base = m == -INFINITY ? 0.f : m;
-                float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                const uint64_t base2 = pack2(-base, -base);
+                uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int h = 0; h < NC / 64; ++h) {
                     uint32_t pv[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float p0 = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * e]), a.scale_log2, -base));
-                        const float p1 = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * e + 1]), a.scale_log2, -base));
-                        sum[(2 * e) & 7] += p0;
-                        sum[(2 * e + 1) & 7] += p1;
+                        const uint64_t x = fma2(pack2(__uint_as_float(s[64 * h + 2 * e]), __uint_as_float(s[64 * h + 2 * e + 1])),
+                                                scale2, base2);
+                        float x0, x1;
+                        unpack2(x, x0, x1);
+                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                        sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
                         pv[e] = pack_bf16(p0, p1);
                     }
                     tmem_st32(sc + 32 * h, pv);
+                    if (h == 0 && NC == 128) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.p_half[t]);
+                    }
                 }
-                l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+                float a0, a1;
+                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+                l += a0 + a1;
+                tmem_st_wait();
             };
             bool ok = true;
             for (int j = 0; j < u.n; ++j) {
                 if (!warp_wait(&bar.s_full[t], (ct + j) & 1, abort, kWaitBudget)) { ok = false; break; }
                 tc_fence_after();
+                const bool all = (u.c0 + j) * kN + 64 < u.g.positions;
                 if (!dead) {
-                    if ((u.c0 + j) * kN + 64 < u.g.positions)
-                        chunk(std::integral_constant<int, 128>{}, j == 0);
-                    else
-                        chunk(std::integral_constant<int, 64>{}, j == 0);
-                    tmem_st_wait();
+                    if (all) chunk(std::integral_constant<int, 128>{}, j == 0);
+                    else chunk(std::integral_constant<int, 64>{}, j == 0);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full[t]);
+                if (lane == 0) {
+                    if (dead || !all) mbar_arrive(&bar.p_half[t]);
+                    mbar_arrive(&bar.p_full[t]);
+                }
             }
             if (!ok || !warp_wait(&bar.o_final[t], ut & 1, abort, kWaitBudget)) { fail(); break; }
             tc_fence_after();
@@ -711,7 +819,7 @@ struct MergeArgs {
 };
 constexpr int kMergeThreads = 256;
 constexpr int kMergePieces = 2;
-constexpr int kMergeRows = 64;
+constexpr int kMergeRows = 32;
 template <int D> constexpr int kMergeSmem = kMergePieces * kMergeRows * D * 4;
 
 template <int D>
@@ -730,21 +838,22 @@ merge_kernel(const MergeArgs a)
     const int all = a.P_max * a.G;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = __ldcg(a.p.eff_len + b);
+    const int4 req = __ldcg(a.p.req + b);
     int n = 0;                                            // the row's pieces
-    if (part == 0 && row < len * a.G) {
-        const int4 req = __ldcg(a.p.req + b);
-        int2 su = make_int2(1, 0);
+    if (part == 0 && row < all) {
+        int2 su = make_int2(1, 0);                        // (a skipped request's entry is not used)
         if (a.table) su = __ldcg(a.p.suffix.unit + ((size_t)(row / a.p.slot_rows) * a.B + b) * a.Hkv + h);
         Pieces pre = {};
-        if (req.x >= 0) {
+        const bool in = row < len * a.G;
+        if (in && req.x >= 0) {
             const int gr = req.z + row;
             pre = pieces_of<D>(__ldcg(a.p.unit + req.x + h * req.y + gr / kUnitRows), a.p, h, req.w + row,
                                gr % kUnitRows);
         }
         s_pc[0][r] = pre;
         s_pc[1][r] = pieces_at<D>(su, a.p.suffix.rows, a.p.suffix.rows_ml, a.p.suffix.rows_cap, h, (size_t)b * all + row,
-                                  a.p.suf_part, a.p.suf_part_ml, a.p.slot_rows, row % a.p.slot_rows);
-        n = pre.n + su.x;
+                                  a.p.suf_part, a.p.suf_part_ml, a.p.slot_rows, row % a.p.slot_rows, a.p.suf_grid);
+        n = in ? pre.n + s_pc[1][r].n : 0;
     }
     const int live = min(kMergeRows, len * a.G - row0);   // may be <= 0
     int most = n;                                         // of the CTA's rows
@@ -881,6 +990,8 @@ size_t layout(Plan& p, void*& suffix_ws, unsigned char* base, int B, int P_max, 
     p.suffix.rows_cap = p.rows_cap;
     p.suffix.skip = p.skip;
     p.slot_rows = suffix.slot_rows;
+    p.grid = pre_grid;
+    p.suf_grid = suffix.grid;
     suffix_ws = base == nullptr ? nullptr : base + at;
     const size_t suf_rows = (size_t)2 * suffix.grid * suffix.slot_rows;
     p.suf_part = static_cast<float4*>(suffix_ws);

@@ -45,6 +45,7 @@ struct Plan {
     float4* suf_part;
     float2* suf_part_ml;
     int slot_rows;
+    int grid, suf_grid;    // CTAs of the two launches
     uint32_t* suf_first;   // [B + 1] suffix chunks of the requests before (shared_suffix.cu)
 };
 
@@ -81,13 +82,19 @@ struct Pieces {
 };
 
 // unit = (pieces, first slot); a whole unit's rows are [h][D / 4][cap] at `row`,
-// pieces lie in slots of R rows at r, those behind the first in slots 2 c
+// pieces lie in slots of R rows at r, those behind the first in slots 2 c, all
+// below 2 `grid`.  A launch whose waits ran out may have left an entry unwritten:
+// what is no such entry counts as no pieces.
 template <int D>
 __device__ __forceinline__ Pieces pieces_at(int2 unit, const float4* rows, const float2* rows_ml, size_t cap, int h,
-                                            size_t row, const float4* part, const float2* part_ml, int R, int r)
+                                            size_t row, const float4* part, const float2* part_ml, int R, int r,
+                                            int grid)
 {
     Pieces p;
-    p.n = unit.x;
+    const bool fine = unit.x == 1 ||
+                      (unit.x > 1 && unit.x <= grid && unit.y >= 0 && unit.y < 2 * grid && unit.y / 2 + unit.x <= grid);
+    p.n = fine ? unit.x : 0;
+    if (!fine) unit = make_int2(1, 0);
     const bool whole = unit.x == 1;
     const size_t next = 2 * (size_t)(unit.y / 2 + 1);
     p.stride = whole ? cap : (size_t)R;
@@ -104,7 +111,7 @@ __device__ __forceinline__ Pieces pieces_at(int2 unit, const float4* rows, const
 template <int D>
 __device__ __forceinline__ Pieces pieces_of(int2 unit, const Plan& p, int h, int row, int r)
 {
-    return pieces_at<D>(unit, p.rows, p.rows_ml, p.rows_cap, h, (size_t)row, p.part, p.part_ml, kUnitRows, r);
+    return pieces_at<D>(unit, p.rows, p.rows_ml, p.rows_cap, h, (size_t)row, p.part, p.part_ml, kUnitRows, r, p.grid);
 }
 
 // ---- the suffix kernel for few rows per kv head (shared_suffix.cu)
