@@ -325,9 +325,10 @@ rd_status rd_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* r
  * its own parent, or is named by an earlier pair sets RD_DEV_BAD_INDEX; a parent whose
  * length is negative or not covered by its pages sets RD_DEV_BAD_LENGTH; a pair
  * for whose last page no free page is left sets RD_DEV_OVERFLOW: that pair is
- * skipped.  Workspace: rd_fork_pages_workspace_size(n) bytes, no initial contents.
+ * skipped.  Workspace: rd_fork_pages_workspace_size() bytes (none for little
+ * data), no initial contents.
  */
-size_t rd_fork_pages_workspace_size(int n);
+size_t rd_fork_pages_workspace_size(int n, int layers, size_t page_bytes);
 rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
                         int page_size, int32_t* block_table, int R, int max_pages,
                         int32_t* row_pages, int32_t* page_refs, int32_t* ctx_lens,
@@ -341,7 +342,8 @@ rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, s
  * side by side, so none may depend on another: a pair with an id out of range,
  * with the destination of an earlier pair, or whose source is the destination of
  * another pair sets RD_DEV_BAD_INDEX and is skipped.  Touches no table.
- * Workspace: rd_copy_pages_workspace_size(n) bytes, no initial contents.
+ * Workspace: rd_copy_pages_workspace_size(n) bytes (none for few pairs), no
+ * initial contents.
  */
 size_t rd_copy_pages_workspace_size(int n);
 rd_status rd_copy_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,

@@ -124,6 +124,8 @@ CASES = {
     "32 rows d64": dict(B=5, W=4, L=4, Hq=8, Hkv=4, D=64, page=128, offsets=[0, 5], pages=[2], suffix=300),
     "33 rows": dict(B=7, W=11, L=1, Hq=6, Hkv=2, D=64, page=64, offsets=[0, 7], pages=[1], suffix=129),
     "48 rows": dict(B=4, W=8, L=6, Hq=3, Hkv=3, D=128, page=256, offsets=[0, 4], pages=[1], suffix=1000),
+    # enough units that the CTAs take them whole off a counter
+    "counter": dict(B=50, W=4, L=3, Hq=120, Hkv=40, D=64, page=64, offsets=[0, 20, 50], pages=[2, 1], suffix=100),
     # two requests whose own contexts are long: cut into many pieces
     "long own contexts": dict(B=2, W=2, L=4, Hq=8, Hkv=2, D=128, page=64, offsets=[0, 2], pages=[4], suffix=6000),
     "long own contexts, one token": dict(B=2, W=1, L=1, Hq=8, Hkv=1, D=64, page=64, offsets=[0, 2], pages=[1],

@@ -28,25 +28,26 @@ def test_resize_validation():
 def test_fork_validation():
     f = rd._lib.rd_fork_pages
     good = dict(k=ONE, v=ONE, layers=2, pages=16, bytes=4096, ps=64, table=ONE, R=4, width=8, rows=ONE,
-                refs=ONE, ctx=ONE, par=ONE, kid=ONE, n=3, ws=ONE, wsb=36)
+                refs=ONE, ctx=ONE, par=ONE, kid=ONE, n=300, ws=ONE, wsb=3600)
 
     def call(**kw):
         return f(*{**good, **kw}.values(), N, N)
     assert call(n=0) == rd.RD_OK and call(R=0) == rd.RD_OK
     for kw in (dict(k=N), dict(v=N), dict(layers=0), dict(pages=-1), dict(bytes=0), dict(ps=0), dict(ps=48),
                dict(table=N), dict(R=-1), dict(width=-1), dict(rows=N), dict(refs=N), dict(ctx=N), dict(par=N),
-               dict(kid=N), dict(n=-1), dict(ws=N), dict(wsb=35), dict(k=ctypes.c_void_p(264))):
+               dict(kid=N), dict(n=-1), dict(ws=N), dict(wsb=3599), dict(k=ctypes.c_void_p(264))):
         assert call(**kw) == rd.RD_ERR_INVALID_ARG, kw
     for kw in (dict(bytes=4104), dict(n=16385, wsb=1 << 20), dict(R=16385), dict(pages=262145)):
         assert call(**kw) == rd.RD_ERR_UNSUPPORTED, kw
-    assert rd._lib.rd_fork_pages_workspace_size(3) == 36 and rd._lib.rd_fork_pages_workspace_size(0) == 0
+    assert rd._lib.rd_fork_pages_workspace_size(300, 2, 4096) == 3600          # 4.9 MB: a list for the copy
+    assert rd._lib.rd_fork_pages_workspace_size(3, 2, 4096) == 0               # little data: no workspace
 
 
 def test_copy_and_compact_validation():
     f = rd._lib.rd_copy_pages
     assert f(N, N, 1, 16, 4096, N, N, 0, N, 0, N, N) == rd.RD_OK
-    good = dict(k=ONE, v=ONE, layers=2, pages=16, bytes=4096, src=ONE, dst=ONE, n=3, ws=ONE, wsb=24)
-    for kw in (dict(k=N), dict(v=N), dict(src=N), dict(dst=N), dict(n=-1), dict(ws=N), dict(wsb=23),
+    good = dict(k=ONE, v=ONE, layers=2, pages=16, bytes=4096, src=ONE, dst=ONE, n=257, ws=ONE, wsb=2056)
+    for kw in (dict(k=N), dict(v=N), dict(src=N), dict(dst=N), dict(n=-1), dict(ws=N), dict(wsb=2055),
                dict(layers=0), dict(v=ctypes.c_void_p(257))):
         assert f(*{**good, **kw}.values(), N, N) == rd.RD_ERR_INVALID_ARG, kw
     for kw in (dict(bytes=4100), dict(n=262145, wsb=1 << 22)):

@@ -72,7 +72,7 @@ def _load() -> ctypes.CDLL:
                                   S, P, P],
         "rd_sample_accept": [P, P, I, I, I, F, P, P, P, P, I, I, P, P, P, P, P, P, P, P],
         "rd_resize_pages": [P, I, I, P, P, I, P, I, P, P],
-        "rd_fork_pages_workspace_size": [I],
+        "rd_fork_pages_workspace_size": [I, I, S],
         "rd_fork_pages": [P, P, I, I, S, I, P, I, I, P, P, P, P, P, I, P, S, P, P],
         "rd_copy_pages_workspace_size": [I],
         "rd_copy_pages": [P, P, I, I, S, P, P, I, P, S, P, P],
@@ -399,7 +399,9 @@ def rd_tree_attention_shared(q, k_new, v_new, k_pool, v_pool, block_table, ctx_l
     if group_offsets.shape[0] != n_groups + 1:
         raise ValueError(f"group_offsets must be [{n_groups + 1}], got {tuple(group_offsets.shape)}")
     _need_status(dev_status, q)
-    out = _new(q.shape, torch.bfloat16, q, stream) if out is None else \
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _new(q.shape, torch.bfloat16, q, stream)
+    else:
         _out(out, "out", q.shape, torch.bfloat16, q)
     if workspace is None:
         workspace = _scratch(None, rd_tree_attention_shared_workspace_size(
@@ -586,9 +588,9 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """A fresh tensor whose memory belongs to the stream that the call runs on, so
     that it is not handed out again while the call still uses it."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _scratch(workspace, size: int, like: torch.Tensor, stream) -> torch.Tensor:
@@ -601,6 +603,14 @@ def _scratch(workspace, size: int, like: torch.Tensor, stream) -> torch.Tensor:
     if workspace.numel() * workspace.element_size() < size:
         raise ValueError(f"workspace must have at least {size} bytes")
     return workspace
+
+
+def _pages_scratch(workspace, size: int, like: torch.Tensor, stream):
+    """(workspace, its bytes) of a page operator; none where none is needed."""
+    if workspace is None and size == 0:
+        return None, 0
+    workspace = _scratch(workspace, size, like, stream)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _need_status(dev_status, like: torch.Tensor):
@@ -669,11 +679,11 @@ def rd_fork_pages(k_pool, v_pool, block_table, row_pages, page_refs, ctx_lens, p
     if ctx_lens.shape[0] != R or child.shape[0] != n:
         raise ValueError("ctx_lens must be [R], and child as long as parent")
     _need_status(dev_status, k_pool)
-    workspace = _scratch(workspace, 12 * n, k_pool, stream)
+    workspace, size = _pages_scratch(workspace, _lib.rd_fork_pages_workspace_size(n, layers, page), k_pool, stream)
     _run("rd_fork_pages", k_pool,
          _ptr(k_pool), _ptr(v_pool), layers, num_pages, page, page_size, _ptr(block_table), R,
          max_pages, _ptr(row_pages), _ptr(page_refs), _ptr(ctx_lens), _ptr(parent), _ptr(child), n,
-         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
+         _ptr(workspace), size, _ptr(dev_status), stream=stream)
 
 
 def rd_copy_pages(k_pool, v_pool, src, dst, *, workspace=None, dev_status=None, stream=None) -> None:
@@ -686,10 +696,10 @@ def rd_copy_pages(k_pool, v_pool, src, dst, *, workspace=None, dev_status=None, 
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
     _need_status(dev_status, k_pool)
-    workspace = _scratch(workspace, 8 * n, k_pool, stream)
+    workspace, size = _pages_scratch(workspace, 8 * n if n > 256 else 0, k_pool, stream)
     _run("rd_copy_pages", k_pool,
          _ptr(k_pool), _ptr(v_pool), layers, num_pages, page, _ptr(src), _ptr(dst), n,
-         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
+         _ptr(workspace), size, _ptr(dev_status), stream=stream)
 
 
 def rd_compact_pages(k_pool, v_pool, block_table, row_pages, page_refs, *, remap=None, n_live=None,
@@ -699,16 +709,22 @@ def rd_compact_pages(k_pool, v_pool, block_table, row_pages, page_refs, *, remap
     rd_compact_pages in rd.h)."""
     layers, num_pages, _, page = _pools(k_pool, v_pool)
     R, max_pages = _tables(block_table, row_pages, page_refs, num_pages, k_pool.device)
+    _need_status(dev_status, k_pool)
     remap = _new((num_pages,), torch.int32, k_pool, stream) if remap is None else \
         _out(remap, "remap", (num_pages,), torch.int32, k_pool)
-    n_live = _new((1,), torch.int32, k_pool, stream) if n_live is None else \
-        _out(n_live, "n_live", (1,), torch.int32, k_pool)
-    _need_status(dev_status, k_pool)
-    workspace = _scratch(workspace, 16 + 8 * (num_pages // 2), k_pool, stream)
+    need = 16 + 8 * (num_pages // 2)
+    if n_live is None and workspace is None:             # one allocation for both
+        both = _new((1 + need // 4,), torch.int32, k_pool, stream)
+        n_live, ws, ws_bytes = both[:1], both.data_ptr() + 4, need
+    else:
+        n_live = _new((1,), torch.int32, k_pool, stream) if n_live is None else \
+            _out(n_live, "n_live", (1,), torch.int32, k_pool)
+        workspace = _scratch(workspace, need, k_pool, stream)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _run("rd_compact_pages", k_pool,
          _ptr(k_pool), _ptr(v_pool), layers, num_pages, page, _ptr(block_table), R, max_pages,
-         _ptr(row_pages), _ptr(page_refs), _ptr(remap), _ptr(n_live), _ptr(workspace),
-         workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
+         _ptr(row_pages), _ptr(page_refs), _ptr(remap), _ptr(n_live), ws, ws_bytes, _ptr(dev_status),
+         stream=stream)
     return remap, n_live
 
 

@@ -143,40 +143,48 @@ resize_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, in
     extern __shared__ int dyn[];
     int* off = dyn;                        // [R + 1] new pages of the rows before
     int* have = dyn + R + 1;               // [R] pages held at the start, -1: invalid row
+    int* want = have + R;                  // [R] pages after the call
     __shared__ ScanSmem sc;
     const cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank();
-    const int warp = rank * kTableWarps + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
-    auto wanted = [&](int r, int h) {      // pages of row r after the call
-        const int n = __ldg(new_lens + r);
-        if (n < 0) return h;
-        const int w = n == 0 ? 0 : (n - 1) / page_size + 1;
-        return w;
-    };
     const int demand = cta_scan_array(R, off, sc.warp_sum, [&](int r) {
         int h = __ldcg(row_pages + r);
-        const int w = wanted(r, h);
+        const int n = __ldg(new_lens + r);
+        const int w = n < 0 ? h : n == 0 ? 0 : (n - 1) / page_size + 1;
         if (h < 0 || h > max_pages || w > max_pages) {
             if (rank == 0) rd_flag(status, RD_DEV_BAD_LENGTH);
             h = -1;
         }
         have[r] = h;
+        want[r] = w;
         return h < 0 ? 0 : max(0, w - h);
     });
-    // give pages back
-    for (int r = warp; r < R; r += kTableCtas * kTableWarps) {
+    // give pages back: as many lanes a row as leaves every row its own, four entries
+    // of a lane on the way at once
+    constexpr int kAll = kTableCtas * kTableThreads, kAtOnce = 4;
+    const int lanes = R <= kAll / 32 ? 32 : R <= kAll / 16 ? 16 : 8;
+    const int me = rank * kTableThreads + (int)threadIdx.x;
+    for (int r = me / lanes; r < R; r += kAll / lanes) {
         const int h = have[r];
         if (h < 0) continue;
         int32_t* row = block_table + (size_t)r * max_pages;
-        for (int j = wanted(r, h) + lane; j < h; j += 32) {
-            const int page = row[j];
-            row[j] = -1;
-            if (page < 0 || page >= num_pages) {
-                rd_flag(status, RD_DEV_BAD_INDEX);
-            } else if (atomicSub(refs + page, 1) <= 0) {        // held by nobody: leave it free
-                atomicAdd(refs + page, 1);
-                rd_flag(status, RD_DEV_BAD_INDEX);
+        for (int j0 = want[r] + me % lanes; j0 < h; j0 += lanes * kAtOnce) {
+            int page[kAtOnce], held[kAtOnce];
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) page[e] = j0 + e * lanes < h ? __ldcg(row + j0 + e * lanes) : -1;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e)
+                held[e] = page[e] >= 0 && page[e] < num_pages ? atomicSub(refs + page[e], 1) : 0;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+                if (j0 + e * lanes >= h) continue;
+                row[j0 + e * lanes] = -1;
+                if (held[e] <= 0) {
+                    rd_flag(status, RD_DEV_BAD_INDEX);
+                    // held by nobody: leave it free
+                    if (page[e] >= 0 && page[e] < num_pages) atomicAdd(refs + page[e], 1);
+                }
             }
         }
     }
@@ -197,15 +205,23 @@ resize_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, in
         if (h < 0) continue;
         const bool fits = off[r + 1] == off[r] || off[r + 1] <= n_free;
         if (!fits) rd_flag(status, RD_DEV_OVERFLOW);
-        else row_pages[r] = wanted(r, h);
+        else row_pages[r] = want[r];
     }
 }
 
-// Rows branch: tables here, the last pages' data by the copy kernel behind it.
+// Rows branch: tables here, the last pages' data by the copy kernel behind it, or
+// here too when it is little (`here.pool` not null): up to 2 MB, eight SMs take no
+// longer than a second launch does to begin, and no list has to pass between them.
+constexpr size_t kForkHereBytes = 2u << 20;
+struct ForkCopy {
+    uint4* pool[2];                        // K, V
+    int layers;
+    size_t layer_vecs, page_vecs, row_bytes;
+};
 __global__ void __launch_bounds__(kTableThreads, 1)
 fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int32_t* refs, int num_pages,
             int32_t* ctx_lens, const int32_t* __restrict__ parent, const int32_t* __restrict__ child, int n,
-            int page_size, int32_t* src, int32_t* dst, int32_t* used, int32_t* status)
+            int page_size, int32_t* src, int32_t* dst, int32_t* used, const ForkCopy here, int32_t* status)
 {
     extern __shared__ int dyn[];
     int* off = dyn;                        // [n + 1] new pages of the pairs before
@@ -246,7 +262,7 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
         len[i] = l;
         return l >= 0 && l % page_size != 0 ? 1 : 0;
     });
-    if (rank == 0)
+    if (rank == 0 && dst != nullptr)
         for (int i = tid; i < n; i += kTableThreads) dst[i] = -1;
     // every CTA has read the tables before any is changed
     cl.sync();
@@ -263,6 +279,7 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
             rd_flag(status, RD_DEV_BAD_INDEX);                  // nothing to copy
             return;
         }
+        if (dst == nullptr) return;
         src[i] = from;
         dst[i] = page;
         used[i] = len[i] % page_size;
@@ -284,6 +301,35 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
         if (lane == 0) {
             row_pages[to] = full + (off[i + 1] - off[i]);
             ctx_lens[to] = l;
+        }
+    }
+    if (here.pool[0] == nullptr) return;
+    cl.sync();                             // every new entry is written
+    // one block of a page (K or V, one layer) per group of warps
+    const int blocks = n * 2 * here.layers;
+    const int share = max(1, kTableCtas * kTableWarps / blocks);       // warps of a block
+    for (int q = warp; q < blocks * share; q += kTableCtas * kTableWarps) {
+        const int blk = q / share, i = blk / (2 * here.layers), kl = blk % (2 * here.layers);
+        const int l = len[i];
+        if (l < 0 || l % page_size == 0 || off[i] >= n_free) continue;
+        const int full = l / page_size;
+        const int from = __ldcg(block_table + (size_t)__ldg(parent + i) * max_pages + full);
+        const int to = __ldcg(block_table + (size_t)__ldg(child + i) * max_pages + full);
+        if (from < 0 || from >= num_pages) continue;
+        uint4* base = here.pool[kl & 1] + (size_t)(kl >> 1) * here.layer_vecs;
+        const uint4* s = base + (size_t)from * here.page_vecs;
+        uint4* d = base + (size_t)to * here.page_vecs;
+        const size_t vecs = min(here.page_vecs, ((size_t)(l % page_size) * here.row_bytes + 15) / 16);
+        constexpr int kAtOnce = 4;
+        const size_t step = (size_t)share * 32;
+        for (size_t v = (size_t)(q % share) * 32 + lane; v < vecs; v += step * kAtOnce) {
+            uint4 x[kAtOnce];
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e)
+                if (v + e * step < vecs) x[e] = __ldcg(s + v + e * step);
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e)
+                if (v + e * step < vecs) d[v + e * step] = x[e];
         }
     }
 }
@@ -348,6 +394,21 @@ compact_plan_kernel(int32_t* refs, int num_pages, int32_t* remap, int32_t* n_liv
 // its source.  Every thread compares its pair with the list, staged through
 // shared memory.
 constexpr int kResolveThreads = 256;
+__device__ __forceinline__ int2 pair_at(const int32_t* src, const int32_t* dst, int k, int n, int num_pages)
+{
+    int2 v = make_int2(-1, -1);            // copies nothing
+    if (k < n) {
+        v = make_int2(__ldg(src + k), __ldg(dst + k));
+        if (v.x < 0 || v.x >= num_pages || v.y < 0 || v.y >= num_pages || v.x == v.y) v = make_int2(-1, -1);
+    }
+    return v;
+}
+// whether a pair that copies nothing is wrong
+__device__ __forceinline__ bool pair_wrong(const int32_t* src, const int32_t* dst, int k, int num_pages)
+{
+    const int s = __ldg(src + k), d = __ldg(dst + k);
+    return s >= num_pages || (s >= 0 && s != d);
+}
 __global__ void __launch_bounds__(kResolveThreads)
 resolve_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, int num_pages,
                int32_t* src_out, int32_t* dst_out, int32_t* status)
@@ -355,39 +416,33 @@ resolve_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
     __shared__ int2 tile[kResolveThreads];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int i = blockIdx.x * kResolveThreads + threadIdx.x;
-    auto load = [&](int k) {               // (-1, -1): copies nothing
-        int2 v = make_int2(-1, -1);
-        if (k < n) {
-            v = make_int2(__ldg(src + k), __ldg(dst + k));
-            if (v.x < 0 || v.x >= num_pages || v.y < 0 || v.y >= num_pages || v.x == v.y) v = make_int2(-1, -1);
-        }
-        return v;
-    };
-    int2 mine = load(i);
+    int2 mine = pair_at(src, dst, i, n, num_pages);
     bool clash = false;
     for (int k0 = 0; k0 < n; k0 += kResolveThreads) {
         __syncthreads();
-        tile[threadIdx.x] = load(k0 + threadIdx.x);
+        tile[threadIdx.x] = pair_at(src, dst, k0 + threadIdx.x, n, num_pages);
         __syncthreads();
         const int m = min(kResolveThreads, n - k0);
+#pragma unroll 8
         for (int k = 0; k < m; ++k) {
-            const int d = tile[k].y;
-            clash = clash || (d >= 0 && (d == mine.x || (d == mine.y && k0 + k < i)));
+            const int d = tile[k].y;       // (a pair of no effect has d = -1, and so have its x and y)
+            clash |= (d == mine.x) | ((d == mine.y) & (k0 + k < i));
         }
     }
     if (i >= n) return;
     if (mine.y < 0) {
-        const int s = __ldg(src + i), d = __ldg(dst + i);
-        if (s >= num_pages || (s >= 0 && s != d)) rd_flag(status, RD_DEV_BAD_INDEX);
+        if (pair_wrong(src, dst, i, num_pages)) rd_flag(status, RD_DEV_BAD_INDEX);
     } else if (clash) {
         rd_flag(status, RD_DEV_BAD_INDEX);
         mine.y = -1;
     }
+    if (clash) mine.y = -1;                // (also a pair that copies nothing)
     src_out[i] = mine.x;
     dst_out[i] = mine.y;
 }
 
-constexpr int kCopyThreads = 128;          // thread 0 copies; the others rewrite tables (compaction)
+constexpr int kCopyThreads = 128;          // warp 0 copies; the others rewrite tables (compaction)
+constexpr int kFewPairs = 256;             // pairs that each CTA resolves by itself
 constexpr int kCopyStages = 6;
 constexpr int kCopyPiece = 16384;          // bytes of a piece at most
 constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
@@ -402,6 +457,7 @@ struct CopyArgs {
     const int32_t* used;                   // positions of the page to copy (null: the whole page)
     const int32_t* count;                  // pairs, on the device (null: n)
     int n;
+    bool few;                              // src and dst as the caller gave them, at most kFewPairs
     // compaction: the tables that name the pages
     int32_t* block_table;
     const int32_t* row_pages;
@@ -434,75 +490,135 @@ copy_pages_kernel(const CopyArgs a)
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the pairs (and tables) are written
 
-    if (tid == 0) {
+    __shared__ int2 pairs[kFewPairs];
+    if (a.few) {
+        // few pairs: every CTA finds out by itself which may be copied
+        for (int i = tid; i < a.n; i += kCopyThreads) pairs[i] = pair_at(a.src, a.dst, i, a.n, a.num_pages);
+        __syncthreads();
+        bool clash[kFewPairs / kCopyThreads];
+#pragma unroll
+        for (int q = 0; q < kFewPairs / kCopyThreads; ++q) {
+            const int i = tid + q * kCopyThreads;
+            clash[q] = false;
+            if (i >= a.n) continue;
+            const int2 mine = pairs[i];
+#pragma unroll 8
+            for (int k = 0; k < a.n; ++k) clash[q] |= (pairs[k].y == mine.x) | ((pairs[k].y == mine.y) & (k < i));
+            if (blockIdx.x == 0 && (mine.y < 0 ? pair_wrong(a.src, a.dst, i, a.num_pages) : clash[q]))
+                rd_flag(a.status, RD_DEV_BAD_INDEX);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kFewPairs / kCopyThreads; ++q)
+            if (clash[q]) pairs[tid + q * kCopyThreads].y = -1;
+        __syncthreads();
+    }
+    if (tid < 32) {
+        const int lane = tid;
         const int n = a.count != nullptr ? __ldcg(a.count) : a.n;
         const long long total = (long long)n * 2 * a.layers * a.pieces;
         volatile int no_abort = 0;
-        long long next = blockIdx.x;
-        // the next piece to copy from `next` on; false: no more
-        struct Piece { unsigned char* to; const unsigned char* from; uint32_t bytes; };
-        auto take = [&](Piece& pc) -> bool {
-            for (; next < total; next += gridDim.x) {
-                const int k = (int)(next % a.pieces);
-                const long long t = next / a.pieces;
-                const int kl = (int)(t % (2 * a.layers)), i = (int)(t / (2 * a.layers));
-                const int s = __ldcg(a.src + i), d = __ldcg(a.dst + i);
-                if (d < 0) continue;
-                size_t bytes = a.page_bytes;
-                if (a.used != nullptr) bytes = min(bytes, ((size_t)__ldcg(a.used + i) * a.row_bytes + 15) & ~size_t(15));
-                const size_t o = (size_t)k * a.piece;
-                if (o >= bytes) continue;
-                unsigned char* base = a.pool[kl & 1] + (size_t)(kl >> 1) * a.layer_bytes + o;
-                pc.from = base + (size_t)s * a.page_bytes;
-                pc.to = base + (size_t)d * a.page_bytes;
-                pc.bytes = (uint32_t)min((size_t)a.piece, bytes - o);
-                next += gridDim.x;
-                return true;
-            }
-            return false;
+        // The warp works out 32 pieces at a time, a lane each, with the pairs of the 32
+        // behind them already on their way; lane 0 copies them in turn
+        long long batch = blockIdx.x;                     // first piece of the batch after the one looked up
+        bool looked_up = false;
+        int at_page = 0, at_pool = 0, src = 0, dst = -1, used = 0;
+        auto look_up = [&]() {
+            looked_up = batch < total;
+            const long long piece = batch + (long long)lane * gridDim.x;
+            batch += 32ll * gridDim.x;
+            dst = -1;
+            if (piece >= total) return;
+            const long long t = piece / a.pieces;
+            at_page = (int)(piece - t * a.pieces);
+            const int i = (int)(t / (2 * a.layers));
+            at_pool = (int)(t - (long long)i * 2 * a.layers);
+            src = a.few ? pairs[i].x : __ldcg(a.src + i);
+            dst = a.few ? pairs[i].y : __ldcg(a.dst + i);
+            if (a.used != nullptr) used = __ldcg(a.used + i);
         };
-        Piece held[kCopyStages];
+        look_up();
+        unsigned left = 0u;                               // pieces of the present batch still to copy
+        const unsigned char* my_from = nullptr;
+        unsigned char* my_to = nullptr;
+        uint32_t my_bytes = 0u;
+        struct Piece { unsigned char* to; const unsigned char* from; uint32_t bytes; };
+        auto take = [&](Piece& pc) -> bool {              // the next piece to copy; false: no more
+            while (left == 0u) {
+                if (!looked_up) return false;
+                size_t bytes = a.page_bytes;
+                if (a.used != nullptr) bytes = min(bytes, ((size_t)max(used, 0) * a.row_bytes + 15) & ~size_t(15));
+                const size_t o = (size_t)at_page * a.piece;
+                my_bytes = 0u;
+                if (dst >= 0 && o < bytes) {
+                    unsigned char* base = a.pool[at_pool & 1] + (size_t)(at_pool >> 1) * a.layer_bytes + o;
+                    my_from = base + (size_t)src * a.page_bytes;
+                    my_to = base + (size_t)dst * a.page_bytes;
+                    my_bytes = (uint32_t)min((size_t)a.piece, bytes - o);
+                }
+                left = __ballot_sync(0xffffffffu, my_bytes > 0u);
+                look_up();
+            }
+            const int from = __ffs((int)left) - 1;
+            left &= left - 1u;
+            pc.from = reinterpret_cast<const unsigned char*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(my_from), from));
+            pc.to = reinterpret_cast<unsigned char*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(my_to), from));
+            pc.bytes = __shfl_sync(0xffffffffu, my_bytes, from);
+            return true;
+        };
+        unsigned char* to[kCopyStages] = {};
+        uint32_t len[kCopyStages] = {};
+        Piece next = {};
+        bool more = take(next);                           // always one piece ahead
         uint32_t issued = 0, done = 0;
-        bool more = true;
+        auto load = [&](int st) {                         // the piece ahead into stage st
+            to[st] = next.to;
+            len[st] = next.bytes;
+            if (lane == 0) {
+                rdtc::mbar_arrive_expect_tx(&full[st], next.bytes);
+                bulk_load(ring + (size_t)st * a.piece, next.from, next.bytes, &full[st]);
+            }
+            __syncwarp();
+            ++issued;
+            more = take(next);
+        };
         // stage st takes piece number st, st + kCopyStages, ...
 #pragma unroll
-        for (int st = 0; st < kCopyStages; ++st) {
-            if (more && (more = take(held[st]))) {
-                rdtc::mbar_arrive_expect_tx(&full[st], held[st].bytes);
-                bulk_load(ring + (size_t)st * a.piece, held[st].from, held[st].bytes, &full[st]);
-                ++issued;
-            }
-        }
+        for (int st = 0; st < kCopyStages; ++st)
+            if (more) load(st);
         bool ok = true;
         while (ok && done < issued) {
 #pragma unroll
             for (int st = 0; st < kCopyStages; ++st) {
                 if (done >= issued) break;
                 const uint32_t round = done / kCopyStages;
-                if (!rdtc::mbar_wait(&full[st], round & 1, &no_abort, kWaitBudget)) { ok = false; break; }
-                bulk_store(held[st].to, ring + (size_t)st * a.piece, held[st].bytes);
-                rdtc::tma_store_commit();
-                ++done;
-                // refill the stage before this one: its store, the last but one, has
-                // read it once at most one store is still reading
-                if (done >= 2 && more) {
-                    const int ps = (st + kCopyStages - 1) % kCopyStages;
-                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    if ((more = take(held[ps]))) {
-                        rdtc::mbar_arrive_expect_tx(&full[ps], held[ps].bytes);
-                        bulk_load(ring + (size_t)ps * a.piece, held[ps].from, held[ps].bytes, &full[ps]);
-                        ++issued;
+                uint32_t landed = 1u;
+                if (lane == 0) {
+                    landed = rdtc::mbar_wait(&full[st], round & 1, &no_abort, kWaitBudget);
+                    if (landed) {
+                        bulk_store(to[st], ring + (size_t)st * a.piece, len[st]);
+                        rdtc::tma_store_commit();
+                        // refill the stage before this one: its store, the last but one,
+                        // has read it once at most one store is still reading
+                        if (done >= 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                     }
                 }
+                ok = __shfl_sync(0xffffffffu, landed, 0) != 0u;
+                if (!ok) break;
+                ++done;
+                constexpr int before[kCopyStages] = {kCopyStages - 1, 0, 1, 2, 3, 4};
+                if (done >= 2 && more) load(before[st]);
             }
         }
         if (!ok) {
-            rd_flag(a.status, RD_DEV_TIMEOUT);
+            if (lane == 0) rd_flag(a.status, RD_DEV_TIMEOUT);
             // the loads in flight must land before the CTA may exit
             for (uint32_t k = done; k < issued; ++k)
                 rdtc::mbar_wait(&full[k % kCopyStages], (k / kCopyStages) & 1, &no_abort, kWaitBudget);
         }
-        rdtc::tma_store_wait_all();
+        if (lane == 0) rdtc::tma_store_wait_all();
     } else if (a.remap != nullptr && tid >= 32) {
         // table entries through the map, one row per three warps' turn
         for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
@@ -587,9 +703,14 @@ cudaError_t rd_launch_resize_pages(int32_t* block_table, int R, int max_pages, i
                                    int32_t* page_refs, int num_pages, const int32_t* new_lens, int page_size,
                                    int32_t* dev_status, cudaStream_t stream)
 {
-    const size_t smem = (size_t)(2 * R + 1) * sizeof(int);
+    const size_t smem = (size_t)(3 * R + 1) * sizeof(int);
     return launch_table(resize_kernel, smem, stream, block_table, R, max_pages, row_pages, page_refs, num_pages,
                         new_lens, page_size, dev_status);
+}
+
+bool rd_fork_copies_itself(int n, int layers, size_t page_bytes)
+{
+    return (double)n * 2 * layers * (double)page_bytes <= (double)kForkHereBytes;
 }
 
 cudaError_t rd_launch_fork_pages(const rd_page_pools& pools, int page_size, int32_t* block_table, int R,
@@ -597,13 +718,23 @@ cudaError_t rd_launch_fork_pages(const rd_page_pools& pools, int page_size, int3
                                  const int32_t* parent, const int32_t* child, int n, void* workspace,
                                  int32_t* dev_status, cudaStream_t stream)
 {
-    int32_t* src = static_cast<int32_t*>(workspace);
-    int32_t* dst = src + n;
-    int32_t* used = dst + n;
+    const bool here = rd_fork_copies_itself(n, pools.layers, pools.page_bytes);
+    int32_t* src = here ? nullptr : static_cast<int32_t*>(workspace);
+    int32_t* dst = here ? nullptr : src + n;
+    int32_t* used = here ? nullptr : dst + n;
+    ForkCopy fc = {};
+    if (here) {
+        fc.pool[0] = static_cast<uint4*>(pools.k_pool);
+        fc.pool[1] = static_cast<uint4*>(pools.v_pool);
+        fc.layers = pools.layers;
+        fc.page_vecs = pools.page_bytes / 16;
+        fc.layer_vecs = fc.page_vecs * (size_t)pools.num_pages;
+        fc.row_bytes = pools.page_bytes / page_size;
+    }
     const size_t smem = (size_t)(2 * n + 1 + R) * sizeof(int);
     cudaError_t e = launch_table(fork_kernel, smem, stream, block_table, R, max_pages, row_pages, page_refs,
-                                 pools.num_pages, ctx_lens, parent, child, n, page_size, src, dst, used, dev_status);
-    if (e != cudaSuccess) return e;
+                                 pools.num_pages, ctx_lens, parent, child, n, page_size, src, dst, used, fc, dev_status);
+    if (e != cudaSuccess || here) return e;
     CopyArgs a = copy_args(pools, dev_status);
     a.row_bytes = pools.page_bytes / page_size;
     a.src = src;
@@ -613,19 +744,27 @@ cudaError_t rd_launch_fork_pages(const rd_page_pools& pools, int page_size, int3
     return launch_copy(a, n, stream);
 }
 
+// comparing every pair with every other in each CTA takes a microsecond at 256
+bool rd_copy_resolves_itself(int n) { return n <= kFewPairs; }
+
 cudaError_t rd_launch_copy_pages(const rd_page_pools& pools, const int32_t* src, const int32_t* dst, int n,
                                  void* workspace, int32_t* dev_status, cudaStream_t stream)
 {
-    int32_t* rs = static_cast<int32_t*>(workspace);
-    int32_t* rt = rs + n;
-    resolve_kernel<<<(n + kResolveThreads - 1) / kResolveThreads, kResolveThreads, 0, stream>>>(
-        src, dst, n, pools.num_pages, rs, rt, dev_status);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
     CopyArgs a = copy_args(pools, dev_status);
-    a.src = rs;
-    a.dst = rt;
+    a.src = src;
+    a.dst = dst;
     a.n = n;
+    a.few = rd_copy_resolves_itself(n);
+    if (!a.few) {
+        int32_t* rs = static_cast<int32_t*>(workspace);
+        int32_t* rt = rs + n;
+        resolve_kernel<<<(n + kResolveThreads - 1) / kResolveThreads, kResolveThreads, 0, stream>>>(
+            src, dst, n, pools.num_pages, rs, rt, dev_status);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        a.src = rs;
+        a.dst = rt;
+    }
     return launch_copy(a, n, stream);
 }
 

@@ -228,8 +228,8 @@ rd_status rd_tree_attention_shared(int B, int P_max, int Hq, int Hkv, int D, flo
     if (page_size % 64 != 0) return RD_ERR_UNSUPPORTED;
     if (P_max > RD_MAX_PACKED || B > 65535 || Hkv > 65535 || n_groups > 65535) return RD_ERR_UNSUPPORTED;
     if ((long long)num_pages * page_size > 0x7fffffffLL) return RD_ERR_UNSUPPORTED;
-    /* the prefix's chunks of 128 positions x 256 rows, counted in 32 bits */
-    if (((long long)B * P_max * (Hq / Hkv) / 256 + n_groups) * Hkv * (max_ctx / 128 + 1LL) > 0x7fffffffLL)
+    /* the prefix's chunks of 128 positions x 256 rows, in eighths, counted in 32 bits */
+    if (((long long)B * P_max * (Hq / Hkv) / 256 + n_groups) * Hkv * (max_ctx / 128 + 4LL) * 8 > 0x7fffffffLL)
         return RD_ERR_UNSUPPORTED;
     if (mask_words != (P_max + 31) / 32) return RD_ERR_INVALID_ARG;
     if (!q || !k_new || !v_new || !k_pool || !v_pool || !block_table || !ctx_lens || !group_offsets ||
@@ -413,7 +413,11 @@ rd_status rd_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* r
                                             new_lens, page_size, dev_status, (cudaStream_t)stream));
 }
 
-size_t rd_fork_pages_workspace_size(int n) { return n > 0 ? (size_t)n * 3 * sizeof(int32_t) : 0; }
+size_t rd_fork_pages_workspace_size(int n, int layers, size_t page_bytes)
+{
+    if (n <= 0 || layers < 1 || rd_fork_copies_itself(n, layers, page_bytes)) return 0;
+    return (size_t)n * 3 * sizeof(int32_t);
+}
 
 rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
                         int page_size, int32_t* block_table, int R, int max_pages, int32_t* row_pages,
@@ -429,9 +433,10 @@ rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, s
     if (n > RD_MAX_ROWS) return RD_ERR_UNSUPPORTED;
     if (n == 0 || R == 0) return RD_OK;
     if ((num_pages > 0 && (!k_pool || !v_pool || !page_refs)) || (max_pages > 0 && !block_table) ||
-        !row_pages || !ctx_lens || !parent || !child || !workspace)
+        !row_pages || !ctx_lens || !parent || !child)
         return RD_ERR_INVALID_ARG;
-    if (ws_bytes < rd_fork_pages_workspace_size(n) || reinterpret_cast<uintptr_t>(workspace) % 4 != 0)
+    const size_t need = rd_fork_pages_workspace_size(n, layers, page_bytes);
+    if (need > 0 && (!workspace || ws_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 4 != 0))
         return RD_ERR_INVALID_ARG;
     const rd_page_pools pools = {k_pool, v_pool, layers, num_pages, page_bytes};
     return from_cuda(rd_launch_fork_pages(pools, page_size, block_table, R, max_pages, row_pages, page_refs,
@@ -439,7 +444,10 @@ rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, s
                                           (cudaStream_t)stream));
 }
 
-size_t rd_copy_pages_workspace_size(int n) { return n > 0 ? (size_t)n * 2 * sizeof(int32_t) : 0; }
+size_t rd_copy_pages_workspace_size(int n)
+{
+    return n <= 0 || rd_copy_resolves_itself(n) ? 0 : (size_t)n * 2 * sizeof(int32_t);
+}
 
 rd_status rd_copy_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,
                         const int32_t* src, const int32_t* dst, int n, void* workspace, size_t ws_bytes,
@@ -450,8 +458,9 @@ rd_status rd_copy_pages(void* k_pool, void* v_pool, int layers, int num_pages, s
     if (st != RD_OK) return st;
     if (n > RD_MAX_PAGES) return RD_ERR_UNSUPPORTED;
     if (n == 0) return RD_OK;
-    if ((num_pages > 0 && (!k_pool || !v_pool)) || !src || !dst || !workspace) return RD_ERR_INVALID_ARG;
-    if (ws_bytes < rd_copy_pages_workspace_size(n) || reinterpret_cast<uintptr_t>(workspace) % 4 != 0)
+    if ((num_pages > 0 && (!k_pool || !v_pool)) || !src || !dst) return RD_ERR_INVALID_ARG;
+    const size_t need = rd_copy_pages_workspace_size(n);
+    if (need > 0 && (!workspace || ws_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 4 != 0))
         return RD_ERR_INVALID_ARG;
     const rd_page_pools pools = {k_pool, v_pool, layers, num_pages, page_bytes};
     return from_cuda(rd_launch_copy_pages(pools, src, dst, n, workspace, dev_status, (cudaStream_t)stream));

@@ -131,6 +131,9 @@ struct rd_page_pools {
     int layers, num_pages;
     size_t page_bytes;
 };
+// small calls need no workspace
+bool rd_fork_copies_itself(int n, int layers, size_t page_bytes);
+bool rd_copy_resolves_itself(int n);
 cudaError_t rd_launch_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* row_pages,
                                    int32_t* page_refs, int num_pages, const int32_t* new_lens, int page_size,
                                    int32_t* dev_status, cudaStream_t stream);

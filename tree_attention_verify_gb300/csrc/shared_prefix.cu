@@ -23,15 +23,20 @@
 // chunks form one sequence that the CTAs take in equal ranges, so that one group
 // with few rows still fills the GPU; a unit cut by a range boundary leaves its
 // pieces to the merge.
-// Warp roles (384 threads):
-//   warps 0-3, 4-7  softmax of tile A, of tile B: row r is TMEM lane r.  S from
-//              TMEM, online softmax in exp2 form (O rescaled only when a row
-//              maximum grows by more than 2^8), bf16 P written over S.
-//   warp 8     producer: K_0, V_0, K_1, V_1, ... by TMA into one ring
-//   warp 9     MMA issuer: per chunk j and tile t, O_t += P_t V_j, then S_t of
+// Warp roles (640 threads):
+//   warps 0-15  softmax: a warpgroup for each half (64 positions) of each tile's
+//              chunk; row r is TMEM lane r of both.  S from TMEM, online softmax in
+//              exp2 form, bf16 P written over S.  A row's two threads share its
+//              running maximum, and only a chunk in which some row's grows by more
+//              than 2^8 makes them exchange it and rescale O; one reducing barrier
+//              a chunk tells.  (One warpgroup a tile had the tensor core wait: its
+//              1,900 cycles a chunk and the 768 of the products behind it come one
+//              after the other.)
+//   warp 16    producer: K_0, V_0, K_1, V_1, ... by TMA into one ring
+//   warp 17    MMA issuer: per chunk j and tile t, O_t += P_t V_j, then S_t of
 //              chunk j + 1, so that the tensor core works on one tile while the
 //              other's softmax runs
-//   warps 10-11  the unit's query rows into shared memory (cp.async, row list),
+//   warps 18-19  the unit's query rows into shared memory (cp.async, row list),
 //              then the check that a group's tables name the same pages
 // Every wait is bounded by a clock budget; on expiry the CTA records
 // RD_DEV_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
@@ -54,21 +59,37 @@ using namespace rdshared;
 constexpr int kM = 128;                    // rows per tile = TMEM lanes
 static_assert(kUnitRows == 2 * kM, "two tiles");
 constexpr int kN = 128;                    // KV positions per chunk (two TMA boxes)
-constexpr int kThreads = 384;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kQWarp0 = 10;                // two query warps
-// Register split: 384 threads launch with 168 registers each (64,512); the two
-// softmax warpgroups take 200 (a row's 128 scores stay in registers), the third
-// keeps 104: 128 x (200 + 200 + 104) = 64,512, per sub-partition 32 x 504.
-constexpr int kRegsLaunch = 168;
-constexpr int kRegsSoftmax = 200;
-constexpr int kRegsOther = 104;
-static_assert(128 * (2 * kRegsSoftmax + kRegsOther) <= kThreads * kRegsLaunch, "register split");
-static_assert(32 * (2 * kRegsSoftmax + kRegsOther) <= 16384, "register split per sub-partition");
-constexpr uint32_t kMinChunks = 2;         // chunks per CTA at least
+constexpr int kSoftmaxWarps = 16;          // four warpgroups: (tile, half)
+constexpr int kThreads = kSoftmaxWarps * 32 + 128;
+constexpr int kProducerWarp = 16;
+constexpr int kMmaWarp = 17;
+constexpr int kQWarp0 = 18;                // two query warps
+// 640 threads leave 96 registers each: the softmax warps read their scores twice,
+// 32 at a time, rather than hold half a row (64) over the barrier between.
+// Division over the CTAs, in eighths of a chunk of two tiles.  A chunk of one tile (a
+// unit of at most 128 rows) takes five; beginning a unit (its queries, the first
+// scores, the last sums) takes a CTA as long as three chunks.  At 320 units on 152
+// CTAs, equal numbers of chunks left the slowest CTA 22% behind the fastest.
+constexpr uint32_t kTwoTiles = 8;
+constexpr uint32_t kOneTile = 5;
+constexpr uint32_t kUnitStart = 24;
+constexpr uint32_t kMinRange = 2 * kTwoTiles;   // a CTA's share at least
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
+
+// What the units of one kv head of a group count in the division.
+struct UnitCost {
+    uint32_t n;               // chunks of a unit
+    uint32_t full, head;      // a unit of two tiles, all units of a kv head
+    uint32_t last;            // weight of a chunk of the last unit
+    __device__ __forceinline__ UnitCost(const Group& g, int G)
+    {
+        n = (uint32_t)(g.positions + kN - 1) / kN;
+        full = kUnitStart + kTwoTiles * n;
+        last = g.nodes * G - (g.pairs - 1) * kUnitRows <= kM ? kOneTile : kTwoTiles;
+        head = (uint32_t)(g.pairs - 1) * full + kUnitStart + last * n;
+    }
+};
 
 // ------------------------------------------------------------------------ plan
 struct PlanArgs {
@@ -196,7 +217,7 @@ plan_kernel(const PlanArgs a)
             grp.positions = max(0, pg) * a.page_size;
             grp.pairs = (grp.nodes * a.G + kUnitRows - 1) / kUnitRows;
             units = a.Hkv * grp.pairs;
-            w = units * ((grp.positions + kN - 1) / kN);
+            w = grp.positions > 0 && grp.nodes > 0 ? a.Hkv * (int)UnitCost(grp, a.G).head : 0;
         }
         int total, total_units;
         const int at = cta_scan(w, warp_sum, total);
@@ -209,7 +230,10 @@ plan_kernel(const PlanArgs a)
         chunks += total;
         all_units += total_units;
     }
-    if (tid == 0) a.p.first[a.n_groups] = chunks;
+    if (tid == 0) {
+        a.p.first[a.n_groups] = chunks;
+        *a.p.suf_next = 0;
+    }
     __syncthreads();
     for (int b = tid; b < a.B; b += kScanThreads) {
         const int g = kSmall ? my_gid : a.p.gid[b];
@@ -231,9 +255,11 @@ template <int D> struct Cfg {
     static constexpr int kQBytes = kM * D * 2;          // one tile's queries
     static constexpr int kQOff = kStages * kStageBytes;
     static constexpr int kBarOff = kQOff + 2 * kQBytes;
-    static constexpr int kSmemBytes = kBarOff + 512 + 1024;   // + barriers + alignment slack
+    static constexpr int kShareOff = kBarOff + 512;           // a float per row: what a row's two threads exchange
+    static constexpr int kSmemBytes = kShareOff + 1024 + 1024;   // + alignment slack
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-    // TMEM (512 columns): S of tile t (P over its first half), O of tile t
+    // TMEM (512 columns): S of tile t (P of each half of the positions over the first
+    // half of its scores), O of tile t
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t s_col(int t) { return 128u * t; }
     __host__ __device__ static constexpr uint32_t o_col(int t) { return 256u + 128u * t; }
@@ -255,8 +281,7 @@ struct Bar {
     uint64_t q_full;          // the unit's query tiles are in shared memory
     uint64_t q_free;          // every S MMA of the unit has completed
     uint64_t s_full[2];       // S of the tile's chunk is in TMEM (and PV of the one before is done)
-    uint64_t p_half[2];       // P of the chunk's first 64 positions is written (four softmax warps)
-    uint64_t p_full[2];       // ... of all of them
+    uint64_t p_full[2];       // P of the tile's chunk is written (eight softmax warps)
     uint64_t o_final[2];      // the tile's last PV of the unit has completed
     uint64_t o_free[2];       // the tile's epilogue has read O
     uint64_t drain;
@@ -273,49 +298,59 @@ struct Piece {
     int c0, n;                // chunks [c0, c0 + n)
     int slot;                 // piece slot, -1: a whole unit
     int unit;
-    uint32_t last;            // the unit's last chunk in the sequence
+    uint32_t last;            // where the unit's last chunk begins in the sequence
     Group g;
 };
 
-// This CTA's range of the chunk sequence, in pieces.
+// This CTA's range of the sequence, in pieces.  A unit is its start, then its
+// chunks; a chunk belongs to the CTA whose range holds its first eighth.
 struct Walk {
-    uint32_t x, end, start;
+    uint32_t x, end;
+    bool first;               // no piece yet
     __device__ __forceinline__ void begin(const PrefixArgs& a)
     {
         const uint32_t W = a.p.first[a.n_groups];
-        x = end = start = 0u;
+        x = end = 0u;
+        first = true;
         if (W == 0u) return;
-        const uint32_t n = range_ctas(W, gridDim.x, kMinChunks);
+        const uint32_t n = range_ctas(W, gridDim.x, kMinRange);
         if (blockIdx.x >= n) return;
-        x = start = range_start(W, n, blockIdx.x);
+        x = range_start(W, n, blockIdx.x);
         end = range_start(W, n, blockIdx.x + 1);
     }
     __device__ __forceinline__ bool next(const PrefixArgs& a, Piece& u)
     {
-        if (x >= end) return false;
-        int lo = 0, hi = a.n_groups - 1;                    // last group with first <= x
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.p.first[mid] <= x) lo = mid; else hi = mid - 1;
+        while (x < end) {
+            int lo = 0, hi = a.n_groups - 1;                // last group with first <= x
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (a.p.first[mid] <= x) lo = mid; else hi = mid - 1;
+            }
+            u.g = a.p.group[lo];
+            const UnitCost cost(u.g, a.G);
+            const uint32_t base = a.p.first[lo];
+            const uint32_t h = (x - base) / cost.head;
+            const uint32_t pair = min((x - base - h * cost.head) / cost.full, (uint32_t)u.g.pairs - 1);
+            const uint32_t u0 = base + h * cost.head + pair * cost.full;
+            const uint32_t w = pair + 1 == (uint32_t)u.g.pairs ? cost.last : kTwoTiles;
+            const uint32_t at = u0 + kUnitStart;            // its first chunk
+            const uint32_t stop = min(at + w * cost.n, end);
+            const uint32_t c0 = x > at ? (x - at + w - 1) / w : 0u;
+            const uint32_t c1 = stop > at ? (stop - at + w - 1) / w : 0u;
+            x = stop;
+            if (c1 <= c0) continue;                         // no chunk's first eighth
+            u.h = (int)h;
+            u.row0 = (int)pair * kUnitRows;
+            u.rows = min(kUnitRows, u.g.nodes * a.G - u.row0);
+            u.c0 = (int)c0;
+            u.n = (int)(c1 - c0);
+            u.slot = c1 - c0 == cost.n ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
+            u.unit = u.g.unit0 + (int)(h * u.g.pairs + pair);
+            u.last = at + w * (cost.n - 1);
+            first = false;
+            return true;
         }
-        u.g = a.p.group[lo];
-        const uint32_t base = a.p.first[lo];
-        const uint32_t n = (uint32_t)(u.g.positions + kN - 1) / kN;
-        const int all = u.g.nodes * a.G;
-        const uint32_t pairs = (uint32_t)u.g.pairs;
-        const uint32_t unit = (x - base) / n;
-        const uint32_t u0 = base + unit * n;
-        u.h = (int)(unit / pairs);
-        u.row0 = (int)(unit % pairs) * kUnitRows;
-        u.rows = min(kUnitRows, all - u.row0);
-        u.c0 = (int)(x - u0);
-        const uint32_t stop = min(u0 + n, end);
-        u.n = (int)(stop - x);
-        u.slot = (uint32_t)u.n == n ? -1 : 2 * (int)blockIdx.x + (u.c0 == 0 && u0 > start ? 1 : 0);
-        u.unit = u.g.unit0 + (int)unit;
-        u.last = u0 + n - 1;
-        x = stop;
-        return true;
+        return false;
     }
 };
 
@@ -333,6 +368,16 @@ __device__ __forceinline__ bool elect_one()
 __device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// OR of a predicate over `count` threads at named barrier `id` (0 is __syncthreads)
+__device__ __forceinline__ bool barrier_or(int id, int count, bool p)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(id), "r"(count), "r"((uint32_t)p) : "memory");
+    return r != 0;
+}
 
 // two floats in one 64-bit register pair (first: low half)
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
@@ -382,10 +427,9 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
         mbar_init(&bar.q_free, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar.s_full[t], 1);
-            mbar_init(&bar.p_half[t], 4);
-            mbar_init(&bar.p_full[t], 4);
+            mbar_init(&bar.p_full[t], 8);
             mbar_init(&bar.o_final[t], 1);
-            mbar_init(&bar.o_free[t], 4);
+            mbar_init(&bar.o_free[t], 8);
         }
         mbar_init(&bar.drain, 1);
         mbar_init(&bar.never, 1);
@@ -413,8 +457,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
         rd_flag(a.status, RD_DEV_TIMEOUT);
     };
 
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp >= kSoftmaxWarps) {
     if (warp == kProducerWarp) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
@@ -425,7 +468,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
             const uint32_t W = a.p.first[a.n_groups];
             while (!*abort && w.next(a, u)) {
                 if (u.c0 == 0) {                          // the unit starts here: name its pieces
-                    const uint32_t nc = range_ctas(W, gridDim.x, kMinChunks);
+                    const uint32_t nc = range_ctas(W, gridDim.x, kMinRange);
                     const int n = u.slot < 0 ? 1 : (int)(range_of(W, nc, u.last) - blockIdx.x) + 1;
                     a.p.unit[u.unit] = make_int2(n, u.slot);
                 }
@@ -507,7 +550,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
                 unsigned char* base = smem + C::kQOff + t * C::kQBytes + (c >> 3) * (kM * 128);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-#pragma unroll 4
+#pragma unroll 2
                     for (int i = 0; i < 32; i += kRowsAtOnce) {
                         const int m = i + lane / kVecs;
                         const uint32_t row = __shfl_sync(0xffffffffu, at[k], m);
@@ -560,7 +603,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
         if (a.stall_budget > 0 && !warp_wait(&bar.never, 0, abort, a.stall_budget)) fail();
         uint32_t st = 0, ph = 0;                          // the ring's next entry, its phase
         uint32_t it = 0;                                  // units
-        uint32_t pp[2] = {0u, 0u};                        // phase of p_half and p_full
+        uint32_t pp[2] = {0u, 0u};                        // phase of p_full
         uint32_t ut[2] = {0u, 0u};                        // units with tile t so far
         auto step = [&](uint32_t& s_, uint32_t& p_) {     // take the ring's next entry
             s_ = st;
@@ -614,27 +657,18 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
                     if (t >= nb) break;
                     if (t == 0) ok = wait(&bar.kv_full[vs], vp);
                     if (j == 0 && ut[t] > 0) ok = ok && wait(&bar.o_free[t], (ut[t] - 1) & 1);
-                    // the first 64 positions' product starts while the softmax warps
-                    // work on the other half
-                    ok = ok && wait(&bar.p_half[t], pp[t]);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t vd = v_lo + vs * kStage16;
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < kN / 32; ++k)
-                            mma_tmem_a(tm + C::o_col(t), tm + C::s_col(t) + k * 8, desc64(vd + k * 128, v_hi), idPV,
-                                       j > 0 || k > 0);
-                    }
-                    __syncwarp();
-                    ok = wait(&bar.p_full[t], pp[t]);
+                    ok = ok && wait(&bar.p_full[t], pp[t]);
                     if (!ok) break;
                     pp[t] ^= 1u;
                     tc_fence_after();
-                    if (j != odd && leader) {
+                    const uint32_t vd = v_lo + vs * kStage16;
+                    if (leader) {
+                        // the weights of the second 64 positions lie 64 columns on
 #pragma unroll
-                        for (int k = kN / 32; k < kN / 16; ++k)
-                            mma_tmem_a(tm + C::o_col(t), tm + C::s_col(t) + k * 8, desc64(vd + k * 128, v_hi), idPV, true);
+                        for (int k = 0; k < kN / 16; ++k)
+                            if (k < kN / 32 || j != odd)
+                                mma_tmem_a(tm + C::o_col(t), tm + C::s_col(t) + (k >> 2) * 64 + (k & 3) * 8,
+                                           desc64(vd + k * 128, v_hi), idPV, j > 0 || k > 0);
                     }
                     __syncwarp();
                     if (t == nb - 1) commit(&bar.kv_empty[vs]);
@@ -663,17 +697,22 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
     }
     } else {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int t = warp >> 2;                          // tile
+        const int t = warp >> 3, half = (warp >> 2) & 1;  // tile, half of the chunk's positions
         const int r = tid & (kM - 1);                     // row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t sc = tmem + lane_base + C::s_col(t);
-        const uint32_t oc = tmem + lane_base + C::o_col(t);
+        const uint32_t sc = tmem + lane_base + C::s_col(t) + half * 64;     // this half's scores
+        constexpr int DH = D / 2;                         // this thread's columns of O
+        const uint32_t oc = tmem + lane_base + C::o_col(t) + half * DH;
+        float* const share = reinterpret_cast<float*>(smem + C::kShareOff) + t * kM + r;
+        // The eight warps of a tile go through the same barriers whatever happens: a
+        // wait that ran out joins the next reduction and all of them leave together.
+        auto any_of_tile = [&](bool p) { return barrier_or(1 + t, 256, p); };
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
         uint32_t ct = 0, ut = 0;
         Walk w;
         w.begin(a);
         Piece u;
-        while (!*abort && w.next(a, u)) {
+        while (w.next(a, u)) {
             const int row = t * kM + r;                   // row of the unit
             if (t == 1 && u.rows <= kM) continue;
             const bool valid = row < u.rows;
@@ -681,116 +720,115 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
             // never read
             const bool dead = __all_sync(0xffffffffu, !valid);
             float m = -INFINITY, l = 0.f;
-            // one chunk: NC = 128 positions, or the 64 of an odd last half.  Two
-            // columns an instruction where the machine has one (fma, add), and P in
-            // two halves, each handed to the issuer as soon as it is written
-            const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
-            auto chunk = [&](auto nc, bool first) {
-                constexpr int NC = decltype(nc)::value;
-                uint32_t s[NC];
-#pragma unroll
-                for (int c = 0; c < NC / 32; ++c)
-                    tmem_ld32(sc + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
-                tmem_ld_wait();
-                float mx8[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mx8[e] = __uint_as_float(s[e]);
-#pragma unroll
-                for (int c = 8; c < NC; c += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        mx8[e] = c + 8 + e < NC ? fmaxf(fmaxf(mx8[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 8 + e]))
-                                                : fmaxf(mx8[e], __uint_as_float(s[c + e]));
-                const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-                const float ms = mx * a.scale_log2;
-                const bool need = ms > m + kRescaleThreshold;
-                if (__any_sync(0xffffffffu, need) && !first) {
-                    const float alpha = need ? fast_exp2(m - ms) : 1.f;
-#pragma unroll
-                    for (int cb = 0; cb < D / 32; ++cb) {
-                        uint32_t o[32];
-                        tmem_ld32(oc + cb * 32, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                        tmem_st32(oc + cb * 32, o);
-                    }
-                }
-                if (need) {
-                    l *= fast_exp2(m - ms);               // 0 while m is -inf
-                    m = ms;
-                }
-                const float base = m == -INFINITY ? 0.f : m;
-                const uint64_t base2 = pack2(-base, -base);
-                uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                for (int h = 0; h < NC / 64; ++h) {
-                    uint32_t pv[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint64_t x = fma2(pack2(__uint_as_float(s[64 * h + 2 * e]), __uint_as_float(s[64 * h + 2 * e + 1])),
-                                                scale2, base2);
-                        float x0, x1;
-                        unpack2(x, x0, x1);
-                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                        sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
-                        pv[e] = pack_bf16(p0, p1);
-                    }
-                    tmem_st32(sc + 32 * h, pv);
-                    if (h == 0 && NC == 128) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.p_half[t]);
-                    }
-                }
-                float a0, a1;
-                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
-                l += a0 + a1;
-                tmem_st_wait();
-            };
             bool ok = true;
             for (int j = 0; j < u.n; ++j) {
-                if (!warp_wait(&bar.s_full[t], (ct + j) & 1, abort, kWaitBudget)) { ok = false; break; }
+                ok = warp_wait(&bar.s_full[t], (ct + j) & 1, abort, kWaitBudget);
                 tc_fence_after();
-                const bool all = (u.c0 + j) * kN + 64 < u.g.positions;
-                if (!dead) {
-                    if (all) chunk(std::integral_constant<int, 128>{}, j == 0);
-                    else chunk(std::integral_constant<int, 64>{}, j == 0);
+                // the odd last chunk has 64 positions: none for the second half
+                const bool mine = ok && !dead && (half == 0 || (u.c0 + j) * kN + 64 < u.g.positions);
+                uint32_t pv[32];                          // this half's weights, as bf16 pairs
+                uint64_t sum[2];
+                // Weights against the maximum so far, and the scores' own: only where
+                // that has grown too much are they worked out again, from the same
+                // scores (nothing is written before the tile has agreed)
+                auto weights = [&]() -> float {
+                    const float base = m == -INFINITY ? 0.f : m;
+                    const uint64_t base2 = pack2(-base, -base);
+                    float mx[4];
+                    sum[0] = sum[1] = 0ull;
+#pragma unroll
+                    for (int c0 = 0; c0 < 64; c0 += 16) {
+                        uint32_t s[16];
+                        tmem_ld16(sc + c0, s);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float y0 = __uint_as_float(s[2 * e]), y1 = __uint_as_float(s[2 * e + 1]);
+                            mx[e & 3] = c0 == 0 && e < 4 ? fmaxf(y0, y1) : fmaxf(fmaxf(mx[e & 3], y0), y1);
+                            float x0, x1;
+                            unpack2(fma2(pack2(y0, y1), scale2, base2), x0, x1);
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                            sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+                            pv[c0 / 2 + e] = pack_bf16(p0, p1);
+                        }
+                    }
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                };
+                float ms = -INFINITY;
+                if (mine) ms = weights();
+                if (any_of_tile(!ok || ms > m + kRescaleThreshold)) {
+                    if (any_of_tile(!ok)) { ok = false; break; }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) pv[i] = 0u;      // (nothing to keep over the exchange)
+                    if (half == 1) *share = ms;
+                    any_of_tile(false);
+                    if (half == 0) {
+                        const float top = fmaxf(ms, *share);
+                        ms = top > m + kRescaleThreshold ? top : m;
+                        *share = ms;
+                    }
+                    any_of_tile(false);
+                    if (half == 1) ms = *share;           // the row's maximum from here on
+                    const float f = ms != m ? fast_exp2(m - ms) : 1.f;    // 0 while m is -inf
+                    l *= f;
+                    m = ms;
+                    if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                        for (int cb = 0; cb < DH / 32; ++cb) {
+                            uint32_t o[32];
+                            tmem_ld32(oc + cb * 32, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                            tmem_st32(oc + cb * 32, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    if (mine) weights();
+                    // (PV adds to all columns of O: it waits for both halves' arrivals below)
+                }
+                if (mine) {
+                    tmem_st32(sc, pv);                    // over this half's scores
+                    float a0, a1;
+                    unpack2(add2(sum[0], sum[1]), a0, a1);
+                    l += a0 + a1;
+                    tmem_st_wait();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (dead || !all) mbar_arrive(&bar.p_half[t]);
-                    mbar_arrive(&bar.p_full[t]);
-                }
+                if (lane == 0) mbar_arrive(&bar.p_full[t]);
             }
-            if (!ok || !warp_wait(&bar.o_final[t], ut & 1, abort, kWaitBudget)) { fail(); break; }
+            if (ok) ok = warp_wait(&bar.o_final[t], ut & 1, abort, kWaitBudget);
+            else { fail(); break; }                       // (every warp of the tile leaves here)
+            if (half == 1) *share = l;
+            if (any_of_tile(!ok)) { fail(); break; }
             tc_fence_after();
-            uint32_t o[D / 32][32];
+            // fp32 partials, four columns of consecutive rows side by side
+            const bool whole = u.slot < 0;
+            const size_t stride = whole ? a.p.rows_cap : kUnitRows;
+            const size_t at = whole ? (size_t)u.g.node0 * a.G + u.row0 + row : (size_t)row;
+            const size_t block = whole ? u.h : u.slot;
+            float4* dst = (whole ? a.p.rows : a.p.part) + (block * (D / 4) + half * (DH / 4)) * stride + at;
 #pragma unroll
-            for (int cb = 0; cb < D / 32; ++cb) tmem_ld32(oc + cb * 32, o[cb]);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.o_free[t]);
-            if (valid) {
-                // fp32 partials, four columns of consecutive rows side by side
-                const bool whole = u.slot < 0;
-                const size_t stride = whole ? a.p.rows_cap : kUnitRows;
-                const size_t at = whole ? (size_t)u.g.node0 * a.G + u.row0 + row : (size_t)row;
-                const size_t block = whole ? u.h : u.slot;
-                float4* dst = (whole ? a.p.rows : a.p.part) + block * (D / 4) * stride + at;
-#pragma unroll
-                for (int cb = 0; cb < D / 32; ++cb)
+            for (int cb = 0; cb < DH / 32; ++cb) {
+                uint32_t o[32];
+                tmem_ld32(oc + cb * 32, o);
+                tmem_ld_wait();
+                if (cb == DH / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.o_free[t]);
+                }
+                if (valid) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         dst[(size_t)(cb * 8 + i) * stride] =
-                            make_float4(__uint_as_float(o[cb][4 * i]), __uint_as_float(o[cb][4 * i + 1]),
-                                        __uint_as_float(o[cb][4 * i + 2]), __uint_as_float(o[cb][4 * i + 3]));
-                (whole ? a.p.rows_ml : a.p.part_ml)[block * stride + at] = make_float2(m, l);
+                            make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                }
             }
+            if (valid && half == 0)
+                (whole ? a.p.rows_ml : a.p.part_ml)[block * stride + at] = make_float2(m, l + *share);
             ct += u.n;
             ++ut;
         }
@@ -940,6 +978,7 @@ cudaError_t launch_merge(dim3 grid, cudaStream_t stream, MergeArgs& a)
 // the tcgen05 kernel, whose tiles hold 128.
 struct SuffixChoice {
     bool few_rows;
+    bool by_unit;             // few_rows: CTAs take whole units off a counter
     bool table;               // units have an entry in the table of pieces
     int grid, slot_rows, tiles;
     rd_attn_plan plan;        // tcgen05
@@ -950,8 +989,9 @@ SuffixChoice choose_suffix(int B, int P_max, int Hq, int Hkv, int D, int max_ctx
     const int rows = P_max * (Hq / Hkv);
     s.few_rows = rows <= kSuffixMaxRows;
     s.plan = rd_attn_make_plan(B, P_max, Hq, Hkv, D, max_ctx);
-    s.table = s.few_rows || s.plan.stream_k;
     s.grid = s.few_rows ? rd_suffix_grid(rows) : s.plan.grid;
+    s.by_unit = s.few_rows && rd_suffix_by_unit(B, Hkv, s.grid);
+    s.table = s.few_rows ? !s.by_unit : s.plan.stream_k;
     s.slot_rows = s.few_rows ? kSuffixMaxRows : kM;
     s.tiles = s.few_rows ? 1 : s.plan.tiles;
     return s;
@@ -987,6 +1027,7 @@ size_t layout(Plan& p, void*& suffix_ws, unsigned char* base, int B, int P_max, 
     take(p.suffix.rows_ml, p.rows_cap * Hkv);
     take(p.suffix.unit, suffix.table ? (size_t)suffix.tiles * B * Hkv : 0);
     take(p.suf_first, suffix.few_rows ? (size_t)B + 1 : 0);
+    take(p.suf_next, 1);
     p.suffix.rows_cap = p.rows_cap;
     p.suffix.skip = p.skip;
     p.slot_rows = suffix.slot_rows;
@@ -1039,7 +1080,7 @@ cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D,
     pa.max_pages = paged.max_pages;
     pa.max_ctx = max_ctx;
     pa.n_groups = n_groups;
-    pa.suffix_chunk = suffix.few_rows ? rd_suffix_chunk(rd_suffix_row_warps(P_max * pa.G)) : 0;
+    pa.suffix_chunk = suffix.few_rows && !suffix.by_unit ? rd_suffix_chunk(rd_suffix_row_warps(P_max * pa.G)) : 0;
     pa.lens = packed_len;
     pa.ctx_lens = paged.ctx_lens;
     pa.group_offsets = group_offsets;
@@ -1076,7 +1117,7 @@ cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D,
 
     if (suffix.few_rows)
         e = rd_launch_shared_suffix(pa.p, B, P_max, Hq, Hkv, D, fa.scale_log2, q, k_new, v_new, k_pool, v_pool, paged,
-                                    mask, mask_words, dev_status, stream);
+                                    mask, mask_words, suffix.by_unit, dev_status, stream);
     else
         e = rd_launch_attention(suffix.plan, B, P_max, Hq, Hkv, D, scale, q, k_new, v_new, k_pool, v_pool, nullptr, 0, max_ctx,
                                 pa.p.eff_len, mask, mask_words, o, suffix_ws, dev_status, stream, &paged, nullptr,

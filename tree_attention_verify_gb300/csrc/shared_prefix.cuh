@@ -29,7 +29,7 @@ struct Plan {
     int32_t* node_base;    // [B + 1] its first node in the compact list
     int32_t* node_row;     // [B P_max] compact node -> b P_max + p
     Group* group;          // [n_groups]
-    uint32_t* first;       // [n_groups + 1] prefix chunks of the groups before
+    uint32_t* first;       // [n_groups + 1] what the groups before count in the prefix's division
     int4* req;             // [B] first unit of its group (-1: no prefix), units per kv head,
                            // first row within the group, first compact row
     // over the prefix: whole units by compact row, [Hkv][D / 4][rows_cap]; pieces of
@@ -47,6 +47,7 @@ struct Plan {
     int slot_rows;
     int grid, suf_grid;    // CTAs of the two launches
     uint32_t* suf_first;   // [B + 1] suffix chunks of the requests before (shared_suffix.cu)
+    int* suf_next;         // the next suffix unit that nobody has taken
 };
 
 // n CTAs of `grid` take the W chunks of a sequence in equal ranges, each of at least
@@ -145,8 +146,9 @@ inline cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, s
 }  // namespace rdshared
 
 int rd_suffix_grid(int rows);
+bool rd_suffix_by_unit(int B, int Hkv, int grid);
 cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, int Hq, int Hkv, int D,
                                     float scale_log2, const void* q, const void* k_new, const void* v_new,
                                     const void* k_pool, const void* v_pool, const rd_paged_kv& paged,
-                                    const uint32_t* mask, int mask_words, int32_t* dev_status,
+                                    const uint32_t* mask, int mask_words, bool by_unit, int32_t* dev_status,
                                     cudaStream_t stream);

@@ -15,8 +15,11 @@
 // Warp roles: one producer (TMA: a unit's queries and what the others need to know
 // of it, then its chunks of CH positions through a ring of ST stages), NW x KS
 // compute warps: NW of 16 rows each, times KS that split each chunk's positions
-// (few rows) and join their sums in shared memory at the unit's end.  The units'
-// chunks form one sequence that the CTAs take in equal ranges, as in the prefix.
+// (few rows) and join their sums in shared memory at the unit's end.  With many
+// units the CTAs take them whole off a counter, as they come free from the prefix
+// (equal ranges, begun when the prefix's CTAs end, left the last one 35 us behind the
+// median at 2,560 units); with few, the units' chunks form one sequence that the
+// CTAs take in equal ranges.
 // Every wait is bounded; on expiry the CTA records RD_DEV_TIMEOUT, drains its
 // copies and returns.
 #include <cuda.h>
@@ -65,6 +68,7 @@ struct SuffixArgs {
     const int32_t* ctx_lens;
     const uint32_t* mask;
     Plan p;
+    bool by_unit;
     int32_t* status;
     long long stall_budget;
 };
@@ -143,7 +147,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
 
     if (warp == C::kWarps) {
         // ------------------------------------------------------------ producer
-        const uint32_t W = __ldcg(a.p.suf_first + a.B);
+        const uint32_t W = a.by_unit ? 0u : __ldcg(a.p.suf_first + a.B);
         const uint32_t nc = W > 0u ? range_ctas(W, gridDim.x, kSuffixMinChunks) : 0u;
         uint32_t x = 0u, end = 0u;
         int b = 0;
@@ -174,38 +178,56 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
             if (a.stall_budget > 0 && !mbar_wait(&bar.never, 0, abort, a.stall_budget)) fail();
             uint32_t g = 0, it = 0;
             bool ok = true;
-            // request b: own context, drafts, chunks of a unit; the next request's first
-            int len = 0, ctx = 0, skip = 0;
-            uint32_t next = 0u, nb = 0u;
+            int len = 0, ctx = 0, skip = 0;               // of request b
+            auto request = [&]() {
+                len = __ldcg(a.p.eff_len + b);
+                skip = __ldcg(a.p.skip + b);
+                ctx = __ldg(a.ctx_lens + b) - skip;
+            };
+            uint32_t next = 0u, nb = 0u;                  // ranges: the next request's first chunk, chunks of a unit
             bool fresh = true;
+            int unit = a.by_unit ? atomicAdd(a.p.suf_next, 1) : 0;
             while (ok && !*abort) {
+                int h = 0, c0 = 0, n = 0, slot = -1;
+                uint32_t stop = 0u;
+                if (a.by_unit) {
+                    while (unit < a.B * a.Hkv) {
+                        b = unit / a.Hkv;
+                        h = unit % a.Hkv;
+                        unit = atomicAdd(a.p.suf_next, 1);     // the one after, on its way meanwhile
+                        request();
+                        if (len > 0) {
+                            n = (ctx + CH - 1) / CH + (len + CH - 1) / CH;
+                            break;
+                        }
+                    }
+                } else if (x < end) {
+                    while (fresh || x >= next) {          // on to the request that holds chunk x
+                        if (!fresh) {
+                            ++b;
+                            base = next;
+                        }
+                        fresh = false;
+                        next = __ldcg(a.p.suf_first + b + 1);
+                        request();
+                        nb = (next - base) / (uint32_t)a.Hkv;
+                    }
+                    h = (int)((x - base) / nb);
+                    const uint32_t u0 = base + (uint32_t)h * nb;
+                    c0 = (int)(x - u0);
+                    stop = min(u0 + nb, end);
+                    n = (int)(stop - x);
+                    slot = (uint32_t)n == nb ? -1 : 2 * (int)blockIdx.x + (c0 == 0 && u0 > start ? 1 : 0);
+                    if (c0 == 0)                          // the unit starts here: name its pieces
+                        a.p.suffix.unit[b * a.Hkv + h] =
+                            make_int2(slot < 0 ? 1 : (int)(range_of(W, nc, u0 + nb - 1) - blockIdx.x) + 1, slot);
+                }
                 if (it > 0 && !mbar_wait(&bar.q_empty, (it - 1) & 1, abort, kWaitBudget)) { ok = false; break; }
-                if (x >= end) {
+                if (n == 0) {                             // no more
                     bar.unit.n = 0;
                     mbar_arrive(&bar.q_full);
                     break;
                 }
-                while (fresh || x >= next) {              // on to the request that holds chunk x
-                    if (!fresh) {
-                        ++b;
-                        base = next;
-                    }
-                    fresh = false;
-                    next = __ldcg(a.p.suf_first + b + 1);
-                    len = __ldcg(a.p.eff_len + b);
-                    skip = __ldcg(a.p.skip + b);
-                    ctx = __ldg(a.ctx_lens + b) - skip;
-                    nb = (next - base) / (uint32_t)a.Hkv;
-                }
-                const int h = (int)((x - base) / nb);
-                const uint32_t u0 = base + (uint32_t)h * nb;
-                const int c0 = (int)(x - u0);
-                const uint32_t stop = min(u0 + nb, end);
-                const int n = (int)(stop - x);
-                const int slot = (uint32_t)n == nb ? -1 : 2 * (int)blockIdx.x + (c0 == 0 && u0 > start ? 1 : 0);
-                if (c0 == 0)                              // the unit starts here: name its pieces
-                    a.p.suffix.unit[b * a.Hkv + h] =
-                        make_int2(slot < 0 ? 1 : (int)(range_of(W, nc, u0 + nb - 1) - blockIdx.x) + 1, slot);
                 bar.unit = Unit{b, h, c0, n, ctx, len, slot};
                 mbar_arrive_expect_tx(&bar.q_full, a.P_max * a.G * D * 2);
 #pragma unroll
@@ -536,12 +558,15 @@ cudaError_t launch_rows(int grid, cudaStream_t stream, SuffixArgs& a, CUtensorMa
 
 }  // namespace
 
+// whole units off a counter when they are many enough to level out
+bool rd_suffix_by_unit(int B, int Hkv, int grid) { return (long long)B * Hkv >= 4LL * grid; }
+
 int rd_suffix_grid(int rows) { return rd_device_sm_count() * rd_suffix_ctas(rd_suffix_row_warps(rows)); }
 
 cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, int Hq, int Hkv, int D,
                                     float scale_log2, const void* q, const void* k_new, const void* v_new,
                                     const void* k_pool, const void* v_pool, const rd_paged_kv& paged,
-                                    const uint32_t* mask, int mask_words, int32_t* dev_status,
+                                    const uint32_t* mask, int mask_words, bool by_unit, int32_t* dev_status,
                                     cudaStream_t stream)
 {
     SuffixArgs a = {};
@@ -559,6 +584,7 @@ cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, i
     a.ctx_lens = paged.ctx_lens;
     a.mask = mask;
     a.p = p;
+    a.by_unit = by_unit;
     a.status = dev_status;
     a.stall_budget = rd_attention_stall_budget();
     const int rows = P_max * a.G, ch = rd_suffix_chunk(rd_suffix_row_warps(rows));
