@@ -466,17 +466,6 @@ struct CopyArgs {
     int32_t* status;
 };
 
-__device__ __forceinline__ void bulk_load(void* smem, const void* gmem, uint32_t bytes, uint64_t* bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(rdtc::smem_addr(smem)), "l"(gmem), "r"(bytes), "r"(rdtc::smem_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void bulk_store(void* gmem, const void* smem, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                 ::"l"(gmem), "r"(rdtc::smem_addr(smem)), "r"(bytes) : "memory");
-}
-
 __global__ void __launch_bounds__(kCopyThreads)
 copy_pages_kernel(const CopyArgs a)
 {
@@ -578,7 +567,7 @@ copy_pages_kernel(const CopyArgs a)
             len[st] = next.bytes;
             if (lane == 0) {
                 rdtc::mbar_arrive_expect_tx(&full[st], next.bytes);
-                bulk_load(ring + (size_t)st * a.piece, next.from, next.bytes, &full[st]);
+                rdtc::bulk_load(ring + (size_t)st * a.piece, next.from, next.bytes, &full[st]);
             }
             __syncwarp();
             ++issued;
@@ -598,7 +587,7 @@ copy_pages_kernel(const CopyArgs a)
                 if (lane == 0) {
                     landed = rdtc::mbar_wait(&full[st], round & 1, &no_abort, kWaitBudget);
                     if (landed) {
-                        bulk_store(to[st], ring + (size_t)st * a.piece, len[st]);
+                        rdtc::bulk_store(to[st], ring + (size_t)st * a.piece, len[st]);
                         rdtc::tma_store_commit();
                         // refill the stage before this one: its store, the last but one,
                         // has read it once at most one store is still reading

@@ -14,7 +14,8 @@
 //   suffix  partials of every row over its request's own context and drafts
 //           (shared_suffix.cu for up to 64 rows per kv head, else the shared-prefix
 //           variant of attention_tc.cu);
-//   merge   the formula above, rounded once to bf16; zeros in padded rows.
+//   merge   the formula above, rounded once to bf16; zeros in padded rows.  With many
+//           units the suffix kernel ends each in this way itself.
 //
 // The prefix kernel: unit = (group, kv head, 256 rows), the rows being the G
 // query heads of each live node of the group, in request order.  One CTA per SM
@@ -73,7 +74,7 @@ constexpr int kQWarp0 = 18;                // two query warps
 constexpr uint32_t kTwoTiles = 8;
 constexpr uint32_t kOneTile = 5;
 constexpr uint32_t kUnitStart = 24;
-constexpr uint32_t kMinRange = 2 * kTwoTiles;   // a CTA's share at least
+constexpr uint32_t kMinRange = 3 * kTwoTiles;   // a CTA's share at least
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
 
@@ -856,7 +857,7 @@ struct MergeArgs {
     uint16_t* o;
 };
 constexpr int kMergeThreads = 256;
-constexpr int kMergePieces = 2;
+constexpr int kMergePieces = 4;
 constexpr int kMergeRows = 32;
 template <int D> constexpr int kMergeSmem = kMergePieces * kMergeRows * D * 4;
 
@@ -978,7 +979,7 @@ cudaError_t launch_merge(dim3 grid, cudaStream_t stream, MergeArgs& a)
 // the tcgen05 kernel, whose tiles hold 128.
 struct SuffixChoice {
     bool few_rows;
-    bool by_unit;             // few_rows: CTAs take whole units off a counter
+    bool by_unit;             // few_rows: CTAs take whole units off a counter and write the output
     bool table;               // units have an entry in the table of pieces
     int grid, slot_rows, tiles;
     rd_attn_plan plan;        // tcgen05
@@ -1023,8 +1024,8 @@ size_t layout(Plan& p, void*& suffix_ws, unsigned char* base, int B, int P_max, 
     take(p.rows_ml, p.rows_cap * Hkv);
     take(p.part, slots * kUnitRows * (D / 4));
     take(p.part_ml, slots * kUnitRows);
-    take(p.suffix.rows, p.rows_cap * Hkv * (D / 4));
-    take(p.suffix.rows_ml, p.rows_cap * Hkv);
+    take(p.suffix.rows, suffix.by_unit ? 0 : p.rows_cap * Hkv * (D / 4));
+    take(p.suffix.rows_ml, suffix.by_unit ? 0 : p.rows_cap * Hkv);
     take(p.suffix.unit, suffix.table ? (size_t)suffix.tiles * B * Hkv : 0);
     take(p.suf_first, suffix.few_rows ? (size_t)B + 1 : 0);
     take(p.suf_next, 1);
@@ -1034,7 +1035,7 @@ size_t layout(Plan& p, void*& suffix_ws, unsigned char* base, int B, int P_max, 
     p.grid = pre_grid;
     p.suf_grid = suffix.grid;
     suffix_ws = base == nullptr ? nullptr : base + at;
-    const size_t suf_rows = (size_t)2 * suffix.grid * suffix.slot_rows;
+    const size_t suf_rows = suffix.by_unit ? 0 : (size_t)2 * suffix.grid * suffix.slot_rows;
     p.suf_part = static_cast<float4*>(suffix_ws);
     p.suf_part_ml = reinterpret_cast<float2*>(p.suf_part + suf_rows * (D / 4));
     return at + (suffix.few_rows ? suf_rows * (D * sizeof(float) + sizeof(float2)) : suffix.plan.ws_bytes);
@@ -1117,12 +1118,12 @@ cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D,
 
     if (suffix.few_rows)
         e = rd_launch_shared_suffix(pa.p, B, P_max, Hq, Hkv, D, fa.scale_log2, q, k_new, v_new, k_pool, v_pool, paged,
-                                    mask, mask_words, suffix.by_unit, dev_status, stream);
+                                    mask, mask_words, suffix.by_unit, o, dev_status, stream);
     else
         e = rd_launch_attention(suffix.plan, B, P_max, Hq, Hkv, D, scale, q, k_new, v_new, k_pool, v_pool, nullptr, 0, max_ctx,
                                 pa.p.eff_len, mask, mask_words, o, suffix_ws, dev_status, stream, &paged, nullptr,
                                 &pa.p.suffix);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || suffix.by_unit) return e;      // (its units end in output rows)
 
     MergeArgs ma = {};
     ma.P_max = P_max;

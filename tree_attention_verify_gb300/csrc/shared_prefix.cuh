@@ -117,7 +117,7 @@ __device__ __forceinline__ Pieces pieces_of(int2 unit, const Plan& p, int h, int
 
 // ---- the suffix kernel for few rows per kv head (shared_suffix.cu)
 constexpr int kSuffixMaxRows = 64;
-constexpr uint32_t kSuffixMinChunks = 4;   // chunks per CTA at least
+constexpr uint32_t kSuffixMinChunks = 2;   // chunks per CTA at least
 // warps of 16 rows for `rows` rows
 __host__ __device__ constexpr int rd_suffix_row_warps(int rows) { return (rows + 15) / 16; }
 // positions of a chunk: with one or two row warps several warps split them
@@ -150,5 +150,5 @@ bool rd_suffix_by_unit(int B, int Hkv, int grid);
 cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, int Hq, int Hkv, int D,
                                     float scale_log2, const void* q, const void* k_new, const void* v_new,
                                     const void* k_pool, const void* v_pool, const rd_paged_kv& paged,
-                                    const uint32_t* mask, int mask_words, bool by_unit, int32_t* dev_status,
+                                    const uint32_t* mask, int mask_words, bool by_unit, void* o, int32_t* dev_status,
                                     cudaStream_t stream);

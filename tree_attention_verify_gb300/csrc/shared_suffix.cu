@@ -18,8 +18,11 @@
 // (few rows) and join their sums in shared memory at the unit's end.  With many
 // units the CTAs take them whole off a counter, as they come free from the prefix
 // (equal ranges, begun when the prefix's CTAs end, left the last one 35 us behind the
-// median at 2,560 units); with few, the units' chunks form one sequence that the
-// CTAs take in equal ranges.
+// median at 2,560 units).  Each unit then ends with its rows' partials over the
+// prefix, which come through the same ring like further chunks, and with the output
+// rows: no partials of its own leave the SM, and no merge follows (48 + 36 us for this
+// kernel and the merge at 64 requests x 40 heads).  With few units, their chunks form
+// one sequence that the CTAs take in equal ranges, and all partials go to the merge.
 // Every wait is bounded; on expiry the CTA records RD_DEV_TIMEOUT, drains its
 // copies and returns.
 #include <cuda.h>
@@ -54,11 +57,16 @@ template <int D, int NW, int KS> struct SCfg {
     static constexpr int kQOff = kStages * kStageBytes;
     static constexpr int kJoinOff = kQOff + kQBytes;                // (KS - 1) NW warps' sums
     static constexpr int kJoinBytes = (KS - 1) * NW * (16 * D * 4 + 16 * 8);
-    static constexpr int kBarOff = kJoinOff + kJoinBytes;
+    static constexpr int kMlOff = kJoinOff + kJoinBytes;            // (m, l) of a stage's rows over the prefix
+    static constexpr int kMlRows = kQRows + 2;
+    static constexpr int kBarOff = kMlOff + kStages * kMlRows * 8;
     static constexpr int kSmemBytes = kBarOff + 512 + 1024;
     static constexpr int kCtas = rd_suffix_ctas(NW);                // per SM
     static_assert(kCtas * (kSmemBytes + 1024) <= 227 * 1024, "CTAs per SM");
     static_assert(kKw % 16 == 0, "a warp's positions are whole k-steps");
+    // half the columns of every row's partials fit a stage
+    static_assert(kQRows * (D / 2) * 4 <= kStageBytes, "partials in the ring");
+    static_assert(kMlOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
 };
 
 struct SuffixArgs {
@@ -67,15 +75,24 @@ struct SuffixArgs {
     const int32_t* block_table;
     const int32_t* ctx_lens;
     const uint32_t* mask;
+    uint16_t* o;
     Plan p;
     bool by_unit;
     int32_t* status;
     long long stall_budget;
 };
 
-// What the compute warps need to know of a unit (or piece); n = 0: no more.
+// What the compute warps need to know of a unit (or piece); n = 0: no more, -1: a
+// skipped request's rows (zeros).
 struct Unit {
     int b, h, c_first, n, C, Pb, slot;     // slot -1: a whole unit
+};
+
+// What a ring entry holds.
+struct Entry {
+    int kind;                              // 0: chunk c of the unit, 1: partials over the prefix, 2: nothing
+    int c, last;                           // last: the unit ends with it
+    int r0, r1, half, shift;               // partials: rows [r0, r1), half of the columns; first (m, l) at `shift`
 };
 
 struct SBar {
@@ -87,6 +104,7 @@ struct SBar {
     uint64_t join_empty;
     uint64_t never;
     Unit unit;
+    Entry entry[4];
     int abort;
 };
 static_assert(sizeof(SBar) <= 512, "barrier block");
@@ -107,6 +125,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  "{%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four lanes with four words each: word k of lane t becomes word t of lane k.
+__device__ __forceinline__ void swap4(uint32_t (&v)[4], int t)
+{
+    const bool odd = t & 1, high = t & 2;
+    const uint32_t a0 = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
+    const uint32_t a1 = __shfl_xor_sync(0xffffffffu, odd ? v[2] : v[3], 1);
+    if (odd) { v[0] = a0; v[2] = a1; } else { v[1] = a0; v[3] = a1; }
+    const uint32_t b0 = __shfl_xor_sync(0xffffffffu, high ? v[0] : v[2], 2);
+    const uint32_t b1 = __shfl_xor_sync(0xffffffffu, high ? v[1] : v[3], 2);
+    if (high) { v[0] = b0; v[1] = b1; } else { v[2] = b0; v[3] = b1; }
 }
 
 template <int D, int NW, int KS>
@@ -185,21 +215,18 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 ctx = __ldg(a.ctx_lens + b) - skip;
             };
             uint32_t next = 0u, nb = 0u;                  // ranges: the next request's first chunk, chunks of a unit
-            bool fresh = true;
+            bool fresh = true, prefix_written = false;
             int unit = a.by_unit ? atomicAdd(a.p.suf_next, 1) : 0;
             while (ok && !*abort) {
                 int h = 0, c0 = 0, n = 0, slot = -1;
                 uint32_t stop = 0u;
                 if (a.by_unit) {
-                    while (unit < a.B * a.Hkv) {
+                    if (unit < a.B * a.Hkv) {
                         b = unit / a.Hkv;
                         h = unit % a.Hkv;
                         unit = atomicAdd(a.p.suf_next, 1);     // the one after, on its way meanwhile
                         request();
-                        if (len > 0) {
-                            n = (ctx + CH - 1) / CH + (len + CH - 1) / CH;
-                            break;
-                        }
+                        n = len > 0 ? (ctx + CH - 1) / CH + (len + CH - 1) / CH : -1;
                     }
                 } else if (x < end) {
                     while (fresh || x >= next) {          // on to the request that holds chunk x
@@ -229,16 +256,28 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                     break;
                 }
                 bar.unit = Unit{b, h, c0, n, ctx, len, slot};
+                if (n < 0) {
+                    mbar_arrive(&bar.q_full);
+                    ++it;
+                    continue;
+                }
+                int4 req = make_int4(-1, 0, 0, 0);
+                if (a.by_unit) req = __ldcg(a.p.req + b);
                 mbar_arrive_expect_tx(&bar.q_full, a.P_max * a.G * D * 2);
 #pragma unroll
                 for (int db = 0; db < C::kDB; ++db)
                     tma_load_3d(smem + C::kQOff + db * (C::kQRows * 128), &map_q, &bar.q_full, db * 64, h * a.G,
                                 b * a.P_max);
                 ++it;
+                // the next ring entry, free; false: the wait ran out
+                auto stage = [&](int& st) -> bool {
+                    st = (int)(g % C::kStages);
+                    return g < (uint32_t)C::kStages ||
+                           mbar_wait(&bar.empty[st], ((g / C::kStages) - 1) & 1, abort, kWaitBudget);
+                };
                 const int n_ctx = (ctx + CH - 1) / CH;
                 int entry = -1, page = 0;
                 for (int c = c0; c < c0 + n; ++c, ++g) {
-                    const int st = (int)(g % C::kStages);
                     const CUtensorMap* mk = &map_kd;
                     const CUtensorMap* mv = &map_vd;
                     int z = b * a.P_max + (c - n_ctx) * CH;
@@ -256,12 +295,10 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                         mv = &map_vc;
                         z = page * a.page_size + pos % a.page_size;
                     }
-                    if (g >= (uint32_t)C::kStages &&
-                        !mbar_wait(&bar.empty[st], ((g / C::kStages) - 1) & 1, abort, kWaitBudget)) {
-                        ok = false;
-                        break;
-                    }
+                    int st;
+                    if (!stage(st)) { ok = false; break; }
                     unsigned char* ks = smem + st * C::kStageBytes;
+                    bar.entry[st] = Entry{0, c, c + 1 == c0 + n && req.x < 0, 0, 0, 0, 0};
                     mbar_arrive_expect_tx(&bar.full[st], C::kStageBytes);
 #pragma unroll
                     for (int db = 0; db < C::kDB; ++db) {
@@ -270,6 +307,41 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                     }
                 }
                 x = stop;
+                if (!ok || req.x < 0) continue;
+                // the rows' partials over the prefix: their unit's pieces (of two units,
+                // where the rows cross one's end), half of the columns at a time
+                if (!prefix_written) asm volatile("griddepcontrol.wait;" ::: "memory");
+                prefix_written = true;
+                const int rows = len * a.G;
+                for (int r0 = 0; ok && r0 < rows;) {
+                    const int at = req.z + r0, r1 = min(rows, r0 + kUnitRows - at % kUnitRows);
+                    const Pieces pc = pieces_of<D>(__ldcg(a.p.unit + req.x + h * req.y + at / kUnitRows), a.p, h,
+                                                   req.w + r0, at % kUnitRows);
+                    for (int k = 0; ok && k < pc.n; ++k) {
+                        const float4* src = pc.o(k);
+                        const float2* ml = pc.ml(k);
+                        const int shift = (int)((reinterpret_cast<uintptr_t>(ml) >> 3) & 1);   // copies begin at 16 bytes
+                        const uint32_t ml_bytes = (uint32_t)((r1 - r0 + shift + 1) & ~1) * 8u;
+                        const uint32_t col_bytes = (uint32_t)(r1 - r0) * 16u;
+                        for (int half = 0; half < 2; ++half, ++g) {
+                            int st;
+                            if (!stage(st)) { ok = false; break; }
+                            bar.entry[st] = Entry{1, 0, 0, r0, r1, half, shift};
+                            mbar_arrive_expect_tx(&bar.full[st], col_bytes * (D / 8) + (half == 0 ? ml_bytes : 0u));
+                            if (half == 0)
+                                bulk_load(smem + C::kMlOff + st * C::kMlRows * 8, ml - shift, ml_bytes, &bar.full[st]);
+                            for (int c = 0; c < D / 8; ++c)
+                                bulk_load(smem + st * C::kStageBytes + (size_t)c * col_bytes,
+                                          src + (size_t)(half * (D / 8) + c) * pc.stride, col_bytes, &bar.full[st]);
+                        }
+                    }
+                    r0 = r1;
+                }
+                int st;
+                if (!ok || !stage(st)) { ok = false; continue; }
+                bar.entry[st] = Entry{2, 0, 1, 0, 0, 0, 0};
+                mbar_arrive(&bar.full[st]);
+                ++g;
             }
             if (!ok || *abort) {
                 // the compute warps may have left before the last queries landed
@@ -289,7 +361,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
         const int a_row = rw * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, a_c = lane >> 4;
         const int k_row = ks * C::kKw + (lane & 7) + ((lane >> 4) & 1) * 8, k_c = (lane >> 3) & 1;
         const int v_row = ks * C::kKw + (lane & 7) + ((lane >> 3) & 1) * 8, v_c = lane >> 4;
-        uint32_t g = 0, it = 0;
+        uint32_t g = 0, it = 0, joins = 0;
         bool ok = true;
         for (;; ++it) {
             if (!warp_wait(&bar.q_full, it & 1, abort, kWaitBudget)) { ok = false; break; }
@@ -322,11 +394,111 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            float wp[2] = {0.f, 0.f};                     // weights of the prefix piece at hand
+            // the unit's own sums: over a row's four lanes, then over the warps that split
+            // the positions (those of ks > 0 leave theirs and only keep step from there on)
+            auto finish = [&]() -> bool {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                }
+                if constexpr (KS > 1) {
+                    float* const jo = reinterpret_cast<float*>(smem + C::kJoinOff);
+                    float2* const jml = reinterpret_cast<float2*>(smem + C::kJoinOff + (KS - 1) * NW * 16 * D * 4);
+                    if (ks > 0) {
+                        if (joins > 0 && !warp_wait(&bar.join_empty, (joins - 1) & 1, abort, kWaitBudget)) return false;
+                        ++joins;
+                        const int at = (ks - 1) * NW + rw;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j)
+                            *reinterpret_cast<float4*>(jo + ((size_t)(at * (D / 8) + j) * 32 + lane) * 4) =
+                                make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                        if (tc == 0) {
+                            jml[at * 16 + gr] = make_float2(m[0], l[0]);
+                            jml[at * 16 + gr + 8] = make_float2(m[1], l[1]);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.join_full);
+                        return true;
+                    }
+                    if (!warp_wait(&bar.join_full, joins & 1, abort, kWaitBudget)) return false;
+                    ++joins;
+#pragma unroll
+                    for (int t = 0; t < KS - 1; ++t) {
+                        const int at = t * NW + rw;
+                        float f[2], q[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 ml = jml[at * 16 + gr + 8 * i];
+                            const float M = fmaxf(m[i], ml.x), base = M == -INFINITY ? 0.f : M;
+                            f[i] = fast_exp2(m[i] - base);
+                            q[i] = fast_exp2(ml.x - base);
+                            l[i] = l[i] * f[i] + ml.y * q[i];
+                            m[i] = M;
+                        }
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            const float4 y = *reinterpret_cast<const float4*>(jo + ((size_t)(at * (D / 8) + j) * 32 + lane) * 4);
+                            o[j][0] = o[j][0] * f[0] + y.x * q[0];
+                            o[j][1] = o[j][1] * f[0] + y.y * q[0];
+                            o[j][2] = o[j][2] * f[1] + y.z * q[1];
+                            o[j][3] = o[j][3] * f[1] + y.w * q[1];
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.join_empty);
+                }
+                return true;
+            };
+            bool finished = false;
             const int n_ctx = (u.C + CH - 1) / CH;
-            for (int c = u.c_first; c < u.c_first + u.n; ++c, ++g) {
+            for (bool last = u.n < 0; !last; ++g) {
                 const int st = (int)(g % C::kStages);
                 if (!warp_wait(&bar.full[st], (g / C::kStages) & 1, abort, kWaitBudget)) { ok = false; break; }
-                if (!dead) {
+                const Entry en = bar.entry[st];
+                last = en.last != 0;
+                const int c = en.c;
+                if (en.kind != 0) {
+                    if (!finished && !finish()) { ok = false; break; }
+                    finished = true;
+                    if (en.kind == 1 && ks == 0 && !dead) {
+                        const int rows = en.r1 - en.r0;
+                        if (en.half == 0) {
+                            const float2* ml = reinterpret_cast<const float2*>(smem + C::kMlOff) + st * C::kMlRows + en.shift;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int at = rw * 16 + gr + 8 * i - en.r0;
+                                const float2 x = at >= 0 && at < rows ? ml[at] : make_float2(-INFINITY, 0.f);
+                                const float M = fmaxf(m[i], x.x), base = M == -INFINITY ? 0.f : M;
+                                const float f = fast_exp2(m[i] - base);
+                                wp[i] = fast_exp2(x.x - base);
+                                l[i] = l[i] * f + x.y * wp[i];
+                                m[i] = M;
+#pragma unroll
+                                for (int j = 0; j < D / 8; ++j) {
+                                    o[j][2 * i] *= f;
+                                    o[j][2 * i + 1] *= f;
+                                }
+                            }
+                        }
+                        // columns [half D/2, ..): float4 [D / 8][rows]
+                        const unsigned char* part = smem + st * C::kStageBytes;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = rw * 16 + gr + 8 * i - en.r0;
+                            if (at < 0 || at >= rows) continue;
+#pragma unroll
+                            for (int j = 0; j < D / 8; ++j) {
+                                if ((j >= D / 16) != (en.half == 1)) continue;
+                                const int c4 = 2 * (j % (D / 16)) + (tc >> 1);
+                                const float2 y = *reinterpret_cast<const float2*>(part + ((size_t)c4 * rows + at) * 16 + (tc & 1) * 8);
+                                o[j][2 * i] += y.x * wp[i];
+                                o[j][2 * i + 1] += y.y * wp[i];
+                            }
+                        }
+                    }
+                } else if (!dead) {
                     const uint32_t kb = smem_u + st * C::kStageBytes, vb = kb + C::kKBytes;
                     float s[C::kKw / 8][4];
 #pragma unroll
@@ -442,55 +614,28 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 if (lane == 0) mbar_arrive(&bar.empty[st]);
             }
             if (!ok) break;
+            if (!finished && u.n > 0 && !finish()) { ok = false; break; }
+            if (ks > 0) continue;
+            if (a.by_unit) {
+                // ---- output rows, 16 bytes a lane (four lanes swap their pairs of columns);
+                // rows behind the packed length: zeros
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            }
-            if constexpr (KS > 1) {
-                // the warps of one row tile join: those of ks > 0 leave their sums
-                float* const jo = reinterpret_cast<float*>(smem + C::kJoinOff);
-                float2* const jml = reinterpret_cast<float2*>(smem + C::kJoinOff + (KS - 1) * NW * 16 * D * 4);
-                if (ks > 0) {
-                    if (it > 0 && !warp_wait(&bar.join_empty, (it - 1) & 1, abort, kWaitBudget)) { ok = false; break; }
-                    const int at = (ks - 1) * NW + rw;
+                for (int i = 0; i < 2; ++i) {
+                    const int row = rw * 16 + gr + 8 * i;
+                    const float inv = row < live && l[i] != 0.f ? 1.f / l[i] : 0.f;
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        a.o + (((size_t)u.b * a.P_max + row / a.G) * a.Hq + u.h * a.G + row % a.G) * D);
 #pragma unroll
-                    for (int j = 0; j < D / 8; ++j)
-                        *reinterpret_cast<float4*>(jo + ((size_t)(at * (D / 8) + j) * 32 + lane) * 4) =
-                            make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
-                    if (tc == 0) {
-                        jml[at * 16 + gr] = make_float2(m[0], l[0]);
-                        jml[at * 16 + gr + 8] = make_float2(m[1], l[1]);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.join_full);
-                    continue;
-                }
-                if (!warp_wait(&bar.join_full, it & 1, abort, kWaitBudget)) { ok = false; break; }
+                    for (int j0 = 0; j0 < D / 8; j0 += 4) {
+                        uint32_t v[4];
 #pragma unroll
-                for (int t = 0; t < KS - 1; ++t) {
-                    const int at = t * NW + rw;
-                    float f[2], q[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 ml = jml[at * 16 + gr + 8 * i];
-                        const float M = fmaxf(m[i], ml.x), base = M == -INFINITY ? 0.f : M;
-                        f[i] = fast_exp2(m[i] - base);
-                        q[i] = fast_exp2(ml.x - base);
-                        l[i] = l[i] * f[i] + ml.y * q[i];
-                        m[i] = M;
-                    }
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        const float4 y = *reinterpret_cast<const float4*>(jo + ((size_t)(at * (D / 8) + j) * 32 + lane) * 4);
-                        o[j][0] = o[j][0] * f[0] + y.x * q[0];
-                        o[j][1] = o[j][1] * f[0] + y.y * q[0];
-                        o[j][2] = o[j][2] * f[1] + y.z * q[1];
-                        o[j][3] = o[j][3] * f[1] + y.w * q[1];
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = row < live ? pack_bf16(o[j0 + k][2 * i] * inv, o[j0 + k][2 * i + 1] * inv) : 0u;
+                        swap4(v, tc);
+                        if (row < a.P_max * a.G) dst[j0 + tc] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.join_empty);
+                continue;
             }
             // ---- fp32 partials, float4 [D / 4][rows]: eight rows' column pairs make
             // whole lines
@@ -566,7 +711,7 @@ int rd_suffix_grid(int rows) { return rd_device_sm_count() * rd_suffix_ctas(rd_s
 cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, int Hq, int Hkv, int D,
                                     float scale_log2, const void* q, const void* k_new, const void* v_new,
                                     const void* k_pool, const void* v_pool, const rd_paged_kv& paged,
-                                    const uint32_t* mask, int mask_words, bool by_unit, int32_t* dev_status,
+                                    const uint32_t* mask, int mask_words, bool by_unit, void* o, int32_t* dev_status,
                                     cudaStream_t stream)
 {
     SuffixArgs a = {};
@@ -584,6 +729,7 @@ cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, i
     a.ctx_lens = paged.ctx_lens;
     a.mask = mask;
     a.p = p;
+    a.o = static_cast<uint16_t*>(o);
     a.by_unit = by_unit;
     a.status = dev_status;
     a.stall_budget = rd_attention_stall_budget();
