@@ -82,20 +82,26 @@ struct Pieces {
     __device__ __forceinline__ const float2* ml(int i) const { return i == 0 ? ml0 : ml1 + (size_t)(i - 1) * ml_step; }
 };
 
+// How many pieces an entry (pieces, first slot) of a table names, all in slots below
+// 2 `grid`.  A launch whose waits ran out may have left an entry unwritten: what is
+// no such entry counts as no pieces.
+__device__ __forceinline__ int pieces_in(int2 unit, int grid)
+{
+    const bool fine = unit.x == 1 ||
+                      (unit.x > 1 && unit.x <= grid && unit.y >= 0 && unit.y < 2 * grid && unit.y / 2 + unit.x <= grid);
+    return fine ? unit.x : 0;
+}
+
 // unit = (pieces, first slot); a whole unit's rows are [h][D / 4][cap] at `row`,
-// pieces lie in slots of R rows at r, those behind the first in slots 2 c, all
-// below 2 `grid`.  A launch whose waits ran out may have left an entry unwritten:
-// what is no such entry counts as no pieces.
+// pieces lie in slots of R rows at r, those behind the first in slots 2 c
 template <int D>
 __device__ __forceinline__ Pieces pieces_at(int2 unit, const float4* rows, const float2* rows_ml, size_t cap, int h,
                                             size_t row, const float4* part, const float2* part_ml, int R, int r,
                                             int grid)
 {
     Pieces p;
-    const bool fine = unit.x == 1 ||
-                      (unit.x > 1 && unit.x <= grid && unit.y >= 0 && unit.y < 2 * grid && unit.y / 2 + unit.x <= grid);
-    p.n = fine ? unit.x : 0;
-    if (!fine) unit = make_int2(1, 0);
+    p.n = pieces_in(unit, grid);
+    if (p.n == 0) unit = make_int2(1, 0);
     const bool whole = unit.x == 1;
     const size_t next = 2 * (size_t)(unit.y / 2 + 1);
     p.stride = whole ? cap : (size_t)R;

@@ -143,7 +143,8 @@ template <int D, int NW, int KS>
 __global__ void __launch_bounds__((NW * KS + 1) * 32, SCfg<D, NW, KS>::kCtas)
 suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
               const __grid_constant__ CUtensorMap map_vc, const __grid_constant__ CUtensorMap map_kd,
-              const __grid_constant__ CUtensorMap map_vd, const __grid_constant__ CUtensorMap map_q)
+              const __grid_constant__ CUtensorMap map_vd, const __grid_constant__ CUtensorMap map_q,
+              const __grid_constant__ CUtensorMap map_rows, const __grid_constant__ CUtensorMap map_part)
 {
     using C = SCfg<D, NW, KS>;
     constexpr int CH = C::kCh;
@@ -205,6 +206,10 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
             tma_prefetch_desc(&map_kd);
             tma_prefetch_desc(&map_vd);
             tma_prefetch_desc(&map_q);
+            if (a.by_unit) {
+                tma_prefetch_desc(&map_rows);
+                tma_prefetch_desc(&map_part);
+            }
             if (a.stall_budget > 0 && !mbar_wait(&bar.never, 0, abort, a.stall_budget)) fail();
             uint32_t g = 0, it = 0;
             bool ok = true;
@@ -216,16 +221,38 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
             };
             uint32_t next = 0u, nb = 0u;                  // ranges: the next request's first chunk, chunks of a unit
             bool fresh = true, prefix_written = false;
-            int unit = a.by_unit ? atomicAdd(a.p.suf_next, 1) : 0;
+            // by unit: what is read of a unit comes a unit ahead, its number two ahead
+            const int units = a.B * a.Hkv;
+            int unit = units, after = units, n_len = 0, n_ctx_len = 0, n_skip = 0;
+            int4 n_req = make_int4(-1, 0, 0, 0);
+            auto read_ahead = [&]() {
+                if (unit >= units) return;
+                const int q = unit / a.Hkv;
+                n_len = __ldcg(a.p.eff_len + q);
+                n_skip = __ldcg(a.p.skip + q);
+                n_ctx_len = __ldg(a.ctx_lens + q);
+                n_req = __ldcg(a.p.req + q);
+            };
+            if (a.by_unit) {
+                unit = atomicAdd(a.p.suf_next, 1);
+                after = atomicAdd(a.p.suf_next, 1);
+                read_ahead();
+            }
             while (ok && !*abort) {
                 int h = 0, c0 = 0, n = 0, slot = -1;
                 uint32_t stop = 0u;
+                int4 req = make_int4(-1, 0, 0, 0);
                 if (a.by_unit) {
-                    if (unit < a.B * a.Hkv) {
+                    if (unit < units) {
                         b = unit / a.Hkv;
                         h = unit % a.Hkv;
-                        unit = atomicAdd(a.p.suf_next, 1);     // the one after, on its way meanwhile
-                        request();
+                        len = n_len;
+                        skip = n_skip;
+                        ctx = n_ctx_len - skip;
+                        req = n_req;
+                        unit = after;
+                        if (after < units) after = atomicAdd(a.p.suf_next, 1);
+                        read_ahead();
                         n = len > 0 ? (ctx + CH - 1) / CH + (len + CH - 1) / CH : -1;
                     }
                 } else if (x < end) {
@@ -261,8 +288,6 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                     ++it;
                     continue;
                 }
-                int4 req = make_int4(-1, 0, 0, 0);
-                if (a.by_unit) req = __ldcg(a.p.req + b);
                 mbar_arrive_expect_tx(&bar.q_full, a.P_max * a.G * D * 2);
 #pragma unroll
                 for (int db = 0; db < C::kDB; ++db)
@@ -314,25 +339,26 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 prefix_written = true;
                 const int rows = len * a.G;
                 for (int r0 = 0; ok && r0 < rows;) {
-                    const int at = req.z + r0, r1 = min(rows, r0 + kUnitRows - at % kUnitRows);
-                    const Pieces pc = pieces_of<D>(__ldcg(a.p.unit + req.x + h * req.y + at / kUnitRows), a.p, h,
-                                                   req.w + r0, at % kUnitRows);
-                    for (int k = 0; ok && k < pc.n; ++k) {
-                        const float4* src = pc.o(k);
-                        const float2* ml = pc.ml(k);
+                    const int at = req.z + r0, r = at % kUnitRows, r1 = min(rows, r0 + kUnitRows - r);
+                    const int2 table = __ldcg(a.p.unit + req.x + h * req.y + at / kUnitRows);
+                    const int pieces = pieces_in(table, a.p.grid);
+                    const bool whole = pieces == 1;
+                    for (int k = 0; ok && k < pieces; ++k) {
+                        const int sl = k == 0 ? table.y : 2 * (table.y / 2 + k);       // its slot
+                        const CUtensorMap* map = whole ? &map_rows : &map_part;
+                        const int px = (whole ? req.w + r0 : r) * 4, py = (whole ? h : sl) * (D / 4);
+                        const float2* ml = whole ? a.p.rows_ml + (size_t)h * a.p.rows_cap + req.w + r0
+                                                 : a.p.part_ml + (size_t)sl * kUnitRows + r;
                         const int shift = (int)((reinterpret_cast<uintptr_t>(ml) >> 3) & 1);   // copies begin at 16 bytes
                         const uint32_t ml_bytes = (uint32_t)((r1 - r0 + shift + 1) & ~1) * 8u;
-                        const uint32_t col_bytes = (uint32_t)(r1 - r0) * 16u;
                         for (int half = 0; half < 2; ++half, ++g) {
                             int st;
                             if (!stage(st)) { ok = false; break; }
                             bar.entry[st] = Entry{1, 0, 0, r0, r1, half, shift};
-                            mbar_arrive_expect_tx(&bar.full[st], col_bytes * (D / 8) + (half == 0 ? ml_bytes : 0u));
+                            mbar_arrive_expect_tx(&bar.full[st], C::kQRows * 16 * (D / 8) + (half == 0 ? ml_bytes : 0u));
+                            tma_load_2d(smem + st * C::kStageBytes, map, &bar.full[st], px, py + half * (D / 8));
                             if (half == 0)
                                 bulk_load(smem + C::kMlOff + st * C::kMlRows * 8, ml - shift, ml_bytes, &bar.full[st]);
-                            for (int c = 0; c < D / 8; ++c)
-                                bulk_load(smem + st * C::kStageBytes + (size_t)c * col_bytes,
-                                          src + (size_t)(half * (D / 8) + c) * pc.stride, col_bytes, &bar.full[st]);
                         }
                     }
                     r0 = r1;
@@ -482,7 +508,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                                 }
                             }
                         }
-                        // columns [half D/2, ..): float4 [D / 8][rows]
+                        // columns [half D/2, ..): float4 [D / 8][kQRows]
                         const unsigned char* part = smem + st * C::kStageBytes;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -492,7 +518,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                             for (int j = 0; j < D / 8; ++j) {
                                 if ((j >= D / 16) != (en.half == 1)) continue;
                                 const int c4 = 2 * (j % (D / 16)) + (tc >> 1);
-                                const float2 y = *reinterpret_cast<const float2*>(part + ((size_t)c4 * rows + at) * 16 + (tc & 1) * 8);
+                                const float2 y = *reinterpret_cast<const float2*>(part + (c4 * C::kQRows + at) * 16 + (tc & 1) * 8);
                                 o[j][2 * i] += y.x * wp[i];
                                 o[j][2 * i + 1] += y.y * wp[i];
                             }
@@ -678,6 +704,20 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int D
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// partials: float4 [blocks][D / 4][rows] -> boxes of `box` rows x D / 8 column groups
+bool make_partial_map(CUtensorMap* map, const void* base, size_t rows, size_t groups, int box, int D)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)rows * 4, (cuuint64_t)groups};
+    cuuint64_t strides[1] = {(cuuint64_t)rows * 16};
+    cuuint32_t boxes[2] = {(cuuint32_t)box * 4, (cuuint32_t)D / 8};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int NW, int KS>
 cudaError_t launch(int grid, cudaStream_t stream, SuffixArgs& a, CUtensorMap* m)
 {
@@ -685,7 +725,7 @@ cudaError_t launch(int grid, cudaStream_t stream, SuffixArgs& a, CUtensorMap* m)
     cudaError_t e = cudaFuncSetAttribute(suffix_kernel<D, NW, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    void* args[] = {&a, &m[0], &m[1], &m[2], &m[3], &m[4]};
+    void* args[] = {&a, &m[0], &m[1], &m[2], &m[3], &m[4], &m[5], &m[6]};
     return launch_dependent(reinterpret_cast<const void*>(suffix_kernel<D, NW, KS>), dim3(grid), dim3(C::kThreads),
                             C::kSmemBytes, stream, args);
 }
@@ -735,11 +775,19 @@ cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, i
     a.stall_budget = rd_attention_stall_budget();
     const int rows = P_max * a.G, ch = rd_suffix_chunk(rd_suffix_row_warps(rows));
     const int64_t pool_rows = (int64_t)paged.num_pages * paged.page_size, new_rows = (int64_t)B * P_max;
-    CUtensorMap m[5];
+    CUtensorMap m[7];
+    const int box = rd_suffix_row_warps(rows) * 16;
     if (!make_map(&m[0], k_pool, pool_rows, Hkv, D, 1, ch) || !make_map(&m[1], v_pool, pool_rows, Hkv, D, 1, ch) ||
         !make_map(&m[2], k_new, new_rows, Hkv, D, 1, ch) || !make_map(&m[3], v_new, new_rows, Hkv, D, 1, ch) ||
         !make_map(&m[4], q, new_rows, Hq, D, a.G, P_max))
         return cudaErrorInvalidValue;
+    if (by_unit) {
+        if (!make_partial_map(&m[5], p.rows, p.rows_cap, (size_t)Hkv * (D / 4), box, D) ||
+            !make_partial_map(&m[6], p.part, kUnitRows, (size_t)2 * p.grid * (D / 4), box, D))
+            return cudaErrorInvalidValue;
+    } else {
+        m[5] = m[6] = m[0];                               // not used
+    }
     const int grid = rd_suffix_grid(rows);
     return D == 128 ? launch_rows<128>(grid, stream, a, m) : launch_rows<64>(grid, stream, a, m);
 }
