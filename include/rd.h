@@ -223,7 +223,8 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
  *              that name different prefix pages set RD_DEV_BAD_INDEX; its first
  *              request's pages are read for all.
  * workspace    rd_tree_attention_shared_workspace_size() bytes, 16-byte aligned, no
- *              initial contents; query it with the device current that the call runs on
+ *              initial contents; query it for each shape (a larger batch may need
+ *              less) and with the device current that the call runs on
  * Everything else as rd_tree_attention_paged, its limits among them; page_size is a
  * multiple of 64, and work that does not count in 31 bits (B Hkv max_ctx / 32, and an
  * eighth of B P_max Hq max_ctx / 512 or n_groups Hkv max_ctx / 2) RD_ERR_UNSUPPORTED.  K and V of
