@@ -849,6 +849,9 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
 // that chain once for its rows and then has all their pieces on the way at the same
 // time: copies into shared memory (cp.async) hold no registers.  A row's pieces are
 // those of its prefix unit and of its suffix unit, kMergePieces of them a round.
+// Few rows a CTA: many CTAs' chains run side by side, and none waits for a second
+// wave (32 rows take 69.7 us for the whole call where 8 take 65.7: 16 requests x 8
+// heads x 120 rows; half the columns a thread cost 2 to 6 us on top).
 struct MergeArgs {
     int P_max, Hq, Hkv, G, B;
     int blocks;               // CTAs per (request, kv head)
@@ -856,28 +859,29 @@ struct MergeArgs {
     Plan p;
     uint16_t* o;
 };
-constexpr int kMergeThreads = 256;
+constexpr int kMergeQ = 4;                 // float4 columns of a thread
 constexpr int kMergePieces = 4;
-constexpr int kMergeRows = 32;
+constexpr int kMergeRows = 8;
+template <int D> constexpr int kMergeThreads = kMergeRows * (D / 4 / kMergeQ);
 template <int D> constexpr int kMergeSmem = kMergePieces * kMergeRows * D * 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(kMergeThreads<D>)
 merge_kernel(const MergeArgs a)
 {
     extern __shared__ float4 stage[];                     // [piece][D / 4][kMergeRows]
     __shared__ Pieces s_pc[2][kMergeRows];
-    constexpr int kParts = kMergeThreads / kMergeRows;    // threads of a row
-    constexpr int kQ = D / 4 / kParts;                    // float4 columns of a thread
+    constexpr int kQ = kMergeQ, kParts = D / 4 / kQ;      // threads of a row
     const int bh = blockIdx.x / a.blocks;
     const int b = bh / a.Hkv, h = bh % a.Hkv;
     const int row0 = (blockIdx.x % a.blocks) * kMergeRows;
     const int tid = threadIdx.x;
     const int r = tid % kMergeRows, part = tid / kMergeRows, row = row0 + r;      // row = p G + g
     const int all = a.P_max * a.G;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the plan is written: the suffix kernel's launch has waited for it
     const int len = __ldcg(a.p.eff_len + b);
     const int4 req = __ldcg(a.p.req + b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int n = 0;                                            // the row's pieces
     if (part == 0 && row < all) {
         int2 su = make_int2(1, 0);                        // (a skipped request's entry is not used)
@@ -898,12 +902,12 @@ merge_kernel(const MergeArgs a)
     int most = n;                                         // of the CTA's rows
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-    __shared__ int s_most[kMergeThreads / 32];
+    __shared__ int s_most[kMergeThreads<D> / 32];
     if ((tid & 31) == 0) s_most[tid >> 5] = most;
     __syncthreads();
     most = 0;
 #pragma unroll
-    for (int i = 0; i < kMergeThreads / 32; ++i) most = max(most, s_most[i]);
+    for (int i = 0; i < kMergeThreads<D> / 32; ++i) most = max(most, s_most[i]);
     n = r < live ? s_pc[0][r].n + s_pc[1][r].n : 0;
     float M = -INFINITY, L = 0.f;
     float4 acc[kQ];
@@ -970,7 +974,7 @@ cudaError_t launch_merge(dim3 grid, cudaStream_t stream, MergeArgs& a)
     cudaError_t e = cudaFuncSetAttribute(merge_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem<D>);
     if (e != cudaSuccess) return e;
     void* args[] = {&a};
-    return launch_dependent(reinterpret_cast<const void*>(merge_kernel<D>), grid, dim3(kMergeThreads), kMergeSmem<D>,
+    return launch_dependent(reinterpret_cast<const void*>(merge_kernel<D>), grid, dim3(kMergeThreads<D>), kMergeSmem<D>,
                             stream, args);
 }
 
