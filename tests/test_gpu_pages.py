@@ -270,3 +270,62 @@ def test_given_stream_and_workspace():
     with pytest.raises(rd.RdError):           # pages of 12 bytes: not whole 16-byte units
         rd.rd_copy_pages(torch.zeros(4, 1, 2, 3, dtype=torch.bfloat16, device=DEV),
                          torch.zeros(4, 1, 2, 3, dtype=torch.bfloat16, device=DEV), src, dst)
+
+
+def test_fork_at_the_limit_of_rows():
+    """16,384 rows and pairs: half of the pairs name rows that hold nothing."""
+    rd = _rd()
+    rng = np.random.default_rng(8)
+    R = n = 16384
+    N, width, ps = 20000, 2, 16
+    table, held, refs = _tables(rng, R, N, width)
+    held[R // 2:] = 0
+    refs[:] = 0
+    for r in range(R):
+        table[r, :held[r]] = rng.choice(N // 2, held[r])
+        np.add.at(refs, table[r, :held[r]], 1)
+    ctx = np.maximum(0, held * ps - rng.integers(0, ps, R)).astype(np.int32)
+    k, v = _pool(rng, 1, N, ps, 1, 8), _pool(rng, 1, N, ps, 1, 8)
+    par = rng.integers(-1, R // 2, n).astype(np.int32)
+    kid = (R // 2 + rng.permutation(n) % (R // 2)).astype(np.int32)
+    want = op.oracle_fork_pages(k, v, table, held, refs, ctx, par, kid)
+    kp, vp, t, h, f, c, st = _bf16(k), _bf16(v), _d(table), _d(held), _d(refs), _d(ctx), _status()
+    rd.rd_fork_pages(kp, vp, t, h, f, c, _d(par), _d(kid), dev_status=st)
+    assert st.item() == want[6]
+    for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, h, f, c), want):
+        np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("n", [3, 300])
+def test_copy_and_fork_past_32_bits(n):
+    """Pools whose last pages begin behind 2^32 bytes, and 2^32 elements in the last layer."""
+    rd = _rd()
+    ps, Hkv, D, layers = 64, 8, 128, 2
+    N = 2 ** 31 // (ps * Hkv * D) + 2 * n + 1          # per layer; 8.6 GB a pool
+    k = torch.zeros((layers, N, ps, Hkv, D), dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros_like(k)
+    src, dst = torch.arange(N - 2 * n, N - n, device=DEV), torch.arange(N - n, N, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    for p in (k, v):
+        p[:, N - 2 * n:N - n] = torch.randn(layers, n, ps, Hkv, D, generator=gen, device=DEV, dtype=torch.bfloat16)
+    st = _status()
+    rd.rd_copy_pages(k, v, src.int(), dst.int(), dev_status=st)
+    assert st.item() == 0
+    for p in (k, v):
+        assert torch.equal(p[:, N - n:], p[:, N - 2 * n:N - n])
+        assert not p[:, :N - 2 * n].any() and p[:, N - n:].any()
+    # n rows of one page each, the lowest free pages being the pool's last
+    refs = torch.ones(N, dtype=torch.int32, device=DEV)
+    refs[N - n:] = 0
+    k[:, N - n:], v[:, N - n:] = 7, 7
+    table = torch.full((2 * n, 1), -1, dtype=torch.int32, device=DEV)
+    table[:n, 0] = src.int()
+    held = torch.zeros(2 * n, dtype=torch.int32, device=DEV)
+    held[:n] = 1
+    ctx = torch.where(held > 0, 33, 0).int()
+    rows = torch.arange(n, device=DEV).int()
+    rd.rd_fork_pages(k, v, table, held, refs, ctx, rows, rows + n, dev_status=st)
+    assert st.item() == 0 and torch.equal(table[n:, 0], dst.int()) and (refs == 1).all()
+    for p in (k, v):
+        assert torch.equal(p[:, N - n:, :33], p[:, N - 2 * n:N - n, :33])
+        assert (p[:, N - n:, 33:] == 7).all()

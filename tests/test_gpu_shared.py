@@ -131,6 +131,18 @@ CASES = {
     "long own contexts, one token": dict(B=2, W=1, L=1, Hq=8, Hkv=1, D=64, page=64, offsets=[0, 2], pages=[1],
                                          suffix=9000),
     "long": dict(B=3, W=5, L=4, Hq=4, Hkv=2, D=128, page=64, offsets=[0, 3], pages=[129], suffix=200),
+    # more requests and groups than the plan keeps in shared memory: in ranges, off the counter
+    "1100 requests": dict(B=1100, W=1, L=1, Hq=2, Hkv=1, D=64, page=64, offsets=list(range(0, 82, 2)) + list(range(81, 1101)),
+                          pages=[i % 3 for i in range(1060)], suffix=40),
+    "1500 requests": dict(B=1500, W=1, L=2, Hq=2, Hkv=1, D=64, page=64, offsets=list(range(0, 800, 2)) + list(range(800, 1501)),
+                          pages=[(i + 1) % 2 for i in range(1100)], suffix=50),
+    # one of many units far longer than the others
+    "counter, long own contexts": dict(B=160, W=1, L=3, Hq=8, Hkv=8, D=64, page=64, offsets=[0, 150], pages=[1],
+                                       suffix=2500),
+    # as many drafts as a request may have; many query heads of one kv head
+    "256 drafts": dict(B=2, W=32, L=8, Hq=8, Hkv=2, D=128, page=64, offsets=[0, 2], pages=[3], suffix=200),
+    "200 heads of one": dict(B=3, W=1, L=1, Hq=200, Hkv=1, D=128, page=64, offsets=[0, 3], pages=[4], suffix=150),
+    "64 heads of one": dict(B=3, W=1, L=1, Hq=64, Hkv=1, D=64, page=64, offsets=[0, 3], pages=[4], suffix=150),
 }
 
 
@@ -261,6 +273,49 @@ def test_graphs_streams_and_one_workspace():
             check(o, s)
 
 
+@pytest.mark.parametrize("pair", [("one token each", "many rows"), ("counter", "48 rows"), ("whole units", "whole units")])
+def test_two_streams_at_once(pair):
+    """Calls that overlap in time, each with a workspace of its own."""
+    rd = _rd()
+    runs = []
+    for i, name in enumerate(pair):
+        s = make(**CASES[name], seed=20 + i)
+        d = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(DEV)  # noqa: E731
+        args = [s["q"], s["k_new"], s["v_new"], s["k_pool"], s["v_pool"], d(s["table"]), d(s["ctx"]), d(s["offsets"]),
+                d(s["pages"]), d(s["lens"]), d(s["mask"].view(np.int32))]
+        alone = rd.rd_tree_attention_shared(*args, max_ctx=s["max_ctx"])
+        runs.append((args, s, alone, torch.cuda.Stream(), torch.zeros(1, dtype=torch.int32, device=DEV)))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(12):
+        for i, (args, s, _, stream, st) in enumerate(runs):
+            outs[i].append(rd.rd_tree_attention_shared(*args, max_ctx=s["max_ctx"], dev_status=st, stream=stream))
+    torch.cuda.synchronize()
+    for i, (_, s, alone, _, st) in enumerate(runs):
+        assert st.item() == 0
+        check(alone, s)
+        assert all(torch.equal(alone.view(torch.int16), o.view(torch.int16)) for o in outs[i])
+
+
+@pytest.mark.parametrize("name", ["one token each", "66 rows", "counter"])
+def test_pages_past_32_bits(name):
+    """Pools whose last pages begin behind 2^32 elements."""
+    s = make(**CASES[name], seed=30)
+    n, page, Hkv, D = s["k_pool"].shape
+    total = 2 ** 32 // (page * Hkv * D) + 1 + n        # 8.6 GB each
+    first = total - n
+    big = {}
+    for p in ("k_pool", "v_pool"):
+        big[p] = torch.empty((total, page, Hkv, D), dtype=torch.bfloat16, device=DEV)
+        big[p][:first].fill_(NAN)
+        big[p][first:].copy_(s[p])
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o = call({**s, **big, "table": s["table"] + first}, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check(o, s)
+
+
 def test_refuses_before_a_launch():
     rd = _rd()
     s = make(**CASES["one"], seed=1)
@@ -278,7 +333,7 @@ def test_refuses_before_a_launch():
         call(s, out=torch.empty(1, 1, 2, 64, dtype=torch.bfloat16, device=DEV))
 
 
-@pytest.mark.parametrize("name", ["one token each", "many rows", "48 rows"])
+@pytest.mark.parametrize("name", ["one token each", "many rows", "48 rows", "counter"])
 def test_a_wait_that_runs_out_is_reported(name):
     rd = _rd()
     s = make(**CASES[name], seed=2)

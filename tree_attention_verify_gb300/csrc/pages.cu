@@ -623,7 +623,9 @@ copy_pages_kernel(const CopyArgs a)
     }
 }
 
-cudaError_t launch_copy(CopyArgs& a, size_t max_pairs, cudaStream_t stream)
+// `dependent`: behind a kernel of the same call, which lets it start early.  The
+// first kernel of a call waits for all that the stream holds.
+cudaError_t launch_copy(CopyArgs& a, size_t max_pairs, bool dependent, cudaStream_t stream)
 {
     const long long sms = rd_device_sm_count();
     // Pieces of 16 KB keep 2 x 6 x 16 KB in flight per SM; a copy with fewer
@@ -648,7 +650,7 @@ cudaError_t launch_copy(CopyArgs& a, size_t max_pairs, cudaStream_t stream)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, copy_pages_kernel, a);
 }
 
@@ -730,7 +732,7 @@ cudaError_t rd_launch_fork_pages(const rd_page_pools& pools, int page_size, int3
     a.dst = dst;
     a.used = used;
     a.n = n;
-    return launch_copy(a, n, stream);
+    return launch_copy(a, n, true, stream);
 }
 
 // comparing every pair with every other in each CTA takes a microsecond at 256
@@ -754,7 +756,7 @@ cudaError_t rd_launch_copy_pages(const rd_page_pools& pools, const int32_t* src,
         a.src = rs;
         a.dst = rt;
     }
-    return launch_copy(a, n, stream);
+    return launch_copy(a, n, !a.few, stream);
 }
 
 cudaError_t rd_launch_compact_pages(const rd_page_pools& pools, int32_t* block_table, int R, int max_pages,
@@ -778,5 +780,5 @@ cudaError_t rd_launch_compact_pages(const rd_page_pools& pools, int32_t* block_t
     a.remap = remap;
     a.R = R;
     a.max_pages = max_pages;
-    return launch_copy(a, most, stream);
+    return launch_copy(a, most, true, stream);
 }
