@@ -124,7 +124,21 @@ def _need(t: torch.Tensor, name: str, dtype, device=None, ndim=None):
 
 # A call of a few microseconds on the GPU waits for its host side, so the binding
 # asks torch for plain integers: the current stream's handle (of a device's index),
-# the current device's index.
+# the current device's index; and looks at many tensors with one call.
+def _fine(index: int, dtype, ndim: int, *tensors) -> bool:
+    """Whether all are contiguous `ndim`-dimensional tensors of `dtype` on GPU `index`;
+    if not, `_need` says what is wrong (or takes a subclass of Tensor)."""
+    for t in tensors:
+        if (type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != index or t.dim() != ndim
+                or not t.is_contiguous()):
+            return False
+    return index >= 0
+
+
+def _index(t) -> int:
+    return t.get_device() if type(t) is torch.Tensor else -1
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -375,28 +389,33 @@ def rd_tree_attention_shared(q, k_new, v_new, k_pool, v_pool, block_table, ctx_l
     pages: group g is the requests group_offsets[g] .. group_offsets[g+1] - 1
     (int32 [n_groups+1]) and shares prefix_pages[g] pages (int32 [n_groups]);
     each prefix is read once for its group (see rd_tree_attention_shared in rd.h)."""
-    _need(q, "q", torch.bfloat16, ndim=4)
-    dev = q.device
-    for n, t in (("k_new", k_new), ("v_new", v_new), ("k_pool", k_pool), ("v_pool", v_pool)):
-        _need(t, n, torch.bfloat16, dev, ndim=4)
-    _need(block_table, "block_table", torch.int32, dev, ndim=2)
-    for n, t in (("ctx_lens", ctx_lens), ("group_offsets", group_offsets),
-                 ("prefix_pages", prefix_pages), ("packed_len", packed_len)):
-        _need(t, n, torch.int32, dev, ndim=1)
+    index = _index(q)
+    if not (_fine(index, torch.bfloat16, 4, q, k_new, v_new, k_pool, v_pool)
+            and _fine(index, torch.int32, 1, ctx_lens, group_offsets, prefix_pages, packed_len)
+            and _fine(index, torch.int32, 2, block_table)):
+        _need(q, "q", torch.bfloat16, ndim=4)
+        dev = q.device
+        for n, t in (("k_new", k_new), ("v_new", v_new), ("k_pool", k_pool), ("v_pool", v_pool)):
+            _need(t, n, torch.bfloat16, dev, ndim=4)
+        _need(block_table, "block_table", torch.int32, dev, ndim=2)
+        for n, t in (("ctx_lens", ctx_lens), ("group_offsets", group_offsets),
+                     ("prefix_pages", prefix_pages), ("packed_len", packed_len)):
+            _need(t, n, torch.int32, dev, ndim=1)
     if (not isinstance(mask, torch.Tensor) or mask.dim() != 3 or not mask.is_contiguous()
-            or mask.element_size() != 4 or mask.device != dev):
+            or mask.element_size() != 4 or mask.get_device() != q.get_device()):
         raise ValueError("mask must be a contiguous 32-bit [B, P_max, NW] tensor on q's device")
-    B, P, Hq, D = q.shape
-    Hkv = k_new.shape[2]
-    n_groups = prefix_pages.shape[0]
-    if k_new.shape != (B, P, Hkv, D) or v_new.shape != k_new.shape:
+    shape, pool, width = q.shape, k_pool.shape, block_table.shape
+    B, P, Hq, D = shape
+    num_pages, page_size, Hkv, pool_D = pool
+    mask_B, mask_P, words = mask.shape
+    n_groups = prefix_pages.numel()
+    if k_new.shape != (B, P, k_new.shape[2], D) or v_new.shape != k_new.shape:
         raise ValueError("k_new/v_new must be [B, P_max, Hkv, D]")
-    if k_pool.shape[2:] != (Hkv, D) or v_pool.shape != k_pool.shape:
+    if k_new.shape[2] != Hkv or pool_D != D or v_pool.shape != pool:
         raise ValueError("k_pool/v_pool must be [num_pages, page_size, Hkv, D]")
-    if (block_table.shape[0] != B or ctx_lens.shape[0] != B or packed_len.shape[0] != B
-            or mask.shape[0] != B or mask.shape[1] != P):
+    if width[0] != B or ctx_lens.numel() != B or packed_len.numel() != B or mask_B != B or mask_P != P:
         raise ValueError("block_table/ctx_lens/packed_len/mask do not match the batch")
-    if group_offsets.shape[0] != n_groups + 1:
+    if group_offsets.numel() != n_groups + 1:
         raise ValueError(f"group_offsets must be [{n_groups + 1}], got {tuple(group_offsets.shape)}")
     _need_status(dev_status, q)
     if out is None:
@@ -405,15 +424,15 @@ def rd_tree_attention_shared(q, k_new, v_new, k_pool, v_pool, block_table, ctx_l
         _out(out, "out", q.shape, torch.bfloat16, q)
     if workspace is None:
         workspace = _scratch(None, rd_tree_attention_shared_workspace_size(
-            B, P, Hq, Hkv, D, max_ctx, n_groups, dev), q, stream)
+            B, P, Hq, Hkv, D, max_ctx, n_groups, q.device), q, stream)
     else:
         workspace = _scratch(workspace, 0, q, stream)   # its size is checked by the call
     _run("rd_tree_attention_shared", q,
-         B, P, Hq, Hkv, D, float(scale), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool),
-         _ptr(v_pool), k_pool.shape[0], k_pool.shape[1], _ptr(block_table), block_table.shape[1],
-         _ptr(ctx_lens), int(max_ctx), n_groups, _ptr(group_offsets), _ptr(prefix_pages),
-         _ptr(packed_len), _ptr(mask), mask.shape[2], _ptr(out), _ptr(workspace),
-         workspace.numel() * workspace.element_size(), _ptr(dev_status), stream=stream)
+         B, P, Hq, Hkv, D, float(scale), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(),
+         v_pool.data_ptr(), num_pages, page_size, block_table.data_ptr(), width[1],
+         ctx_lens.data_ptr(), int(max_ctx), n_groups, group_offsets.data_ptr(), prefix_pages.data_ptr(),
+         packed_len.data_ptr(), mask.data_ptr(), words, out.data_ptr(), workspace.data_ptr(),
+         workspace.nbytes, _ptr(dev_status), stream=stream)
     return out
 
 
@@ -598,9 +617,9 @@ def _scratch(workspace, size: int, like: torch.Tensor, stream) -> torch.Tensor:
         return _new((max(16, size),), torch.uint8, like, stream)
     if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
-    if workspace.device != like.device or not workspace.is_contiguous():
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    if workspace.numel() * workspace.element_size() < size:
+    if workspace.nbytes < size:
         raise ValueError(f"workspace must have at least {size} bytes")
     return workspace
 
@@ -610,7 +629,7 @@ def _pages_scratch(workspace, size: int, like: torch.Tensor, stream):
     if workspace is None and size == 0:
         return None, 0
     workspace = _scratch(workspace, size, like, stream)
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.nbytes
 
 
 def _need_status(dev_status, like: torch.Tensor):
@@ -625,9 +644,10 @@ def _pools(k_pool, v_pool):
     [num_pages, page_size, Hkv, D] or [layers, num_pages, page_size, Hkv, D]."""
     if not isinstance(k_pool, torch.Tensor) or not isinstance(v_pool, torch.Tensor):
         raise TypeError("k_pool and v_pool must be torch tensors")
-    _need(k_pool, "k_pool", k_pool.dtype)
-    _need(v_pool, "v_pool", k_pool.dtype, k_pool.device)
     shape = k_pool.shape
+    if not _fine(_index(k_pool), k_pool.dtype, len(shape), k_pool, v_pool):
+        _need(k_pool, "k_pool", k_pool.dtype)
+        _need(v_pool, "v_pool", k_pool.dtype, k_pool.device)
     if len(shape) not in (4, 5) or v_pool.shape != shape:
         raise ValueError("k_pool/v_pool must be [num_pages, page_size, Hkv, D] or "
                          "[layers, num_pages, page_size, Hkv, D], of one shape")
@@ -637,13 +657,16 @@ def _pools(k_pool, v_pool):
 
 def _tables(block_table, row_pages, page_refs, num_pages, device):
     """(rows, entries of a row) of the page tables, checked against each other."""
-    _need(block_table, "block_table", torch.int32, device, ndim=2)
-    _need(row_pages, "row_pages", torch.int32, block_table.device, ndim=1)
-    _need(page_refs, "page_refs", torch.int32, block_table.device, ndim=1)
+    index = _index(block_table)
+    if not (_fine(index, torch.int32, 2, block_table) and _fine(index, torch.int32, 1, row_pages, page_refs)
+            and (device is None or device.index == index)):
+        _need(block_table, "block_table", torch.int32, device, ndim=2)
+        _need(row_pages, "row_pages", torch.int32, block_table.device, ndim=1)
+        _need(page_refs, "page_refs", torch.int32, block_table.device, ndim=1)
     R, max_pages = block_table.shape
-    if row_pages.shape[0] != R:
+    if row_pages.numel() != R:
         raise ValueError(f"row_pages must be [{R}], got {tuple(row_pages.shape)}")
-    if num_pages is not None and page_refs.shape[0] != num_pages:
+    if num_pages is not None and page_refs.numel() != num_pages:
         raise ValueError(f"page_refs must be [{num_pages}], got {tuple(page_refs.shape)}")
     return R, max_pages
 
@@ -673,10 +696,11 @@ def rd_fork_pages(k_pool, v_pool, block_table, row_pages, page_refs, ctx_lens, p
     rd_fork_pages in rd.h)."""
     layers, num_pages, page_size, page = _pools(k_pool, v_pool)
     R, max_pages = _tables(block_table, row_pages, page_refs, num_pages, k_pool.device)
-    for name, t in (("ctx_lens", ctx_lens), ("parent", parent), ("child", child)):
-        _need(t, name, torch.int32, k_pool.device, ndim=1)
-    n = parent.shape[0]
-    if ctx_lens.shape[0] != R or child.shape[0] != n:
+    if not _fine(_index(k_pool), torch.int32, 1, ctx_lens, parent, child):
+        for name, t in (("ctx_lens", ctx_lens), ("parent", parent), ("child", child)):
+            _need(t, name, torch.int32, k_pool.device, ndim=1)
+    n = parent.numel()
+    if ctx_lens.numel() != R or child.numel() != n:
         raise ValueError("ctx_lens must be [R], and child as long as parent")
     _need_status(dev_status, k_pool)
     workspace, size = _pages_scratch(workspace, _lib.rd_fork_pages_workspace_size(n, layers, page), k_pool, stream)
@@ -690,10 +714,11 @@ def rd_copy_pages(k_pool, v_pool, src, dst, *, workspace=None, dev_status=None, 
     """Page dst[i] = page src[i] (int32 [n]; src -1: no pair), K and V, all layers
     (see rd_copy_pages in rd.h)."""
     layers, num_pages, _, page = _pools(k_pool, v_pool)
-    _need(src, "src", torch.int32, k_pool.device, ndim=1)
-    _need(dst, "dst", torch.int32, k_pool.device, ndim=1)
-    n = src.shape[0]
-    if dst.shape[0] != n:
+    if not _fine(_index(k_pool), torch.int32, 1, src, dst):
+        _need(src, "src", torch.int32, k_pool.device, ndim=1)
+        _need(dst, "dst", torch.int32, k_pool.device, ndim=1)
+    n = src.numel()
+    if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
     _need_status(dev_status, k_pool)
     workspace, size = _pages_scratch(workspace, 8 * n if n > 256 else 0, k_pool, stream)
