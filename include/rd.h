@@ -226,9 +226,9 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
  *              initial contents; query it for each shape (a larger batch may need
  *              less) and with the device current that the call runs on
  * Everything else as rd_tree_attention_paged, its limits among them; page_size is a
- * multiple of 64, and work that does not count in 31 bits (B Hkv max_ctx / 32, and an
- * eighth of B P_max Hq max_ctx / 512 or n_groups Hkv max_ctx / 2) RD_ERR_UNSUPPORTED.  K and V of
- * the packed drafts must be finite (an infinity or NaN in a live draft's V can
+ * multiple of 64, and a batch whose work does not count in 31 bits (above about
+ * (B P_max Hq / 256 + n_groups Hkv) max_ctx / 16, or 5 B Hkv max_ctx / 32) is
+ * RD_ERR_UNSUPPORTED.  K and V of the packed drafts must be finite (an infinity or NaN in a live draft's V can
  * reach rows that do not see that draft); what lies behind a context's end in its
  * last page, and behind packed_len, may hold anything.
  */

@@ -136,9 +136,18 @@ CASES = {
                           pages=[i % 3 for i in range(1060)], suffix=40),
     "1500 requests": dict(B=1500, W=1, L=2, Hq=2, Hkv=1, D=64, page=64, offsets=list(range(0, 800, 2)) + list(range(800, 1501)),
                           pages=[(i + 1) % 2 for i in range(1100)], suffix=50),
-    # more than 64 rows per kv head: units enough to be taken whole, more requests than a table of them holds
+    # more than 64 rows per kv head, units enough to be taken whole; more requests than a table of them holds
     "80 rows, whole units": dict(B=80, W=5, L=4, Hq=32, Hkv=8, D=128, page=64, offsets=[0, 30, 80], pages=[3, 1], suffix=100),
     "72 rows, 600 requests": dict(B=600, W=3, L=4, Hq=6, Hkv=1, D=64, page=64, offsets=[0, 600], pages=[2], suffix=70),
+    # two and three units of up to 64 rows a kv head, the last one short or empty
+    "160 rows": dict(B=6, W=8, L=5, Hq=8, Hkv=2, D=128, page=64, offsets=[0, 4, 6], pages=[5, 2], suffix=300),
+    "2 x 33 heads": dict(B=3, W=2, L=1, Hq=66, Hkv=2, D=64, page=64, offsets=[0, 3], pages=[2], suffix=90),
+    "192 rows, whole units": dict(B=70, W=8, L=8, Hq=24, Hkv=8, D=64, page=64, offsets=[0, 50], pages=[3], suffix=60),
+    "160 rows, long own contexts": dict(B=2, W=8, L=5, Hq=8, Hkv=2, D=64, page=64, offsets=[0, 2], pages=[2], suffix=5000),
+    "100 rows, long own contexts": dict(B=2, W=5, L=5, Hq=8, Hkv=2, D=128, page=64, offsets=[0, 2], pages=[2], suffix=5000),
+    "128 rows": dict(B=9, W=8, L=4, Hq=8, Hkv=2, D=128, page=64, offsets=[0, 2, 9], pages=[9, 3], suffix=200),
+    "120 rows, whole units": dict(B=80, W=5, L=1, Hq=192, Hkv=8, D=64, page=64, offsets=[0, 50], pages=[3], suffix=60),
+    "150 rows, 600 requests": dict(B=600, W=5, L=5, Hq=6, Hkv=1, D=64, page=64, offsets=[0, 600], pages=[2], suffix=70),
     # one of many units far longer than the others
     "counter, long own contexts": dict(B=160, W=1, L=3, Hq=8, Hkv=8, D=64, page=64, offsets=[0, 150], pages=[1],
                                        suffix=2500),

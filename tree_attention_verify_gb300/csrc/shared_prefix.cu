@@ -12,7 +12,7 @@
 //           and the table that divides the prefix work over the CTAs;
 //   prefix  (below) fp32 partials of every live row over its group's prefix;
 //   suffix  partials of every row over its request's own context and drafts
-//           (shared_suffix.cu for up to 64 rows per kv head, else the shared-prefix
+//           (shared_suffix.cu for up to 128 rows per kv head, else the shared-prefix
 //           variant of attention_tc.cu);
 //   merge   the formula above, rounded once to bf16; zeros in padded rows.  With many
 //           units the suffix kernel ends each in this way itself.
@@ -102,6 +102,7 @@ struct UnitCost {
 struct PlanArgs {
     int B, P_max, Hkv, G, page_size, max_pages, max_ctx, n_groups;
     int suffix_chunk;          // positions of a suffix chunk (0: the tcgen05 kernel divides by itself)
+    int suffix_nodes;          // nodes of a suffix unit
     const int32_t* lens;
     const int32_t* ctx_lens;
     const int32_t* group_offsets;
@@ -189,7 +190,8 @@ plan_kernel(const PlanArgs a)
             a.p.gid[b] = my_gid = g;
             n = g >= 0 ? len : 0;
             if (a.suffix_chunk > 0 && len > 0)
-                suf = a.Hkv * ((ctx - skip + a.suffix_chunk - 1) / a.suffix_chunk + (len + a.suffix_chunk - 1) / a.suffix_chunk);
+                suf = a.Hkv * ((len + a.suffix_nodes - 1) / a.suffix_nodes) *
+                      ((ctx - skip + a.suffix_chunk - 1) / a.suffix_chunk + (len + a.suffix_chunk - 1) / a.suffix_chunk);
         }
         int total;
         const int at = carry + cta_scan(n, warp_sum, total);
@@ -984,27 +986,36 @@ cudaError_t launch_merge(dim3 grid, cudaStream_t stream, MergeArgs& a)
                             stream, args);
 }
 
-// Which kernel takes the part behind the prefix.  Up to 64 rows per kv head the one
-// of shared_suffix.cu, which reads each key once for all of them; with more rows
-// the tcgen05 kernel, whose tiles hold 128.
+// Which kernel takes the part behind the prefix.  Up to 128 rows per kv head (and 64
+// nodes) the one of shared_suffix.cu, in units of up to 64 rows that read each key
+// once; with more the tcgen05 kernel, whose tiles hold 128.  The whole call, 64
+// requests of 8 kv heads behind 2,048 shared positions, either way: 96 rows and up to
+// 300 positions each 70 against 88 us, up to 4,000 169 against 180; but 160 rows and up
+// to 3,000 positions 283 against 185 (to 300: 84 against 102).  16 requests of 80 rows,
+// D 64, to 3,000: 52 against 63; four of 128 rows, to 8,000: 44 against 43.
+constexpr int kSuffixMaxRows = 128;
+constexpr int kSuffixMaxNodes = 64;        // (two mask words a row)
 struct SuffixChoice {
     bool few_rows;
     bool by_unit;             // few_rows: CTAs take whole units off a counter and write the output
     bool table;               // units have an entry in the table of pieces
-    int grid, slot_rows, tiles;
+    int grid, slot_rows, tiles;   // tiles: units of a (request, kv head)
+    int nodes;                // few_rows: of a unit
     rd_attn_plan plan;        // tcgen05
 };
 SuffixChoice choose_suffix(int B, int P_max, int Hq, int Hkv, int D, int max_ctx)
 {
     SuffixChoice s;
-    const int rows = P_max * (Hq / Hkv);
-    s.few_rows = rows <= kSuffixMaxRows;
+    const int G = Hq / Hkv;
+    s.few_rows = P_max <= kSuffixMaxNodes && G <= kSuffixRows && P_max * G <= kSuffixMaxRows;
+    s.nodes = s.few_rows ? rd_suffix_nodes(P_max, G) : P_max;
+    const int rows = s.nodes * G;
     s.plan = rd_attn_make_plan(B, P_max, Hq, Hkv, D, max_ctx);
     s.grid = s.few_rows ? rd_suffix_grid(rows) : s.plan.grid;
-    s.by_unit = s.few_rows && rd_suffix_by_unit(B, Hkv, s.grid);
+    s.tiles = s.few_rows ? (P_max + s.nodes - 1) / s.nodes : s.plan.tiles;
+    s.by_unit = s.few_rows && rd_suffix_by_unit((long long)B * Hkv * s.tiles, s.grid);
     s.table = s.few_rows ? !s.by_unit : s.plan.stream_k;
-    s.slot_rows = s.few_rows ? kSuffixMaxRows : kM;
-    s.tiles = s.few_rows ? 1 : s.plan.tiles;
+    s.slot_rows = s.few_rows ? rows : kM;
     return s;
 }
 
@@ -1091,7 +1102,8 @@ cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D,
     pa.max_pages = paged.max_pages;
     pa.max_ctx = max_ctx;
     pa.n_groups = n_groups;
-    pa.suffix_chunk = suffix.few_rows && !suffix.by_unit ? rd_suffix_chunk(rd_suffix_row_warps(P_max * pa.G)) : 0;
+    pa.suffix_chunk = suffix.few_rows && !suffix.by_unit ? rd_suffix_chunk(rd_suffix_row_warps(suffix.nodes * pa.G)) : 0;
+    pa.suffix_nodes = suffix.nodes;
     pa.lens = packed_len;
     pa.ctx_lens = paged.ctx_lens;
     pa.group_offsets = group_offsets;

@@ -122,7 +122,9 @@ __device__ __forceinline__ Pieces pieces_of(int2 unit, const Plan& p, int h, int
 }
 
 // ---- the suffix kernel for few rows per kv head (shared_suffix.cu)
-constexpr int kSuffixMaxRows = 64;
+constexpr int kSuffixRows = 64;            // of a unit at most
+// nodes of a unit (all G heads of each)
+__host__ __device__ constexpr int rd_suffix_nodes(int P_max, int G) { return P_max * G <= kSuffixRows ? P_max : kSuffixRows / G; }
 // chunks per CTA at least: 1, 2 and 4 make 4 requests x 32 heads x 20 rows 29.1, 28.3
 // and 30.8 us
 constexpr uint32_t kSuffixMinChunks = 2;
@@ -154,7 +156,7 @@ inline cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, s
 }  // namespace rdshared
 
 int rd_suffix_grid(int rows);
-bool rd_suffix_by_unit(int B, int Hkv, int grid);
+bool rd_suffix_by_unit(long long units, int grid);
 cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, int Hq, int Hkv, int D,
                                     float scale_log2, const void* q, const void* k_new, const void* v_new,
                                     const void* k_pool, const void* v_pool, const rd_paged_kv& paged,

@@ -1,15 +1,15 @@
-// The part of rd_tree_attention_shared behind the prefix, for up to 64 query rows
+// The part of rd_tree_attention_shared behind the prefix, for up to 128 query rows
 // per kv head (P_max G): fp32 partials of every live row over its request's own
 // context and its drafts.
 //
-// Behind a shared prompt a request has a few hundred positions of its own, so a
-// unit (request, kv head) is a handful of chunks, and what bounds it is not bytes
-// or products but the chain of steps per unit.  The tcgen05 kernel pays that chain
+// Unit = (request, kv head, up to 64 rows: as many nodes, with all their G heads, as
+// fit).  Behind a shared prompt a request has a few hundred positions of its own, so a
+// unit is a handful of chunks, and what bounds it is not bytes or products but the chain of steps per unit.  The tcgen05 kernel pays that chain
 // across four roles (64 positions take it 2,500 to 4,000 cycles behind a prefix, its
 // epilogue 4,000 more): 120 us at 64 requests x 40 heads x 150 positions and 30
 // rows.  Here a warp holds 16 rows' queries, scores, statistics and sums in its own
 // registers (mma.sync m16n8k16), so that nothing waits on another role but for
-// loads, and three CTAs share an SM.  With 64 rows or fewer the products stay far
+// loads, and two or three CTAs share an SM.  With 64 rows or fewer the products stay
 // under what mma.sync can do at the rate the keys arrive.
 //
 // Warp roles: one producer (TMA: a unit's queries and what the others need to know
@@ -22,8 +22,8 @@
 // prefix, which come through the same ring like further chunks, and with the output
 // rows: no partials of its own leave the SM, and no merge follows.  At 64 requests x
 // 40 heads that takes 73 us (355 MB from and to HBM, 4.9 TB/s) where this kernel and
-// the merge took 48 + 36.  With few units, their chunks form
-// one sequence that the CTAs take in equal ranges, and all partials go to the merge.
+// the merge took 48 + 36.  With few units, their chunks form one sequence that the
+// CTAs take in equal ranges, and all partials go to the merge.
 // Every wait is bounded; on expiry the CTA records RD_DEV_TIMEOUT, drains its
 // copies and returns.
 #include <cuda.h>
@@ -72,6 +72,7 @@ template <int D, int NW, int KS> struct SCfg {
 
 struct SuffixArgs {
     int B, P_max, Hq, Hkv, G, page_size, max_pages, num_pages, mask_words;
+    int nodes, blocks;         // of a unit at most; units of a (request, kv head)
     float scale_log2;
     const int32_t* block_table;
     const int32_t* ctx_lens;
@@ -86,7 +87,7 @@ struct SuffixArgs {
 // What the compute warps need to know of a unit (or piece); n = 0: no more, -1: a
 // skipped request's rows (zeros).
 struct Unit {
-    int b, h, c_first, n, C, Pb, slot;     // slot -1: a whole unit
+    int b, h, n0, c_first, n, C, Pb, slot; // n0: first node; Pb: the request's nodes; slot -1: a whole unit
 };
 
 // What a ring entry holds.
@@ -220,15 +221,16 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 skip = __ldcg(a.p.skip + b);
                 ctx = __ldg(a.ctx_lens + b) - skip;
             };
-            uint32_t next = 0u, nb = 0u;                  // ranges: the next request's first chunk, chunks of a unit
+            // ranges: the next request's first chunk, chunks of a unit, units of a kv head
+            uint32_t next = 0u, nb = 0u, live = 1u;
             bool fresh = true, prefix_written = false;
             // by unit: what is read of a unit comes a unit ahead, its number two ahead
-            const int units = a.B * a.Hkv;
+            const int per = a.Hkv * a.blocks, units = a.B * per;
             int unit = units, after = units, n_len = 0, n_ctx_len = 0, n_skip = 0;
             int4 n_req = make_int4(-1, 0, 0, 0);
             auto read_ahead = [&]() {
                 if (unit >= units) return;
-                const int q = unit / a.Hkv;
+                const int q = unit / per;
                 n_len = __ldcg(a.p.eff_len + q);
                 n_skip = __ldcg(a.p.skip + q);
                 n_ctx_len = __ldg(a.ctx_lens + q);
@@ -240,13 +242,14 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 read_ahead();
             }
             while (ok && !*abort) {
-                int h = 0, c0 = 0, n = 0, slot = -1;
+                int h = 0, n0 = 0, c0 = 0, n = 0, slot = -1;
                 uint32_t stop = 0u;
                 int4 req = make_int4(-1, 0, 0, 0);
                 if (a.by_unit) {
                     if (unit < units) {
-                        b = unit / a.Hkv;
-                        h = unit % a.Hkv;
+                        b = unit / per;
+                        h = unit % per / a.blocks;
+                        n0 = unit % a.blocks * a.nodes;
                         len = n_len;
                         skip = n_skip;
                         ctx = n_ctx_len - skip;
@@ -254,7 +257,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                         unit = after;
                         if (after < units) after = atomicAdd(a.p.suf_next, 1);
                         read_ahead();
-                        n = len > 0 ? (ctx + CH - 1) / CH + (len + CH - 1) / CH : -1;
+                        n = len > n0 ? (ctx + CH - 1) / CH + (len + CH - 1) / CH : -1;
                     }
                 } else if (x < end) {
                     while (fresh || x >= next) {          // on to the request that holds chunk x
@@ -265,16 +268,19 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                         fresh = false;
                         next = __ldcg(a.p.suf_first + b + 1);
                         request();
-                        nb = (next - base) / (uint32_t)a.Hkv;
+                        live = max(1u, (uint32_t)((len + a.nodes - 1) / a.nodes));
+                        nb = (next - base) / ((uint32_t)a.Hkv * live);
                     }
-                    h = (int)((x - base) / nb);
-                    const uint32_t u0 = base + (uint32_t)h * nb;
+                    const uint32_t at = (x - base) / nb, u0 = base + at * nb;
+                    h = (int)(at / live);
+                    const int blk = (int)(at % live);
+                    n0 = blk * a.nodes;
                     c0 = (int)(x - u0);
                     stop = min(u0 + nb, end);
                     n = (int)(stop - x);
                     slot = (uint32_t)n == nb ? -1 : 2 * (int)blockIdx.x + (c0 == 0 && u0 > start ? 1 : 0);
                     if (c0 == 0)                          // the unit starts here: name its pieces
-                        a.p.suffix.unit[b * a.Hkv + h] =
+                        a.p.suffix.unit[(blk * a.B + b) * a.Hkv + h] =
                             make_int2(slot < 0 ? 1 : (int)(range_of(W, nc, u0 + nb - 1) - blockIdx.x) + 1, slot);
                 }
                 if (it > 0 && !mbar_wait(&bar.q_empty, (it - 1) & 1, abort, kWaitBudget)) { ok = false; break; }
@@ -283,17 +289,17 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                     mbar_arrive(&bar.q_full);
                     break;
                 }
-                bar.unit = Unit{b, h, c0, n, ctx, len, slot};
+                bar.unit = Unit{b, h, n0, c0, n, ctx, len, slot};
                 if (n < 0) {
                     mbar_arrive(&bar.q_full);
                     ++it;
                     continue;
                 }
-                mbar_arrive_expect_tx(&bar.q_full, a.P_max * a.G * D * 2);
+                mbar_arrive_expect_tx(&bar.q_full, a.nodes * a.G * D * 2);
 #pragma unroll
                 for (int db = 0; db < C::kDB; ++db)
                     tma_load_3d(smem + C::kQOff + db * (C::kQRows * 128), &map_q, &bar.q_full, db * 64, h * a.G,
-                                b * a.P_max);
+                                b * a.P_max + n0);
                 ++it;
                 // the next ring entry, free; false: the wait ran out
                 auto stage = [&](int& st) -> bool {
@@ -338,17 +344,18 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 // where the rows cross one's end), half of the columns at a time
                 if (!prefix_written) asm volatile("griddepcontrol.wait;" ::: "memory");
                 prefix_written = true;
-                const int rows = len * a.G;
+                const int rows = min(len - n0, a.nodes) * a.G;
                 for (int r0 = 0; ok && r0 < rows;) {
-                    const int at = req.z + r0, r = at % kUnitRows, r1 = min(rows, r0 + kUnitRows - r);
+                    const int at = req.z + n0 * a.G + r0, r = at % kUnitRows, r1 = min(rows, r0 + kUnitRows - r);
                     const int2 table = __ldcg(a.p.unit + req.x + h * req.y + at / kUnitRows);
                     const int pieces = pieces_in(table, a.p.grid);
                     const bool whole = pieces == 1;
+                    const int row = req.w + n0 * a.G + r0;                         // compact
                     for (int k = 0; ok && k < pieces; ++k) {
                         const int sl = k == 0 ? table.y : 2 * (table.y / 2 + k);       // its slot
                         const CUtensorMap* map = whole ? &map_rows : &map_part;
-                        const int px = (whole ? req.w + r0 : r) * 4, py = (whole ? h : sl) * (D / 4);
-                        const float2* ml = whole ? a.p.rows_ml + (size_t)h * a.p.rows_cap + req.w + r0
+                        const int px = (whole ? row : r) * 4, py = (whole ? h : sl) * (D / 4);
+                        const float2* ml = whole ? a.p.rows_ml + (size_t)h * a.p.rows_cap + row
                                                  : a.p.part_ml + (size_t)sl * kUnitRows + r;
                         const int shift = (int)((reinterpret_cast<uintptr_t>(ml) >> 3) & 1);   // copies begin at 16 bytes
                         const uint32_t ml_bytes = (uint32_t)((r1 - r0 + shift + 1) & ~1) * 8u;
@@ -394,7 +401,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
             if (!warp_wait(&bar.q_full, it & 1, abort, kWaitBudget)) { ok = false; break; }
             const Unit u = bar.unit;
             if (u.n == 0) break;
-            const int live = u.Pb * a.G;                  // rows of the unit
+            const int live = max(0, min(u.Pb - u.n0, a.nodes)) * a.G;     // rows of the unit
             const bool dead = rw * 16 >= live;            // none of this warp's
             uint32_t qf[D / 16][4];
             if (!dead) {
@@ -413,7 +420,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
                     mw[i][w] = row < live && w < a.mask_words
-                        ? __ldg(a.mask + ((size_t)u.b * a.P_max + row / a.G) * a.mask_words + w) : 0u;
+                        ? __ldg(a.mask + ((size_t)u.b * a.P_max + u.n0 + row / a.G) * a.mask_words + w) : 0u;
             }
             float o[D / 8][4];
 #pragma unroll
@@ -651,7 +658,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                     const int row = rw * 16 + gr + 8 * i;
                     const float inv = row < live && l[i] != 0.f ? 1.f / l[i] : 0.f;
                     uint4* dst = reinterpret_cast<uint4*>(
-                        a.o + (((size_t)u.b * a.P_max + row / a.G) * a.Hq + u.h * a.G + row % a.G) * D);
+                        a.o + (((size_t)u.b * a.P_max + u.n0 + row / a.G) * a.Hq + u.h * a.G + row % a.G) * D);
 #pragma unroll
                     for (int j0 = 0; j0 < D / 8; j0 += 4) {
                         uint32_t v[4];
@@ -659,7 +666,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                         for (int k = 0; k < 4; ++k)
                             v[k] = row < live ? pack_bf16(o[j0 + k][2 * i] * inv, o[j0 + k][2 * i + 1] * inv) : 0u;
                         swap4(v, tc);
-                        if (row < a.P_max * a.G) dst[j0 + tc] = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (row < min(a.P_max - u.n0, a.nodes) * a.G) dst[j0 + tc] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
                 continue;
@@ -675,7 +682,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
             for (int i = 0; i < 2; ++i) {
                 const int row = rw * 16 + gr + 8 * i;
                 if (row >= live) continue;
-                const size_t at = whole ? (size_t)u.b * a.P_max * a.G + row : (size_t)row;
+                const size_t at = whole ? ((size_t)u.b * a.P_max + u.n0) * a.G + row : (size_t)row;
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j)           // columns 8 j + 2 tc, + 1
                     *reinterpret_cast<float2*>(dst + (((size_t)(2 * j + (tc >> 1))) * stride + at) * 4 + (tc & 1) * 2) =
@@ -734,7 +741,7 @@ cudaError_t launch(int grid, cudaStream_t stream, SuffixArgs& a, CUtensorMap* m)
 template <int D>
 cudaError_t launch_rows(int grid, cudaStream_t stream, SuffixArgs& a, CUtensorMap* m)
 {
-    switch (rd_suffix_row_warps(a.P_max * a.G)) {
+    switch (rd_suffix_row_warps(a.nodes * a.G)) {
     case 1: return launch<D, 1, 4>(grid, stream, a, m);
     case 2: return launch<D, 2, 2>(grid, stream, a, m);
     case 3: return launch<D, 3, 1>(grid, stream, a, m);
@@ -747,7 +754,7 @@ cudaError_t launch_rows(int grid, cudaStream_t stream, SuffixArgs& a, CUtensorMa
 // Whole units off a counter when they are many enough to level out: 64 and 128 units
 // (one token of 8 requests, 20 nodes of 4) make the whole call 33 and 42 us that way,
 // 23 and 28 in ranges; 2,560 units 262 us against 277 with partials and a merge.
-bool rd_suffix_by_unit(int B, int Hkv, int grid) { return (long long)B * Hkv >= 4LL * grid; }
+bool rd_suffix_by_unit(long long units, int grid) { return units >= 4LL * grid; }
 
 int rd_suffix_grid(int rows) { return rd_device_sm_count() * rd_suffix_ctas(rd_suffix_row_warps(rows)); }
 
@@ -776,13 +783,15 @@ cudaError_t rd_launch_shared_suffix(const rdshared::Plan& p, int B, int P_max, i
     a.by_unit = by_unit;
     a.status = dev_status;
     a.stall_budget = rd_attention_stall_budget();
-    const int rows = P_max * a.G, ch = rd_suffix_chunk(rd_suffix_row_warps(rows));
+    a.nodes = rd_suffix_nodes(P_max, a.G);
+    a.blocks = (P_max + a.nodes - 1) / a.nodes;
+    const int rows = a.nodes * a.G, ch = rd_suffix_chunk(rd_suffix_row_warps(rows));
     const int64_t pool_rows = (int64_t)paged.num_pages * paged.page_size, new_rows = (int64_t)B * P_max;
     CUtensorMap m[7];
     const int box = rd_suffix_row_warps(rows) * 16;
     if (!make_map(&m[0], k_pool, pool_rows, Hkv, D, 1, ch) || !make_map(&m[1], v_pool, pool_rows, Hkv, D, 1, ch) ||
         !make_map(&m[2], k_new, new_rows, Hkv, D, 1, ch) || !make_map(&m[3], v_new, new_rows, Hkv, D, 1, ch) ||
-        !make_map(&m[4], q, new_rows, Hq, D, a.G, P_max))
+        !make_map(&m[4], q, new_rows, Hq, D, a.G, a.nodes))
         return cudaErrorInvalidValue;
     if (by_unit) {
         if (!make_partial_map(&m[5], p.rows, p.rows_cap, (size_t)Hkv * (D / 4), box, D) ||
