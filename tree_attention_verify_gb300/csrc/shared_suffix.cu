@@ -87,7 +87,9 @@ struct SuffixArgs {
 // What the compute warps need to know of a unit (or piece); n = 0: no more, -1: a
 // skipped request's rows (zeros).
 struct Unit {
-    int b, h, n0, c_first, n, C, Pb, slot; // n0: first node; Pb: the request's nodes; slot -1: a whole unit
+    int row0, h;               // first node b P_max + n0
+    int rows;                  // live rows, and << 16 those with padded nodes
+    int n, C, Pb, slot;        // Pb: the request's nodes; slot -1: a whole unit
 };
 
 // What a ring entry holds.
@@ -289,7 +291,8 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                     mbar_arrive(&bar.q_full);
                     break;
                 }
-                bar.unit = Unit{b, h, n0, c0, n, ctx, len, slot};
+                const int live_rows = max(0, min(len - n0, a.nodes)) * a.G;
+                bar.unit = Unit{b * a.P_max + n0, h, live_rows | min(a.P_max - n0, a.nodes) * a.G << 16, n, ctx, len, slot};
                 if (n < 0) {
                     mbar_arrive(&bar.q_full);
                     ++it;
@@ -344,9 +347,8 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 // where the rows cross one's end), half of the columns at a time
                 if (!prefix_written) asm volatile("griddepcontrol.wait;" ::: "memory");
                 prefix_written = true;
-                const int rows = min(len - n0, a.nodes) * a.G;
-                for (int r0 = 0; ok && r0 < rows;) {
-                    const int at = req.z + n0 * a.G + r0, r = at % kUnitRows, r1 = min(rows, r0 + kUnitRows - r);
+                for (int r0 = 0; ok && r0 < live_rows;) {
+                    const int at = req.z + n0 * a.G + r0, r = at % kUnitRows, r1 = min(live_rows, r0 + kUnitRows - r);
                     const int2 table = __ldcg(a.p.unit + req.x + h * req.y + at / kUnitRows);
                     const int pieces = pieces_in(table, a.p.grid);
                     const bool whole = pieces == 1;
@@ -401,7 +403,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
             if (!warp_wait(&bar.q_full, it & 1, abort, kWaitBudget)) { ok = false; break; }
             const Unit u = bar.unit;
             if (u.n == 0) break;
-            const int live = max(0, min(u.Pb - u.n0, a.nodes)) * a.G;     // rows of the unit
+            const int live = u.rows & 0xffff;             // rows of the unit
             const bool dead = rw * 16 >= live;            // none of this warp's
             uint32_t qf[D / 16][4];
             if (!dead) {
@@ -420,7 +422,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
                     mw[i][w] = row < live && w < a.mask_words
-                        ? __ldg(a.mask + ((size_t)u.b * a.P_max + u.n0 + row / a.G) * a.mask_words + w) : 0u;
+                        ? __ldg(a.mask + (size_t)(u.row0 + row / a.G) * a.mask_words + w) : 0u;
             }
             float o[D / 8][4];
 #pragma unroll
@@ -658,7 +660,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                     const int row = rw * 16 + gr + 8 * i;
                     const float inv = row < live && l[i] != 0.f ? 1.f / l[i] : 0.f;
                     uint4* dst = reinterpret_cast<uint4*>(
-                        a.o + (((size_t)u.b * a.P_max + u.n0 + row / a.G) * a.Hq + u.h * a.G + row % a.G) * D);
+                        a.o + ((size_t)(u.row0 + row / a.G) * a.Hq + u.h * a.G + row % a.G) * D);
 #pragma unroll
                     for (int j0 = 0; j0 < D / 8; j0 += 4) {
                         uint32_t v[4];
@@ -666,7 +668,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                         for (int k = 0; k < 4; ++k)
                             v[k] = row < live ? pack_bf16(o[j0 + k][2 * i] * inv, o[j0 + k][2 * i + 1] * inv) : 0u;
                         swap4(v, tc);
-                        if (row < min(a.P_max - u.n0, a.nodes) * a.G) dst[j0 + tc] = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (row < u.rows >> 16) dst[j0 + tc] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
                 continue;
@@ -682,7 +684,7 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
             for (int i = 0; i < 2; ++i) {
                 const int row = rw * 16 + gr + 8 * i;
                 if (row >= live) continue;
-                const size_t at = whole ? ((size_t)u.b * a.P_max + u.n0) * a.G + row : (size_t)row;
+                const size_t at = whole ? (size_t)u.row0 * a.G + row : (size_t)row;
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j)           // columns 8 j + 2 tc, + 1
                     *reinterpret_cast<float2*>(dst + (((size_t)(2 * j + (tc >> 1))) * stride + at) * 4 + (tc & 1) * 2) =
