@@ -487,54 +487,16 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 }
                 return true;
             };
-            bool finished = false;
             const int n_ctx = (u.C + CH - 1) / CH;
-            for (bool last = u.n < 0; !last; ++g) {
+            bool last = u.n < 0;
+            for (; !last; ++g) {                          // the unit's own chunks
                 const int st = (int)(g % C::kStages);
                 if (!warp_wait(&bar.full[st], (g / C::kStages) & 1, abort, kWaitBudget)) { ok = false; break; }
                 const Entry en = bar.entry[st];
+                if (en.kind != 0) break;
                 last = en.last != 0;
                 const int c = en.c;
-                if (en.kind != 0) {
-                    if (!finished && !finish()) { ok = false; break; }
-                    finished = true;
-                    if (en.kind == 1 && ks == 0 && !dead) {
-                        const int rows = en.r1 - en.r0;
-                        if (en.half == 0) {
-                            const float2* ml = reinterpret_cast<const float2*>(smem + C::kMlOff) + st * C::kMlRows + en.shift;
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int at = rw * 16 + gr + 8 * i - en.r0;
-                                const float2 x = at >= 0 && at < rows ? ml[at] : make_float2(-INFINITY, 0.f);
-                                const float M = fmaxf(m[i], x.x), base = M == -INFINITY ? 0.f : M;
-                                const float f = fast_exp2(m[i] - base);
-                                wp[i] = fast_exp2(x.x - base);
-                                l[i] = l[i] * f + x.y * wp[i];
-                                m[i] = M;
-#pragma unroll
-                                for (int j = 0; j < D / 8; ++j) {
-                                    o[j][2 * i] *= f;
-                                    o[j][2 * i + 1] *= f;
-                                }
-                            }
-                        }
-                        // columns [half D/2, ..): float4 [D / 8][kQRows]
-                        const unsigned char* part = smem + st * C::kStageBytes;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int at = rw * 16 + gr + 8 * i - en.r0;
-                            if (at < 0 || at >= rows) continue;
-#pragma unroll
-                            for (int j = 0; j < D / 8; ++j) {
-                                if ((j >= D / 16) != (en.half == 1)) continue;
-                                const int c4 = 2 * (j % (D / 16)) + (tc >> 1);
-                                const float2 y = *reinterpret_cast<const float2*>(part + (c4 * C::kQRows + at) * 16 + (tc & 1) * 8);
-                                o[j][2 * i] += y.x * wp[i];
-                                o[j][2 * i + 1] += y.y * wp[i];
-                            }
-                        }
-                    }
-                } else if (!dead) {
+                if (!dead) {
                     const uint32_t kb = smem_u + st * C::kStageBytes, vb = kb + C::kKBytes;
                     float s[C::kKw / 8][4];
 #pragma unroll
@@ -650,7 +612,52 @@ suffix_kernel(const SuffixArgs a, const __grid_constant__ CUtensorMap map_kc,
                 if (lane == 0) mbar_arrive(&bar.empty[st]);
             }
             if (!ok) break;
-            if (!finished && u.n > 0 && !finish()) { ok = false; break; }
+            if (u.n > 0 && !finish()) { ok = false; break; }
+            for (; !last; ++g) {                          // its rows' partials over the prefix
+                const int st = (int)(g % C::kStages);
+                if (!warp_wait(&bar.full[st], (g / C::kStages) & 1, abort, kWaitBudget)) { ok = false; break; }
+                const Entry en = bar.entry[st];
+                last = en.last != 0;
+                if (en.kind == 1 && ks == 0 && !dead) {
+                    const int rows = en.r1 - en.r0;
+                    if (en.half == 0) {
+                        const float2* ml = reinterpret_cast<const float2*>(smem + C::kMlOff) + st * C::kMlRows + en.shift;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = rw * 16 + gr + 8 * i - en.r0;
+                            const float2 x = at >= 0 && at < rows ? ml[at] : make_float2(-INFINITY, 0.f);
+                            const float M = fmaxf(m[i], x.x), base = M == -INFINITY ? 0.f : M;
+                            const float f = fast_exp2(m[i] - base);
+                            wp[i] = fast_exp2(x.x - base);
+                            l[i] = l[i] * f + x.y * wp[i];
+                            m[i] = M;
+#pragma unroll
+                            for (int j = 0; j < D / 8; ++j) {
+                                o[j][2 * i] *= f;
+                                o[j][2 * i + 1] *= f;
+                            }
+                        }
+                    }
+                    // columns [half D/2, ..): float4 [D / 8][kQRows]
+                    const unsigned char* part = smem + st * C::kStageBytes;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = rw * 16 + gr + 8 * i - en.r0;
+                        if (at < 0 || at >= rows) continue;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            if ((j >= D / 16) != (en.half == 1)) continue;
+                            const int c4 = 2 * (j % (D / 16)) + (tc >> 1);
+                            const float2 y = *reinterpret_cast<const float2*>(part + (c4 * C::kQRows + at) * 16 + (tc & 1) * 8);
+                            o[j][2 * i] += y.x * wp[i];
+                            o[j][2 * i + 1] += y.y * wp[i];
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.empty[st]);
+            }
+            if (!ok) break;
             if (ks > 0) continue;
             if (a.by_unit) {
                 // ---- output rows, 16 bytes a lane (four lanes swap their pairs of columns);
