@@ -219,17 +219,18 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
  *              prefix pages outside [0, max_pages] or longer than max_ctx
  *              RD_DEV_BAD_LENGTH: nobody shares then (that group does not), and the outputs
  *              are the same.  A request shorter than its group's prefix sets
- *              RD_DEV_BAD_LENGTH and is skipped (zero rows).  Rows of a group
- *              that name different prefix pages set RD_DEV_BAD_INDEX; its first
- *              request's pages are read for all.
+ *              RD_DEV_BAD_LENGTH and is skipped (zero rows).  One without drafts
+ *              (packed_len 0) may be shorter, and its table row is not read.  Of
+ *              the others, rows of a group that name different prefix pages set
+ *              RD_DEV_BAD_INDEX; its first such request's pages are read for all.
  * workspace    rd_tree_attention_shared_workspace_size() bytes, 16-byte aligned, no
  *              initial contents; query it for each shape (a larger batch may need
  *              less) and with the device current that the call runs on
  * Everything else as rd_tree_attention_paged, its limits among them; page_size is a
  * multiple of 64, and a batch whose work does not count in 31 bits (above about
  * (B P_max Hq / 256 + n_groups Hkv) max_ctx / 16, or 5 B Hkv max_ctx / 32) is
- * RD_ERR_UNSUPPORTED.  K and V of the packed drafts must be finite (an infinity or NaN in a live draft's V can
- * reach rows that do not see that draft); what lies behind a context's end in its
+ * RD_ERR_UNSUPPORTED.  K and V of the packed drafts must be finite (an infinity or
+ * NaN in a live draft's V can reach rows that do not see that draft); what lies behind a context's end in its
  * last page, and behind packed_len, may hold anything.
  */
 size_t rd_tree_attention_shared_workspace_size(int B, int P_max, int Hq, int Hkv, int D,

@@ -240,6 +240,26 @@ def test_wrong_requests_are_skipped():
     assert st.item() == rd.DEV_BAD_INDEX
 
 
+@pytest.mark.parametrize("name", ["half chunks", "groups of five heads", "counter", "many rows", "192 rows, whole units",
+                                  "1100 requests"])
+def test_padded_requests_in_a_group(name):
+    """Finished requests stay in their groups: no drafts, no context, no pages.  The
+    others' outputs and the status do not depend on them, a group's first among them."""
+    s = make(**CASES[name], seed=13)
+    for n in ("ctx", "lens", "table"):
+        s[n] = s[n].copy()
+    o = s["offsets"]
+    for b in {int(o[0]), int(o[1]) - 1, int(o[-2])}:
+        s["ctx"][b] = s["lens"][b] = 0
+        s["table"][b] = -1
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = call(s, st)
+    assert st.item() == 0
+    check(out, s)
+    s["lens"][:] = 0                                   # and nobody has any
+    assert not call(s, st).any() and st.item() == 0
+
+
 def test_equals_the_paged_call_without_groups():
     rd = _rd()
     s = make(**CASES["half chunks"], seed=11)

@@ -180,10 +180,14 @@ plan_kernel(const PlanArgs a)
                 ctx = a.ctx_lens[b];
                 len = a.lens[b];
             }
-            if (ctx < skip || ctx > a.max_ctx || (long long)ctx > (long long)a.max_pages * a.page_size || len < 0 ||
+            if (ctx < (len > 0 ? skip : 0) || ctx > a.max_ctx || (long long)ctx > (long long)a.max_pages * a.page_size || len < 0 ||
                 len > a.P_max) {
                 rd_flag(a.status, RD_DEV_BAD_LENGTH);
                 len = 0;
+            }
+            if (len == 0) {                                // no rows: of no group, its table is not read
+                g = -1;
+                skip = 0;
             }
             a.p.eff_len[b] = len;
             a.p.skip[b] = skip;
@@ -220,7 +224,8 @@ plan_kernel(const PlanArgs a)
         if (g < a.n_groups && !bad_offsets) {
             const int pg = pages_of(g);
             if (pg < 0) rd_flag(a.status, RD_DEV_BAD_LENGTH);
-            grp.leader = offsets[g];
+            grp.leader = offsets[g];                       // the first with rows
+            while (grp.leader + 1 < offsets[g + 1] && base[grp.leader + 1] == base[grp.leader]) ++grp.leader;
             grp.node0 = base[grp.leader];
             grp.nodes = base[offsets[g + 1]] - grp.node0;
             grp.positions = max(0, pg) * a.page_size;

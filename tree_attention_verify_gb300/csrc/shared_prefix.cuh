@@ -15,7 +15,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Group {
     int node0, nodes;      // its part of the list
     int positions;         // prefix length
-    int leader;            // its first request, whose table names the pages
+    int leader;            // its first request with rows, whose table names the pages
     int unit0, pairs;      // its first unit, units (of 256 rows) per kv head
 };
 
