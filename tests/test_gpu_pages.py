@@ -329,3 +329,46 @@ def test_copy_and_fork_past_32_bits(n):
     for p in (k, v):
         assert torch.equal(p[:, N - n:, :33], p[:, N - 2 * n:N - n, :33])
         assert (p[:, N - n:, 33:] == 7).all()
+
+
+@pytest.mark.parametrize("op_name", ["resize", "fork"])
+def test_large_and_small_tables_from_many_threads(op_name):
+    """Host threads, each with its own stream and tables: one changes tables of 16,384
+    rows, the others of 16, many times over.  No call may fail for what another
+    thread's needs.  (The C entries are called directly: the threads then spend their
+    time in them, at the same time, and not in Python.)"""
+    import threading
+    rd = _rd()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    wrong, running, start = [], [True], threading.Barrier(4)
+
+    def work(R, times):
+        s = torch.cuda.Stream()
+        t, h, f, c = torch.full((R, 1), -1, **i32), torch.zeros(R, **i32), torch.zeros(R, **i32), torch.zeros(R, **i32)
+        kp, vp = (torch.zeros(R, 16, 1, 8, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        lens, none, st = torch.full((R,), 5, **i32), torch.full((R,), -1, **i32), _status()
+        ws = torch.empty(12 * R, dtype=torch.uint8, device=DEV)
+        p = lambda x: x.data_ptr()  # noqa: E731
+        if op_name == "resize":
+            call, args = rd._lib.rd_resize_pages, (p(t), R, 1, p(h), p(f), R, p(lens), 16, p(st), s.cuda_stream)
+        else:
+            call, args = rd._lib.rd_fork_pages, (p(kp), p(vp), 1, R, 256, 16, p(t), R, 1, p(h), p(f), p(c), p(none),
+                                                 p(none), R, p(ws), ws.nbytes, p(st), s.cuda_stream)
+        torch.cuda.synchronize()
+        start.wait()
+        while running[0]:
+            got = [call(*args) for _ in range(50)]
+            if any(got):
+                wrong.append((R, got))
+            times -= 1
+            if times == 0:
+                running[0] = False
+        s.synchronize()
+        if st.item() or op_name == "resize" and not ((h == 1).all() and (f == 1).all()):
+            wrong.append((R, st.item()))
+    threads = [threading.Thread(target=work, args=a) for a in ((16384, 200), (16, -1), (16, -1), (16, -1))]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not wrong, wrong[:2]

@@ -659,11 +659,18 @@ cudaError_t launch_copy(CopyArgs& a, size_t max_pairs, bool dependent, cudaStrea
     return cudaLaunchKernelEx(&cfg, copy_pages_kernel, a);
 }
 
-// One launch of a table kernel: a cluster of kTableCtas CTAs.
+// One launch of a table kernel: a cluster of kTableCtas CTAs.  The limit on dynamic
+// shared memory belongs to the kernel, for all host threads: it is set to what the
+// largest tables take (`most`), never to what this call does (`smem`), which another
+// thread's call could find too small between its setting and its launch.
+constexpr size_t kResizeSmemMost = (3 * (size_t)RD_MAX_ROWS + 1) * sizeof(int);
+constexpr size_t kForkSmemMost = (3 * (size_t)RD_MAX_ROWS + 1) * sizeof(int);
+static_assert(kResizeSmemMost + sizeof(ScanSmem) <= 227 * 1024 && kForkSmemMost + sizeof(ScanSmem) <= 227 * 1024,
+              "shared memory");
 template <typename... P, typename... A>
-cudaError_t launch_table(void (*kernel)(P...), size_t smem, cudaStream_t stream, A... args)
+cudaError_t launch_table(void (*kernel)(P...), size_t smem, size_t most, cudaStream_t stream, A... args)
 {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kTableCtas);
@@ -700,8 +707,8 @@ cudaError_t rd_launch_resize_pages(int32_t* block_table, int R, int max_pages, i
                                    int32_t* dev_status, cudaStream_t stream)
 {
     const size_t smem = (size_t)(3 * R + 1) * sizeof(int);
-    return launch_table(resize_kernel, smem, stream, block_table, R, max_pages, row_pages, page_refs, num_pages,
-                        new_lens, page_size, dev_status);
+    return launch_table(resize_kernel, smem, kResizeSmemMost, stream, block_table, R, max_pages, row_pages, page_refs,
+                        num_pages, new_lens, page_size, dev_status);
 }
 
 bool rd_fork_copies_itself(int n, int layers, size_t page_bytes)
@@ -728,8 +735,9 @@ cudaError_t rd_launch_fork_pages(const rd_page_pools& pools, int page_size, int3
         fc.row_bytes = pools.page_bytes / page_size;
     }
     const size_t smem = (size_t)(2 * n + 1 + R) * sizeof(int);
-    cudaError_t e = launch_table(fork_kernel, smem, stream, block_table, R, max_pages, row_pages, page_refs,
-                                 pools.num_pages, ctx_lens, parent, child, n, page_size, src, dst, used, fc, dev_status);
+    cudaError_t e = launch_table(fork_kernel, smem, kForkSmemMost, stream, block_table, R, max_pages, row_pages,
+                                 page_refs, pools.num_pages, ctx_lens, parent, child, n, page_size, src, dst, used, fc,
+                                 dev_status);
     if (e != cudaSuccess || here) return e;
     CopyArgs a = copy_args(pools, dev_status);
     a.row_bytes = pools.page_bytes / page_size;
@@ -773,7 +781,7 @@ cudaError_t rd_launch_compact_pages(const rd_page_pools& pools, int32_t* block_t
     int32_t* n_moves = static_cast<int32_t*>(workspace);
     int32_t* src = n_moves + 4;
     int32_t* dst = src + most;
-    cudaError_t e = launch_table(compact_plan_kernel, 0, stream, page_refs, pools.num_pages, remap, n_live, n_moves,
+    cudaError_t e = launch_table(compact_plan_kernel, 0, 0, stream, page_refs, pools.num_pages, remap, n_live, n_moves,
                                  src, dst);
     if (e != cudaSuccess) return e;
     CopyArgs a = copy_args(pools, dev_status);
