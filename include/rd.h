@@ -329,7 +329,9 @@ rd_status rd_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* r
  * its own parent, or is named by an earlier pair sets RD_DEV_BAD_INDEX; a parent whose
  * length is negative or not covered by its pages sets RD_DEV_BAD_LENGTH; a pair
  * for whose last page no free page is left sets RD_DEV_OVERFLOW: that pair is
- * skipped.  Workspace: rd_fork_pages_workspace_size() bytes (none for little
+ * skipped.  An entry of the parent that is out of range or names a page that nobody
+ * held before the call sets RD_DEV_BAD_INDEX: the child's row receives it, but it is
+ * not counted, and a last page's positions are not copied from it.  Workspace: rd_fork_pages_workspace_size() bytes (none for little
  * data), no initial contents.
  */
 size_t rd_fork_pages_workspace_size(int n, int layers, size_t page_bytes);

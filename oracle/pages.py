@@ -55,7 +55,7 @@ def oracle_resize_pages(table, held, refs, new_lens, page_size):
 def oracle_fork_pages(k_pool, v_pool, table, held, refs, ctx, parent, child):
     """Pools [layers, pages, page_size, ...].  Returns (k_pool, v_pool, table, held,
     refs, ctx, status)."""
-    old_held, old_ctx, old_table = held.copy(), ctx.copy(), table.copy()
+    old_held, old_ctx, old_table, old_refs = held.copy(), ctx.copy(), table.copy(), refs.copy()
     k_pool, v_pool = k_pool.copy(), v_pool.copy()
     table, held, refs, ctx = table.copy(), held.copy(), refs.copy(), ctx.copy()
     R, page, N, status = len(held), k_pool.shape[2], len(refs), 0
@@ -81,7 +81,7 @@ def oracle_fork_pages(k_pool, v_pool, table, held, refs, ctx, parent, child):
             new, last = free.pop(0), int(old_table[p, full])
             table[c, full] = new
             refs[new] = 1
-            if 0 <= last < N:
+            if 0 <= last < N and old_refs[last] != 0:
                 k_pool[:, new, :part] = k_pool[:, last, :part]
                 v_pool[:, new, :part] = v_pool[:, last, :part]
             else:
@@ -89,7 +89,7 @@ def oracle_fork_pages(k_pool, v_pool, table, held, refs, ctx, parent, child):
         for j in range(full):
             q = int(old_table[p, j])
             table[c, j] = q
-            if 0 <= q < N:
+            if 0 <= q < N and old_refs[q] != 0:
                 shared.append(q)
             else:
                 status |= BAD_INDEX

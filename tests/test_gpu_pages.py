@@ -372,3 +372,51 @@ def test_large_and_small_tables_from_many_threads(op_name):
     for x in threads:
         x.join()
     assert not wrong, wrong[:2]
+
+
+@pytest.mark.parametrize("layers", [1, 3])
+def test_fork_of_rows_that_name_free_pages(layers):
+    """Parents whose rows name pages that nobody holds, the lowest free ones, which the
+    same call hands out: flagged, entries copied but not counted, nothing copied from
+    them, and the outcome the same every time."""
+    rd = _rd()
+    rng = np.random.default_rng(layers)
+    R, N, width, ps, n = 400, 4000, 9, 64, 180
+    table, held, refs = np.full((R, width), -1, np.int32), np.zeros(R, np.int32), np.zeros(N, np.int32)
+    held[:n] = rng.integers(1, width + 1, n)
+    for r in range(n):
+        table[r, :held[r]] = rng.integers(0, 2 * n, held[r])         # half of them among those held
+    refs[rng.permutation(2 * n)[:n]] = 3
+    ctx = np.maximum(0, held * ps - rng.integers(0, ps, R)).astype(np.int32)
+    k, v = _pool(rng, layers, N, ps, 1, 64), _pool(rng, layers, N, ps, 1, 64)
+    for pairs in (n, 4):                      # with a copy launch, and without
+        par, kid = np.arange(pairs).astype(np.int32), (n + np.arange(pairs)).astype(np.int32)
+        want = op.oracle_fork_pages(k, v, table, held, refs, ctx, par, kid)
+        for _ in range(5):
+            kp, vp, t, h, f, c, st = _bf16(k), _bf16(v), _d(table), _d(held), _d(refs), _d(ctx), _status()
+            rd.rd_fork_pages(kp, vp, t, h, f, c, _d(par), _d(kid), dev_status=st)
+            assert st.item() == want[6] == rd.DEV_BAD_INDEX
+            for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, h, f, c), want):
+                np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+def test_fork_at_the_limits_of_rows_and_pages():
+    """16,384 rows and pairs over 262,144 pages: all that the table kernel holds in
+    shared memory.  Every 16th pair is one; the free pages are the last of the pool."""
+    rd = _rd()
+    R = n = 16384
+    N, ps = 262144, 8
+    table, held, refs = np.full((R, 2), -1, np.int32), np.zeros(R, np.int32), np.ones(N, np.int32)
+    held[:R // 2] = 2
+    table[:R // 2] = np.arange(R).reshape(-1, 2)
+    refs[N - 3000::3] = 0
+    ctx = np.where(held > 0, 13, 0).astype(np.int32)
+    par, kid = np.full(n, -1, np.int32), np.zeros(n, np.int32)
+    par[::16], kid[::16] = np.arange(n // 16), R // 2 + np.arange(n // 16)
+    k = np.broadcast_to(np.arange(N, dtype=np.int32).astype(np.int16)[None, :, None, None, None], (1, N, ps, 1, 8)).copy()
+    want = op.oracle_fork_pages(k, k, table, held, refs, ctx, par, kid)
+    kp, vp, t, h, f, c, st = _bf16(k), _bf16(k), _d(table), _d(held), _d(refs), _d(ctx), _status()
+    rd.rd_fork_pages(kp, vp, t, h, f, c, _d(par), _d(kid), dev_status=st)
+    assert st.item() == want[6] == rd.DEV_OVERFLOW          # 1,000 free pages for 1,024 pairs
+    for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, h, f, c), want):
+        np.testing.assert_array_equal(a.cpu().numpy(), b)

@@ -45,6 +45,16 @@ def test_fork_worked_example():
     assert v[0, 2, 0] == pool[0, 1, 0] + 100
 
 
+def test_fork_of_a_row_that_names_a_free_page():
+    # pages of 2; the parent names the free pages 0 (full) and 2 (its last, half used)
+    pool = np.arange(5 * 2, dtype=np.int32).reshape(1, 5, 2)
+    table = _i([1, 0, 2], [-1, -1, -1])
+    k, _, t, h, r, c, st = op.oracle_fork_pages(pool, pool, table, _i(3, 0), _i(0, 1, 0, 0, 1), _i(5, 0), _i(0), _i(1))
+    assert st == op.BAD_INDEX and h.tolist() == [3, 3] and c.tolist() == [5, 5]
+    assert t[1].tolist() == [1, 0, 0] and r.tolist() == [1, 2, 0, 0, 1]      # page 0 is handed out, not shared
+    assert (k == pool).all()
+
+
 def test_copy_skips_pairs_that_depend_on_one_another():
     pool = np.arange(8, dtype=np.int32).reshape(1, 8, 1)
     # 0 -> 1 and 1 -> 2 (reads what the first writes); 3 -> 4 twice; swap 5, 6

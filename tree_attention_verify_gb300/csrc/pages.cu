@@ -76,12 +76,17 @@ struct PageWords {
     uint32_t bits;         // lane i: bit k set iff page first + 32 i + k is free (refs == 0)
 };
 
+// words of a warp, for a pool of that many pages
+__host__ __device__ __forceinline__ int words_per_warp(int num_pages)
+{
+    return ((num_pages + 31) / 32 + kTableCtas * kTableWarps - 1) / (kTableCtas * kTableWarps);
+}
+
 __device__ __forceinline__ PageWords read_free(const int32_t* refs, int num_pages, int rank)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int words = (num_pages + 31) / 32;
     PageWords p;
-    p.q = (words + kTableCtas * kTableWarps - 1) / (kTableCtas * kTableWarps);
+    p.q = words_per_warp(num_pages);
     p.first = (rank * kTableWarps + warp) * p.q * 32;
     p.bits = 0u;
 #pragma unroll 4
@@ -232,6 +237,9 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
     int* off = dyn;                        // [n + 1] new pages of the pairs before
     int* len = dyn + n + 1;                // [n] the parent's length, -1: no pair
     int* owner = len + n;                  // [R] first pair that names the row as its child
+    // the pool's free pages before the call, a bit each: a parent's row may name one of
+    // them by mistake, and the same call hands them out
+    uint32_t* free_word = reinterpret_cast<uint32_t*>(owner + R);
     __shared__ ScanSmem sc;
     const cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank();
@@ -273,14 +281,19 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
     cl.sync();
     int n_free;
     const PageWords p = read_free(refs, num_pages, rank);
-    const int base = cluster_rank(p.bits, sc, cl, n_free);
+    if (lane < p.q)
+        for (int i = 0; i < kTableCtas; ++i) cl.map_shared_rank(free_word, i)[p.first / 32 + lane] = p.bits;
+    const int base = cluster_rank(p.bits, sc, cl, n_free);      // (and its barrier: the words have arrived)
+    auto held = [&](int page) {
+        return page >= 0 && page < num_pages && !((free_word[page >> 5] >> (page & 31)) & 1u);
+    };
     for_ranked(p, p.bits, base, min(demand, n_free), [&](int page, int k) {
         const int i = last_at_most(off, n, k);
         const int full = len[i] / page_size;
         const int from = __ldcg(block_table + (size_t)__ldg(parent + i) * max_pages + full);
         block_table[(size_t)__ldg(child + i) * max_pages + full] = page;
         refs[page] = 1;
-        if (from < 0 || from >= num_pages) {
+        if (!held(from)) {
             rd_flag(status, RD_DEV_BAD_INDEX);                  // nothing to copy
             return;
         }
@@ -300,7 +313,7 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
         for (int j = lane; j < full; j += 32) {
             const int page = __ldcg(block_table + (size_t)from * max_pages + j);
             block_table[(size_t)to * max_pages + j] = page;
-            if (page < 0 || page >= num_pages) rd_flag(status, RD_DEV_BAD_INDEX);
+            if (!held(page)) rd_flag(status, RD_DEV_BAD_INDEX);
             else atomicAdd(refs + page, 1);
         }
         if (lane == 0) {
@@ -320,7 +333,7 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
         const int full = l / page_size;
         const int from = __ldcg(block_table + (size_t)__ldg(parent + i) * max_pages + full);
         const int to = __ldcg(block_table + (size_t)__ldg(child + i) * max_pages + full);
-        if (from < 0 || from >= num_pages) continue;
+        if (!held(from)) continue;
         uint4* base = here.pool[kl & 1] + (size_t)(kl >> 1) * here.layer_vecs;
         const uint4* s = base + (size_t)from * here.page_vecs;
         uint4* d = base + (size_t)to * here.page_vecs;
@@ -664,7 +677,7 @@ cudaError_t launch_copy(CopyArgs& a, size_t max_pairs, bool dependent, cudaStrea
 // largest tables take (`most`), never to what this call does (`smem`), which another
 // thread's call could find too small between its setting and its launch.
 constexpr size_t kResizeSmemMost = (3 * (size_t)RD_MAX_ROWS + 1) * sizeof(int);
-constexpr size_t kForkSmemMost = (3 * (size_t)RD_MAX_ROWS + 1) * sizeof(int);
+constexpr size_t kForkSmemMost = (3 * (size_t)RD_MAX_ROWS + 1) * sizeof(int) + RD_MAX_PAGES / 8;
 static_assert(kResizeSmemMost + sizeof(ScanSmem) <= 227 * 1024 && kForkSmemMost + sizeof(ScanSmem) <= 227 * 1024,
               "shared memory");
 template <typename... P, typename... A>
@@ -734,7 +747,8 @@ cudaError_t rd_launch_fork_pages(const rd_page_pools& pools, int page_size, int3
         fc.layer_vecs = fc.page_vecs * (size_t)pools.num_pages;
         fc.row_bytes = pools.page_bytes / page_size;
     }
-    const size_t smem = (size_t)(2 * n + 1 + R) * sizeof(int);
+    const size_t smem =
+        (size_t)(2 * n + 1 + R + words_per_warp(pools.num_pages) * kTableCtas * kTableWarps) * sizeof(int);
     cudaError_t e = launch_table(fork_kernel, smem, kForkSmemMost, stream, block_table, R, max_pages, row_pages,
                                  page_refs, pools.num_pages, ctx_lens, parent, child, n, page_size, src, dst, used, fc,
                                  dev_status);
