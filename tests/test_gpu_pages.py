@@ -420,3 +420,19 @@ def test_fork_at_the_limits_of_rows_and_pages():
     assert st.item() == want[6] == rd.DEV_OVERFLOW          # 1,000 free pages for 1,024 pairs
     for a, b in zip((kp.view(torch.int16), vp.view(torch.int16), t, h, f, c), want):
         np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+def test_resize_of_a_row_that_ends_behind_31_bits():
+    """A row of 2^31 - 1 entries (8.6 GB) gives its last ones back: a step of several
+    entries a lane may end behind 2^31."""
+    rd = _rd()
+    width, keep, N = 2 ** 31 - 1, 2 ** 31 - 1 - 900, 64
+    t = torch.empty((1, width), dtype=torch.int32, device=DEV)
+    t[0, keep - 100:] = torch.arange(1000, device=DEV) % N
+    refs, held = torch.full((N,), 1000, dtype=torch.int32, device=DEV), _d(np.array([width], np.int32))
+    st = _status()
+    rd.rd_resize_pages(t, held, refs, _d(np.array([keep], np.int32)), 1, dev_status=st)
+    assert st.item() == 0 and held.item() == keep
+    assert (t[0, keep:] == -1).all() and torch.equal(t[0, keep - 100:keep].long(), torch.arange(100, device=DEV) % N)
+    given = torch.bincount(torch.arange(100, 1000, device=DEV) % N, minlength=N)
+    assert torch.equal(refs.long(), 1000 - given)

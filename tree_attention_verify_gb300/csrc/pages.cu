@@ -179,17 +179,19 @@ resize_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, in
         const int h = have[r];
         if (h < 0) continue;
         int32_t* row = block_table + (size_t)r * max_pages;
-        for (int j0 = want[r] + me % lanes; j0 < h; j0 += lanes * kAtOnce) {
+        // (entries counted unsigned: the last step may end behind 2^31)
+        const uint32_t end = (uint32_t)h, step = (uint32_t)lanes;
+        for (uint32_t j0 = (uint32_t)want[r] + (uint32_t)(me % lanes); j0 < end; j0 += step * kAtOnce) {
             int page[kAtOnce], held[kAtOnce];
 #pragma unroll
-            for (int e = 0; e < kAtOnce; ++e) page[e] = j0 + e * lanes < h ? __ldcg(row + j0 + e * lanes) : -1;
+            for (int e = 0; e < kAtOnce; ++e) page[e] = j0 + e * step < end ? __ldcg(row + j0 + e * step) : -1;
 #pragma unroll
             for (int e = 0; e < kAtOnce; ++e)
                 held[e] = page[e] >= 0 && page[e] < num_pages ? atomicSub(refs + page[e], 1) : 0;
 #pragma unroll
             for (int e = 0; e < kAtOnce; ++e) {
-                if (j0 + e * lanes >= h) continue;
-                row[j0 + e * lanes] = -1;
+                if (j0 + e * step >= end) continue;
+                row[j0 + e * step] = -1;
                 if (held[e] <= 0) {
                     rd_flag(status, RD_DEV_BAD_INDEX);
                     // held by nobody: leave it free
@@ -310,7 +312,7 @@ fork_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, int3
             continue;
         }
         const int from = __ldg(parent + i), to = __ldg(child + i), full = l / page_size;
-        for (int j = lane; j < full; j += 32) {
+        for (uint32_t j = lane; j < (uint32_t)full; j += 32) {
             const int page = __ldcg(block_table + (size_t)from * max_pages + j);
             block_table[(size_t)to * max_pages + j] = page;
             if (!held(page)) rd_flag(status, RD_DEV_BAD_INDEX);
@@ -629,9 +631,9 @@ copy_pages_kernel(const CopyArgs a)
     } else if (a.remap != nullptr && tid >= 32) {
         // table entries through the map, one row per three warps' turn
         for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
-            const int h = min(__ldcg(a.row_pages + r), a.max_pages);
+            const uint32_t h = (uint32_t)max(0, min(__ldcg(a.row_pages + r), a.max_pages));
             int32_t* row = a.block_table + (size_t)r * a.max_pages;
-            for (int j = tid - 32; j < h; j += kCopyThreads - 32) {
+            for (uint32_t j = tid - 32; j < h; j += kCopyThreads - 32) {
                 const int page = row[j];
                 const int to = page >= 0 && page < a.num_pages ? __ldcg(a.remap + page) : -1;
                 if (to < 0) rd_flag(a.status, RD_DEV_BAD_INDEX);
