@@ -218,8 +218,9 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
  *              [n_groups].  Offsets that do not ascend set RD_DEV_BAD_INDEX, and
  *              prefix pages outside [0, max_pages] or longer than max_ctx
  *              RD_DEV_BAD_LENGTH: nobody shares then (that group does not), and the outputs
- *              are the same.  A request shorter than its group's prefix sets
- *              RD_DEV_BAD_LENGTH and is skipped (zero rows).  One without drafts
+ *              are the same.  A request shorter than its group's prefix, or of
+ *              2^31 - 256 positions or more, sets RD_DEV_BAD_LENGTH and is skipped
+ *              (zero rows).  One without drafts
  *              (packed_len 0) may be shorter, and its table row is not read.  Of
  *              the others, rows of a group that name different prefix pages set
  *              RD_DEV_BAD_INDEX; its first such request's pages are read for all.

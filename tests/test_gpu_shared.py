@@ -431,3 +431,26 @@ def test_a_run_of_steps_over_one_cache():
             _, n_live = rd.rd_compact_pages(k_pool, v_pool, table, held, refs, dev_status=st)
             assert n_live.item() == int((refs > 0).sum()) and (refs[n_live.item():] == 0).all()
     assert st.item() == 0
+
+
+def test_contexts_at_the_end_of_31_bits_are_refused():
+    """A context whose last chunk would end behind 2^31 positions (its row names one
+    page over and over) is flagged and its rows are zeros; the others are as ever."""
+    rd = _rd()
+    s = make(**CASES["half chunks"], seed=41)
+    d = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(DEV)  # noqa: E731
+    page, width = s["k_pool"].shape[1], 2 ** 25
+    table = torch.zeros((len(s["ctx"]), width), dtype=torch.int32, device=DEV)
+    table[:, :s["table"].shape[1]] = d(s["table"])
+    want, size = reference(s)
+    for ctx in (2 ** 31 - 1, 2 ** 31 - 256):
+        t = s["ctx"].copy()
+        t[1] = ctx
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        o = rd.rd_tree_attention_shared(s["q"], s["k_new"], s["v_new"], s["k_pool"], s["v_pool"], table, d(t),
+                                        d(s["offsets"]), d(s["pages"]), d(s["lens"]), d(s["mask"].view(np.int32)),
+                                        max_ctx=2 ** 31 - 1, dev_status=st).float().cpu().numpy()
+        assert st.item() == rd.DEV_BAD_LENGTH and (o[1] == 0).all()
+        rest = np.arange(len(t)) != 1
+        assert (np.abs(o - want)[rest] <= (2.0 ** -8 * (size + np.abs(want)) + 2.0 ** -11 * size)[rest]).all()
+    assert width * page == 2 ** 31
