@@ -231,8 +231,11 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
  * multiple of 64, and a batch whose work does not count in 31 bits (above about
  * (B P_max Hq / 256 + n_groups Hkv) max_ctx / 16, or 5 B Hkv max_ctx / 32) is
  * RD_ERR_UNSUPPORTED.  K and V of the packed drafts must be finite (an infinity or
- * NaN in a live draft's V can reach rows that do not see that draft); what lies behind a context's end in its
- * last page, and behind packed_len, may hold anything.
+ * NaN in a live draft's V can reach rows that do not see that draft).  An infinite
+ * element of a cached key makes the rows with a score of +inf NaN and weighs nothing
+ * where the score is -inf; one of a cached value comes out infinite or NaN in that
+ * element of the rows that see it, and in no other.  What lies behind a context's end
+ * in its last page, and behind packed_len, may hold anything.
  */
 size_t rd_tree_attention_shared_workspace_size(int B, int P_max, int Hq, int Hkv, int D,
                                                int max_ctx, int n_groups);

@@ -454,3 +454,56 @@ def test_contexts_at_the_end_of_31_bits_are_refused():
         rest = np.arange(len(t)) != 1
         assert (np.abs(o - want)[rest] <= (2.0 ** -8 * (size + np.abs(want)) + 2.0 ** -11 * size)[rest]).all()
     assert width * page == 2 ** 31
+
+
+@pytest.mark.parametrize("where", ["prefix", "own"])
+@pytest.mark.parametrize("name", ["outside any group", "66 rows", "counter", "many rows", "80 rows, whole units"])
+def test_infinite_key_and_value(name, where):
+    """An infinite element of a key that a whole group shares, or of one request's own:
+    scores of +inf make their rows NaN (inf - inf), scores of -inf give the key no
+    weight, and nobody else is touched.  An infinite element of a value makes that
+    element of the rows that see it infinite or NaN (a tile of at most 64 rows of the
+    kernel for many rows gives each row two lanes, with weights of zero where the other
+    lane's positions are: zero times infinity), and no other element.  In ranges with a
+    merge, in two units a head, off the counter, and in the kernel for many rows."""
+    s = make(**CASES[name], seed=40)
+    page, Hkv = s["k_pool"].shape[1:3]
+    B, _, Hq, _ = s["q"].shape
+    if where == "prefix":
+        g = int(np.argmax(s["pages"]))
+        seen = np.arange(s["offsets"][g], s["offsets"][g + 1])
+        at, pos = int(s["table"][seen[0], s["pages"][g] - 1]), page - 2
+    else:
+        gid = np.searchsorted(s["offsets"], np.arange(B), side="right") - 1
+        skip = np.array([s["pages"][g] * page if 0 <= g < len(s["pages"]) else 0 for g in gid])
+        b = int(np.argmax(s["ctx"] - skip))
+        assert s["ctx"][b] > skip[b]
+        seen, at, pos = np.array([b]), int(s["table"][b, skip[b] // page]), 0
+    h, e = Hkv - 1, 3
+    heads = np.arange(h * (Hq // Hkv), (h + 1) * (Hq // Hkv))
+    live = np.arange(s["q"].shape[1])[None] < s["lens"][:, None]
+    rows = np.zeros((B, s["q"].shape[1], Hq), bool)            # (request, node, head) that see the element
+    rows[np.ix_(seen, np.arange(rows.shape[1]), heads)] = True
+    rows &= live[:, :, None]
+    assert rows.any() and not rows.all()
+
+    def compare(t, skipped):
+        want, size = reference(t)                              # infinities read as the largest finite value
+        got = call(t).float().cpu().numpy()
+        err, tol = np.abs(got - want), 2.0 ** -8 * (size + np.abs(want)) + 2.0 ** -11 * size
+        assert (err <= tol)[~skipped].all()
+        return got
+    k = s["k_pool"].clone()
+    k[at, pos, h, e] = float("inf")
+    q = torch.nan_to_num(s["q"]).float().cpu().numpy()[..., e]
+    assert (q[rows] != 0).all()
+    nan = rows & (q > 0)
+    assert nan.any() and (rows & (q < 0)).any()
+    got = compare({**s, "k_pool": k}, np.broadcast_to(nan[..., None], s["q"].shape))
+    assert np.isnan(got[nan]).all()
+    v = s["v_pool"].clone()
+    v[at, pos, h, e] = float("inf")
+    out = np.zeros(tuple(s["q"].shape), bool)
+    out[..., e] = rows
+    got = compare({**s, "v_pool": v}, out)
+    assert not np.isfinite(got[out]).any() and not np.isneginf(got[out]).any()
