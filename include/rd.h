@@ -228,9 +228,10 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
  *              initial contents; query it for each shape (a larger batch may need
  *              less) and with the device current that the call runs on
  * Everything else as rd_tree_attention_paged, its limits among them; page_size is a
- * multiple of 64, and a batch whose work does not count in 31 bits (above about
- * (B P_max Hq / 256 + n_groups Hkv) max_ctx / 16, or 5 B Hkv max_ctx / 32) is
- * RD_ERR_UNSUPPORTED.  K and V of the packed drafts must be finite (an infinity or
+ * multiple of 64, and a batch whose work does not count in 31 bits is
+ * RD_ERR_UNSUPPORTED: above about (B P_max Hq / 256 + n_groups Hkv) max_ctx / 16, or,
+ * with at most 128 rows per kv head and too few units of 64 to be taken whole (under 8
+ * to 12 per SM), 3 B Hkv max_ctx / 32.  K and V of the packed drafts must be finite (an infinity or
  * NaN in a live draft's V can reach rows that do not see that draft).  An infinite
  * element of a cached key makes the rows with a score of +inf NaN and weighs nothing
  * where the score is -inf; one of a cached value comes out infinite or NaN in that

@@ -507,3 +507,14 @@ def test_infinite_key_and_value(name, where):
     out[..., e] = rows
     got = compare({**s, "v_pool": v}, out)
     assert not np.isfinite(got[out]).any() and not np.isneginf(got[out]).any()
+
+
+@pytest.mark.parametrize("name,max_ctx", [("counter", 50_000_000), ("150 rows, 600 requests", 50_000_000)])
+def test_loose_bound_of_the_contexts(name, max_ctx):
+    """Many units with a max_ctx far above the contexts: their chunks at that length would
+    not count in 31 bits, and nobody counts them."""
+    s = make(**CASES[name], seed=42)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o = call({**s, "max_ctx": max_ctx}, st)
+    assert st.item() == 0
+    check(o, s)

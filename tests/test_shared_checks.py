@@ -71,3 +71,12 @@ def test_binding_refuses_before_a_launch():
         rd.rd_tree_attention_shared(bf, bf, bf, pool, pool, table, i, i[:2], i[:1], i, mask, max_ctx=64)
     with pytest.raises((TypeError, ValueError)):
         rd.rd_tree_attention_shared(None, bf, bf, pool, pool, table, i, i[:2], i[:1], i, mask, max_ctx=64)
+
+
+@pytest.mark.parametrize("kw", [dict(B=512, P=48, words=2, Hq=40, Hkv=40, max_ctx=1_700_000),
+                                dict(B=481, P=64, words=2, Hq=32, Hkv=8, max_ctx=4_000_000)], ids=str)
+def test_counts_only_what_it_divides(kw):
+    """Many units are taken whole, off a counter or in turn: their chunks are not counted
+    and need not fit 31 bits.  (Without a workspace the call ends at that check, before a
+    launch.)"""
+    assert call(**kw, wsb=0) == rd.RD_ERR_INVALID_ARG

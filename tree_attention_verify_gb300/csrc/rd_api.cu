@@ -231,9 +231,8 @@ rd_status rd_tree_attention_shared(int B, int P_max, int Hq, int Hkv, int D, flo
     /* the prefix's chunks of 128 positions x 256 rows, in eighths, counted in 32 bits */
     if (((long long)B * P_max * (Hq / Hkv) / 256 + n_groups) * Hkv * (max_ctx / 128 + 4LL) * 8 > 0x7fffffffLL)
         return RD_ERR_UNSUPPORTED;
-    /* and those behind it, of 32 positions at least, for units of 33 to 64 rows */
-    const long long rows = (long long)P_max * (Hq / Hkv), units = rows / 32 + 1 < 5 ? rows / 32 + 1 : 5;
-    if (B * units * Hkv * (max_ctx / 32 + 4LL) > 0x7fffffffLL) return RD_ERR_UNSUPPORTED;
+    /* and what the part behind it counts */
+    if (!rd_shared_suffix_counts(B, P_max, Hq, Hkv, D, max_ctx)) return RD_ERR_UNSUPPORTED;
     if (mask_words != (P_max + 31) / 32) return RD_ERR_INVALID_ARG;
     if (!q || !k_new || !v_new || !k_pool || !v_pool || !block_table || !ctx_lens || !group_offsets ||
         !prefix_pages || !packed_len || !mask || !o || !workspace)

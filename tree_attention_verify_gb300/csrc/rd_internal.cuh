@@ -115,6 +115,8 @@ cudaError_t rd_launch_beam_step(const void* logits, const float* scores_in,
                                 int32_t* dev_status, cudaStream_t stream);
 
 // Tree attention of groups that share a prefix (shared_prefix.cu).
+// whether the part behind the prefix counts its work in 31 bits
+bool rd_shared_suffix_counts(int B, int P_max, int Hq, int Hkv, int D, int max_ctx);
 size_t rd_shared_workspace_bytes(int B, int P_max, int Hq, int Hkv, int D, int max_ctx, int n_groups);
 cudaError_t rd_launch_shared_attention(int B, int P_max, int Hq, int Hkv, int D, float scale, const void* q,
                                        const void* k_new, const void* v_new, const void* k_pool,

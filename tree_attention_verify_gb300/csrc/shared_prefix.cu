@@ -1082,6 +1082,19 @@ cudaError_t launch_prefix(int grid, cudaStream_t stream, PrefixArgs& a, CUtensor
 
 }  // namespace
 
+bool rd_shared_suffix_counts(int B, int P_max, int Hq, int Hkv, int D, int max_ctx)
+{
+    const SuffixChoice s = choose_suffix(B, P_max, Hq, Hkv, D, max_ctx);
+    // units (and twice as many numbers as CTAs drawn behind the last off the counter)
+    long long n = (long long)B * Hkv * s.tiles;
+    if (s.few_rows && !s.by_unit) {
+        // divided into ranges: all chunks, those of the context and of the drafts rounded up
+        const int ch = rd_suffix_chunk(rd_suffix_row_warps(s.nodes * (Hq / Hkv)));
+        n *= max_ctx / ch + 1LL + P_max / ch + 1LL;
+    }
+    return n <= 0x7fffffffLL - 4LL * s.grid;              // (the tcgen05 kernel counts chunks only where they fit)
+}
+
 size_t rd_shared_workspace_bytes(int B, int P_max, int Hq, int Hkv, int D, int max_ctx, int n_groups)
 {
     Plan p;
