@@ -80,3 +80,21 @@ def test_out_helper_rejects_wrong_shape_and_dtype():
         rd._out_dict(dict(a=torch.zeros(2, 4, dtype=torch.int32)), shapes, dtypes, like)
     got = rd._out_dict(None, shapes, dtypes, like)
     assert tuple(got["a"].shape) == (2, 3) and tuple(got["b"].shape) == (2,)
+
+
+def test_imports_with_a_torch_that_has_no_cuda():
+    """Host-only uses (the C entries' checks, workspace sizes) need no CUDA in torch: a
+    build without it lacks torch._C._cuda_*."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, n)\n"
+            "import tree_attention_verify_gb300 as rd\n"
+            "assert rd.rd_tree_attention_workspace_size(4, 8, 8, 2, 128, 4096) > 0\n"
+            "try:\n"
+            "    rd.rd_unpack(torch.zeros(1, 1, 1), torch.zeros(1, 1, 1, dtype=torch.int32))\n"
+            "except (ValueError, TypeError):\n"
+            "    print('refused')\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout == "refused\n", r.stderr

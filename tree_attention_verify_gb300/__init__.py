@@ -139,8 +139,10 @@ def _index(t) -> int:
     return t.get_device() if type(t) is torch.Tensor else -1
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (A torch without CUDA has neither call, and no tensor that would reach them.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _check(fn: str, status: int):
