@@ -85,3 +85,34 @@ def test_binding_refuses_before_a_launch():
         rd._scratch(torch.zeros(3, dtype=torch.uint8), 16, pool, None)
     with pytest.raises(TypeError):
         rd._need_status(torch.zeros(1), pool)
+
+
+def test_binding_asks_the_library_how_much_workspace(monkeypatch):
+    """Workspaces are as large as the library says, whatever it says."""
+    runs = {}
+    monkeypatch.setattr(rd, "_fine", lambda *a: True)         # as if the tensors were on a GPU
+    monkeypatch.setattr(rd, "_need", lambda *a, **kw: None)
+    monkeypatch.setattr(rd, "_run", lambda name, like, *a, stream=None: runs.__setitem__(name, a))
+    pool, table = torch.zeros(8, 64, 1, 64, dtype=torch.bfloat16), _i(4, 3)
+    for extra in (0, 4096):
+        for name in ("rd_fork_pages", "rd_copy_pages", "rd_compact_pages"):
+            f = getattr(rd._lib, name + "_workspace_size")
+            monkeypatch.setattr(rd._lib, name + "_workspace_size", lambda *a, f=f, extra=extra: f(*a) + extra)
+        for n in (2, 256, 257, 300):
+            need = rd._lib.rd_copy_pages_workspace_size(n)
+            rd.rd_copy_pages(pool, pool, _i(n), _i(n))
+            assert runs["rd_copy_pages"][9] >= need and (need > 0 or runs["rd_copy_pages"][9] == 0)
+            if need:
+                with pytest.raises(ValueError, match="at least"):
+                    rd.rd_copy_pages(pool, pool, _i(n), _i(n), workspace=torch.zeros(need - 1, dtype=torch.uint8))
+        for pages in (1, 2, 7, 8):
+            need = rd._lib.rd_compact_pages_workspace_size(pages)
+            args = [pool[:pages].clone(), pool[:pages].clone(), table, _i(4), _i(pages)]
+            rd.rd_compact_pages(*args)
+            assert runs["rd_compact_pages"][13] >= need
+            rd.rd_compact_pages(*args, n_live=_i(1))
+            assert runs["rd_compact_pages"][13] >= need
+            with pytest.raises(ValueError, match="at least"):
+                rd.rd_compact_pages(*args, workspace=torch.zeros(need - 1, dtype=torch.uint8))
+        rd.rd_fork_pages(pool, pool, table, _i(4), _i(8), _i(4), _i(300), _i(300))
+        assert runs["rd_fork_pages"][16] >= rd._lib.rd_fork_pages_workspace_size(300, 1, 64 * 64 * 2)

@@ -723,7 +723,7 @@ def rd_copy_pages(k_pool, v_pool, src, dst, *, workspace=None, dev_status=None, 
     if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
     _need_status(dev_status, k_pool)
-    workspace, size = _pages_scratch(workspace, 8 * n if n > 256 else 0, k_pool, stream)
+    workspace, size = _pages_scratch(workspace, _lib.rd_copy_pages_workspace_size(n), k_pool, stream)
     _run("rd_copy_pages", k_pool,
          _ptr(k_pool), _ptr(v_pool), layers, num_pages, page, _ptr(src), _ptr(dst), n,
          _ptr(workspace), size, _ptr(dev_status), stream=stream)
@@ -739,9 +739,9 @@ def rd_compact_pages(k_pool, v_pool, block_table, row_pages, page_refs, *, remap
     _need_status(dev_status, k_pool)
     remap = _new((num_pages,), torch.int32, k_pool, stream) if remap is None else \
         _out(remap, "remap", (num_pages,), torch.int32, k_pool)
-    need = 16 + 8 * (num_pages // 2)
+    need = _lib.rd_compact_pages_workspace_size(num_pages)
     if n_live is None and workspace is None:             # one allocation for both
-        both = _new((1 + need // 4,), torch.int32, k_pool, stream)
+        both = _new((1 + (need + 3) // 4,), torch.int32, k_pool, stream)
         n_live, ws, ws_bytes = both[:1], both.data_ptr() + 4, need
     else:
         n_live = _new((1,), torch.int32, k_pool, stream) if n_live is None else \
