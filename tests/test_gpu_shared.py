@@ -518,3 +518,45 @@ def test_loose_bound_of_the_contexts(name, max_ctx):
     o = call({**s, "max_ctx": max_ctx}, st)
     assert st.item() == 0
     check(o, s)
+
+
+@pytest.mark.parametrize("B", [1000, 20000])
+def test_plan_of_requests_without_rows(B):
+    """A group without prefix pages, and one whose requests have finished but for the
+    last, take no longer to plan than requests in no group: its first request with rows
+    is searched, not walked to (20,000 requests: 1,260 and 1,150 us so, against 240 and
+    130 outside of a group)."""
+    rd = _rd()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(B)
+    q, kn, vn = (torch.randn(B, 1, 1, 64, generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(3))
+    pool = torch.randn(2, 64, 64, 1, 64, generator=gen, device=DEV, dtype=torch.bfloat16)
+    table = (torch.arange(2 * B, **i32) % 64).view(B, 2)
+    table[:, 0] = 5
+    ctx, mask = torch.full((B,), 70, **i32), torch.ones(B, 1, 1, **i32)
+    top = max(pool[1].abs().max().item(), vn.abs().max().item())
+    live = torch.ones(B, **i32)
+    last = torch.zeros(B, **i32)
+    last[-1] = 1
+
+    def run(lens, offsets, pages):
+        args = [q, kn, vn, pool[0], pool[1], table, ctx, torch.tensor(offsets, **i32), torch.tensor(pages, **i32), lens, mask]
+        o = rd.rd_tree_attention_shared(*args, max_ctx=128)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            rd.rd_tree_attention_shared(*args, max_ctx=128)
+        times = []
+        for _ in range(20):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            graph.replay()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return o.float(), min(times)
+    for lens, pages in ((live, 0), (last, 1)):
+        want, alone = run(lens, [0, 1, 2], [1, 1])
+        got, grouped = run(lens, [0, B], [pages])
+        # both within the tolerance above of the formula; A and |o| are at most max |v|
+        assert (got - want).abs().max() <= 2 * (2.0 ** -7 + 2.0 ** -11) * top
+        assert grouped < 1.6 * alone + 0.01, (grouped, alone)

@@ -226,10 +226,18 @@ plan_kernel(const PlanArgs a)
         if (g < a.n_groups && !bad_offsets) {
             const int pg = pages_of(g);
             if (pg < 0) rd_flag(a.status, RD_DEV_BAD_LENGTH);
-            grp.leader = offsets[g];                       // the first with rows
-            while (grp.leader + 1 < offsets[g + 1] && base[grp.leader + 1] == base[grp.leader]) ++grp.leader;
+            grp.leader = offsets[g];
             grp.node0 = base[grp.leader];
             grp.nodes = base[offsets[g + 1]] - grp.node0;
+            if (grp.nodes > 0) {
+                // the first with rows: the last before which there are none
+                int lo = grp.leader, hi = offsets[g + 1] - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (base[mid] == grp.node0) lo = mid; else hi = mid - 1;
+                }
+                grp.leader = lo;
+            }
             grp.positions = max(0, pg) * a.page_size;
             grp.pairs = (grp.nodes * a.G + kUnitRows - 1) / kUnitRows;
             units = a.Hkv * grp.pairs;
