@@ -270,7 +270,8 @@ rd_status rd_tree_attention_shared(int B, int P_max, int Hq, int Hkv, int D, flo
  * new_ctx_lens int32 [B] (written; must not alias ctx_lens).
  * A best beam, accepted length, unpacker index or page id out of range sets
  * RD_DEV_BAD_INDEX; a position beyond max_pages*page_size sets
- * RD_DEV_BAD_LENGTH; the offending row is skipped.
+ * RD_DEV_BAD_LENGTH; the offending row is skipped.  The pages written to must be
+ * held by no other row (see the page operators below).
  */
 rd_status rd_commit_accepted(int B, int W, int L, int P_max, int Hkv, int D,
                              const void* k_new, const void* v_new, const int32_t* unpacker,
@@ -300,6 +301,18 @@ rd_status rd_commit_accepted(int B, int W, int L, int P_max, int Hkv, int D,
  * depends on the tables alone.  R and n <= RD_MAX_ROWS, num_pages <=
  * RD_MAX_PAGES, R * max_pages < 2^31 (RD_ERR_UNSUPPORTED).  Calls that change the
  * same tables must not overlap in time.
+ *
+ * Who may write: rd_commit_accepted writes behind a row's length and does not look at
+ * page_refs.  Forks share only pages that are full, so no row writes where another
+ * reads, until a row is cut back into a page that it shares: writing on there would
+ * change every sharer's context, and no call can tell (an owner that keeps a
+ * prompt holds its last page too, and the row behind it may go on).  Such a row needs
+ * a page of its own first, either way:
+ *  - set ctx_lens to the new length, fork the row into an empty one (which copies the
+ *    used part of that page), and give the old row's pages back;
+ *  - read the page's id from the table, resize the row to the multiple of page_size
+ *    below and then to the new length (a new page takes its place), and rd_copy_pages
+ *    from the old id to the new.
  */
 
 /*
@@ -314,6 +327,10 @@ rd_status rd_commit_accepted(int B, int W, int L, int P_max, int Hkv, int D,
  * wants more than max_pages sets RD_DEV_BAD_LENGTH and is left alone; an entry
  * out of range, or naming a page that nobody holds, sets RD_DEV_BAD_INDEX and
  * gives nothing back.
+ *
+ * Cutting a row back moves no data.  Where its new end lies inside a page that others
+ * hold too (page_refs above 1: the row has branched behind that point), the row may
+ * be read and forked, but not written on: see above.
  */
 rd_status rd_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* row_pages,
                           int32_t* page_refs, int num_pages, const int32_t* new_lens,
@@ -336,8 +353,9 @@ rd_status rd_resize_pages(int32_t* block_table, int R, int max_pages, int32_t* r
  * for whose last page no free page is left sets RD_DEV_OVERFLOW: that pair is
  * skipped.  An entry of the parent that is out of range or names a page that nobody
  * held before the call sets RD_DEV_BAD_INDEX: the child's row receives it, but it is
- * not counted, and a last page's positions are not copied from it.  Workspace: rd_fork_pages_workspace_size() bytes (none for little
- * data), no initial contents.
+ * not counted, and a last page's positions are not copied from it.
+ * Workspace: rd_fork_pages_workspace_size() bytes (none for little data), no initial
+ * contents.
  */
 size_t rd_fork_pages_workspace_size(int n, int layers, size_t page_bytes);
 rd_status rd_fork_pages(void* k_pool, void* v_pool, int layers, int num_pages, size_t page_bytes,

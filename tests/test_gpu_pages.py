@@ -436,3 +436,52 @@ def test_resize_of_a_row_that_ends_behind_31_bits():
     assert (t[0, keep:] == -1).all() and torch.equal(t[0, keep - 100:keep].long(), torch.arange(100, device=DEV) % N)
     given = torch.bincount(torch.arange(100, 1000, device=DEV) % N, minlength=N)
     assert torch.equal(refs.long(), 1000 - given)
+
+
+@pytest.mark.parametrize("way", ["fork", "copy"])
+@pytest.mark.parametrize("cut", [100, 64, 1])
+def test_a_row_cut_back_into_a_shared_page_goes_on_in_its_own(way, cut):
+    """The two ways in which a row that is cut back into a page that it shares may be
+    written on: its branch keeps every position, the row keeps its first ones and
+    receives the committed rows behind them."""
+    rd = _rd()
+    rng = np.random.default_rng(cut)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    R, N, ps, width, L = 3, 12, 64, 4, 3
+    k0 = _pool(rng, 1, N, ps, 2, 64)
+    kp, vp, st = _bf16(k0), _bf16(k0[:, ::-1]), _status()
+    t, h, f, c = torch.full((R, width), -1, **i32), torch.zeros(R, **i32), torch.zeros(N, **i32), torch.zeros(R, **i32)
+    length = 158                              # two full pages and 30 positions
+    rd.rd_resize_pages(t, h, f, torch.tensor([length, 0, 0], **i32), ps, dev_status=st)
+    c[0] = length
+    rd.rd_fork_pages(kp, vp, t, h, f, c, torch.tensor([0], **i32), torch.tensor([1], **i32), dev_status=st)
+
+    def contents(r, n):
+        pages = t[r, :-(-n // ps)].long()
+        return [x[0, pages].view(torch.int16).reshape(-1, 2, 64)[:n].clone() for x in (kp, vp)]
+    branch, row = contents(1, length), contents(0, cut)
+    if way == "fork":
+        r = 2
+        c[0] = cut
+        rd.rd_fork_pages(kp, vp, t, h, f, c, torch.tensor([0], **i32), torch.tensor([r], **i32), dev_status=st)
+        rd.rd_resize_pages(t, h, f, torch.tensor([0, -1, cut + L], **i32), ps, dev_status=st)
+    else:
+        r = 0
+        last = cut // ps
+        old = t[0, last:last + 1].clone()
+        rd.rd_resize_pages(t, h, f, torch.tensor([last * ps, -1, -1], **i32), ps, dev_status=st)
+        rd.rd_resize_pages(t, h, f, torch.tensor([cut + L, -1, -1], **i32), ps, dev_status=st)
+        rd.rd_copy_pages(kp, vp, old, t[0, last:last + 1].clone(), dev_status=st)
+        c[0] = cut
+    # one beam of L tokens a row, all accepted; only row r's are looked at (the branch
+    # has room behind its length, and the third row no pages: flagged and skipped)
+    kn, vn = (torch.randn(R, L, 2, 64, device=DEV).bfloat16() for _ in range(2))
+    unpacker = torch.arange(L, **i32).expand(R, 1, L).contiguous()
+    assert st.item() == 0
+    new = rd.rd_commit_accepted(kn, vn, unpacker, torch.zeros(R, **i32), torch.full((R,), L - 1, **i32), kp[0], vp[0],
+                                t, c)
+    assert new[r].item() == cut + L
+    for got, want in zip(contents(1, length), branch):
+        assert torch.equal(got, want)
+    for got, want, rows in zip(contents(r, cut + L), row, (kn, vn)):
+        assert torch.equal(got[:cut], want) and torch.equal(got[cut:], rows[r].view(torch.int16))

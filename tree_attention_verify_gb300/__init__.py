@@ -677,6 +677,8 @@ def rd_resize_pages(block_table, row_pages, page_refs, new_lens, page_size: int,
                     dev_status=None, stream=None) -> torch.Tensor:
     """Reserve, trim and free pages: row r comes to hold ceil(new_lens[r] / page_size)
     of them (new_lens int32 [R]; 0 frees the row, negative leaves it alone).
+    A row cut back into a page that others hold may be read and forked, but not written
+    on before it has a page of its own.
     block_table int32 [R, max_pages], row_pages int32 [R] and page_refs int32
     [num_pages] change in place; returns row_pages (see rd_resize_pages in rd.h)."""
     R, max_pages = _tables(block_table, row_pages, page_refs, None, None)
