@@ -11,8 +11,11 @@
 //    of atomics.  The work is a few hundred KB at most; what bounds it is the
 //    chain of dependent L2 reads and cluster barriers, hence one cluster (a
 //    hardware barrier instead of further launches) and no free list to keep.
-//    Resizing 16 rows of 4,096 pages takes 6.8 us, 1,000 rows of 65,536 pages 14.0;
-//    five forks with their 1.3 MB of data 12.3.
+//    Resizing 16 rows of 4,096 pages takes 7.2 us, 1,000 rows of 65,536 pages 14.7
+//    (by clock reads, of 25,000 cycles: row demands 2,800, pages given back and the
+//    barrier 7,100, reference counts 2,200, their ranks 2,300, then the new entries
+//    9,900 in the first CTA against 900 in the others: the lowest free pages all lie in
+//    its share); five forks with their 1.3 MB of data 13.
 //  - the page copy: bulk copies (TMA) through a shared-memory ring, one issuing
 //    thread per CTA, two CTAs per SM; a page of K or V is one contiguous block,
 //    so nothing but the ring's depth and HBM bounds it.  300 pages of 131 KB in 8
@@ -222,8 +225,12 @@ resize_kernel(int32_t* block_table, int R, int max_pages, int32_t* row_pages, in
 }
 
 // Rows branch: tables here, the last pages' data by the copy kernel behind it, or
-// here too when it is little (`here.pool` not null): up to 2 MB, eight SMs take no
-// longer than a second launch does to begin, and no list has to pass between them.
+// here too when it is little (`here.pool` not null): no second launch, no list between
+// them, and no workspace.  Measured here against a copy launch (one layer, 128 and
+// 256 KB a page; L2 cold): 0.25 MB 18.6 against 19.3 us, 0.5 MB 18.8 / 19.1, 1 MB 20.0 / 19.4,
+// 2 MB 21.9 / 20.7, 4 MB 25.6 / 20.2; warm 15.3 / 16.2, 14.8 / 14.4, 16.0 / 15.4, 18.1 / 15.3,
+// 20.4 / 15.6.  So time alone would end it at 0.5 MB; up to 2 MB it costs 1 to 3 us
+// and spares the caller the workspace.
 constexpr size_t kForkHereBytes = 2u << 20;
 struct ForkCopy {
     uint4* pool[2];                        // K, V

@@ -40,7 +40,7 @@
 //   warps 18-19  the unit's query rows into shared memory (cp.async, row list),
 //              then the check that a group's tables name the same pages
 // What bounds it: with many rows the chain S -> softmax -> P -> PV of a tile (64
-// requests of 30 nodes, 40 heads, 8,192 positions: 244 GFLOP in 170 us, 1.44 PFLOP/s,
+// requests of 23 live nodes, 40 heads, 8,192 positions: 244 GFLOP in 170 us, 1.44 PFLOP/s,
 // tensor pipe active 63% of the time; L2 misses on K and V cost 4% of it, measured by
 // reading one head's K and V for all), with few rows the start and end of a unit.
 // Every wait is bounded by a clock budget; on expiry the CTA records
@@ -79,7 +79,7 @@ constexpr uint32_t kTwoTiles = 8;
 constexpr uint32_t kOneTile = 5;
 constexpr uint32_t kUnitStart = 24;
 // A CTA's share at least: 2, 3 and 4 chunks make 8 single tokens over 2,048 positions
-// 22.6, 23.0 and 25.5 us, 4 requests of 20 nodes 28.9, 28.3 and 26.7.
+// 22.6, 23.0 and 25.5 us, 4 requests of 20 nodes (10 of them live) 28.9, 28.3 and 26.7.
 constexpr uint32_t kMinRange = 3 * kTwoTiles;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr long long kWaitBudget = 4000000000LL;   // ~2 s of SM clock per wait
@@ -874,7 +874,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map_k,
 // those of its prefix unit and of its suffix unit, kMergePieces of them a round.
 // Few rows a CTA: many CTAs' chains run side by side, and none waits for a second
 // wave (32 rows take 69.7 us for the whole call where 8 take 65.7: 16 requests x 8
-// heads x 120 rows; half the columns a thread cost 2 to 6 us on top).
+// heads x 160 rows, 75 of them live; half the columns a thread cost 2 to 6 us on top).
 struct MergeArgs {
     int P_max, Hq, Hkv, G, B;
     int blocks;               // CTAs per (request, kv head)
@@ -1004,10 +1004,11 @@ cudaError_t launch_merge(dim3 grid, cudaStream_t stream, MergeArgs& a)
 // Which kernel takes the part behind the prefix.  Up to 128 rows per kv head (and 64
 // nodes) the one of shared_suffix.cu, in units of up to 64 rows that read each key
 // once; with more the tcgen05 kernel, whose tiles hold 128.  The whole call, 64
-// requests of 8 kv heads behind 2,048 shared positions, either way: 96 rows and up to
-// 300 positions each 70 against 88 us, up to 4,000 169 against 180; but 160 rows and up
-// to 3,000 positions 283 against 185 (to 300: 84 against 102).  16 requests of 80 rows,
-// D 64, to 3,000: 52 against 63; four of 128 rows, to 8,000: 44 against 43.
+// requests of 8 kv heads behind 2,048 shared positions, either way (rows as allocated,
+// P_max G; about half of them live): 96 rows and up to 300 positions each 70 against 88
+// us, up to 4,000 169 against 180; but 160 rows and up to 3,000 positions 283 against 185
+// (to 300: 84 against 102).  16 requests of 80 rows, D 64, to 3,000: 52 against 63; four
+// of 128 rows, to 8,000: 44 against 43.
 constexpr int kSuffixMaxRows = 128;
 constexpr int kSuffixMaxNodes = 64;        // (two mask words a row)
 struct SuffixChoice {

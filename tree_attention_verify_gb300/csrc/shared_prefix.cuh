@@ -125,8 +125,8 @@ __device__ __forceinline__ Pieces pieces_of(int2 unit, const Plan& p, int h, int
 constexpr int kSuffixRows = 64;            // of a unit at most
 // nodes of a unit (all G heads of each)
 __host__ __device__ constexpr int rd_suffix_nodes(int P_max, int G) { return P_max * G <= kSuffixRows ? P_max : kSuffixRows / G; }
-// chunks per CTA at least: 1, 2 and 4 make 4 requests x 32 heads x 20 rows 29.1, 28.3
-// and 30.8 us
+// chunks per CTA at least: 1, 2 and 4 make 4 requests x 32 heads x 20 rows (10 of them
+// live) 29.1, 28.3 and 30.8 us
 constexpr uint32_t kSuffixMinChunks = 2;
 // warps of 16 rows for `rows` rows
 __host__ __device__ constexpr int rd_suffix_row_warps(int rows) { return (rows + 15) / 16; }

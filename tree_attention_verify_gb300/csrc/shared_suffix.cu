@@ -6,8 +6,8 @@
 // fit).  Behind a shared prompt a request has a few hundred positions of its own, so a
 // unit is a handful of chunks, and what bounds it is not bytes or products but the chain of steps per unit.  The tcgen05 kernel pays that chain
 // across four roles (64 positions take it 2,500 to 4,000 cycles behind a prefix, its
-// epilogue 4,000 more): 120 us at 64 requests x 40 heads x 150 positions and 30
-// rows.  Here a warp holds 16 rows' queries, scores, statistics and sums in its own
+// epilogue 4,000 more): 120 us at 64 requests x 40 heads x 150 positions and 23 live
+// rows of 48.  Here a warp holds 16 rows' queries, scores, statistics and sums in its own
 // registers (mma.sync m16n8k16), so that nothing waits on another role but for
 // loads, and two or three CTAs share an SM.  With 64 rows or fewer the products stay
 // under what mma.sync can do at the rate the keys arrive.
@@ -761,7 +761,7 @@ cudaError_t launch_rows(int grid, cudaStream_t stream, SuffixArgs& a, CUtensorMa
 }  // namespace
 
 // Whole units off a counter when they are many enough to level out: 64 and 128 units
-// (one token of 8 requests, 20 nodes of 4) make the whole call 33 and 42 us that way,
+// (one token of 8 requests, up to 20 nodes of 4) make the whole call 33 and 42 us that way,
 // 23 and 28 in ranges; 2,560 units 262 us against 277 with partials and a merge.
 bool rd_suffix_by_unit(long long units, int grid) { return units >= 4LL * grid; }
 
