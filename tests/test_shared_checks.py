@@ -80,3 +80,28 @@ def test_counts_only_what_it_divides(kw):
     and need not fit 31 bits.  (Without a workspace the call ends at that check, before a
     launch.)"""
     assert call(**kw, wsb=0) == rd.RD_ERR_INVALID_ARG
+
+
+def test_numbers_past_32_bits_are_refused(monkeypatch):
+    """ctypes would cut them: 2^32 + 64 positions became 64, and longer requests zero rows."""
+    runs = []
+    monkeypatch.setattr(rd, "_fine", lambda *a: True)         # as if the tensors were on a GPU
+    monkeypatch.setattr(rd, "_need", lambda *a, **kw: None)
+    monkeypatch.setattr(rd, "_run", lambda name, like, *a, stream=None: runs.append(a))
+    bf = torch.zeros(4, 8, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32)
+    pool, table = torch.zeros(8, 64, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 3, dtype=torch.int32)
+    mask = torch.zeros(4, 8, 1, dtype=torch.int32)
+    for bad in (2 ** 32 + 64, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="max_ctx must fit 32 bits"):
+            rd.rd_tree_attention_shared_workspace_size(4, 8, 2, 2, 64, bad, 1)
+        for kw in ({}, dict(workspace=torch.zeros(1 << 20, dtype=torch.uint8))):
+            with pytest.raises(ValueError, match="max_ctx must fit 32 bits"):
+                rd.rd_tree_attention_shared(bf, bf, bf, pool, pool, table, i, i[:2], i[:1], i, mask, max_ctx=bad, **kw)
+        with pytest.raises(ValueError, match="max_ctx must fit 32 bits"):
+            rd.rd_tree_attention_workspace_size(4, 8, 2, 2, 64, bad)
+        with pytest.raises(ValueError, match="page_size must fit 32 bits"):
+            rd.rd_resize_pages(table, i, torch.zeros(8, dtype=torch.int32), i, bad)
+    assert not runs
+    rd.rd_resize_pages(table, i, torch.zeros(8, dtype=torch.int32), i, 64)
+    assert runs[0][7] == 64

@@ -145,6 +145,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def _c_int(name: str, x) -> int:
+    """A number that the caller gives, as a C int (ctypes would cut it to 32 bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _check(fn: str, status: int):
     if status != RD_OK:
         raise RdError(fn, status)
@@ -254,8 +262,8 @@ def rd_tree_attention_workspace_size(B: int, P_max: int, Hq: int, Hkv: int, D: i
     call will run on (`device`, else the current device)."""
     if device is not None and torch.device(device).type == "cuda":
         with torch.cuda.device(device):
-            return int(_lib.rd_tree_attention_workspace_size(B, P_max, Hq, Hkv, D, max_ctx))
-    return int(_lib.rd_tree_attention_workspace_size(B, P_max, Hq, Hkv, D, max_ctx))
+            return int(_lib.rd_tree_attention_workspace_size(B, P_max, Hq, Hkv, D, _c_int("max_ctx", max_ctx)))
+    return int(_lib.rd_tree_attention_workspace_size(B, P_max, Hq, Hkv, D, _c_int("max_ctx", max_ctx)))
 
 
 def rd_tree_attention(q, k_new, v_new, k_cache, v_cache, ctx_offsets, packed_len, mask, *,
@@ -289,7 +297,7 @@ def rd_tree_attention(q, k_new, v_new, k_cache, v_cache, ctx_offsets, packed_len
         workspace = torch.empty(ws_need, dtype=torch.uint8, device=q.device)
     _run("rd_tree_attention", q,
         B, P, Hq, Hkv, D, float(scale), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
-        _ptr(v_cache), _ptr(ctx_offsets), int(k_cache.shape[0]), int(max_ctx), _ptr(packed_len),
+        _ptr(v_cache), _ptr(ctx_offsets), int(k_cache.shape[0]), _c_int("max_ctx", max_ctx), _ptr(packed_len),
         _ptr(mask), int(mask.shape[2]), _ptr(out), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _ptr(dev_status), stream=stream)
@@ -330,7 +338,7 @@ def rd_tree_attention_fp8(q, k_new, v_new, k_cache, v_cache, k_scale: float, v_s
     _run("rd_tree_attention_fp8", q,
         B, P, Hq, Hkv, D, float(scale), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
         _ptr(v_cache), float(k_scale), float(v_scale), _ptr(ctx_offsets),
-        int(k_cache.shape[0]), int(max_ctx), _ptr(packed_len), _ptr(mask), int(mask.shape[2]),
+        int(k_cache.shape[0]), _c_int("max_ctx", max_ctx), _ptr(packed_len), _ptr(mask), int(mask.shape[2]),
         _ptr(out), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _ptr(dev_status), stream=stream)
@@ -367,7 +375,7 @@ def rd_tree_attention_paged(q, k_new, v_new, k_pool, v_pool, block_table, ctx_le
     _run("rd_tree_attention_paged", q,
         B, P, Hq, Hkv, D, float(scale), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool),
         _ptr(v_pool), n_pages, page_size, _ptr(block_table), block_table.shape[1],
-        _ptr(ctx_lens), int(max_ctx), _ptr(packed_len), _ptr(mask), int(mask.shape[2]),
+        _ptr(ctx_lens), _c_int("max_ctx", max_ctx), _ptr(packed_len), _ptr(mask), int(mask.shape[2]),
         _ptr(out), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _ptr(dev_status), stream=stream)
@@ -380,8 +388,8 @@ def rd_tree_attention_shared_workspace_size(B: int, P_max: int, Hq: int, Hkv: in
     f = _lib.rd_tree_attention_shared_workspace_size
     if device is not None and torch.device(device).type == "cuda":
         with torch.cuda.device(device):
-            return int(f(B, P_max, Hq, Hkv, D, max_ctx, n_groups))
-    return int(f(B, P_max, Hq, Hkv, D, max_ctx, n_groups))
+            return int(f(B, P_max, Hq, Hkv, D, _c_int("max_ctx", max_ctx), n_groups))
+    return int(f(B, P_max, Hq, Hkv, D, _c_int("max_ctx", max_ctx), n_groups))
 
 
 def rd_tree_attention_shared(q, k_new, v_new, k_pool, v_pool, block_table, ctx_lens, group_offsets,
@@ -432,7 +440,7 @@ def rd_tree_attention_shared(q, k_new, v_new, k_pool, v_pool, block_table, ctx_l
     _run("rd_tree_attention_shared", q,
          B, P, Hq, Hkv, D, float(scale), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(),
          v_pool.data_ptr(), num_pages, page_size, block_table.data_ptr(), width[1],
-         ctx_lens.data_ptr(), int(max_ctx), n_groups, group_offsets.data_ptr(), prefix_pages.data_ptr(),
+         ctx_lens.data_ptr(), _c_int("max_ctx", max_ctx), n_groups, group_offsets.data_ptr(), prefix_pages.data_ptr(),
          packed_len.data_ptr(), mask.data_ptr(), words, out.data_ptr(), workspace.data_ptr(),
          workspace.nbytes, _ptr(dev_status), stream=stream)
     return out
@@ -475,7 +483,7 @@ def rd_causal_attention(q, k, v, cu_seqlens, *, max_seqlen: int, scale: float = 
     out = _out(out, "out", q.shape, torch.bfloat16, q)
     _run("rd_causal_attention", q,
         cu_seqlens.numel() - 1, Hq, k.shape[1], D, float(scale), _ptr(q), _ptr(k), _ptr(v),
-        _ptr(cu_seqlens), T, int(max_seqlen), _ptr(out), _ptr(dev_status), stream=stream)
+        _ptr(cu_seqlens), T, _c_int("max_seqlen", max_seqlen), _ptr(out), _ptr(dev_status), stream=stream)
     return out
 
 
@@ -688,7 +696,7 @@ def rd_resize_pages(block_table, row_pages, page_refs, new_lens, page_size: int,
     _need_status(dev_status, block_table)
     _run("rd_resize_pages", block_table,
          _ptr(block_table), R, max_pages, _ptr(row_pages), _ptr(page_refs), page_refs.shape[0],
-         _ptr(new_lens), int(page_size), _ptr(dev_status), stream=stream)
+         _ptr(new_lens), _c_int("page_size", page_size), _ptr(dev_status), stream=stream)
     return row_pages
 
 
