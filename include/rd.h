@@ -187,8 +187,8 @@ rd_status rd_tree_attention_fp8(int B, int P_max, int Hq, int Hkv, int D, float 
  * k_pool,v_pool bf16 [num_pages, page_size, Hkv, D]
  * block_table  int32 [B, max_pages]: context position j of request b is row
  *              j % page_size of page block_table[b, j / page_size]
- * ctx_lens     int32 [B] context lengths (<= max_ctx and <= max_pages*page_size,
- *              else RD_DEV_BAD_LENGTH and the request is skipped)
+ * ctx_lens     int32 [B] context lengths (<= max_ctx, <= max_pages*page_size and
+ *              < 2^31 - 256, else RD_DEV_BAD_LENGTH and the request is skipped)
  * page_size    a multiple of 64 (RD_ERR_UNSUPPORTED otherwise); num_pages *
  *              page_size < 2^31.  A page id outside [0, num_pages) sets
  *              RD_DEV_BAD_INDEX (page 0 is read in its place).

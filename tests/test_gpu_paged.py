@@ -154,3 +154,39 @@ def test_paged_attention_13b_full_size_sampled():
             bf16_bits(inp["v_draft"][b:b + 1, :, h:h + 1]), bf16_bits(sub_k), bf16_bits(sub_v),
             sub_table, lens[b:b + 1], pk_ref["packed_len"][b:b + 1], pk_ref["mask"][b:b + 1])
         _close(got[b:b + 1, :, h:h + 1], ref, f"paged 13B b={b} h={h}")
+
+
+@pytest.mark.parametrize("B,Hkv", [(4, 4), (40, 40)])
+@pytest.mark.parametrize("call", ["paged", "shared, no groups"])
+def test_paged_context_at_the_end_of_31_bits_is_flagged(B, Hkv, call):
+    """A context whose last chunk would end behind 2^31 positions (its row names one page
+    over and over) is flagged and its rows are zeros; the others are as ever.  Chunk
+    ranges and whole units."""
+    import tree_attention_verify_gb300 as rd
+    P, D, page, width, n = 4, 64, 256, 2 ** 23, 3
+    gen = torch.Generator(device=DEV).manual_seed(B)
+    r = dict(dtype=torch.bfloat16, device=DEV, generator=gen)
+    q, kn, vn = (torch.randn(B, P, Hkv, D, **r) for _ in range(3))
+    kp, vp = (torch.randn(n, page, Hkv, D, **r) for _ in range(2))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.zeros((B, width), **i32)
+    table[:, :2] = torch.randint(0, n, (B, 2), **i32)
+    ctx = torch.randint(0, 2 * page + 1, (B,), **i32)
+    lens = torch.full((B,), P, **i32)
+    mask = (2 ** torch.arange(1, P + 1, device=DEV) - 1).to(torch.int32).expand(B, P)[..., None].contiguous()
+    short = [x.cpu().numpy() for x in (table[:, :2].contiguous(), ctx, lens)]
+    want = oracle.oracle_tree_attention_paged(bf16_bits(q), bf16_bits(kn), bf16_bits(vn), bf16_bits(kp), bf16_bits(vp),
+                                              *short, mask.cpu().numpy().view(np.uint32))
+    for wrong in (2 ** 31 - 1, 2 ** 31 - 256):
+        c, st = ctx.clone(), torch.zeros(1, **i32)
+        c[1] = wrong
+        kw = dict(max_ctx=2 ** 31 - 1, dev_status=st)
+        if call == "paged":
+            o = rd.rd_tree_attention_paged(q, kn, vn, kp, vp, table, c, lens, mask, **kw)
+        else:
+            none = torch.zeros(1, **i32)
+            o = rd.rd_tree_attention_shared(q, kn, vn, kp, vp, table, c, none, none[:0], lens, mask, **kw)
+        got = o.float().cpu().numpy()
+        assert st.item() == rd.DEV_BAD_LENGTH and (got[1] == 0).all()
+        rest = np.arange(B) != 1
+        assert (np.abs(got - want) <= 2e-2 + 1e-2 * np.abs(want))[rest].all()

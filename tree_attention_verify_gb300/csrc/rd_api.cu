@@ -192,7 +192,8 @@ rd_status rd_tree_attention_paged(int B, int P_max, int Hq, int Hkv, int D, floa
     pg.num_pages = num_pages;
     return from_cuda(rd_launch_attention(plan, B, P_max, Hq, Hkv, D, scale, q, k_new,
                                          v_new, num_pages > 0 ? k_pool : nullptr,
-                                         num_pages > 0 ? v_pool : nullptr, nullptr, 0, max_ctx,
+                                         num_pages > 0 ? v_pool : nullptr, nullptr, 0,
+                                         max_ctx < kRdMaxContext ? max_ctx : kRdMaxContext,
                                          packed_len, mask, mask_words, o, workspace,
                                          dev_status, (cudaStream_t)stream, &pg));
 }

@@ -23,6 +23,9 @@ int rd_device_sm_count();
 // Clock budget of the planted wait armed by rd_debug_stall_attention (0 = off).
 long long rd_attention_stall_budget();
 
+// Longest context of a request over pages: the kernels round it up to whole chunks in 32 bits.
+constexpr int kRdMaxContext = 0x7fffffff - 256;
+
 // Launchers (one per kernel family), called by the C entry points in rd_api.cu
 // after host-side validation.  Each returns the cudaGetLastError() of its launches.
 cudaError_t rd_launch_pack(const int32_t* beams, int B, int W, int L, int P_cap,

@@ -99,8 +99,6 @@ struct UnitCost {
 };
 
 // ------------------------------------------------------------------------ plan
-// The kernels round a context up to whole chunks in 32 bits.
-constexpr int kMaxContext = 0x7fffffff - 256;
 struct PlanArgs {
     int B, P_max, Hkv, G, page_size, max_pages, max_ctx, n_groups;
     int suffix_chunk;          // positions of a suffix chunk (0: the tcgen05 kernel divides by itself)
@@ -182,7 +180,7 @@ plan_kernel(const PlanArgs a)
                 ctx = a.ctx_lens[b];
                 len = a.lens[b];
             }
-            if (ctx < (len > 0 ? skip : 0) || ctx > a.max_ctx || ctx > kMaxContext ||
+            if (ctx < (len > 0 ? skip : 0) || ctx > a.max_ctx || ctx > kRdMaxContext ||
                 (long long)ctx > (long long)a.max_pages * a.page_size || len < 0 || len > a.P_max) {
                 rd_flag(a.status, RD_DEV_BAD_LENGTH);
                 len = 0;
