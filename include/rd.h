@@ -270,7 +270,8 @@ rd_status rd_tree_attention_shared(int B, int P_max, int Hq, int Hkv, int D, flo
  * new_ctx_lens int32 [B] (written; must not alias ctx_lens).
  * A best beam, accepted length, unpacker index or page id out of range sets
  * RD_DEV_BAD_INDEX; a position beyond max_pages*page_size sets
- * RD_DEV_BAD_LENGTH; the offending row is skipped.  The pages written to must be
+ * RD_DEV_BAD_LENGTH; the offending row is skipped.  A new length that leaves 31 bits
+ * sets RD_DEV_BAD_LENGTH, and nothing of that request is written.  The pages written to must be
  * held by no other row (see the page operators below).
  */
 rd_status rd_commit_accepted(int B, int W, int L, int P_max, int Hkv, int D,

@@ -190,3 +190,25 @@ def test_paged_context_at_the_end_of_31_bits_is_flagged(B, Hkv, call):
         assert st.item() == rd.DEV_BAD_LENGTH and (got[1] == 0).all()
         rest = np.arange(B) != 1
         assert (np.abs(got - want) <= 2e-2 + 1e-2 * np.abs(want))[rest].all()
+
+
+def test_commit_at_the_end_of_31_bits_is_flagged():
+    """A context length at the end of 31 bits (garbage, here) must not become a negative
+    position: flagged, nothing written for that request, the others as ever."""
+    import tree_attention_verify_gb300 as rd
+    i32 = dict(dtype=torch.int32, device=DEV)
+    B, L, Hkv, D, page, n = 4, 3, 2, 64, 64, 5
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    kn, vn = (torch.randn(B, L, Hkv, D, generator=gen, device=DEV).bfloat16() for _ in range(2))
+    unpacker = torch.arange(L, **i32).expand(B, 1, L).contiguous()
+    table, ctx = torch.arange(B, **i32)[:, None].contiguous(), torch.tensor([0, 2 ** 31 - 1, 30, 2 ** 31 - 3], **i32)
+    kp, vp = (torch.zeros(n, page, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    st = torch.zeros(1, **i32)
+    new = rd.rd_commit_accepted(kn, vn, unpacker, torch.zeros(B, **i32), torch.full((B,), L - 1, **i32), kp, vp, table, ctx,
+                                dev_status=st)
+    assert st.item() == rd.DEV_BAD_LENGTH
+    assert new.tolist() == [3, 2 ** 31 - 1, 33, 2 ** 31 - 3]
+    for pool, rows in ((kp, kn), (vp, vn)):
+        assert torch.equal(pool[0, :3], rows[0]) and torch.equal(pool[2, 30:33], rows[2])
+        assert not pool[0, 3:].any() and not pool[1].any() and not pool[2, :30].any() and not pool[2, 33:].any()
+        assert not pool[3:].any()

@@ -28,11 +28,13 @@ commit_kernel(int W, int L, int P_max, int row_vecs, const uint4* __restrict__ k
     const int b = blockIdx.y;
     const int w = best_beam[b], a = n_accepted[b], C = ctx_lens[b];
     const bool bad = w < 0 || w >= W || a < 0 || a >= L || C < 0;
+    const bool full = !bad && C > 0x7fffffff - a - 1;        // the new length leaves 31 bits
     if (i == 0 && threadIdx.x == 0) {
         if (bad) rd_flag(dev_status, RD_DEV_BAD_INDEX);
-        new_ctx_lens[b] = bad ? C : C + a + 1;
+        if (full) rd_flag(dev_status, RD_DEV_BAD_LENGTH);
+        new_ctx_lens[b] = bad || full ? C : C + a + 1;
     }
-    if (bad || i > a) return;
+    if (bad || full || i > a) return;
     const int pos = C + i;
     const int slot = pos / page_size;
     if (slot >= max_pages) {
