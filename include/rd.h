@@ -66,6 +66,7 @@ typedef enum { RD_BF16 = 0, RD_F16 = 1, RD_F32 = 2, RD_I32 = 3 } rd_dtype;
 #define RD_MAX_PACKED    256    /* P_cap / P_max                       */
 #define RD_MAX_ROWS    16384    /* rows of a block table, pairs of a fork (page operators) */
 #define RD_MAX_PAGES  262144    /* pages of a pool (page operators)     */
+#define RD_MAX_TOP        32    /* alternatives of rd_token_logprobs    */
 
 const char* rd_status_string(rd_status s);
 
@@ -399,6 +400,146 @@ rd_status rd_compact_pages(void* k_pool, void* v_pool, int layers, int num_pages
                            int32_t* dev_status, rd_stream_t stream);
 
 /*
+ * The quantised paged cache: K and V of the context in 8 or in 4 bits (TensorRT-LLM's
+ * quantised KV caching: NVIDIA blog "ReDrafter in TensorRT-LLM", introduction; the
+ * formats are the OCP ones).  A row is one position of one kv head:
+ *
+ *   bits 8  D e4m3 codes c; the value is g c
+ *   bits 4  D / 2 bytes of e2m1 codes c (element 2 j in the low half of byte j), then
+ *           D / 16 e4m3 scales s, one for each block of 16 elements; the value is g s c
+ *
+ * with g the tensor's scale, k_scale or v_scale (finite, > 0).  e2m1 has a sign, two
+ * exponent bits and one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6.  rd_quant_row_bytes is D for 8
+ * bits, D / 2 + D / 16 for 4 (0 for what is not supported).  Pools are
+ * [num_pages, page_size, Hkv, row bytes] with 16-byte aligned bases, tables as for
+ * rd_tree_attention_paged; the page operators above take the pools as they are.
+ * D in {64, 128}, bits in {4, 8} (RD_ERR_UNSUPPORTED otherwise).
+ *
+ * Writing a value x: in 8 bits c = e4m3(x / g); in 4 bits s = e4m3(min(448, amax / (6 g)))
+ * over the block, c = e2m1(x / (g s)), and c = 0 where s is 0.  All roundings are to
+ * the nearest, ties to the even code, and saturate; an infinity is stored as the largest value of
+ * its sign, and what a NaN is stored as is not defined.  A calibrated g is amax / 448 of
+ * the tensor for 8 bits, amax / (6 448) for 4.
+ */
+int rd_quant_row_bytes(int D, int bits);
+
+/*
+ * rd_append_quant -- write the K/V of prompt tokens (the context half of an in-flight
+ * batch, what rd_causal_attention attends to) to the quantised pages: token
+ * cu_seqlens[b] + i becomes position ctx_lens[b] + i of request b, and
+ * new_ctx_lens[b] = ctx_lens[b] + cu_seqlens[b+1] - cu_seqlens[b].
+ *
+ * k,v        bf16 [total_tokens, Hkv, D]; cu_seqlens int32 [B+1], ascending and within
+ *            [0, total_tokens] (tokens of no sequence are not written)
+ * new_ctx_lens int32 [B]; must not alias ctx_lens.
+ * A sequence outside these bounds, a negative context or a new length that leaves 31 bits
+ * sets RD_DEV_BAD_LENGTH, and nothing of that request is written (its new length is the
+ * old); a position beyond max_pages*page_size sets RD_DEV_BAD_LENGTH and a page id out
+ * of range RD_DEV_BAD_INDEX, and that row is skipped.  The pages written to must be held by no
+ * other row (see the page operators).
+ */
+rd_status rd_append_quant(int B, int Hkv, int D, int bits, const void* k, const void* v, int64_t total_tokens,
+                          const int32_t* cu_seqlens, void* k_pool, void* v_pool, float k_scale, float v_scale,
+                          int num_pages, int page_size, const int32_t* block_table, int max_pages,
+                          const int32_t* ctx_lens, int32_t* new_ctx_lens, int32_t* dev_status, rd_stream_t stream);
+
+/*
+ * rd_commit_accepted_quant -- rd_commit_accepted into the quantised pages: the same
+ * rows, positions, lengths and errors.
+ */
+rd_status rd_commit_accepted_quant(int B, int W, int L, int P_max, int Hkv, int D, int bits, const void* k_new,
+                                   const void* v_new, const int32_t* unpacker, const int32_t* best_beam,
+                                   const int32_t* n_accepted, void* k_pool, void* v_pool, float k_scale, float v_scale,
+                                   int num_pages, int page_size, const int32_t* block_table, int max_pages,
+                                   const int32_t* ctx_lens, int32_t* new_ctx_lens, int32_t* dev_status,
+                                   rd_stream_t stream);
+
+/*
+ * rd_read_quant -- the values of quantised rows in bf16, contiguous and ragged as
+ * rd_tree_attention takes a context: row offsets[b] + i of k_out and v_out is position
+ * starts[b] + i of request b, for i < offsets[b+1] - offsets[b].
+ *
+ * offsets    int64 [B+1], ascending and within [0, total] (RD_DEV_BAD_LENGTH); rows of the
+ *            outputs that belong to no request are left as they are
+ * starts     int32 [B], or null: 0.  A negative one, or a position beyond
+ *            max_pages*page_size, sets RD_DEV_BAD_LENGTH, a page id out of range
+ *            RD_DEV_BAD_INDEX: that row is zeros.
+ * k_out,v_out bf16 [total, Hkv, D]: g s c (g c) rounded once
+ */
+rd_status rd_read_quant(int B, int Hkv, int D, int bits, const void* k_pool, const void* v_pool, float k_scale, float v_scale,
+                        int num_pages, int page_size, const int32_t* block_table, int max_pages, const int64_t* offsets,
+                        const int32_t* starts, int64_t total, void* k_out, void* v_out, int32_t* dev_status,
+                        rd_stream_t stream);
+
+/*
+ * rd_tree_attention_quant -- rd_tree_attention_paged over the quantised pages: the
+ * packed drafts stay bf16 (they are quantised when they are committed).  Single-token decoding
+ * is the case P_max = 1.
+ *
+ * Everything as rd_tree_attention_paged (page_size a multiple of 64; a context longer than
+ * max_ctx or than its table row sets RD_DEV_BAD_LENGTH and the request is skipped, its rows
+ * zeros; a page id out of range sets RD_DEV_BAD_INDEX and page 0 is read in its place; a
+ * row that sees no key is zeros), and:
+ * workspace  rd_tree_attention_quant_workspace_size() bytes, 16-byte aligned, no initial
+ *            contents; the size depends on the SM count of the current device.  Calls that
+ *            share a workspace must not overlap in time.
+ * Queries may have any finite value; elements below 2^-28 of their row's largest may lose
+ * precision.  K and V of the packed drafts must be finite.  A NaN code of a cached row
+ * (e4m3 0x7f, 0xff, as a code or a block's scale) makes what sees it NaN.  What lies behind a
+ * context's end in its last page, and behind packed_len, may hold anything.
+ */
+size_t rd_tree_attention_quant_workspace_size(int B, int P_max, int Hq, int Hkv, int D, int max_ctx);
+rd_status rd_tree_attention_quant(int B, int P_max, int Hq, int Hkv, int D, int bits, float scale, const void* q,
+                                  const void* k_new, const void* v_new, const void* k_pool, const void* v_pool,
+                                  float k_scale, float v_scale, int num_pages, int page_size, const int32_t* block_table,
+                                  int max_pages, const int32_t* ctx_lens, int max_ctx, const int32_t* packed_len,
+                                  const uint32_t* mask, int mask_words, void* o, void* workspace, size_t ws_bytes,
+                                  int32_t* dev_status, rd_stream_t stream);
+
+/*
+ * rd_token_logprobs -- log probabilities of given tokens, with the entropy and the most
+ * likely alternatives of their distributions: what a server answers beside the tokens that
+ * rd_greedy_accept or rd_sample_accept emits, and the scores of a prompt's tokens.
+ *
+ * For entry i, with x = logits[rows[i]] (logits[i] where rows is null) and
+ * p = softmax(x / temperature):
+ *   logprob[i] = log p(tokens[i]),  entropy[i] = -sum_v p(v) log p(v)   (natural logarithms)
+ *   top_tokens[i, 0 .. top-1]       the tokens with the largest logits, largest first, the
+ *                                   lower id first among equals; top_logprobs their log p
+ *
+ * logits     [n_rows, V] of dt: RD_BF16, RD_F16 or RD_F32 (rows need no alignment beyond
+ *            their elements')
+ * rows, tokens int32 [n]; without rows n <= n_rows.  tokens[i] == -1: no entry, all of its
+ *            outputs are 0, its top_tokens -1.  Another token outside [0, V) sets
+ *            RD_DEV_BAD_TOKEN and a row outside [0, n_rows) RD_DEV_BAD_INDEX: the same.
+ * logprob, entropy fp32 [n]; top_tokens int32 [n, top], top_logprobs fp32 [n, top] (may be
+ *            null when top == 0)
+ * temperature finite, at least 2^-126; 0 <= top <= V; top <= RD_MAX_TOP, V <= 2^30
+ *            (RD_ERR_UNSUPPORTED).
+ * Logits of -inf have probability 0 and add nothing to the entropy.  A row with a NaN or
+ * +inf, or of -inf alone, has no distribution: its logprob, entropy and top_logprobs are NaN.
+ * Sums are fp32.  No workspace.
+ */
+rd_status rd_token_logprobs(const void* logits, rd_dtype dt, int64_t n_rows, int V, const int32_t* rows,
+                            const int32_t* tokens, int64_t n, float temperature, int top, float* logprob, float* entropy,
+                            int32_t* top_tokens, float* top_logprobs, int32_t* dev_status, rd_stream_t stream);
+
+/*
+ * rd_accepted_logprobs -- rd_token_logprobs of the tokens that a verification step emitted:
+ * entry (b, i), i <= n_accepted[b], is token out_tokens[b, i] under the logits at packed node
+ * unpacker[b, best_beam[b], i]; entries behind them are 0 and -1.
+ *
+ * logits [B, P_max, V]; unpacker int32 [B, W, L]; best_beam, n_accepted int32 [B];
+ * out_tokens int32 [B, L], as rd_greedy_accept and rd_sample_accept write them.  Outputs
+ * [B, L] and [B, L, top].  A beam, an accepted length or a node out of range sets RD_DEV_BAD_INDEX
+ * (outputs 0 and -1).
+ */
+rd_status rd_accepted_logprobs(const void* logits, rd_dtype dt, int B, int P_max, int V, const int32_t* unpacker, int W, int L,
+                               const int32_t* best_beam, const int32_t* n_accepted, const int32_t* out_tokens,
+                               float temperature, int top, float* logprob, float* entropy, int32_t* top_tokens,
+                               float* top_logprobs, int32_t* dev_status, rd_stream_t stream);
+
+/*
  * rd_causal_attention -- causal prefill of the context-phase requests of an
  * in-flight batch (NVIDIA blog "ReDrafter in TensorRT-LLM", section
  * "Inflight-batching Compatible Engine": the batch splits into a context and a
@@ -504,8 +645,9 @@ rd_status rd_greedy_accept(const void* logits, int B, int P_max, int V,
  * counterpart: it exists to test the kernels' bounded waits without a GPU fault.
  *
  * budget_cycles > 0 arms it for every later rd_tree_attention,
- * rd_tree_attention_paged, rd_tree_attention_shared, rd_tree_attention_fp8 and
- * rd_causal_attention launch of this process: before its first MMA, each CTA's MMA-issuing thread
+ * rd_tree_attention_paged, rd_tree_attention_shared, rd_tree_attention_quant, rd_tree_attention_fp8
+ * and rd_causal_attention launch of this process: before its first MMA, each CTA's MMA-issuing thread
+ * (or its computing warps)
  * waits on a barrier that nothing completes, for at most budget_cycles SM
  * clock cycles.  That wait runs out, the CTA records RD_DEV_TIMEOUT, its other
  * roles stop at their next wait, it waits (with the normal budget) for the

@@ -1,0 +1,209 @@
+"""rd_token_logprobs and rd_accepted_logprobs against 64-bit numpy."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import quant as oq
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def _rd():
+    import tree_attention_verify_gb300 as rd
+    return rd
+
+
+def _d(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def check(out, i, x, token, T=1.0, top=0):
+    """fp32 sums of V terms over 256 threads or more, each 2^z off by 2^-21 and z by 2^-22 of
+    itself; the same for the products of the entropy, relative to sum p |log p|."""
+    x = x.double().cpu().numpy()
+    lp, h, ids, tops, hs = oq.logprobs(x, token, T, top)
+    eps = (len(x) / 256 + 60) * 2.0 ** -24 + 2.0 ** -20
+    got = {k: v[i].cpu().numpy() for k, v in out.items()}
+    close = lambda a, b: a == b or abs(a - b) <= eps * (1 + hs) + abs(b) * 2.0 ** -21
+    assert close(float(got["logprob"]), lp), (got["logprob"], lp)
+    assert abs(float(got["entropy"]) - h) <= eps * (1 + 2 * hs), (got["entropy"], h)
+    np.testing.assert_array_equal(got["top_tokens"], ids)
+    assert all(close(a, b) for a, b in zip(got["top_logprobs"].astype(float), tops))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,V,top", [(1, 1, 1), (3, 2, 2), (5, 40, 32), (2, 997, 0), (7, 1000, 5), (1, 4096, 32),
+                                     (3, 16385, 8), (1, 32001, 20), (2, 128256, 20), (700, 2051, 3), (310, 9000, 32)])
+def test_rows(dtype, n, V, top):
+    rd = _rd()
+    gen = torch.Generator(device=DEV).manual_seed(V)
+    x = (2.5 * torch.randn(n, V, generator=gen, device=DEV)).to(TYPES[dtype])
+    tokens = torch.randint(0, V, (n,), generator=gen, device=DEV, dtype=torch.int32)
+    T = 1.0 if n % 2 else 0.6
+    st = _status()
+    out = rd.rd_token_logprobs(x, tokens, top=top, temperature=T, dev_status=st)
+    assert int(st) == 0
+    for i in sorted({0, n // 2, n - 1, min(n - 1, 5)}):
+        check(out, i, x[i], int(tokens[i]), float(np.float32(T)), top)
+
+
+@pytest.mark.parametrize("V", [5, 300, 20000, 70001])
+def test_equal_logits(V):
+    """Every logit alike (the list of candidates overfills), or two values."""
+    rd = _rd()
+    top = min(V, 32)
+    x = torch.zeros(3, V, dtype=torch.bfloat16, device=DEV)
+    x[1, 1::2] = -0.0
+    x[2, V // 2:] = 3.0
+    out = rd.rd_token_logprobs(x, _i32([0, V - 1, 0]), top=top)
+    for i, token in enumerate((0, V - 1, 0)):
+        check(out, i, x[i], token, 1.0, top)
+
+
+@pytest.mark.parametrize("V", [3000, 50001, 128256])
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_sorted_logits(V, order):
+    """A row that keeps rising passes the threshold all the way."""
+    rd = _rd()
+    x = torch.linspace(-20, 20, V, device=DEV)
+    x = (x if order == "rising" else x.flip(0)).expand(2, V).contiguous()
+    for t in (x, x.bfloat16()):
+        out = rd.rd_token_logprobs(t, _i32([0, V - 1]), top=32)
+        check(out, 0, t[0], 0, 1.0, 32)
+        check(out, 1, t[1], V - 1, 1.0, 32)
+
+
+def test_masked_logits():
+    """-inf in all but a few places, as a grammar leaves them."""
+    rd = _rd()
+    V = 32000
+    x = torch.full((4, V), -float("inf"), device=DEV)
+    x[0, 31999] = 3.0
+    x[1, [5, 700, 30000]] = torch.tensor([-1e4, -1e4 + 1, -1e4], device=DEV)
+    x[2, ::7] = torch.randn(len(range(0, V, 7)), device=DEV)
+    x[3, 17] = -3e38
+    tokens = [31999, 6, 7, 17]
+    for t in (x, x.bfloat16()):
+        out = rd.rd_token_logprobs(t, _i32(tokens), top=8)
+        for i in range(4):
+            check(out, i, t[i], tokens[i], 1.0, 8)
+    x[:] = -float("inf")
+    x[1, 5], x[2, 9] = float("nan"), float("inf")
+    out = rd.rd_token_logprobs(x, _i32([0, 5, 9, 3]), top=2)
+    for k in ("logprob", "entropy", "top_logprobs"):
+        assert torch.isnan(out[k][:3]).all()
+    assert out["top_tokens"][0].tolist() == [0, 1] and int(out["top_tokens"][2, 0]) == 9
+    assert ((out["top_tokens"] >= 0) & (out["top_tokens"] < V)).all()
+
+
+def test_far_and_large_logits():
+    rd = _rd()
+    x = torch.tensor([[1e30, 0.0, -1e30, 5e29], [60000.0, 59999.0, 0.0, -60000.0], [1e-30, 0.0, -1e-30, 0.0],
+                      [0.0, 200.0, 100.0, 199.5]], device=DEV)
+    for T in (1.0, 1e-3, 1e6):
+        out = rd.rd_token_logprobs(x, _i32([0, 1, 2, 3]), top=4, temperature=T)
+        for i in range(4):
+            check(out, i, x[i], i, float(np.float32(T)), 4)
+    # each thread's first logits far below the others
+    V = 40000
+    y = torch.full((1, V), -500.0, device=DEV)
+    y[0, 20000:] = torch.linspace(0, 100, V - 20000, device=DEV)
+    check(rd.rd_token_logprobs(y, _i32([V - 1]), top=3), 0, y[0], V - 1, 1.0, 3)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_unaligned_rows_and_row_indices(dtype):
+    """Rows that start anywhere; the same row twice; entries that are skipped; nothing is read outside."""
+    rd = _rd()
+    V, n_rows = 1001, 6
+    flat = torch.full((n_rows * V + 16,), float("nan"), dtype=TYPES[dtype], device=DEV)
+    for shift in (0, 1, 3, 7):
+        x = flat[shift:shift + n_rows * V].view(n_rows, V)
+        x.copy_(torch.randn(n_rows, V, device=DEV) * 3)
+        rows, tokens = [5, 0, 0, 3, 2, 6, -1, 1], [7, V - 1, 0, -1, V, 3, 4, -5]
+        st = _status()
+        out = rd.rd_token_logprobs(x, _i32(tokens), rows=_i32(rows), top=3, dev_status=st)
+        assert int(st) == rd.DEV_BAD_TOKEN | rd.DEV_BAD_INDEX
+        for i in (0, 1, 2):
+            check(out, i, x[rows[i]], tokens[i], 1.0, 3)
+        assert (out["logprob"][3:] == 0).all() and (out["entropy"][3:] == 0).all()
+        assert (out["top_tokens"][3:] == -1).all() and (out["top_logprobs"][3:] == 0).all()
+        flat.fill_(float("nan"))
+
+
+def test_accepted():
+    rd = _rd()
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    B, W, L, V, top = 6, 3, 4, 5000, 5
+    beams = torch.randint(0, 3, (B, W, L), generator=gen, device=DEV, dtype=torch.int32)
+    beams[:, :, 0] = 1
+    pk = rd.rd_pack_beams(beams)
+    P = W * L
+    logits = (2 * torch.randn(B, P, V, generator=gen, device=DEV)).bfloat16()
+    logits[:, :, :3] += 9
+    acc = rd.rd_greedy_accept(logits, beams, pk["unpacker"], pk["packed_len"])
+    st = _status()
+    out = rd.rd_accepted_logprobs(logits, pk["unpacker"], acc["best_beam"], acc["n_accepted"], acc["out_tokens"], top=top,
+                                  dev_status=st)
+    assert int(st) == 0
+    for b in range(B):
+        a = int(acc["n_accepted"][b])
+        for i in range(L):
+            if i <= a:
+                node = int(pk["unpacker"][b, int(acc["best_beam"][b]), i])
+                token = int(acc["out_tokens"][b, i])
+                check({k: v[b] for k, v in out.items()}, i, logits[b, node], token, 1.0, top)
+                assert int(out["top_tokens"][b, i, 0]) == token       # greedy
+            else:
+                assert out["logprob"][b, i] == 0 and (out["top_tokens"][b, i] == -1).all()
+    # wrong beams, lengths and nodes
+    best, n, unp = acc["best_beam"].clone(), acc["n_accepted"].clone(), pk["unpacker"].clone()
+    best[0], n[1] = W, L
+    unp[2, int(best[2]), 0] = P
+    got = rd.rd_accepted_logprobs(logits, unp, best, n, acc["out_tokens"], top=top, dev_status=st)
+    assert int(st) == rd.DEV_BAD_INDEX
+    assert (got["top_tokens"][:2] == -1).all() and (got["top_tokens"][2, 0] == -1).all() and (got["logprob"][:2] == 0).all()
+    for k in out:
+        assert torch.equal(got[k][3:], out[k][3:])
+
+
+def test_graph_stream_and_given_outputs():
+    rd = _rd()
+    x = torch.randn(9, 30000, device=DEV).bfloat16()
+    t = _i32(range(9))
+    want = rd.rd_token_logprobs(x, t, top=4)
+    out = {k: torch.empty_like(v) for k, v in want.items()}
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        assert rd.rd_token_logprobs(x, t, top=4, out=out)["entropy"] is out["entropy"]
+    for _ in range(2):
+        for v in out.values():
+            v.zero_()
+        g.replay()
+        assert all(torch.equal(out[k], want[k]) for k in want)
+    torch.cuda.synchronize()
+    got = rd.rd_token_logprobs(x, t, top=4, stream=side)
+    side.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    none = rd.rd_token_logprobs(x, t[:0], top=4)
+    assert none["top_tokens"].shape == (0, 4)
+
+
+def test_rows_past_32_bits():
+    rd = _rd()
+    V, n_rows = 131072, 17000                 # 2^31 logits and some
+    x = torch.zeros(n_rows, V, dtype=torch.bfloat16, device=DEV)
+    x[-1] = torch.randn(V, device=DEV).bfloat16()
+    out = rd.rd_token_logprobs(x, _i32([5]), rows=_i32([n_rows - 1]), top=2)
+    check(out, 0, x[-1], 5, 1.0, 2)

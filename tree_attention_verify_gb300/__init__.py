@@ -26,7 +26,10 @@ __all__ = [
     "rd_tree_attention_paged", "rd_tree_attention_shared",
     "rd_tree_attention_shared_workspace_size", "rd_commit_accepted", "rd_beam_search_step",
     "rd_tree_attention_fp8", "rd_sample_accept", "rd_resize_pages", "rd_fork_pages",
-    "rd_copy_pages", "rd_compact_pages", "rd_debug_stall_attention", "RdError",
+    "rd_copy_pages", "rd_compact_pages", "rd_quant_row_bytes", "rd_append_quant",
+    "rd_commit_accepted_quant", "rd_read_quant", "rd_tree_attention_quant",
+    "rd_tree_attention_quant_workspace_size", "rd_token_logprobs", "rd_accepted_logprobs",
+    "rd_debug_stall_attention", "RdError",
     "DEV_BAD_INDEX", "DEV_BAD_TOKEN", "DEV_OVERFLOW", "DEV_BAD_LENGTH", "DEV_TIMEOUT",
     "lib_path",
 ]
@@ -78,6 +81,15 @@ def _load() -> ctypes.CDLL:
         "rd_copy_pages": [P, P, I, I, S, P, P, I, P, S, P, P],
         "rd_compact_pages_workspace_size": [I],
         "rd_compact_pages": [P, P, I, I, S, P, I, I, P, P, P, P, P, S, P, P],
+        "rd_quant_row_bytes": [I, I],
+        "rd_append_quant": [I, I, I, I, P, P, I64, P, P, P, F, F, I, I, P, I, P, P, P, P],
+        "rd_commit_accepted_quant": [I, I, I, I, I, I, I, P, P, P, P, P, P, P, F, F, I, I, P, I, P, P, P, P],
+        "rd_read_quant": [I, I, I, I, P, P, F, F, I, I, P, I, P, P, I64, P, P, P, P],
+        "rd_tree_attention_quant_workspace_size": [I, I, I, I, I, I],
+        "rd_tree_attention_quant": [I, I, I, I, I, I, F, P, P, P, P, P, F, F, I, I, P, I, P, I, P, P, I, P, P, S,
+                                    P, P],
+        "rd_token_logprobs": [P, I, I64, I, P, P, I64, F, I, P, P, P, P, P, P],
+        "rd_accepted_logprobs": [P, I, I, I, I, P, I, I, P, P, P, F, I, P, P, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -763,6 +775,258 @@ def rd_compact_pages(k_pool, v_pool, block_table, row_pages, page_refs, *, remap
          _ptr(row_pages), _ptr(page_refs), _ptr(remap), _ptr(n_live), ws, ws_bytes, _ptr(dev_status),
          stream=stream)
     return remap, n_live
+
+
+# ----------------------------------------------------------------------------
+# the quantised paged cache
+# ----------------------------------------------------------------------------
+def rd_quant_row_bytes(D: int, bits: int) -> int:
+    """Bytes of a row (one position of one kv head) of a cache in 4 or 8 bits."""
+    return int(_lib.rd_quant_row_bytes(D, bits))
+
+
+_ROWS = {(D, D): 8 for D in (64, 128)}
+_ROWS.update({(D // 2 + D // 16, D): 4 for D in (64, 128)})
+_DIM_OF_ROW = {row: D for row, D in _ROWS}
+
+
+def _quant_pools(k_pool, v_pool, block_table, D=None, device=None):
+    """(num_pages, page_size, Hkv, D, bits, table's width) of uint8 pools
+    [num_pages, page_size, Hkv, row bytes] and their block table."""
+    index = _index(k_pool) if device is None else device.index
+    if not (_fine(index, torch.uint8, 4, k_pool, v_pool) and _fine(index, torch.int32, 2, block_table)):
+        _need(k_pool, "k_pool", torch.uint8, device, ndim=4)
+        _need(v_pool, "v_pool", torch.uint8, k_pool.device, ndim=4)
+        _need(block_table, "block_table", torch.int32, k_pool.device, ndim=2)
+    num_pages, page_size, Hkv, row = k_pool.shape
+    if D is None:
+        D = _DIM_OF_ROW.get(row)
+    bits = _ROWS.get((row, D))
+    if bits is None:
+        raise ValueError(f"k_pool/v_pool must be [num_pages, page_size, Hkv, row bytes] with rows of D bytes (8 bits) or "
+                         f"D / 2 + D / 16 (4 bits) and D = 64 or 128; got {tuple(k_pool.shape)}"
+                         + ("" if D is None else f" for D = {D}"))
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must have one shape")
+    return num_pages, page_size, Hkv, D, bits, block_table.shape[1]
+
+
+def _of_batch(B: int, device_index: int, **tensors):
+    for name, t in tensors.items():
+        if not _fine(device_index, torch.int32, 1, t):
+            _need(t, name, torch.int32, torch.device("cuda", device_index), ndim=1)
+        if t.shape[0] != B:
+            raise ValueError(f"{name} must be [{B}], got {tuple(t.shape)}")
+
+
+def _new_lens(new_ctx_lens, ctx_lens, like, stream):
+    if new_ctx_lens is None:
+        return _new(ctx_lens.shape, torch.int32, like, stream)
+    _out(new_ctx_lens, "new_ctx_lens", ctx_lens.shape, torch.int32, like)
+    if new_ctx_lens.data_ptr() == ctx_lens.data_ptr() and ctx_lens.numel() > 0:
+        raise ValueError("new_ctx_lens must not alias ctx_lens")
+    return new_ctx_lens
+
+
+def rd_append_quant(k, v, cu_seqlens, k_pool, v_pool, k_scale: float, v_scale: float, block_table, ctx_lens, *,
+                    new_ctx_lens=None, dev_status=None, stream=None) -> torch.Tensor:
+    """Quantise the K/V of prompt tokens (k, v bf16 [T, Hkv, D], cu_seqlens int32 [B+1]) into the
+    pages behind ctx_lens (int32 [B]); the pools, uint8 [num_pages, page_size, Hkv, row bytes], change in
+    place.  Returns new_ctx_lens (see rd_append_quant in rd.h)."""
+    index = _index(k)
+    if not _fine(index, torch.bfloat16, 3, k, v):
+        _need(k, "k", torch.bfloat16, ndim=3)
+        _need(v, "v", torch.bfloat16, k.device, ndim=3)
+        index = k.get_device()
+    T, Hkv, D = k.shape
+    num_pages, page_size, heads, _, bits, width = _quant_pools(k_pool, v_pool, block_table, D, k.device)
+    if v.shape != k.shape or heads != Hkv:
+        raise ValueError("k/v must be [T, Hkv, D] with the pools' heads")
+    B = block_table.shape[0]
+    _of_batch(B, index, ctx_lens=ctx_lens)
+    _of_batch(B + 1, index, cu_seqlens=cu_seqlens)
+    _need_status(dev_status, k)
+    new_ctx_lens = _new_lens(new_ctx_lens, ctx_lens, k, stream)
+    _run("rd_append_quant", k,
+         B, Hkv, D, bits, k.data_ptr(), v.data_ptr(), T, cu_seqlens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+         float(k_scale), float(v_scale), num_pages, page_size, block_table.data_ptr(), width, ctx_lens.data_ptr(),
+         new_ctx_lens.data_ptr(), _ptr(dev_status), stream=stream)
+    return new_ctx_lens
+
+
+def rd_commit_accepted_quant(k_new, v_new, unpacker, best_beam, n_accepted, k_pool, v_pool, k_scale: float,
+                             v_scale: float, block_table, ctx_lens, *, new_ctx_lens=None, dev_status=None,
+                             stream=None) -> torch.Tensor:
+    """rd_commit_accepted into the quantised pages (pools as for rd_append_quant, modified in
+    place).  Returns new_ctx_lens = ctx_lens + n_accepted + 1 (see rd.h)."""
+    index = _index(k_new)
+    if not (_fine(index, torch.bfloat16, 4, k_new, v_new) and _fine(index, torch.int32, 3, unpacker)):
+        _need(k_new, "k_new", torch.bfloat16, ndim=4)
+        _need(v_new, "v_new", torch.bfloat16, k_new.device, ndim=4)
+        _need(unpacker, "unpacker", torch.int32, k_new.device, ndim=3)
+        index = k_new.get_device()
+    B, P, Hkv, D = k_new.shape
+    num_pages, page_size, heads, _, bits, width = _quant_pools(k_pool, v_pool, block_table, D, k_new.device)
+    if v_new.shape != k_new.shape or heads != Hkv or unpacker.shape[0] != B or block_table.shape[0] != B:
+        raise ValueError("k_new/v_new must be [B, P_max, Hkv, D] with the pools' heads, unpacker and block_table of B")
+    _, W, L = unpacker.shape
+    _of_batch(B, index, best_beam=best_beam, n_accepted=n_accepted, ctx_lens=ctx_lens)
+    _need_status(dev_status, k_new)
+    new_ctx_lens = _new_lens(new_ctx_lens, ctx_lens, k_new, stream)
+    _run("rd_commit_accepted_quant", k_new,
+         B, W, L, P, Hkv, D, bits, k_new.data_ptr(), v_new.data_ptr(), unpacker.data_ptr(), best_beam.data_ptr(),
+         n_accepted.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), float(k_scale), float(v_scale), num_pages, page_size,
+         block_table.data_ptr(), width, ctx_lens.data_ptr(), new_ctx_lens.data_ptr(), _ptr(dev_status), stream=stream)
+    return new_ctx_lens
+
+
+def rd_read_quant(k_pool, v_pool, k_scale: float, v_scale: float, block_table, offsets, *, total: int, starts=None,
+                  k_out=None, v_out=None, dev_status=None, stream=None):
+    """The values of quantised rows, bf16 [total, Hkv, D]: rows offsets[b] .. offsets[b+1] - 1
+    (int64 [B+1]) are the positions of request b from starts[b] (int32 [B]; None: 0).  Returns
+    (k, v), laid out as rd_tree_attention takes a context (see rd_read_quant in rd.h)."""
+    num_pages, page_size, Hkv, D, bits, width = _quant_pools(k_pool, v_pool, block_table)
+    B = block_table.shape[0]
+    index = k_pool.get_device()
+    if not _fine(index, torch.int64, 1, offsets):
+        _need(offsets, "offsets", torch.int64, k_pool.device, ndim=1)
+    if offsets.shape[0] != B + 1:
+        raise ValueError(f"offsets must be [{B + 1}], got {tuple(offsets.shape)}")
+    if starts is not None:
+        _of_batch(B, index, starts=starts)
+    total = int(total)
+    if not 0 <= total < 2 ** 63:
+        raise ValueError(f"total must be a length, got {total}")
+    _need_status(dev_status, k_pool)
+    shape = (total, Hkv, D)
+    k_out = _new(shape, torch.bfloat16, k_pool, stream) if k_out is None else \
+        _out(k_out, "k_out", shape, torch.bfloat16, k_pool)
+    v_out = _new(shape, torch.bfloat16, k_pool, stream) if v_out is None else \
+        _out(v_out, "v_out", shape, torch.bfloat16, k_pool)
+    _run("rd_read_quant", k_pool,
+         B, Hkv, D, bits, k_pool.data_ptr(), v_pool.data_ptr(), float(k_scale), float(v_scale), num_pages, page_size,
+         block_table.data_ptr(), width, offsets.data_ptr(), _ptr(starts), total, k_out.data_ptr(), v_out.data_ptr(),
+         _ptr(dev_status), stream=stream)
+    return k_out, v_out
+
+
+def rd_tree_attention_quant_workspace_size(B: int, P_max: int, Hq: int, Hkv: int, D: int, max_ctx: int,
+                                           device=None) -> int:
+    """Bytes of workspace of rd_tree_attention_quant on `device` (else the current one)."""
+    f = _lib.rd_tree_attention_quant_workspace_size
+    if device is not None and torch.device(device).type == "cuda":
+        with torch.cuda.device(device):
+            return int(f(B, P_max, Hq, Hkv, D, _c_int("max_ctx", max_ctx)))
+    return int(f(B, P_max, Hq, Hkv, D, _c_int("max_ctx", max_ctx)))
+
+
+def rd_tree_attention_quant(q, k_new, v_new, k_pool, v_pool, k_scale: float, v_scale: float, block_table, ctx_lens,
+                            packed_len, mask, *, max_ctx: int, scale: float = 0.0, out=None, workspace=None,
+                            dev_status=None, stream=None) -> torch.Tensor:
+    """rd_tree_attention_paged over a cache held in 4 or 8 bits: k_pool/v_pool uint8
+    [num_pages, page_size, Hkv, row bytes], whose rows' size tells the format (see
+    rd_quant_row_bytes, and rd_tree_attention_quant in rd.h)."""
+    index = _index(q)
+    if not _fine(index, torch.bfloat16, 4, q, k_new, v_new):
+        _need(q, "q", torch.bfloat16, ndim=4)
+        _need(k_new, "k_new", torch.bfloat16, q.device, ndim=4)
+        _need(v_new, "v_new", torch.bfloat16, q.device, ndim=4)
+        index = q.get_device()
+    B, P, Hq, D = q.shape
+    num_pages, page_size, Hkv, _, bits, width = _quant_pools(k_pool, v_pool, block_table, D, q.device)
+    if k_new.shape != (B, P, Hkv, D) or v_new.shape != k_new.shape:
+        raise ValueError("k_new/v_new must be [B, P_max, Hkv, D] with the pools' heads")
+    _of_batch(B, index, ctx_lens=ctx_lens, packed_len=packed_len)
+    if (not isinstance(mask, torch.Tensor) or mask.dim() != 3 or not mask.is_contiguous()
+            or mask.element_size() != 4 or mask.get_device() != index or mask.shape[:2] != (B, P)):
+        raise ValueError("mask must be a contiguous 32-bit [B, P_max, NW] tensor on q's device")
+    if block_table.shape[0] != B:
+        raise ValueError("block_table does not match the batch")
+    _need_status(dev_status, q)
+    out = _new(q.shape, torch.bfloat16, q, stream) if out is None else _out(out, "out", q.shape, torch.bfloat16, q)
+    if workspace is None:
+        workspace = _scratch(None, rd_tree_attention_quant_workspace_size(B, P, Hq, Hkv, D, max_ctx, q.device), q, stream)
+    else:
+        workspace = _scratch(workspace, 0, q, stream)   # its size is checked by the call
+    _run("rd_tree_attention_quant", q,
+         B, P, Hq, Hkv, D, bits, float(scale), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(),
+         v_pool.data_ptr(), float(k_scale), float(v_scale), num_pages, page_size, block_table.data_ptr(), width,
+         ctx_lens.data_ptr(), _c_int("max_ctx", max_ctx), packed_len.data_ptr(), mask.data_ptr(), mask.shape[2],
+         out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(dev_status), stream=stream)
+    return out
+
+
+# ----------------------------------------------------------------------------
+# log probabilities
+# ----------------------------------------------------------------------------
+def _logits_type(logits, ndim):
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    _need(logits, "logits", logits.dtype, ndim=ndim)
+    return _DTYPES[logits.dtype]
+
+
+def _logprob_outs(out, shape, top, like, stream) -> dict:
+    shapes = dict(logprob=shape, entropy=shape, top_tokens=(*shape, top), top_logprobs=(*shape, top))
+    types = dict(logprob=torch.float32, entropy=torch.float32, top_tokens=torch.int32, top_logprobs=torch.float32)
+    if out is not None and not isinstance(out, dict):
+        raise TypeError("out must be a dict of tensors")
+    return {k: _out(out[k], f"out[{k!r}]", shapes[k], types[k], like) if out is not None and k in out
+            else _new(shapes[k], types[k], like, stream) for k in shapes}
+
+
+def rd_token_logprobs(logits, tokens, *, rows=None, top: int = 0, temperature: float = 1.0, out=None, dev_status=None,
+                      stream=None) -> dict:
+    """Log probabilities of tokens (int32 [n], -1: no entry) under softmax(logits / temperature),
+    logits [n_rows, V] bf16, fp16 or fp32, entry i under row rows[i] (int32 [n]; None: i).  Returns
+    dict(logprob [n], entropy [n], top_tokens [n, top], top_logprobs [n, top]) (see
+    rd_token_logprobs in rd.h)."""
+    dt = _logits_type(logits, 2)
+    n_rows, V = logits.shape
+    index = logits.get_device()
+    if not _fine(index, torch.int32, 1, tokens):
+        _need(tokens, "tokens", torch.int32, logits.device, ndim=1)
+    n, top = tokens.shape[0], _c_int("top", top)
+    if rows is not None:
+        _of_batch(n, index, rows=rows)
+    elif n > n_rows:
+        raise ValueError(f"tokens must be [n] with n <= {n_rows}, got {tuple(tokens.shape)}")
+    _need_status(dev_status, logits)
+    out = _logprob_outs(out, (n,), max(0, top), logits, stream)
+    _run("rd_token_logprobs", logits,
+         logits.data_ptr(), dt, n_rows, V, _ptr(rows), tokens.data_ptr(), n, float(temperature), top,
+         out["logprob"].data_ptr(), out["entropy"].data_ptr(), out["top_tokens"].data_ptr(),
+         out["top_logprobs"].data_ptr(), _ptr(dev_status), stream=stream)
+    return out
+
+
+def rd_accepted_logprobs(logits, unpacker, best_beam, n_accepted, out_tokens, *, top: int = 0, temperature: float = 1.0,
+                         out=None, dev_status=None, stream=None) -> dict:
+    """Log probabilities of the tokens that a verification step emitted: out_tokens[b, i] (int32 [B, L], as
+    rd_greedy_accept and rd_sample_accept write them) under logits [B, P_max, V] at node unpacker[b, best_beam[b], i].
+    Returns dict(logprob [B, L], entropy [B, L], top_tokens [B, L, top], top_logprobs [B, L, top]); entries
+    behind n_accepted are 0 and -1 (see rd_accepted_logprobs in rd.h)."""
+    dt = _logits_type(logits, 3)
+    B, P, V = logits.shape
+    index = logits.get_device()
+    if not (_fine(index, torch.int32, 3, unpacker) and _fine(index, torch.int32, 2, out_tokens)):
+        _need(unpacker, "unpacker", torch.int32, logits.device, ndim=3)
+        _need(out_tokens, "out_tokens", torch.int32, logits.device, ndim=2)
+    W, L = unpacker.shape[1:]
+    if unpacker.shape[0] != B or out_tokens.shape != (B, L):
+        raise ValueError(f"unpacker must be [{B}, W, L] and out_tokens [{B}, L], got {tuple(unpacker.shape)} and "
+                         f"{tuple(out_tokens.shape)}")
+    _of_batch(B, index, best_beam=best_beam, n_accepted=n_accepted)
+    _need_status(dev_status, logits)
+    top = _c_int("top", top)
+    out = _logprob_outs(out, (B, L), max(0, top), logits, stream)
+    _run("rd_accepted_logprobs", logits,
+         logits.data_ptr(), dt, B, P, V, unpacker.data_ptr(), W, L, best_beam.data_ptr(), n_accepted.data_ptr(),
+         out_tokens.data_ptr(), float(temperature), top, out["logprob"].data_ptr(), out["entropy"].data_ptr(),
+         out["top_tokens"].data_ptr(), out["top_logprobs"].data_ptr(), _ptr(dev_status), stream=stream)
+    return out
 
 
 def rd_debug_stall_attention(budget_cycles: int) -> None:

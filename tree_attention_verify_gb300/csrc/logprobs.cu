@@ -1,0 +1,476 @@
+// rd_token_logprobs and rd_accepted_logprobs: for rows x of V logits, with p = softmax(x / T),
+// log p(token), the entropy H = -sum p log p, and the k most likely tokens.
+//
+// One pass over each row.  In units of log2, with c = log2(e) / T and a reference m,
+//   z = c (x - m),  l = sum 2^z,  w = sum 2^z z:
+//   log p(x_t) = ln 2 (z_t - log2 l),   H = ln 2 (log2 l - w / l).
+// The reference need not be the maximum: 32-bit floats hold 2^z up to 2^127, so a thread keeps
+// that of its first logits and only moves it when a logit lies 2^64 above.  So a logit costs a
+// difference, a product, an exponential and two accumulations, about half of what the SM can
+// issue while HBM delivers 16-bit logits.  (c x - c m in one operation would leave 32 bits for
+// logits above 2^127 / c.)
+//
+// The top k come from the same pass: a threshold that at least k logits of the row reach
+// is known after the first 64 logits of each thread (the k-th largest of the threads'
+// maxima); what reaches it afterwards, a few times k of them, is collected as 64-bit keys
+// (value, then the lower index first) and ranked by counting at the end.  A row that keeps
+// rising overfills the list; its k-th key is then a better threshold for another pass.
+//
+// Few rows: a cluster of up to eight CTAs takes one, and its first CTA joins the parts.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "rd_internal.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 8;                  // 16-byte loads of a thread in flight
+constexpr int kMostCtas = 8;               // of a row
+constexpr int kList = 1024;                // candidates of a CTA
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFar = 64.f;               // how far (log2) a logit may lie above the reference
+
+struct Args {
+    const void* logits;
+    const int32_t* rows;                   // row of entry n (null: n)
+    const int32_t* tokens;
+    // the accepted path's rows, where `unpacker` is given: entry (b, i)
+    const int32_t *unpacker, *best, *accepted;
+    int W, L, P;
+    int64_t n, rows_total;
+    int V, k;
+    float c;                               // log2(e) / T
+    float *logprob, *entropy;
+    int32_t* top;
+    float* top_logprob;
+    int32_t* status;
+};
+
+// ------------------------------------------------------------------ 16 bytes of logits
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[4])
+    {
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ float one(const void* p, int64_t i)
+    {
+        return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+    }
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8])
+    {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Vec<__half> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ float one(const void* p, int64_t i) { return __half2float(static_cast<const __half*>(p)[i]); }
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8])
+    {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[2 * i] = v.x;
+            x[2 * i + 1] = v.y;
+        }
+    }
+};
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float exp2_(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// numbers as unsigned ones of the same order (-0 as +0), and back
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float number(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu)); }
+__device__ __forceinline__ unsigned long long key_of(float x, int i)
+{
+    return (unsigned long long)ordered(x) << 32 | (uint32_t)~i;
+}
+
+struct Stats {
+    float m, l, w;                         // reference (a logit; -inf: nothing yet), sums
+    __device__ __forceinline__ void move(float to, float c)       // to another reference
+    {
+        if (m != -INFINITY) {
+            const float d = (m - to) * c, f = exp2_(d);
+            w = f * (w + d * l);
+            l *= f;
+            if (f == 0.f) w = 0.f;
+        }
+        m = to;
+    }
+    __device__ __forceinline__ void join(const Stats& o, float c)
+    {
+        if (o.m == -INFINITY && o.l == 0.f) return;
+        if (m == -INFINITY && l == 0.f) {
+            *this = o;
+            return;
+        }
+        Stats b = o;
+        const float to = max_nan(m, b.m);
+        if (m != to) move(to, c);          // (two equal references may be infinite)
+        if (b.m != to) b.move(to, c);
+        l += b.l;
+        w += b.w;
+    }
+};
+
+struct Shared {
+    unsigned long long list[kList];
+    unsigned long long best[32];           // this CTA's top k, in order
+    unsigned long long from[kMostCtas][32];
+    Stats part[kMostCtas];                 // of the CTAs of the cluster
+    Stats warp[kWarps];
+    int count;
+    unsigned long long least;              // the k-th key of an overfull list
+};
+
+__device__ __forceinline__ void push(Shared& sh, unsigned long long key)
+{
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kList) sh.list[at] = key;
+}
+
+// The row's 16-byte groups (of aligned addresses: the first and the last may lie partly outside
+// of it), and the share of this CTA.
+template <typename T>
+struct Row {
+    static constexpr int N = Vec<T>::n;
+    const T* x;
+    const uint4* base;
+    int V, off, first, last;               // elements of group 0 before the row; this CTA's groups
+    __device__ __forceinline__ Row(const T* row, int V_, int part, int parts) : x(row), V(V_)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+        off = (int)((at & 15) / sizeof(T));
+        base = reinterpret_cast<const uint4*>(at & ~uintptr_t(15));
+        const int groups = (V + off + N - 1) / N, each = (groups + parts - 1) / parts;
+        first = min(groups, part * each);
+        last = min(groups, first + each);
+    }
+    __device__ __forceinline__ bool inside(int g) const { return g * N >= off && (g + 1) * N - off <= V; }
+    __device__ __forceinline__ int index(int g, int e) const { return g * N + e - off; }
+    // a group that lies partly outside, element by element; what is outside counts as -inf
+    __device__ __forceinline__ void edge(int g, float (&v)[N]) const
+    {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = index(g, e);
+            v[e] = i >= 0 && i < V ? Vec<T>::one(x, i) : -INFINITY;
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 load16(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <int N>
+__device__ __forceinline__ float top_of(const float (&x)[N])
+{
+    float t = x[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) t = max_nan(t, x[e]);
+    return t;
+}
+
+template <int N>
+__device__ __forceinline__ void add(Stats& s, const float (&x)[N], float top, float c)
+{
+    if (top == -INFINITY) return;
+    if (!((top - s.m) * c <= kFar)) s.move(top, c);      // (the first time too)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        // 2^-200 is 0, and 0 x -200 too: an element of -inf adds nothing
+        const float z = max_nan((x[e] - s.m) * c, -200.f), p = exp2_(z);
+        s.l += p;
+        s.w = fmaf(p, z, s.w);
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void collect(Shared& sh, const Row<T>& row, int g, const float (&x)[N], unsigned long long least)
+{
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int i = row.index(g, e);
+        const unsigned long long key = key_of(x[e], i);
+        if (key >= least && i >= 0 && i < row.V) push(sh, key);
+    }
+}
+
+// sh.list[0 .. n) -> the keys of rank below k, in order; one sync behind
+__device__ __forceinline__ void rank(Shared& sh, int n, int k, unsigned long long* out)
+{
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const unsigned long long key = sh.list[i];
+        int r = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) r += sh.list[j] > key;
+        if (r < k) out[r] = key;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const __grid_constant__ Args a)
+{
+    __shared__ Shared sh;
+    constexpr int N = Vec<T>::n;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t n = blockIdx.x / parts;
+    const int k = a.k;
+
+    // ---- the entry's row and token (the same for the whole cluster)
+    int64_t r = n;
+    int token = a.tokens[n];
+    bool live = token != -1;
+    unsigned wrong = 0;
+    if (a.unpacker != nullptr) {
+        const int b = (int)(n / a.L), i = (int)(n % a.L);
+        const int w = a.best[b], acc = a.accepted[b];
+        if (w < 0 || w >= a.W || acc < 0 || acc >= a.L) wrong = RD_DEV_BAD_INDEX;
+        else if (i > acc) live = false;
+        else {
+            const int node = a.unpacker[((size_t)b * a.W + w) * a.L + i];
+            if (node < 0 || node >= a.P) wrong = RD_DEV_BAD_INDEX;
+            r = (int64_t)b * a.P + node;
+        }
+    } else if (a.rows != nullptr) {
+        r = a.rows[n];
+    }
+    if (live && !wrong) {
+        if (token < 0 || token >= a.V) wrong = RD_DEV_BAD_TOKEN;
+        else if (r < 0 || r >= a.rows_total) wrong = RD_DEV_BAD_INDEX;
+    }
+    if (!live || wrong) {
+        if (part == 0) {
+            if (tid == 0) {
+                if (wrong) rd_flag(a.status, wrong);
+                a.logprob[n] = 0.f;
+                a.entropy[n] = 0.f;
+            }
+            if (tid < k) {
+                a.top[n * k + tid] = -1;
+                a.top_logprob[n * k + tid] = 0.f;
+            }
+        }
+        return;
+    }
+    // every CTA of the cluster has started before one writes into another's shared memory
+    if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+
+    const T* x = static_cast<const T*>(a.logits) + r * a.V;
+    const Row<T> row(x, a.V, part, parts);
+    const float chosen = part == 0 && tid == 0 ? Vec<T>::one(x, token) : 0.f;
+    if (tid == 0) sh.count = 0;
+    Stats s = {-INFINITY, 0.f, 0.f};
+    unsigned long long least = 0;
+    float floor_ = -INFINITY;              // no logit below it is among the top k
+    constexpr int kStep = kThreads * kAhead;
+    for (int g0 = row.first; g0 < row.last; g0 += kStep) {
+        uint4 u[kAhead];
+        bool in[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int g = g0 + j * kThreads + tid;
+            in[j] = g < row.last && row.inside(g);
+            if (in[j]) u[j] = load16<T>(row.base + g);
+        }
+        if (g0 == row.first && k > 0) {
+            // the k-th largest of the threads' maxima, to 16 bits below
+            float top = -INFINITY;
+            bool some = false;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int g = g0 + j * kThreads + tid;
+                if (g >= row.last) continue;
+                float v[N];
+                if (in[j]) Vec<T>::unpack(u[j], v);
+                else row.edge(g, v);
+                top = max_nan(top, top_of<N>(v));
+                some = true;
+            }
+            const uint32_t mine = some ? ordered(top) >> 16 : 0u;
+            uint32_t at = 0;
+            for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1)
+                if (__syncthreads_count(mine >= (at | bit)) >= k) at |= bit;
+            least = (unsigned long long)at << 48;
+            floor_ = number(at << 16);
+            if (at == 0 || floor_ != floor_) floor_ = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int g = g0 + j * kThreads + tid;
+            if (g >= row.last) continue;
+            float v[N];
+            if (in[j]) Vec<T>::unpack(u[j], v);
+            else row.edge(g, v);
+            const float top = top_of<N>(v);
+            add<N>(s, v, top, a.c);
+            if (k > 0 && !(top < floor_)) collect<T, N>(sh, row, g, v, least);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stats b;
+        b.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+        b.l = __shfl_xor_sync(0xffffffffu, s.l, o);
+        b.w = __shfl_xor_sync(0xffffffffu, s.w, o);
+        // both lanes of a pair join in the same order, so that they stay alike
+        Stats lo = lane & o ? b : s;
+        lo.join(lane & o ? s : b, a.c);
+        s = lo;
+    }
+    if (lane == 0) sh.warp[warp] = s;
+    if (tid < 32) sh.best[tid] = 0;
+    __syncthreads();
+    if (k > 0) {
+        while (sh.count > kList) {         // too many: the k-th of those kept is a better threshold
+            rank(sh, kList, k, sh.best);
+            __syncthreads();
+            least = sh.best[k - 1];
+            floor_ = number((uint32_t)(least >> 32));
+            if (floor_ != floor_) floor_ = -INFINITY;
+            __syncthreads();
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            for (int g = row.first + tid; g < row.last; g += kThreads) {
+                float v[N];
+                if (row.inside(g)) Vec<T>::unpack(load16<T>(row.base + g), v);
+                else row.edge(g, v);
+                if (!(top_of<N>(v) < floor_)) collect<T, N>(sh, row, g, v, least);
+            }
+            if (tid < 32) sh.best[tid] = 0;
+            __syncthreads();
+        }
+        rank(sh, sh.count, k, sh.best);
+        __syncthreads();
+    }
+    Stats all = sh.warp[0];
+    for (int w = 1; w < kWarps; ++w) all.join(sh.warp[w], a.c);
+    if (parts > 1) {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        Shared* to = cluster.map_shared_rank(&sh, 0);
+        if (tid < 32) to->from[part][tid] = sh.best[tid];
+        if (tid == 0) to->part[part] = all;
+        cluster.sync();
+        if (part != 0) return;
+        all = sh.part[0];
+        for (int p = 1; p < parts; ++p) all.join(sh.part[p], a.c);
+        if (k > 0) {
+            // at most 8 x 32 keys, one a thread
+            const unsigned long long key = tid < parts * 32 ? sh.from[tid / 32][lane] : 0;
+            if (tid < 32) sh.best[tid] = 0;
+            __syncthreads();
+            if (key != 0) {
+                int rk = 0;
+                for (int p = 0; p < parts; ++p)
+                    for (int j = 0; j < k; ++j) rk += sh.from[p][j] > key;
+                if (rk < k) sh.best[rk] = key;
+            }
+            __syncthreads();
+        }
+    }
+    const float lg = log2f(all.l);
+    const float m = all.m == -INFINITY ? 0.f : all.m;
+    if (tid == 0) {
+        a.logprob[n] = kLn2 * ((chosen - m) * a.c - lg);
+        a.entropy[n] = kLn2 * (lg - all.w / all.l);
+    }
+    if (tid < k) {
+        const unsigned long long key = sh.best[tid];
+        a.top[n * k + tid] = (int32_t)~(uint32_t)key;
+        a.top_logprob[n * k + tid] = kLn2 * ((number((uint32_t)(key >> 32)) - m) * a.c - lg);
+    }
+}
+
+template <typename T>
+cudaError_t launch(const Args& a, cudaStream_t stream)
+{
+    // a row on several CTAs while they all run at once and each has a few thousand logits
+    const int sms = rd_device_sm_count();
+    int parts = 1;
+    while (parts < kMostCtas && a.n * parts * 2 <= 2 * sms && a.V / (parts * 2) >= 2048) parts *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.n * parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a);
+}
+
+}  // namespace
+
+cudaError_t rd_launch_logprobs(const rd_logprobs& q, cudaStream_t stream)
+{
+    Args a = {};
+    a.logits = q.logits;
+    a.rows = q.rows;
+    a.tokens = q.tokens;
+    a.unpacker = q.unpacker;
+    a.best = q.best_beam;
+    a.accepted = q.n_accepted;
+    a.W = q.W;
+    a.L = q.L;
+    a.P = q.P_max;
+    a.n = q.n;
+    a.rows_total = q.n_rows;
+    a.V = q.V;
+    a.k = q.top;
+    a.c = 1.4426950408889634f / q.temperature;
+    a.logprob = q.logprob;
+    a.entropy = q.entropy;
+    a.top = q.top_tokens;
+    a.top_logprob = q.top_logprobs;
+    a.status = q.dev_status;
+    if (q.dt == RD_BF16) return launch<__nv_bfloat16>(a, stream);
+    if (q.dt == RD_F16) return launch<__half>(a, stream);
+    return launch<float>(a, stream);
+}

@@ -1,0 +1,1132 @@
+// rd_tree_attention_quant: tree attention over a paged cache held in 4 or in 8 bits
+// (quant_format.cuh), single-token decoding among it.
+//
+//   o[r] = sum_j softmax_j(scale q[r] . k[j]) v[j]
+//
+// over the context (all visible) and the packed drafts (ancestors and the node itself), in one
+// pass with a running maximum and sum.  What it must read is half to a quarter of the 16-bit
+// cache, so widening the codes, not the stream, is the nearest bound: per position and kv
+// head 2 D codes become 16-bit floats.  Each code is widened once per 32 rows, in the registers
+// that feed the matrix instructions, with no way through shared memory:
+//
+//   S^T[16 positions x 8 rows] += K[16 x 16] Q^T[16 x 8]      A = K, straight from the codes
+//   O^T[16 columns x 8 rows]   += V^T[16 x 16] P^T[16 x 8]    A = V^T, straight from the codes
+//
+// The order in which a contraction runs is free, so a thread takes 16 consecutive elements
+// of a row of K (one block, one scale) as its share of four steps, and V's columns are dealt
+// so that a thread owns 16 consecutive ones: its loads are whole blocks and its outputs whole
+// 16-byte words.  Rows are the products' short side: 8 at a time, so that five rows cost a
+// quarter of what 32 do.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
+#include "quant_format.cuh"
+#include "rd_internal.cuh"
+
+namespace {
+
+using rdattn::fast_exp2;
+using rdattn::pack_bf16;
+using rdtc::smem_addr;
+
+constexpr int kConsumers = 8;              // warps that compute
+constexpr int kLoaders = 4;                // warps that load
+constexpr int kThreads = 32 * (kConsumers + kLoaders);
+constexpr int kLaunchRegs = 168;           // 384 x 168 = 64,512 registers, dealt anew:
+constexpr int kComputeRegs = 232, kLoadRegs = 40;
+static_assert(32 * kConsumers * kComputeRegs + 32 * kLoaders * kLoadRegs <= kThreads * kLaunchRegs, "registers");
+constexpr int kRows = 32;                  // rows of a unit at most
+constexpr int kDraftTile = 16;             // packed drafts of a chunk
+constexpr int kMostStages = 8;
+constexpr long long kWaitBudget = 4000000000LL;     // cycles, about two seconds
+constexpr float kLog2e = 1.4426950408889634f;
+// A row's weights are powers of two above a reference that lies kBelow under the row's maximum,
+// or up to kLag more: a weight P reaches 2^15 (a 16-bit float ends at 2^16), O is
+// rescaled only when the reference lags more, and weights down to 2^-21 of the largest
+// keep all 11 bits, those below an absolute 2^-32 of it.
+constexpr float kBelow = 7.f, kLag = 8.f;
+
+// positions of a warp's share of a chunk, in tiles of 16
+template <int BITS>
+__host__ __device__ constexpr int tiles_of() { return BITS == 4 ? 2 : 1; }
+
+struct Args {
+    const __nv_bfloat16 *q, *k_new, *v_new;
+    const unsigned char *k_pool, *v_pool;
+    const int32_t *table, *ctx_lens, *lens;
+    const uint32_t* mask;
+    __nv_bfloat16* o;
+    float* part;               // [2 grid slots][heads][kRows][D]
+    float2* part_ml;           // [2 grid slots][heads][kRows] maximum (log2 units), sum
+    int4* desc;                // [grid] the unit that a CTA begins and does not end
+    int32_t* status;
+    int B, P, Hq, Hkv, G, mask_words, num_pages, page_size, max_pages, max_ctx;
+    float scale_log2, k_scale, v_scale;
+    long long stall;
+    int heads;                 // kv heads of a unit: 4, 2 or 1
+    int seg, pitch, gran, per_row;     // bytes of a position's rows, apart in shared memory, a copy; copies
+    uint32_t per_row_magic;
+    int draft_pitch, half, stages;     // bytes of a stage's K (and of its V)
+};
+
+// ------------------------------------------------------------------ the division of the work
+// A unit is (request, group of `heads` kv heads, group of up to 32 rows).  Its chunks
+// (context, then tiles of drafts) stand in one sequence with all other units', weighted by
+// what they cost, and the CTAs take equal ranges of it.
+struct Shape {
+    int rows, groups, per;     // rows of the request, row groups, rows of a group (a multiple of 8)
+    int C, n_ctx, n;           // context, its chunks, all chunks
+    uint32_t chunk_cost, unit_cost;
+    uint64_t cost;             // of the request
+};
+
+// Widening a chunk costs the same for any number of rows, its products go with them (measured
+// beside the kernel); a unit's start and end take as long as a few chunks.
+__host__ __device__ constexpr uint32_t chunk_cost(int tiles) { return 3u + 2u * (uint32_t)tiles; }
+constexpr uint32_t kUnitCost = 24;
+constexpr uint32_t kLeastCost = 24;        // of a CTA's range: at least two chunks
+
+__device__ __forceinline__ Shape shape_of(const Args& a, int b, int chunk)
+{
+    Shape s;
+    s.cost = 0;
+    const int len = a.lens[b];
+    if (len <= 0 || len > a.P) return s;
+    s.C = a.ctx_lens[b];
+    if (s.C < 0 || s.C > a.max_ctx) return s;
+    s.rows = len * a.G;
+    s.groups = (s.rows + kRows - 1) / kRows;
+    s.per = ((s.rows + s.groups - 1) / s.groups + 7) & ~7;
+    s.n_ctx = (int)(((int64_t)s.C + chunk - 1) / chunk);
+    s.n = s.n_ctx + (len + kDraftTile - 1) / kDraftTile;
+    s.chunk_cost = chunk_cost(s.per / 8);
+    s.unit_cost = 0;
+    const uint64_t unit = kUnitCost + (uint64_t)s.n * s.chunk_cost;
+    s.cost = unit * (uint64_t)s.groups * (uint64_t)(a.Hkv / a.heads);
+    return s;
+}
+
+__device__ __forceinline__ uint64_t unit_cost(const Shape& s) { return kUnitCost + (uint64_t)s.n * s.chunk_cost; }
+
+struct Division {
+    uint64_t W;                // cost of everything
+    uint32_t n;                // CTAs that work
+    int b;                     // the request in which this CTA's range begins
+    uint64_t S;                // cost of the requests before it
+    __device__ __forceinline__ uint64_t begin(uint32_t c) const
+    {
+        // floor(c W / n) without leaving 64 bits
+        return (W / n) * c + (W % n) * c / n;
+    }
+    __device__ __forceinline__ uint32_t of(uint64_t x) const      // the CTA whose range holds x
+    {
+        uint32_t c = (uint32_t)min((uint64_t)(n - 1), x / max((uint64_t)1, W / n));
+        while (c > 0 && begin(c) > x) --c;
+        while (c + 1 < n && begin(c + 1) <= x) ++c;
+        return c;
+    }
+};
+
+struct Piece {
+    int b, hg, r0, rows;       // request, head group, first row, rows
+    int j0, j1, n_ctx, n, C;   // chunks of this piece, context chunks and all chunks of the unit
+    int unit;                  // within the request
+    int tiles;                 // of 8 rows
+};
+
+// The pieces of a CTA's range, one after the other; every warp walks through them by itself.
+struct Walk {
+    const Args& a;
+    const int chunk;
+    uint64_t lo, hi, S;
+    int b, unit;
+    Shape s;
+    __device__ __forceinline__ Walk(const Args& args, const Division& d, int chunk_) : a(args), chunk(chunk_)
+    {
+        const uint32_t c = blockIdx.x;
+        lo = hi = 0;
+        S = d.S;
+        b = d.b;
+        unit = -1;
+        if (d.W == 0 || c >= d.n) {
+            b = a.B;
+            return;
+        }
+        lo = d.begin(c);
+        hi = c + 1 < d.n ? d.begin(c + 1) : d.W;
+        if (b < a.B) s = shape_of(a, b, chunk);
+    }
+    __device__ __forceinline__ bool next(Piece& p)
+    {
+        for (; b < a.B && S < hi;) {
+            if (s.cost != 0) {
+                const uint64_t uc = unit_cost(s);
+                if (unit < 0) unit = lo > S ? (int)((lo - S) / uc) : 0;
+                const int units = s.groups * (a.Hkv / a.heads);
+                while (unit < units) {
+                    const uint64_t first = S + (uint64_t)unit * uc + kUnitCost;
+                    if (S + (uint64_t)unit * uc >= hi) return false;
+                    const uint64_t c = s.chunk_cost;
+                    const uint64_t j0 = lo > first ? (lo - first + c - 1) / c : 0;
+                    const uint64_t j1 = hi > first ? min((uint64_t)s.n, (hi - first + c - 1) / c) : 0;
+                    const int u = unit++;
+                    if (j0 >= j1) continue;
+                    p.b = b;
+                    p.unit = u;
+                    p.hg = u / s.groups;
+                    p.r0 = (u % s.groups) * s.per;
+                    p.rows = min(s.per, s.rows - p.r0);
+                    p.tiles = (p.rows + 7) / 8;
+                    p.j0 = (int)j0;
+                    p.j1 = (int)j1;
+                    p.n_ctx = s.n_ctx;
+                    p.n = s.n;
+                    p.C = s.C;
+                    return true;
+                }
+                S += s.cost;
+            }
+            unit = 0;
+            if (++b < a.B) s = shape_of(a, b, chunk);
+        }
+        return false;
+    }
+};
+
+struct Shared {                            // static part
+    uint64_t full[kMostStages], empty[kMostStages], never;
+    int abort;
+    int b;
+    unsigned long long S, sum[kThreads / 32];
+};
+
+// Every CTA sums the requests' costs and finds the request where its range begins.
+__device__ __forceinline__ Division divide(const Args& a, Shared& sh, int chunk)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned long long mine = 0;
+    for (int b = tid; b < a.B; b += kThreads) {
+        const Shape s = shape_of(a, b, chunk);
+        mine += s.cost;
+        if (blockIdx.x == 0) {
+            const int len = a.lens[b];
+            if (len < 0 || len > a.P || (len > 0 && s.cost == 0)) rd_flag(a.status, RD_DEV_BAD_LENGTH);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sh.sum[warp] = mine;
+    __syncthreads();
+    Division d;
+    d.W = 0;
+    for (int w = 0; w < kThreads / 32; ++w) d.W += sh.sum[w];
+    const uint64_t most = d.W / kLeastCost;
+    d.n = (uint32_t)(most < 1 ? 1 : (most < gridDim.x ? most : gridDim.x));
+    d.b = a.B;
+    d.S = 0;
+    __syncthreads();
+    if (d.W == 0 || blockIdx.x >= d.n) return d;
+    const uint64_t lo = d.begin(blockIdx.x);
+    uint64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        const unsigned long long cost = b < a.B ? shape_of(a, b, chunk).cost : 0;
+        unsigned long long inc = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) sh.sum[warp] = inc;
+        if (tid == 0) sh.b = -1;
+        __syncthreads();
+        uint64_t base = before;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) base += sh.sum[w];
+            before += sh.sum[w];
+        }
+        const uint64_t S = base + inc - cost;
+        if (cost != 0 && S <= lo && lo < S + cost) {
+            sh.b = b;
+            sh.S = S;
+        }
+        __syncthreads();
+        const int found = sh.b;
+        const uint64_t at = sh.S;
+        __syncthreads();
+        if (found >= 0) {
+            d.b = found;
+            d.S = at;
+            break;
+        }
+    }
+    return d;
+}
+
+// ------------------------------------------------------------------ small pieces of PTX
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ void compute_sync() { rdtc::named_sync(1, 32 * kConsumers); }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+
+// ------------------------------------------------------------------ loading
+// The positions of a warp's tile are dealt to the products' indices so that both the four
+// rows of K and the four rows of V that a half-warp reads lie in different banks.
+__device__ __forceinline__ int position_of(int t, int e) { return 4 * e + ((t + 2 * e) & 3); }    // e: 0, 1
+
+template <int BYTES>
+__device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t v_to, const size_t (&base)[4], int rows,
+                                          int tid)
+{
+    const size_t row = (size_t)a.Hkv * a.seg / a.heads;
+    const int copies = rows * a.per_row;
+    for (int i = tid; i < copies; i += 32 * kLoaders) {
+        const int pos = (int)__umulhi((uint32_t)i, a.per_row_magic), part = i - pos * a.per_row;
+        const int blk = pos >> 6;
+        const size_t at0 = blk < 2 ? (blk == 0 ? base[0] : base[1]) : (blk == 2 ? base[2] : base[3]);
+        const size_t at = at0 + (size_t)(pos & 63) * row + (size_t)part * BYTES;
+        const uint32_t to = (uint32_t)(pos * a.pitch + part * BYTES);
+        copy_async<BYTES>(k_to + to, a.k_pool + at);
+        copy_async<BYTES>(v_to + to, a.v_pool + at);
+    }
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void load(const Args& a, Shared& sh, unsigned char* ring, const Division& d, int chunk)
+{
+    const int tid = threadIdx.x - 32 * kConsumers;
+    const size_t row = (size_t)a.Hkv * a.seg / a.heads;
+    Walk walk(a, d, chunk);
+    Piece p;
+    uint32_t it = 0;
+    bool alive = true;
+    while (walk.next(p)) {
+        for (int j = p.j0; j < p.j1; ++j, ++it) {
+            const int stage = (int)(it % (uint32_t)a.stages);
+            // where the positions lie, before the wait
+            size_t base[4] = {0, 0, 0, 0};
+            int rows = 0;
+            if (j < p.n_ctx) {
+                const int pos0 = j * chunk;
+                rows = min(chunk, p.C - pos0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int pos = pos0 + 64 * k;
+                    if (64 * k < rows) {
+                        int page = a.table[(size_t)p.b * a.max_pages + pos / a.page_size];
+                        if (page < 0 || page >= a.num_pages) {
+                            if (tid == 0) rd_flag(a.status, RD_DEV_BAD_INDEX);
+                            page = 0;
+                        }
+                        base[k] = ((size_t)page * a.page_size + pos % a.page_size) * row + (size_t)p.hg * a.seg;
+                    }
+                }
+            }
+            if (alive && it >= (uint32_t)a.stages)
+                alive = rdattn::warp_wait(&sh.empty[stage], ((it / (uint32_t)a.stages) & 1u) ^ 1u, &sh.abort, kWaitBudget);
+            const uint32_t k_to = smem_addr(ring + (size_t)stage * 2 * a.half), v_to = k_to + (uint32_t)a.half;
+            if (j < p.n_ctx) {
+                if (a.gran == 16) load_rows<16>(a, k_to, v_to, base, rows, tid);
+                else if (a.gran == 8) load_rows<8>(a, k_to, v_to, base, rows, tid);
+                else load_rows<4>(a, k_to, v_to, base, rows, tid);
+            } else {
+                const int node0 = (j - p.n_ctx) * kDraftTile;
+                const int nodes = min(kDraftTile, a.lens[p.b] - node0);
+                const int copies = a.heads * D * 2 / 16;
+                for (int i = tid; i < nodes * copies; i += 32 * kLoaders) {
+                    const int node = i / copies, part = i % copies;
+                    const size_t at = (((size_t)p.b * a.P + node0 + node) * a.Hkv + (size_t)p.hg * a.heads) * D + (size_t)part * 8;
+                    const uint32_t to = (uint32_t)(node * a.draft_pitch + part * 16);
+                    copy_async<16>(k_to + to, a.k_new + at);
+                    copy_async<16>(v_to + to, a.v_new + at);
+                }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sh.full[stage])) : "memory");
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // rows behind the last node, and those of skipped requests
+    const int vecs = a.Hq * D / 8;
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const int from = shape_of(a, b, chunk).cost != 0 ? a.lens[b] : 0;
+        uint4* o = reinterpret_cast<uint4*>(a.o) + (size_t)b * a.P * vecs;
+        for (size_t v = (size_t)from * vecs + tid; v < (size_t)a.P * vecs; v += 32 * kLoaders) o[v] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// ------------------------------------------------------------------ computing
+// What a warp needs to know of its place.
+struct Place {
+    int warp, lane, g, t;      // lane = 4 g + t
+    int head, split, splits;   // kv head within the group, share of each chunk's positions
+};
+
+template <int D, int BITS, int NT>
+struct Sums {                              // of 8 NT rows; this thread's columns D / 8 * g ..., rows 8 i + 2 t, + 1
+    float o[D / 16][NT][4];
+    float m[2 * NT], l[2 * NT];            // references, sums of the weights
+    bool fresh;                            // some row has no finite reference yet
+};
+
+template <int D, int BITS, int NT>
+__device__ __forceinline__ void raise(Sums<D, BITS, NT>& s, const float (&top)[2 * NT])
+{
+    bool none = false;
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) {
+        float v = top[k];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        const float m = fmaxf(s.m[k], v - kBelow);
+        const float f = fast_exp2(s.m[k] - (m == -INFINITY ? 0.f : m));
+        s.m[k] = m;
+        s.l[k] *= f;
+        none = none || m == -INFINITY;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            s.o[j][k / 2][k & 1] *= f;
+            s.o[j][k / 2][2 + (k & 1)] *= f;
+        }
+    }
+    s.fresh = __any_sync(0xffffffffu, none);
+}
+
+// one tile of 16 positions of the context; `valid` of them count
+template <int D, int BITS, int NT>
+__device__ __forceinline__ void context_tile(const Args& a, const Place& w, Sums<D, BITS, NT>& s, uint32_t k_at,
+                                             uint32_t v_at, uint32_t q_at, uint32_t f_at, int valid)
+{
+    using namespace rdquant;
+    constexpr int KB = D / 64;             // blocks of a row of K that a thread widens
+    float x[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[i][c] = 0.f;
+    const int pos = position_of(w.g >> 1, w.g & 1);
+    const uint32_t row0 = k_at + (uint32_t)(pos * a.pitch), row1 = row0 + (uint32_t)(8 * a.pitch);
+    // ---- S^T
+    uint32_t sc0[KB], sc1[KB];
+    if constexpr (BITS == 4) {
+        if constexpr (D == 128) {
+            const uint32_t sel = (uint32_t)w.t * 0x1111u + 0x4400u;
+            const uint2 b0 = lds64(row0 + D / 2), b1 = lds64(row1 + D / 2);
+            e4m3x4(__byte_perm(b0.x, b0.y, sel), sc0[0], sc0[KB - 1]);
+            e4m3x4(__byte_perm(b1.x, b1.y, sel), sc1[0], sc1[KB - 1]);
+        } else {
+            const uint32_t sel = (uint32_t)w.t * 0x1111u;
+            uint32_t drop;
+            e4m3x4(__byte_perm(lds32(row0 + D / 2), 0u, sel), sc0[0], drop);
+            e4m3x4(__byte_perm(lds32(row1 + D / 2), 0u, sel), sc1[0], drop);
+        }
+    }
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+        uint32_t w0[4], w1[4];             // the thread's 16 codes of each of its two positions
+        if constexpr (BITS == 4) {
+            const uint32_t off = (uint32_t)(8 * (w.t + 4 * kb));
+            if constexpr (D == 128) {
+                const uint2 u0 = lds64(row0 + off), u1 = lds64(row1 + off);
+                w0[0] = u0.x, w0[1] = u0.y, w1[0] = u1.x, w1[1] = u1.y;
+            } else {
+                w0[0] = lds32(row0 + off), w0[1] = lds32(row0 + off + 4);
+                w1[0] = lds32(row1 + off), w1[1] = lds32(row1 + off + 4);
+            }
+        } else {
+            const uint4 u0 = lds128(row0 + (uint32_t)(16 * (w.t + 4 * kb))), u1 = lds128(row1 + (uint32_t)(16 * (w.t + 4 * kb)));
+            w0[0] = u0.x, w0[1] = u0.y, w0[2] = u0.z, w0[3] = u0.w;
+            w1[0] = u1.x, w1[1] = u1.y, w1[2] = u1.z, w1[3] = u1.w;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {      // two steps of 16 at a time
+            uint32_t f[2][4];
+            if constexpr (BITS == 4) {
+                uint32_t c0[4], c1[4];
+                e2m1x8(w0[h], c0);
+                e2m1x8(w1[h], c1);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[e][0] = mul_f16x2(c0[2 * e], sc0[kb]);
+                    f[e][1] = mul_f16x2(c1[2 * e], sc1[kb]);
+                    f[e][2] = mul_f16x2(c0[2 * e + 1], sc0[kb]);
+                    f[e][3] = mul_f16x2(c1[2 * e + 1], sc1[kb]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    e4m3x4(w0[2 * h + e], f[e][0], f[e][2]);
+                    e4m3x4(w1[2 * h + e], f[e][1], f[e][3]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const uint4 qb = lds128(q_at + (uint32_t)(i * 8 * (2 * D + 16) + 128 * kb + 16 * h));
+                mma_f16(x[i], f[0], qb.x, qb.y);
+                mma_f16(x[i], f[1], qb.z, qb.w);
+            }
+        }
+    }
+    // ---- softmax of the rows over these positions
+    if (valid < 16) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if (pos >= valid) x[i][0] = x[i][1] = -INFINITY;
+            if (pos + 8 >= valid) x[i][2] = x[i][3] = -INFINITY;
+        }
+    }
+    bool over = s.fresh;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const uint2 fb = lds64(f_at + (uint32_t)(32 * i));
+        const float f0 = __uint_as_float(fb.x), f1 = __uint_as_float(fb.y);
+        x[i][0] *= f0, x[i][1] *= f1, x[i][2] *= f0, x[i][3] *= f1;
+        over = over || fmaxf(x[i][0], x[i][2]) > s.m[2 * i] + (kBelow + kLag) || fmaxf(x[i][1], x[i][3]) > s.m[2 * i + 1] + (kBelow + kLag);
+    }
+    if (__any_sync(0xffffffffu, over)) {
+        float top[2 * NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            top[2 * i] = fmaxf(x[i][0], x[i][2]);
+            top[2 * i + 1] = fmaxf(x[i][1], x[i][3]);
+        }
+        raise<D, BITS, NT>(s, top);
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const float m0 = s.fresh && s.m[2 * i] == -INFINITY ? 0.f : s.m[2 * i];
+        const float m1 = s.fresh && s.m[2 * i + 1] == -INFINITY ? 0.f : s.m[2 * i + 1];
+        const float p0 = fast_exp2(x[i][0] - m0), p1 = fast_exp2(x[i][1] - m1);
+        const float p2 = fast_exp2(x[i][2] - m0), p3 = fast_exp2(x[i][3] - m1);
+        s.l[2 * i] += p0 + p2;
+        s.l[2 * i + 1] += p1 + p3;
+        pb[i][0] = transpose8x8(pack_f16(p0, p1));       // 2^-11 of each weight
+        pb[i][1] = transpose8x8(pack_f16(p2, p3));
+    }
+    // ---- O^T
+    const int v0 = position_of(w.t, 0), v1 = position_of(w.t, 1);
+    const uint32_t r0 = v_at + (uint32_t)(v0 * a.pitch), r1 = v_at + (uint32_t)(v1 * a.pitch);
+    const uint32_t r2 = r0 + (uint32_t)(8 * a.pitch), r3 = r1 + (uint32_t)(8 * a.pitch);
+    if constexpr (BITS == 4) {
+        constexpr int NW = D / 64;         // words of the thread's columns
+        uint32_t u[4][NW];
+        const uint32_t off = (uint32_t)(D / 16 * w.g);
+        if constexpr (D == 128) {
+            const uint2 y0 = lds64(r0 + off), y1 = lds64(r1 + off), y2 = lds64(r2 + off), y3 = lds64(r3 + off);
+            u[0][0] = y0.x, u[1][0] = y1.x, u[2][0] = y2.x, u[3][0] = y3.x;
+            u[0][NW - 1] = y0.y, u[1][NW - 1] = y1.y, u[2][NW - 1] = y2.y, u[3][NW - 1] = y3.y;
+        } else {
+            u[0][0] = lds32(r0 + off), u[1][0] = lds32(r1 + off), u[2][0] = lds32(r2 + off), u[3][0] = lds32(r3 + off);
+        }
+        const uint32_t so = (uint32_t)(D / 2 + (D == 128 ? w.g : w.g >> 1));
+        uint32_t b0 = lds8(r0 + so), b1 = lds8(r1 + so), b2 = lds8(r2 + so), b3 = lds8(r3 + so);
+        if (valid < 16) {                  // what lies behind the end may be anything: its scale is 0
+            if (v0 >= valid) b0 = 0;
+            if (v1 >= valid) b1 = 0;
+            if (v0 + 8 >= valid) b2 = 0;
+            if (v1 + 8 >= valid) b3 = 0;
+        }
+        uint32_t s01, s23;
+        e4m3x4(b0 | b1 << 8 | b2 << 16 | b3 << 24, s01, s23);
+#pragma unroll
+        for (int q = 0; q < NW; ++q) {
+            // the codes of one column at two positions, side by side
+            constexpr uint32_t kLow = 0x0f0f0f0fu;
+            uint32_t e0[4], o0[4], e1[4], o1[4];
+            e2m1x8((u[0][q] & kLow) | ((u[1][q] << 4) & ~kLow), e0);
+            e2m1x8(((u[0][q] >> 4) & kLow) | (u[1][q] & ~kLow), o0);
+            e2m1x8((u[2][q] & kLow) | ((u[3][q] << 4) & ~kLow), e1);
+            e2m1x8(((u[2][q] >> 4) & kLow) | (u[3][q] & ~kLow), o1);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t f[4] = {mul_f16x2(e0[c], s01), mul_f16x2(o0[c], s01), mul_f16x2(e1[c], s23),
+                                       mul_f16x2(o1[c], s23)};
+#pragma unroll
+                for (int i = 0; i < NT; ++i) mma_f16(s.o[4 * q + c][i], f, pb[i][0], pb[i][1]);
+            }
+        }
+    } else {
+        constexpr int NW = D / 32;
+        uint32_t u[4][NW];
+        const uint32_t off = (uint32_t)(D / 8 * w.g);
+        const uint32_t r[4] = {r0, r1, r2, r3};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (D == 128) {
+                const uint4 y = lds128(r[e] + off);
+                u[e][0] = y.x, u[e][1] = y.y, u[e][NW - 2] = y.z, u[e][NW - 1] = y.w;
+            } else {
+                const uint2 y = lds64(r[e] + off);
+                u[e][0] = y.x, u[e][1] = y.y;
+            }
+            const int at = (e & 1 ? v1 : v0) + 4 * (e & 2);
+            if (at >= valid) {
+#pragma unroll
+                for (int q = 0; q < NW; ++q) u[e][q] = 0;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NW; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
+                uint32_t f[4];
+                e4m3x4(__byte_perm(u[0][q], u[1][q], sel), f[0], f[1]);
+                e4m3x4(__byte_perm(u[2][q], u[3][q], sel), f[2], f[3]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) mma_f16(s.o[2 * q + h][i], f, pb[i][0], pb[i][1]);
+            }
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_of_f16(uint32_t x)
+{
+    const float2 v = __half22float2(*reinterpret_cast<__half2*>(&x));
+    return pack_bf16(v.x, v.y);
+}
+
+// one tile of 16 packed drafts: bf16 as they are; P is rounded to bf16 too (both factors of
+// a product have one type), 2^-9 of each weight
+template <int D, int BITS, int NT>
+__device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const Piece& pc, Sums<D, BITS, NT>& s, uint32_t k_at,
+                                           uint32_t v_at, uint32_t q_at, uint32_t f_at, int node0, int nodes)
+{
+    constexpr int KB = D / 64;
+    float x[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[i][c] = 0.f;
+    const int pos = position_of(w.g >> 1, w.g & 1);
+    // which of the rows' mask bits are these nodes'
+    uint32_t seen[2 * NT];
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) {
+        const int r = 8 * (k / 2) + 2 * w.t + (k & 1);
+        seen[k] = 0;
+        if (r < pc.rows)
+            seen[k] = a.mask[((size_t)pc.b * a.P + (pc.r0 + r) / a.G) * a.mask_words + node0 / 32] >> (node0 % 32);
+        if (nodes < 16) seen[k] &= (1u << nodes) - 1u;
+    }
+    const uint32_t row0 = k_at + (uint32_t)(pos * a.draft_pitch), row1 = row0 + (uint32_t)(8 * a.draft_pitch);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t off = (uint32_t)(32 * (w.t + 4 * kb) + 16 * h);
+            const uint4 y0 = lds128(row0 + off), y1 = lds128(row1 + off);
+            const uint32_t f0[4] = {y0.x, y1.x, y0.y, y1.y}, f1[4] = {y0.z, y1.z, y0.w, y1.w};
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const uint4 qb = lds128(q_at + (uint32_t)(i * 8 * (2 * D + 16) + 128 * kb + 16 * h));
+                mma_bf16(x[i], f0, bf16_of_f16(qb.x), bf16_of_f16(qb.y));
+                mma_bf16(x[i], f1, bf16_of_f16(qb.z), bf16_of_f16(qb.w));
+            }
+        }
+    float top[2 * NT];
+    const float back = 1.f / a.k_scale;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const uint2 fb = lds64(f_at + (uint32_t)(32 * i));
+        const float f[2] = {__uint_as_float(fb.x) * back, __uint_as_float(fb.y) * back};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            x[i][c] = (seen[2 * i + (c & 1)] >> (pos + 4 * (c & 2)) & 1u) ? x[i][c] * f[c & 1] : -INFINITY;
+        top[2 * i] = fmaxf(x[i][0], x[i][2]);
+        top[2 * i + 1] = fmaxf(x[i][1], x[i][3]);
+    }
+    raise<D, BITS, NT>(s, top);
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const float m0 = s.m[2 * i] == -INFINITY ? 0.f : s.m[2 * i];
+        const float m1 = s.m[2 * i + 1] == -INFINITY ? 0.f : s.m[2 * i + 1];
+        const float p0 = fast_exp2(x[i][0] - m0), p1 = fast_exp2(x[i][1] - m1);
+        const float p2 = fast_exp2(x[i][2] - m0), p3 = fast_exp2(x[i][3] - m1);
+        s.l[2 * i] += p0 + p2;
+        s.l[2 * i + 1] += p1 + p3;
+        pb[i][0] = transpose8x8(pack_bf16(p0, p1));
+        pb[i][1] = transpose8x8(pack_bf16(p2, p3));
+    }
+    const int v[4] = {position_of(w.t, 0), position_of(w.t, 1), position_of(w.t, 0) + 8, position_of(w.t, 1) + 8};
+#pragma unroll
+    for (int part = 0; part < D / 64; ++part) {           // eight columns at a time
+        uint4 y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[e] = v[e] < nodes ? lds128(v_at + (uint32_t)(v[e] * a.draft_pitch + D / 4 * w.g + 16 * part)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = q == 0 ? y[e].x : q == 1 ? y[e].y : q == 2 ? y[e].z : y[e].w;
+            const uint32_t f[4] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[0], z[1], 0x7632),
+                                   __byte_perm(z[2], z[3], 0x5410), __byte_perm(z[2], z[3], 0x7632)};
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mma_bf16(s.o[4 * part + q][i], f, pb[i][0], pb[i][1]);
+        }
+    }
+}
+
+struct Buffers {
+    unsigned char* ring;
+    __half* q;                 // [heads][kRows][D + 8]
+    float* f;                  // [heads][kRows] score = product x f (log2 units, the cache's scale in it)
+    float4* join;              // [4][2][D / 16][32]
+    float2* join_ml;           // [4][8][32]
+};
+
+// The queries of a unit as 16-bit floats.  A power of two per row brings its largest element to
+// [2^14, 2^15): elements down to 2^-28 of it stay exact, and no finite query leaves the range.
+template <int D>
+__device__ __forceinline__ void stage_queries(const Args& a, const Place& w, const Piece& p, const Buffers& buf, int tiles)
+{
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+    const int sub = w.lane % kLanes;
+    const int h = p.hg * a.heads + w.head;
+    for (int r = w.split * kAtOnce + w.lane / kLanes; r < 8 * tiles; r += w.splits * kAtOnce) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < p.rows) {
+            const int row = p.r0 + r;
+            v = *(reinterpret_cast<const uint4*>(
+                      a.q + (((size_t)p.b * a.P + row / a.G) * a.Hq + (size_t)h * a.G + row % a.G) * D) + sub);
+        }
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        float x[8], top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+            top = fmaxf(top, fabsf(x[e]));
+        }
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = (int)(__float_as_uint(top) >> 23);
+        const int k = top == 0.f || e == 255 ? 127 : min(240, 268 - e);
+        const float up = __uint_as_float((uint32_t)k << 23), down = __uint_as_float((uint32_t)(254 - k) << 23);
+        uint4 out;
+        out.x = pack_f16(x[0] * up, x[1] * up);
+        out.y = pack_f16(x[2] * up, x[3] * up);
+        out.z = pack_f16(x[4] * up, x[5] * up);
+        out.w = pack_f16(x[6] * up, x[7] * up);
+        *reinterpret_cast<uint4*>(buf.q + ((size_t)w.head * kRows + r) * (D + 8) + 8 * sub) = out;
+        if (sub == 0) buf.f[w.head * kRows + r] = a.scale_log2 * a.k_scale * down;
+    }
+}
+
+template <int D, int BITS, int NT>
+__device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& buf, const Place& w, const Piece& p,
+                                   const Division& d, uint32_t& it, bool& alive)
+{
+    constexpr int TILES = tiles_of<BITS>();
+    const int chunk = 16 * TILES * w.splits;
+    Sums<D, BITS, NT> s;
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) s.m[k] = -INFINITY, s.l[k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s.o[j][i][c] = 0.f;
+    s.fresh = true;
+    compute_sync();                        // nobody reads the last piece's queries any more
+    stage_queries<D>(a, w, p, buf, NT);
+    compute_sync();
+    const uint32_t q_at = smem_addr(buf.q) + (uint32_t)((w.head * kRows + w.g) * (2 * D + 16) + 32 * w.t);
+    const uint32_t f_at = smem_addr(buf.f) + (uint32_t)(4 * (w.head * kRows + 2 * w.t));
+    const uint32_t ring = smem_addr(buf.ring);
+    bool scaled = false;                   // O holds values, no longer values / v_scale
+    auto scale_values = [&]() {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s.o[j][i][c] *= a.v_scale;
+        scaled = true;
+    };
+    for (int j = p.j0; j < p.j1; ++j, ++it) {
+        const int stage = (int)(it % (uint32_t)a.stages);
+        if (alive) {
+            alive = rdattn::warp_wait(&sh.full[stage], (it / (uint32_t)a.stages) & 1u, &sh.abort, kWaitBudget);
+            if (!alive && w.lane == 0) {
+                sh.abort = 1;
+                rd_flag(a.status, RD_DEV_TIMEOUT);
+            }
+        }
+        const uint32_t k_at = ring + (uint32_t)(stage * 2 * a.half), v_at = k_at + (uint32_t)a.half;
+        if (j < p.n_ctx) {
+            const int first = w.split * 16 * TILES, valid = p.C - j * chunk - first;
+            const uint32_t off = (uint32_t)(first * a.pitch + w.head * rdquant::row_bytes(D, BITS));
+#pragma unroll 1
+            for (int x = 0; x < TILES; ++x)
+                if (valid > 16 * x)
+                    context_tile<D, BITS, NT>(a, w, s, k_at + off + (uint32_t)(16 * x * a.pitch),
+                                              v_at + off + (uint32_t)(16 * x * a.pitch), q_at, f_at, min(16, valid - 16 * x));
+        } else {
+            const int tile = j - p.n_ctx;
+            if (!scaled) scale_values();
+            if (tile % w.splits == w.split) {
+                const uint32_t off = (uint32_t)(w.head * D * 2);
+                draft_tile<D, BITS, NT>(a, w, p, s, k_at + off, v_at + off, q_at, f_at, tile * kDraftTile,
+                                        min(kDraftTile, a.lens[p.b] - tile * kDraftTile));
+            }
+        }
+        __syncwarp();
+        if (w.lane == 0) rdtc::mbar_arrive(&sh.empty[stage]);
+    }
+    if (!scaled) scale_values();
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) s.l[k] += __shfl_xor_sync(0xffffffffu, s.l[k], o);
+
+    // ---- the warps of a head join their sums, the upper half of them into the lower
+    for (int half = w.splits / 2; half >= 1; half /= 2) {
+        const bool gives = w.split >= half && w.split < 2 * half, takes = w.split < half;
+        const int slot = (takes ? w.split : w.split - half) * a.heads + w.head;
+        float fo[2 * NT];
+#pragma unroll
+        for (int i0 = 0; i0 < NT; i0 += 2) {
+            if (gives) {
+                if (i0 == 0) {
+#pragma unroll
+                    for (int k = 0; k < 2 * NT; ++k) buf.join_ml[(slot * 8 + k) * 32 + w.lane] = make_float2(s.m[k], s.l[k]);
+                }
+#pragma unroll
+                for (int i = i0; i < i0 + 2 && i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        buf.join[((slot * 2 + i - i0) * (D / 16) + j) * 32 + w.lane] =
+                            make_float4(s.o[j][i][0], s.o[j][i][1], s.o[j][i][2], s.o[j][i][3]);
+            }
+            compute_sync();
+            if (takes) {
+                if (i0 == 0) {
+#pragma unroll
+                    for (int k = 0; k < 2 * NT; ++k) {
+                        const float2 ml = buf.join_ml[(slot * 8 + k) * 32 + w.lane];
+                        const float m = fmaxf(s.m[k], ml.x), mu = m == -INFINITY ? 0.f : m;
+                        const float f = fast_exp2(s.m[k] - mu);
+                        fo[k] = fast_exp2(ml.x - mu);
+                        s.m[k] = m;
+                        s.l[k] = s.l[k] * f + ml.y * fo[k];
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            s.o[j][k / 2][k & 1] *= f;
+                            s.o[j][k / 2][2 + (k & 1)] *= f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = i0; i < i0 + 2 && i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        const float4 v = buf.join[((slot * 2 + i - i0) * (D / 16) + j) * 32 + w.lane];
+                        s.o[j][i][0] += v.x * fo[2 * i];
+                        s.o[j][i][1] += v.y * fo[2 * i + 1];
+                        s.o[j][i][2] += v.z * fo[2 * i];
+                        s.o[j][i][3] += v.w * fo[2 * i + 1];
+                    }
+            }
+            compute_sync();
+        }
+    }
+    if (w.split != 0) return;
+
+    // ---- rows, or partials of a unit that the ranges cut
+    const bool whole = p.j0 == 0 && p.j1 == p.n;
+    const int h = p.hg * a.heads + w.head;
+    const size_t slot = ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * a.heads + w.head;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * i + 2 * w.t + e;
+            if (r >= p.rows) continue;
+            if (whole) {
+                const float f = s.l[2 * i + e] == 0.f ? 0.f : 1.f / s.l[2 * i + e];
+                const int row = p.r0 + r;
+                uint32_t u[D / 16];
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) u[j] = pack_bf16(s.o[j][i][e] * f, s.o[j][i][2 + e] * f);
+                uint4* o = reinterpret_cast<uint4*>(
+                    a.o + (((size_t)p.b * a.P + row / a.G) * a.Hq + (size_t)h * a.G + row % a.G) * D + D / 8 * w.g);
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) o[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+            } else {
+                float4* o = reinterpret_cast<float4*>(a.part + (slot * kRows + r) * D + D / 8 * w.g);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                    o[j] = make_float4(s.o[2 * j][i][e], s.o[2 * j][i][2 + e], s.o[2 * j + 1][i][e], s.o[2 * j + 1][i][2 + e]);
+                if (w.g == 0) a.part_ml[slot * kRows + r] = make_float2(s.m[2 * i + e], s.l[2 * i + e]);
+            }
+        }
+}
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __grid_constant__ Args a)
+{
+    extern __shared__ __align__(128) unsigned char dyn[];
+    __shared__ Shared sh;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5;
+    const int splits = kConsumers / a.heads, chunk = 16 * tiles_of<BITS>() * splits;
+    Buffers buf;
+    buf.ring = dyn;
+    buf.q = reinterpret_cast<__half*>(dyn + (size_t)a.stages * 2 * a.half);
+    buf.f = reinterpret_cast<float*>(buf.q + (size_t)a.heads * kRows * (D + 8));
+    buf.join = reinterpret_cast<float4*>(buf.f + (size_t)a.heads * kRows);
+    buf.join_ml = reinterpret_cast<float2*>(buf.join + 4 * 2 * (D / 16) * 32);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMostStages; ++i) {
+            rdtc::mbar_init(&sh.full[i], 32 * kLoaders);
+            rdtc::mbar_init(&sh.empty[i], kConsumers);
+        }
+        rdtc::mbar_init(&sh.never, 1);
+        rdtc::mbar_fence_init();
+        sh.abort = 0;
+    }
+    const Division d = divide(a, sh, chunk);               // (its barriers order the set-up too)
+    __syncthreads();
+    if (warp >= kConsumers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        load<D, BITS>(a, sh, buf.ring, d, chunk);
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+    Place w;
+    w.warp = warp;
+    w.lane = threadIdx.x & 31;
+    w.g = w.lane >> 2;
+    w.t = w.lane & 3;
+    w.head = warp % a.heads;
+    w.split = warp / a.heads;
+    w.splits = splits;
+    bool alive = true;
+    if (a.stall > 0) {                     // the test hook: a wait that runs out
+        alive = rdattn::warp_wait(&sh.never, 0, &sh.abort, a.stall);
+        if (w.lane == 0) {
+            sh.abort = 1;
+            rd_flag(a.status, RD_DEV_TIMEOUT);
+        }
+    }
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    Walk walk(a, d, chunk);
+    Piece p;
+    uint32_t it = 0;
+    while (walk.next(p)) {
+        if (threadIdx.x == 0 && p.j0 == 0 && p.j1 < p.n) {
+            // the CTA that has the unit's last chunk
+            const uint64_t last = walk.S + (uint64_t)p.unit * unit_cost(walk.s) + kUnitCost + (uint64_t)(p.n - 1) * walk.s.chunk_cost;
+            a.desc[blockIdx.x] = make_int4(p.b, p.unit, (int)d.of(last), 0);
+        }
+        if (p.tiles == 1) piece<D, BITS, 1>(a, sh, buf, w, p, d, it, alive);
+        else if (p.tiles == 2) piece<D, BITS, 2>(a, sh, buf, w, p, d, it, alive);
+        else if (p.tiles == 3) piece<D, BITS, 3>(a, sh, buf, w, p, d, it, alive);
+        else piece<D, BITS, 4>(a, sh, buf, w, p, d, it, alive);
+    }
+}
+
+// o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the pieces of a cut unit
+template <int D>
+__global__ void __launch_bounds__(256) quant_merge_kernel(const Args a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 unit = a.desc[blockIdx.x];
+    const int first = blockIdx.x, last = unit.z;
+    if (unit.x < 0 || unit.x >= a.B || last <= first || last >= (int)gridDim.x) return;
+    const int len = a.lens[unit.x];
+    if (len <= 0 || len > a.P) return;
+    const int rows_all = len * a.G, groups = (rows_all + kRows - 1) / kRows;
+    const int per = ((rows_all + groups - 1) / groups + 7) & ~7;
+    const int hg = unit.y / groups, r0 = unit.y % groups * per;
+    const int rows = min(per, rows_all - r0), h = hg * a.heads + blockIdx.y;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        auto at = [&](int cta) { return (((size_t)2 * cta + (cta == first ? 1 : 0)) * a.heads + blockIdx.y) * kRows + r; };
+        float M = -INFINITY;
+        for (int k = first; k <= last; ++k) M = fmaxf(M, a.part_ml[at(k)].x);
+        const float mu = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = first; k <= last; ++k) {
+            const float2 ml = a.part_ml[at(k)];
+            const float4 v = reinterpret_cast<const float4*>(a.part)[at(k) * (D / 4) + c];
+            const float f = fast_exp2(ml.x - mu);
+            L += f * ml.y;
+            o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+        }
+        const float f = L == 0.f ? 0.f : 1.f / L;
+        const int row = r0 + r;
+        uint2 out;
+        out.x = pack_bf16(o.x * f, o.y * f);
+        out.y = pack_bf16(o.z * f, o.w * f);
+        reinterpret_cast<uint2*>(a.o)[((((size_t)unit.x * a.P + row / a.G) * a.Hq + (size_t)h * a.G + row % a.G) * D) / 4 + c] = out;
+    }
+}
+
+int heads_of(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
+
+// bytes apart in shared memory: four rows that a half-warp reads at once start 8 banks apart (4
+// bits), two that a quarter reads 16 banks (8 bits)
+int pitch_of(int seg, int bits)
+{
+    const int step = bits == 4 ? 32 : 64;
+    int p = (seg + step - 1) / step * step;
+    if (p / step % 2 == 0) p += step;
+    return p;
+}
+
+size_t desc_bytes(int grid) { return ((size_t)grid * sizeof(int4) + 127) & ~size_t(127); }
+
+template <int D, int BITS>
+cudaError_t launch(Args& a, int grid, cudaStream_t stream)
+{
+    const int splits = kConsumers / a.heads, chunk = 16 * tiles_of<BITS>() * splits;
+    a.seg = a.heads * rdquant::row_bytes(D, BITS);
+    a.pitch = pitch_of(a.seg, BITS);
+    const int stride = a.Hkv * rdquant::row_bytes(D, BITS);
+    a.gran = a.seg % 16 == 0 && stride % 16 == 0 ? 16 : a.seg % 8 == 0 && stride % 8 == 0 ? 8 : 4;
+    a.per_row = a.seg / a.gran;
+    a.per_row_magic = (uint32_t)((0x100000000ULL + a.per_row - 1) / a.per_row);
+    a.draft_pitch = a.heads * D * 2 + 16;
+    const int rows = chunk * a.pitch, drafts = kDraftTile * a.draft_pitch;
+    a.half = ((rows > drafts ? rows : drafts) + 127) / 128 * 128;
+    const int fixed = a.heads * kRows * ((D + 8) * 2 + 4) + 4 * 2 * (D / 16) * 32 * 16 + 4 * 8 * 32 * 8;
+    constexpr int kSmem = 227 * 1024 - 1024;               // what the static part leaves
+    a.stages = (kSmem - fixed) / (2 * a.half);
+    if (a.stages > kMostStages) a.stages = kMostStages;
+    const int smem = a.stages * 2 * a.half + fixed;
+    auto kernel = quant_attention_kernel<D, BITS>;
+    static const cudaError_t ready = [&]() {
+        cudaFuncAttributes f;
+        cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+        // setmaxnreg deals out the registers of the launch
+        return e != cudaSuccess ? e : f.numRegs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+    }();
+    if (ready != cudaSuccess) return ready;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, smem, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)a.heads);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, quant_merge_kernel<D>, (const Args&)a);
+}
+
+}  // namespace
+
+size_t rd_quant_attention_workspace_bytes(int Hkv, int D)
+{
+    const int grid = rd_device_sm_count();
+    const size_t rows = (size_t)2 * grid * heads_of(Hkv) * kRows;
+    return desc_bytes(grid) + rows * (sizeof(float2) + (size_t)D * sizeof(float));
+}
+
+cudaError_t rd_launch_quant_attention(const rd_quant_kv& kv, int B, int P_max, int Hq, int Hkv, int D, float scale,
+                                      const void* q, const void* k_new, const void* v_new, int max_ctx,
+                                      const int32_t* packed_len, const uint32_t* mask, int mask_words, void* o,
+                                      void* workspace, int32_t* dev_status, cudaStream_t stream)
+{
+    const int grid = rd_device_sm_count();
+    Args a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    a.k_pool = static_cast<const unsigned char*>(kv.k_pool);
+    a.v_pool = static_cast<const unsigned char*>(kv.v_pool);
+    a.table = kv.pages.block_table;
+    a.ctx_lens = kv.pages.ctx_lens;
+    a.lens = packed_len;
+    a.mask = mask;
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.heads = heads_of(Hkv);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.desc = reinterpret_cast<int4*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + desc_bytes(grid));
+    a.part = reinterpret_cast<float*>(a.part_ml + (size_t)2 * grid * a.heads * kRows);
+    a.status = dev_status;
+    a.B = B;
+    a.P = P_max;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.mask_words = mask_words;
+    a.num_pages = kv.pages.num_pages;
+    a.page_size = kv.pages.page_size;
+    a.max_pages = kv.pages.max_pages;
+    // no context is longer than its row of the table, or there is no page to read
+    const long long row = kv.pages.num_pages > 0 ? (long long)kv.pages.max_pages * kv.pages.page_size : 0;
+    a.max_ctx = (int)(row < max_ctx ? row : max_ctx);
+    a.scale_log2 = scale * kLog2e;
+    a.k_scale = kv.k_scale;
+    a.v_scale = kv.v_scale;
+    a.stall = rd_attention_stall_budget();
+    if (D == 128) return kv.bits == 4 ? launch<128, 4>(a, grid, stream) : launch<128, 8>(a, grid, stream);
+    return kv.bits == 4 ? launch<64, 4>(a, grid, stream) : launch<64, 8>(a, grid, stream);
+}

@@ -2,6 +2,7 @@
 // caller's stream.  See include/rd.h for the contract of every function.
 #include <atomic>
 
+#include "quant_format.cuh"
 #include "rd_internal.cuh"
 
 namespace {
@@ -490,6 +491,222 @@ rd_status rd_compact_pages(void* k_pool, void* v_pool, int layers, int num_pages
     const rd_page_pools pools = {k_pool, v_pool, layers, num_pages, page_bytes};
     return from_cuda(rd_launch_compact_pages(pools, block_table, R, max_pages, row_pages, page_refs, remap,
                                              n_live, workspace, dev_status, (cudaStream_t)stream));
+}
+
+// ---- the quantised paged cache
+namespace {
+
+bool scales_ok(float k_scale, float v_scale)
+{
+    return k_scale > 0.f && v_scale > 0.f && isfinite(k_scale) && isfinite(v_scale);
+}
+
+rd_status check_quant(int Hkv, int D, int bits, int num_pages, int page_size, int max_pages, float k_scale, float v_scale)
+{
+    if (Hkv < 1 || D < 1 || num_pages < 0 || page_size < 1 || max_pages < 0 || !scales_ok(k_scale, v_scale))
+        return RD_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || (bits != 4 && bits != 8) || Hkv > 65535) return RD_ERR_UNSUPPORTED;
+    return RD_OK;
+}
+
+rd_quant_kv quant_kv(const void* k_pool, const void* v_pool, float k_scale, float v_scale, int bits, int num_pages,
+                     int page_size, const int32_t* block_table, int max_pages, const int32_t* ctx_lens)
+{
+    rd_quant_kv kv;
+    kv.k_pool = const_cast<void*>(k_pool);
+    kv.v_pool = const_cast<void*>(v_pool);
+    kv.k_scale = k_scale;
+    kv.v_scale = v_scale;
+    kv.bits = bits;
+    kv.pages.block_table = block_table;
+    kv.pages.ctx_lens = ctx_lens;
+    kv.pages.max_pages = max_pages;
+    kv.pages.page_size = page_size;
+    kv.pages.num_pages = num_pages;
+    return kv;
+}
+
+}  // namespace
+
+int rd_quant_row_bytes(int D, int bits)
+{
+    return (D != 64 && D != 128) || (bits != 4 && bits != 8) ? 0 : rdquant::row_bytes(D, bits);
+}
+
+rd_status rd_append_quant(int B, int Hkv, int D, int bits, const void* k, const void* v, int64_t total_tokens,
+                          const int32_t* cu_seqlens, void* k_pool, void* v_pool, float k_scale, float v_scale,
+                          int num_pages, int page_size, const int32_t* block_table, int max_pages,
+                          const int32_t* ctx_lens, int32_t* new_ctx_lens, int32_t* dev_status, rd_stream_t stream)
+{
+    if (B < 0 || total_tokens < 0) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_quant(Hkv, D, bits, num_pages, page_size, max_pages, k_scale, v_scale);
+    if (st != RD_OK) return st;
+    if (total_tokens > 0x7fffffff) return RD_ERR_UNSUPPORTED;
+    if (B == 0) return RD_OK;
+    if (!cu_seqlens || !ctx_lens || !new_ctx_lens || (max_pages > 0 && !block_table) || (total_tokens > 0 && (!k || !v)) ||
+        (num_pages > 0 && (!k_pool || !v_pool)))
+        return RD_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool)) return RD_ERR_INVALID_ARG;
+    return from_cuda(rd_launch_append_quant(
+        quant_kv(k_pool, v_pool, k_scale, v_scale, bits, num_pages, page_size, block_table, max_pages, nullptr), B, Hkv, D, k,
+        v, total_tokens, cu_seqlens, ctx_lens, new_ctx_lens, dev_status, (cudaStream_t)stream));
+}
+
+rd_status rd_commit_accepted_quant(int B, int W, int L, int P_max, int Hkv, int D, int bits, const void* k_new,
+                                   const void* v_new, const int32_t* unpacker, const int32_t* best_beam,
+                                   const int32_t* n_accepted, void* k_pool, void* v_pool, float k_scale, float v_scale,
+                                   int num_pages, int page_size, const int32_t* block_table, int max_pages,
+                                   const int32_t* ctx_lens, int32_t* new_ctx_lens, int32_t* dev_status,
+                                   rd_stream_t stream)
+{
+    if (B < 0 || W < 1 || L < 1 || P_max < 1) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_quant(Hkv, D, bits, num_pages, page_size, max_pages, k_scale, v_scale);
+    if (st != RD_OK) return st;
+    if (B > 65535 || (long)W * L > 4096) return RD_ERR_UNSUPPORTED;
+    if (B == 0) return RD_OK;
+    if (!k_new || !v_new || !unpacker || !best_beam || !n_accepted || !ctx_lens || !new_ctx_lens ||
+        (max_pages > 0 && !block_table) || (num_pages > 0 && (!k_pool || !v_pool)))
+        return RD_ERR_INVALID_ARG;
+    if (ctx_lens == new_ctx_lens) return RD_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool)) return RD_ERR_INVALID_ARG;
+    return from_cuda(rd_launch_commit_quant(
+        quant_kv(k_pool, v_pool, k_scale, v_scale, bits, num_pages, page_size, block_table, max_pages, nullptr), B, W, L,
+        P_max, Hkv, D, k_new, v_new, unpacker, best_beam, n_accepted, ctx_lens, new_ctx_lens, dev_status,
+        (cudaStream_t)stream));
+}
+
+rd_status rd_read_quant(int B, int Hkv, int D, int bits, const void* k_pool, const void* v_pool, float k_scale, float v_scale,
+                        int num_pages, int page_size, const int32_t* block_table, int max_pages, const int64_t* offsets,
+                        const int32_t* starts, int64_t total, void* k_out, void* v_out, int32_t* dev_status,
+                        rd_stream_t stream)
+{
+    if (B < 0 || total < 0) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_quant(Hkv, D, bits, num_pages, page_size, max_pages, k_scale, v_scale);
+    if (st != RD_OK) return st;
+    if (B == 0 || total == 0) return RD_OK;
+    if (total > rd_quant_tokens_most(Hkv, D)) return RD_ERR_UNSUPPORTED;
+    if (!offsets || !k_out || !v_out || (max_pages > 0 && !block_table) || (num_pages > 0 && (!k_pool || !v_pool)))
+        return RD_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_pool) || !aligned16(v_pool)) return RD_ERR_INVALID_ARG;
+    return from_cuda(rd_launch_read_quant(
+        quant_kv(k_pool, v_pool, k_scale, v_scale, bits, num_pages, page_size, block_table, max_pages, nullptr), B, Hkv, D,
+        offsets, starts, total, k_out, v_out, dev_status, (cudaStream_t)stream));
+}
+
+size_t rd_tree_attention_quant_workspace_size(int B, int P_max, int Hq, int Hkv, int D, int max_ctx)
+{
+    if (B <= 0 || P_max < 1 || !attn_shape_ok(Hq, Hkv, D) || max_ctx < 0) return 0;
+    return rd_quant_attention_workspace_bytes(Hkv, D);
+}
+
+rd_status rd_tree_attention_quant(int B, int P_max, int Hq, int Hkv, int D, int bits, float scale, const void* q,
+                                  const void* k_new, const void* v_new, const void* k_pool, const void* v_pool,
+                                  float k_scale, float v_scale, int num_pages, int page_size, const int32_t* block_table,
+                                  int max_pages, const int32_t* ctx_lens, int max_ctx, const int32_t* packed_len,
+                                  const uint32_t* mask, int mask_words, void* o, void* workspace, size_t ws_bytes,
+                                  int32_t* dev_status, rd_stream_t stream)
+{
+    if (B < 0 || P_max < 1 || !attn_shape_ok(Hq, Hkv, D) || max_ctx < 0) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_quant(Hkv, D, bits, num_pages, page_size, max_pages, k_scale, v_scale);
+    if (st != RD_OK) return st;
+    if (page_size % 64 != 0) return RD_ERR_UNSUPPORTED;
+    if (P_max > RD_MAX_PACKED || B > 65535 || Hq > 65535) return RD_ERR_UNSUPPORTED;
+    if (mask_words != (P_max + 31) / 32) return RD_ERR_INVALID_ARG;
+    if (B == 0) return RD_OK;
+    if (!q || !k_new || !v_new || !ctx_lens || !packed_len || !mask || !o || !workspace ||
+        (max_pages > 0 && !block_table) || (num_pages > 0 && (!k_pool || !v_pool)))
+        return RD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool) ||
+        !aligned16(o) || !aligned16(workspace))
+        return RD_ERR_INVALID_ARG;
+    if (ws_bytes < rd_quant_attention_workspace_bytes(Hkv, D)) return RD_ERR_INVALID_ARG;
+    if (scale <= 0.f) scale = 1.0f / sqrtf((float)D);
+    return from_cuda(rd_launch_quant_attention(
+        quant_kv(k_pool, v_pool, k_scale, v_scale, bits, num_pages, page_size, block_table, max_pages, ctx_lens), B, P_max, Hq,
+        Hkv, D, scale, q, k_new, v_new, max_ctx < kRdMaxContext ? max_ctx : kRdMaxContext, packed_len, mask, mask_words, o,
+        workspace, dev_status, (cudaStream_t)stream));
+}
+
+// ---- log probabilities
+namespace {
+
+rd_status check_logprobs(rd_dtype dt, int V, float temperature, int top)
+{
+    if (V < 1 || top < 0 || top > V || !(temperature >= 0x1p-126f) || !isfinite(temperature)) return RD_ERR_INVALID_ARG;
+    if ((dt != RD_BF16 && dt != RD_F16 && dt != RD_F32) || top > RD_MAX_TOP || V > (1 << 30)) return RD_ERR_UNSUPPORTED;
+    return RD_OK;
+}
+
+bool aligned_to(const void* p, rd_dtype dt) { return (reinterpret_cast<uintptr_t>(p) & (dt == RD_F32 ? 3 : 1)) == 0; }
+
+}  // namespace
+
+rd_status rd_token_logprobs(const void* logits, rd_dtype dt, int64_t n_rows, int V, const int32_t* rows,
+                            const int32_t* tokens, int64_t n, float temperature, int top, float* logprob, float* entropy,
+                            int32_t* top_tokens, float* top_logprobs, int32_t* dev_status, rd_stream_t stream)
+{
+    if (n_rows < 0 || n < 0 || (!rows && n > n_rows)) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_logprobs(dt, V, temperature, top);
+    if (st != RD_OK) return st;
+    if (n > 0x7fffffff) return RD_ERR_UNSUPPORTED;
+    if (n == 0) return RD_OK;
+    if ((n_rows > 0 && !logits) || !tokens || !logprob || !entropy || (top > 0 && (!top_tokens || !top_logprobs)))
+        return RD_ERR_INVALID_ARG;
+    if (!aligned_to(logits, dt)) return RD_ERR_INVALID_ARG;
+    rd_logprobs a = {};
+    a.logits = logits;
+    a.dt = dt;
+    a.n_rows = n_rows;
+    a.n = n;
+    a.V = V;
+    a.top = top;
+    a.temperature = temperature;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_tokens = top_tokens;
+    a.top_logprobs = top_logprobs;
+    a.dev_status = dev_status;
+    return from_cuda(rd_launch_logprobs(a, (cudaStream_t)stream));
+}
+
+rd_status rd_accepted_logprobs(const void* logits, rd_dtype dt, int B, int P_max, int V, const int32_t* unpacker, int W, int L,
+                               const int32_t* best_beam, const int32_t* n_accepted, const int32_t* out_tokens,
+                               float temperature, int top, float* logprob, float* entropy, int32_t* top_tokens,
+                               float* top_logprobs, int32_t* dev_status, rd_stream_t stream)
+{
+    if (B < 0 || P_max < 1 || W < 1 || L < 1) return RD_ERR_INVALID_ARG;
+    const rd_status st = check_logprobs(dt, V, temperature, top);
+    if (st != RD_OK) return st;
+    if (W > RD_MAX_BEAMS || P_max > RD_MAX_PACKED || (long)W * L > 4096 || (long long)B * L > 0x7fffffff)
+        return RD_ERR_UNSUPPORTED;
+    if (B == 0) return RD_OK;
+    if (!logits || !unpacker || !best_beam || !n_accepted || !out_tokens || !logprob || !entropy ||
+        (top > 0 && (!top_tokens || !top_logprobs)))
+        return RD_ERR_INVALID_ARG;
+    if (!aligned_to(logits, dt)) return RD_ERR_INVALID_ARG;
+    rd_logprobs a = {};
+    a.logits = logits;
+    a.dt = dt;
+    a.n_rows = (int64_t)B * P_max;
+    a.n = (int64_t)B * L;
+    a.V = V;
+    a.top = top;
+    a.temperature = temperature;
+    a.tokens = out_tokens;
+    a.unpacker = unpacker;
+    a.best_beam = best_beam;
+    a.n_accepted = n_accepted;
+    a.W = W;
+    a.L = L;
+    a.P_max = P_max;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_tokens = top_tokens;
+    a.top_logprobs = top_logprobs;
+    a.dev_status = dev_status;
+    return from_cuda(rd_launch_logprobs(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

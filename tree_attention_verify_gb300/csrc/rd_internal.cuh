@@ -151,3 +151,45 @@ cudaError_t rd_launch_copy_pages(const rd_page_pools& pools, const int32_t* src,
 cudaError_t rd_launch_compact_pages(const rd_page_pools& pools, int32_t* block_table, int R, int max_pages,
                                     const int32_t* row_pages, int32_t* page_refs, int32_t* remap,
                                     int32_t* n_live, void* workspace, int32_t* dev_status, cudaStream_t stream);
+
+// The quantised paged cache (quant_cache.cu writes and reads it, quant_attention.cu attends to it).
+struct rd_quant_kv {
+    void* k_pool;             // [num_pages, page_size, Hkv, row bytes] (quant_format.cuh)
+    void* v_pool;
+    float k_scale, v_scale;
+    int bits;                 // 4 or 8
+    rd_paged_kv pages;        // (ctx_lens: the attention's)
+};
+int64_t rd_quant_tokens_most(int Hkv, int D);      // what one launch covers
+cudaError_t rd_launch_append_quant(const rd_quant_kv& kv, int B, int Hkv, int D, const void* k, const void* v, int64_t total,
+                                   const int32_t* cu_seqlens, const int32_t* ctx_lens, int32_t* new_ctx_lens,
+                                   int32_t* dev_status, cudaStream_t stream);
+cudaError_t rd_launch_commit_quant(const rd_quant_kv& kv, int B, int W, int L, int P_max, int Hkv, int D, const void* k_new,
+                                   const void* v_new, const int32_t* unpacker, const int32_t* best_beam,
+                                   const int32_t* n_accepted, const int32_t* ctx_lens, int32_t* new_ctx_lens,
+                                   int32_t* dev_status, cudaStream_t stream);
+cudaError_t rd_launch_read_quant(const rd_quant_kv& kv, int B, int Hkv, int D, const int64_t* offsets, const int32_t* starts,
+                                 int64_t total, void* k_out, void* v_out, int32_t* dev_status, cudaStream_t stream);
+size_t rd_quant_attention_workspace_bytes(int Hkv, int D);
+cudaError_t rd_launch_quant_attention(const rd_quant_kv& kv, int B, int P_max, int Hq, int Hkv, int D, float scale,
+                                      const void* q, const void* k_new, const void* v_new, int max_ctx,
+                                      const int32_t* packed_len, const uint32_t* mask, int mask_words, void* o,
+                                      void* workspace, int32_t* dev_status, cudaStream_t stream);
+
+// Log probabilities of tokens (logprobs.cu).
+struct rd_logprobs {
+    const void* logits;       // [n_rows, V] of dt
+    rd_dtype dt;
+    int64_t n_rows, n;        // rows of logits, entries of the output
+    int V, top;
+    float temperature;
+    const int32_t* tokens;    // [n]
+    const int32_t* rows;      // [n], or null: entry n is row n
+    const int32_t *unpacker, *best_beam, *n_accepted;      // entries (b, i) of an accepted path, if given
+    int W, L, P_max;
+    float *logprob, *entropy;
+    int32_t* top_tokens;
+    float* top_logprobs;
+    int32_t* dev_status;
+};
+cudaError_t rd_launch_logprobs(const rd_logprobs& q, cudaStream_t stream);
