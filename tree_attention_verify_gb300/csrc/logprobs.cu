@@ -4,15 +4,15 @@
 // One pass over each row.  In units of log2, with c = log2(e) / T and a reference m,
 //   z = c (x - m),  l = sum 2^z,  w = sum 2^z z:
 //   log p(x_t) = ln 2 (z_t - log2 l),   H = ln 2 (log2 l - w / l).
-// The reference need not be the maximum: 32-bit floats hold 2^z up to 2^127, so a thread keeps
-// that of its first logits and only moves it when a logit lies 2^64 above.  So a logit costs a
-// difference, a product, an exponential and two accumulations, about half of what the SM can
-// issue while HBM delivers 16-bit logits.  (c x - c m in one operation would leave 32 bits for
-// logits above 2^127 / c.)
+// The reference is the maximum of the CTA's first 16,384 logits; a thread that meets a larger one
+// moves its own.  So a logit costs a difference, a product, a lower bound (2^-200 is 0, and 0 x -200
+// too: a logit of -inf adds nothing), an exponential and two accumulations: about 60 instructions
+// for eight 16-bit logits, somewhat more than half of what the SM can issue while HBM
+// delivers them.  What is rare (a larger maximum, a candidate) stays out of the loop's way.
 //
 // The top k come from the same pass: a threshold that at least k logits of the row reach
 // is known after the first 64 logits of each thread (the k-th largest of the threads'
-// maxima); what reaches it afterwards, a few times k of them, is collected as 64-bit keys
+// maxima, found bit by bit); what reaches it afterwards, a few times k of them, is collected as 64-bit keys
 // (value, then the lower index first) and ranked by counting at the end.  A row that keeps
 // rising overfills the list; its k-th key is then a better threshold for another pass.
 //
@@ -33,7 +33,6 @@ constexpr int kAhead = 8;                  // 16-byte loads of a thread in fligh
 constexpr int kMostCtas = 8;               // of a row
 constexpr int kList = 1024;                // candidates of a CTA
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kFar = 64.f;               // how far (log2) a logit may lie above the reference
 
 struct Args {
     const void* logits;
@@ -51,6 +50,19 @@ struct Args {
     int32_t* status;
 };
 
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float exp2_(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ------------------------------------------------------------------ 16 bytes of logits
 template <typename T>
 struct Vec;
@@ -61,6 +73,11 @@ struct Vec<float> {
     static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[4])
     {
         x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    }
+    static constexpr uint32_t kNone = 0xff800000u;       // -inf
+    static __device__ __forceinline__ float top(const uint4& u)
+    {
+        return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)), max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
     }
 };
 template <>
@@ -79,6 +96,18 @@ struct Vec<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    static constexpr uint32_t kNone = 0xff80ff80u;
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t d;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ float top(const uint4& u)
+    {
+        const uint32_t t = max2(max2(u.x, u.y), max2(u.z, u.w));
+        return max_nan(__uint_as_float(t << 16), __uint_as_float(t & 0xffff0000u));
+    }
 };
 template <>
 struct Vec<__half> {
@@ -94,20 +123,20 @@ struct Vec<__half> {
             x[2 * i + 1] = v.y;
         }
     }
+    static constexpr uint32_t kNone = 0xfc00fc00u;
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t d;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ float top(const uint4& u)
+    {
+        const uint32_t t = max2(max2(u.x, u.y), max2(u.z, u.w));
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t));
+        return max_nan(v.x, v.y);
+    }
 };
-
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ float exp2_(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // numbers as unsigned ones of the same order (-0 as +0), and back
 __device__ __forceinline__ uint32_t ordered(float x)
@@ -184,18 +213,24 @@ struct Row {
     }
     __device__ __forceinline__ bool inside(int g) const { return g * N >= off && (g + 1) * N - off <= V; }
     __device__ __forceinline__ int index(int g, int e) const { return g * N + e - off; }
-    // a group that lies partly outside, element by element; what is outside counts as -inf
-    __device__ __forceinline__ void edge(int g, float (&v)[N]) const
+    // a group that lies partly outside of the row, element by element; what is outside counts as -inf
+    __device__ __noinline__ uint4 edge(int g) const
     {
-#pragma unroll
+        union {
+            uint4 u;
+            T x[N];
+        } v;
+        constexpr uint32_t none = Vec<T>::kNone;
+        v.u = make_uint4(none, none, none, none);
         for (int e = 0; e < N; ++e) {
             const int i = index(g, e);
-            v[e] = i >= 0 && i < V ? Vec<T>::one(x, i) : -INFINITY;
+            if (i >= 0 && i < V) v.x[e] = x[i];
         }
+        return v.u;
     }
+    __device__ __forceinline__ uint4 group(int g) const;
 };
 
-template <typename T>
 __device__ __forceinline__ uint4 load16(const uint4* p)
 {
     uint4 v;
@@ -204,32 +239,16 @@ __device__ __forceinline__ uint4 load16(const uint4* p)
     return v;
 }
 
-template <int N>
-__device__ __forceinline__ float top_of(const float (&x)[N])
-{
-    float t = x[0];
-#pragma unroll
-    for (int e = 1; e < N; ++e) t = max_nan(t, x[e]);
-    return t;
-}
+template <typename T>
+__device__ __forceinline__ uint4 Row<T>::group(int g) const { return inside(g) ? load16(base + g) : edge(g); }
 
-template <int N>
-__device__ __forceinline__ void add(Stats& s, const float (&x)[N], float top, float c)
+// the logits of group g that are among the top k as far as is known
+template <typename T>
+__device__ __noinline__ void collect(Shared& sh, const Row<T>& row, int g, uint4 u, unsigned long long least)
 {
-    if (top == -INFINITY) return;
-    if (!((top - s.m) * c <= kFar)) s.move(top, c);      // (the first time too)
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        // 2^-200 is 0, and 0 x -200 too: an element of -inf adds nothing
-        const float z = max_nan((x[e] - s.m) * c, -200.f), p = exp2_(z);
-        s.l += p;
-        s.w = fmaf(p, z, s.w);
-    }
-}
-
-template <typename T, int N>
-__device__ __forceinline__ void collect(Shared& sh, const Row<T>& row, int g, const float (&x)[N], unsigned long long least)
-{
+    constexpr int N = Vec<T>::n;
+    float x[N];
+    Vec<T>::unpack(u, x);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         const int i = row.index(g, e);
@@ -251,7 +270,7 @@ __device__ __forceinline__ void rank(Shared& sh, int n, int k, unsigned long lon
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ Args a)
 {
     __shared__ Shared sh;
     constexpr int N = Vec<T>::n;
@@ -304,53 +323,72 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const __grid_cons
     const Row<T> row(x, a.V, part, parts);
     const float chosen = part == 0 && tid == 0 ? Vec<T>::one(x, token) : 0.f;
     if (tid == 0) sh.count = 0;
+    if (tid < 32) sh.best[tid] = 0;
     Stats s = {-INFINITY, 0.f, 0.f};
+    float l1 = 0.f, w1 = 0.f;              // (two chains of sums, of one reference)
     unsigned long long least = 0;
-    float floor_ = -INFINITY;              // no logit below it is among the top k
+    float floor_ = -INFINITY;              // what reaches it is looked at
     constexpr int kStep = kThreads * kAhead;
     for (int g0 = row.first; g0 < row.last; g0 += kStep) {
         uint4 u[kAhead];
-        bool in[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int g = g0 + j * kThreads + tid;
-            in[j] = g < row.last && row.inside(g);
-            if (in[j]) u[j] = load16<T>(row.base + g);
+            u[j] = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
+            if (g < row.last) u[j] = row.group(g);
         }
-        if (g0 == row.first && k > 0) {
-            // the k-th largest of the threads' maxima, to 16 bits below
-            float top = -INFINITY;
-            bool some = false;
+        if (g0 == row.first) {
+            float top = Vec<T>::top(u[0]);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int g = g0 + j * kThreads + tid;
-                if (g >= row.last) continue;
-                float v[N];
-                if (in[j]) Vec<T>::unpack(u[j], v);
-                else row.edge(g, v);
-                top = max_nan(top, top_of<N>(v));
-                some = true;
+            for (int j = 1; j < kAhead; ++j) top = max_nan(top, Vec<T>::top(u[j]));
+            const uint32_t mine = g0 + tid < row.last ? ordered(top) : 0u;
+            const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
+            if (lane == 0) sh.warp[warp].m = __uint_as_float(warp_top);
+            __syncthreads();
+            uint32_t most = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) most = max(most, __float_as_uint(sh.warp[w].m));
+            s.m = number(most);
+            floor_ = s.m;
+            if (k > 0) {
+                // the k-th largest of the threads' maxima, rounded down to 16 bits
+                uint32_t at = 0;
+                for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1)
+                    if (__syncthreads_count(mine >> 16 >= (at | bit)) >= k) at |= bit;
+                least = (unsigned long long)at << 48;
+                floor_ = number(at << 16);
+                if (at == 0 || floor_ != floor_) floor_ = -INFINITY;
             }
-            const uint32_t mine = some ? ordered(top) >> 16 : 0u;
-            uint32_t at = 0;
-            for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1)
-                if (__syncthreads_count(mine >= (at | bit)) >= k) at |= bit;
-            least = (unsigned long long)at << 48;
-            floor_ = number(at << 16);
-            if (at == 0 || floor_ != floor_) floor_ = -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int g = g0 + j * kThreads + tid;
-            if (g >= row.last) continue;
+            const float top = Vec<T>::top(u[j]);
+            if (!(top < floor_)) {
+                const int g = g0 + j * kThreads + tid;
+                if (k > 0 && g < row.last) collect<T>(sh, row, g, u[j], least);
+                if (!(top <= s.m)) {
+                    s.l += l1, s.w += w1;
+                    l1 = w1 = 0.f;
+                    s.move(top, a.c);
+                }
+            }
+            if (s.m == -INFINITY) continue;
             float v[N];
-            if (in[j]) Vec<T>::unpack(u[j], v);
-            else row.edge(g, v);
-            const float top = top_of<N>(v);
-            add<N>(s, v, top, a.c);
-            if (k > 0 && !(top < floor_)) collect<T, N>(sh, row, g, v, least);
+            Vec<T>::unpack(u[j], v);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                const float z0 = max_nan((v[e] - s.m) * a.c, -200.f), z1 = max_nan((v[e + 1] - s.m) * a.c, -200.f);
+                const float p0 = exp2_(z0), p1 = exp2_(z1);
+                s.l += p0;
+                l1 += p1;
+                s.w = fmaf(p0, z0, s.w);
+                w1 = fmaf(p1, z1, w1);
+            }
         }
     }
+    s.l += l1;
+    s.w += w1;
+    __syncthreads();                       // (sh.warp is read above and written below)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         Stats b;
@@ -363,7 +401,6 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const __grid_cons
         s = lo;
     }
     if (lane == 0) sh.warp[warp] = s;
-    if (tid < 32) sh.best[tid] = 0;
     __syncthreads();
     if (k > 0) {
         while (sh.count > kList) {         // too many: the k-th of those kept is a better threshold
@@ -376,10 +413,8 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const __grid_cons
             if (tid == 0) sh.count = 0;
             __syncthreads();
             for (int g = row.first + tid; g < row.last; g += kThreads) {
-                float v[N];
-                if (row.inside(g)) Vec<T>::unpack(load16<T>(row.base + g), v);
-                else row.edge(g, v);
-                if (!(top_of<N>(v) < floor_)) collect<T, N>(sh, row, g, v, least);
+                const uint4 u = row.group(g);
+                if (!(Vec<T>::top(u) < floor_)) collect<T>(sh, row, g, u, least);
             }
             if (tid < 32) sh.best[tid] = 0;
             __syncthreads();
