@@ -38,6 +38,7 @@ constexpr int kComputeRegs = 232, kLoadRegs = 40;
 static_assert(32 * kConsumers * kComputeRegs + 32 * kLoaders * kLoadRegs <= kThreads * kLaunchRegs, "registers");
 constexpr int kRows = 32;                  // rows of a unit at most
 constexpr int kDraftTile = 16;             // packed drafts of a chunk
+constexpr int kPairTiles = 2;              // up to 16 rows, two tiles of positions at a time
 constexpr int kMostStages = 8;
 constexpr long long kWaitBudget = 4000000000LL;     // cycles, about two seconds
 constexpr float kLog2e = 1.4426950408889634f;
@@ -68,6 +69,8 @@ struct Args {
     int seg, pitch, gran, per_row;     // bytes of a position's rows, apart in shared memory, a copy; copies
     uint32_t per_row_magic;
     int draft_pitch, half, stages;     // bytes of a stage's K (and of its V)
+    bool tiled;                // the pools' rows come as TMA boxes
+    CUtensorMap k_map, v_map;
 };
 
 // ------------------------------------------------------------------ the division of the work
@@ -75,39 +78,47 @@ struct Args {
 // (context, then tiles of drafts) stand in one sequence with all other units', weighted by
 // what they cost, and the CTAs take equal ranges of it.
 struct Shape {
-    int rows, groups, per;     // rows of the request, row groups, rows of a group (a multiple of 8)
-    int C, n_ctx, n;           // context, its chunks, all chunks
-    uint32_t chunk_cost, unit_cost;
-    uint64_t cost;             // of the request
+    int len, C;                // nodes (0: the request is skipped or has none), context
+    __device__ __forceinline__ int rows(const Args& a) const { return len * a.G; }
+    // row groups, and rows of a group (a multiple of 8)
+    __device__ __forceinline__ int groups(const Args& a) const { return (rows(a) + kRows - 1) / kRows; }
+    __device__ __forceinline__ int per(const Args& a) const { return ((rows(a) + groups(a) - 1) / groups(a) + 7) & ~7; }
+    // chunks of the context, and all
+    __device__ __forceinline__ int n_ctx(int chunk) const { return (int)(((uint32_t)C + (uint32_t)chunk - 1u) / (uint32_t)chunk); }
+    __device__ __forceinline__ int n(int chunk) const { return n_ctx(chunk) + (len + kDraftTile - 1) / kDraftTile; }
+    __device__ __forceinline__ uint32_t chunk_cost(const Args& a) const;
+    __device__ __forceinline__ uint32_t unit_cost(const Args& a, int chunk) const;
+    __device__ __forceinline__ uint64_t cost(const Args& a, int chunk) const
+    {
+        return len == 0 ? 0 : (uint64_t)unit_cost(a, chunk) * (uint32_t)(groups(a) * (a.Hkv / a.heads));
+    }
 };
 
 // Widening a chunk costs the same for any number of rows, its products go with them (measured
-// beside the kernel); a unit's start and end take as long as a few chunks.
-__host__ __device__ constexpr uint32_t chunk_cost(int tiles) { return 3u + 2u * (uint32_t)tiles; }
+// beside the kernel); a unit's start and end take as long as a few chunks.  (A unit of 2^31
+// positions in chunks of 32 costs less than 2^30.)
+__host__ __device__ constexpr uint32_t cost_of_tiles(int tiles) { return 3u + 2u * (uint32_t)tiles; }
 constexpr uint32_t kUnitCost = 24;
 constexpr uint32_t kLeastCost = 24;        // of a CTA's range: at least two chunks
-
-__device__ __forceinline__ Shape shape_of(const Args& a, int b, int chunk)
+__device__ __forceinline__ uint32_t Shape::chunk_cost(const Args& a) const { return cost_of_tiles(per(a) / 8); }
+__device__ __forceinline__ uint32_t Shape::unit_cost(const Args& a, int chunk) const
 {
-    Shape s;
-    s.cost = 0;
-    const int len = a.lens[b];
-    if (len <= 0 || len > a.P) return s;
-    s.C = a.ctx_lens[b];
-    if (s.C < 0 || s.C > a.max_ctx) return s;
-    s.rows = len * a.G;
-    s.groups = (s.rows + kRows - 1) / kRows;
-    s.per = ((s.rows + s.groups - 1) / s.groups + 7) & ~7;
-    s.n_ctx = (int)(((int64_t)s.C + chunk - 1) / chunk);
-    s.n = s.n_ctx + (len + kDraftTile - 1) / kDraftTile;
-    s.chunk_cost = chunk_cost(s.per / 8);
-    s.unit_cost = 0;
-    const uint64_t unit = kUnitCost + (uint64_t)s.n * s.chunk_cost;
-    s.cost = unit * (uint64_t)s.groups * (uint64_t)(a.Hkv / a.heads);
-    return s;
+    return kUnitCost + (uint32_t)n(chunk) * chunk_cost(a);
 }
 
-__device__ __forceinline__ uint64_t unit_cost(const Shape& s) { return kUnitCost + (uint64_t)s.n * s.chunk_cost; }
+__device__ __forceinline__ Shape shape_of(const Args& a, int b)
+{
+    Shape s;
+    s.len = a.lens[b];
+    s.C = 0;
+    if (s.len <= 0 || s.len > a.P) {
+        s.len = 0;
+        return s;
+    }
+    s.C = a.ctx_lens[b];
+    if (s.C < 0 || s.C > a.max_ctx) s.len = 0;
+    return s;
+}
 
 struct Division {
     uint64_t W;                // cost of everything
@@ -129,66 +140,59 @@ struct Division {
 };
 
 struct Piece {
-    int b, hg, r0, rows;       // request, head group, first row, rows
-    int j0, j1, n_ctx, n, C;   // chunks of this piece, context chunks and all chunks of the unit
-    int unit;                  // within the request
-    int tiles;                 // of 8 rows
+    int b, unit;               // request, unit within it
+    int hg, r0, rows;          // head group, first row, rows
+    int j0, j1;                // chunks of this piece
+    int C, len, n_ctx;         // context, nodes, chunks of the context
+    __device__ __forceinline__ int n() const { return n_ctx + (len + kDraftTile - 1) / kDraftTile; }
 };
 
 // The pieces of a CTA's range, one after the other; every warp walks through them by itself.
 struct Walk {
-    const Args& a;
-    const int chunk;
-    uint64_t lo, hi, S;
-    int b, unit;
-    Shape s;
-    __device__ __forceinline__ Walk(const Args& args, const Division& d, int chunk_) : a(args), chunk(chunk_)
+    uint64_t lo, hi, S;        // the range, and where the request begins
+    int b, unit;               // the next unit to look at (-1: the first in the range)
+    __device__ __forceinline__ Walk(const Args& a, const Division& d)
     {
         const uint32_t c = blockIdx.x;
-        lo = hi = 0;
+        const bool idle = d.W == 0 || c >= d.n;
         S = d.S;
-        b = d.b;
+        b = idle ? a.B : d.b;
         unit = -1;
-        if (d.W == 0 || c >= d.n) {
-            b = a.B;
-            return;
-        }
-        lo = d.begin(c);
-        hi = c + 1 < d.n ? d.begin(c + 1) : d.W;
-        if (b < a.B) s = shape_of(a, b, chunk);
+        lo = idle ? 0 : d.begin(c);
+        hi = idle ? 0 : c + 1 < d.n ? d.begin(c + 1) : d.W;
     }
-    __device__ __forceinline__ bool next(Piece& p)
+    __device__ __forceinline__ bool next(const Args& a, int chunk, Piece& p)
     {
-        for (; b < a.B && S < hi;) {
-            if (s.cost != 0) {
-                const uint64_t uc = unit_cost(s);
+        while (b < a.B && S < hi) {
+            const Shape s = shape_of(a, b);
+            if (s.len != 0) {
+                const uint32_t uc = s.unit_cost(a, chunk), c = s.chunk_cost(a);
+                const int groups = s.groups(a), units = groups * (a.Hkv / a.heads);
                 if (unit < 0) unit = lo > S ? (int)((lo - S) / uc) : 0;
-                const int units = s.groups * (a.Hkv / a.heads);
                 while (unit < units) {
-                    const uint64_t first = S + (uint64_t)unit * uc + kUnitCost;
-                    if (S + (uint64_t)unit * uc >= hi) return false;
-                    const uint64_t c = s.chunk_cost;
-                    const uint64_t j0 = lo > first ? (lo - first + c - 1) / c : 0;
-                    const uint64_t j1 = hi > first ? min((uint64_t)s.n, (hi - first + c - 1) / c) : 0;
-                    const int u = unit++;
-                    if (j0 >= j1) continue;
+                    const uint64_t at = S + (uint64_t)unit * uc, first = at + kUnitCost;
+                    if (at >= hi) return false;
+                    const int n = s.n(chunk);
+                    // (a range that ends behind the unit takes all of its chunks)
+                    const uint32_t j0 = lo > first ? (uint32_t)min((uint64_t)uc, lo - first) : 0;
+                    const uint32_t j1 = hi > first ? (uint32_t)min((uint64_t)uc, hi - first) : 0;
+                    p.j0 = (int)((j0 + c - 1) / c);
+                    p.j1 = min(n, (int)((j1 + c - 1) / c));
+                    p.unit = unit++;
+                    if (p.j0 >= p.j1) continue;
                     p.b = b;
-                    p.unit = u;
-                    p.hg = u / s.groups;
-                    p.r0 = (u % s.groups) * s.per;
-                    p.rows = min(s.per, s.rows - p.r0);
-                    p.tiles = (p.rows + 7) / 8;
-                    p.j0 = (int)j0;
-                    p.j1 = (int)j1;
-                    p.n_ctx = s.n_ctx;
-                    p.n = s.n;
+                    p.hg = p.unit / groups;
+                    p.r0 = p.unit % groups * s.per(a);
+                    p.rows = min(s.per(a), s.rows(a) - p.r0);
                     p.C = s.C;
+                    p.len = s.len;
+                    p.n_ctx = s.n_ctx(chunk);
                     return true;
                 }
-                S += s.cost;
+                S += s.cost(a, chunk);
             }
             unit = 0;
-            if (++b < a.B) s = shape_of(a, b, chunk);
+            ++b;
         }
         return false;
     }
@@ -196,7 +200,7 @@ struct Walk {
 
 struct Shared {                            // static part
     uint64_t full[kMostStages], empty[kMostStages], never;
-    int abort;
+    int abort, never_abort;
     int b;
     unsigned long long S, sum[kThreads / 32];
 };
@@ -207,12 +211,9 @@ __device__ __forceinline__ Division divide(const Args& a, Shared& sh, int chunk)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned long long mine = 0;
     for (int b = tid; b < a.B; b += kThreads) {
-        const Shape s = shape_of(a, b, chunk);
-        mine += s.cost;
-        if (blockIdx.x == 0) {
-            const int len = a.lens[b];
-            if (len < 0 || len > a.P || (len > 0 && s.cost == 0)) rd_flag(a.status, RD_DEV_BAD_LENGTH);
-        }
+        const Shape s = shape_of(a, b);
+        mine += s.cost(a, chunk);
+        if (blockIdx.x == 0 && s.len != a.lens[b]) rd_flag(a.status, RD_DEV_BAD_LENGTH);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -231,7 +232,7 @@ __device__ __forceinline__ Division divide(const Args& a, Shared& sh, int chunk)
     uint64_t before = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
-        const unsigned long long cost = b < a.B ? shape_of(a, b, chunk).cost : 0;
+        const unsigned long long cost = b < a.B ? shape_of(a, b).cost(a, chunk) : 0;
         unsigned long long inc = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -346,16 +347,88 @@ __device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t
     }
 }
 
-template <int D, int BITS>
-__device__ __forceinline__ void load(const Args& a, Shared& sh, unsigned char* ring, const Division& d, int chunk)
+// where the 64 positions from pos0 + 64 k of request b lie: the pool's row
+__device__ __forceinline__ int64_t row_at(const Args& a, int b, int pos, bool flags)
 {
-    const int tid = threadIdx.x - 32 * kConsumers;
-    const size_t row = (size_t)a.Hkv * a.seg / a.heads;
-    Walk walk(a, d, chunk);
+    int page = a.table[(size_t)b * a.max_pages + pos / a.page_size];
+    if (page < 0 || page >= a.num_pages) {
+        if (flags) rd_flag(a.status, RD_DEV_BAD_INDEX);
+        page = 0;
+    }
+    return (int64_t)page * a.page_size + pos % a.page_size;
+}
+
+// One warp fetches everything by TMA: a box of up to 64 positions x the unit's heads (for 8 bits one
+// for each 128 bytes of them, swizzled) per pool, the drafts' rows as bulk copies.  Lane k looks
+// up the k-th block of 64 positions of the next chunk while it waits.
+template <int D, int BITS>
+__device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned char* ring, const Division& d, int chunk)
+{
+    const int lane = threadIdx.x & 31;
+    const int box = chunk < 64 ? chunk : 64, row_bytes_ = a.heads * D * 2;
+    Walk walk(a, d);
     Piece p;
     uint32_t it = 0;
     bool alive = true;
-    while (walk.next(p)) {
+    while (walk.next(a, chunk, p)) {
+        for (int j = p.j0; j < p.j1; ++j, ++it) {
+            const int stage = (int)(it % (uint32_t)a.stages);
+            const int pos0 = j * chunk, rows = j < p.n_ctx ? min(chunk, p.C - pos0) : 0, blocks = (rows + box - 1) / box;
+            int64_t row = 0;
+            if (lane < blocks) row = row_at(a, p.b, pos0 + lane * box, true);
+            if (alive && it >= (uint32_t)a.stages)
+                alive = rdattn::warp_wait(&sh.empty[stage], ((it / (uint32_t)a.stages) & 1u) ^ 1u, &sh.abort, kWaitBudget);
+            unsigned char* k_to = ring + (size_t)stage * 2 * a.half;
+            unsigned char* v_to = k_to + a.half;
+            uint64_t* bar = &sh.full[stage];
+            if (j < p.n_ctx) {
+                if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * blocks * box * a.seg));
+                __syncwarp();
+                if (lane < blocks) {
+                    if constexpr (BITS == 4) {
+                        const size_t to = (size_t)lane * box * a.seg;
+                        rdtc::tma_load_2d(k_to + to, &a.k_map, bar, p.hg * (a.seg / 4), (int)row);
+                        rdtc::tma_load_2d(v_to + to, &a.v_map, bar, p.hg * (a.seg / 4), (int)row);
+                    } else {
+                        for (int x = 0; x < a.seg / 128; ++x) {
+                            const size_t to = (size_t)x * chunk * 128 + (size_t)lane * box * 128;
+                            rdtc::tma_load_2d(k_to + to, &a.k_map, bar, p.hg * (a.seg / 4) + 32 * x, (int)row);
+                            rdtc::tma_load_2d(v_to + to, &a.v_map, bar, p.hg * (a.seg / 4) + 32 * x, (int)row);
+                        }
+                    }
+                }
+            } else {
+                const int node0 = (j - p.n_ctx) * kDraftTile;
+                const int nodes = min(kDraftTile, p.len - node0);
+                if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * nodes * row_bytes_));
+                __syncwarp();
+                if (lane < nodes) {
+                    const size_t at = (((size_t)p.b * a.P + node0 + lane) * a.Hkv + (size_t)p.hg * a.heads) * D;
+                    rdtc::bulk_load(k_to + lane * a.draft_pitch, a.k_new + at, (uint32_t)row_bytes_, bar);
+                    rdtc::bulk_load(v_to + lane * a.draft_pitch, a.v_new + at, (uint32_t)row_bytes_, bar);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    // no copy may be under way when the CTA ends: the last stages' have all landed
+    const uint32_t first = it > (uint32_t)a.stages ? it - (uint32_t)a.stages : 0;
+    for (uint32_t i = first; i < it; ++i)
+        rdattn::warp_wait(&sh.full[i % (uint32_t)a.stages], (i / (uint32_t)a.stages) & 1u, &sh.never_abort, kWaitBudget);
+}
+
+// The same by 128 threads with copies of 16, 8 or 4 bytes, for rows that TMA's rules leave out (an
+// odd number of kv heads).
+template <int D, int BITS>
+__device__ __forceinline__ void load_rowwise(const Args& a, Shared& sh, unsigned char* ring, const Division& d, int chunk)
+{
+    const int tid = threadIdx.x - 32 * kConsumers;
+    const int64_t row = (int64_t)a.Hkv * a.seg / a.heads;
+    Walk walk(a, d);
+    Piece p;
+    uint32_t it = 0;
+    bool alive = true;
+    while (walk.next(a, chunk, p)) {
         for (int j = p.j0; j < p.j1; ++j, ++it) {
             const int stage = (int)(it % (uint32_t)a.stages);
             // where the positions lie, before the wait
@@ -365,17 +438,8 @@ __device__ __forceinline__ void load(const Args& a, Shared& sh, unsigned char* r
                 const int pos0 = j * chunk;
                 rows = min(chunk, p.C - pos0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int pos = pos0 + 64 * k;
-                    if (64 * k < rows) {
-                        int page = a.table[(size_t)p.b * a.max_pages + pos / a.page_size];
-                        if (page < 0 || page >= a.num_pages) {
-                            if (tid == 0) rd_flag(a.status, RD_DEV_BAD_INDEX);
-                            page = 0;
-                        }
-                        base[k] = ((size_t)page * a.page_size + pos % a.page_size) * row + (size_t)p.hg * a.seg;
-                    }
-                }
+                for (int k = 0; k < 4; ++k)
+                    if (64 * k < rows) base[k] = (size_t)(row_at(a, p.b, pos0 + 64 * k, tid == 0) * row + (int64_t)p.hg * a.seg);
             }
             if (alive && it >= (uint32_t)a.stages)
                 alive = rdattn::warp_wait(&sh.empty[stage], ((it / (uint32_t)a.stages) & 1u) ^ 1u, &sh.abort, kWaitBudget);
@@ -386,7 +450,7 @@ __device__ __forceinline__ void load(const Args& a, Shared& sh, unsigned char* r
                 else load_rows<4>(a, k_to, v_to, base, rows, tid);
             } else {
                 const int node0 = (j - p.n_ctx) * kDraftTile;
-                const int nodes = min(kDraftTile, a.lens[p.b] - node0);
+                const int nodes = min(kDraftTile, p.len - node0);
                 const int copies = a.heads * D * 2 / 16;
                 for (int i = tid; i < nodes * copies; i += 32 * kLoaders) {
                     const int node = i / copies, part = i % copies;
@@ -400,10 +464,16 @@ __device__ __forceinline__ void load(const Args& a, Shared& sh, unsigned char* r
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // rows behind the last node, and those of skipped requests
+}
+
+// rows behind the last node, and those of skipped requests
+template <int D>
+__device__ __forceinline__ void clear_rows(const Args& a)
+{
+    const int tid = threadIdx.x - 32 * kConsumers;
     const int vecs = a.Hq * D / 8;
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const int from = shape_of(a, b, chunk).cost != 0 ? a.lens[b] : 0;
+        const int from = shape_of(a, b).len;
         uint4* o = reinterpret_cast<uint4*>(a.o) + (size_t)b * a.P * vecs;
         for (size_t v = (size_t)from * vecs + tid; v < (size_t)a.P * vecs; v += 32 * kLoaders) o[v] = make_uint4(0, 0, 0, 0);
     }
@@ -419,218 +489,258 @@ struct Place {
 template <int D, int BITS, int NT>
 struct Sums {                              // of 8 NT rows; this thread's columns D / 8 * g ..., rows 8 i + 2 t, + 1
     float o[D / 16][NT][4];
-    float m[2 * NT], l[2 * NT];            // references, sums of the weights
-    bool fresh;                            // some row has no finite reference yet
+    float r[2 * NT], l[2 * NT];            // references (0: none yet), sums of the weights
+    uint32_t none;                         // bit k: row k has none
+    bool fresh;                            // some row of the warp has none
 };
 
+// new references, kBelow under the rows' maxima: `top` is this thread's
 template <int D, int BITS, int NT>
 __device__ __forceinline__ void raise(Sums<D, BITS, NT>& s, const float (&top)[2 * NT])
 {
-    bool none = false;
+    uint32_t none = 0;
 #pragma unroll
     for (int k = 0; k < 2 * NT; ++k) {
         float v = top[k];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-        const float m = fmaxf(s.m[k], v - kBelow);
-        const float f = fast_exp2(s.m[k] - (m == -INFINITY ? 0.f : m));
-        s.m[k] = m;
+        v -= kBelow;
+        const bool had = !(s.none >> k & 1u);
+        if (v == -INFINITY && !had) {
+            none |= 1u << k;
+            continue;
+        }
+        const float r = had ? fmaxf(s.r[k], v) : v;
+        const float f = had ? fast_exp2(s.r[k] - r) : 0.f;       // (nothing summed yet)
+        s.r[k] = r;
         s.l[k] *= f;
-        none = none || m == -INFINITY;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             s.o[j][k / 2][k & 1] *= f;
             s.o[j][k / 2][2 + (k & 1)] *= f;
         }
     }
-    s.fresh = __any_sync(0xffffffffu, none);
+    s.none = none;
+    s.fresh = __any_sync(0xffffffffu, none != 0);
 }
 
-// one tile of 16 positions of the context; `valid` of them count
-template <int D, int BITS, int NT>
-__device__ __forceinline__ void context_tile(const Args& a, const Place& w, Sums<D, BITS, NT>& s, uint32_t k_at,
-                                             uint32_t v_at, uint32_t q_at, uint32_t f_at, int valid)
+// Byte `at` of the row of position `pos` (of this warp's tile) within a stage.
+template <int BITS>
+struct Rows {
+    uint32_t base;             // of the tile's first position
+    int pitch;
+    uint32_t first;            // byte of the head's row within 128 bytes (8 bits, swizzled)
+    bool swizzled;
+    __device__ __forceinline__ uint32_t operator()(int pos, int at) const
+    {
+        if constexpr (BITS == 4) return base + (uint32_t)(pos * pitch + at);
+        const uint32_t x = first + (uint32_t)at;
+        return base + (uint32_t)(pos * pitch) + (swizzled ? x ^ (uint32_t)((pos & 7) << 4) : x);
+    }
+};
+
+// MT tiles of 16 positions of the context; `valid` of them count
+template <int D, int BITS, int NT, int MT>
+__device__ __forceinline__ void context_tiles(const Args& a, const Place& w, Sums<D, BITS, NT>& s, const Rows<BITS>& k_row,
+                                              const Rows<BITS>& v_row, uint32_t q_at, uint32_t f_at, int valid)
 {
     using namespace rdquant;
     constexpr int KB = D / 64;             // blocks of a row of K that a thread widens
-    float x[NT][4];
+    float x[MT][NT][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[i][c] = 0.f;
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[m][i][c] = 0.f;
     const int pos = position_of(w.g >> 1, w.g & 1);
-    const uint32_t row0 = k_at + (uint32_t)(pos * a.pitch), row1 = row0 + (uint32_t)(8 * a.pitch);
     // ---- S^T
-    uint32_t sc0[KB], sc1[KB];
+    uint32_t sc[MT][2][KB];
     if constexpr (BITS == 4) {
-        if constexpr (D == 128) {
-            const uint32_t sel = (uint32_t)w.t * 0x1111u + 0x4400u;
-            const uint2 b0 = lds64(row0 + D / 2), b1 = lds64(row1 + D / 2);
-            e4m3x4(__byte_perm(b0.x, b0.y, sel), sc0[0], sc0[KB - 1]);
-            e4m3x4(__byte_perm(b1.x, b1.y, sel), sc1[0], sc1[KB - 1]);
-        } else {
-            const uint32_t sel = (uint32_t)w.t * 0x1111u;
-            uint32_t drop;
-            e4m3x4(__byte_perm(lds32(row0 + D / 2), 0u, sel), sc0[0], drop);
-            e4m3x4(__byte_perm(lds32(row1 + D / 2), 0u, sel), sc1[0], drop);
-        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t at = k_row(16 * m + pos + 8 * e, D / 2);
+                if constexpr (D == 128) {
+                    const uint2 b = lds64(at);
+                    e4m3x4(__byte_perm(b.x, b.y, (uint32_t)w.t * 0x1111u + 0x4400u), sc[m][e][0], sc[m][e][KB - 1]);
+                } else {
+                    uint32_t drop;
+                    e4m3x4(__byte_perm(lds32(at), 0u, (uint32_t)w.t * 0x1111u), sc[m][e][0], drop);
+                }
+            }
     }
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-        uint32_t w0[4], w1[4];             // the thread's 16 codes of each of its two positions
-        if constexpr (BITS == 4) {
-            const uint32_t off = (uint32_t)(8 * (w.t + 4 * kb));
-            if constexpr (D == 128) {
-                const uint2 u0 = lds64(row0 + off), u1 = lds64(row1 + off);
-                w0[0] = u0.x, w0[1] = u0.y, w1[0] = u1.x, w1[1] = u1.y;
-            } else {
-                w0[0] = lds32(row0 + off), w0[1] = lds32(row0 + off + 4);
-                w1[0] = lds32(row1 + off), w1[1] = lds32(row1 + off + 4);
+        uint32_t c[MT][2][BITS == 4 ? 2 : 4];          // the thread's 16 codes of each of its positions
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t at = k_row(16 * m + pos + 8 * e, (BITS == 4 ? 8 : 16) * (w.t + 4 * kb));
+                if constexpr (BITS == 8) {
+                    const uint4 u = lds128(at);
+                    c[m][e][0] = u.x, c[m][e][1] = u.y, c[m][e][BITS == 8 ? 2 : 0] = u.z, c[m][e][BITS == 8 ? 3 : 0] = u.w;
+                } else if constexpr (D == 128) {
+                    const uint2 u = lds64(at);
+                    c[m][e][0] = u.x, c[m][e][1] = u.y;
+                } else {
+                    c[m][e][0] = lds32(at), c[m][e][1] = lds32(at + 4);
+                }
             }
-        } else {
-            const uint4 u0 = lds128(row0 + (uint32_t)(16 * (w.t + 4 * kb))), u1 = lds128(row1 + (uint32_t)(16 * (w.t + 4 * kb)));
-            w0[0] = u0.x, w0[1] = u0.y, w0[2] = u0.z, w0[3] = u0.w;
-            w1[0] = u1.x, w1[1] = u1.y, w1[2] = u1.z, w1[3] = u1.w;
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {      // two steps of 16 at a time
-            uint32_t f[2][4];
-            if constexpr (BITS == 4) {
-                uint32_t c0[4], c1[4];
-                e2m1x8(w0[h], c0);
-                e2m1x8(w1[h], c1);
+            uint32_t f[MT][2][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    f[e][0] = mul_f16x2(c0[2 * e], sc0[kb]);
-                    f[e][1] = mul_f16x2(c1[2 * e], sc1[kb]);
-                    f[e][2] = mul_f16x2(c0[2 * e + 1], sc0[kb]);
-                    f[e][3] = mul_f16x2(c1[2 * e + 1], sc1[kb]);
+                    if constexpr (BITS == 4) {
+                        uint32_t v[4];
+                        e2m1x8(c[m][e][h], v);
+                        f[m][0][e] = mul_f16x2(v[0], sc[m][e][kb]);
+                        f[m][0][2 + e] = mul_f16x2(v[1], sc[m][e][kb]);
+                        f[m][1][e] = mul_f16x2(v[2], sc[m][e][kb]);
+                        f[m][1][2 + e] = mul_f16x2(v[3], sc[m][e][kb]);
+                    } else {
+                        e4m3x4(c[m][e][2 * h], f[m][0][e], f[m][0][2 + e]);
+                        e4m3x4(c[m][e][2 * h + 1], f[m][1][e], f[m][1][2 + e]);
+                    }
                 }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    e4m3x4(w0[2 * h + e], f[e][0], f[e][2]);
-                    e4m3x4(w1[2 * h + e], f[e][1], f[e][3]);
-                }
-            }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const uint4 qb = lds128(q_at + (uint32_t)(i * 8 * (2 * D + 16) + 128 * kb + 16 * h));
-                mma_f16(x[i], f[0], qb.x, qb.y);
-                mma_f16(x[i], f[1], qb.z, qb.w);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma_f16(x[m][i], f[m][0], qb.x, qb.y);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma_f16(x[m][i], f[m][1], qb.z, qb.w);
             }
         }
     }
     // ---- softmax of the rows over these positions
-    if (valid < 16) {
+    if (valid < 16 * MT) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if (pos >= valid) x[i][0] = x[i][1] = -INFINITY;
-            if (pos + 8 >= valid) x[i][2] = x[i][3] = -INFINITY;
-        }
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if (16 * m + pos >= valid) x[m][i][0] = x[m][i][1] = -INFINITY;
+                if (16 * m + pos + 8 >= valid) x[m][i][2] = x[m][i][3] = -INFINITY;
+            }
     }
-    bool over = s.fresh;
+    // exponents over the references; one above kBelow + kLag, or a row without a reference, needs new ones
+    float most = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const uint2 fb = lds64(f_at + (uint32_t)(32 * i));
-        const float f0 = __uint_as_float(fb.x), f1 = __uint_as_float(fb.y);
-        x[i][0] *= f0, x[i][1] *= f1, x[i][2] *= f0, x[i][3] *= f1;
-        over = over || fmaxf(x[i][0], x[i][2]) > s.m[2 * i] + (kBelow + kLag) || fmaxf(x[i][1], x[i][3]) > s.m[2 * i + 1] + (kBelow + kLag);
-    }
-    if (__any_sync(0xffffffffu, over)) {
-        float top[2 * NT];
+        const float f[2] = {__uint_as_float(fb.x), __uint_as_float(fb.y)};
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            top[2 * i] = fmaxf(x[i][0], x[i][2]);
-            top[2 * i + 1] = fmaxf(x[i][1], x[i][3]);
-        }
-        raise<D, BITS, NT>(s, top);
-    }
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const float m0 = s.fresh && s.m[2 * i] == -INFINITY ? 0.f : s.m[2 * i];
-        const float m1 = s.fresh && s.m[2 * i + 1] == -INFINITY ? 0.f : s.m[2 * i + 1];
-        const float p0 = fast_exp2(x[i][0] - m0), p1 = fast_exp2(x[i][1] - m1);
-        const float p2 = fast_exp2(x[i][2] - m0), p3 = fast_exp2(x[i][3] - m1);
-        s.l[2 * i] += p0 + p2;
-        s.l[2 * i + 1] += p1 + p3;
-        pb[i][0] = transpose8x8(pack_f16(p0, p1));       // 2^-11 of each weight
-        pb[i][1] = transpose8x8(pack_f16(p2, p3));
-    }
-    // ---- O^T
-    const int v0 = position_of(w.t, 0), v1 = position_of(w.t, 1);
-    const uint32_t r0 = v_at + (uint32_t)(v0 * a.pitch), r1 = v_at + (uint32_t)(v1 * a.pitch);
-    const uint32_t r2 = r0 + (uint32_t)(8 * a.pitch), r3 = r1 + (uint32_t)(8 * a.pitch);
-    if constexpr (BITS == 4) {
-        constexpr int NW = D / 64;         // words of the thread's columns
-        uint32_t u[4][NW];
-        const uint32_t off = (uint32_t)(D / 16 * w.g);
-        if constexpr (D == 128) {
-            const uint2 y0 = lds64(r0 + off), y1 = lds64(r1 + off), y2 = lds64(r2 + off), y3 = lds64(r3 + off);
-            u[0][0] = y0.x, u[1][0] = y1.x, u[2][0] = y2.x, u[3][0] = y3.x;
-            u[0][NW - 1] = y0.y, u[1][NW - 1] = y1.y, u[2][NW - 1] = y2.y, u[3][NW - 1] = y3.y;
-        } else {
-            u[0][0] = lds32(r0 + off), u[1][0] = lds32(r1 + off), u[2][0] = lds32(r2 + off), u[3][0] = lds32(r3 + off);
-        }
-        const uint32_t so = (uint32_t)(D / 2 + (D == 128 ? w.g : w.g >> 1));
-        uint32_t b0 = lds8(r0 + so), b1 = lds8(r1 + so), b2 = lds8(r2 + so), b3 = lds8(r3 + so);
-        if (valid < 16) {                  // what lies behind the end may be anything: its scale is 0
-            if (v0 >= valid) b0 = 0;
-            if (v1 >= valid) b1 = 0;
-            if (v0 + 8 >= valid) b2 = 0;
-            if (v1 + 8 >= valid) b3 = 0;
-        }
-        uint32_t s01, s23;
-        e4m3x4(b0 | b1 << 8 | b2 << 16 | b3 << 24, s01, s23);
-#pragma unroll
-        for (int q = 0; q < NW; ++q) {
-            // the codes of one column at two positions, side by side
-            constexpr uint32_t kLow = 0x0f0f0f0fu;
-            uint32_t e0[4], o0[4], e1[4], o1[4];
-            e2m1x8((u[0][q] & kLow) | ((u[1][q] << 4) & ~kLow), e0);
-            e2m1x8(((u[0][q] >> 4) & kLow) | (u[1][q] & ~kLow), o0);
-            e2m1x8((u[2][q] & kLow) | ((u[3][q] << 4) & ~kLow), e1);
-            e2m1x8(((u[2][q] >> 4) & kLow) | (u[3][q] & ~kLow), o1);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint32_t f[4] = {mul_f16x2(e0[c], s01), mul_f16x2(o0[c], s01), mul_f16x2(e1[c], s23),
-                                       mul_f16x2(o1[c], s23)};
-#pragma unroll
-                for (int i = 0; i < NT; ++i) mma_f16(s.o[4 * q + c][i], f, pb[i][0], pb[i][1]);
+                x[m][i][c] = fmaf(x[m][i][c], f[c & 1], -s.r[2 * i + (c & 1)]);
+                most = fmaxf(most, x[m][i][c]);
             }
+    }
+    if (__any_sync(0xffffffffu, most > kBelow + kLag) || s.fresh) {
+        float was[2 * NT], top[2 * NT];
+#pragma unroll
+        for (int k = 0; k < 2 * NT; ++k) {
+            was[k] = s.r[k];
+            top[k] = -INFINITY;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) top[k] = fmaxf(top[k], fmaxf(x[m][k / 2][k & 1], x[m][k / 2][2 + (k & 1)]));
+            top[k] += was[k];
         }
-    } else {
-        constexpr int NW = D / 32;
-        uint32_t u[4][NW];
-        const uint32_t off = (uint32_t)(D / 8 * w.g);
-        const uint32_t r[4] = {r0, r1, r2, r3};
+        raise<D, BITS, NT>(s, top);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (D == 128) {
-                const uint4 y = lds128(r[e] + off);
-                u[e][0] = y.x, u[e][1] = y.y, u[e][NW - 2] = y.z, u[e][NW - 1] = y.w;
-            } else {
-                const uint2 y = lds64(r[e] + off);
-                u[e][0] = y.x, u[e][1] = y.y;
-            }
-            const int at = (e & 1 ? v1 : v0) + 4 * (e & 2);
-            if (at >= valid) {
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int q = 0; q < NW; ++q) u[e][q] = 0;
-            }
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[m][i][c] += was[2 * i + (c & 1)] - s.r[2 * i + (c & 1)];
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            float p[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[c] = fast_exp2(x[m][i][c]);
+            s.l[2 * i] += p[0] + p[2];
+            s.l[2 * i + 1] += p[1] + p[3];
+            pb[i][0] = transpose8x8(pack_f16(p[0], p[1]));       // 2^-11 of each weight
+            pb[i][1] = transpose8x8(pack_f16(p[2], p[3]));
         }
+        // ---- O^T
+        const int first = 16 * m, v[4] = {first + position_of(w.t, 0), first + position_of(w.t, 1),
+                                          first + position_of(w.t, 0) + 8, first + position_of(w.t, 1) + 8};
+        if constexpr (BITS == 4) {
+            constexpr int NW = D / 64;     // words of the thread's columns
+            uint32_t u[4][NW], b[4];
 #pragma unroll
-        for (int q = 0; q < NW; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
-                uint32_t f[4];
-                e4m3x4(__byte_perm(u[0][q], u[1][q], sel), f[0], f[1]);
-                e4m3x4(__byte_perm(u[2][q], u[3][q], sel), f[2], f[3]);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) mma_f16(s.o[2 * q + h][i], f, pb[i][0], pb[i][1]);
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (D == 128) {
+                    const uint2 y = lds64(v_row(v[e], 8 * w.g));
+                    u[e][0] = y.x, u[e][NW - 1] = y.y;
+                    b[e] = lds8(v_row(v[e], D / 2 + w.g));
+                } else {
+                    u[e][0] = lds32(v_row(v[e], 4 * w.g));
+                    b[e] = lds8(v_row(v[e], D / 2 + (w.g >> 1)));
+                }
+                // what lies behind the end may be anything: its scale is 0
+                if (valid < 16 * MT && v[e] >= valid) b[e] = 0;
             }
+            uint32_t s01, s23;
+            e4m3x4(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, s01, s23);
+#pragma unroll
+            for (int q = 0; q < NW; ++q) {
+                // the codes of one column at two positions, side by side
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t e0[4], o0[4], e1[4], o1[4];
+                e2m1x8((u[0][q] & kLow) | ((u[1][q] << 4) & ~kLow), e0);
+                e2m1x8(((u[0][q] >> 4) & kLow) | (u[1][q] & ~kLow), o0);
+                e2m1x8((u[2][q] & kLow) | ((u[3][q] << 4) & ~kLow), e1);
+                e2m1x8(((u[2][q] >> 4) & kLow) | (u[3][q] & ~kLow), o1);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t f[4] = {mul_f16x2(e0[c], s01), mul_f16x2(o0[c], s01), mul_f16x2(e1[c], s23),
+                                           mul_f16x2(o1[c], s23)};
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) mma_f16(s.o[4 * q + c][i], f, pb[i][0], pb[i][1]);
+                }
+            }
+        } else {
+            constexpr int NW = D / 32;
+            uint32_t u[4][NW];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t at = v_row(v[e], D / 8 * w.g);
+                if constexpr (D == 128) {
+                    const uint4 y = lds128(at);
+                    u[e][0] = y.x, u[e][1] = y.y, u[e][NW - 2] = y.z, u[e][NW - 1] = y.w;
+                } else {
+                    const uint2 y = lds64(at);
+                    u[e][0] = y.x, u[e][1] = y.y;
+                }
+                if (valid < 16 * MT && v[e] >= valid) {
+#pragma unroll
+                    for (int q = 0; q < NW; ++q) u[e][q] = 0;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NW; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
+                    uint32_t f[4];
+                    e4m3x4(__byte_perm(u[0][q], u[1][q], sel), f[0], f[1]);
+                    e4m3x4(__byte_perm(u[2][q], u[3][q], sel), f[2], f[3]);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) mma_f16(s.o[2 * q + h][i], f, pb[i][0], pb[i][1]);
+                }
+        }
     }
 }
 
@@ -694,10 +804,8 @@ __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const 
     uint32_t pb[NT][2];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const float m0 = s.m[2 * i] == -INFINITY ? 0.f : s.m[2 * i];
-        const float m1 = s.m[2 * i + 1] == -INFINITY ? 0.f : s.m[2 * i + 1];
-        const float p0 = fast_exp2(x[i][0] - m0), p1 = fast_exp2(x[i][1] - m1);
-        const float p2 = fast_exp2(x[i][2] - m0), p3 = fast_exp2(x[i][3] - m1);
+        const float p0 = fast_exp2(x[i][0] - s.r[2 * i]), p1 = fast_exp2(x[i][1] - s.r[2 * i + 1]);
+        const float p2 = fast_exp2(x[i][2] - s.r[2 * i]), p3 = fast_exp2(x[i][3] - s.r[2 * i + 1]);
         s.l[2 * i] += p0 + p2;
         s.l[2 * i + 1] += p1 + p3;
         pb[i][0] = transpose8x8(pack_bf16(p0, p1));
@@ -776,7 +884,8 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     const int chunk = 16 * TILES * w.splits;
     Sums<D, BITS, NT> s;
 #pragma unroll
-    for (int k = 0; k < 2 * NT; ++k) s.m[k] = -INFINITY, s.l[k] = 0.f;
+    for (int k = 0; k < 2 * NT; ++k) s.r[k] = s.l[k] = 0.f;
+    s.none = (1u << 2 * NT) - 1u;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -812,19 +921,35 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
         const uint32_t k_at = ring + (uint32_t)(stage * 2 * a.half), v_at = k_at + (uint32_t)a.half;
         if (j < p.n_ctx) {
             const int first = w.split * 16 * TILES, valid = p.C - j * chunk - first;
-            const uint32_t off = (uint32_t)(first * a.pitch + w.head * rdquant::row_bytes(D, BITS));
+            Rows<BITS> k_row, v_row;
+            k_row.swizzled = v_row.swizzled = a.tiled;
+            k_row.pitch = v_row.pitch = a.pitch;
+            uint32_t off = (uint32_t)(first * a.pitch);
+            k_row.first = v_row.first = 0;
+            if (BITS == 8 && a.tiled) {    // boxes of 128 bytes of the heads' rows
+                k_row.first = v_row.first = (uint32_t)(w.head * D % 128);
+                off += (uint32_t)(w.head * D / 128 * chunk * 128);
+            } else {
+                off += (uint32_t)(w.head * rdquant::row_bytes(D, BITS));
+            }
+            k_row.base = k_at + off;
+            v_row.base = v_at + off;
+            // (two tiles at a time where the registers last: more products in flight)
+            constexpr int MT = TILES == 2 && NT <= kPairTiles ? 2 : 1;
 #pragma unroll 1
-            for (int x = 0; x < TILES; ++x)
-                if (valid > 16 * x)
-                    context_tile<D, BITS, NT>(a, w, s, k_at + off + (uint32_t)(16 * x * a.pitch),
-                                              v_at + off + (uint32_t)(16 * x * a.pitch), q_at, f_at, min(16, valid - 16 * x));
+            for (int x = 0; x < TILES; x += MT)
+                if (valid > 16 * x) {
+                    context_tiles<D, BITS, NT, MT>(a, w, s, k_row, v_row, q_at, f_at, min(16 * MT, valid - 16 * x));
+                    k_row.base += (uint32_t)(16 * a.pitch);
+                    v_row.base += (uint32_t)(16 * a.pitch);
+                }
         } else {
             const int tile = j - p.n_ctx;
             if (!scaled) scale_values();
             if (tile % w.splits == w.split) {
                 const uint32_t off = (uint32_t)(w.head * D * 2);
                 draft_tile<D, BITS, NT>(a, w, p, s, k_at + off, v_at + off, q_at, f_at, tile * kDraftTile,
-                                        min(kDraftTile, a.lens[p.b] - tile * kDraftTile));
+                                        min(kDraftTile, p.len - tile * kDraftTile));
             }
         }
         __syncwarp();
@@ -846,7 +971,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
             if (gives) {
                 if (i0 == 0) {
 #pragma unroll
-                    for (int k = 0; k < 2 * NT; ++k) buf.join_ml[(slot * 8 + k) * 32 + w.lane] = make_float2(s.m[k], s.l[k]);
+                    for (int k = 0; k < 2 * NT; ++k) buf.join_ml[(slot * 8 + k) * 32 + w.lane] = make_float2(s.none >> k & 1u ? -INFINITY : s.r[k], s.l[k]);
                 }
 #pragma unroll
                 for (int i = i0; i < i0 + 2 && i < NT; ++i)
@@ -861,10 +986,12 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
 #pragma unroll
                     for (int k = 0; k < 2 * NT; ++k) {
                         const float2 ml = buf.join_ml[(slot * 8 + k) * 32 + w.lane];
-                        const float m = fmaxf(s.m[k], ml.x), mu = m == -INFINITY ? 0.f : m;
-                        const float f = fast_exp2(s.m[k] - mu);
+                        const float mine = s.none >> k & 1u ? -INFINITY : s.r[k];
+                        const float m = fmaxf(mine, ml.x), mu = m == -INFINITY ? 0.f : m;
+                        const float f = fast_exp2(mine - mu);
                         fo[k] = fast_exp2(ml.x - mu);
-                        s.m[k] = m;
+                        s.r[k] = mu;
+                        if (m != -INFINITY) s.none &= ~(1u << k);
                         s.l[k] = s.l[k] * f + ml.y * fo[k];
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
@@ -890,7 +1017,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     if (w.split != 0) return;
 
     // ---- rows, or partials of a unit that the ranges cut
-    const bool whole = p.j0 == 0 && p.j1 == p.n;
+    const bool whole = p.j0 == 0 && p.j1 == p.n();
     const int h = p.hg * a.heads + w.head;
     const size_t slot = ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * a.heads + w.head;
 #pragma unroll
@@ -914,7 +1041,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
                     o[j] = make_float4(s.o[2 * j][i][e], s.o[2 * j][i][2 + e], s.o[2 * j + 1][i][e], s.o[2 * j + 1][i][2 + e]);
-                if (w.g == 0) a.part_ml[slot * kRows + r] = make_float2(s.m[2 * i + e], s.l[2 * i + e]);
+                if (w.g == 0) a.part_ml[slot * kRows + r] = make_float2(s.none >> (2 * i + e) & 1u ? -INFINITY : s.r[2 * i + e], s.l[2 * i + e]);
             }
         }
 }
@@ -922,7 +1049,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
 template <int D, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __grid_constant__ Args a)
 {
-    extern __shared__ __align__(128) unsigned char dyn[];
+    extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ Shared sh;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5;
@@ -935,18 +1062,20 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
     buf.join_ml = reinterpret_cast<float2*>(buf.join + 4 * 2 * (D / 16) * 32);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMostStages; ++i) {
-            rdtc::mbar_init(&sh.full[i], 32 * kLoaders);
+            rdtc::mbar_init(&sh.full[i], a.tiled ? 1 : 32 * kLoaders);
             rdtc::mbar_init(&sh.empty[i], kConsumers);
         }
         rdtc::mbar_init(&sh.never, 1);
         rdtc::mbar_fence_init();
-        sh.abort = 0;
+        sh.abort = sh.never_abort = 0;
     }
     const Division d = divide(a, sh, chunk);               // (its barriers order the set-up too)
     __syncthreads();
     if (warp >= kConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-        load<D, BITS>(a, sh, buf.ring, d, chunk);
+        if (!a.tiled) load_rowwise<D, BITS>(a, sh, buf.ring, d, chunk);
+        else if (warp == kConsumers) load_tiled<D, BITS>(a, sh, buf.ring, d, chunk);
+        clear_rows<D>(a);
         return;
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
@@ -967,18 +1096,21 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
         }
     }
     if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    Walk walk(a, d, chunk);
+    Walk walk(a, d);
     Piece p;
     uint32_t it = 0;
-    while (walk.next(p)) {
-        if (threadIdx.x == 0 && p.j0 == 0 && p.j1 < p.n) {
+    while (walk.next(a, chunk, p)) {
+        if (threadIdx.x == 0 && p.j0 == 0 && p.j1 < p.n()) {
             // the CTA that has the unit's last chunk
-            const uint64_t last = walk.S + (uint64_t)p.unit * unit_cost(walk.s) + kUnitCost + (uint64_t)(p.n - 1) * walk.s.chunk_cost;
+            const Shape s = shape_of(a, p.b);
+            const uint64_t last = walk.S + (uint64_t)p.unit * s.unit_cost(a, chunk) + kUnitCost +
+                                  (uint64_t)(p.n() - 1) * s.chunk_cost(a);
             a.desc[blockIdx.x] = make_int4(p.b, p.unit, (int)d.of(last), 0);
         }
-        if (p.tiles == 1) piece<D, BITS, 1>(a, sh, buf, w, p, d, it, alive);
-        else if (p.tiles == 2) piece<D, BITS, 2>(a, sh, buf, w, p, d, it, alive);
-        else if (p.tiles == 3) piece<D, BITS, 3>(a, sh, buf, w, p, d, it, alive);
+        const int tiles = (p.rows + 7) / 8;
+        if (tiles == 1) piece<D, BITS, 1>(a, sh, buf, w, p, d, it, alive);
+        else if (tiles == 2) piece<D, BITS, 2>(a, sh, buf, w, p, d, it, alive);
+        else if (tiles == 3) piece<D, BITS, 3>(a, sh, buf, w, p, d, it, alive);
         else piece<D, BITS, 4>(a, sh, buf, w, p, d, it, alive);
     }
 }
@@ -993,10 +1125,10 @@ __global__ void __launch_bounds__(256) quant_merge_kernel(const Args a)
     if (unit.x < 0 || unit.x >= a.B || last <= first || last >= (int)gridDim.x) return;
     const int len = a.lens[unit.x];
     if (len <= 0 || len > a.P) return;
-    const int rows_all = len * a.G, groups = (rows_all + kRows - 1) / kRows;
-    const int per = ((rows_all + groups - 1) / groups + 7) & ~7;
-    const int hg = unit.y / groups, r0 = unit.y % groups * per;
-    const int rows = min(per, rows_all - r0), h = hg * a.heads + blockIdx.y;
+    Shape s;
+    s.len = len;
+    const int groups = s.groups(a), hg = unit.y / groups, r0 = unit.y % groups * s.per(a);
+    const int rows = min(s.per(a), s.rows(a) - r0), h = hg * a.heads + blockIdx.y;
     for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
         const int r = i / (D / 4), c = i % (D / 4);
         auto at = [&](int cta) { return (((size_t)2 * cta + (cta == first ? 1 : 0)) * a.heads + blockIdx.y) * kRows + r; };
@@ -1034,6 +1166,20 @@ int pitch_of(int seg, int bits)
     return p;
 }
 
+// the pool as [rows][row bytes]; boxes of `box` rows x `width` bytes
+bool make_map(CUtensorMap* map, const void* pool, int64_t rows, int row_bytes, int width, int box, bool swizzled)
+{
+    auto fn = rdattn::encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)row_bytes / 4, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    cuuint32_t boxes[2] = {(cuuint32_t)width / 4, (cuuint32_t)box};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(pool), dims, strides, boxes, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t desc_bytes(int grid) { return ((size_t)grid * sizeof(int4) + 127) & ~size_t(127); }
 
 template <int D, int BITS>
@@ -1046,9 +1192,19 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     a.gran = a.seg % 16 == 0 && stride % 16 == 0 ? 16 : a.seg % 8 == 0 && stride % 8 == 0 ? 8 : 4;
     a.per_row = a.seg / a.gran;
     a.per_row_magic = (uint32_t)((0x100000000ULL + a.per_row - 1) / a.per_row);
+    // TMA: rows of whole 16 bytes, the unit's part among them, and coordinates of 31 bits
+    const int64_t rows_all = (int64_t)a.num_pages * a.page_size;
+    a.tiled = a.gran == 16 && rows_all > 0 && rows_all <= 0x7fffffff && (BITS == 4 || a.seg % 128 == 0);
+    if (a.tiled) {
+        const int box = chunk < 64 ? chunk : 64, width = BITS == 4 ? a.seg : 128;
+        if (!make_map(&a.k_map, a.k_pool, rows_all, stride, width, box, BITS == 8) ||
+            !make_map(&a.v_map, a.v_pool, rows_all, stride, width, box, BITS == 8))
+            return cudaErrorUnknown;
+        a.pitch = width;
+    }
     a.draft_pitch = a.heads * D * 2 + 16;
-    const int rows = chunk * a.pitch, drafts = kDraftTile * a.draft_pitch;
-    a.half = ((rows > drafts ? rows : drafts) + 127) / 128 * 128;
+    const int rows = a.tiled ? chunk * a.seg : chunk * a.pitch, drafts = kDraftTile * a.draft_pitch;
+    a.half = ((rows > drafts ? rows : drafts) + 1023) / 1024 * 1024;       // (swizzled tiles repeat every 1024 bytes)
     const int fixed = a.heads * kRows * ((D + 8) * 2 + 4) + 4 * 2 * (D / 16) * 32 * 16 + 4 * 8 * 32 * 8;
     constexpr int kSmem = 227 * 1024 - 1024;               // what the static part leaves
     a.stages = (kSmem - fixed) / (2 * a.half);
