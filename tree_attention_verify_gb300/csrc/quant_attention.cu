@@ -6,7 +6,7 @@
 // over the context (all visible) and the packed drafts (ancestors and the node itself), in one
 // pass with a running maximum and sum.  What it must read is half to a quarter of the 16-bit
 // cache, so widening the codes, not the stream, is the nearest bound: per position and kv
-// head 2 D codes become 16-bit floats.  Each code is widened once per 32 rows, in the registers
+// head 2 D codes become 16-bit floats.  Each code is widened once per unit's rows, in the registers
 // that feed the matrix instructions, with no way through shared memory:
 //
 //   S^T[16 positions x 8 rows] += K[16 x 16] Q^T[16 x 8]      A = K, straight from the codes
@@ -17,253 +17,43 @@
 // so that a thread owns 16 consecutive ones: its loads are whole blocks and its outputs whole
 // 16-byte words.  Rows are the products' short side: 8 at a time, so that five rows cost a
 // quarter of what 32 do.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "attn_common.cuh"
-#include "quant_format.cuh"
-#include "rd_internal.cuh"
+#include "quant_attention.cuh"
 
 namespace {
 
-using rdattn::fast_exp2;
-using rdattn::pack_bf16;
-using rdtc::smem_addr;
+using namespace rdquant;
 
-constexpr int kConsumers = 8;              // warps that compute
-constexpr int kLoaders = 4;                // warps that load
-constexpr int kThreads = 32 * (kConsumers + kLoaders);
+constexpr int kWarps = 8;                  // that compute
+constexpr int kLoaders = 4;                // that load
+constexpr int kThreads = 32 * (kWarps + kLoaders);
 constexpr int kLaunchRegs = 168;           // 384 x 168 = 64,512 registers, dealt anew:
 constexpr int kComputeRegs = 232, kLoadRegs = 40;
-static_assert(32 * kConsumers * kComputeRegs + 32 * kLoaders * kLoadRegs <= kThreads * kLaunchRegs, "registers");
+static_assert(32 * kWarps * kComputeRegs + 32 * kLoaders * kLoadRegs <= kThreads * kLaunchRegs, "registers");
 constexpr int kRows = 32;                  // rows of a unit at most
+// tiles of 16 positions of a warp's share of a chunk (the ring holds few chunks of 8-bit rows of 128)
+constexpr int tiles_of(int D, int bits) { return D == 128 && bits == 8 ? 1 : 2; }
 constexpr int kDraftTile = 16;             // packed drafts of a chunk
-constexpr int kPairTiles = 2;              // up to 16 rows, two tiles of positions at a time
 constexpr int kMostStages = 8;
-constexpr long long kWaitBudget = 4000000000LL;     // cycles, about two seconds
-constexpr float kLog2e = 1.4426950408889634f;
-// A row's weights are powers of two above a reference that lies kBelow under the row's maximum,
-// or up to kLag more: a weight P reaches 2^15 (a 16-bit float ends at 2^16), O is
-// rescaled only when the reference lags more, and weights down to 2^-21 of the largest
-// keep all 11 bits, those below an absolute 2^-32 of it.
-constexpr float kBelow = 7.f, kLag = 8.f;
-
-// positions of a warp's share of a chunk, in tiles of 16
-template <int BITS>
-__host__ __device__ constexpr int tiles_of() { return BITS == 4 ? 2 : 1; }
-
-struct Args {
-    const __nv_bfloat16 *q, *k_new, *v_new;
-    const unsigned char *k_pool, *v_pool;
-    const int32_t *table, *ctx_lens, *lens;
-    const uint32_t* mask;
-    __nv_bfloat16* o;
-    float* part;               // [2 grid slots][heads][kRows][D]
-    float2* part_ml;           // [2 grid slots][heads][kRows] maximum (log2 units), sum
-    int4* desc;                // [grid] the unit that a CTA begins and does not end
-    int32_t* status;
-    int B, P, Hq, Hkv, G, mask_words, num_pages, page_size, max_pages, max_ctx;
-    float scale_log2, k_scale, v_scale;
-    long long stall;
-    int heads;                 // kv heads of a unit: 4, 2 or 1
-    int seg, pitch, gran, per_row;     // bytes of a position's rows, apart in shared memory, a copy; copies
-    uint32_t per_row_magic;
-    int draft_pitch, half, stages;     // bytes of a stage's K (and of its V)
-    bool tiled;                // the pools' rows come as TMA boxes
-    CUtensorMap k_map, v_map;
-};
-
-// ------------------------------------------------------------------ the division of the work
-// A unit is (request, group of `heads` kv heads, group of up to 32 rows).  Its chunks
-// (context, then tiles of drafts) stand in one sequence with all other units', weighted by
-// what they cost, and the CTAs take equal ranges of it.
-struct Shape {
-    int len, C;                // nodes (0: the request is skipped or has none), context
-    __device__ __forceinline__ int rows(const Args& a) const { return len * a.G; }
-    // row groups, and rows of a group (a multiple of 8)
-    __device__ __forceinline__ int groups(const Args& a) const { return (rows(a) + kRows - 1) / kRows; }
-    __device__ __forceinline__ int per(const Args& a) const { return ((rows(a) + groups(a) - 1) / groups(a) + 7) & ~7; }
-    // chunks of the context, and all
-    __device__ __forceinline__ int n_ctx(int chunk) const { return (int)(((uint32_t)C + (uint32_t)chunk - 1u) / (uint32_t)chunk); }
-    __device__ __forceinline__ int n(int chunk) const { return n_ctx(chunk) + (len + kDraftTile - 1) / kDraftTile; }
-    __device__ __forceinline__ uint32_t chunk_cost(const Args& a) const;
-    __device__ __forceinline__ uint32_t unit_cost(const Args& a, int chunk) const;
-    __device__ __forceinline__ uint64_t cost(const Args& a, int chunk) const
-    {
-        return len == 0 ? 0 : (uint64_t)unit_cost(a, chunk) * (uint32_t)(groups(a) * (a.Hkv / a.heads));
-    }
-};
-
-// Widening a chunk costs the same for any number of rows, its products go with them (measured
-// beside the kernel); a unit's start and end take as long as a few chunks.  (A unit of 2^31
-// positions in chunks of 32 costs less than 2^30.)
-__host__ __device__ constexpr uint32_t cost_of_tiles(int tiles) { return 3u + 2u * (uint32_t)tiles; }
-constexpr uint32_t kUnitCost = 24;
-constexpr uint32_t kLeastCost = 24;        // of a CTA's range: at least two chunks
-__device__ __forceinline__ uint32_t Shape::chunk_cost(const Args& a) const { return cost_of_tiles(per(a) / 8); }
-__device__ __forceinline__ uint32_t Shape::unit_cost(const Args& a, int chunk) const
-{
-    return kUnitCost + (uint32_t)n(chunk) * chunk_cost(a);
-}
-
-__device__ __forceinline__ Shape shape_of(const Args& a, int b)
-{
-    Shape s;
-    s.len = a.lens[b];
-    s.C = 0;
-    if (s.len <= 0 || s.len > a.P) {
-        s.len = 0;
-        return s;
-    }
-    s.C = a.ctx_lens[b];
-    if (s.C < 0 || s.C > a.max_ctx) s.len = 0;
-    return s;
-}
-
-struct Division {
-    uint64_t W;                // cost of everything
-    uint32_t n;                // CTAs that work
-    int b;                     // the request in which this CTA's range begins
-    uint64_t S;                // cost of the requests before it
-    __device__ __forceinline__ uint64_t begin(uint32_t c) const
-    {
-        // floor(c W / n) without leaving 64 bits
-        return (W / n) * c + (W % n) * c / n;
-    }
-    __device__ __forceinline__ uint32_t of(uint64_t x) const      // the CTA whose range holds x
-    {
-        uint32_t c = (uint32_t)min((uint64_t)(n - 1), x / max((uint64_t)1, W / n));
-        while (c > 0 && begin(c) > x) --c;
-        while (c + 1 < n && begin(c + 1) <= x) ++c;
-        return c;
-    }
-};
-
-struct Piece {
-    int b, unit;               // request, unit within it
-    int hg, r0, rows;          // head group, first row, rows
-    int j0, j1;                // chunks of this piece
-    int C, len, n_ctx;         // context, nodes, chunks of the context
-    __device__ __forceinline__ int n() const { return n_ctx + (len + kDraftTile - 1) / kDraftTile; }
-};
-
-// The pieces of a CTA's range, one after the other; every warp walks through them by itself.
-struct Walk {
-    uint64_t lo, hi, S;        // the range, and where the request begins
-    int b, unit;               // the next unit to look at (-1: the first in the range)
-    __device__ __forceinline__ Walk(const Args& a, const Division& d)
-    {
-        const uint32_t c = blockIdx.x;
-        const bool idle = d.W == 0 || c >= d.n;
-        S = d.S;
-        b = idle ? a.B : d.b;
-        unit = -1;
-        lo = idle ? 0 : d.begin(c);
-        hi = idle ? 0 : c + 1 < d.n ? d.begin(c + 1) : d.W;
-    }
-    __device__ __forceinline__ bool next(const Args& a, int chunk, Piece& p)
-    {
-        while (b < a.B && S < hi) {
-            const Shape s = shape_of(a, b);
-            if (s.len != 0) {
-                const uint32_t uc = s.unit_cost(a, chunk), c = s.chunk_cost(a);
-                const int groups = s.groups(a), units = groups * (a.Hkv / a.heads);
-                if (unit < 0) unit = lo > S ? (int)((lo - S) / uc) : 0;
-                while (unit < units) {
-                    const uint64_t at = S + (uint64_t)unit * uc, first = at + kUnitCost;
-                    if (at >= hi) return false;
-                    const int n = s.n(chunk);
-                    // (a range that ends behind the unit takes all of its chunks)
-                    const uint32_t j0 = lo > first ? (uint32_t)min((uint64_t)uc, lo - first) : 0;
-                    const uint32_t j1 = hi > first ? (uint32_t)min((uint64_t)uc, hi - first) : 0;
-                    p.j0 = (int)((j0 + c - 1) / c);
-                    p.j1 = min(n, (int)((j1 + c - 1) / c));
-                    p.unit = unit++;
-                    if (p.j0 >= p.j1) continue;
-                    p.b = b;
-                    p.hg = p.unit / groups;
-                    p.r0 = p.unit % groups * s.per(a);
-                    p.rows = min(s.per(a), s.rows(a) - p.r0);
-                    p.C = s.C;
-                    p.len = s.len;
-                    p.n_ctx = s.n_ctx(chunk);
-                    return true;
-                }
-                S += s.cost(a, chunk);
-            }
-            unit = 0;
-            ++b;
-        }
-        return false;
-    }
-};
+constexpr int kBox = 64;                   // positions of a TMA box at most
 
 struct Shared {                            // static part
     uint64_t full[kMostStages], empty[kMostStages], never;
     int abort, never_abort;
-    int b;
-    unsigned long long S, sum[kThreads / 32];
+    DivisionShared division;
 };
 
-// Every CTA sums the requests' costs and finds the request where its range begins.
-__device__ __forceinline__ Division divide(const Args& a, Shared& sh, int chunk)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned long long mine = 0;
-    for (int b = tid; b < a.B; b += kThreads) {
-        const Shape s = shape_of(a, b);
-        mine += s.cost(a, chunk);
-        if (blockIdx.x == 0 && s.len != a.lens[b]) rd_flag(a.status, RD_DEV_BAD_LENGTH);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sh.sum[warp] = mine;
-    __syncthreads();
-    Division d;
-    d.W = 0;
-    for (int w = 0; w < kThreads / 32; ++w) d.W += sh.sum[w];
-    const uint64_t most = d.W / kLeastCost;
-    d.n = (uint32_t)(most < 1 ? 1 : (most < gridDim.x ? most : gridDim.x));
-    d.b = a.B;
-    d.S = 0;
-    __syncthreads();
-    if (d.W == 0 || blockIdx.x >= d.n) return d;
-    const uint64_t lo = d.begin(blockIdx.x);
-    uint64_t before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        const unsigned long long cost = b < a.B ? shape_of(a, b).cost(a, chunk) : 0;
-        unsigned long long inc = cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) sh.sum[warp] = inc;
-        if (tid == 0) sh.b = -1;
-        __syncthreads();
-        uint64_t base = before;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) base += sh.sum[w];
-            before += sh.sum[w];
-        }
-        const uint64_t S = base + inc - cost;
-        if (cost != 0 && S <= lo && lo < S + cost) {
-            sh.b = b;
-            sh.S = S;
-        }
-        __syncthreads();
-        const int found = sh.b;
-        const uint64_t at = sh.S;
-        __syncthreads();
-        if (found >= 0) {
-            d.b = found;
-            d.S = at;
-            break;
+// a place in the ring
+struct Turn {
+    int stage;
+    uint32_t parity;           // of the stage's phase
+    __device__ __forceinline__ void next(int stages)
+    {
+        if (++stage == stages) {
+            stage = 0;
+            parity ^= 1u;
         }
     }
-    return d;
-}
+};
 
 // ------------------------------------------------------------------ small pieces of PTX
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -284,37 +74,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t at)
-{
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t at)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t at)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
-    return v;
-}
-__device__ __forceinline__ void compute_sync() { rdtc::named_sync(1, 32 * kConsumers); }
+__device__ __forceinline__ void compute_sync() { rdtc::named_sync(1, 32 * kWarps); }
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from)
@@ -347,88 +107,95 @@ __device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t
     }
 }
 
-// where the 64 positions from pos0 + 64 k of request b lie: the pool's row
-__device__ __forceinline__ int64_t row_at(const Args& a, int b, int pos, bool flags)
-{
-    int page = a.table[(size_t)b * a.max_pages + pos / a.page_size];
-    if (page < 0 || page >= a.num_pages) {
-        if (flags) rd_flag(a.status, RD_DEV_BAD_INDEX);
-        page = 0;
-    }
-    return (int64_t)page * a.page_size + pos % a.page_size;
-}
-
 // One warp fetches everything by TMA: a box of up to 64 positions x the unit's heads (for 8 bits one
-// for each 128 bytes of them, swizzled) per pool, the drafts' rows as bulk copies.  Lane k looks
-// up the k-th block of 64 positions of the next chunk while it waits.
+// for each 128 bytes of them, swizzled) per pool, the drafts' rows as bulk copies.  Lane k has the k-th
+// box of a chunk, and reads the next chunk's entry of the table while this one's copies go out: the
+// warp's time per chunk is what bounds small rows (without this, 1,500 cycles for 32 positions).
 template <int D, int BITS>
-__device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned char* ring, const Division& d, int chunk)
+__device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned char* ring, const Division& d)
 {
-    const int lane = threadIdx.x & 31;
-    const int box = chunk < 64 ? chunk : 64, row_bytes_ = a.heads * D * 2;
-    Walk walk(a, d);
+    const int lane = threadIdx.x & 31, chunk = a.chunk, box = min(kBox, chunk);
+    const bool mine = lane * box < chunk;
+    Walk walk = Walk::over(a, d);
     Piece p;
-    uint32_t it = 0;
+    Turn at = {0, 1};                      // (an empty stage's first phase counts as done)
     bool alive = true;
-    while (walk.next(a, chunk, p)) {
-        for (int j = p.j0; j < p.j1; ++j, ++it) {
-            const int stage = (int)(it % (uint32_t)a.stages);
-            const int pos0 = j * chunk, rows = j < p.n_ctx ? min(chunk, p.C - pos0) : 0, blocks = (rows + box - 1) / box;
-            int64_t row = 0;
-            if (lane < blocks) row = row_at(a, p.b, pos0 + lane * box, true);
-            if (alive && it >= (uint32_t)a.stages)
-                alive = rdattn::warp_wait(&sh.empty[stage], ((it / (uint32_t)a.stages) & 1u) ^ 1u, &sh.abort, kWaitBudget);
-            unsigned char* k_to = ring + (size_t)stage * 2 * a.half;
+    uint32_t filled = 0;
+    while (alive && walk.next(a, p)) {
+        const int32_t* table = a.table + (size_t)p.b * a.max_pages;
+        int pos = p.j0 * chunk + lane * box, in_page = pos % a.page_size;
+        table += pos / a.page_size;
+        int page = mine && pos < p.C ? __ldg(table) : 0;
+        const int x = p.hg * (a.seg / 4);
+        for (int j = p.j0; j < p.j1; ++j) {
+            unsigned char* k_to = ring + (size_t)at.stage * 2 * a.half;
             unsigned char* v_to = k_to + a.half;
-            uint64_t* bar = &sh.full[stage];
+            uint64_t* bar = &sh.full[at.stage];
+            uint64_t* empty = &sh.empty[at.stage];
             if (j < p.n_ctx) {
-                if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * blocks * box * a.seg));
+                const bool live = mine && pos < p.C;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, live));
+                if (live && (page < 0 || page >= a.num_pages)) {
+                    rd_flag(a.status, RD_DEV_BAD_INDEX);
+                    page = 0;
+                }
+                const int row = page * a.page_size + in_page;            // (31 bits: see launch)
+                pos += chunk;
+                for (in_page += chunk; in_page >= a.page_size; in_page -= a.page_size) ++table;
+                page = mine && pos < p.C ? __ldg(table) : 0;
+                alive = rdattn::warp_wait(empty, at.parity, &sh.abort, kWaitBudget);
+                if (!alive) break;         // nobody waits for copies any more
+                if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * boxes * box * a.seg));
                 __syncwarp();
-                if (lane < blocks) {
+                if (live) {
                     if constexpr (BITS == 4) {
                         const size_t to = (size_t)lane * box * a.seg;
-                        rdtc::tma_load_2d(k_to + to, &a.k_map, bar, p.hg * (a.seg / 4), (int)row);
-                        rdtc::tma_load_2d(v_to + to, &a.v_map, bar, p.hg * (a.seg / 4), (int)row);
+                        rdtc::tma_load_2d(k_to + to, &a.k_map, bar, x, row);
+                        rdtc::tma_load_2d(v_to + to, &a.v_map, bar, x, row);
                     } else {
-                        for (int x = 0; x < a.seg / 128; ++x) {
-                            const size_t to = (size_t)x * chunk * 128 + (size_t)lane * box * 128;
-                            rdtc::tma_load_2d(k_to + to, &a.k_map, bar, p.hg * (a.seg / 4) + 32 * x, (int)row);
-                            rdtc::tma_load_2d(v_to + to, &a.v_map, bar, p.hg * (a.seg / 4) + 32 * x, (int)row);
+                        for (int i = 0; i < a.seg / 128; ++i) {
+                            const size_t to = ((size_t)i * chunk + lane * box) * 128;
+                            rdtc::tma_load_2d(k_to + to, &a.k_map, bar, x + 32 * i, row);
+                            rdtc::tma_load_2d(v_to + to, &a.v_map, bar, x + 32 * i, row);
                         }
                     }
                 }
             } else {
-                const int node0 = (j - p.n_ctx) * kDraftTile;
-                const int nodes = min(kDraftTile, p.len - node0);
-                if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * nodes * row_bytes_));
+                alive = rdattn::warp_wait(empty, at.parity, &sh.abort, kWaitBudget);
+                if (!alive) break;
+                const int node0 = (j - p.n_ctx) * kDraftTile, nodes = min(kDraftTile, p.len - node0), bytes = a.heads * D * 2;
+                if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * nodes * bytes));
                 __syncwarp();
                 if (lane < nodes) {
-                    const size_t at = (((size_t)p.b * a.P + node0 + lane) * a.Hkv + (size_t)p.hg * a.heads) * D;
-                    rdtc::bulk_load(k_to + lane * a.draft_pitch, a.k_new + at, (uint32_t)row_bytes_, bar);
-                    rdtc::bulk_load(v_to + lane * a.draft_pitch, a.v_new + at, (uint32_t)row_bytes_, bar);
+                    const size_t from = (((size_t)p.b * a.P + node0 + lane) * a.Hkv + (size_t)p.hg * a.heads) * D;
+                    rdtc::bulk_load(k_to + lane * a.draft_pitch, a.k_new + from, (uint32_t)bytes, bar);
+                    rdtc::bulk_load(v_to + lane * a.draft_pitch, a.v_new + from, (uint32_t)bytes, bar);
                 }
             }
             __syncwarp();
+            at.next(a.stages);
+            ++filled;
         }
     }
     // no copy may be under way when the CTA ends: the last stages' have all landed
-    const uint32_t first = it > (uint32_t)a.stages ? it - (uint32_t)a.stages : 0;
-    for (uint32_t i = first; i < it; ++i)
-        rdattn::warp_wait(&sh.full[i % (uint32_t)a.stages], (i / (uint32_t)a.stages) & 1u, &sh.never_abort, kWaitBudget);
+    const uint32_t stages = (uint32_t)a.stages;
+    for (uint32_t i = filled > stages ? filled - stages : 0; i < filled; ++i)
+        rdattn::warp_wait(&sh.full[i % stages], (i / stages) & 1u, &sh.never_abort, kWaitBudget);
 }
 
 // The same by 128 threads with copies of 16, 8 or 4 bytes, for rows that TMA's rules leave out (an
 // odd number of kv heads).
 template <int D, int BITS>
-__device__ __forceinline__ void load_rowwise(const Args& a, Shared& sh, unsigned char* ring, const Division& d, int chunk)
+__device__ __forceinline__ void load_rowwise(const Args& a, Shared& sh, unsigned char* ring, const Division& d)
 {
-    const int tid = threadIdx.x - 32 * kConsumers;
+    const int chunk = a.chunk;
+    const int tid = threadIdx.x - 32 * kWarps;
     const int64_t row = (int64_t)a.Hkv * a.seg / a.heads;
-    Walk walk(a, d);
+    Walk walk = Walk::over(a, d);
     Piece p;
     uint32_t it = 0;
     bool alive = true;
-    while (walk.next(a, chunk, p)) {
+    while (walk.next(a, p)) {
         for (int j = p.j0; j < p.j1; ++j, ++it) {
             const int stage = (int)(it % (uint32_t)a.stages);
             // where the positions lie, before the wait
@@ -470,7 +237,7 @@ __device__ __forceinline__ void load_rowwise(const Args& a, Shared& sh, unsigned
 template <int D>
 __device__ __forceinline__ void clear_rows(const Args& a)
 {
-    const int tid = threadIdx.x - 32 * kConsumers;
+    const int tid = threadIdx.x - 32 * kWarps;
     const int vecs = a.Hq * D / 8;
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const int from = shape_of(a, b).len;
@@ -489,37 +256,72 @@ struct Place {
 template <int D, int BITS, int NT>
 struct Sums {                              // of 8 NT rows; this thread's columns D / 8 * g ..., rows 8 i + 2 t, + 1
     float o[D / 16][NT][4];
-    float r[2 * NT], l[2 * NT];            // references (0: none yet), sums of the weights
-    uint32_t none;                         // bit k: row k has none
+    uint32_t none;                         // bit k: row k has no reference yet
     bool fresh;                            // some row of the warp has none
+    // A thread's factors, references and sums of weights lie in shared memory: its registers are taken.
+    uint32_t fr, l;
+    __device__ __forceinline__ float reference(int k) const { return -__uint_as_float(lds32(fr + (uint32_t)(64 * (k / 2) + 8 * (k & 1) + 4))); }
+    __device__ __forceinline__ void set_reference(int k, float r) const
+    {
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(fr + (uint32_t)(64 * (k / 2) + 8 * (k & 1) + 4)), "f"(-r) : "memory");
+    }
+    __device__ __forceinline__ void sums(float (&v)[2 * NT]) const
+    {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const uint2 u = lds64(l + (uint32_t)(256 * i));
+            v[2 * i] = __uint_as_float(u.x), v[2 * i + 1] = __uint_as_float(u.y);
+        }
+    }
+    __device__ __forceinline__ void set_sums(const float (&v)[2 * NT]) const
+    {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(l + (uint32_t)(256 * i)), "f"(v[2 * i]), "f"(v[2 * i + 1]) : "memory");
+    }
 };
+
+// maximum (or sum) over the lanes that share a row
+template <int NT, bool SUM>
+__device__ __forceinline__ void over_lanes(float (&v)[2 * NT])
+{
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, v[k], o);
+            v[k] = SUM ? v[k] + x : fmaxf(v[k], x);
+        }
+}
 
 // new references, kBelow under the rows' maxima: `top` is this thread's
 template <int D, int BITS, int NT>
-__device__ __forceinline__ void raise(Sums<D, BITS, NT>& s, const float (&top)[2 * NT])
+__device__ __forceinline__ void raise(Sums<D, BITS, NT>& s, float (&top)[2 * NT])
 {
+    // (No lane may leave the common way here: rows without a reference differ from lane to lane.)
     uint32_t none = 0;
+    float l[2 * NT];
+    over_lanes<NT, false>(top);
+    s.sums(l);
 #pragma unroll
     for (int k = 0; k < 2 * NT; ++k) {
-        float v = top[k];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-        v -= kBelow;
-        const bool had = !(s.none >> k & 1u);
-        if (v == -INFINITY && !had) {
-            none |= 1u << k;
-            continue;
-        }
-        const float r = had ? fmaxf(s.r[k], v) : v;
-        const float f = had ? fast_exp2(s.r[k] - r) : 0.f;       // (nothing summed yet)
-        s.r[k] = r;
-        s.l[k] *= f;
+        const float v = top[k] - kBelow, was = s.reference(k);
+        const bool had = !(s.none >> k & 1u), still = v == -INFINITY && !had;
+        top[k] = had ? fmaxf(was, v) : still ? 0.f : v;
+        const float f = had ? fast_exp2(was - top[k]) : 0.f;         // (nothing summed yet)
+        none |= still ? 1u << k : 0u;
+        l[k] *= f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             s.o[j][k / 2][k & 1] *= f;
             s.o[j][k / 2][2 + (k & 1)] *= f;
         }
     }
+    s.set_sums(l);
+    __syncwarp();                                      // all have read the old references
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) s.set_reference(k, top[k]);     // (lanes that share a row agree)
+    __syncwarp();
     s.none = none;
     s.fresh = __any_sync(0xffffffffu, none != 0);
 }
@@ -542,7 +344,7 @@ struct Rows {
 // MT tiles of 16 positions of the context; `valid` of them count
 template <int D, int BITS, int NT, int MT>
 __device__ __forceinline__ void context_tiles(const Args& a, const Place& w, Sums<D, BITS, NT>& s, const Rows<BITS>& k_row,
-                                              const Rows<BITS>& v_row, uint32_t q_at, uint32_t f_at, int valid)
+                                              const Rows<BITS>& v_row, uint32_t q_at, int valid)
 {
     using namespace rdquant;
     constexpr int KB = D / 64;             // blocks of a row of K that a thread widens
@@ -610,11 +412,15 @@ __device__ __forceinline__ void context_tiles(const Args& a, const Place& w, Sum
                 }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const uint4 qb = lds128(q_at + (uint32_t)(i * 8 * (2 * D + 16) + 128 * kb + 16 * h));
+                const uint2 qb = lds64(q_at + (uint32_t)(i * 8 * (2 * D + 16) + 128 * kb + 16 * h));
 #pragma unroll
                 for (int m = 0; m < MT; ++m) mma_f16(x[m][i], f[m][0], qb.x, qb.y);
+            }
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma_f16(x[m][i], f[m][1], qb.z, qb.w);
+            for (int i = 0; i < NT; ++i) {
+                const uint2 qb = lds64(q_at + (uint32_t)(i * 8 * (2 * D + 16) + 128 * kb + 16 * h + 8));
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma_f16(x[m][i], f[m][1], qb.x, qb.y);
             }
         }
     }
@@ -632,25 +438,27 @@ __device__ __forceinline__ void context_tiles(const Args& a, const Place& w, Sum
     float most = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const uint2 fb = lds64(f_at + (uint32_t)(32 * i));
-        const float f[2] = {__uint_as_float(fb.x), __uint_as_float(fb.y)};
+        const uint4 v = lds128(s.fr + (uint32_t)(64 * i));
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                x[m][i][c] = fmaf(x[m][i][c], f[c & 1], -s.r[2 * i + (c & 1)]);
+                x[m][i][c] = fmaf(x[m][i][c], __uint_as_float(c & 1 ? v.z : v.x), __uint_as_float(c & 1 ? v.w : v.y));
                 most = fmaxf(most, x[m][i][c]);
             }
     }
     if (__any_sync(0xffffffffu, most > kBelow + kLag) || s.fresh) {
-        float was[2 * NT], top[2 * NT];
+        float top[2 * NT];
 #pragma unroll
         for (int k = 0; k < 2 * NT; ++k) {
-            was[k] = s.r[k];
+            const float was = s.reference(k);
             top[k] = -INFINITY;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) top[k] = fmaxf(top[k], fmaxf(x[m][k / 2][k & 1], x[m][k / 2][2 + (k & 1)]));
-            top[k] += was[k];
+            for (int m = 0; m < MT; ++m) {
+                x[m][k / 2][k & 1] += was;
+                x[m][k / 2][2 + (k & 1)] += was;
+                top[k] = fmaxf(top[k], fmaxf(x[m][k / 2][k & 1], x[m][k / 2][2 + (k & 1)]));
+            }
         }
         raise<D, BITS, NT>(s, top);
 #pragma unroll
@@ -658,8 +466,10 @@ __device__ __forceinline__ void context_tiles(const Args& a, const Place& w, Sum
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) x[m][i][c] += was[2 * i + (c & 1)] - s.r[2 * i + (c & 1)];
+                for (int c = 0; c < 4; ++c) x[m][i][c] -= top[2 * i + (c & 1)];
     }
+    float l[2 * NT];
+    s.sums(l);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         uint32_t pb[NT][2];
@@ -668,11 +478,12 @@ __device__ __forceinline__ void context_tiles(const Args& a, const Place& w, Sum
             float p[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) p[c] = fast_exp2(x[m][i][c]);
-            s.l[2 * i] += p[0] + p[2];
-            s.l[2 * i + 1] += p[1] + p[3];
+            l[2 * i] += p[0] + p[2];
+            l[2 * i + 1] += p[1] + p[3];
             pb[i][0] = transpose8x8(pack_f16(p[0], p[1]));       // 2^-11 of each weight
             pb[i][1] = transpose8x8(pack_f16(p[2], p[3]));
         }
+        if (m == MT - 1) s.set_sums(l);
         // ---- O^T
         const int first = 16 * m, v[4] = {first + position_of(w.t, 0), first + position_of(w.t, 1),
                                           first + position_of(w.t, 0) + 8, first + position_of(w.t, 1) + 8};
@@ -754,7 +565,7 @@ __device__ __forceinline__ uint32_t bf16_of_f16(uint32_t x)
 // a product have one type), 2^-9 of each weight
 template <int D, int BITS, int NT>
 __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const Piece& pc, Sums<D, BITS, NT>& s, uint32_t k_at,
-                                           uint32_t v_at, uint32_t q_at, uint32_t f_at, int node0, int nodes)
+                                           uint32_t v_at, uint32_t q_at, int node0, int nodes)
 {
     constexpr int KB = D / 64;
     float x[NT][4];
@@ -792,8 +603,8 @@ __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const 
     const float back = 1.f / a.k_scale;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const uint2 fb = lds64(f_at + (uint32_t)(32 * i));
-        const float f[2] = {__uint_as_float(fb.x) * back, __uint_as_float(fb.y) * back};
+        const uint4 fr = lds128(s.fr + (uint32_t)(64 * i));
+        const float f[2] = {__uint_as_float(fr.x) * back, __uint_as_float(fr.z) * back};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             x[i][c] = (seen[2 * i + (c & 1)] >> (pos + 4 * (c & 2)) & 1u) ? x[i][c] * f[c & 1] : -INFINITY;
@@ -802,15 +613,18 @@ __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const 
     }
     raise<D, BITS, NT>(s, top);
     uint32_t pb[NT][2];
+    float l[2 * NT];
+    s.sums(l);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const float p0 = fast_exp2(x[i][0] - s.r[2 * i]), p1 = fast_exp2(x[i][1] - s.r[2 * i + 1]);
-        const float p2 = fast_exp2(x[i][2] - s.r[2 * i]), p3 = fast_exp2(x[i][3] - s.r[2 * i + 1]);
-        s.l[2 * i] += p0 + p2;
-        s.l[2 * i + 1] += p1 + p3;
+        const float p0 = fast_exp2(x[i][0] - top[2 * i]), p1 = fast_exp2(x[i][1] - top[2 * i + 1]);
+        const float p2 = fast_exp2(x[i][2] - top[2 * i]), p3 = fast_exp2(x[i][3] - top[2 * i + 1]);
+        l[2 * i] += p0 + p2;
+        l[2 * i + 1] += p1 + p3;
         pb[i][0] = transpose8x8(pack_bf16(p0, p1));
         pb[i][1] = transpose8x8(pack_bf16(p2, p3));
     }
+    s.set_sums(l);
     const int v[4] = {position_of(w.t, 0), position_of(w.t, 1), position_of(w.t, 0) + 8, position_of(w.t, 1) + 8};
 #pragma unroll
     for (int part = 0; part < D / 64; ++part) {           // eight columns at a time
@@ -835,8 +649,10 @@ struct Buffers {
     unsigned char* ring;
     __half* q;                 // [heads][kRows][D + 8]
     float* f;                  // [heads][kRows] score = product x f (log2 units, the cache's scale in it)
-    float4* join;              // [4][2][D / 16][32]
-    float2* join_ml;           // [4][8][32]
+    float2* fr;                // [warps][kRows] f, and minus the row's reference
+    float2* l;                 // [warps][kRows / 8][32] each thread's sums of weights
+    float4* join;              // [warps / 2][2][D / 16][32]
+    float2* join_ml;           // [warps / 2][8][32]
 };
 
 // The queries of a unit as 16-bit floats.  A power of two per row brings its largest element to
@@ -878,14 +694,14 @@ __device__ __forceinline__ void stage_queries(const Args& a, const Place& w, con
 
 template <int D, int BITS, int NT>
 __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& buf, const Place& w, const Piece& p,
-                                   const Division& d, uint32_t& it, bool& alive)
+                                      Turn& at, bool& alive)
 {
-    constexpr int TILES = tiles_of<BITS>();
-    const int chunk = 16 * TILES * w.splits;
+    constexpr int TILES = tiles_of(D, BITS);
+    const int chunk = a.chunk;
     Sums<D, BITS, NT> s;
-#pragma unroll
-    for (int k = 0; k < 2 * NT; ++k) s.r[k] = s.l[k] = 0.f;
     s.none = (1u << 2 * NT) - 1u;
+    s.fr = smem_addr(buf.fr + w.warp * kRows + 2 * w.t);
+    s.l = smem_addr(buf.l + w.warp * (kRows / 8) * 32 + w.lane);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -897,7 +713,14 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     stage_queries<D>(a, w, p, buf, NT);
     compute_sync();
     const uint32_t q_at = smem_addr(buf.q) + (uint32_t)((w.head * kRows + w.g) * (2 * D + 16) + 32 * w.t);
-    const uint32_t f_at = smem_addr(buf.f) + (uint32_t)(4 * (w.head * kRows + 2 * w.t));
+    if (w.lane < kRows) buf.fr[w.warp * kRows + w.lane] = make_float2(buf.f[w.head * kRows + w.lane], 0.f);
+    {
+        float zeros[2 * NT];
+#pragma unroll
+        for (int k = 0; k < 2 * NT; ++k) zeros[k] = 0.f;
+        s.set_sums(zeros);
+    }
+    __syncwarp();
     const uint32_t ring = smem_addr(buf.ring);
     bool scaled = false;                   // O holds values, no longer values / v_scale
     auto scale_values = [&]() {
@@ -909,16 +732,15 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
                 for (int c = 0; c < 4; ++c) s.o[j][i][c] *= a.v_scale;
         scaled = true;
     };
-    for (int j = p.j0; j < p.j1; ++j, ++it) {
-        const int stage = (int)(it % (uint32_t)a.stages);
+    for (int j = p.j0; j < p.j1; ++j) {
         if (alive) {
-            alive = rdattn::warp_wait(&sh.full[stage], (it / (uint32_t)a.stages) & 1u, &sh.abort, kWaitBudget);
+            alive = rdattn::warp_wait(&sh.full[at.stage], at.parity, &sh.abort, kWaitBudget);
             if (!alive && w.lane == 0) {
                 sh.abort = 1;
                 rd_flag(a.status, RD_DEV_TIMEOUT);
             }
         }
-        const uint32_t k_at = ring + (uint32_t)(stage * 2 * a.half), v_at = k_at + (uint32_t)a.half;
+        const uint32_t k_at = ring + (uint32_t)(at.stage * 2 * a.half), v_at = k_at + (uint32_t)a.half;
         if (j < p.n_ctx) {
             const int first = w.split * 16 * TILES, valid = p.C - j * chunk - first;
             Rows<BITS> k_row, v_row;
@@ -935,11 +757,11 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
             k_row.base = k_at + off;
             v_row.base = v_at + off;
             // (two tiles at a time where the registers last: more products in flight)
-            constexpr int MT = TILES == 2 && NT <= kPairTiles ? 2 : 1;
+            constexpr int MT = TILES;
 #pragma unroll 1
             for (int x = 0; x < TILES; x += MT)
                 if (valid > 16 * x) {
-                    context_tiles<D, BITS, NT, MT>(a, w, s, k_row, v_row, q_at, f_at, min(16 * MT, valid - 16 * x));
+                    context_tiles<D, BITS, NT, MT>(a, w, s, k_row, v_row, q_at, min(16 * MT, valid - 16 * x));
                     k_row.base += (uint32_t)(16 * a.pitch);
                     v_row.base += (uint32_t)(16 * a.pitch);
                 }
@@ -948,18 +770,20 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
             if (!scaled) scale_values();
             if (tile % w.splits == w.split) {
                 const uint32_t off = (uint32_t)(w.head * D * 2);
-                draft_tile<D, BITS, NT>(a, w, p, s, k_at + off, v_at + off, q_at, f_at, tile * kDraftTile,
+                draft_tile<D, BITS, NT>(a, w, p, s, k_at + off, v_at + off, q_at, tile * kDraftTile,
                                         min(kDraftTile, p.len - tile * kDraftTile));
             }
         }
         __syncwarp();
-        if (w.lane == 0) rdtc::mbar_arrive(&sh.empty[stage]);
+        if (w.lane == 0) rdtc::mbar_arrive(&sh.empty[at.stage]);
+        at.next(a.stages);
     }
     if (!scaled) scale_values();
+    float l[2 * NT], r[2 * NT];
+    s.sums(l);
+    over_lanes<NT, true>(l);
 #pragma unroll
-    for (int k = 0; k < 2 * NT; ++k)
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) s.l[k] += __shfl_xor_sync(0xffffffffu, s.l[k], o);
+    for (int k = 0; k < 2 * NT; ++k) r[k] = s.reference(k);
 
     // ---- the warps of a head join their sums, the upper half of them into the lower
     for (int half = w.splits / 2; half >= 1; half /= 2) {
@@ -971,7 +795,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
             if (gives) {
                 if (i0 == 0) {
 #pragma unroll
-                    for (int k = 0; k < 2 * NT; ++k) buf.join_ml[(slot * 8 + k) * 32 + w.lane] = make_float2(s.none >> k & 1u ? -INFINITY : s.r[k], s.l[k]);
+                    for (int k = 0; k < 2 * NT; ++k) buf.join_ml[(slot * 8 + k) * 32 + w.lane] = make_float2(s.none >> k & 1u ? -INFINITY : r[k], l[k]);
                 }
 #pragma unroll
                 for (int i = i0; i < i0 + 2 && i < NT; ++i)
@@ -986,13 +810,13 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
 #pragma unroll
                     for (int k = 0; k < 2 * NT; ++k) {
                         const float2 ml = buf.join_ml[(slot * 8 + k) * 32 + w.lane];
-                        const float mine = s.none >> k & 1u ? -INFINITY : s.r[k];
+                        const float mine = s.none >> k & 1u ? -INFINITY : r[k];
                         const float m = fmaxf(mine, ml.x), mu = m == -INFINITY ? 0.f : m;
                         const float f = fast_exp2(mine - mu);
                         fo[k] = fast_exp2(ml.x - mu);
-                        s.r[k] = mu;
+                        r[k] = mu;
                         if (m != -INFINITY) s.none &= ~(1u << k);
-                        s.l[k] = s.l[k] * f + ml.y * fo[k];
+                        l[k] = l[k] * f + ml.y * fo[k];
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
                             s.o[j][k / 2][k & 1] *= f;
@@ -1017,18 +841,18 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     if (w.split != 0) return;
 
     // ---- rows, or partials of a unit that the ranges cut
-    const bool whole = p.j0 == 0 && p.j1 == p.n();
+    const bool whole = p.j0 == 0 && p.j1 == p.n(a);
     const int h = p.hg * a.heads + w.head;
     const size_t slot = ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * a.heads + w.head;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = 8 * i + 2 * w.t + e;
-            if (r >= p.rows) continue;
+            const int at = 8 * i + 2 * w.t + e;
+            if (at >= p.rows) continue;
             if (whole) {
-                const float f = s.l[2 * i + e] == 0.f ? 0.f : 1.f / s.l[2 * i + e];
-                const int row = p.r0 + r;
+                const float f = l[2 * i + e] == 0.f ? 0.f : 1.f / l[2 * i + e];
+                const int row = p.r0 + at;
                 uint32_t u[D / 16];
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) u[j] = pack_bf16(s.o[j][i][e] * f, s.o[j][i][2 + e] * f);
@@ -1037,11 +861,11 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j) o[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
             } else {
-                float4* o = reinterpret_cast<float4*>(a.part + (slot * kRows + r) * D + D / 8 * w.g);
+                float4* o = reinterpret_cast<float4*>(a.part + (slot * kRows + at) * D + D / 8 * w.g);
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
                     o[j] = make_float4(s.o[2 * j][i][e], s.o[2 * j][i][2 + e], s.o[2 * j + 1][i][e], s.o[2 * j + 1][i][2 + e]);
-                if (w.g == 0) a.part_ml[slot * kRows + r] = make_float2(s.none >> (2 * i + e) & 1u ? -INFINITY : s.r[2 * i + e], s.l[2 * i + e]);
+                if (w.g == 0) a.part_ml[slot * kRows + at] = make_float2(s.none >> (2 * i + e) & 1u ? -INFINITY : r[2 * i + e], l[2 * i + e]);
             }
         }
 }
@@ -1053,28 +877,30 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
     __shared__ Shared sh;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5;
-    const int splits = kConsumers / a.heads, chunk = 16 * tiles_of<BITS>() * splits;
+    const int splits = kWarps / a.heads;
     Buffers buf;
     buf.ring = dyn;
     buf.q = reinterpret_cast<__half*>(dyn + (size_t)a.stages * 2 * a.half);
     buf.f = reinterpret_cast<float*>(buf.q + (size_t)a.heads * kRows * (D + 8));
-    buf.join = reinterpret_cast<float4*>(buf.f + (size_t)a.heads * kRows);
-    buf.join_ml = reinterpret_cast<float2*>(buf.join + 4 * 2 * (D / 16) * 32);
+    buf.fr = reinterpret_cast<float2*>(buf.f + (size_t)a.heads * kRows);
+    buf.l = buf.fr + kWarps * kRows;
+    buf.join = reinterpret_cast<float4*>(buf.l + kWarps * (kRows / 8) * 32);
+    buf.join_ml = reinterpret_cast<float2*>(buf.join + kWarps / 2 * 2 * (D / 16) * 32);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMostStages; ++i) {
             rdtc::mbar_init(&sh.full[i], a.tiled ? 1 : 32 * kLoaders);
-            rdtc::mbar_init(&sh.empty[i], kConsumers);
+            rdtc::mbar_init(&sh.empty[i], kWarps);
         }
         rdtc::mbar_init(&sh.never, 1);
         rdtc::mbar_fence_init();
         sh.abort = sh.never_abort = 0;
     }
-    const Division d = divide(a, sh, chunk);               // (its barriers order the set-up too)
+    const Division d = divide<kThreads>(a, sh.division);               // (its barriers order the set-up too)
     __syncthreads();
-    if (warp >= kConsumers) {
+    if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-        if (!a.tiled) load_rowwise<D, BITS>(a, sh, buf.ring, d, chunk);
-        else if (warp == kConsumers) load_tiled<D, BITS>(a, sh, buf.ring, d, chunk);
+        if (!a.tiled) load_rowwise<D, BITS>(a, sh, buf.ring, d);
+        else if (warp == kWarps) load_tiled<D, BITS>(a, sh, buf.ring, d);
         clear_rows<D>(a);
         return;
     }
@@ -1096,22 +922,22 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
         }
     }
     if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    Walk walk(a, d);
+    Walk walk = Walk::over(a, d);
     Piece p;
-    uint32_t it = 0;
-    while (walk.next(a, chunk, p)) {
-        if (threadIdx.x == 0 && p.j0 == 0 && p.j1 < p.n()) {
+    Turn at = {0, 0};
+    while (walk.next(a, p)) {
+        if (threadIdx.x == 0 && p.j0 == 0 && p.j1 < p.n(a)) {
             // the CTA that has the unit's last chunk
             const Shape s = shape_of(a, p.b);
-            const uint64_t last = walk.S + (uint64_t)p.unit * s.unit_cost(a, chunk) + kUnitCost +
-                                  (uint64_t)(p.n() - 1) * s.chunk_cost(a);
+            const uint64_t last = walk.S + (uint64_t)p.unit * s.unit_cost(a) + a.unit_cost +
+                                  (uint64_t)(p.n(a) - 1) * s.chunk_cost(a);
             a.desc[blockIdx.x] = make_int4(p.b, p.unit, (int)d.of(last), 0);
         }
         const int tiles = (p.rows + 7) / 8;
-        if (tiles == 1) piece<D, BITS, 1>(a, sh, buf, w, p, d, it, alive);
-        else if (tiles == 2) piece<D, BITS, 2>(a, sh, buf, w, p, d, it, alive);
-        else if (tiles == 3) piece<D, BITS, 3>(a, sh, buf, w, p, d, it, alive);
-        else piece<D, BITS, 4>(a, sh, buf, w, p, d, it, alive);
+        if (tiles == 1) piece<D, BITS, 1>(a, sh, buf, w, p, at, alive);
+        else if (tiles == 2) piece<D, BITS, 2>(a, sh, buf, w, p, at, alive);
+        else if (tiles == 3) piece<D, BITS, 3>(a, sh, buf, w, p, at, alive);
+        else piece<D, BITS, 4>(a, sh, buf, w, p, at, alive);
     }
 }
 
@@ -1131,7 +957,7 @@ __global__ void __launch_bounds__(256) quant_merge_kernel(const Args a)
     const int rows = min(s.per(a), s.rows(a) - r0), h = hg * a.heads + blockIdx.y;
     for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
         const int r = i / (D / 4), c = i % (D / 4);
-        auto at = [&](int cta) { return (((size_t)2 * cta + (cta == first ? 1 : 0)) * a.heads + blockIdx.y) * kRows + r; };
+        auto at = [&](int cta) { return (((size_t)2 * cta + (cta == first ? 1 : 0)) * a.heads + blockIdx.y) * a.unit_rows + r; };
         float M = -INFINITY;
         for (int k = first; k <= last; ++k) M = fmaxf(M, a.part_ml[at(k)].x);
         const float mu = M == -INFINITY ? 0.f : M;
@@ -1166,26 +992,20 @@ int pitch_of(int seg, int bits)
     return p;
 }
 
-// the pool as [rows][row bytes]; boxes of `box` rows x `width` bytes
-bool make_map(CUtensorMap* map, const void* pool, int64_t rows, int row_bytes, int width, int box, bool swizzled)
-{
-    auto fn = rdattn::encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)row_bytes / 4, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t boxes[2] = {(cuuint32_t)width / 4, (cuuint32_t)box};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(pool), dims, strides, boxes, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t desc_bytes(int grid) { return ((size_t)grid * sizeof(int4) + 127) & ~size_t(127); }
 
 template <int D, int BITS>
 cudaError_t launch(Args& a, int grid, cudaStream_t stream)
 {
-    const int splits = kConsumers / a.heads, chunk = 16 * tiles_of<BITS>() * splits;
+    const int chunk = 16 * tiles_of(D, BITS) * (kWarps / a.heads);
+    a.chunk = chunk;
+    a.draft_chunk = kDraftTile;
+    a.unit_rows = kRows;
+    a.row_step = 8;
+    a.chunk_cost = 3;
+    a.step_cost = 2;
+    a.unit_cost = 24;
+    a.least_cost = 24;
     a.seg = a.heads * rdquant::row_bytes(D, BITS);
     a.pitch = pitch_of(a.seg, BITS);
     const int stride = a.Hkv * rdquant::row_bytes(D, BITS);
@@ -1196,7 +1016,7 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     const int64_t rows_all = (int64_t)a.num_pages * a.page_size;
     a.tiled = a.gran == 16 && rows_all > 0 && rows_all <= 0x7fffffff && (BITS == 4 || a.seg % 128 == 0);
     if (a.tiled) {
-        const int box = chunk < 64 ? chunk : 64, width = BITS == 4 ? a.seg : 128;
+        const int box = chunk < kBox ? chunk : kBox, width = BITS == 4 ? a.seg : 128;
         if (!make_map(&a.k_map, a.k_pool, rows_all, stride, width, box, BITS == 8) ||
             !make_map(&a.v_map, a.v_pool, rows_all, stride, width, box, BITS == 8))
             return cudaErrorUnknown;
@@ -1205,7 +1025,7 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     a.draft_pitch = a.heads * D * 2 + 16;
     const int rows = a.tiled ? chunk * a.seg : chunk * a.pitch, drafts = kDraftTile * a.draft_pitch;
     a.half = ((rows > drafts ? rows : drafts) + 1023) / 1024 * 1024;       // (swizzled tiles repeat every 1024 bytes)
-    const int fixed = a.heads * kRows * ((D + 8) * 2 + 4) + 4 * 2 * (D / 16) * 32 * 16 + 4 * 8 * 32 * 8;
+    const int fixed = a.heads * kRows * ((D + 8) * 2 + 4) + kWarps * (kRows + kRows / 8 * 32) * 8 + kWarps / 2 * 32 * (2 * (D / 16) * 16 + 8 * 8);
     constexpr int kSmem = 227 * 1024 - 1024;               // what the static part leaves
     a.stages = (kSmem - fixed) / (2 * a.half);
     if (a.stages > kMostStages) a.stages = kMostStages;
@@ -1223,6 +1043,12 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     kernel<<<grid, kThreads, smem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch_merge(const Args& a, int grid, cudaStream_t stream)
+{
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, (unsigned)a.heads);
     cfg.blockDim = dim3(256);
@@ -1232,7 +1058,7 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quant_merge_kernel<D>, (const Args&)a);
+    return cudaLaunchKernelEx(&cfg, quant_merge_kernel<D>, a);
 }
 
 }  // namespace
@@ -1283,6 +1109,9 @@ cudaError_t rd_launch_quant_attention(const rd_quant_kv& kv, int B, int P_max, i
     a.k_scale = kv.k_scale;
     a.v_scale = kv.v_scale;
     a.stall = rd_attention_stall_budget();
-    if (D == 128) return kv.bits == 4 ? launch<128, 4>(a, grid, stream) : launch<128, 8>(a, grid, stream);
-    return kv.bits == 4 ? launch<64, 4>(a, grid, stream) : launch<64, 8>(a, grid, stream);
+    const cudaError_t e = D == 128 ? kv.bits == 4 ? launch<128, 4>(a, grid, stream) : launch<128, 8>(a, grid, stream)
+                          : kv.bits == 4 ? launch<64, 4>(a, grid, stream)
+                                         : launch<64, 8>(a, grid, stream);
+    if (e != cudaSuccess) return e;
+    return D == 128 ? launch_merge<128>(a, grid, stream) : launch_merge<64>(a, grid, stream);
 }
