@@ -2,18 +2,18 @@
 // log p(token), the entropy H = -sum p log p, and the k most likely tokens.
 //
 // One pass over each row.  In units of log2, with c = log2(e) / T and a reference m,
-//   z = c (x - m),  l = sum 2^z,  w = sum 2^z z:
-//   log p(x_t) = ln 2 (z_t - log2 l),   H = ln 2 (log2 l - w / l).
+//   z = c (x - m),  l = sum 2^z,  w = sum 2^z (x - m):
+//   log p(x_t) = ln 2 (z_t - log2 l),   H = ln 2 (log2 l - c w / l).
 // The reference is the maximum of the CTA's first 16,384 logits; a thread that meets a larger one
-// moves its own.  So a logit costs a difference, a product, a lower bound (2^-200 is 0, and 0 x -200
-// too: a logit of -inf adds nothing), an exponential and two accumulations: about 60 instructions
-// for eight 16-bit logits, somewhat more than half of what the SM can issue while HBM
-// delivers them.  What is rare (a larger maximum, a candidate) stays out of the loop's way.
+// moves its own.  So a logit costs a difference, a product, an exponential and two accumulations:
+// about 50 instructions for eight 16-bit logits, somewhat more than half of what the SM can
+// issue while HBM delivers them.  What is rare (a larger maximum, a candidate, numbers at the ends of
+// the range) stays out of the loop's way.
 //
 // The top k come from the same pass: a threshold that at least k logits of the row reach
 // is known after the first 64 logits of each thread (the k-th largest of the threads'
-// maxima, found bit by bit); what reaches it afterwards, a few times k of them, is collected as 64-bit keys
-// (value, then the lower index first) and ranked by counting at the end.  A row that keeps
+// maxima, found bit by bit); the 16-byte groups with what reaches it afterwards, a few times k of
+// them, are kept, and their 64-bit keys (value, then the lower index first) ranked by counting at the end.  A row that keeps
 // rising overfills the list; its k-th key is then a better threshold for another pass.
 //
 // Few rows: a cluster of up to eight CTAs takes one, and its first CTA joins the parts.
@@ -32,6 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 8;                  // 16-byte loads of a thread in flight
 constexpr int kMostCtas = 8;               // of a row
 constexpr int kList = 1024;                // candidates of a CTA
+constexpr int kGroups = 512;               // 16-byte groups that hold some
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -63,7 +64,43 @@ __device__ __forceinline__ float exp2_(float x)
     return y;
 }
 
+// two 32-bit numbers in one operation each
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 both(uint64_t x)
+{
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // ------------------------------------------------------------------ 16 bytes of logits
+// The fast way takes logits below kLow as that, and references between -1e38 and 1e30: differences
+// are finite, and those of such logits have no weight.
+constexpr float kLow = -3.0e38f;
+
 template <typename T>
 struct Vec;
 template <>
@@ -75,6 +112,13 @@ struct Vec<float> {
         x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
     }
     static constexpr uint32_t kNone = 0xff800000u;       // -inf
+    // with what lies below kLow as that
+    static __device__ __forceinline__ void unpack_finite(const uint4& u, float (&x)[4])
+    {
+        unpack(u, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = max_nan(x[i], kLow);
+    }
     static __device__ __forceinline__ float top(const uint4& u)
     {
         return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)), max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
@@ -103,6 +147,11 @@ struct Vec<__nv_bfloat16> {
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
         return d;
     }
+    static __device__ __forceinline__ void unpack_finite(const uint4& u, float (&x)[8])
+    {
+        constexpr uint32_t low = 0xff62ff62u;            // kLow
+        unpack(make_uint4(max2(u.x, low), max2(u.y, low), max2(u.z, low), max2(u.w, low)), x);
+    }
     static __device__ __forceinline__ float top(const uint4& u)
     {
         const uint32_t t = max2(max2(u.x, u.y), max2(u.z, u.w));
@@ -130,6 +179,12 @@ struct Vec<__half> {
         asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
         return d;
     }
+    static __device__ __forceinline__ void unpack_finite(const uint4& u, float (&x)[8])
+    {
+        unpack(u, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = max_nan(x[i], kLow);
+    }
     static __device__ __forceinline__ float top(const uint4& u)
     {
         const uint32_t t = max2(max2(u.x, u.y), max2(u.z, u.w));
@@ -155,31 +210,21 @@ struct Stats {
     __device__ __forceinline__ void move(float to, float c)       // to another reference
     {
         if (m != -INFINITY) {
-            const float d = (m - to) * c, f = exp2_(d);
+            const float d = m - to, f = exp2_(d * c);
             w = f * (w + d * l);
             l *= f;
             if (f == 0.f) w = 0.f;
         }
         m = to;
     }
-    __device__ __forceinline__ void join(const Stats& o, float c)
-    {
-        if (o.m == -INFINITY && o.l == 0.f) return;
-        if (m == -INFINITY && l == 0.f) {
-            *this = o;
-            return;
-        }
-        Stats b = o;
-        const float to = max_nan(m, b.m);
-        if (m != to) move(to, c);          // (two equal references may be infinite)
-        if (b.m != to) b.move(to, c);
-        l += b.l;
-        w += b.w;
-    }
+    __device__ __forceinline__ void add(float2 ls, float2 ws) { l += ls.x + ls.y, w += ws.x + ws.y; }
 };
 
 struct Shared {
     unsigned long long list[kList];
+    uint4 group[kGroups];                  // groups in which some logit reaches the threshold, and their numbers
+    int group_id[kGroups];
+    int groups;
     unsigned long long best[32];           // this CTA's top k, in order
     unsigned long long from[kMostCtas][32];
     Stats part[kMostCtas];                 // of the CTAs of the cluster
@@ -242,7 +287,17 @@ __device__ __forceinline__ uint4 load16(const uint4* p)
 template <typename T>
 __device__ __forceinline__ uint4 Row<T>::group(int g) const { return inside(g) ? load16(base + g) : edge(g); }
 
-// the logits of group g that are among the top k as far as is known
+// a group that has a candidate
+__device__ __forceinline__ void keep(Shared& sh, int g, const uint4& u)
+{
+    const int at = atomicAdd(&sh.groups, 1);
+    if (at < kGroups) {
+        sh.group[at] = u;
+        sh.group_id[at] = g;
+    }
+}
+
+// the logits of group g whose keys reach `least`
 template <typename T>
 __device__ __noinline__ void collect(Shared& sh, const Row<T>& row, int g, uint4 u, unsigned long long least)
 {
@@ -257,16 +312,68 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& row, int g, uint4
     }
 }
 
-// sh.list[0 .. n) -> the keys of rank below k, in order; one sync behind
-__device__ __forceinline__ void rank(Shared& sh, int n, int k, unsigned long long* out)
+// One group after the other, for rows where the fast way would not do: references near the lowest
+// number, extreme temperatures.  2^-200 is 0, and 0 x -200 too: a logit of -inf adds nothing.
+template <typename T>
+__device__ __noinline__ void add_slowly(Stats& s, uint4 u, float top, float c)
 {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const unsigned long long key = sh.list[i];
+    constexpr int N = Vec<T>::n;
+    if (top == -INFINITY) return;
+    if (!(top <= s.m)) s.move(top, c);
+    float v[N];
+    Vec<T>::unpack(u, v);
+    for (int e = 0; e < N; ++e) {
+        const float d = v[e] - s.m, p = exp2_(max_nan(d * c, -200.f));
+        s.l += p;
+        if (p != 0.f) s.w = fmaf(p, d, s.w);
+    }
+}
+
+// One warp: sh.list[0 .. n) -> sh.best, the keys of rank below k, in order.  The k-th largest upper
+// 16 bits are found bit by bit, what reaches them (few more than k) is ranked by counting.
+__device__ __forceinline__ void rank(Shared& sh, int n, int k)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t at = 0;
+    if (n > 64) {                          // (fewer are as quickly ranked as searched)
+        for (uint32_t bit = 0x80000000u; bit > 0x8000u; bit >>= 1) {
+            int reach = 0;
+            for (int i = lane; i < n; i += 32) reach += (uint32_t)(sh.list[i] >> 32) >= (at | bit);
+            if (__reduce_add_sync(0xffffffffu, reach) >= k) at |= bit;
+        }
+    }
+    unsigned long long* kept = reinterpret_cast<unsigned long long*>(sh.group);
+    int m = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const unsigned long long key = i0 + lane < n ? sh.list[i0 + lane] : 0;
+        const bool mine = i0 + lane < n && (uint32_t)(key >> 32) >= at;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        if (mine) kept[m + __popc(who & ((1u << lane) - 1))] = key;
+        m += __popc(who);
+    }
+    sh.best[lane] = 0;
+    __syncwarp();
+    for (int i = lane; i < m; i += 32) {
+        const unsigned long long key = kept[i];
         int r = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) r += sh.list[j] > key;
-        if (r < k) out[r] = key;
+        for (int j = 0; j < m; ++j) r += kept[j] > key;
+        if (r < k) sh.best[r] = key;
     }
+    __syncwarp();
+}
+
+// the sums of a warp's lanes, in all of them
+__device__ __forceinline__ Stats join_warp(Stats s, float c)
+{
+    const float m = number(__reduce_max_sync(0xffffffffu, ordered(s.m)));
+    if (s.m != m) s.move(m, c);            // (two equal references may be infinite)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s.l += __shfl_xor_sync(0xffffffffu, s.l, o);
+        s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    }
+    return s;
 }
 
 template <typename T>
@@ -322,26 +429,35 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     const T* x = static_cast<const T*>(a.logits) + r * a.V;
     const Row<T> row(x, a.V, part, parts);
     const float chosen = part == 0 && tid == 0 ? Vec<T>::one(x, token) : 0.f;
-    if (tid == 0) sh.count = 0;
-    if (tid < 32) sh.best[tid] = 0;
+    if (tid == 0) sh.count = sh.groups = 0;
     Stats s = {-INFINITY, 0.f, 0.f};
-    float l1 = 0.f, w1 = 0.f;              // (two chains of sums, of one reference)
+    uint64_t l2 = 0, w2 = 0;               // (two chains of sums each, of the reference s.m)
+    const uint64_t c2 = pair(a.c, a.c);
     unsigned long long least = 0;
     float floor_ = -INFINITY;              // what reaches it is looked at
+    bool fast = false;                     // (where it is not, every group is looked at)
     constexpr int kStep = kThreads * kAhead;
-    for (int g0 = row.first; g0 < row.last; g0 += kStep) {
+    // groups that lie inside of the row: the first and the last of all may not
+    const int inside0 = row.first + (row.first < row.last && !row.inside(row.first) ? 1 : 0);
+    const int inside1 = row.last - (row.last > inside0 && !row.inside(row.last - 1) ? 1 : 0);
+    for (int g0 = inside0; g0 < inside1; g0 += kStep) {
         uint4 u[kAhead];
+        if (g0 + kStep <= inside1) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int g = g0 + j * kThreads + tid;
-            u[j] = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
-            if (g < row.last) u[j] = row.group(g);
+            for (int j = 0; j < kAhead; ++j) u[j] = load16(row.base + g0 + j * kThreads + tid);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int g = g0 + j * kThreads + tid;
+                u[j] = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
+                if (g < inside1) u[j] = load16(row.base + g);
+            }
         }
-        if (g0 == row.first) {
+        if (g0 == inside0) {
             float top = Vec<T>::top(u[0]);
 #pragma unroll
             for (int j = 1; j < kAhead; ++j) top = max_nan(top, Vec<T>::top(u[j]));
-            const uint32_t mine = g0 + tid < row.last ? ordered(top) : 0u;
+            const uint32_t mine = g0 + tid < inside1 ? ordered(top) : 0u;
             const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
             if (lane == 0) sh.warp[warp].m = __uint_as_float(warp_top);
             __syncthreads();
@@ -350,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             for (int w = 0; w < kWarps; ++w) most = max(most, __float_as_uint(sh.warp[w].m));
             s.m = number(most);
             floor_ = s.m;
+            fast = s.m > -1e38f && s.m < 1e30f && a.c > 1e-30f;
             if (k > 0) {
                 // the k-th largest of the threads' maxima, rounded down to 16 bits
                 uint32_t at = 0;
@@ -365,48 +482,60 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             const float top = Vec<T>::top(u[j]);
             if (!(top < floor_)) {
                 const int g = g0 + j * kThreads + tid;
-                if (k > 0 && g < row.last) collect<T>(sh, row, g, u[j], least);
-                if (!(top <= s.m)) {
-                    s.l += l1, s.w += w1;
-                    l1 = w1 = 0.f;
+                if (k > 0 && g < inside1) keep(sh, g, u[j]);
+                if (fast && !(top <= s.m)) {
+                    s.add(both(l2), both(w2));
+                    l2 = w2 = 0;
                     s.move(top, a.c);
+                    fast = top < 1e30f;
                 }
             }
-            if (s.m == -INFINITY) continue;
+            if (!fast) {
+                add_slowly<T>(s, u[j], top, a.c);
+                continue;
+            }
             float v[N];
-            Vec<T>::unpack(u[j], v);
+            Vec<T>::unpack_finite(u[j], v);
 #pragma unroll
             for (int e = 0; e < N; e += 2) {
-                const float z0 = max_nan((v[e] - s.m) * a.c, -200.f), z1 = max_nan((v[e + 1] - s.m) * a.c, -200.f);
-                const float p0 = exp2_(z0), p1 = exp2_(z1);
-                s.l += p0;
-                l1 += p1;
-                s.w = fmaf(p0, z0, s.w);
-                w1 = fmaf(p1, z1, w1);
+                const uint64_t d = add2(pair(v[e], v[e + 1]), pair(-s.m, -s.m));
+                const float2 z = both(mul2(d, c2));
+                const uint64_t p = pair(exp2_(z.x), exp2_(z.y));
+                l2 = add2(l2, p);
+                w2 = fma2(p, d, w2);
             }
         }
     }
-    s.l += l1;
-    s.w += w1;
-    __syncthreads();                       // (sh.warp is read above and written below)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stats b;
-        b.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-        b.l = __shfl_xor_sync(0xffffffffu, s.l, o);
-        b.w = __shfl_xor_sync(0xffffffffu, s.w, o);
-        // both lanes of a pair join in the same order, so that they stay alike
-        Stats lo = lane & o ? b : s;
-        lo.join(lane & o ? s : b, a.c);
-        s = lo;
+    s.add(both(l2), both(w2));
+    // the row's first and last group, where they are partly outside
+    if (tid < 2) {
+        const int g = tid == 0 ? row.first : row.last - 1;
+        if (tid == 0 ? inside0 > row.first : inside1 < row.last) {
+            const uint4 u = row.edge(g);
+            const float top = Vec<T>::top(u);
+            if (k > 0 && !(top < floor_)) keep(sh, g, u);
+            add_slowly<T>(s, u, top, a.c);
+        }
     }
+    __syncthreads();                       // (sh.warp is read above and written below; the groups are there)
+    if (k > 0 && sh.groups <= kGroups)
+        for (int i = tid; i < sh.groups; i += kThreads) collect<T>(sh, row, sh.group_id[i], sh.group[i], least);
+    s = join_warp(s, a.c);
     if (lane == 0) sh.warp[warp] = s;
     __syncthreads();
     if (k > 0) {
-        while (sh.count > kList) {         // too many: the k-th of those kept is a better threshold
-            rank(sh, kList, k, sh.best);
+        // too many: the k-th of those kept is a better threshold for another pass
+        bool again = sh.groups > kGroups;
+        while (again || sh.count > kList) {
+            if (again) {
+                // (of the groups that were kept, if the keys are not yet a list)
+                for (int i = tid; i < kList / N; i += kThreads) collect<T>(sh, row, sh.group_id[i], sh.group[i], least);
+                __syncthreads();
+            }
+            if (warp == 0) rank(sh, min(sh.count, kList), k);
             __syncthreads();
-            least = sh.best[k - 1];
+            again = false;
+            least = max(least, sh.best[k - 1]);
             floor_ = number((uint32_t)(least >> 32));
             if (floor_ != floor_) floor_ = -INFINITY;
             __syncthreads();
@@ -416,14 +545,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
                 const uint4 u = row.group(g);
                 if (!(Vec<T>::top(u) < floor_)) collect<T>(sh, row, g, u, least);
             }
-            if (tid < 32) sh.best[tid] = 0;
             __syncthreads();
         }
-        rank(sh, sh.count, k, sh.best);
-        __syncthreads();
+        if (warp == 0) rank(sh, sh.count, k);
     }
-    Stats all = sh.warp[0];
-    for (int w = 1; w < kWarps; ++w) all.join(sh.warp[w], a.c);
+    Stats all = {-INFINITY, 0.f, 0.f};     // (in the first warp)
+    if (warp == 0) {
+        if (lane < kWarps) all = sh.warp[lane];
+        all = join_warp(all, a.c);
+    }
     if (parts > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         Shared* to = cluster.map_shared_rank(&sh, 0);
@@ -431,8 +561,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         if (tid == 0) to->part[part] = all;
         cluster.sync();
         if (part != 0) return;
-        all = sh.part[0];
-        for (int p = 1; p < parts; ++p) all.join(sh.part[p], a.c);
+        if (warp == 0) {
+            all = {-INFINITY, 0.f, 0.f};
+            if (lane < parts) all = sh.part[lane];
+            all = join_warp(all, a.c);
+        }
         if (k > 0) {
             // at most 8 x 32 keys, one a thread
             const unsigned long long key = tid < parts * 32 ? sh.from[tid / 32][lane] : 0;
@@ -451,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     const float m = all.m == -INFINITY ? 0.f : all.m;
     if (tid == 0) {
         a.logprob[n] = kLn2 * ((chosen - m) * a.c - lg);
-        a.entropy[n] = kLn2 * (lg - all.w / all.l);
+        a.entropy[n] = kLn2 * (lg - all.w / all.l * a.c);
     }
     if (tid < k) {
         const unsigned long long key = sh.best[tid];
