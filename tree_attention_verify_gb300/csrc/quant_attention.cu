@@ -16,25 +16,39 @@
 // of a row of K (one block, one scale) as its share of four steps, and V's columns are dealt
 // so that a thread owns 16 consecutive ones: its loads are whole blocks and its outputs whole
 // 16-byte words.  Rows are the products' short side: 8 at a time, so that five rows cost a
-// quarter of what 32 do.
+// quarter of what 32 do.  The matrix unit takes one of these products every two cycles: 862 of the
+// 1,208 us that 64 contexts of 8,192 with 41 nodes and 40 heads take (2.5 TB/s of codes), so it,
+// then the widening beside it, bounds calls of many rows; calls of a few rows by one pass through the code (7,000
+// cycles the first time) and the unit's start and end.
 #include "quant_attention.cuh"
 
 namespace {
 
 using namespace rdquant;
 
-constexpr int kWarps = 8;                  // that compute
-constexpr int kLoaders = 4;                // that load
-constexpr int kThreads = 32 * (kWarps + kLoaders);
-constexpr int kLaunchRegs = 168;           // 384 x 168 = 64,512 registers, dealt anew:
-constexpr int kComputeRegs = 232, kLoadRegs = 40;
-static_assert(32 * kWarps * kComputeRegs + 32 * kLoaders * kLoadRegs <= kThreads * kLaunchRegs, "registers");
-constexpr int kRows = 32;                  // rows of a unit at most
+// Warps that compute: the sums of 32 rows take 128 registers of a thread with D = 128, which leaves room for
+// 8; with D = 64 12 fit, and hide more of each other's latency.
+constexpr int warps_of(int D) { return D == 128 ? 8 : 12; }
+constexpr int kLoaders = 4;                // warps that load
+constexpr int threads_of(int D) { return 32 * (warps_of(D) + kLoaders); }
+// registers of a thread: the launch's (all of an SM's), dealt anew
+constexpr int launch_regs(int D) { return D == 128 ? 168 : 128; }
+constexpr int compute_regs(int D) { return D == 128 ? 232 : 152; }
+constexpr int load_regs(int D) { return D == 128 ? 40 : 56; }
+constexpr bool regs_fit(int D)
+{
+    return 32 * (warps_of(D) * compute_regs(D) + kLoaders * load_regs(D)) <= threads_of(D) * launch_regs(D);
+}
+static_assert(regs_fit(64) && regs_fit(128), "registers");
+// rows of a unit at most (with D = 64, 32 rows spill from 152 registers: two contexts of 50,000 74 us, not 51)
+constexpr int kMostRows = 32;
+constexpr int rows_of(int D) { return D == 128 ? kMostRows : 24; }
 // tiles of 16 positions of a warp's share of a chunk (the ring holds few chunks of 8-bit rows of 128)
 constexpr int tiles_of(int D, int bits) { return D == 128 && bits == 8 ? 1 : 2; }
 constexpr int kDraftTile = 16;             // packed drafts of a chunk
 constexpr int kMostStages = 8;
-constexpr int kBox = 64;                   // positions of a TMA box at most
+// positions of a TMA box: chunks of 96 positions are no whole number of 64
+constexpr int box_of(int D, int bits) { return tiles_of(D, bits) * warps_of(D) % 16 == 0 ? 64 : 32; }
 
 struct Shared {                            // static part
     uint64_t full[kMostStages], empty[kMostStages], never;
@@ -74,7 +88,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ void compute_sync() { rdtc::named_sync(1, 32 * kWarps); }
+template <int D>
+__device__ __forceinline__ void compute_sync() { rdtc::named_sync(1, 32 * warps_of(D)); }
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from)
@@ -91,7 +106,7 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from)
 __device__ __forceinline__ int position_of(int t, int e) { return 4 * e + ((t + 2 * e) & 3); }    // e: 0, 1
 
 template <int BYTES>
-__device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t v_to, const size_t (&base)[4], int rows,
+__device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t v_to, const size_t (&base)[6], int rows,
                                           int tid)
 {
     const size_t row = (size_t)a.Hkv * a.seg / a.heads;
@@ -99,7 +114,9 @@ __device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t
     for (int i = tid; i < copies; i += 32 * kLoaders) {
         const int pos = (int)__umulhi((uint32_t)i, a.per_row_magic), part = i - pos * a.per_row;
         const int blk = pos >> 6;
-        const size_t at0 = blk < 2 ? (blk == 0 ? base[0] : base[1]) : (blk == 2 ? base[2] : base[3]);
+        size_t at0 = base[0];
+#pragma unroll
+        for (int k = 1; k < 6; ++k) at0 = blk == k ? base[k] : at0;
         const size_t at = at0 + (size_t)(pos & 63) * row + (size_t)part * BYTES;
         const uint32_t to = (uint32_t)(pos * a.pitch + part * BYTES);
         copy_async<BYTES>(k_to + to, a.k_pool + at);
@@ -107,14 +124,14 @@ __device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t
     }
 }
 
-// One warp fetches everything by TMA: a box of up to 64 positions x the unit's heads (for 8 bits one
+// One warp fetches everything by TMA: a box of 64 or 32 positions x the unit's heads (for 8 bits one
 // for each 128 bytes of them, swizzled) per pool, the drafts' rows as bulk copies.  Lane k has the k-th
 // box of a chunk, and reads the next chunk's entry of the table while this one's copies go out: the
 // warp's time per chunk is what bounds small rows (without this, 1,500 cycles for 32 positions).
 template <int D, int BITS>
 __device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned char* ring, const Division& d)
 {
-    const int lane = threadIdx.x & 31, chunk = a.chunk, box = min(kBox, chunk);
+    const int lane = threadIdx.x & 31, chunk = a.chunk, box = box_of(D, BITS);
     const bool mine = lane * box < chunk;
     Walk walk = Walk::over(a, d);
     Piece p;
@@ -189,7 +206,7 @@ template <int D, int BITS>
 __device__ __forceinline__ void load_rowwise(const Args& a, Shared& sh, unsigned char* ring, const Division& d)
 {
     const int chunk = a.chunk;
-    const int tid = threadIdx.x - 32 * kWarps;
+    const int tid = threadIdx.x - 32 * warps_of(D);
     const int64_t row = (int64_t)a.Hkv * a.seg / a.heads;
     Walk walk = Walk::over(a, d);
     Piece p;
@@ -199,13 +216,13 @@ __device__ __forceinline__ void load_rowwise(const Args& a, Shared& sh, unsigned
         for (int j = p.j0; j < p.j1; ++j, ++it) {
             const int stage = (int)(it % (uint32_t)a.stages);
             // where the positions lie, before the wait
-            size_t base[4] = {0, 0, 0, 0};
+            size_t base[6] = {0, 0, 0, 0, 0, 0};
             int rows = 0;
             if (j < p.n_ctx) {
                 const int pos0 = j * chunk;
                 rows = min(chunk, p.C - pos0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 6; ++k)
                     if (64 * k < rows) base[k] = (size_t)(row_at(a, p.b, pos0 + 64 * k, tid == 0) * row + (int64_t)p.hg * a.seg);
             }
             if (alive && it >= (uint32_t)a.stages)
@@ -237,7 +254,7 @@ __device__ __forceinline__ void load_rowwise(const Args& a, Shared& sh, unsigned
 template <int D>
 __device__ __forceinline__ void clear_rows(const Args& a)
 {
-    const int tid = threadIdx.x - 32 * kWarps;
+    const int tid = threadIdx.x - 32 * warps_of(D);
     const int vecs = a.Hq * D / 8;
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const int from = shape_of(a, b).len;
@@ -647,10 +664,10 @@ __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const 
 
 struct Buffers {
     unsigned char* ring;
-    __half* q;                 // [heads][kRows][D + 8]
-    float* f;                  // [heads][kRows] score = product x f (log2 units, the cache's scale in it)
-    float2* fr;                // [warps][kRows] f, and minus the row's reference
-    float2* l;                 // [warps][kRows / 8][32] each thread's sums of weights
+    __half* q;                 // [heads][rows][D + 8]
+    float* f;                  // [heads][rows] score = product x f (log2 units, the cache's scale in it)
+    float2* fr;                // [warps][rows] f, and minus the row's reference
+    float2* l;                 // [warps][rows / 8][32] each thread's sums of weights
     float4* join;              // [warps / 2][2][D / 16][32]
     float2* join_ml;           // [warps / 2][8][32]
 };
@@ -687,8 +704,8 @@ __device__ __forceinline__ void stage_queries(const Args& a, const Place& w, con
         out.y = pack_f16(x[2] * up, x[3] * up);
         out.z = pack_f16(x[4] * up, x[5] * up);
         out.w = pack_f16(x[6] * up, x[7] * up);
-        *reinterpret_cast<uint4*>(buf.q + ((size_t)w.head * kRows + r) * (D + 8) + 8 * sub) = out;
-        if (sub == 0) buf.f[w.head * kRows + r] = a.scale_log2 * a.k_scale * down;
+        *reinterpret_cast<uint4*>(buf.q + ((size_t)w.head * rows_of(D) + r) * (D + 8) + 8 * sub) = out;
+        if (sub == 0) buf.f[w.head * rows_of(D) + r] = a.scale_log2 * a.k_scale * down;
     }
 }
 
@@ -700,8 +717,8 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     const int chunk = a.chunk;
     Sums<D, BITS, NT> s;
     s.none = (1u << 2 * NT) - 1u;
-    s.fr = smem_addr(buf.fr + w.warp * kRows + 2 * w.t);
-    s.l = smem_addr(buf.l + w.warp * (kRows / 8) * 32 + w.lane);
+    s.fr = smem_addr(buf.fr + w.warp * rows_of(D) + 2 * w.t);
+    s.l = smem_addr(buf.l + w.warp * (rows_of(D) / 8) * 32 + w.lane);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -709,11 +726,11 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
 #pragma unroll
             for (int c = 0; c < 4; ++c) s.o[j][i][c] = 0.f;
     s.fresh = true;
-    compute_sync();                        // nobody reads the last piece's queries any more
+    compute_sync<D>();                        // nobody reads the last piece's queries any more
     stage_queries<D>(a, w, p, buf, NT);
-    compute_sync();
-    const uint32_t q_at = smem_addr(buf.q) + (uint32_t)((w.head * kRows + w.g) * (2 * D + 16) + 32 * w.t);
-    if (w.lane < kRows) buf.fr[w.warp * kRows + w.lane] = make_float2(buf.f[w.head * kRows + w.lane], 0.f);
+    compute_sync<D>();
+    const uint32_t q_at = smem_addr(buf.q) + (uint32_t)((w.head * rows_of(D) + w.g) * (2 * D + 16) + 32 * w.t);
+    if (w.lane < rows_of(D)) buf.fr[w.warp * rows_of(D) + w.lane] = make_float2(buf.f[w.head * rows_of(D) + w.lane], 0.f);
     {
         float zeros[2 * NT];
 #pragma unroll
@@ -757,7 +774,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
             k_row.base = k_at + off;
             v_row.base = v_at + off;
             // (two tiles at a time where the registers last: more products in flight)
-            constexpr int MT = TILES;
+            constexpr int MT = D == 64 && NT > 2 ? 1 : TILES;
 #pragma unroll 1
             for (int x = 0; x < TILES; x += MT)
                 if (valid > 16 * x) {
@@ -786,8 +803,9 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     for (int k = 0; k < 2 * NT; ++k) r[k] = s.reference(k);
 
     // ---- the warps of a head join their sums, the upper half of them into the lower
-    for (int half = w.splits / 2; half >= 1; half /= 2) {
-        const bool gives = w.split >= half && w.split < 2 * half, takes = w.split < half;
+    for (int n = w.splits; n > 1;) {
+        const int half = (n + 1) / 2;
+        const bool gives = w.split >= half && w.split < n, takes = w.split < n - half;
         const int slot = (takes ? w.split : w.split - half) * a.heads + w.head;
         float fo[2 * NT];
 #pragma unroll
@@ -804,7 +822,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
                         buf.join[((slot * 2 + i - i0) * (D / 16) + j) * 32 + w.lane] =
                             make_float4(s.o[j][i][0], s.o[j][i][1], s.o[j][i][2], s.o[j][i][3]);
             }
-            compute_sync();
+            compute_sync<D>();
             if (takes) {
                 if (i0 == 0) {
 #pragma unroll
@@ -835,8 +853,9 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
                         s.o[j][i][3] += v.w * fo[2 * i + 1];
                     }
             }
-            compute_sync();
+            compute_sync<D>();
         }
+        n = half;
     }
     if (w.split != 0) return;
 
@@ -861,50 +880,50 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j) o[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
             } else {
-                float4* o = reinterpret_cast<float4*>(a.part + (slot * kRows + at) * D + D / 8 * w.g);
+                float4* o = reinterpret_cast<float4*>(a.part + (slot * rows_of(D) + at) * D + D / 8 * w.g);
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
                     o[j] = make_float4(s.o[2 * j][i][e], s.o[2 * j][i][2 + e], s.o[2 * j + 1][i][e], s.o[2 * j + 1][i][2 + e]);
-                if (w.g == 0) a.part_ml[slot * kRows + at] = make_float2(s.none >> (2 * i + e) & 1u ? -INFINITY : r[2 * i + e], l[2 * i + e]);
+                if (w.g == 0) a.part_ml[slot * rows_of(D) + at] = make_float2(s.none >> (2 * i + e) & 1u ? -INFINITY : r[2 * i + e], l[2 * i + e]);
             }
         }
 }
 
 template <int D, int BITS>
-__global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(threads_of(D), 1) quant_attention_kernel(const __grid_constant__ Args a)
 {
     extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ Shared sh;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5;
-    const int splits = kWarps / a.heads;
+    const int splits = warps_of(D) / a.heads;
     Buffers buf;
     buf.ring = dyn;
     buf.q = reinterpret_cast<__half*>(dyn + (size_t)a.stages * 2 * a.half);
-    buf.f = reinterpret_cast<float*>(buf.q + (size_t)a.heads * kRows * (D + 8));
-    buf.fr = reinterpret_cast<float2*>(buf.f + (size_t)a.heads * kRows);
-    buf.l = buf.fr + kWarps * kRows;
-    buf.join = reinterpret_cast<float4*>(buf.l + kWarps * (kRows / 8) * 32);
-    buf.join_ml = reinterpret_cast<float2*>(buf.join + kWarps / 2 * 2 * (D / 16) * 32);
+    buf.f = reinterpret_cast<float*>(buf.q + (size_t)a.heads * rows_of(D) * (D + 8));
+    buf.fr = reinterpret_cast<float2*>(buf.f + (size_t)a.heads * rows_of(D));
+    buf.l = buf.fr + warps_of(D) * rows_of(D);
+    buf.join = reinterpret_cast<float4*>(buf.l + warps_of(D) * (rows_of(D) / 8) * 32);
+    buf.join_ml = reinterpret_cast<float2*>(buf.join + warps_of(D) / 2 * 2 * (D / 16) * 32);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMostStages; ++i) {
             rdtc::mbar_init(&sh.full[i], a.tiled ? 1 : 32 * kLoaders);
-            rdtc::mbar_init(&sh.empty[i], kWarps);
+            rdtc::mbar_init(&sh.empty[i], warps_of(D));
         }
         rdtc::mbar_init(&sh.never, 1);
         rdtc::mbar_fence_init();
         sh.abort = sh.never_abort = 0;
     }
-    const Division d = divide<kThreads>(a, sh.division);               // (its barriers order the set-up too)
+    const Division d = divide<threads_of(D)>(a, sh.division);               // (its barriers order the set-up too)
     __syncthreads();
-    if (warp >= kWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    if (warp >= warps_of(D)) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(load_regs(D)));
         if (!a.tiled) load_rowwise<D, BITS>(a, sh, buf.ring, d);
-        else if (warp == kWarps) load_tiled<D, BITS>(a, sh, buf.ring, d);
+        else if (warp == warps_of(D)) load_tiled<D, BITS>(a, sh, buf.ring, d);
         clear_rows<D>(a);
         return;
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(compute_regs(D)));
     Place w;
     w.warp = warp;
     w.lane = threadIdx.x & 31;
@@ -937,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
         if (tiles == 1) piece<D, BITS, 1>(a, sh, buf, w, p, at, alive);
         else if (tiles == 2) piece<D, BITS, 2>(a, sh, buf, w, p, at, alive);
         else if (tiles == 3) piece<D, BITS, 3>(a, sh, buf, w, p, at, alive);
-        else piece<D, BITS, 4>(a, sh, buf, w, p, at, alive);
+        else if constexpr (rows_of(D) > 24) piece<D, BITS, 4>(a, sh, buf, w, p, at, alive);
     }
 }
 
@@ -997,15 +1016,17 @@ size_t desc_bytes(int grid) { return ((size_t)grid * sizeof(int4) + 127) & ~size
 template <int D, int BITS>
 cudaError_t launch(Args& a, int grid, cudaStream_t stream)
 {
-    const int chunk = 16 * tiles_of(D, BITS) * (kWarps / a.heads);
+    const int chunk = 16 * tiles_of(D, BITS) * (warps_of(D) / a.heads);
     a.chunk = chunk;
     a.draft_chunk = kDraftTile;
-    a.unit_rows = kRows;
+    a.unit_rows = rows_of(D);
     a.row_step = 8;
-    a.chunk_cost = 3;
-    a.step_cost = 2;
-    a.unit_cost = 24;
-    a.least_cost = 24;
+    // (cycles of 64 positions x 4 heads, D = 128: 3,050 with 16 rows, 3,600 with 24, 4,700 with 32; a unit's
+    // start and end 18,000)
+    a.chunk_cost = 16;
+    a.step_cost = 5;
+    a.unit_cost = 120;
+    a.least_cost = 72;
     a.seg = a.heads * rdquant::row_bytes(D, BITS);
     a.pitch = pitch_of(a.seg, BITS);
     const int stride = a.Hkv * rdquant::row_bytes(D, BITS);
@@ -1016,7 +1037,7 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     const int64_t rows_all = (int64_t)a.num_pages * a.page_size;
     a.tiled = a.gran == 16 && rows_all > 0 && rows_all <= 0x7fffffff && (BITS == 4 || a.seg % 128 == 0);
     if (a.tiled) {
-        const int box = chunk < kBox ? chunk : kBox, width = BITS == 4 ? a.seg : 128;
+        const int box = box_of(D, BITS), width = BITS == 4 ? a.seg : 128;
         if (!make_map(&a.k_map, a.k_pool, rows_all, stride, width, box, BITS == 8) ||
             !make_map(&a.v_map, a.v_pool, rows_all, stride, width, box, BITS == 8))
             return cudaErrorUnknown;
@@ -1025,7 +1046,7 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     a.draft_pitch = a.heads * D * 2 + 16;
     const int rows = a.tiled ? chunk * a.seg : chunk * a.pitch, drafts = kDraftTile * a.draft_pitch;
     a.half = ((rows > drafts ? rows : drafts) + 1023) / 1024 * 1024;       // (swizzled tiles repeat every 1024 bytes)
-    const int fixed = a.heads * kRows * ((D + 8) * 2 + 4) + kWarps * (kRows + kRows / 8 * 32) * 8 + kWarps / 2 * 32 * (2 * (D / 16) * 16 + 8 * 8);
+    const int fixed = a.heads * rows_of(D) * ((D + 8) * 2 + 4) + warps_of(D) * (rows_of(D) + rows_of(D) / 8 * 32) * 8 + warps_of(D) / 2 * 32 * (2 * (D / 16) * 16 + 8 * 8);
     constexpr int kSmem = 227 * 1024 - 1024;               // what the static part leaves
     a.stages = (kSmem - fixed) / (2 * a.half);
     if (a.stages > kMostStages) a.stages = kMostStages;
@@ -1035,12 +1056,12 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
         cudaFuncAttributes f;
         cudaError_t e = cudaFuncGetAttributes(&f, kernel);
         // setmaxnreg deals out the registers of the launch
-        return e != cudaSuccess ? e : f.numRegs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+        return e != cudaSuccess ? e : f.numRegs == launch_regs(D) ? cudaSuccess : cudaErrorInvalidConfiguration;
     }();
     if (ready != cudaSuccess) return ready;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, stream>>>(a);
+    kernel<<<grid, threads_of(D), smem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return cudaSuccess;
@@ -1066,7 +1087,7 @@ cudaError_t launch_merge(const Args& a, int grid, cudaStream_t stream)
 size_t rd_quant_attention_workspace_bytes(int Hkv, int D)
 {
     const int grid = rd_device_sm_count();
-    const size_t rows = (size_t)2 * grid * heads_of(Hkv) * kRows;
+    const size_t rows = (size_t)2 * grid * heads_of(Hkv) * kMostRows;
     return desc_bytes(grid) + rows * (sizeof(float2) + (size_t)D * sizeof(float));
 }
 
@@ -1091,7 +1112,7 @@ cudaError_t rd_launch_quant_attention(const rd_quant_kv& kv, int B, int P_max, i
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.desc = reinterpret_cast<int4*>(ws);
     a.part_ml = reinterpret_cast<float2*>(ws + desc_bytes(grid));
-    a.part = reinterpret_cast<float*>(a.part_ml + (size_t)2 * grid * a.heads * kRows);
+    a.part = reinterpret_cast<float*>(a.part_ml + (size_t)2 * grid * a.heads * kMostRows);
     a.status = dev_status;
     a.B = B;
     a.P = P_max;
