@@ -7,10 +7,14 @@
 // are e4m3(x / g), saturating.
 //
 // All three are streams, bound by HBM: a thread takes one block of K and the same of V
-// (32 bytes each on the 16-bit side, 9 or 16 on the other), so that a block's maximum needs no other
-// thread and neighbours' accesses are consecutive.  A CTA first finds where each of its tokens lies
-// (request, position, page: a search and two dependent reads), a thread per token, then moves
-// about kBlocks blocks; the divisions are IEEE ones, so that ties are decided as defined.
+// (32 bytes each on the 16-bit side, one access; 9 or 16 on the other), so that a block's maximum needs
+// no other thread and neighbours' accesses are consecutive.  A CTA first finds where each of its
+// tokens lies (request, position, page: a search and two dependent reads), a thread per token, then
+// moves about kBlocks blocks; the divisions are IEEE ones, so that ties are decided as defined.
+// Two 16-byte accesses for a block's 32 bytes would take longer (16 x 4,096 tokens of 8 heads read from 4
+// bits: 53 us, not 45), and so would CTAs of 1,024 blocks, which wait longer for their first
+// bytes than they then move (12,000 tokens written and read back: 39 us, not 37).  Reading 8 x 8,192 tokens of 40 heads
+// from 8 bits takes 234 us, 6.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -22,7 +26,7 @@ namespace {
 using namespace rdquant;
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 1024;              // blocks of 16 elements that a CTA moves (of K, and of V)
+constexpr int kBlocks = 512;               // blocks of 16 elements that a CTA moves (of K, and of V)
 constexpr int kMostTokens = 64;            // tokens of a CTA
 
 struct Pools {
@@ -62,9 +66,8 @@ __device__ __forceinline__ int request_of(const T* __restrict__ offsets, int n, 
 }
 
 // ------------------------------------------------------------------ one block
-__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16])
+__device__ __forceinline__ void unpack16(const uint32_t (&u)[8], float (&x)[16])
 {
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         x[2 * i] = __uint_as_float(u[i] << 16);
@@ -134,44 +137,78 @@ __device__ __forceinline__ void store_block(unsigned char* row, int block, const
     }
 }
 
+// a block as it lies in the pool, and its values
 template <int D, int BITS>
-__device__ __forceinline__ void load_block(const unsigned char* row, int block, float g, uint4& a, uint4& b)
-{
-    uint32_t w[8];                         // 16-bit floats, in order
-    if constexpr (BITS == 8) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + 16 * block));
-        e4m3x4(u.x, w[0], w[1]);
-        e4m3x4(u.y, w[2], w[3]);
-        e4m3x4(u.z, w[4], w[5]);
-        e4m3x4(u.w, w[6], w[7]);
-    } else {
-        uint2 u;
-        if constexpr (D == 128) {
-            u = __ldg(reinterpret_cast<const uint2*>(row + 8 * block));
+struct Raw {
+    uint4 c;                               // 4 bits: codes, codes, scale
+    __device__ __forceinline__ void load(const unsigned char* row, int block)
+    {
+        if constexpr (BITS == 8) {
+            c = __ldg(reinterpret_cast<const uint4*>(row + 16 * block));
         } else {
-            const uint32_t* from = reinterpret_cast<const uint32_t*>(row + 8 * block);
-            u = make_uint2(__ldg(from), __ldg(from + 1));
+            if constexpr (D == 128) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + 8 * block));
+                c.x = u.x, c.y = u.y;
+            } else {
+                const uint32_t* from = reinterpret_cast<const uint32_t*>(row + 8 * block);
+                c.x = __ldg(from), c.y = __ldg(from + 1);
+            }
+            c.z = __ldg(row + D / 2 + block);
         }
-        const uint32_t byte = __ldg(row + D / 2 + block);
-        uint32_t s, same;
-        e4m3x4(byte * 0x01010101u, s, same);
-        uint32_t c[4];
-        e2m1x8(u.x, c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = mul_f16x2(c[i], s);          // exact
-        e2m1x8(u.y, c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 + i] = mul_f16x2(c[i], s);
     }
-    uint32_t o[8];
+    __device__ __forceinline__ void values(float g, uint32_t (&o)[8]) const
+    {
+        uint32_t w[8];                     // 16-bit floats, in order
+        if constexpr (BITS == 8) {
+            e4m3x4(c.x, w[0], w[1]);
+            e4m3x4(c.y, w[2], w[3]);
+            e4m3x4(c.z, w[4], w[5]);
+            e4m3x4(c.w, w[6], w[7]);
+        } else {
+            uint32_t s, same, u[4];
+            e4m3x4(c.z * 0x01010101u, s, same);
+            e2m1x8(c.x, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 v = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
-        __nv_bfloat162 r = __floats2bfloat162_rn(v.x * g, v.y * g);
-        o[i] = *reinterpret_cast<uint32_t*>(&r);
+            for (int i = 0; i < 4; ++i) w[i] = mul_f16x2(u[i], s);          // exact
+            e2m1x8(c.y, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 + i] = mul_f16x2(u[i], s);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
+            __nv_bfloat162 r = __floats2bfloat162_rn(v.x * g, v.y * g);
+            o[i] = *reinterpret_cast<uint32_t*>(&r);
+        }
     }
-    a = make_uint4(o[0], o[1], o[2], o[3]);
-    b = make_uint4(o[4], o[5], o[6], o[7]);
+};
+
+// 32 bytes in one access, where they are aligned so
+__device__ __forceinline__ void store32(uint4* to, const uint32_t (&o)[8], bool aligned)
+{
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                     "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                     : "memory");
+    } else {
+        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+__device__ __forceinline__ void load32(const uint4* from, uint32_t (&o)[8], bool aligned)
+{
+    if (aligned) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
+                     : "l"(from));
+    } else {
+        const uint4 a = __ldg(from), b = __ldg(from + 1);
+        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+    }
+}
+__device__ __forceinline__ bool aligned32(const void* a, const void* b)
+{
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 31) == 0;
 }
 
 // ------------------------------------------------------------------ writing
@@ -255,17 +292,20 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
     if ((int)threadIdx.x < n) where[threadIdx.x] = src.find(p, t0 + threadIdx.x, status);
     __syncthreads();
     const int blocks = Hkv * (D / 16);     // of a token
+    const bool wide = aligned32(k, v);
     for (int i = threadIdx.x; i < n * blocks; i += kThreads) {
         const int t = i / blocks, c = i - t * blocks;
         const Where at = where[t];
         if (at.to < 0) continue;
         const size_t from = ((size_t)at.from * blocks + c) * 2;
-        const uint4 k0 = __ldg(k + from), k1 = __ldg(k + from + 1), v0 = __ldg(v + from), v1 = __ldg(v + from + 1);
+        uint32_t ku[8], vu[8];
+        load32(k + from, ku, wide);
+        load32(v + from, vu, wide);
         const size_t to = ((size_t)at.to * Hkv + c / (D / 16)) * row_bytes(D, BITS);
         float x[16];
-        unpack16(k0, k1, x);
+        unpack16(ku, x);
         store_block<D, BITS>(p.k + to, c % (D / 16), x, p.k_scale);
-        unpack16(v0, v1, x);
+        unpack16(vu, x);
         store_block<D, BITS>(p.v + to, c % (D / 16), x, p.v_scale);
     }
 }
@@ -300,21 +340,23 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
             if (offsets[b] < 0 || offsets[b] > offsets[b + 1] || offsets[b + 1] > total) rd_flag(status, RD_DEV_BAD_LENGTH);
     __syncthreads();
     const int blocks = Hkv * (D / 16);
+    const bool wide = aligned32(k, v);
     for (int i = threadIdx.x; i < n * blocks; i += kThreads) {
         const int t = i / blocks, c = i - t * blocks;
         const int64_t row = where[t];
         if (row == -2) continue;
-        uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;
+        uint32_t ku[8] = {}, vu[8] = {};
         if (row >= 0) {
             const size_t from = ((size_t)row * Hkv + c / (D / 16)) * row_bytes(D, BITS);
-            load_block<D, BITS>(p.k + from, c % (D / 16), p.k_scale, k0, k1);
-            load_block<D, BITS>(p.v + from, c % (D / 16), p.v_scale, v0, v1);
+            Raw<D, BITS> kr, vr;
+            kr.load(p.k + from, c % (D / 16));
+            vr.load(p.v + from, c % (D / 16));
+            kr.values(p.k_scale, ku);
+            vr.values(p.v_scale, vu);
         }
         const size_t to = ((size_t)(t0 + t) * blocks + c) * 2;
-        k[to] = k0;
-        k[to + 1] = k1;
-        v[to] = v0;
-        v[to + 1] = v1;
+        store32(k + to, ku, wide);
+        store32(v + to, vu, wide);
     }
 }
 
