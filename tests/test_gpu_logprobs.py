@@ -207,3 +207,62 @@ def test_rows_past_32_bits():
     x[-1] = torch.randn(V, device=DEV).bfloat16()
     out = rd.rd_token_logprobs(x, _i32([5]), rows=_i32([n_rows - 1]), top=2)
     check(out, 0, x[-1], 5, 1.0, 2)
+
+
+@pytest.mark.parametrize("n", [1, 400])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_candidates_behind_a_low_start(dtype, n):
+    """The first part of a row tells nothing of the rest: every later group is a candidate, and the
+    list of them overfills (a row alone is shared by several CTAs, 400 are not)."""
+    rd = _rd()
+    V = 60000
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    x = torch.full((1, V), -60.0, device=DEV)
+    x[0, 20000:] = 3 * torch.randn(V - 20000, generator=gen, device=DEV)
+    x = x.to(TYPES[dtype]).expand(n, V).contiguous()
+    out = rd.rd_token_logprobs(x, _i32([V - 7] * n), top=32)
+    for i in {0, n - 1}:
+        check(out, i, x[i], V - 7, 1.0, 32)
+
+
+def test_numbers_at_the_ends_of_the_range():
+    """References and logits near the largest and the lowest numbers of each type, and infinities."""
+    rd = _rd()
+    V = 9000
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    noise = torch.randn(V, generator=gen, device=DEV)
+    low32, low16 = torch.finfo(torch.bfloat16).min, torch.finfo(torch.float16).min
+    for dtype, low, tops in ((torch.float32, -3.4e38, (0.0, 9e29, 2e30, 3.3e38, -9e37, -2e38)),
+                             (torch.bfloat16, low32, (0.0, 9e29, 2e30, 3.3e38, -9e37, -2e38)),
+                             (torch.float16, low16, (0.0, 65504.0, -60000.0))):
+        x = torch.full((len(tops), V), low, dtype=torch.float64, device=DEV)
+        for i, top in enumerate(tops):
+            x[i, 3::50] = top
+            x[i, 7::50] = top + noise[7::50] * (abs(top) * 2.0 ** -6 + 1)
+            x[i, 11::50] = -float("inf")
+        x = x.clamp(max=torch.finfo(dtype).max).to(dtype)
+        tokens = [3, 7, 53, 57, 103, 107][:len(tops)]
+        for T in (1.0, 1e3, 1e-2):
+            out = rd.rd_token_logprobs(x, _i32(tokens), top=4, temperature=T)
+            for i, t in enumerate(tokens):
+                far = oq.logprobs(x[i].double().cpu().numpy(), t, float(np.float32(T)), 4)[0] < -2.0 ** 128
+                if far:                       # below every 32-bit number: its rounding is -inf
+                    assert float(out["logprob"][i]) == -float("inf")
+                    # (the rest of the entry against a token that has a logarithm)
+                    t = int(out["top_tokens"][i, 0])
+                    one = rd.rd_token_logprobs(x[i:i + 1], _i32([t]), top=4, temperature=T)
+                    check(one, 0, x[i], t, float(np.float32(T)), 4)
+                else:
+                    check(out, i, x[i], t, float(np.float32(T)), 4)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_nan_anywhere(dtype):
+    rd = _rd()
+    V = 40009
+    x = torch.randn(6, V, device=DEV).to(TYPES[dtype])
+    for i, at in enumerate((0, 5, 16390, 20000, V - 1)):
+        x[i, at] = float("nan")
+    out = rd.rd_token_logprobs(x, _i32([9] * 6), top=2)
+    assert torch.isnan(out["logprob"][:5]).all() and torch.isnan(out["entropy"][:5]).all()
+    check(out, 5, x[5], 9, 1.0, 2)

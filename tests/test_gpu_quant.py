@@ -649,3 +649,63 @@ def test_matches_the_bf16_attention():
     check(call(s), s)
     a = np.abs(_f64(want)) + 4.0              # |v| is below 16: both are within 2^-7 of the weighted means
     assert (np.abs(_f64(call(s)) - _f64(want)) <= a * 2.0 ** -6).all()
+
+
+MORE = {
+    # B, P, Hq, Hkv, D, page, bits, lens, ctx
+    "rows 40 8 bits": (2, 40, 4, 4, 128, 64, 8, [40, 33], [500, 130]),
+    "rows 33 two heads 8 bits": (2, 33, 2, 2, 128, 64, 8, [33, 32], [260, 129]),
+    "chunk ends, four heads": (6, 20, 4, 4, 64, 64, 4, [20, 17, 16, 8, 9, 1], [95, 96, 97, 191, 192, 193]),
+    "chunk ends, two heads": (5, 25, 2, 2, 64, 64, 8, [25, 24, 16, 7, 1], [191, 192, 193, 383, 385]),
+    "chunk ends, one head": (5, 24, 1, 1, 64, 64, 4, [24, 20, 1, 9, 17], [383, 384, 385, 767, 769]),
+    "chunk ends, wide rows": (6, 33, 4, 4, 128, 64, 4, [33, 32, 31, 16, 8, 1], [63, 64, 65, 127, 128, 129]),
+    "one token, 64 rows of a head": (2, 1, 64, 1, 128, 64, 4, [1, 1], [700, 1]),
+    "five rows of a head, small pages": (3, 5, 15, 3, 64, 64, 8, [5, 4, 5], [65, 640, 0]),
+}
+
+
+@pytest.mark.parametrize("name", MORE)
+def test_attention_at_the_ends_of_chunks(name):
+    s, st = make(*MORE[name], seed=11), _status()
+    o = call(s, st)
+    assert int(st) == 0
+    check(o, s)
+    lens = s["np"][2]
+    for b in range(len(lens)):
+        assert (o[b, int(lens[b]):] == 0).all()
+
+
+def _shifted(t):
+    """The same tensor 16 bytes behind a 32-byte boundary."""
+    flat = torch.empty(t.numel() + 16, dtype=t.dtype, device=DEV)
+    at = 8 if flat.data_ptr() % 32 == 0 else 0
+    u = flat[at:at + t.numel()].view(t.shape)
+    u.copy_(t)
+    assert u.data_ptr() % 32 == 16
+    return u
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_tensors_on_16_byte_boundaries(bits):
+    """Sources and outputs that 32-byte accesses do not fit give the same bytes."""
+    rd, rng = _rd(), np.random.default_rng(bits)
+    Hkv, D, page, T = 3, 64, 64, 100
+    k, v = (_bf(rng.standard_normal((T, Hkv, D))) for _ in range(2))
+    cu, ctx, table = _d(np.array([0, 40, T], np.int32)), _d(np.array([30, 0], np.int32)), _d(np.array([[0, 1], [2, 3]], np.int32))
+    pools = [[torch.zeros(4, page, Hkv, oq.row_bytes(D, bits), dtype=torch.uint8, device=DEV) for _ in range(2)]
+             for _ in range(3)]
+    rd.rd_append_quant(k, v, cu, *pools[0], 0.5, 0.25, table, ctx)
+    rd.rd_append_quant(_shifted(k), _shifted(v), cu, *pools[1], 0.5, 0.25, table, ctx)
+    rd.rd_append_quant(_shifted(k), v, cu, *pools[2], 0.5, 0.25, table, ctx)
+    for other in pools[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(pools[0], other))
+    off = _d(np.array([0, 40, T], np.int64))
+    want = rd.rd_read_quant(*pools[0], 0.5, 0.25, table, off, total=T, starts=ctx)
+    out = [_shifted(torch.zeros_like(k)), torch.zeros_like(v)]
+    rd.rd_read_quant(*pools[0], 0.5, 0.25, table, off, total=T, starts=ctx, k_out=out[0], v_out=out[1])
+    assert all(torch.equal(a, b) for a, b in zip(want, out))
+    unp, best, acc = _d(np.arange(8, dtype=np.int32).reshape(2, 1, 4)), _d(np.zeros(2, np.int32)), _d(np.array([3, 1], np.int32))
+    kn, vn = (_bf(rng.standard_normal((2, 8, Hkv, D))) for _ in range(2))
+    rd.rd_commit_accepted_quant(kn, vn, unp, best, acc, *pools[0], 0.5, 0.25, table, ctx)
+    rd.rd_commit_accepted_quant(_shifted(kn), _shifted(vn), unp, best, acc, *pools[1], 0.5, 0.25, table, ctx)
+    assert all(torch.equal(a, b) for a, b in zip(pools[0], pools[1]))

@@ -3,7 +3,7 @@
 //
 // One pass over each row.  In units of log2, with c = log2(e) / T and a reference m,
 //   z = c (x - m),  l = sum 2^z,  w = sum 2^z (x - m):
-//   log p(x_t) = ln 2 (z_t - log2 l),   H = ln 2 (log2 l - c w / l).
+//   log p(x_t) = (x_t - m) / T - ln 2 log2 l,   H = ln 2 (log2 l - c w / l).
 // The reference is the maximum of the CTA's first 16,384 logits; a thread that meets a larger one
 // moves its own.  So a logit costs a difference, a product, an exponential and two accumulations:
 // about 50 instructions for eight 16-bit logits, somewhat more than half of what the SM can
@@ -44,7 +44,7 @@ struct Args {
     int W, L, P;
     int64_t n, rows_total;
     int V, k;
-    float c;                               // log2(e) / T
+    float T, c;                            // temperature, log2(e) / T
     float *logprob, *entropy;
     int32_t* top;
     float* top_logprob;
@@ -583,13 +583,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     const float lg = log2f(all.l);
     const float m = all.m == -INFINITY ? 0.f : all.m;
     if (tid == 0) {
-        a.logprob[n] = kLn2 * ((chosen - m) * a.c - lg);
+        a.logprob[n] = (chosen - m) / a.T - kLn2 * lg;
         a.entropy[n] = kLn2 * (lg - all.w / all.l * a.c);
     }
     if (tid < k) {
         const unsigned long long key = sh.best[tid];
         a.top[n * k + tid] = (int32_t)~(uint32_t)key;
-        a.top_logprob[n * k + tid] = kLn2 * ((number((uint32_t)(key >> 32)) - m) * a.c - lg);
+        a.top_logprob[n * k + tid] = (number((uint32_t)(key >> 32)) - m) / a.T - kLn2 * lg;
     }
 }
 
@@ -632,6 +632,7 @@ cudaError_t rd_launch_logprobs(const rd_logprobs& q, cudaStream_t stream)
     a.rows_total = q.n_rows;
     a.V = q.V;
     a.k = q.top;
+    a.T = q.temperature;
     a.c = 1.4426950408889634f / q.temperature;
     a.logprob = q.logprob;
     a.entropy = q.entropy;
