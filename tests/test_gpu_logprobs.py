@@ -266,3 +266,15 @@ def test_one_nan_anywhere(dtype):
     out = rd.rd_token_logprobs(x, _i32([9] * 6), top=2)
     assert torch.isnan(out["logprob"][:5]).all() and torch.isnan(out["entropy"][:5]).all()
     check(out, 5, x[5], 9, 1.0, 2)
+
+
+@pytest.mark.parametrize("size", [1e36, 1e28, 1e-28, 2e-38])
+def test_very_large_and_small_temperatures(size):
+    """Logits of the temperature's size: sums of differences would leave 32 bits."""
+    rd = _rd()
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = (3 * torch.randn(2, 50000, generator=gen, device=DEV).double() * size).float()
+    T = float(np.float32(size))
+    out = rd.rd_token_logprobs(x, _i32([7, 49999]), top=3, temperature=T)
+    check(out, 0, x[0], 7, T, 3)
+    check(out, 1, x[1], 49999, T, 3)

@@ -145,3 +145,7 @@ def test_binding_checks_shapes(monkeypatch):
     with pytest.raises(ValueError):
         rd.rd_read_quant(pool, pool, 1.0, 1.0, z(4, 3), z(4), total=3)
     assert runs == ["rd_append_quant"]
+
+
+def test_append_refuses_lengths_in_place():
+    assert call("rd_append_quant", ctx=ONE, new=ONE) == rd.RD_ERR_INVALID_ARG

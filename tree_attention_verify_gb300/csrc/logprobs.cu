@@ -2,8 +2,8 @@
 // log p(token), the entropy H = -sum p log p, and the k most likely tokens.
 //
 // One pass over each row.  In units of log2, with c = log2(e) / T and a reference m,
-//   z = c (x - m),  l = sum 2^z,  w = sum 2^z (x - m):
-//   log p(x_t) = (x_t - m) / T - ln 2 log2 l,   H = ln 2 (log2 l - c w / l).
+//   z = c (x - m),  l = sum 2^z,  w = sum 2^z z:
+//   log p(x_t) = (x_t - m) / T - ln 2 log2 l,   H = ln 2 (log2 l - w / l).
 // The reference is the maximum of the CTA's first 16,384 logits; a thread that meets a larger one
 // moves its own.  So a logit costs a difference, a product, an exponential and two accumulations:
 // about 50 instructions for eight 16-bit logits, somewhat more than half of what the SM can
@@ -44,7 +44,7 @@ struct Args {
     int W, L, P;
     int64_t n, rows_total;
     int V, k;
-    float T, c;                            // temperature, log2(e) / T
+    float T, c, off;                       // temperature, log2(e) / T, and what c is short of, relative
     float *logprob, *entropy;
     int32_t* top;
     float* top_logprob;
@@ -98,7 +98,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 
 // ------------------------------------------------------------------ 16 bytes of logits
 // The fast way takes logits below kLow as that, and references between -1e38 and 1e30: differences
-// are finite, and those of such logits have no weight.
+// are finite, and those of such logits have no weight.  It sums 2^z (x - m), at most 150 / c each,
+// and for c between 1e-27 and 1e27 2^30 of them stay within the range.
 constexpr float kLow = -3.0e38f;
 
 template <typename T>
@@ -210,14 +211,15 @@ struct Stats {
     __device__ __forceinline__ void move(float to, float c)       // to another reference
     {
         if (m != -INFINITY) {
-            const float d = m - to, f = exp2_(d * c);
-            w = f * (w + d * l);
+            const float z = (m - to) * c, f = exp2_(z);
+            w = f * (w + z * l);
             l *= f;
             if (f == 0.f) w = 0.f;
         }
         m = to;
     }
-    __device__ __forceinline__ void add(float2 ls, float2 ws) { l += ls.x + ls.y, w += ws.x + ws.y; }
+    // (sums of 2^z and 2^z (x - m))
+    __device__ __forceinline__ void add(float2 ls, float2 ws, float c) { l += ls.x + ls.y, w = fmaf(ws.x + ws.y, c, w); }
 };
 
 struct Shared {
@@ -323,9 +325,9 @@ __device__ __noinline__ void add_slowly(Stats& s, uint4 u, float top, float c)
     float v[N];
     Vec<T>::unpack(u, v);
     for (int e = 0; e < N; ++e) {
-        const float d = v[e] - s.m, p = exp2_(max_nan(d * c, -200.f));
+        const float z = max_nan((v[e] - s.m) * c, -200.f), p = exp2_(z);
         s.l += p;
-        if (p != 0.f) s.w = fmaf(p, d, s.w);
+        s.w = fmaf(p, z, s.w);
     }
 }
 
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             for (int w = 0; w < kWarps; ++w) most = max(most, __float_as_uint(sh.warp[w].m));
             s.m = number(most);
             floor_ = s.m;
-            fast = s.m > -1e38f && s.m < 1e30f && a.c > 1e-30f;
+            fast = s.m > -1e38f && s.m < 1e30f && a.c > 1e-27f && a.c < 1e27f;
             if (k > 0) {
                 // the k-th largest of the threads' maxima, rounded down to 16 bits
                 uint32_t at = 0;
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
                 const int g = g0 + j * kThreads + tid;
                 if (k > 0 && g < inside1) keep(sh, g, u[j]);
                 if (fast && !(top <= s.m)) {
-                    s.add(both(l2), both(w2));
+                    s.add(both(l2), both(w2), a.c);
                     l2 = w2 = 0;
                     s.move(top, a.c);
                     fast = top < 1e30f;
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             }
         }
     }
-    s.add(both(l2), both(w2));
+    s.add(both(l2), both(w2), a.c);
     // the row's first and last group, where they are partly outside
     if (tid < 2) {
         const int g = tid == 0 ? row.first : row.last - 1;
@@ -581,15 +583,17 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         }
     }
     const float lg = log2f(all.l);
+    // a c that is off by `off` moves log l by the mean of z: to log p, where differences are over T itself, it is given back
+    const float ln_l = kLn2 * fmaf(a.off, all.w / all.l, lg);
     const float m = all.m == -INFINITY ? 0.f : all.m;
     if (tid == 0) {
-        a.logprob[n] = (chosen - m) / a.T - kLn2 * lg;
-        a.entropy[n] = kLn2 * (lg - all.w / all.l * a.c);
+        a.logprob[n] = (chosen - m) / a.T - ln_l;
+        a.entropy[n] = kLn2 * (lg - all.w / all.l);
     }
     if (tid < k) {
         const unsigned long long key = sh.best[tid];
         a.top[n * k + tid] = (int32_t)~(uint32_t)key;
-        a.top_logprob[n * k + tid] = (number((uint32_t)(key >> 32)) - m) / a.T - kLn2 * lg;
+        a.top_logprob[n * k + tid] = (number((uint32_t)(key >> 32)) - m) / a.T - ln_l;
     }
 }
 
@@ -633,7 +637,9 @@ cudaError_t rd_launch_logprobs(const rd_logprobs& q, cudaStream_t stream)
     a.V = q.V;
     a.k = q.top;
     a.T = q.temperature;
-    a.c = 1.4426950408889634f / q.temperature;
+    const double c = 1.4426950408889634 / q.temperature;
+    a.c = (float)c;
+    a.off = (float)((c - a.c) / c);
     a.logprob = q.logprob;
     a.entropy = q.entropy;
     a.top = q.top_tokens;

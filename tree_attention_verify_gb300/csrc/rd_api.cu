@@ -546,6 +546,7 @@ rd_status rd_append_quant(int B, int Hkv, int D, int bits, const void* k, const 
     if (!cu_seqlens || !ctx_lens || !new_ctx_lens || (max_pages > 0 && !block_table) || (total_tokens > 0 && (!k || !v)) ||
         (num_pages > 0 && (!k_pool || !v_pool)))
         return RD_ERR_INVALID_ARG;
+    if (ctx_lens == new_ctx_lens) return RD_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool)) return RD_ERR_INVALID_ARG;
     return from_cuda(rd_launch_append_quant(
         quant_kv(k_pool, v_pool, k_scale, v_scale, bits, num_pages, page_size, block_table, max_pages, nullptr), B, Hkv, D, k,
