@@ -278,3 +278,26 @@ def test_very_large_and_small_temperatures(size):
     out = rd.rd_token_logprobs(x, _i32([7, 49999]), top=3, temperature=T)
     check(out, 0, x[0], 7, T, 3)
     check(out, 1, x[1], 49999, T, 3)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [538, 40000, 128256])
+def test_a_token_with_nearly_all_of_the_probability(V, dtype):
+    """log p = -log(1 + l) with l the sum of the other weights: as exact, relative to itself, as l.  Each weight
+    is off by its exponent's roundings (|z| up to 64, 2 x 2^-24 of it) and the hardware's 2^x (2^-21), the sum by
+    a rounding a term of a thread and of the joins."""
+    rd = _rd()
+    gen = torch.Generator(device=DEV).manual_seed(V)
+    x = torch.randn(6, V, generator=gen, device=DEV).clamp(-4, 4)
+    for i, (at, top) in enumerate(((0, 14.0), (V - 1, 20.0), (300, 24.0), (V // 2, 31.0), (7, 38.0), (V - 9, 9.0))):
+        x[i, at] = top
+    x = x.to(TYPES[dtype])
+    tokens = x.float().argmax(1).int()
+    out = rd.rd_token_logprobs(x, tokens, top=1)
+    want = x.double()
+    others = torch.exp(want - want.amax(1, keepdim=True))
+    others.scatter_(1, tokens.long()[:, None], 0.0)
+    want = -torch.log1p(others.sum(1))
+    eps = (V / 256 + 60) * 2.0 ** -24 + 64 * 0.7 * 2.0 ** -23 + 2.0 ** -21
+    assert ((out["logprob"].double() - want).abs() <= eps * want.abs()).all(), (out["logprob"], want)
+    assert torch.equal(out["top_logprobs"][:, 0], out["logprob"])

@@ -3,7 +3,7 @@
 //
 // One pass over each row.  In units of log2, with c = log2(e) / T and a reference m,
 //   z = c (x - m),  l = sum 2^z,  w = sum 2^z z:
-//   log p(x_t) = (x_t - m) / T - ln 2 log2 l,   H = ln 2 (log2 l - w / l).
+//   log p(x_t) = (x_t - m) / T - ln l,   H = ln l - ln 2 w / l.
 // The reference is the maximum of the CTA's first 16,384 logits; a thread that meets a larger one
 // moves its own.  So a logit costs a difference, a product, an exponential and two accumulations:
 // about 50 instructions for eight 16-bit logits, somewhat more than half of what the SM can
@@ -207,15 +207,18 @@ __device__ __forceinline__ unsigned long long key_of(float x, int i)
 }
 
 struct Stats {
-    float m, l, w;                         // reference (a logit; -inf: nothing yet), sums
+    // Reference (a logit; -inf: nothing yet), sums of the others, and how many stand at the reference: where one token has
+    // nearly all of the probability, log l is that of 1 + l, and nothing of l is lost beside the 1.
+    float m, l, w, ones;
     __device__ __forceinline__ void move(float to, float c)       // to another reference
     {
         if (m != -INFINITY) {
-            const float z = (m - to) * c, f = exp2_(z);
-            w = f * (w + z * l);
-            l *= f;
+            const float z = (m - to) * c, f = exp2_(z), all = l + ones;
+            w = f * (w + z * all);
+            l = f * all;
             if (f == 0.f) w = 0.f;
         }
+        ones = 0.f;
         m = to;
     }
     // (sums of 2^z and 2^z (x - m))
@@ -314,21 +317,27 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& row, int g, uint4
     }
 }
 
-// One group after the other, for rows where the fast way would not do: references near the lowest
-// number, extreme temperatures.  2^-200 is 0, and 0 x -200 too: a logit of -inf adds nothing.
+// One group after the other: the one with the reference itself, and all of rows where the fast way would not do
+// (references near the lowest number, extreme temperatures).  2^-200 is 0, and 0 x -200 too: a logit of -inf
+// adds nothing.
 template <typename T>
-__device__ __noinline__ void add_slowly(Stats& s, uint4 u, float top, float c)
+__device__ __noinline__ Stats add_slowly(Stats s, uint4 u, float top, float c)
 {
     constexpr int N = Vec<T>::n;
-    if (top == -INFINITY) return;
+    if (top == -INFINITY) return s;
     if (!(top <= s.m)) s.move(top, c);
     float v[N];
     Vec<T>::unpack(u, v);
     for (int e = 0; e < N; ++e) {
-        const float z = max_nan((v[e] - s.m) * c, -200.f), p = exp2_(z);
-        s.l += p;
-        s.w = fmaf(p, z, s.w);
+        const float d = v[e] - s.m, z = max_nan(d * c, -200.f), p = exp2_(z);
+        if (d == 0.f) {
+            s.ones += 1.f;
+        } else {
+            s.l += p;
+            s.w = fmaf(p, z, s.w);
+        }
     }
+    return s;
 }
 
 // One warp: sh.list[0 .. n) -> sh.best, the keys of rank below k, in order.  The k-th largest upper
@@ -374,6 +383,7 @@ __device__ __forceinline__ Stats join_warp(Stats s, float c)
     for (int o = 16; o > 0; o >>= 1) {
         s.l += __shfl_xor_sync(0xffffffffu, s.l, o);
         s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+        s.ones += __shfl_xor_sync(0xffffffffu, s.ones, o);
     }
     return s;
 }
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     const Row<T> row(x, a.V, part, parts);
     const float chosen = part == 0 && tid == 0 ? Vec<T>::one(x, token) : 0.f;
     if (tid == 0) sh.count = sh.groups = 0;
-    Stats s = {-INFINITY, 0.f, 0.f};
+    Stats s = {-INFINITY, 0.f, 0.f, 0.f};
     uint64_t l2 = 0, w2 = 0;               // (two chains of sums each, of the reference s.m)
     const uint64_t c2 = pair(a.c, a.c);
     unsigned long long least = 0;
@@ -485,15 +495,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             if (!(top < floor_)) {
                 const int g = g0 + j * kThreads + tid;
                 if (k > 0 && g < inside1) keep(sh, g, u[j]);
-                if (fast && !(top <= s.m)) {
-                    s.add(both(l2), both(w2), a.c);
-                    l2 = w2 = 0;
-                    s.move(top, a.c);
-                    fast = top < 1e30f;
+                if (fast && !(top < s.m)) {
+                    if (top != s.m) {
+                        s.add(both(l2), both(w2), a.c);
+                        l2 = w2 = 0;
+                        fast = top < 1e30f;
+                    }
+                    s = add_slowly<T>(s, u[j], top, a.c);
+                    continue;
                 }
             }
             if (!fast) {
-                add_slowly<T>(s, u[j], top, a.c);
+                s = add_slowly<T>(s, u[j], top, a.c);
                 continue;
             }
             float v[N];
@@ -516,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             const uint4 u = row.edge(g);
             const float top = Vec<T>::top(u);
             if (k > 0 && !(top < floor_)) keep(sh, g, u);
-            add_slowly<T>(s, u, top, a.c);
+            s = add_slowly<T>(s, u, top, a.c);
         }
     }
     __syncthreads();                       // (sh.warp is read above and written below; the groups are there)
@@ -551,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         }
         if (warp == 0) rank(sh, sh.count, k);
     }
-    Stats all = {-INFINITY, 0.f, 0.f};     // (in the first warp)
+    Stats all = {-INFINITY, 0.f, 0.f, 0.f};     // (in the first warp)
     if (warp == 0) {
         if (lane < kWarps) all = sh.warp[lane];
         all = join_warp(all, a.c);
@@ -564,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         cluster.sync();
         if (part != 0) return;
         if (warp == 0) {
-            all = {-INFINITY, 0.f, 0.f};
+            all = {-INFINITY, 0.f, 0.f, 0.f};
             if (lane < parts) all = sh.part[lane];
             all = join_warp(all, a.c);
         }
@@ -582,18 +595,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             __syncthreads();
         }
     }
-    const float lg = log2f(all.l);
-    // a c that is off by `off` moves log l by the mean of z: to log p, where differences are over T itself, it is given back
-    const float ln_l = kLn2 * fmaf(a.off, all.w / all.l, lg);
+    const float l = all.l + all.ones, mean = kLn2 * (all.w / l);          // of (x - m) / T
+    const float ln_l = all.ones > 0.f ? logf(all.ones) + log1pf(all.l / all.ones) : logf(l);
+    // A c that is off by `off` moves log l by as much of the mean: for log p, whose difference is over T itself, it is given back.
+    const float ln_p = fmaf(a.off, mean, ln_l);
     const float m = all.m == -INFINITY ? 0.f : all.m;
     if (tid == 0) {
-        a.logprob[n] = (chosen - m) / a.T - ln_l;
-        a.entropy[n] = kLn2 * (lg - all.w / all.l);
+        a.logprob[n] = (chosen - m) / a.T - ln_p;
+        a.entropy[n] = ln_l - mean;
     }
     if (tid < k) {
         const unsigned long long key = sh.best[tid];
         a.top[n * k + tid] = (int32_t)~(uint32_t)key;
-        a.top_logprob[n * k + tid] = (number((uint32_t)(key >> 32)) - m) / a.T - ln_l;
+        a.top_logprob[n * k + tid] = (number((uint32_t)(key >> 32)) - m) / a.T - ln_p;
     }
 }
 
