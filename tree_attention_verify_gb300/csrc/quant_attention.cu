@@ -960,20 +960,15 @@ __global__ void __launch_bounds__(threads_of(D), 1) quant_attention_kernel(const
     }
 }
 
-// o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the pieces of a cut unit.  A few long contexts
-// leave a few units of many pieces, so a CTA takes single rows of one head, and its threads
-// share the pieces (with one CTA for a head's rows and a thread for all pieces of its columns, two contexts of 40,000 with
-// 32 rows a head spent 90 of 132 us here).
-constexpr int kMergeThreads = 128, kMergeRows = 8;     // CTAs along a head's rows, at most
-constexpr int kMostPieces = 512;           // whose factors fit; more CTAs than any SM count
+// o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the pieces of a cut unit.  A warp takes a row of
+// one head, so that a few units of many pieces (long contexts) keep as many warps busy as they have rows (with one CTA
+// for a head's rows, two contexts of 40,000 with 32 rows a head spent 90 of 132 us here).
+constexpr int kMergeWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) quant_merge_kernel(const Args a)
+__global__ void __launch_bounds__(32 * kMergeWarps) quant_merge_kernel(const Args a)
 {
-    constexpr int kCols = D / 4, kShares = kMergeThreads / kCols;
-    __shared__ float factor[kMostPieces];
-    __shared__ float4 share[kShares][kCols];
-    __shared__ float total;
+    constexpr int kCols = D / 4, kShares = 32 / kCols;     // D = 64: two halves of the pieces
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 unit = a.desc[blockIdx.x];
     const int first = blockIdx.x, last = unit.z;
@@ -984,49 +979,48 @@ __global__ void __launch_bounds__(kMergeThreads) quant_merge_kernel(const Args a
     s.len = len;
     const int groups = s.groups(a), hg = unit.y / groups, r0 = unit.y % groups * s.per(a);
     const int rows = min(s.per(a), s.rows(a) - r0), h = hg * a.heads + blockIdx.y, n = last - first + 1;
-    const int c = threadIdx.x % kCols, mine = threadIdx.x / kCols, lane = threadIdx.x & 31;
-    for (int r = blockIdx.z; r < rows; r += gridDim.z) {
+    const int lane = threadIdx.x & 31, c = lane % kCols, share = lane / kCols;
+    for (int r = blockIdx.z * kMergeWarps + (threadIdx.x >> 5); r < rows; r += gridDim.z * kMergeWarps) {
         auto at = [&](int k) { return (((size_t)2 * (first + k) + (k == 0 ? 1 : 0)) * a.heads + blockIdx.y) * a.unit_rows + r; };
-        if (threadIdx.x < 32) {
-            float M = -INFINITY, L = 0.f;
-            for (int k = lane; k < n; k += 32) M = fmaxf(M, a.part_ml[at(k)].x);
+        float M = -INFINITY, L = 0.f;
+        for (int k = lane; k < n; k += 32) M = fmaxf(M, a.part_ml[at(k)].x);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float mu = M == -INFINITY ? 0.f : M;
-            for (int k = lane; k < n; k += 32) {
-                const float2 ml = a.part_ml[at(k)];
-                const float f = fast_exp2(ml.x - mu);
-                factor[k] = f;
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float mu = M == -INFINITY ? 0.f : M;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            float f = 0.f;
+            if (k0 + lane < n) {
+                const float2 ml = a.part_ml[at(k0 + lane)];
+                f = fast_exp2(ml.x - mu);
                 L += f * ml.y;
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (lane == 0) total = L;
-        }
-        __syncthreads();
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int some = min(32, n - k0);
 #pragma unroll 8
-        for (int k = mine; k < n; k += kShares) {
-            const float4 v = reinterpret_cast<const float4*>(a.part)[at(k) * kCols + c];
-            const float f = factor[k];
-            o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
-        }
-        share[mine][c] = o;
-        __syncthreads();
-        if (mine == 0) {
-#pragma unroll
-            for (int i = 1; i < kShares; ++i) {
-                const float4 v = share[i][c];
-                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            for (int k = 0; k < some; k += kShares) {
+                const float by = __shfl_sync(0xffffffffu, f, (k + share) & 31);
+                if (k + share < some) {
+                    const float4 v = reinterpret_cast<const float4*>(a.part)[at(k0 + k + share) * kCols + c];
+                    o.x += by * v.x, o.y += by * v.y, o.z += by * v.z, o.w += by * v.w;
+                }
             }
-            const float L = total, f = L == 0.f ? 0.f : 1.f / L;
-            const int row = r0 + r;
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+        if constexpr (kShares == 2) {
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+        }
+        const float f = L == 0.f ? 0.f : 1.f / L;
+        const int row = r0 + r;
+        if (share == 0) {
             uint2 out;
             out.x = pack_bf16(o.x * f, o.y * f);
             out.y = pack_bf16(o.z * f, o.w * f);
             reinterpret_cast<uint2*>(a.o)[((((size_t)unit.x * a.P + row / a.G) * a.Hq + (size_t)h * a.G + row % a.G) * D) / 4 + c] = out;
         }
-        __syncthreads();                   // (total, the shares and the factors are read)
     }
 }
 
@@ -1102,9 +1096,9 @@ template <int D>
 cudaError_t launch_merge(const Args& a, int grid, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
-    const long long rows = (long long)a.P * a.G;
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)a.heads, (unsigned)(rows < kMergeRows ? rows : kMergeRows));
-    cfg.blockDim = dim3(kMergeThreads);
+    const long long rows = (long long)a.P * a.G < a.unit_rows ? (long long)a.P * a.G : a.unit_rows;
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)a.heads, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps));
+    cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1129,7 +1123,6 @@ cudaError_t rd_launch_quant_attention(const rd_quant_kv& kv, int B, int P_max, i
                                       void* workspace, int32_t* dev_status, cudaStream_t stream)
 {
     const int grid = rd_device_sm_count();
-    if (grid > kMostPieces) return cudaErrorInvalidConfiguration;
     Args a = {};
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.k_new = static_cast<const __nv_bfloat16*>(k_new);
