@@ -889,6 +889,21 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
         }
 }
 
+// The unit that this CTA's range begins and does not end, for the merge: and the CTA that has its last chunk.
+__device__ __forceinline__ void describe(const Args& a, const Division& d)
+{
+    int4 unit = make_int4(-1, 0, 0, 0);
+    Walk walk = Walk::over(a, d);
+    Piece p;
+    while (walk.next(a, p)) {
+        if (p.j0 != 0 || p.j1 >= p.n(a)) continue;
+        const Shape s = shape_of(a, p.b);
+        const uint64_t last = walk.S + (uint64_t)p.unit * s.unit_cost(a) + a.unit_cost + (uint64_t)(p.n(a) - 1) * s.chunk_cost(a);
+        unit = make_int4(p.b, p.unit, (int)d.of(last), 0);
+    }
+    if ((threadIdx.x & 31) == 0) a.desc[blockIdx.x] = unit;
+}
+
 template <int D, int BITS>
 __global__ void __launch_bounds__(threads_of(D), 1) quant_attention_kernel(const __grid_constant__ Args a)
 {
@@ -920,6 +935,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) quant_attention_kernel(const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(load_regs(D)));
         if (!a.tiled) load_rowwise<D, BITS>(a, sh, buf.ring, d);
         else if (warp == warps_of(D)) load_tiled<D, BITS>(a, sh, buf.ring, d);
+        if (warp == warps_of(D)) describe(a, d);       // (now, so that its code is not fetched beside that of the first chunks)
         clear_rows<D>(a);
         return;
     }
@@ -940,18 +956,10 @@ __global__ void __launch_bounds__(threads_of(D), 1) quant_attention_kernel(const
             rd_flag(a.status, RD_DEV_TIMEOUT);
         }
     }
-    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     Walk walk = Walk::over(a, d);
     Piece p;
     Turn at = {0, 0};
     while (walk.next(a, p)) {
-        if (threadIdx.x == 0 && p.j0 == 0 && p.j1 < p.n(a)) {
-            // the CTA that has the unit's last chunk
-            const Shape s = shape_of(a, p.b);
-            const uint64_t last = walk.S + (uint64_t)p.unit * s.unit_cost(a) + a.unit_cost +
-                                  (uint64_t)(p.n(a) - 1) * s.chunk_cost(a);
-            a.desc[blockIdx.x] = make_int4(p.b, p.unit, (int)d.of(last), 0);
-        }
         const int tiles = (p.rows + 7) / 8;
         if (tiles == 1) piece<D, BITS, 1>(a, sh, buf, w, p, at, alive);
         else if (tiles == 2) piece<D, BITS, 2>(a, sh, buf, w, p, at, alive);

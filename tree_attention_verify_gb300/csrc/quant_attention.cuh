@@ -99,17 +99,18 @@ struct Division {
     uint32_t n;                // CTAs that work
     int b;                     // the request in which this CTA's range begins
     uint64_t S;                // cost of the requests before it
-    __device__ __forceinline__ uint64_t begin(uint32_t c) const
-    {
-        // floor(c W / n) without leaving 64 bits
-        return (W / n) * c + (W % n) * c / n;
-    }
+    uint64_t each;             // floor(W / n): the first W mod n ranges have one more
+    uint32_t rest;
+    __device__ __forceinline__ uint64_t begin(uint32_t c) const { return each * c + min(c, rest); }
     __device__ __forceinline__ uint32_t of(uint64_t x) const      // the CTA whose range holds x
     {
-        uint32_t c = (uint32_t)min((uint64_t)(n - 1), x / max((uint64_t)1, W / n));
-        while (c > 0 && begin(c) > x) --c;
-        while (c + 1 < n && begin(c + 1) <= x) ++c;
-        return c;
+        uint32_t lo = 0, hi = n;
+        while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) / 2;
+            if (begin(mid) <= x) lo = mid;
+            else hi = mid;
+        }
+        return lo;
     }
 };
 
@@ -144,7 +145,15 @@ struct Walk {
             if (s.len != 0) {
                 const uint32_t uc = s.unit_cost(a), c = s.chunk_cost(a);
                 const int groups = s.groups(a), units = groups * (a.Hkv / a.heads);
-                if (unit < 0) unit = lo > S ? (int)((lo - S) / uc) : 0;
+                if (unit < 0) {
+                    unit = 0;
+                    if (lo > S) {          // (lo - S) / uc, below 2^22, from a quotient that is off by one at most
+                        const uint64_t x = lo - S;
+                        unit = (int)__fdividef((float)x, (float)uc);
+                        if ((uint64_t)unit * uc > x) --unit;
+                        else if ((uint64_t)(unit + 1) * uc <= x) ++unit;
+                    }
+                }
                 while (unit < units) {
                     const uint64_t at = S + (uint64_t)unit * uc, first = at + a.unit_cost;
                     if (at >= hi) return false;
@@ -198,8 +207,10 @@ __device__ __forceinline__ Division divide(const Args& a, DivisionShared& sh)
     Division d;
     d.W = 0;
     for (int w = 0; w < kThreads / 32; ++w) d.W += sh.sum[w];
-    const uint64_t most = d.W / a.least_cost;
-    d.n = (uint32_t)(most < 1 ? 1 : (most < gridDim.x ? most : gridDim.x));
+    d.n = gridDim.x;
+    if (d.W < (uint64_t)gridDim.x * a.least_cost) d.n = max(1u, (uint32_t)d.W / a.least_cost);
+    d.each = d.W / d.n;
+    d.rest = (uint32_t)(d.W - d.each * d.n);
     d.b = a.B;
     d.S = 0;
     __syncthreads();
