@@ -8,7 +8,8 @@
 // moves its own.  So a logit costs a difference, a product, an exponential and two accumulations:
 // about 50 instructions for eight 16-bit logits, somewhat more than half of what the SM can
 // issue while HBM delivers them.  What is rare (a larger maximum, a candidate, numbers at the ends of
-// the range) stays out of the loop's way.
+// the range) stays out of the loop's way.  4,096 rows of 128,256 bf16 logits with 20 alternatives
+// take 227 us (4.6 TB/s; 40,000 instructions a row, whose loads' latency is not hidden all of the time).
 //
 // The top k come from the same pass: a threshold that at least k logits of the row reach
 // is known after the first 64 logits of each thread (the k-th largest of the threads'

@@ -16,10 +16,13 @@
 // of a row of K (one block, one scale) as its share of four steps, and V's columns are dealt
 // so that a thread owns 16 consecutive ones: its loads are whole blocks and its outputs whole
 // 16-byte words.  Rows are the products' short side: 8 at a time, so that five rows cost a
-// quarter of what 32 do.  The matrix unit takes one of these products every two cycles: 862 of the
-// 1,208 us that 64 contexts of 8,192 with 41 nodes and 40 heads take (2.5 TB/s of codes), so it,
-// then the widening beside it, bounds calls of many rows; calls of a few rows by one pass through the code (7,000
-// cycles the first time) and the unit's start and end.
+// quarter of what 32 do.
+//
+// 64 contexts of 8,192 with 23 nodes of 48 and 40 heads take 1,123 us (2.7 TB/s of codes): the matrix
+// unit, one of these products every two cycles, is busy for 490 of them, and the 8 warps that the registers leave room
+// for do not hide each other's chains (code to float, product, exponential, product) any better.
+// Calls of a few rows take 20 us and more before their first chunk is done: a CTA's first pass
+// through 30 KB of code costs as much as fetching it.
 #include "quant_attention.cuh"
 
 namespace {
