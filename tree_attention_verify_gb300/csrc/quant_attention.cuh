@@ -53,7 +53,7 @@ struct Args {
 // they cost, and the CTAs take equal ranges of it.  Widening a chunk costs the same for any number
 // of rows (chunk_cost), its products go with them (step_cost for each row_step rows); a unit's start and
 // end take as long as a few chunks (unit_cost).  A range is at least least_cost, more than any
-// chunk.  (A unit of 2^31 positions in chunks of 32 costs less than 2^31.)
+// chunk.  (A unit of 2^31 positions in chunks of 32 costs less than 2^32.)
 struct Shape {
     int len, C;                // nodes (0: the request is skipped or has none), context
     __device__ __forceinline__ int rows(const Args& a) const { return len * a.G; }
