@@ -1007,12 +1007,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps) quant_merge_kernel(const Arg
                 L += f * ml.y;
             }
             const int some = min(32, n - k0);
-#pragma unroll 8
-            for (int k = 0; k < some; k += kShares) {
-                const float by = __shfl_sync(0xffffffffu, f, (k + share) & 31);
-                if (k + share < some) {
-                    const float4 v = reinterpret_cast<const float4*>(a.part)[at(k0 + k + share) * kCols + c];
-                    o.x += by * v.x, o.y += by * v.y, o.z += by * v.z, o.w += by * v.w;
+            for (int k1 = 0; k1 < some; k1 += 8) {         // (eight pieces' loads under way together)
+                float4 v[8 / kShares];
+#pragma unroll
+                for (int i = 0; i < 8 / kShares; ++i) {
+                    const int k = k1 + i * kShares + share;
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < some) v[i] = reinterpret_cast<const float4*>(a.part)[at(k0 + k) * kCols + c];
+                }
+#pragma unroll
+                for (int i = 0; i < 8 / kShares; ++i) {
+                    const float by = __shfl_sync(0xffffffffu, f, k1 + i * kShares + share);      // (0 behind the last)
+                    o.x += by * v[i].x, o.y += by * v[i].y, o.z += by * v[i].z, o.w += by * v[i].w;
                 }
             }
         }
