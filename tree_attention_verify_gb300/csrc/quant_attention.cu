@@ -1064,10 +1064,11 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     a.unit_rows = rows_of(D);
     a.row_step = 8;
     // (cycles of 64 positions x 4 heads, D = 128: 3,050 with 16 rows, 3,600 with 24, 4,700 with 32; a unit's
-    // start and end 18,000)
+    // start and end 18,000.  Two contexts of 40,000 with 24 rows a head: 61 us with 120, 58 with 180, 55 with 240; 16 x 40 nodes
+    // on 32/8 heads 86, 84 and 87.)
     a.chunk_cost = 16;
     a.step_cost = 5;
-    a.unit_cost = 120;
+    a.unit_cost = 180 * 2 / tiles_of(D, BITS);              // (chunks of half the positions)
     a.least_cost = 72;
     a.seg = a.heads * rdquant::row_bytes(D, BITS);
     a.pitch = pitch_of(a.seg, BITS);
