@@ -709,3 +709,14 @@ def test_tensors_on_16_byte_boundaries(bits):
     rd.rd_commit_accepted_quant(kn, vn, unp, best, acc, *pools[0], 0.5, 0.25, table, ctx)
     rd.rd_commit_accepted_quant(_shifted(kn), _shifted(vn), unp, best, acc, *pools[1], 0.5, 0.25, table, ctx)
     assert all(torch.equal(a, b) for a, b in zip(pools[0], pools[1]))
+
+
+@pytest.mark.parametrize("case", [(1, 5, 8, 4, 64, 64, 4, [5], [40000]), (1, 24, 4, 4, 128, 64, 4, [24], [30001]),
+                                  (2, 3, 4, 2, 128, 128, 8, [3, 1], [20000, 0]), (3, 4, 4, 4, 64, 64, 8, [4, 1, 2], [9000, 1, 9100])])
+def test_units_in_many_pieces(case):
+    """A few long contexts: every CTA has a piece of the same unit, and the merge joins more than 32."""
+    s, st = make(*case, seed=12), _status()
+    o = call(s, st)
+    assert int(st) == 0
+    check(o, s)
+    assert torch.equal(o, call(s))

@@ -18,10 +18,10 @@
 // 16-byte words.  Rows are the products' short side: 8 at a time, so that five rows cost a
 // quarter of what 32 do.
 //
-// 64 contexts of 8,192 with 23 nodes of 48 and 40 heads take 1,123 us (2.7 TB/s of codes): the matrix
+// 64 contexts of 8,192 with 23 nodes of 48 and 40 heads take 1,125 us (2.7 TB/s of codes): the matrix
 // unit, one of these products every two cycles, is busy for 490 of them, and the 8 warps that the registers leave room
 // for do not hide each other's chains (code to float, product, exponential, product) any better.
-// A call of one short piece a CTA is its start and end: 8 tokens of 2,000 positions take 22.6 us, 18 of them for
+// A call of one short piece a CTA is its start and end: 8 tokens of 2,000 positions take 20.6 us, 16 of them for
 // the division of the work, the walk to the piece, the queries, a slow first chunk, the join and the merge.
 #include "quant_attention.cuh"
 
