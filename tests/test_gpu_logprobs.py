@@ -301,3 +301,24 @@ def test_a_token_with_nearly_all_of_the_probability(V, dtype):
     eps = (V / 256 + 60) * 2.0 ** -24 + 64 * 0.7 * 2.0 ** -23 + 2.0 ** -21
     assert ((out["logprob"].double() - want).abs() <= eps * want.abs()).all(), (out["logprob"], want)
     assert torch.equal(out["top_logprobs"][:, 0], out["logprob"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", range(1, 18))
+def test_rows_without_a_whole_group(V, dtype):
+    """Rows of a few logits at every offset from 16 bytes: none, one or two groups that lie partly outside, and every
+    logit an alternative."""
+    rd = _rd()
+    n = 200
+    gen = torch.Generator(device=DEV).manual_seed(V)
+    flat = torch.full((n * V + 16,), float("nan"), dtype=TYPES[dtype], device=DEV)
+    for shift in range(8):
+        x = flat[shift:shift + n * V].view(n, V)
+        x.copy_(3 * torch.randn(n, V, generator=gen, device=DEV))
+        tokens = torch.randint(0, V, (n,), generator=gen, device=DEV, dtype=torch.int32)
+        out = rd.rd_token_logprobs(x, tokens, top=V)
+        order = torch.sort(x.double(), dim=1, descending=True, stable=True).indices
+        assert torch.equal(out["top_tokens"].long(), order)
+        for i in (0, 1, n // 2, n - 1):
+            check(out, i, x[i], int(tokens[i]), 1.0, V)
+        flat.fill_(float("nan"))

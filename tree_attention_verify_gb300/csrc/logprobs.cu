@@ -453,6 +453,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     // groups that lie inside of the row: the first and the last of all may not
     const int inside0 = row.first + (row.first < row.last && !row.inside(row.first) ? 1 : 0);
     const int inside1 = row.last - (row.last > inside0 && !row.inside(row.last - 1) ? 1 : 0);
+    // (a row without such a group comes to the counts below with no barrier on its way)
+    if (inside0 >= inside1) __syncthreads();
     for (int g0 = inside0; g0 < inside1; g0 += kStep) {
         uint4 u[kAhead];
         if (g0 + kStep <= inside1) {
