@@ -720,3 +720,35 @@ def test_units_in_many_pieces(case):
     assert int(st) == 0
     check(o, s)
     assert torch.equal(o, call(s))
+
+
+@pytest.mark.parametrize("bits,Hkv,D", [(4, 4, 64), (8, 2, 64)])
+def test_contexts_at_the_end_of_31_bits(bits, Hkv, D):
+    """The longest context there is: 2^31 - 257 positions on one page that its row of the table names again and again.  Nodes in
+    many tiles, so that pieces begin with drafts too.  A warp's share is 2^31 / 152 / 3 positions in steps of 16
+    products, each off by 2^-23 of the sum at most (the matrix unit may cut it off), which both the sums of
+    weights and of products may drift by: 2 x 295,000 x 2^-23 of the mean |v|, and 0.01 for the rest."""
+    rd, rng = _rd(), np.random.default_rng(bits)
+    page, C, P = 1 << 16, 2 ** 31 - 257, 40
+    width = 1 << 15
+    rows = _random_rows(rng, (2, 1, page, Hkv), D, bits)
+    kp, vp = _d(rows[0]), _d(rows[1])
+    table = torch.zeros(1, width, dtype=torch.int32, device=DEV)
+    q, kn, vn = (_bf(rng.standard_normal((1, P, Hkv, D))) for _ in range(3))
+    words = np.zeros((1, P, 2), np.int64)
+    for i in range(P):
+        words[0, i, i // 32] = 1 << i % 32
+    mask = _d(words.astype(np.uint32).view(np.int32))
+    st = _status()
+    o = rd.rd_tree_attention_quant(q, kn, vn, kp, vp, 0.25, 0.5, table, _d(np.array([C], np.int32)),
+                                   _d(np.array([P], np.int32)), mask, max_ctx=2 ** 31 - 1, dev_status=st)
+    assert int(st) == 0
+    times = torch.full((page,), float(C // page), dtype=torch.float64, device=DEV)
+    times[:C % page] += 1                     # how often a row of the page is seen
+    k, v = (_d(oq.decode(r[0], g, D, bits)) for r, g in ((rows[0], 0.25), (rows[1], 0.5)))
+    for h in range(Hkv):
+        x = (q[0, :, h].double() @ k[:, h].T) * D ** -0.5
+        w = torch.exp(x - x.amax(1, keepdim=True)) * times
+        w /= w.sum(1, keepdim=True)           # (a draft's own weight is below 2^-20)
+        want, size = w @ v[:, h], w @ v[:, h].abs()
+        assert ((o[0, :, h].double() - want).abs() <= want.abs() * 2.0 ** -8 + size * (2 * 295000 * 2.0 ** -23 + 0.01)).all()

@@ -134,8 +134,11 @@ __device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t
 template <int D, int BITS>
 __device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned char* ring, const Division& d)
 {
-    const int lane = threadIdx.x & 31, chunk = a.chunk, box = box_of(D, BITS);
-    const bool mine = lane * box < chunk;
+    const int lane = threadIdx.x & 31, box = box_of(D, BITS);
+    // (Unsigned: positions of chunks of drafts, of idle lanes and of the chunk after the last one lie up to
+    // 6,000 behind the context's end, which may be 2^31 - 257.)
+    const uint32_t chunk = a.chunk, page_size = a.page_size;
+    const bool mine = lane * box < (int)chunk;
     Walk walk = Walk::over(a, d);
     Piece p;
     Turn at = {0, 1};                      // (an empty stage's first phase counts as done)
@@ -143,9 +146,10 @@ __device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned c
     uint32_t filled = 0;
     while (alive && walk.next(a, p)) {
         const int32_t* table = a.table + (size_t)p.b * a.max_pages;
-        int pos = p.j0 * chunk + lane * box, in_page = pos % a.page_size;
-        table += pos / a.page_size;
-        int page = mine && pos < p.C ? __ldg(table) : 0;
+        const uint32_t C = p.C;
+        uint32_t pos = p.j0 * chunk + lane * box, in_page = pos % page_size;
+        table += pos / page_size;
+        int page = mine && pos < C ? __ldg(table) : 0;
         const int x = p.hg * (a.seg / 4);
         for (int j = p.j0; j < p.j1; ++j) {
             unsigned char* k_to = ring + (size_t)at.stage * 2 * a.half;
@@ -153,16 +157,16 @@ __device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned c
             uint64_t* bar = &sh.full[at.stage];
             uint64_t* empty = &sh.empty[at.stage];
             if (j < p.n_ctx) {
-                const bool live = mine && pos < p.C;
+                const bool live = mine && pos < C;
                 const int boxes = __popc(__ballot_sync(0xffffffffu, live));
                 if (live && (page < 0 || page >= a.num_pages)) {
                     rd_flag(a.status, RD_DEV_BAD_INDEX);
                     page = 0;
                 }
-                const int row = page * a.page_size + in_page;            // (31 bits: see launch)
+                const int row = page * a.page_size + (int)in_page;       // (31 bits: see launch)
                 pos += chunk;
-                for (in_page += chunk; in_page >= a.page_size; in_page -= a.page_size) ++table;
-                page = mine && pos < p.C ? __ldg(table) : 0;
+                for (in_page += chunk; in_page >= page_size; in_page -= page_size) ++table;
+                page = mine && pos < C ? __ldg(table) : 0;
                 alive = rdattn::warp_wait(empty, at.parity, &sh.abort, kWaitBudget);
                 if (!alive) break;         // nobody waits for copies any more
                 if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * boxes * box * a.seg));
