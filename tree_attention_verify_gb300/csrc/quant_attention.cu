@@ -134,11 +134,8 @@ __device__ __forceinline__ void load_rows(const Args& a, uint32_t k_to, uint32_t
 template <int D, int BITS>
 __device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned char* ring, const Division& d)
 {
-    const int lane = threadIdx.x & 31, box = box_of(D, BITS);
-    // (Unsigned: positions of chunks of drafts, of idle lanes and of the chunk after the last one lie up to
-    // 6,000 behind the context's end, which may be 2^31 - 257.)
-    const uint32_t chunk = a.chunk, page_size = a.page_size;
-    const bool mine = lane * box < (int)chunk;
+    const int lane = threadIdx.x & 31, chunk = a.chunk, box = box_of(D, BITS);
+    const bool mine = lane * box < chunk;
     Walk walk = Walk::over(a, d);
     Piece p;
     Turn at = {0, 1};                      // (an empty stage's first phase counts as done)
@@ -146,10 +143,12 @@ __device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned c
     uint32_t filled = 0;
     while (alive && walk.next(a, p)) {
         const int32_t* table = a.table + (size_t)p.b * a.max_pages;
-        const uint32_t C = p.C;
-        uint32_t pos = p.j0 * chunk + lane * box, in_page = pos % page_size;
-        table += pos / page_size;
-        int page = mine && pos < C ? __ldg(table) : 0;
+        // (Positions of chunks of drafts and of idle lanes lie up to 5,200 behind the context's end, which may be
+        // 2^31 - 257: unsigned, and from there on how many are left.)
+        const uint32_t pos = (uint32_t)p.j0 * chunk + lane * box;
+        int left = (int)((uint32_t)p.C - pos), in_page = (int)(pos % (uint32_t)a.page_size);
+        table += pos / (uint32_t)a.page_size;
+        int page = mine && left > 0 ? __ldg(table) : 0;
         const int x = p.hg * (a.seg / 4);
         for (int j = p.j0; j < p.j1; ++j) {
             unsigned char* k_to = ring + (size_t)at.stage * 2 * a.half;
@@ -157,16 +156,16 @@ __device__ __forceinline__ void load_tiled(const Args& a, Shared& sh, unsigned c
             uint64_t* bar = &sh.full[at.stage];
             uint64_t* empty = &sh.empty[at.stage];
             if (j < p.n_ctx) {
-                const bool live = mine && pos < C;
+                const bool live = mine && left > 0;
                 const int boxes = __popc(__ballot_sync(0xffffffffu, live));
                 if (live && (page < 0 || page >= a.num_pages)) {
                     rd_flag(a.status, RD_DEV_BAD_INDEX);
                     page = 0;
                 }
-                const int row = page * a.page_size + (int)in_page;       // (31 bits: see launch)
-                pos += chunk;
-                for (in_page += chunk; in_page >= page_size; in_page -= page_size) ++table;
-                page = mine && pos < C ? __ldg(table) : 0;
+                const int row = page * a.page_size + in_page;            // (31 bits: see launch)
+                left -= chunk;
+                for (in_page += chunk; in_page >= a.page_size; in_page -= a.page_size) ++table;
+                page = mine && left > 0 ? __ldg(table) : 0;
                 alive = rdattn::warp_wait(empty, at.parity, &sh.abort, kWaitBudget);
                 if (!alive) break;         // nobody waits for copies any more
                 if (lane == 0) rdtc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * boxes * box * a.seg));
