@@ -752,3 +752,13 @@ def test_contexts_at_the_end_of_31_bits(bits, Hkv, D):
         w /= w.sum(1, keepdim=True)           # (a draft's own weight is below 2^-20)
         want, size = w @ v[:, h], w @ v[:, h].abs()
         assert ((o[0, :, h].double() - want).abs() <= want.abs() * 2.0 ** -8 + size * (2 * 295000 * 2.0 ** -23 + 0.01)).all()
+
+
+@pytest.mark.parametrize("bits,D", [(4, 64), (4, 128), (8, 64), (8, 128)])
+def test_factors_that_are_zero(bits, D):
+    """Queries and a scale so small that a row's factor is 0 in 32 bits: equal weights, also where the context ends
+    inside a tile."""
+    for lens, ctx in (([3, 1], [70, 41]), ([2, 3], [9, 128])):
+        s = make(2, 3, 4, 4, D, 64, bits, lens, ctx, seed=13, amp=1e-30)
+        s["kn"].nan_to_num_()
+        check(call(s, scale=1e-30), s, 1e-30)

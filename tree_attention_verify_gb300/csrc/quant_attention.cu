@@ -711,7 +711,10 @@ __device__ __forceinline__ void stage_queries(const Args& a, const Place& w, con
         out.z = pack_f16(x[4] * up, x[5] * up);
         out.w = pack_f16(x[6] * up, x[7] * up);
         *reinterpret_cast<uint4*>(buf.q + ((size_t)w.head * rows_of(D) + r) * (D + 8) + 8 * sub) = out;
-        if (sub == 0) buf.f[w.head * rows_of(D) + r] = a.scale_log2 * a.k_scale * down;
+        // (never 0, which times the -inf of what lies behind the context's end is no number: no score moves by as much
+        // as 2^-90)
+        const float f = a.scale_log2 * a.k_scale * down;
+        if (sub == 0) buf.f[w.head * rows_of(D) + r] = f < 0x1p-126f ? 0x1p-126f : f;
     }
 }
 
