@@ -484,8 +484,9 @@ rd_status rd_read_quant(int B, int Hkv, int D, int bits, const void* k_pool, con
  *            contents; the size depends on the SM count of the current device.  Calls that
  *            share a workspace must not overlap in time.
  * Queries may have any finite value; elements below 2^-28 of their row's largest may lose
- * precision.  K and V of the packed drafts must be below 2^100 in size (their products with scaled
- * queries and weights are 32-bit sums).  A NaN code of a cached row
+ * precision.  K of the packed drafts must be below 2^100 in size, V below 2^100 or
+ * 2^35 v_scale, whichever is more (their products with scaled queries and weights are 32-bit
+ * sums), in nodes that a row does not see too.  A NaN code of a cached row
  * (e4m3 0x7f, 0xff, as a code or a block's scale) makes what sees it NaN.  What lies behind a
  * context's end in its last page, and behind packed_len, may hold anything.
  */

@@ -762,3 +762,54 @@ def test_factors_that_are_zero(bits, D):
         s = make(2, 3, 4, 4, D, 64, bits, lens, ctx, seed=13, amp=1e-30)
         s["kn"].nan_to_num_()
         check(call(s, scale=1e-30), s, 1e-30)
+
+
+def _close(o, s, scale):
+    """check() without its absolute term, for outputs of any size: 32-bit sums are off by 2^-150 of nothing, outputs below
+    2^-126 by half a step of 2^-133."""
+    want, a_ctx, a_new, (kc, vc), (q, kn, _) = reference(s, scale)
+    D, P = q.shape[3], q.shape[1]
+    G = q.shape[2] // kn.shape[2]
+    most, sums = np.zeros(q.shape[:3]), np.zeros(q.shape)
+    for b in range(len(kc)):
+        for h in range(q.shape[2]):
+            k = np.abs(np.concatenate([kc[b][:, h // G], kn[b, :, h // G]]))
+            most[b, :, h] = scale * (np.abs(q[b, :, h]) @ k.T).max(1)
+            sums[b, :, h] = np.abs(vc[b][:, h // G]).sum(0)
+    eps = 2 * (D + 8) * 2.0 ** -24 * most[..., None] + 2 * (P + s["max_ctx"]) * 2.0 ** -24 + 2.0 ** -20
+    tol = np.maximum(np.abs(want) * 2.0 ** -8, 2.0 ** -134) + a_ctx * (2.0 ** -11 + eps) + a_new * (2.0 ** -8 + eps) + sums * 2.0 ** -32
+    got = _f64(o)
+    assert np.isfinite(got).all()
+    worst = np.unravel_index(np.argmax(np.abs(got - want) - tol), got.shape)
+    assert (np.abs(got - want) <= tol).all(), (worst, got[worst], want[worst], tol[worst])
+
+
+SCALES = [1e-45, 1e-40, 1e-38, 1e-30, 1e30, 6e37]
+
+
+@pytest.mark.parametrize("bits,D", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("gk", SCALES)
+def test_key_scales(gk, bits, D):
+    """Every scale of the keys: drafts are weighed as ever, and the cached keys too, with queries or a softmax scale
+    that bring their scores to a few units or leave them at nothing."""
+    gk = float(np.float32(gk))
+    for seed, (amp, scale) in enumerate(((1.0, D ** -0.5), (1.0, 0.1 / gk), (0.05 / gk, 1.0))):
+        if not (1e-37 < scale < 1e37 and 1e-37 < amp < 1e37 and amp * scale * gk < 3):
+            continue                          # not numbers of 32 bits, or scores of thousands
+        s = make(2, 5, 4, 4, D, 64, bits, [5, 3], [150, 41], seed=seed, amp=amp)
+        size = 1.0 if seed == 0 else min(gk, 2.0 ** 90)           # drafts of the cache's size, as far as they may reach
+        s["kn"], s["vn"] = (s["kn"].nan_to_num().float() * size).bfloat16(), s["vn"].nan_to_num()
+        s["gk"] = gk
+        _close(call(s, scale=scale), s, float(np.float32(scale)))
+
+
+@pytest.mark.parametrize("bits,D", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("gv", SCALES)
+def test_value_scales(gv, bits, D):
+    """Every scale of the values, in one piece a row and in many, with drafts of the cache's size and with none."""
+    gv = float(np.float32(gv))
+    for mask, ctx in (("tree", [150, 41]), ("none", [150, 41]), ("tree", [9000, 41])):
+        s = make(2, 5, 4, 4, D, 64, bits, [5, 3], ctx, seed=3, mask=mask)
+        s["gv"] = gv
+        s["vn"] = (s["vn"].nan_to_num().float() * gv).bfloat16()
+        _close(call(s, scale=D ** -0.5), s, float(np.float32(D ** -0.5)))

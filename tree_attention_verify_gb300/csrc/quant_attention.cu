@@ -588,7 +588,7 @@ __device__ __forceinline__ uint32_t bf16_of_f16(uint32_t x)
 // a product have one type), 2^-9 of each weight
 template <int D, int BITS, int NT>
 __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const Piece& pc, Sums<D, BITS, NT>& s, uint32_t k_at,
-                                           uint32_t v_at, uint32_t q_at, int node0, int nodes)
+                                           uint32_t v_at, uint32_t q_at, uint32_t f_at, int node0, int nodes)
 {
     constexpr int KB = D / 64;
     float x[NT][4];
@@ -623,11 +623,10 @@ __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const 
             }
         }
     float top[2 * NT];
-    const float back = 1.f / a.k_scale;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const uint4 fr = lds128(s.fr + (uint32_t)(64 * i));
-        const float f[2] = {__uint_as_float(fr.x) * back, __uint_as_float(fr.z) * back};
+        const uint2 u = lds64(f_at + (uint32_t)(32 * i));
+        const float f[2] = {__uint_as_float(u.x), __uint_as_float(u.y)};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             x[i][c] = (seen[2 * i + (c & 1)] >> (pos + 4 * (c & 2)) & 1u) ? x[i][c] * f[c & 1] : -INFINITY;
@@ -644,8 +643,8 @@ __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const 
         const float p2 = fast_exp2(x[i][2] - top[2 * i]), p3 = fast_exp2(x[i][3] - top[2 * i + 1]);
         l[2 * i] += p0 + p2;
         l[2 * i + 1] += p1 + p3;
-        pb[i][0] = transpose8x8(pack_bf16(p0, p1));
-        pb[i][1] = transpose8x8(pack_bf16(p2, p3));
+        pb[i][0] = transpose8x8(pack_bf16(p0 * a.v_down, p1 * a.v_down));
+        pb[i][1] = transpose8x8(pack_bf16(p2 * a.v_down, p3 * a.v_down));
     }
     s.set_sums(l);
     const int v[4] = {position_of(w.t, 0), position_of(w.t, 1), position_of(w.t, 0) + 8, position_of(w.t, 1) + 8};
@@ -671,12 +670,17 @@ __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const 
 struct Buffers {
     unsigned char* ring;
     __half* q;                 // [heads][rows][D + 8]
-    float* f;                  // [heads][rows] score = product x f (log2 units, the cache's scale in it)
+    float* f;                  // [heads][rows] score of a cached key = product x f (log2 units, the cache's scale in it)
+    float* f_new;              // [heads][rows] the same of a draft
     float2* fr;                // [warps][rows] f, and minus the row's reference
     float2* l;                 // [warps][rows / 8][32] each thread's sums of weights
     float4* join;              // [warps / 2][2][D / 16][32]
     float2* join_ml;           // [warps / 2][8][32]
 };
+
+// m 2^e with m in [1, 2], e taken to the nearest exponent that a number has.  Never 0, which times the -inf of what lies
+// behind the context's end is no number: no score moves by as much as 2^-90.
+__device__ __forceinline__ float factor(float m, int e) { return m * __uint_as_float((uint32_t)min(max(e + 127, 1), 253) << 23); }
 
 // The queries of a unit as 16-bit floats.  A power of two per row brings its largest element to
 // [2^14, 2^15): elements down to 2^-28 of it stay exact, and no finite query leaves the range.
@@ -704,17 +708,17 @@ __device__ __forceinline__ void stage_queries(const Args& a, const Place& w, con
         for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int e = (int)(__float_as_uint(top) >> 23);
         const int k = top == 0.f || e == 255 ? 127 : min(240, 268 - e);
-        const float up = __uint_as_float((uint32_t)k << 23), down = __uint_as_float((uint32_t)(254 - k) << 23);
+        const float up = __uint_as_float((uint32_t)k << 23);
         uint4 out;
         out.x = pack_f16(x[0] * up, x[1] * up);
         out.y = pack_f16(x[2] * up, x[3] * up);
         out.z = pack_f16(x[4] * up, x[5] * up);
         out.w = pack_f16(x[6] * up, x[7] * up);
         *reinterpret_cast<uint4*>(buf.q + ((size_t)w.head * rows_of(D) + r) * (D + 8) + 8 * sub) = out;
-        // (never 0, which times the -inf of what lies behind the context's end is no number: no score moves by as much
-        // as 2^-90)
-        const float f = a.scale_log2 * a.k_scale * down;
-        if (sub == 0) buf.f[w.head * rows_of(D) + r] = f < 0x1p-126f ? 0x1p-126f : f;
+        if (sub == 0) {
+            buf.f[w.head * rows_of(D) + r] = factor(a.ctx_m, a.ctx_e + 127 - k);
+            buf.f_new[w.head * rows_of(D) + r] = factor(a.new_m, a.new_e + 127 - k);
+        }
     }
 }
 
@@ -739,6 +743,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     stage_queries<D>(a, w, p, buf, NT);
     compute_sync<D>();
     const uint32_t q_at = smem_addr(buf.q) + (uint32_t)((w.head * rows_of(D) + w.g) * (2 * D + 16) + 32 * w.t);
+    const uint32_t f_at = smem_addr(buf.f_new + w.head * rows_of(D) + 2 * w.t);
     if (w.lane < rows_of(D)) buf.fr[w.warp * rows_of(D) + w.lane] = make_float2(buf.f[w.head * rows_of(D) + w.lane], 0.f);
     {
         float zeros[2 * NT];
@@ -748,7 +753,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
     }
     __syncwarp();
     const uint32_t ring = smem_addr(buf.ring);
-    bool scaled = false;                   // O holds values, no longer values / v_scale
+    bool scaled = false;                   // O holds values x v_down, no longer what codes and blocks' scales stand for
     auto scale_values = [&]() {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
@@ -796,7 +801,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
             if (!scaled) scale_values();
             if (tile % w.splits == w.split) {
                 const uint32_t off = (uint32_t)(w.head * D * 2);
-                draft_tile<D, BITS, NT>(a, w, p, s, k_at + off, v_at + off, q_at, tile * kDraftTile,
+                draft_tile<D, BITS, NT>(a, w, p, s, k_at + off, v_at + off, q_at, f_at, tile * kDraftTile,
                                         min(kDraftTile, p.len - tile * kDraftTile));
             }
         }
@@ -879,7 +884,7 @@ __device__ __forceinline__ void piece(const Args& a, Shared& sh, const Buffers& 
             const int at = 8 * i + 2 * w.t + e;
             if (at >= p.rows) continue;
             if (whole) {
-                const float f = l[2 * i + e] == 0.f ? 0.f : 1.f / l[2 * i + e];
+                const float f = l[2 * i + e] == 0.f ? 0.f : a.v_up * (1.f / l[2 * i + e]);
                 const int row = p.r0 + at;
                 uint32_t u[D / 16];
 #pragma unroll
@@ -925,7 +930,8 @@ __global__ void __launch_bounds__(threads_of(D), 1) quant_attention_kernel(const
     buf.ring = dyn;
     buf.q = reinterpret_cast<__half*>(dyn + (size_t)a.stages * 2 * a.half);
     buf.f = reinterpret_cast<float*>(buf.q + (size_t)a.heads * rows_of(D) * (D + 8));
-    buf.fr = reinterpret_cast<float2*>(buf.f + (size_t)a.heads * rows_of(D));
+    buf.f_new = buf.f + (size_t)a.heads * rows_of(D);
+    buf.fr = reinterpret_cast<float2*>(buf.f_new + (size_t)a.heads * rows_of(D));
     buf.l = buf.fr + warps_of(D) * rows_of(D);
     buf.join = reinterpret_cast<float4*>(buf.l + warps_of(D) * (rows_of(D) / 8) * 32);
     buf.join_ml = reinterpret_cast<float2*>(buf.join + warps_of(D) / 2 * 2 * (D / 16) * 32);
@@ -1036,7 +1042,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) quant_merge_kernel(const Arg
             o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
             o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
         }
-        const float f = L == 0.f ? 0.f : 1.f / L;
+        const float f = L == 0.f ? 0.f : a.v_up * (1.f / L);
         const int row = r0 + r;
         if (share == 0) {
             uint2 out;
@@ -1095,7 +1101,7 @@ cudaError_t launch(Args& a, int grid, cudaStream_t stream)
     a.draft_pitch = a.heads * D * 2 + 16;
     const int rows = a.tiled ? chunk * a.seg : chunk * a.pitch, drafts = kDraftTile * a.draft_pitch;
     a.half = ((rows > drafts ? rows : drafts) + 1023) / 1024 * 1024;       // (swizzled tiles repeat every 1024 bytes)
-    const int fixed = a.heads * rows_of(D) * ((D + 8) * 2 + 4) + warps_of(D) * (rows_of(D) + rows_of(D) / 8 * 32) * 8 + warps_of(D) / 2 * 32 * (2 * (D / 16) * 16 + 8 * 8);
+    const int fixed = a.heads * rows_of(D) * ((D + 8) * 2 + 8) + warps_of(D) * (rows_of(D) + rows_of(D) / 8 * 32) * 8 + warps_of(D) / 2 * 32 * (2 * (D / 16) * 16 + 8 * 8);
     constexpr int kSmem = 227 * 1024 - 1024;               // what the static part leaves
     a.stages = (kSmem - fixed) / (2 * a.half);
     if (a.stages > kMostStages) a.stages = kMostStages;
@@ -1176,9 +1182,16 @@ cudaError_t rd_launch_quant_attention(const rd_quant_kv& kv, int B, int P_max, i
     // no context is longer than its row of the table, or there is no page to read
     const long long row = kv.pages.num_pages > 0 ? (long long)kv.pages.max_pages * kv.pages.page_size : 0;
     a.max_ctx = (int)(row < max_ctx ? row : max_ctx);
-    a.scale_log2 = scale * kLog2e;
-    a.k_scale = kv.k_scale;
-    a.v_scale = kv.v_scale;
+    int exponent;
+    a.new_m = 2.f * (float)frexp(scale * kLog2e, &exponent);
+    a.new_e = exponent - 1;
+    a.ctx_m = 2.f * (float)frexp(scale * kLog2e * kv.k_scale, &exponent);
+    a.ctx_e = exponent - 1;
+    // (sums of 2^31 weights of up to 2^15 each, times values of up to 2688 v_scale, stay below 2^127)
+    frexp(kv.v_scale, &exponent);
+    a.v_up = ldexpf(1.f, exponent > 65 ? exponent - 65 : 0);
+    a.v_down = 1.f / a.v_up;
+    a.v_scale = kv.v_scale * a.v_down;
     a.stall = rd_attention_stall_budget();
     const cudaError_t e = D == 128 ? kv.bits == 4 ? launch<128, 4>(a, grid, stream) : launch<128, 8>(a, grid, stream)
                           : kv.bits == 4 ? launch<64, 4>(a, grid, stream)

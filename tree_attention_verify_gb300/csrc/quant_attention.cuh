@@ -16,7 +16,7 @@ using rdattn::pack_bf16;
 using rdtc::smem_addr;
 
 constexpr long long kWaitBudget = 4000000000LL;     // cycles, about two seconds
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLog2e = 1.4426950408889634;
 // A row's weights are powers of two above a reference that lies kBelow under the row's maximum,
 // or up to kLag more: a weight P reaches 2^15 (a 16-bit float ends at 2^16), O is
 // rescaled only when the reference lags more, and weights down to 2^-21 of the largest
@@ -34,7 +34,11 @@ struct Args {
     int4* desc;                // [grid] the unit that a CTA begins and does not end
     int32_t* status;
     int B, P, Hq, Hkv, G, mask_words, num_pages, page_size, max_pages, max_ctx;
-    float scale_log2, k_scale, v_scale;
+    // Scores in log2 units: of cached keys product x ctx_m 2^ctx_e (the cache's scale in it), of drafts x new_m 2^new_e.
+    float ctx_m, new_m;
+    int ctx_e, new_e;
+    // O holds values x v_down, a power of two that keeps sums of values up to the largest numbers finite
+    float v_scale, v_down, v_up;       // the cache's scale x v_down; 1 / v_down
     long long stall;
     int heads;                 // kv heads of a unit
     int unit_rows, row_step;   // rows of a unit at most, a multiple of row_step
