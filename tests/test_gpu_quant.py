@@ -813,3 +813,25 @@ def test_value_scales(gv, bits, D):
         s["gv"] = gv
         s["vn"] = (s["vn"].nan_to_num().float() * gv).bfloat16()
         _close(call(s, scale=D ** -0.5), s, float(np.float32(D ** -0.5)))
+
+
+@pytest.mark.parametrize("bits,D", [(4, 64), (4, 128), (8, 64)])
+@pytest.mark.parametrize("e", [-149, -140, -127, -126, -100, 0, 90, 110, 124, 126, 127])
+def test_append_at_the_ends_of_the_scales(e, bits, D):
+    """Powers of two for a scale, where every quotient is exact: the definition's bytes, and read back what they stand
+    for in bf16 (infinite behind its largest number)."""
+    rd, rng = _rd(), np.random.default_rng(abs(e) + bits)
+    T, Hkv, g = 40, 3, 2.0 ** e
+    x = rng.standard_normal((T, Hkv, D)) * np.exp2(rng.integers(-12, 13, (T, Hkv, 1)))
+    x[3, 1] = 0
+    with np.errstate(over="ignore"):
+        k = torch.from_numpy(np.clip(x * g * 16, -3.3e38, 3.3e38)).to(torch.bfloat16).to(DEV)
+    kp, vp = (torch.zeros(1, 64, Hkv, oq.row_bytes(D, bits), dtype=torch.uint8, device=DEV) for _ in range(2))
+    table, ctx, st = _d(np.zeros((1, 1), np.int32)), _d(np.zeros(1, np.int32)), _status()
+    rd.rd_append_quant(k, k, _d(np.array([0, T], np.int32)), kp, vp, g, g, table, ctx, dev_status=st)
+    assert int(st) == 0 and torch.equal(kp, vp)
+    rows, xs = kp.cpu().numpy()[0, :T], _f64(k)
+    want = np.stack([[oq.encode_row(xs[t, h], g, bits)[0] for h in range(Hkv)] for t in range(T)])
+    np.testing.assert_array_equal(rows, want)
+    out, _ = rd.rd_read_quant(kp, vp, g, g, table, _d(np.array([0, T], np.int64)), total=T, dev_status=st)
+    np.testing.assert_array_equal(_f64(out), _f64(torch.from_numpy(oq.decode(rows, g, D, bits)).to(torch.bfloat16)))

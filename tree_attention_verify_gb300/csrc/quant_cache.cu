@@ -29,9 +29,15 @@ constexpr int kThreads = 256;
 constexpr int kBlocks = 512;               // blocks of 16 elements that a CTA moves (of K, and of V)
 constexpr int kMostTokens = 64;            // tokens of a CTA
 
+// A tensor's scale: g, and m / (up1 up2) with m in [1, 2) and powers of two.  A value times up1, then up2 over m is
+// x / g whatever g is: up1 and up2 lie on one side of 1, so what leaves the range on the way saturates or is 0 anyway.
+struct Scale {
+    float g, m, up1, up2;
+};
+
 struct Pools {
     unsigned char *k, *v;
-    float k_scale, v_scale;
+    Scale k_scale, v_scale;
     int num_pages, page_size, max_pages;
     const int32_t* table;
 };
@@ -66,12 +72,13 @@ __device__ __forceinline__ int request_of(const T* __restrict__ offsets, int n, 
 }
 
 // ------------------------------------------------------------------ one block
-__device__ __forceinline__ void unpack16(const uint32_t (&u)[8], float (&x)[16])
+// 16 values over the power of two in their scale
+__device__ __forceinline__ void unpack16(const uint32_t (&u)[8], float (&x)[16], const Scale& scale)
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        x[2 * i] = __uint_as_float(u[i] << 16) * scale.up1 * scale.up2;
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * scale.up1 * scale.up2;
     }
 }
 
@@ -104,20 +111,20 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
 }
 
 template <int D, int BITS>
-__device__ __forceinline__ void store_block(unsigned char* row, int block, const float (&x)[16], float g)
+__device__ __forceinline__ void store_block(unsigned char* row, int block, const float (&x)[16], float m)
 {
     if constexpr (BITS == 8) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            u[i] = e4m3_of(x[4 * i] / g, x[4 * i + 1] / g) | e4m3_of(x[4 * i + 2] / g, x[4 * i + 3] / g) << 16;
+            u[i] = e4m3_of(x[4 * i] / m, x[4 * i + 1] / m) | e4m3_of(x[4 * i + 2] / m, x[4 * i + 3] / m) << 16;
         *reinterpret_cast<uint4*>(row + 16 * block) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
-        const uint32_t byte = e4m3_of(fminf(448.f, top / (6.f * g)), 0.f) & 0xffu;
-        const float d = scale_value(byte) * g;
+        const uint32_t byte = e4m3_of(fminf(448.f, top / (6.f * m)), 0.f) & 0xffu;
+        const float d = scale_value(byte) * m;
         uint32_t u[2] = {0, 0};
         if (d > 0.f) {
             float y[16];
@@ -303,10 +310,10 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
         load32(v + from, vu, wide);
         const size_t to = ((size_t)at.to * Hkv + c / (D / 16)) * row_bytes(D, BITS);
         float x[16];
-        unpack16(ku, x);
-        store_block<D, BITS>(p.k + to, c % (D / 16), x, p.k_scale);
-        unpack16(vu, x);
-        store_block<D, BITS>(p.v + to, c % (D / 16), x, p.v_scale);
+        unpack16(ku, x, p.k_scale);
+        store_block<D, BITS>(p.k + to, c % (D / 16), x, p.k_scale.m);
+        unpack16(vu, x, p.v_scale);
+        store_block<D, BITS>(p.v + to, c % (D / 16), x, p.v_scale.m);
     }
 }
 
@@ -351,8 +358,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
             Raw<D, BITS> kr, vr;
             kr.load(p.k + from, c % (D / 16));
             vr.load(p.v + from, c % (D / 16));
-            kr.values(p.k_scale, ku);
-            vr.values(p.v_scale, vu);
+            kr.values(p.k_scale.g, ku);
+            vr.values(p.v_scale.g, vu);
         }
         const size_t to = ((size_t)(t0 + t) * blocks + c) * 2;
         store32(k + to, ku, wide);
@@ -366,13 +373,24 @@ int tokens_of_cta(int Hkv, int D)
     return n < 1 ? 1 : n > kMostTokens ? kMostTokens : n;
 }
 
+Scale scale_of(float g)
+{
+    int e;
+    Scale s;
+    s.g = g;
+    s.m = 2.f * frexpf(g, &e);
+    s.up1 = ldexpf(1.f, (1 - e) / 2);
+    s.up2 = ldexpf(1.f, (1 - e) - (1 - e) / 2);
+    return s;
+}
+
 Pools pools_of(const rd_quant_kv& kv)
 {
     Pools p;
     p.k = static_cast<unsigned char*>(kv.k_pool);
     p.v = static_cast<unsigned char*>(kv.v_pool);
-    p.k_scale = kv.k_scale;
-    p.v_scale = kv.v_scale;
+    p.k_scale = scale_of(kv.k_scale);
+    p.v_scale = scale_of(kv.v_scale);
     p.num_pages = kv.pages.num_pages;
     p.page_size = kv.pages.page_size;
     p.max_pages = kv.pages.max_pages;
