@@ -835,3 +835,53 @@ def test_append_at_the_ends_of_the_scales(e, bits, D):
     np.testing.assert_array_equal(rows, want)
     out, _ = rd.rd_read_quant(kp, vp, g, g, table, _d(np.array([0, T], np.int64)), total=T, dev_status=st)
     np.testing.assert_array_equal(_f64(out), _f64(torch.from_numpy(oq.decode(rows, g, D, bits)).to(torch.bfloat16)))
+
+
+def _written(x, g, bits):
+    """The bytes of rows x [T, Hkv, D], and the values that they were made from."""
+    T, Hkv, D = x.shape
+    k = _bf(x)
+    kp = torch.zeros(-(-T // 64), 64, Hkv, oq.row_bytes(D, bits), dtype=torch.uint8, device=DEV)
+    table = torch.arange(kp.shape[0], dtype=torch.int32, device=DEV)[None].contiguous()
+    _rd().rd_append_quant(k, k, _d(np.array([0, T], np.int32)), kp, torch.empty_like(kp), g, g, table, _d(np.zeros(1, np.int32)))
+    return kp.cpu().numpy().reshape(-1, Hkv, kp.shape[3])[:T], _f64(k)
+
+
+def _neighbours(rows):
+    """Bytes of the definition that differ from these: none may."""
+    got, x, g, bits = rows
+    want = np.stack([oq.encode_row(r, g, bits)[0] for r in x.reshape(-1, x.shape[-1])]).reshape(got.shape)
+    return np.argwhere(got != want)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_values_beside_borders(bits):
+    """Scales calibrated to the largest value are no short numbers, and values in simple ratios to it lie
+    beside a border between two codes, nearer than a 32-bit quotient tells."""
+    D = 64
+    ties = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0] if bits == 4 else list((oq.E4M3[1:] + oq.E4M3[:-1])[-60:] / 2)
+    most = 6.0 if bits == 4 else 448.0
+    for j in range(1, 32):
+        amax = (3.0 if bits == 4 else 7.0) * j
+        g = float(np.float32(amax / (2688 if bits == 4 else 448)))
+        x = np.zeros((8, 1, D))
+        x[:, :, 0] = amax
+        x[:, :, 1:16] = np.resize(np.array(ties) * amax / most, (8, 1, 15)) * np.where(np.arange(15) % 3 == 1, -1, 1)
+        x[:, :, 16:] = np.random.default_rng(j).choice(ties, (8, 1, 48)) * amax / most
+        x[4:] *= 2.0 ** -5                    # (in 4 bits: other scales of blocks)
+        got, x = _written(x, g, bits)
+        assert len(_neighbours((got, x, g, bits))) == 0, j
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_bytes_at_calibrated_scales(bits):
+    """Every byte of many rows is the definition's; none is left out for lying beside a border."""
+    rng = np.random.default_rng(bits)
+    for D, T in ((64, 400), (128, 200)):
+        x = rng.standard_normal((T, 4, D)) * np.exp(0.5 * rng.standard_normal((1, 4, D)))
+        x[::7, :, ::5] = 0
+        x = _f64(_bf(x))
+        g = float(np.float32(np.abs(x).max() / (448 if bits == 8 else 2688)))
+        for by in (1.0, 0.37, 3.0):           # beside the calibrated one, scales that saturate and that leave range
+            got, y = _written(x, float(np.float32(g * by)), bits)
+            assert len(_neighbours((got, y, float(np.float32(g * by)), bits))) == 0, (D, by)

@@ -10,10 +10,13 @@
 // (32 bytes each on the 16-bit side, one access; 9 or 16 on the other), so that a block's maximum needs
 // no other thread and neighbours' accesses are consecutive.  A CTA first finds where each of its
 // tokens lies (request, position, page: a search and two dependent reads), a thread per token, then
-// moves about kBlocks blocks; the divisions are IEEE ones, so that ties are decided as defined.
+// moves about kBlocks blocks.  Codes are the nearest to the exact quotients: by products with a reciprocal, and by the sign
+// of an exact remainder where a border between two codes is within their error (about one value in 250,000, and those
+// of few bits).  IEEE divisions, whose rounded quotients hide on which side of a border they are, also took longer (12,000
+// tokens written and read back: 39 us, not 34).
 // Two 16-byte accesses for a block's 32 bytes would take longer (16 x 4,096 tokens of 8 heads read from 4
 // bits: 53 us, not 45), and so would CTAs of 1,024 blocks, which wait longer for their first
-// bytes than they then move (12,000 tokens written and read back: 39 us, not 37).  Reading 8 x 8,192 tokens of 40 heads
+// bytes than they then move (the same: 39 us, not 37, when the divisions took their part).  Reading 8 x 8,192 tokens of 40 heads
 // from 8 bits takes 234 us, 6.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,10 +32,11 @@ constexpr int kThreads = 256;
 constexpr int kBlocks = 512;               // blocks of 16 elements that a CTA moves (of K, and of V)
 constexpr int kMostTokens = 64;            // tokens of a CTA
 
-// A tensor's scale: g, and m / (up1 up2) with m in [1, 2) and powers of two.  A value times up1, then up2 over m is
-// x / g whatever g is: up1 and up2 lie on one side of 1, so what leaves the range on the way saturates or is 0 anyway.
+// A tensor's scale: g, and m / (up1 up2) with m in [1, 2) and powers of two; inv is 1 / m in 8 bits, 1 / (6 m) in 4.
+// A value times up1, then up2 over m is x / g whatever g is: up1 and up2 lie on one side of 1, so what leaves the
+// range on the way saturates or is 0 anyway.
 struct Scale {
-    float g, m, up1, up2;
+    float g, m, up1, up2, inv;
 };
 
 struct Pools {
@@ -72,14 +76,31 @@ __device__ __forceinline__ int request_of(const T* __restrict__ offsets, int n, 
 }
 
 // ------------------------------------------------------------------ one block
-// 16 values over the power of two in their scale
-__device__ __forceinline__ void unpack16(const uint32_t (&u)[8], float (&x)[16], const Scale& scale)
+__device__ __forceinline__ void unpack16(const uint32_t (&u)[8], float (&x)[16])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16) * scale.up1 * scale.up2;
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * scale.up1 * scale.up2;
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
+}
+
+// The code nearest to a quotient a / d is decided by an approximation y of it (products with a reciprocal, at most
+// 3 units of its last place off), unless a border between two codes is as near.  Borders have BITS bits behind the
+// first one at most: `apart` is at most 8 where some number of so few bits lies within 4 units.
+template <int BITS>
+__device__ __forceinline__ uint32_t apart(float y)
+{
+    return (__float_as_uint(y) + 4u) & ((1u << (23 - BITS)) - 1u);
+}
+// Such a y on the right side of the border t, or t itself: by the sign of |a| - t (d + e), which two fused
+// operations give exactly (t d has few bits more than a 32-bit number, and nearly all cancel).
+template <int BITS>
+__device__ __forceinline__ float settled(float y, float a, float d, float e)
+{
+    const uint32_t u = __float_as_uint(fabsf(y)), t = (u + (1u << (22 - BITS))) & ~((1u << (23 - BITS)) - 1u);
+    const float border = __uint_as_float(t), r = fmaf(-border, e, fmaf(-border, d, fabsf(a)));
+    return apart<BITS>(fabsf(y)) > 8u ? y : copysignf(__uint_as_float(r > 0.f ? t + 8u : r < 0.f && t != 0 ? t - 8u : t), y);
 }
 
 __device__ __forceinline__ uint32_t e4m3_of(float lo, float hi)
@@ -111,25 +132,51 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
 }
 
 template <int D, int BITS>
-__device__ __forceinline__ void store_block(unsigned char* row, int block, const float (&x)[16], float m)
+__device__ __forceinline__ void store_block(unsigned char* row, int block, const float (&x)[16], const Scale& g)
 {
+    const auto scaled = [&](float v) { return v * g.up1 * g.up2; };      // v / g = scaled(v) / m
+    float y[16];
     if constexpr (BITS == 8) {
+        uint32_t near = 9;
+        const float by = g.up2 * g.inv;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            y[i] = x[i] * g.up1 * by;
+            near = min(near, apart<4>(y[i]));
+        }
+        if (near <= 8) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = settled<4>(y[i], scaled(x[i]), g.m, 0.f);
+        }
         uint32_t u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = e4m3_of(x[4 * i] / m, x[4 * i + 1] / m) | e4m3_of(x[4 * i + 2] / m, x[4 * i + 3] / m) << 16;
+        for (int i = 0; i < 4; ++i) u[i] = e4m3_of(y[4 * i], y[4 * i + 1]) | e4m3_of(y[4 * i + 2], y[4 * i + 3]) << 16;
         *reinterpret_cast<uint4*>(row + 16 * block) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
-        const uint32_t byte = e4m3_of(fminf(448.f, top / (6.f * m)), 0.f) & 0xffu;
-        const float d = scale_value(byte) * m;
+        float quotient = top * g.up1 * (g.up2 * g.inv);
+        if (apart<4>(quotient) <= 8) {
+            const float d = 6.f * g.m;
+            quotient = settled<4>(quotient, scaled(top), d, fmaf(6.f, g.m, -d));
+        }
+        const uint32_t byte = e4m3_of(fminf(448.f, quotient), 0.f) & 0xffu;
+        const float s = scale_value(byte), d = s * g.m;
         uint32_t u[2] = {0, 0};
-        if (d > 0.f) {
-            float y[16];
+        if (s > 0.f) {
+            uint32_t near = 9;
+            const float by = g.up2 * (1.f / d);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = x[i] / d;
+            for (int i = 0; i < 16; ++i) {
+                y[i] = x[i] * g.up1 * by;
+                near = min(near, apart<2>(y[i]));
+            }
+            if (near <= 8) {
+                const float e = fmaf(s, g.m, -d);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = settled<2>(y[i], scaled(x[i]), d, e);
+            }
             u[0] = e2m1_of(y);
             u[1] = e2m1_of(y + 8);
         }
@@ -310,10 +357,10 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
         load32(v + from, vu, wide);
         const size_t to = ((size_t)at.to * Hkv + c / (D / 16)) * row_bytes(D, BITS);
         float x[16];
-        unpack16(ku, x, p.k_scale);
-        store_block<D, BITS>(p.k + to, c % (D / 16), x, p.k_scale.m);
-        unpack16(vu, x, p.v_scale);
-        store_block<D, BITS>(p.v + to, c % (D / 16), x, p.v_scale.m);
+        unpack16(ku, x);
+        store_block<D, BITS>(p.k + to, c % (D / 16), x, p.k_scale);
+        unpack16(vu, x);
+        store_block<D, BITS>(p.v + to, c % (D / 16), x, p.v_scale);
     }
 }
 
@@ -373,12 +420,13 @@ int tokens_of_cta(int Hkv, int D)
     return n < 1 ? 1 : n > kMostTokens ? kMostTokens : n;
 }
 
-Scale scale_of(float g)
+Scale scale_of(float g, int bits)
 {
     int e;
     Scale s;
     s.g = g;
     s.m = 2.f * frexpf(g, &e);
+    s.inv = 1.f / (bits == 8 ? s.m : 6.f * s.m);
     s.up1 = ldexpf(1.f, (1 - e) / 2);
     s.up2 = ldexpf(1.f, (1 - e) - (1 - e) / 2);
     return s;
@@ -389,8 +437,8 @@ Pools pools_of(const rd_quant_kv& kv)
     Pools p;
     p.k = static_cast<unsigned char*>(kv.k_pool);
     p.v = static_cast<unsigned char*>(kv.v_pool);
-    p.k_scale = scale_of(kv.k_scale);
-    p.v_scale = scale_of(kv.v_scale);
+    p.k_scale = scale_of(kv.k_scale, kv.bits);
+    p.v_scale = scale_of(kv.v_scale, kv.bits);
     p.num_pages = kv.pages.num_pages;
     p.page_size = kv.pages.page_size;
     p.max_pages = kv.pages.max_pages;
