@@ -885,3 +885,34 @@ def test_bytes_at_calibrated_scales(bits):
         for by in (1.0, 0.37, 3.0):           # beside the calibrated one, scales that saturate and that leave range
             got, y = _written(x, float(np.float32(g * by)), bits)
             assert len(_neighbours((got, y, float(np.float32(g * by)), bits))) == 0, (D, by)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_values_are_rounded_once(bits):
+    """Scales at which a product of 32 bits lies midway between two bf16 numbers and the exact one does not, found on
+    the CPU; and scales whose values have few bits left (below 2^-126)."""
+    rng, D, T = np.random.default_rng(bits), 64, 512
+    rows = rng.integers(0, 256, (T, 1, oq.row_bytes(D, bits))).astype(np.uint8)
+    if bits == 8:
+        rows[(rows & 0x7f) == 0x7f] = 0
+    else:
+        rows[..., 32:] = rng.integers(1, 0x7f, (T, 1, 4))
+    units = oq.decode(rows, 1.0, D, bits)
+    scales, some = [3e-39, 7.3e-38, 1e37], np.unique(np.abs(units[units != 0]))
+    while len(scales) < 12:                   # v g = (2 n + 1) 2^k / 2 + a little, with n of 8 bits
+        v, n = rng.choice(some), 2 * int(rng.integers(128, 256)) + 1
+        g = np.float32(n * 2.0 ** -12 / v)
+        once, twice = (torch.tensor(float(v) * float(g), dtype=t) for t in (torch.float64, torch.float32))
+        if not float(once) == float(twice) and int(twice.view(torch.int32)) & 0xffff == 0x8000:
+            scales.append(float(g))
+    pool, off = _d(rows.reshape(T // 64, 64, 1, -1)), _d(np.array([0, T], np.int64))
+    table = torch.arange(T // 64, dtype=torch.int32, device=DEV)[None].contiguous()
+    for g in scales:
+        g = float(np.float32(g))
+        k, v = _rd().rd_read_quant(pool, pool, g, g, table, off, total=T)
+        x = units * g                         # exact in 64 bits
+        e = np.maximum(np.frexp(x)[1] - 8, -133).astype(float)
+        want = np.rint(x * 2.0 ** -e) * 2.0 ** e               # 8 bits, or multiples of 2^-133; ties to even
+        want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)
+        assert torch.equal(k, v)
+        np.testing.assert_array_equal(_f64(k), want, err_msg=str(g))

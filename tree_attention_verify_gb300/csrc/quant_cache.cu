@@ -37,6 +37,7 @@ constexpr int kMostTokens = 64;            // tokens of a CTA
 // range on the way saturates or is 0 anyway.
 struct Scale {
     float g, m, up1, up2, inv;
+    uint32_t last;             // 1 where g has more than nine bits
 };
 
 struct Pools {
@@ -191,6 +192,14 @@ __device__ __forceinline__ void store_block(unsigned char* row, int block, const
     }
 }
 
+// v g as a number of 32 bits that rounds to 16 bits as the exact product does: cut off, with its last bit set.  A product
+// midway between two 16-bit numbers has nine bits at most, and so has g then, which divides it; with such a g every
+// product fits and its last bit stays.
+__device__ __forceinline__ float product(float v, const Scale& g)
+{
+    return __uint_as_float(__float_as_uint(__fmul_rz(v, g.g)) | g.last);
+}
+
 // a block as it lies in the pool, and its values
 template <int D, int BITS>
 struct Raw {
@@ -210,7 +219,7 @@ struct Raw {
             c.z = __ldg(row + D / 2 + block);
         }
     }
-    __device__ __forceinline__ void values(float g, uint32_t (&o)[8]) const
+    __device__ __forceinline__ void values(const Scale& g, uint32_t (&o)[8]) const
     {
         uint32_t w[8];                     // 16-bit floats, in order
         if constexpr (BITS == 8) {
@@ -231,7 +240,7 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 v = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
-            __nv_bfloat162 r = __floats2bfloat162_rn(v.x * g, v.y * g);
+            __nv_bfloat162 r = __floats2bfloat162_rn(product(v.x, g), product(v.y, g));
             o[i] = *reinterpret_cast<uint32_t*>(&r);
         }
     }
@@ -405,8 +414,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
             Raw<D, BITS> kr, vr;
             kr.load(p.k + from, c % (D / 16));
             vr.load(p.v + from, c % (D / 16));
-            kr.values(p.k_scale.g, ku);
-            vr.values(p.v_scale.g, vu);
+            kr.values(p.k_scale, ku);
+            vr.values(p.v_scale, vu);
         }
         const size_t to = ((size_t)(t0 + t) * blocks + c) * 2;
         store32(k + to, ku, wide);
@@ -427,6 +436,7 @@ Scale scale_of(float g, int bits)
     s.g = g;
     s.m = 2.f * frexpf(g, &e);
     s.inv = 1.f / (bits == 8 ? s.m : 6.f * s.m);
+    s.last = s.m * 256.f != truncf(s.m * 256.f);
     s.up1 = ldexpf(1.f, (1 - e) / 2);
     s.up2 = ldexpf(1.f, (1 - e) - (1 - e) / 2);
     return s;
