@@ -434,9 +434,10 @@ int rd_quant_row_bytes(int D, int bits);
  * new_ctx_lens int32 [B]; must not alias ctx_lens.
  * A sequence outside these bounds, a negative context or a new length that leaves 31 bits
  * sets RD_DEV_BAD_LENGTH, and nothing of that request is written (its new length is the
- * old); a position beyond max_pages*page_size sets RD_DEV_BAD_LENGTH and a page id out
- * of range RD_DEV_BAD_INDEX, and that row is skipped.  The pages written to must be held by no
- * other row (see the page operators).
+ * old; the others are written whole, sequences that overlap too); a position beyond
+ * max_pages*page_size sets RD_DEV_BAD_LENGTH and a page id out of range RD_DEV_BAD_INDEX, and
+ * that row is skipped.  The pages written to must be held by no other row (see the page
+ * operators).
  */
 rd_status rd_append_quant(int B, int Hkv, int D, int bits, const void* k, const void* v, int64_t total_tokens,
                           const int32_t* cu_seqlens, void* k_pool, void* v_pool, float k_scale, float v_scale,
@@ -459,8 +460,9 @@ rd_status rd_commit_accepted_quant(int B, int W, int L, int P_max, int Hkv, int 
  * rd_tree_attention takes a context: row offsets[b] + i of k_out and v_out is position
  * starts[b] + i of request b, for i < offsets[b+1] - offsets[b].
  *
- * offsets    int64 [B+1], ascending and within [0, total] (RD_DEV_BAD_LENGTH); rows of the
- *            outputs that belong to no request are left as they are
+ * offsets    int64 [B+1], ascending and within [0, total] (RD_DEV_BAD_LENGTH, and which
+ *            rows are written is not defined); rows of the outputs that belong to no request
+ *            are left as they are
  * starts     int32 [B], or null: 0.  A negative one, or a position beyond
  *            max_pages*page_size, sets RD_DEV_BAD_LENGTH, a page id out of range
  *            RD_DEV_BAD_INDEX: that row is zeros.

@@ -916,3 +916,57 @@ def test_values_are_rounded_once(bits):
         want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)
         assert torch.equal(k, v)
         np.testing.assert_array_equal(_f64(k), want, err_msg=str(g))
+
+
+@pytest.mark.parametrize("cu", [[0, 10, 5, 30], [0, 30, 1, 2, 3, 4, 30], [20, 30, 0, 20], [5, 25, 5, 25, 5, 25], [0, 30, 0, 30],
+                                [0, 0, 30, 12, 12, 17], [29, 30] + list(range(300)) * 1])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_sequences_that_overlap(cu, bits):
+    """cu_seqlens that does not ascend is flagged, and every request whose own sequence lies within the tokens has
+    all of its rows: none grows by rows that nobody wrote."""
+    rd, rng = _rd(), np.random.default_rng(bits)
+    T, Hkv, D = 30, 2, 64
+    cu = np.array(cu, np.int64)
+    B = len(cu) - 1
+    k = _bf(rng.standard_normal((T, Hkv, D)))
+    ctx = np.arange(B, dtype=np.int32) % 40
+    kp, vp = (torch.full((B + 1, 128, Hkv, oq.row_bytes(D, bits)), 0x55, dtype=torch.uint8, device=DEV) for _ in range(2))
+    table, st = _d(rng.permutation(B + 1)[:B, None].astype(np.int32)), _status()
+    new = rd.rd_append_quant(k, k, _d(cu.astype(np.int32)), kp, vp, 0.25, 0.25, table, _d(ctx), dev_status=st)
+    assert int(st) == rd.DEV_BAD_LENGTH and torch.equal(kp, vp)
+    fine = (cu[:-1] >= 0) & (cu[:-1] <= cu[1:]) & (cu[1:] <= T)
+    np.testing.assert_array_equal(new.cpu().numpy(), ctx + np.where(fine, cu[1:] - cu[:-1], 0))
+    rows = np.stack([[oq.encode_row(_f64(k[t, h]), 0.25, bits)[0] for h in range(Hkv)] for t in range(T)])
+    want = np.full(kp.shape, 0x55, np.uint8)
+    for b in np.flatnonzero(fine):
+        n = int(cu[b + 1] - cu[b])
+        want[int(table[b, 0]), ctx[b]:ctx[b] + n] = rows[cu[b]:cu[b + 1]]
+    np.testing.assert_array_equal(kp.cpu().numpy(), want)
+
+
+def test_long_sequences_that_overlap():
+    """The same with sequences of many tokens, more requests than a CTA has threads, and a page that does not exist."""
+    rd, rng = _rd(), np.random.default_rng(0)
+    T, Hkv, D, B = 300, 40, 128, 400
+    cu = np.sort(rng.integers(0, T + 1, B + 1))
+    cu[[0, 1, 2, 3]] = 0, T, 7, 290           # 0 .. T, then a descent, then 7 .. 290
+    cu[300], cu[301] = 0, 250
+    k = _bf(rng.standard_normal((T, Hkv, D)))
+    need = np.where(cu[1:] >= cu[:-1], cu[1:] - cu[:-1], 0)
+    table, n = _tables(rng, B, -(-need // 64) + 0)
+    table[2, 1] = n + 5
+    st = _status()
+    kp = torch.zeros(n, 64, Hkv, oq.row_bytes(D, 8), dtype=torch.uint8, device=DEV)
+    ctx = _d(np.zeros(B, np.int32))
+    new = rd.rd_append_quant(k, k, _d(cu.astype(np.int32)), kp, kp.clone(), 0.25, 0.25, _d(table), ctx, dev_status=st)
+    assert int(st) == rd.DEV_BAD_LENGTH | rd.DEV_BAD_INDEX
+    np.testing.assert_array_equal(new.cpu().numpy(), need)
+    plain = torch.zeros(T, 1, Hkv, oq.row_bytes(D, 8), dtype=torch.uint8, device=DEV)      # one token a page
+    rd.rd_append_quant(k, k, _d(np.array([0, T], np.int32)), plain, plain.clone(), 0.25, 0.25,
+                       torch.arange(T, dtype=torch.int32, device=DEV)[None].contiguous(), ctx[:1])
+    want = torch.zeros_like(kp)
+    for b in range(B):
+        for i in range(int(need[b])):
+            if table[b, i // 64] < n:
+                want[int(table[b, i // 64]), i % 64] = plain[int(cu[b]) + i, 0]
+    assert torch.equal(kp, want)

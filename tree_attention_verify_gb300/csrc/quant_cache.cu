@@ -281,6 +281,7 @@ struct Where {
 
 // tokens of the prompts: row t of [T, Hkv, D] belongs to the sequence of cu_seqlens that holds t
 struct Prompt {
+    static constexpr bool kSearched = true;
     const int32_t *cu, *ctx;
     int32_t* new_ctx;
     int B;
@@ -297,16 +298,35 @@ struct Prompt {
         if (!ok) rd_flag(status, RD_DEV_BAD_LENGTH);
         new_ctx[i] = ctx[i] + (ok ? cu[i + 1] - cu[i] : 0);
     }
+    // Whether request i has tokens that the search finds elsewhere, or nowhere: where cu does not ascend.  The search comes
+    // to i from the tokens between the entries that it passes on its way.
+    __device__ __forceinline__ bool lost(int i) const
+    {
+        if (i >= B || !fine(i) || cu[i] == cu[i + 1]) return false;
+        int lo = 0, hi = B;
+        bool found = true;
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (i >= mid) found &= cu[i] >= cu[mid], lo = mid;
+            else found &= cu[i + 1] <= cu[mid], hi = mid;
+        }
+        return !found;
+    }
     __device__ __forceinline__ Where find(const Pools& p, int64_t t, int32_t* status) const
     {
         const int b = request_of(cu, B, t);
         if (t < cu[b] || t >= cu[b + 1] || !fine(b)) return {t, -1};
+        return at(p, b, t, status);
+    }
+    __device__ __forceinline__ Where at(const Pools& p, int b, int64_t t, int32_t* status) const
+    {
         return {t, row_of(p, b, (int64_t)ctx[b] + (t - cu[b]), status)};
     }
 };
 
 // the accepted path: token t is position t % L of request t / L
 struct Accepted {
+    static constexpr bool kSearched = false;
     const int32_t *unpacker, *best, *accepted, *ctx;
     int32_t* new_ctx;
     int B, W, L, P;
@@ -348,28 +368,51 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
                                                          const uint4* __restrict__ v, int32_t* status)
 {
     __shared__ Where where[kMostTokens];
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < src.B; i += (int64_t)gridDim.x * kThreads)
+    bool lost = false;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < src.B; i += (int64_t)gridDim.x * kThreads) {
         src.lengths((int)i, status);
+        if constexpr (Source::kSearched) lost |= src.lost((int)i);
+    }
     const int64_t t0 = (int64_t)blockIdx.x * each;
-    const int n = (int)min((int64_t)each, tokens - t0);
+    int n = (int)min((int64_t)each, tokens - t0);
     if ((int)threadIdx.x < n) where[threadIdx.x] = src.find(p, t0 + threadIdx.x, status);
-    __syncthreads();
+    lost = __syncthreads_or(lost);
     const int blocks = Hkv * (D / 16);     // of a token
     const bool wide = aligned32(k, v);
-    for (int i = threadIdx.x; i < n * blocks; i += kThreads) {
-        const int t = i / blocks, c = i - t * blocks;
-        const Where at = where[t];
-        if (at.to < 0) continue;
-        const size_t from = ((size_t)at.from * blocks + c) * 2;
-        uint32_t ku[8], vu[8];
-        load32(k + from, ku, wide);
-        load32(v + from, vu, wide);
-        const size_t to = ((size_t)at.to * Hkv + c / (D / 16)) * row_bytes(D, BITS);
-        float x[16];
-        unpack16(ku, x);
-        store_block<D, BITS>(p.k + to, c % (D / 16), x, p.k_scale);
-        unpack16(vu, x);
-        store_block<D, BITS>(p.v + to, c % (D / 16), x, p.v_scale);
+    int64_t q = 0;
+    int done = 0;
+    for (;;) {
+        for (int i = threadIdx.x; i < n * blocks; i += kThreads) {
+            const int t = i / blocks, c = i - t * blocks;
+            const Where at = where[t];
+            if (at.to < 0) continue;
+            const size_t from = ((size_t)at.from * blocks + c) * 2;
+            uint32_t ku[8], vu[8];
+            load32(k + from, ku, wide);
+            load32(v + from, vu, wide);
+            const size_t to = ((size_t)at.to * Hkv + c / (D / 16)) * row_bytes(D, BITS);
+            float x[16];
+            unpack16(ku, x);
+            store_block<D, BITS>(p.k + to, c % (D / 16), x, p.k_scale);
+            unpack16(vu, x);
+            store_block<D, BITS>(p.v + to, c % (D / 16), x, p.v_scale);
+        }
+        if (!Source::kSearched || !lost) return;
+        // Sequences that do not ascend: the q-th request of those whose lengths this CTA has written, if its search
+        // misses any of its tokens, whole, some tokens at a time (what is written twice are the same bytes).
+        if constexpr (Source::kSearched) {
+            int64_t b;
+            for (;; ++q, done = 0) {
+                b = (q / kThreads * gridDim.x + blockIdx.x) * kThreads + q % kThreads;
+                if (b >= src.B) return;
+                if (src.lost((int)b) && done < src.cu[b + 1] - src.cu[b]) break;
+            }
+            __syncthreads();
+            n = min(kMostTokens, src.cu[b + 1] - src.cu[b] - done);
+            if ((int)threadIdx.x < n) where[threadIdx.x] = src.at(p, (int)b, (int64_t)src.cu[b] + done + threadIdx.x, status);
+            done += n;
+            __syncthreads();
+        }
     }
 }
 
