@@ -322,3 +322,54 @@ def test_rows_without_a_whole_group(V, dtype):
         for i in (0, 1, n // 2, n - 1):
             check(out, i, x[i], int(tokens[i]), 1.0, V)
         flat.fill_(float("nan"))
+
+
+def _rows_of_many_candidates(V, dtype):
+    """Rows whose first part tells nothing of the largest logits, with equal logits where the type is short."""
+    up = torch.linspace(-30, 30, V, device=DEV)
+    steps = torch.floor(torch.linspace(0, 40, V, device=DEV))
+    saw = up + 5 * (torch.arange(V, device=DEV) % 3 == 0)
+    late = torch.where(torch.arange(V, device=DEV) < V // 2, -up - 60, up)
+    few = torch.where(torch.arange(V, device=DEV) % 2048 < 16, up + 100, up)       # some threads have all of the largest
+    return torch.stack([up, steps, saw, late, few, -(up * up)]).to(TYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [20000, 128256, 1 << 20])
+@pytest.mark.parametrize("copies", [1, 40])
+def test_many_candidates(V, dtype, copies):
+    rd = _rd()
+    x = _rows_of_many_candidates(V, dtype)
+    rows = torch.arange(len(x), dtype=torch.int32, device=DEV).repeat(copies)      # (one CTA a row where there are many)
+    for top in (1, 32):
+        out = rd.rd_token_logprobs(x, torch.full_like(rows, 7), rows=rows, top=top)
+        for i in range(len(x)):
+            want = torch.sort(x[i], descending=True, stable=True).indices[:top]
+            for c in {0, copies - 1}:
+                assert torch.equal(out["top_tokens"][c * len(x) + i].long(), want), (i, top)
+            if V < 1 << 20:
+                check(out, i, x[i], 7, 1.0, top)
+
+
+def test_rising_rows_are_read_a_few_times():
+    """2^22 logits that rise: about 500 times the falling row's time, if each pass over them left out a thousand."""
+    rd = _rd()
+    V = 1 << 22
+    up = torch.linspace(-30, 30, V, device=DEV)[None]
+    rows, t = (up.contiguous(), up.flip(1).contiguous()), _i32([5])
+
+    def time(x):
+        rd.rd_token_logprobs(x, t, top=32)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(3):
+            out = rd.rd_token_logprobs(x, t, top=32)
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b), out
+
+    (rising, out), (falling, other) = time(rows[0]), time(rows[1])
+    print(f"rising {rising / 3:.3f} ms, falling {falling / 3:.3f} ms")
+    want = torch.sort(rows[0], descending=True, stable=True)
+    assert torch.equal(out["top_tokens"].long(), want.indices[:, :32])
+    assert rising < 100 * falling
