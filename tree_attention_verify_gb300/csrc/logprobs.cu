@@ -343,24 +343,25 @@ __device__ __noinline__ Stats add_slowly(Stats s, uint4 u, float top, float c)
     return s;
 }
 
-// One warp: sh.list[0 .. n) -> sh.best, the keys of rank below k, in order.  The k-th largest upper
-// 16 bits are found bit by bit, what reaches them (few more than k) is ranked by counting.
+// One warp: sh.list[0 .. n) -> sh.best, the keys of rank below k, in order.  The bits of the k-th largest are found one by
+// one until at most 64 keys reach them (the whole key's if need be: equal logits differ in their places), which
+// are ranked by counting.
 __device__ __forceinline__ void rank(Shared& sh, int n, int k)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t at = 0;
-    if (n > 64) {                          // (fewer are as quickly ranked as searched)
-        for (uint32_t bit = 0x80000000u; bit > 0x8000u; bit >>= 1) {
-            int reach = 0;
-            for (int i = lane; i < n; i += 32) reach += (uint32_t)(sh.list[i] >> 32) >= (at | bit);
-            if (__reduce_add_sync(0xffffffffu, reach) >= k) at |= bit;
-        }
+    unsigned long long at = 0;
+    int reached = n;
+    for (unsigned long long bit = 1ull << 63; bit != 0 && reached > 64; bit >>= 1) {
+        int reach = 0;
+        for (int i = lane; i < n; i += 32) reach += sh.list[i] >= (at | bit);
+        reach = __reduce_add_sync(0xffffffffu, reach);
+        if (reach >= k) at |= bit, reached = reach;
     }
     unsigned long long* kept = reinterpret_cast<unsigned long long*>(sh.group);
     int m = 0;
     for (int i0 = 0; i0 < n; i0 += 32) {
         const unsigned long long key = i0 + lane < n ? sh.list[i0 + lane] : 0;
-        const bool mine = i0 + lane < n && (uint32_t)(key >> 32) >= at;
+        const bool mine = i0 + lane < n && key >= at;
         const uint32_t who = __ballot_sync(0xffffffffu, mine);
         if (mine) kept[m + __popc(who & ((1u << lane) - 1))] = key;
         m += __popc(who);
