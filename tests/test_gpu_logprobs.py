@@ -373,3 +373,22 @@ def test_rising_rows_are_read_a_few_times():
     want = torch.sort(rows[0], descending=True, stable=True)
     assert torch.equal(out["top_tokens"].long(), want.indices[:, :32])
     assert rising < 100 * falling
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_differences_beyond_the_range(dtype):
+    """Logits of either sign near the largest numbers under a temperature of their size: the differences are no 32-bit
+    numbers, their quotients are a few units."""
+    rd = _rd()
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    for V in (3, 700, 40000):
+        x = (torch.rand(4, V, generator=gen, device=DEV) * 6.6e38 - 3.3e38).to(dtype) if V > 3 else \
+            torch.tensor([[3e38, -3e38, 0.0]] * 4, device=DEV).to(dtype)
+        x[1, 1] = -float("inf")
+        for T in (3.0e38, 4e37, 1e30, 2.0):
+            t = [0, 2, V - 1, 1]
+            out = rd.rd_token_logprobs(x, _i32(t), top=3, temperature=T)
+            for i in range(4):
+                far = oq.logprobs(x[i].double().cpu().numpy(), t[i], float(np.float32(T)), 3)
+                if np.isfinite(np.float32(far[0])) and np.isfinite(np.float32(far[3])).all():
+                    check(out, i, x[i], t[i], float(np.float32(T)), 3)

@@ -47,7 +47,9 @@ struct Args {
     int W, L, P;
     int64_t n, rows_total;
     int V, k;
-    float T, c, off;                       // temperature, log2(e) / T, and what c is short of, relative
+    // log2(e) / T, and what c is short of, relative; two numbers' difference over T is (a h - b h) / Th and
+    // in units of log2 (a h - b h) ch, with h 1/2 where the difference may leave the range and its quotient not
+    float c, off, h, Th, ch;
     float *logprob, *entropy;
     int32_t* top;
     float* top_logprob;
@@ -209,14 +211,20 @@ __device__ __forceinline__ unsigned long long key_of(float x, int i)
     return (unsigned long long)ordered(x) << 32 | (uint32_t)~i;
 }
 
+// the difference of two logits in units of log2
+struct Slope {
+    float h, c;
+    __device__ __forceinline__ float operator()(float a, float b) const { return (a * h - b * h) * c; }
+};
+
 struct Stats {
     // Reference (a logit; -inf: nothing yet), sums of the others, and how many stand at the reference: where one token has
     // nearly all of the probability, log l is that of 1 + l, and nothing of l is lost beside the 1.
     float m, l, w, ones;
-    __device__ __forceinline__ void move(float to, float c)       // to another reference
+    __device__ __forceinline__ void move(float to, Slope slope)   // to another reference
     {
         if (m != -INFINITY) {
-            const float z = (m - to) * c, f = exp2_(z), all = l + ones;
+            const float z = slope(m, to), f = exp2_(z), all = l + ones;
             w = f * (w + z * all);
             l = f * all;
             if (f == 0.f) w = 0.f;
@@ -324,15 +332,15 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& row, int g, uint4
 // (references near the lowest number, extreme temperatures).  2^-200 is 0, and 0 x -200 too: a logit of -inf
 // adds nothing.
 template <typename T>
-__device__ __noinline__ Stats add_slowly(Stats s, uint4 u, float top, float c)
+__device__ __noinline__ Stats add_slowly(Stats s, uint4 u, float top, Slope slope)
 {
     constexpr int N = Vec<T>::n;
     if (top == -INFINITY) return s;
-    if (!(top <= s.m)) s.move(top, c);
+    if (!(top <= s.m)) s.move(top, slope);
     float v[N];
     Vec<T>::unpack(u, v);
     for (int e = 0; e < N; ++e) {
-        const float d = v[e] - s.m, z = max_nan(d * c, -200.f), p = exp2_(z);
+        const float d = slope(v[e], s.m), z = max_nan(d, -200.f), p = exp2_(z);
         if (d == 0.f) {
             s.ones += 1.f;
         } else {
@@ -430,10 +438,10 @@ __device__ __noinline__ unsigned long long search(Shared& sh, const Row<T>& row,
 }
 
 // the sums of a warp's lanes, in all of them
-__device__ __forceinline__ Stats join_warp(Stats s, float c)
+__device__ __forceinline__ Stats join_warp(Stats s, Slope slope)
 {
     const float m = number(__reduce_max_sync(0xffffffffu, ordered(s.m)));
-    if (s.m != m) s.move(m, c);            // (two equal references may be infinite)
+    if (s.m != m) s.move(m, slope);            // (two equal references may be infinite)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s.l += __shfl_xor_sync(0xffffffffu, s.l, o);
@@ -499,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     if (tid == 0) sh.count = sh.groups = 0;
     Stats s = {-INFINITY, 0.f, 0.f, 0.f};
     uint64_t l2 = 0, w2 = 0;               // (two chains of sums each, of the reference s.m)
+    const Slope slope = {a.h, a.ch};
     const uint64_t c2 = pair(a.c, a.c);
     unsigned long long least = 0;
     float floor_ = -INFINITY;              // what reaches it is looked at
@@ -558,12 +567,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
                         l2 = w2 = 0;
                         fast = top < 1e30f;
                     }
-                    s = add_slowly<T>(s, u[j], top, a.c);
+                    s = add_slowly<T>(s, u[j], top, slope);
                     continue;
                 }
             }
             if (!fast) {
-                s = add_slowly<T>(s, u[j], top, a.c);
+                s = add_slowly<T>(s, u[j], top, slope);
                 continue;
             }
             float v[N];
@@ -586,13 +595,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             const uint4 u = row.edge(g);
             const float top = Vec<T>::top(u);
             if (k > 0 && !(top < floor_)) keep(sh, g, u);
-            s = add_slowly<T>(s, u, top, a.c);
+            s = add_slowly<T>(s, u, top, slope);
         }
     }
     __syncthreads();                       // (sh.warp is read above and written below; the groups are there)
     if (k > 0 && sh.groups <= kGroups)
         for (int i = tid; i < sh.groups; i += kThreads) collect<T>(sh, row, sh.group_id[i], sh.group[i], least);
-    s = join_warp(s, a.c);
+    s = join_warp(s, slope);
     if (lane == 0) sh.warp[warp] = s;
     __syncthreads();
     if (k > 0) {
@@ -629,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     Stats all = {-INFINITY, 0.f, 0.f, 0.f};     // (in the first warp)
     if (warp == 0) {
         if (lane < kWarps) all = sh.warp[lane];
-        all = join_warp(all, a.c);
+        all = join_warp(all, slope);
     }
     if (parts > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         if (warp == 0) {
             all = {-INFINITY, 0.f, 0.f, 0.f};
             if (lane < parts) all = sh.part[lane];
-            all = join_warp(all, a.c);
+            all = join_warp(all, slope);
         }
         if (k > 0) {
             // at most 8 x 32 keys, one a thread
@@ -663,13 +672,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     const float ln_p = fmaf(a.off, mean, ln_l);
     const float m = all.m == -INFINITY ? 0.f : all.m;
     if (tid == 0) {
-        a.logprob[n] = (chosen - m) / a.T - ln_p;
+        a.logprob[n] = (chosen * a.h - m * a.h) / a.Th - ln_p;
         a.entropy[n] = ln_l - mean;
     }
     if (tid < k) {
         const unsigned long long key = sh.best[tid];
         a.top[n * k + tid] = (int32_t)~(uint32_t)key;
-        a.top_logprob[n * k + tid] = (number((uint32_t)(key >> 32)) - m) / a.T - ln_p;
+        a.top_logprob[n * k + tid] = (number((uint32_t)(key >> 32)) * a.h - m * a.h) / a.Th - ln_p;
     }
 }
 
@@ -712,10 +721,12 @@ cudaError_t rd_launch_logprobs(const rd_logprobs& q, cudaStream_t stream)
     a.rows_total = q.n_rows;
     a.V = q.V;
     a.k = q.top;
-    a.T = q.temperature;
     const double c = 1.4426950408889634 / q.temperature;
     a.c = (float)c;
     a.off = (float)((c - a.c) / c);
+    a.h = q.temperature > 1.f ? 0.5f : 1.f;
+    a.Th = q.temperature * a.h;
+    a.ch = a.c / a.h;
     a.logprob = q.logprob;
     a.entropy = q.entropy;
     a.top = q.top_tokens;
