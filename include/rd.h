@@ -522,7 +522,8 @@ rd_status rd_tree_attention_quant(int B, int P_max, int Hq, int Hkv, int D, int 
  *            (RD_ERR_UNSUPPORTED).
  * Logits of -inf have probability 0 and add nothing to the entropy.  A row with a NaN or
  * +inf, or of -inf alone, has no distribution: its logprob, entropy and top_logprobs are NaN.
- * Sums are fp32.  No workspace.
+ * Sums are fp32.  No workspace.  With alternatives, rows that rise throughout or whose first part is
+ * masked are read several times (up to twelve times an ordinary row's time).
  */
 rd_status rd_token_logprobs(const void* logits, rd_dtype dt, int64_t n_rows, int V, const int32_t* rows,
                             const int32_t* tokens, int64_t n, float temperature, int top, float* logprob, float* entropy,

@@ -9,14 +9,14 @@
 // about 50 instructions for eight 16-bit logits, somewhat more than half of what the SM can
 // issue while HBM delivers them.  What is rare (a larger maximum, a candidate, numbers at the ends of
 // the range) stays out of the loop's way.  4,096 rows of 128,256 bf16 logits with 20 alternatives
-// take 227 us (4.6 TB/s; 40,000 instructions a row, whose loads' latency is not hidden all of the time).
+// take 223.5 us (4.7 TB/s; 40,000 instructions a row, whose loads' latency is not hidden all of the time).
 //
 // The top k come from the same pass: a threshold that at least k logits of the row reach
 // is known after the first 64 logits of each thread (the k-th largest of the threads'
 // maxima, found bit by bit); the 16-byte groups with what reaches it afterwards, a few times k of
 // them, are kept, and their 64-bit keys (value, then the lower index first) ranked by counting at the end.  Where these
 // overfill the list (many equal logits), its k-th key is a better threshold for another pass; where they do so again (a
-// row that keeps rising), a threshold is searched in a few more (608 rising rows of 128,256 with 20 alternatives: 470 us,
+// row that keeps rising), a threshold is searched in a few more (608 rising rows of 128,256 with 20 alternatives: 478 us,
 // ordinary ones 41).
 //
 // Few rows: a cluster of up to eight CTAs takes one, and its first CTA joins the parts.

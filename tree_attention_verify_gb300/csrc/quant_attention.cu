@@ -18,7 +18,7 @@
 // 16-byte words.  Rows are the products' short side: 8 at a time, so that five rows cost a
 // quarter of what 32 do.
 //
-// 64 contexts of 8,192 with 23 nodes of 48 and 40 heads take 1,125 us (2.7 TB/s of codes): the matrix
+// 64 contexts of 8,192 with 23 nodes of 48 and 40 heads take 1,141 us (2.6 TB/s of codes): the matrix
 // unit, one of these products every two cycles, is busy for 490 of them, and the 8 warps that the registers leave room
 // for do not hide each other's chains (code to float, product, exponential, product) any better.
 // A call of one short piece a CTA is its start and end: 8 tokens of 2,000 positions take 20.6 us, 16 of them for
@@ -585,7 +585,7 @@ __device__ __forceinline__ uint32_t bf16_of_f16(uint32_t x)
 }
 
 // one tile of 16 packed drafts: bf16 as they are; P is rounded to bf16 too (both factors of
-// a product have one type), 2^-9 of each weight
+// a product have one type), 2^-8 of each weight
 template <int D, int BITS, int NT>
 __device__ __forceinline__ void draft_tile(const Args& a, const Place& w, const Piece& pc, Sums<D, BITS, NT>& s, uint32_t k_at,
                                            uint32_t v_at, uint32_t q_at, uint32_t f_at, int node0, int nodes)

@@ -1,5 +1,4 @@
-// What the two kernels of rd_tree_attention_quant share: their arguments, the division of the work,
-// small loads.
+// rd_tree_attention_quant's arguments, the division of its work among the CTAs, and small loads.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -16,7 +16,7 @@
 // tokens written and read back: 39 us, not 34).
 // Two 16-byte accesses for a block's 32 bytes would take longer (16 x 4,096 tokens of 8 heads read from 4
 // bits: 53 us, not 45), and so would CTAs of 1,024 blocks, which wait longer for their first
-// bytes than they then move (the same: 39 us, not 37, when the divisions took their part).  Reading 8 x 8,192 tokens of 40 heads
+// bytes than they then move (the same: 39 us, not 37, with the divisions).  Reading 8 x 8,192 tokens of 40 heads
 // from 8 bits takes 234 us, 6.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
