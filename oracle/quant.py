@@ -32,7 +32,7 @@ def e4m3_value(byte):
 
 def encode_row(x, g, bits):
     """Bytes of the row of values x [D], and its smallest distance from a border
-    (nearer than the kernel's 32-bit quotients resolve, the byte may be the neighbour's)."""
+    (relative; in 4 bits, exact ties do not count)."""
     x = np.asarray(x, np.float64)
     if bits == 8:
         code, near = nearest_code(x / g, E4M3)

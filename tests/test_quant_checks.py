@@ -149,3 +149,19 @@ def test_binding_checks_shapes(monkeypatch):
 
 def test_append_refuses_lengths_in_place():
     assert call("rd_append_quant", ctx=ONE, new=ONE) == rd.RD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("top", [33, 10 ** 9, -1, 2 ** 31 - 1])
+def test_refused_alternatives_take_no_memory(top, monkeypatch):
+    """A number of alternatives that the call refuses is refused, before outputs of its size are asked for."""
+    asked = []
+    monkeypatch.setattr(rd, "_fine", lambda *a: True)
+    monkeypatch.setattr(rd, "_need", lambda *a, **kw: None)
+    monkeypatch.setattr(rd, "_run", lambda name, like, *a, stream=None: (_ for _ in ()).throw(rd.RdError(name, rd.RD_ERR_UNSUPPORTED)))
+    monkeypatch.setattr(rd, "_new", lambda shape, dtype, like, stream: asked.append(shape) or torch.zeros(shape, dtype=dtype))
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    with pytest.raises(rd.RdError):
+        rd.rd_token_logprobs(torch.zeros(4, 10), i32(4), top=top)
+    with pytest.raises(rd.RdError):
+        rd.rd_accepted_logprobs(torch.zeros(4, 6, 10), i32(4, 2, 3), i32(4), i32(4), i32(4, 3), top=top)
+    assert len(asked) == 8 and all(max(s) <= 32 for s in asked)

@@ -969,6 +969,7 @@ def _logits_type(logits, ndim):
 
 
 def _logprob_outs(out, shape, top, like, stream) -> dict:
+    top = min(max(0, top), 32)                  # (others are refused by the call: nothing is allocated for them)
     shapes = dict(logprob=shape, entropy=shape, top_tokens=(*shape, top), top_logprobs=(*shape, top))
     types = dict(logprob=torch.float32, entropy=torch.float32, top_tokens=torch.int32, top_logprobs=torch.float32)
     if out is not None and not isinstance(out, dict):
@@ -994,7 +995,7 @@ def rd_token_logprobs(logits, tokens, *, rows=None, top: int = 0, temperature: f
     elif n > n_rows:
         raise ValueError(f"tokens must be [n] with n <= {n_rows}, got {tuple(tokens.shape)}")
     _need_status(dev_status, logits)
-    out = _logprob_outs(out, (n,), max(0, top), logits, stream)
+    out = _logprob_outs(out, (n,), top, logits, stream)
     _run("rd_token_logprobs", logits,
          logits.data_ptr(), dt, n_rows, V, _ptr(rows), tokens.data_ptr(), n, float(temperature), top,
          out["logprob"].data_ptr(), out["entropy"].data_ptr(), out["top_tokens"].data_ptr(),
@@ -1021,7 +1022,7 @@ def rd_accepted_logprobs(logits, unpacker, best_beam, n_accepted, out_tokens, *,
     _of_batch(B, index, best_beam=best_beam, n_accepted=n_accepted)
     _need_status(dev_status, logits)
     top = _c_int("top", top)
-    out = _logprob_outs(out, (B, L), max(0, top), logits, stream)
+    out = _logprob_outs(out, (B, L), top, logits, stream)
     _run("rd_accepted_logprobs", logits,
          logits.data_ptr(), dt, B, P, V, unpacker.data_ptr(), W, L, best_beam.data_ptr(), n_accepted.data_ptr(),
          out_tokens.data_ptr(), float(temperature), top, out["logprob"].data_ptr(), out["entropy"].data_ptr(),
